@@ -65,6 +65,7 @@ typedef int32_t staple_status_t;
 #define STAPLE_ERR_INDEX_RANGE (-5)       /* a kernel met an out-of-range ID or index */
 #define STAPLE_ERR_HOST (-6)              /* host-side failure (thread pool, host ID check) */
 #define STAPLE_ERR_SCRATCH_LIMIT (-7)     /* larger than the allocation-free call's fixed scratch */
+#define STAPLE_ERR_NO_PAGES (-8)          /* the page pool or a table row is too small for the tokens asked for */
 
 /* Element types.  STAPLE_BF16: bfloat16 storage, fp32 accumulation.
  * STAPLE_F32: fp32 storage and accumulation. */
@@ -79,7 +80,8 @@ const char* staple_version(void);
 
 /* Waits for `stream`, then reads and clears the calling device's error word.
  * Returns STAPLE_OK, or STAPLE_ERR_INDEX_RANGE if any kernel since the last
- * call met an out-of-range ID or index. */
+ * call met an out-of-range ID or index, or STAPLE_ERR_NO_PAGES if none did
+ * but a key-value cache ran out of pages. */
 staple_status_t staple_get_device_error(void* stream);
 
 /* ------------------------------------------------------------------------
@@ -746,6 +748,163 @@ staple_status_t staple_ffn_bwd_table_grad(int64_t n_tokens, int64_t d_model, int
                                           float* dw_gate, float* dw_up, float* dw_down,
                                           int32_t freeze_up, void* ws, size_t ws_bytes,
                                           void* rows_event, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention, the layer between two FFN layers: sequences packed one after
+ * the other, query heads grouped over fewer key-value heads (query head h
+ * reads key-value head h / (n_heads / n_kv_heads)), a causal mask with an
+ * optional sliding window and a few first tokens that stay visible (sinks).
+ *
+ * The query i of a sequence with Lq queries and Lk keys stands at position
+ * p = i + Lk - Lq (the queries are the sequence's last Lq positions) and sees
+ * key j when
+ *     j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
+ * With s_j = scale q.k_j over the visible j:
+ *     lse = log sum_j exp s_j,   P_j = exp(s_j - lse),   o = sum_j P_j v_j.
+ * A query that sees nothing (p < 0) has o = 0 and lse = -inf and adds
+ * nothing to any gradient.  A key that a query does not see has no part in
+ * its result, whatever the key's and its value's row hold (NaN, infinities).
+ *
+ * Products and sums are fp32 (bf16: from bf16 operands).  bf16 rounds P
+ * (and, in the backward, dS) to bf16 as the operand of the next product and
+ * o, dq, dk, dv once where they are stored.  The results are deterministic.
+ * ------------------------------------------------------------------------ */
+
+/* A [rows][heads][head_dim] operand: row t, head h at data + t row_stride +
+ * h head_stride, in elements; head_dim elements are contiguous.  data is
+ * 16-byte aligned and the strides are non-negative multiples of 16 bytes. */
+typedef struct staple_heads_t {
+  void* data;
+  int64_t row_stride, head_stride;
+} staple_heads_t;
+
+typedef struct staple_attn_t {
+  int64_t n_seqs, total_q, total_k;
+  int64_t n_heads, n_kv_heads;       /* n_heads a multiple of n_kv_heads */
+  int64_t head_dim;                  /* a multiple of 8, at most 128 */
+  int64_t window;                    /* 0: every key up to p */
+  int64_t sinks;
+  float scale;                       /* finite */
+  int32_t dtype;
+  const int32_t* cu_q;               /* device int32[n_seqs + 1]: sequence b's queries are the rows */
+  const int32_t* cu_k;               /*   [cu_q[b], cu_q[b + 1]) of q, its keys those of cu_k in k, v */
+  staple_heads_t q, k, v;            /* q, o: total_q rows of n_heads; k, v: total_k rows of n_kv_heads */
+  staple_heads_t o;
+  float* lse;                        /* [total_q x n_heads] */
+  staple_heads_t d_o, dq, dk, dv;    /* backward only */
+} staple_attn_t;
+
+/* Forward: writes o and lse from q, k, v.  `a` is read during the call only.
+ * A pair of cu_q or cu_k entries that is out of order or past the totals sets
+ * the device error word, and that sequence counts as empty.  Rows in no
+ * sequence are not written. */
+staple_status_t staple_attn_fwd(const staple_attn_t* a, void* stream);
+
+/* Backward: writes dq, dk, dv from d_o, the forward's operands and its o and
+ * lse (gradients of shared key-value heads are summed over their query
+ * heads).  Overwritten, not accumulated.  Workspace: delta = sum_d d_o o
+ * (fp32, total_q x n_heads) and the partial dk, dv of the sinks' keys. */
+size_t staple_attn_bwd_workspace_bytes(const staple_attn_t* a);
+staple_status_t staple_attn_bwd(const staple_attn_t* a, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache.  A layer's keys (and values) live in pages of
+ * page_size slots; a table row lists a sequence's pages in order, and every
+ * layer uses the same table.  refs counts the table rows that hold a page; a
+ * page with refs 0 is free.  All state is on the device and every call is
+ * asynchronous, so a step that grows, forks or ends sequences needs no host
+ * round trip and can be captured in a graph.
+ *
+ *   k_pages, v_pages: [n_layers][n_pages][n_kv_heads][page_size][head_dim]
+ *     (a kv head's slots of a page are contiguous: what one attention
+ *     workgroup reads);
+ *   refs  int32[n_pages];
+ *   table int32[n_rows][max_pages]: the first ceil(lens[s] / page_size)
+ *     entries of row s are its pages;
+ *   lens  int32[n_rows]: the tokens of each row's sequence, 0: empty.
+ *
+ * page_size is a power of two in [16, 1024]; head_dim as in staple_attn_t.
+ * Row numbers, pages and lengths out of range set the device error word and
+ * are skipped.  Lists of rows (`seqs`, `children`) name each row once.
+ * ------------------------------------------------------------------------ */
+typedef struct staple_kv_t {
+  int64_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
+  int64_t n_rows, max_pages;
+  int32_t dtype;
+  void *k_pages, *v_pages;
+  int32_t *refs, *table, *lens;
+} staple_kv_t;
+
+/* Writes new tokens' keys and values into one layer's pages (n_layers 1): the
+ * rows [cu_new[i], cu_new[i + 1]) of k_new, v_new ([n_new rows] of n_kv_heads)
+ * are the last tokens of sequence seqs[i], whose lens already counts them.
+ * cu_new NULL: one row each, row i for seqs[i].  seqs NULL: row i of the table.
+ * Uses k_pages, v_pages, table, lens. */
+staple_status_t staple_kv_append(const staple_kv_t* kv, const staple_heads_t* k_new,
+                                 const staple_heads_t* v_new, int64_t n_new, const int32_t* seqs,
+                                 int64_t n_seqs, const int32_t* cu_new, void* stream);
+
+/* Grows sequence seqs[i] by n_new[i] tokens (NULL: by one), making the pages
+ * that they need its own: where its last page is partly filled and other rows
+ * hold it too (refs > 1 when the call begins), the row gets a page of its own
+ * in its place, with the slots in use copied in every layer (copy on write);
+ * then one page for every further page_size tokens.  Free pages go out lowest
+ * index first, to seqs[0] first.  Needs every page at once: where too few are
+ * free, or a row would pass max_pages, nothing changes and the device error
+ * word reports STAPLE_ERR_NO_PAGES.  n_seqs <= 4096. */
+size_t staple_kv_extend_workspace_bytes(const staple_kv_t* kv, int64_t n_seqs);
+staple_status_t staple_kv_extend(const staple_kv_t* kv, const int32_t* seqs, const int32_t* n_new,
+                                 int64_t n_seqs, void* ws, size_t ws_bytes, void* stream);
+
+/* Makes the empty row children[i] share parents[i]'s pages (a parent may be
+ * named more than once, but not among the children).  A child that is not
+ * empty sets the device error word and is skipped.  Uses refs, table, lens. */
+staple_status_t staple_kv_fork(const staple_kv_t* kv, const int32_t* parents,
+                               const int32_t* children, int64_t n, void* stream);
+
+/* Ends sequences: each page of row seqs[i] loses a reference, the row's
+ * entries become -1 and its length 0.  Uses refs, table, lens. */
+staple_status_t staple_kv_free(const staple_kv_t* kv, const int32_t* seqs, int64_t n, void* stream);
+
+/* Packs the live pages into the pool's low end: with n_live pages live, the
+ * k-th live page at or past n_live is copied, in every layer, to the k-th
+ * free page below it.  table_out, refs_out: the table and counts that go with
+ * the packed pool; they may be kv's own (in place) or other buffers, and then
+ * readers still running with the old table find its pages whole until
+ * something else is written to them.  *n_live: int32 device scalar.  A pool
+ * can afterwards be cut to n_live pages. */
+size_t staple_kv_compact_workspace_bytes(const staple_kv_t* kv);
+staple_status_t staple_kv_compact(const staple_kv_t* kv, int32_t* table_out, int32_t* refs_out,
+                                  int32_t* n_live, void* ws, size_t ws_bytes, void* stream);
+
+/* Copies page src[i] to page dst[i] in every layer, i < n (device int32
+ * arrays; no page is both a source and a destination, nor a destination
+ * twice).  Uses k_pages, v_pages. */
+staple_status_t staple_kv_copy_pages(const staple_kv_t* kv, const int32_t* src, const int32_t* dst,
+                                     int64_t n, void* stream);
+
+/* Attention of one new token per sequence over one layer's pages (n_layers 1;
+ * mask and formulas of staple_attn_fwd with the query at p = lens - 1).
+ *   q, o: n_seqs rows of n_heads; query i belongs to table row seqs[i]
+ *     (seqs NULL: row i); lse float[n_seqs x n_heads] or NULL;
+ *   k_new, v_new: NULL data, or n_seqs rows of n_kv_heads: the new token's
+ *     key and value, which the call also writes to position lens - 1 of the
+ *     cache (as staple_kv_append would);
+ *   max_len: a bound of the lengths, known on the host (<= max_pages
+ *     page_size); a longer sequence sets the device error word and is cut.
+ * The cache is split along its length over several workgroups where the
+ * batch alone does not fill the GPU; their partial results (workspace) are
+ * joined in a fixed order.  Uses kv's k_pages, v_pages, table, lens. */
+typedef struct staple_attn_decode_t {
+  int64_t n_seqs, n_heads, max_len, window, sinks;
+  float scale;
+  const int32_t* seqs;
+  staple_heads_t q, k_new, v_new, o;
+  float* lse;
+} staple_attn_decode_t;
+size_t staple_attn_decode_workspace_bytes(const staple_kv_t* kv, const staple_attn_decode_t* a);
+staple_status_t staple_attn_decode_paged(const staple_kv_t* kv, const staple_attn_decode_t* a,
+                                         void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

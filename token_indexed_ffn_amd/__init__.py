@@ -801,6 +801,242 @@ def staple_ffn_bwd_table_grad(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
     return out
 
 
+# ----------------------------------------------------------------------------
+# Attention and its key-value cache
+# ----------------------------------------------------------------------------
+_NO_HEADS = _lib.Heads(None, 0, 0)
+
+
+def _heads(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, rows: int, heads: int,
+           dim: int) -> _lib.Heads:
+    """A [rows, heads, dim] device tensor, dim contiguous; rows and heads may be strided."""
+    if t is None:
+        return _NO_HEADS
+    if not t.is_cuda or t.dtype != dtype or t.shape != (rows, heads, dim):
+        raise ValueError(f"{what}: needs a device tensor [{rows}, {heads}, {dim}] of {dtype}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    sr, sh, sd = t.stride()
+    if sd != 1 and dim > 1 and t.numel():
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return _lib.Heads(t.data_ptr(), sr, sh)
+
+
+def _ints(t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[int]:
+    """A contiguous int32 device tensor of n elements (None: any number)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: needs a contiguous int32 device tensor" +
+                         ("" if n is None else f" of {n} elements"))
+    return t.data_ptr()
+
+
+def _scale(scale: Optional[float], dim: int) -> float:
+    return dim ** -0.5 if scale is None else float(scale)
+
+
+def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, dq=None, dk=None,
+          dv=None) -> _lib.Attn:
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k are [tokens, heads, head_dim]")
+    tq, h, d = q.shape
+    tk, hk, _ = k.shape
+    n = cu_q.numel() - 1
+    if n < 0:
+        raise ValueError("cu_q and cu_k hold n_seqs + 1 offsets")
+    if lse.dtype != torch.float32 or lse.shape != (tq, h) or not lse.is_contiguous() or not lse.is_cuda:
+        raise ValueError(f"lse: needs a contiguous float32 device tensor [{tq}, {h}]")
+    dt = q.dtype
+    code = _dt(q)
+    return _lib.Attn(n, tq, tk, h, hk, d, int(window), int(sinks), _scale(scale, d), code,
+                     _ints(cu_q, "cu_q"), _ints(cu_k, "cu_k", n + 1),
+                     _heads(q, "q", dt, tq, h, d), _heads(k, "k", dt, tk, hk, d),
+                     _heads(v, "v", dt, tk, hk, d), _heads(o, "o", dt, tq, h, d), lse.data_ptr(),
+                     _heads(do, "do", dt, tq, h, d), _heads(dq, "dq", dt, tq, h, d),
+                     _heads(dk, "dk", dt, tk, hk, d), _heads(dv, "dv", dt, tk, hk, d))
+
+
+def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                    cu_k: torch.Tensor, *, window: int = 0, sinks: int = 0,
+                    scale: Optional[float] = None, out: Optional[dict] = None,
+                    stream=None) -> dict:
+    """Causal attention of packed sequences: o [tokens, heads, head_dim] and lse
+    [tokens, heads].  q [tokens, heads, head_dim]; k, v [key tokens, kv heads, head_dim]
+    (strided views, such as slices of one fused projection, are read in place); cu_q, cu_k
+    int32 offsets of the sequences.  A query at position p sees key j when j <= p and
+    (window == 0 or j > p - window or j < sinks); the queries are the last positions of
+    their sequence.  scale: head_dim ** -0.5 when None."""
+    if out is None:
+        out = {"o": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
+    a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"])
+    _check(lib().staple_attn_fwd(ctypes.byref(a), _stream(stream)), "staple_attn_fwd")
+    return out
+
+
+def staple_attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    o: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, *,
+                    window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                    out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> dict:
+    """Gradients dq, dk, dv of staple_attn_fwd from do, its operands and its o and lse."""
+    if out is None:
+        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               "dk": torch.empty(k.shape, dtype=k.dtype, device=q.device),
+               "dv": torch.empty(v.shape, dtype=v.dtype, device=q.device)}
+    a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do, out["dq"], out["dk"], out["dv"])
+    ws = _ws(lib().staple_attn_bwd_workspace_bytes(ctypes.byref(a)), workspace, q.device)
+    _check(lib().staple_attn_bwd(ctypes.byref(a), _p(ws), _ws_size(ws), _stream(stream)),
+           "staple_attn_bwd")
+    return out
+
+
+def _kv(refs=None, table=None, lens=None, k_pages=None, v_pages=None,
+        page_size: Optional[int] = None) -> _lib.Kv:
+    """staple_kv_t of a cache: pools [layers, pages, kv heads, page size, head_dim] or one
+    layer's [pages, kv heads, page size, head_dim]."""
+    layers, pages, hk, size, d, dt = 1, 1, 1, page_size, 8, F32
+    if k_pages is not None:
+        _dev(k_pages, v_pages)
+        if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() not in (4, 5):
+            raise ValueError("k_pages and v_pages are pools of one shape and dtype")
+        layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+        pages, hk, size, d = k_pages.shape[-4:]
+        dt = _dt(k_pages)
+    if refs is not None:
+        if k_pages is None:
+            pages = refs.numel()
+        _ints(refs, "refs", pages)
+    rows, width = 1, 1
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table is [rows, max pages]")
+        rows, width = table.shape
+        _ints(table, "table")
+        _ints(lens, "lens", rows)
+    return _lib.Kv(layers, pages, hk, size, d, rows, width, dt, _p(k_pages), _p(v_pages), _p(refs),
+                   _p(table), _p(lens))
+
+
+def staple_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                     v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                     seqs: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None, *,
+                     stream=None) -> None:
+    """Writes the last tokens of sequences (table rows) `seqs` into one layer's pages: rows
+    [cu_new[i], cu_new[i + 1]) of k_new, v_new are sequence seqs[i]'s (cu_new None: one row
+    each; seqs None: row i).  lens already counts them."""
+    kv = _kv(None, table, lens, k_pages, v_pages)
+    n = k_new.shape[0]
+    hk, d = k_pages.shape[-3], k_pages.shape[-1]
+    n_seqs = cu_new.numel() - 1 if cu_new is not None else n
+    kn = _heads(k_new, "k_new", k_pages.dtype, n, hk, d)
+    vn = _heads(v_new, "v_new", k_pages.dtype, n, hk, d)
+    _check(lib().staple_kv_append(ctypes.byref(kv), ctypes.byref(kn), ctypes.byref(vn), n,
+                                  _ints(seqs, "seqs", n_seqs), n_seqs, _ints(cu_new, "cu_new"),
+                                  _stream(stream)), "staple_kv_append")
+
+
+def staple_kv_extend(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                     seqs: torch.Tensor, n_new: Optional[torch.Tensor] = None, *,
+                     k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Grows each sequence seqs[i] by n_new[i] tokens (None: one), with pages of its own for
+    them: a shared, partly filled last page is copied in every layer, further pages come
+    from the free ones, lowest index first.  Too few pages: nothing changes, and
+    staple_get_device_error reports it."""
+    kv = _kv(refs, table, lens, k_pages, v_pages)
+    n = seqs.numel()
+    ws = _ws(lib().staple_kv_extend_workspace_bytes(ctypes.byref(kv), n), workspace, refs.device)
+    _check(lib().staple_kv_extend(ctypes.byref(kv), _ints(seqs, "seqs"), _ints(n_new, "n_new", n), n,
+                                  _p(ws), _ws_size(ws), _stream(stream)), "staple_kv_extend")
+
+
+def staple_kv_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                   parents: torch.Tensor, children: torch.Tensor, *, page_size: int,
+                   stream=None) -> None:
+    """The empty rows children[i] come to share the pages of rows parents[i]."""
+    kv = _kv(refs, table, lens, page_size=page_size)
+    n = children.numel()
+    _check(lib().staple_kv_fork(ctypes.byref(kv), _ints(parents, "parents", n),
+                                _ints(children, "children"), n, _stream(stream)), "staple_kv_fork")
+
+
+def staple_kv_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, seqs: torch.Tensor,
+                   *, page_size: int, stream=None) -> None:
+    """Ends sequences: their pages lose a reference, their rows become empty."""
+    kv = _kv(refs, table, lens, page_size=page_size)
+    _check(lib().staple_kv_free(ctypes.byref(kv), _ints(seqs, "seqs"), seqs.numel(),
+                                _stream(stream)), "staple_kv_free")
+
+
+def staple_kv_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      k_pages: torch.Tensor, v_pages: torch.Tensor, *, out: Optional[dict] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Packs the live pages into the pool's low end and returns the packed pool's "refs" and
+    "table" (in place when `out` gives none) and "n_live" (device int32)."""
+    kv = _kv(refs, table, lens, k_pages, v_pages)
+    out = dict(out or {})
+    for name, own in (("refs", refs), ("table", table)):
+        out.setdefault(name, own)
+        _ints(out[name], name, own.numel())
+    if "n_live" not in out:
+        out["n_live"] = torch.empty(1, dtype=torch.int32, device=refs.device)
+    ws = _ws(lib().staple_kv_compact_workspace_bytes(ctypes.byref(kv)), workspace, refs.device)
+    _check(lib().staple_kv_compact(ctypes.byref(kv), _p(out["table"]), _p(out["refs"]),
+                                   _ints(out["n_live"], "n_live", 1), _p(ws), _ws_size(ws),
+                                   _stream(stream)), "staple_kv_compact")
+    return out
+
+
+def staple_kv_copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, src: torch.Tensor,
+                         dst: torch.Tensor, *, stream=None) -> None:
+    """Page src[i] to page dst[i] in every layer."""
+    kv = _kv(None, None, None, k_pages, v_pages)
+    n = src.numel()
+    _check(lib().staple_kv_copy_pages(ctypes.byref(kv), _ints(src, "src"), _ints(dst, "dst", n), n,
+                                      _stream(stream)), "staple_kv_copy_pages")
+
+
+def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                             table: torch.Tensor, lens: torch.Tensor, *,
+                             seqs: Optional[torch.Tensor] = None,
+                             k_new: Optional[torch.Tensor] = None,
+                             v_new: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                             window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                             out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> dict:
+    """Attention of one new token per sequence over one layer's pages: o [n, heads,
+    head_dim] and lse [n, heads].  Query i belongs to table row seqs[i] (None: row i) and
+    stands at position lens - 1.  k_new, v_new [n, kv heads, head_dim]: the new tokens' keys
+    and values, also written to the cache.  max_len: a bound of the lengths known on the
+    host (None: the table's width)."""
+    kv = _kv(None, table, lens, k_pages, v_pages)
+    n, h, d = q.shape
+    hk = k_pages.shape[-3]
+    dt = k_pages.dtype
+    if out is None:
+        out = {"o": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               "lse": torch.empty((n, h), dtype=torch.float32, device=q.device)}
+    lse = out.get("lse")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, h) or
+                            not lse.is_contiguous() or not lse.is_cuda):
+        raise ValueError(f"lse: needs a contiguous float32 device tensor [{n}, {h}]")
+    if d != k_pages.shape[-1]:
+        raise ValueError("q and the pages have one head_dim")
+    if max_len is None:
+        max_len = table.shape[1] * k_pages.shape[-2]
+    a = _lib.AttnDecode(n, h, int(max_len), int(window), int(sinks), _scale(scale, d),
+                        _ints(seqs, "seqs", n), _heads(q, "q", dt, n, h, d),
+                        _heads(k_new, "k_new", dt, n, hk, d), _heads(v_new, "v_new", dt, n, hk, d),
+                        _heads(out["o"], "o", dt, n, h, d), _p(lse))
+    ws = _ws(lib().staple_attn_decode_workspace_bytes(ctypes.byref(kv), ctypes.byref(a)), workspace,
+             q.device)
+    _check(lib().staple_attn_decode_paged(ctypes.byref(kv), ctypes.byref(a), _p(ws), _ws_size(ws),
+                                          _stream(stream)), "staple_attn_decode_paged")
+    return out
+
+
 def ffn_workspace_bytes(n: int, d: int, f: int, dtype: torch.dtype) -> dict:
     return {"fwd": lib().staple_ffn_fwd_workspace_bytes(n, d, f, _DT[dtype]),
             "bwd": lib().staple_ffn_bwd_workspace_bytes(n, d, f, _DT[dtype]),

@@ -91,7 +91,50 @@ _SIGS = {
                                         c_vp, c_i64, c_vp]),
     "staple_host_adamw_finish": (c_i32, [c_vp, c_vp]),
     "staple_host_adamw_destroy": (None, [c_vp]),
+    "staple_attn_fwd": (c_i32, [c_vp, c_vp]),
+    "staple_attn_bwd_workspace_bytes": (c_sz, [c_vp]),
+    "staple_attn_bwd": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "staple_kv_append": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "staple_kv_extend_workspace_bytes": (c_sz, [c_vp, c_i64]),
+    "staple_kv_extend": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp, c_sz, c_vp]),
+    "staple_kv_fork": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "staple_kv_free": (c_i32, [c_vp, c_vp, c_i64, c_vp]),
+    "staple_kv_compact_workspace_bytes": (c_sz, [c_vp]),
+    "staple_kv_compact": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "staple_kv_copy_pages": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "staple_attn_decode_workspace_bytes": (c_sz, [c_vp, c_vp]),
+    "staple_attn_decode_paged": (c_i32, [c_vp, c_vp, c_vp, c_sz, c_vp]),
 }
+
+
+class Heads(ctypes.Structure):
+    """staple_heads_t"""
+    _fields_ = [("data", c_vp), ("row_stride", c_i64), ("head_stride", c_i64)]
+
+
+class Attn(ctypes.Structure):
+    """staple_attn_t"""
+    _fields_ = ([(n, c_i64) for n in ("n_seqs", "total_q", "total_k", "n_heads", "n_kv_heads",
+                                      "head_dim", "window", "sinks")] +
+                [("scale", c_f32), ("dtype", c_i32), ("cu_q", c_vp), ("cu_k", c_vp),
+                 ("q", Heads), ("k", Heads), ("v", Heads), ("o", Heads), ("lse", c_vp),
+                 ("d_o", Heads), ("dq", Heads), ("dk", Heads), ("dv", Heads)])
+
+
+class Kv(ctypes.Structure):
+    """staple_kv_t"""
+    _fields_ = ([(n, c_i64) for n in ("n_layers", "n_pages", "n_kv_heads", "page_size", "head_dim",
+                                      "n_rows", "max_pages")] +
+                [("dtype", c_i32)] +
+                [(n, c_vp) for n in ("k_pages", "v_pages", "refs", "table", "lens")])
+
+
+class AttnDecode(ctypes.Structure):
+    """staple_attn_decode_t"""
+    _fields_ = ([(n, c_i64) for n in ("n_seqs", "n_heads", "max_len", "window", "sinks")] +
+                [("scale", c_f32), ("seqs", c_vp), ("q", Heads), ("k_new", Heads),
+                 ("v_new", Heads), ("o", Heads), ("lse", c_vp)])
+
 
 EXPORTED = tuple(_SIGS)
 

@@ -8,6 +8,7 @@
 #include <thread>
 #include <vector>
 
+#include "api_util.h"
 #include "common.h"
 #include "dma.h"
 #include "host_pool.h"
@@ -189,10 +190,6 @@ static void* device_scratch() {
   return g_scratch_ptr[dev];
 }
 
-static inline int elem_bytes(int32_t dt) { return dt == STAPLE_BF16 ? 2 : 4; }
-static inline bool valid_dtype(int32_t dt) { return dt == STAPLE_BF16 || dt == STAPLE_F32; }
-static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // True when kernels can address `p`: device memory, or pinned (registered or
 // hipHostMalloc'd) host memory.  Pageable host memory is refused on the host
 // instead of faulting in a kernel.  A failed query leaves no error behind.
@@ -219,25 +216,9 @@ static bool host_memory(const void* p) {
 constexpr unsigned kHostCopyWorkgroups = 64;
 static unsigned copy_workgroups(const void* src) { return host_memory(src) ? kHostCopyWorkgroups : 0; }
 
-static inline hipStream_t S(void* s) { return static_cast<hipStream_t>(s); }
-
 }  // namespace staple
 
 using namespace staple;
-
-#define REQUIRE(cond)                                   \
-  do {                                                  \
-    if (!(cond)) return STAPLE_ERR_INVALID_ARGUMENT;    \
-  } while (0)
-
-#define HIPCALL(expr)                                   \
-  do {                                                  \
-    if ((expr) != hipSuccess) return STAPLE_ERR_HIP;    \
-  } while (0)
-
-#define GET_ERR(var)                                    \
-  int* var = device_error_word();                       \
-  if (var == nullptr) return STAPLE_ERR_HIP
 
 extern "C" {
 
@@ -252,6 +233,7 @@ const char* staple_status_string(staple_status_t st) {
     case STAPLE_ERR_HOST: return "host-side failure";
     case STAPLE_ERR_SCRATCH_LIMIT:
       return "problem larger than the fixed device scratch of the allocation-free entry point";
+    case STAPLE_ERR_NO_PAGES: return "key-value cache out of pages";
     default: return "unknown status";
   }
 }
@@ -267,7 +249,7 @@ staple_status_t staple_get_device_error(void* stream) {
     int zero = 0;
     HIPCALL(hipMemcpyAsync(err, &zero, sizeof(int), hipMemcpyHostToDevice, S(stream)));
     HIPCALL(hipStreamSynchronize(S(stream)));
-    return STAPLE_ERR_INDEX_RANGE;
+    return (v & kErrIndexRange) ? STAPLE_ERR_INDEX_RANGE : STAPLE_ERR_NO_PAGES;
   }
   return STAPLE_OK;
 }

@@ -109,9 +109,11 @@ template <> struct Elem<bf16_t> {
 // about 1 ulp) rather than an IEEE division.
 __device__ __forceinline__ float sigmoidf_(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
-// Kernels that meet an out-of-range ID or index OR this bit into the
-// per-device error word whose address they receive as `err`.
+// Kernels that meet an out-of-range ID or index, or find a key-value cache
+// out of pages, OR these bits into the per-device error word whose address
+// they receive as `err`.
 constexpr int kErrIndexRange = 1;
+constexpr int kErrNoPages = 2;
 
 __device__ __forceinline__ void flag_index_error(int* err) { atomicOr(err, kErrIndexRange); }
 
