@@ -32,7 +32,7 @@ static staple_status_t attn_check(const staple_attn_t* a) {
   REQUIRE(a->window >= 0 && a->sinks >= 0 && std::isfinite(a->scale));
   if (a->n_seqs > kMaxCount - 1 || a->total_q > kMaxCount || a->total_k > kMaxCount ||
       a->n_heads > 65535 || a->total_q * a->n_heads > kMaxLaunchRows * 64 ||
-      a->total_k * a->n_kv_heads > kMaxLaunchRows * 64)
+      a->total_k * a->n_kv_heads > kMaxLaunchRows * 64 || a->n_seqs * a->n_heads > kMaxLaunchRows)
     return STAPLE_ERR_UNSUPPORTED;
   return STAPLE_OK;
 }

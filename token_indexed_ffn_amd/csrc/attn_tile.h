@@ -1,0 +1,217 @@
+// LDS tiles of the attention kernels and the matrix products over them.
+//
+// A tile holds rows (tokens) of one head, DP elements each (head_dim rounded
+// up to 64 or 128; the rest is zeros), as they lie in memory.  Every product
+// of the forward and backward pass puts a tile on the MFMA's A side (32 rows
+// of v_mfma_f32_32x32x16_bf16, or of v_mfma_f32_32x32x2_f32) and keeps the B
+// side in registers, one query (or key) a column:
+//   - by rows:    A = 32 tile rows, contracted over head_dim;
+//   - transposed: A = 32 head elements, contracted over the tile's rows.
+// The result of the first kind has tile row 8 (r / 4) + 4 h + r % 4 of column
+// c in register r of lane c + 32 h, which is the B operand of the second kind
+// as it stands once the contraction visits the rows in that order: no score
+// ever moves between lanes.
+//
+// 16-byte chunks of a row are XORed with a function of the row so that both
+// kinds of read spread over the LDS banks: 16 consecutive rows at one chunk
+// (16-byte reads) fall on 16 different chunks, and the two-chunk pieces that
+// 4 consecutive rows give a transposing read fall on different banks.
+#pragma once
+
+#include "attn.h"
+
+namespace staple {
+
+typedef short v4s_t __attribute__((ext_vector_type(4)));
+typedef short v8s_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4s_t lds_v4s_t;
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+typedef __attribute__((address_space(3))) float lds_f32;
+
+template <typename T, int DP>
+struct Tile {
+  static constexpr int kRow = DP * static_cast<int>(sizeof(T));   // bytes per row
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kSteps = kRow / 32;                        // 16-byte A reads per lane and row block
+  static constexpr int kDT = DP / 32;                             // 32-element blocks of head_dim
+
+  __device__ __forceinline__ static int spread(int row) {
+    if constexpr (kChunks >= 16) return ((row & 7) << 1) | ((row >> 3) & 1);
+    else return (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+  }
+  // By rows: the lane's 16 bytes of row `row0 + lane % 32`, step s.
+  __device__ __forceinline__ static u32x4_t row_frag(const lds_char* tile, int row0, int s) {
+    const int lane = threadIdx.x & 63, row = row0 + (lane & 31);
+    return *reinterpret_cast<const lds_u32x4*>(tile + row * kRow + (((2 * s + (lane >> 5)) ^ spread(row)) << 4));
+  }
+};
+
+__device__ __forceinline__ f32x16_t mma16(const u32x4_t& a, const u32x4_t& b, f32x16_t acc, bf16_t) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                 acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma16(const u32x4_t& a, const u32x4_t& b, f32x16_t acc, float) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc, 0, 0, 0);
+  return acc;
+}
+
+// The B operand of the transposed products: 16 (bf16) or 8 (fp32) tile rows
+// of one column block, from half (bf16) or a quarter (fp32) of a result.
+template <typename T> struct Column;
+template <> struct Column<bf16_t> {
+  u32x4_t v[2];   // rows 0-15, rows 16-31 of the block, rounded to bf16
+  __device__ __forceinline__ void set(const f32x16_t& x) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[t][i] = pack_bf16x2(x[8 * t + 2 * i], x[8 * t + 2 * i + 1]);
+  }
+};
+template <> struct Column<float> {
+  f32x16_t v;
+  __device__ __forceinline__ void set(const f32x16_t& x) { v = x; }
+};
+
+// acc += (rows [row0, row0 + 32) of the tile, elements [32 dt, 32 dt + 32))^T x column.
+template <int DP>
+__device__ __forceinline__ f32x16_t mma_transposed(const lds_char* tile, int row0, int dt,
+                                                   const Column<bf16_t>& col, f32x16_t acc) {
+  using TL = Tile<bf16_t, DP>;
+  const int lane = threadIdx.x & 63, i16 = lane & 15;
+  // 16 lanes read 4 rows x 16 elements and get 4 rows of one element each
+  const int c = dt * 32 + (lane & 16) + 4 * (i16 & 3);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    v4s_t part[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = row0 + 16 * t + 8 * e + 4 * (lane >> 5) + (i16 >> 2);
+      const lds_char* p = tile + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
+      part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p);
+    }
+    const v8s_t a = {part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2], part[1][3]};
+    acc = mma16(__builtin_bit_cast(u32x4_t, a), col.v[t], acc, bf16_t{});
+  }
+  return acc;
+}
+template <int DP>
+__device__ __forceinline__ f32x16_t mma_transposed(const lds_char* tile, int row0, int dt,
+                                                   const Column<float>& col, f32x16_t acc) {
+  using TL = Tile<float, DP>;
+  const int lane = threadIdx.x & 63;
+  const int c = dt * 32 + (lane & 31);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+    const float v = *reinterpret_cast<const lds_f32*>(tile + row * TL::kRow + (((c >> 2) ^ TL::spread(row)) << 4) + (c & 3) * 4);
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v, col.v[r], acc, 0, 0, 0);
+  }
+  return acc;
+}
+
+// Zeros read in place of rows past a sequence and elements past head_dim.
+__device__ const uint4 g_attn_zeros[1] = {};
+
+// Copies R-row tiles of one head from global memory straight into LDS, 16
+// bytes a lane.  Instruction i of wave w fills 1 KB of the tile; the lane's
+// source is the chunk that its LDS place holds.
+template <typename T, int DP, int R, int NW>
+struct TileLoader {
+  using TL = Tile<T, DP>;
+  static constexpr int kPer = R * TL::kRow / (1024 * NW);
+  static_assert(kPer * 1024 * NW == R * TL::kRow, "tile shape");
+  const char* base;        // row 0 of the sequence, this head
+  int64_t row_bytes;
+  int dim_bytes;
+
+  __device__ __forceinline__ void init(const HeadsView& t, int64_t row, int64_t head, int dim) {
+    row_bytes = t.row_stride * static_cast<int64_t>(sizeof(T));
+    base = t.data + row * row_bytes + head * t.head_stride * static_cast<int64_t>(sizeof(T));
+    dim_bytes = dim * static_cast<int>(sizeof(T));
+  }
+  // Rows [row0, row0 + R) of the sequence's n.
+  __device__ __forceinline__ void load(int64_t row0, int64_t n, lds_char* lds) const {
+    const int w = threadIdx.x >> 6;
+    const int left = static_cast<int>(n - row0 < R ? n - row0 : R);
+    const char* tile = base + row0 * row_bytes;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int byte = (i * NW + w) * 1024 + (threadIdx.x & 63) * 16;
+      const int row = byte / TL::kRow;
+      const int chunk = (byte % TL::kRow / 16) ^ TL::spread(row);
+      const char* src = tile + row * row_bytes + chunk * 16;
+      const bool in = row < left && chunk * 16 < dim_bytes;
+      dma16(in ? static_cast<const void*>(src) : static_cast<const void*>(g_attn_zeros),
+            static_cast<lds_void*>(lds + (i * NW + w) * 1024));
+    }
+  }
+};
+
+// The lane's 16 bytes of step s of row `row` (zeros where !in or past dim).
+template <typename T>
+__device__ __forceinline__ u32x4_t load_frag(const HeadsView& t, int64_t row, int64_t head, int dim, int s, bool in) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  const int e = (2 * s + ((threadIdx.x & 63) >> 5)) * kVec;
+  if (!in || e >= dim) return u32x4_t{0, 0, 0, 0};
+  return *reinterpret_cast<const u32x4_t*>(t.data + (row * t.row_stride + head * t.head_stride + e) * static_cast<int64_t>(sizeof(T)));
+}
+// The operand negated (sign bits flipped, exactly).
+template <typename T>
+__device__ __forceinline__ u32x4_t flip_sign(u32x4_t v) {
+  const uint32_t m = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+  return v ^ u32x4_t{m, m, m, m};
+}
+
+// The other half-wave's value of the same column.
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// Stores a transposed result's column (head elements 32 dt + 8 (r / 4) + 4 h +
+// r % 4 of one row) times `mul` as 16-byte pieces: the half-waves trade 4-element
+// groups first, so that each lane holds 8 consecutive elements (fp32: 4).
+template <typename T>
+__device__ __forceinline__ void store_column(const HeadsView& t, int64_t row, int64_t head, int dim, int dt,
+                                             const f32x16_t& x, float mul, bool in);
+template <>
+__device__ __forceinline__ void store_column<bf16_t>(const HeadsView& t, int64_t row, int64_t head, int dim, int dt,
+                                                     const f32x16_t& x, float mul, bool in) {
+  const int h = (threadIdx.x & 63) >> 5;
+  char* p = t.data + (row * t.row_stride + head * t.head_stride) * 2;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t a[2], b[2];   // groups 2 g and 2 g + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = pack_bf16x2(x[8 * g + 2 * i] * mul, x[8 * g + 2 * i + 1] * mul);
+      b[i] = pack_bf16x2(x[8 * g + 4 + 2 * i] * mul, x[8 * g + 4 + 2 * i + 1] * mul);
+    }
+    // lower lanes keep group 2 g and take the upper lanes' half of it
+    const uint32_t s0 = h ? a[0] : b[0], s1 = h ? a[1] : b[1];
+    const uint32_t o0 = __shfl_xor(s0, 32), o1 = __shfl_xor(s1, 32);
+    const u32x4_t v = h ? u32x4_t{o0, o1, b[0], b[1]} : u32x4_t{a[0], a[1], o0, o1};
+    const int e = dt * 32 + 16 * g + 8 * h;
+    if (in && e < dim) *reinterpret_cast<u32x4_t*>(p + e * 2) = v;
+  }
+}
+template <>
+__device__ __forceinline__ void store_column<float>(const HeadsView& t, int64_t row, int64_t head, int dim, int dt,
+                                                    const f32x16_t& x, float mul, bool in) {
+  const int h = (threadIdx.x & 63) >> 5;
+  char* p = t.data + (row * t.row_stride + head * t.head_stride) * 4;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int e = dt * 32 + 8 * g + 4 * h;
+    if (in && e < dim)
+      *reinterpret_cast<f32x4_t*>(p + e * 4) = f32x4_t{x[4 * g] * mul, x[4 * g + 1] * mul, x[4 * g + 2] * mul, x[4 * g + 3] * mul};
+  }
+}
+
+// Which of a 32-row key block's rows a query sees, and the other way round:
+// `at` is the relative position of the lane's column, rows are numbered as in
+// a result's registers.  Positions are clamped to small integers first.
+__device__ __forceinline__ int clamp_rel(int64_t v) {
+  return static_cast<int>(v < -(1 << 20) ? -(1 << 20) : v > (1 << 20) ? (1 << 20) : v);
+}
+
+}  // namespace staple

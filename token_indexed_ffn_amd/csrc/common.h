@@ -30,6 +30,19 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// One 16-byte-per-lane global -> LDS load (global_load_lds_dwordx4: lane l
+// writes LDS bytes [dst + 16 l, +16), dst wave-uniform, passed in M0).  It is
+// issued from inline asm so that the compiler does not count it among the
+// LDS-counter events: with such a load in flight it would otherwise wait for
+// every outstanding LDS read (lgkmcnt(0)) before each MFMA group instead of
+// only the ones the group needs.  The asm has no register outputs (the data
+// goes to LDS); its completion is waited for by hand (vmcnt) before the
+// barrier that publishes the stage, as for the builtin form.
+__device__ __forceinline__ void dma16(const void* src, lds_void* dst) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+
 // Compute units of the current device, looked up once per device (256 when
 // the query fails).
 inline int device_cus() {
