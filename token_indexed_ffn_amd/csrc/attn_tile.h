@@ -27,6 +27,7 @@ typedef short v8s_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4s_t lds_v4s_t;
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
 typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) f32x4_t lds_f32x4;
 
 template <typename T, int DP>
 struct Tile {
@@ -157,6 +158,22 @@ __device__ __forceinline__ u32x4_t load_frag(const HeadsView& t, int64_t row, in
   if (!in || e >= dim) return u32x4_t{0, 0, 0, 0};
   return *reinterpret_cast<const u32x4_t*>(t.data + (row * t.row_stride + head * t.head_stride + e) * static_cast<int64_t>(sizeof(T)));
 }
+// Sum of the products of two such pieces.
+__device__ __forceinline__ float dot_frag(const u32x4_t& a, const u32x4_t& b, bf16_t) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s += __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16);
+    s += __uint_as_float(a[i] & 0xffff0000u) * __uint_as_float(b[i] & 0xffff0000u);
+  }
+  return s;
+}
+__device__ __forceinline__ float dot_frag(const u32x4_t& a, const u32x4_t& b, float) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s += __uint_as_float(a[i]) * __uint_as_float(b[i]);
+  return s;
+}
 // The operand negated (sign bits flipped, exactly).
 template <typename T>
 __device__ __forceinline__ u32x4_t flip_sign(u32x4_t v) {
@@ -207,9 +224,7 @@ __device__ __forceinline__ void store_column<float>(const HeadsView& t, int64_t 
   }
 }
 
-// Which of a 32-row key block's rows a query sees, and the other way round:
-// `at` is the relative position of the lane's column, rows are numbered as in
-// a result's registers.  Positions are clamped to small integers first.
+// Relative positions as small integers (a tile is far narrower than the clamp).
 __device__ __forceinline__ int clamp_rel(int64_t v) {
   return static_cast<int>(v < -(1 << 20) ? -(1 << 20) : v > (1 << 20) ? (1 << 20) : v);
 }

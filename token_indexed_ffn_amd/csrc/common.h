@@ -43,6 +43,12 @@ __device__ __forceinline__ void dma16(const void* src, lds_void* dst) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
 }
 
+// One 4-byte-per-lane global -> LDS load (lane l writes LDS bytes [dst + 4 l, +4)).
+__device__ __forceinline__ void dma4(const void* src, lds_void* dst) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+
 // Compute units of the current device, looked up once per device (256 when
 // the query fails).
 inline int device_cus() {
