@@ -30,7 +30,7 @@ static staple_status_t attn_check(const staple_attn_t* a) {
   REQUIRE(a->n_seqs >= 0 && a->total_q >= 0 && a->total_k >= 0);
   REQUIRE(a->n_heads >= 1 && a->n_kv_heads >= 1 && a->n_heads % a->n_kv_heads == 0);
   REQUIRE(a->window >= 0 && a->sinks >= 0 && std::isfinite(a->scale));
-  if (a->n_seqs > kMaxCount - 1 || a->total_q > kMaxCount || a->total_k > kMaxCount ||
+  if (a->n_seqs > kMaxTokens || a->total_q > kMaxTokens || a->total_k > kMaxTokens ||
       a->n_heads > 65535 || a->total_q * a->n_heads > kMaxLaunchRows * 64 ||
       a->total_k * a->n_kv_heads > kMaxLaunchRows * 64 || a->n_seqs * a->n_heads > kMaxLaunchRows)
     return STAPLE_ERR_UNSUPPORTED;
@@ -46,8 +46,9 @@ static AttnView view(const staple_attn_t* a) {
   v.n_kv_heads = static_cast<int>(a->n_kv_heads);
   v.group = static_cast<int>(a->n_heads / a->n_kv_heads);
   v.head_dim = static_cast<int>(a->head_dim);
-  v.window = a->window;
-  v.sinks = a->sinks;
+  // a window past every position hides nothing; more sinks than positions are all of them
+  v.window = a->window >= kMaxTokens ? 0 : static_cast<int>(a->window);
+  v.sinks = a->sinks >= kMaxTokens ? kMaxTokens : static_cast<int>(a->sinks);
   v.scale = a->scale;
   v.cu_q = a->cu_q;
   v.cu_k = a->cu_k;

@@ -6,10 +6,17 @@
 
 namespace staple {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Positions and row numbers stay below this, so that 32-bit sums of a
+// few of them cannot overflow.
+constexpr int kMaxTokens = 1 << 29;
+
 struct AttnView {
   int64_t n_seqs, total_q, total_k;
   int n_heads, n_kv_heads, group, head_dim;
-  int64_t window, sinks;   // window 0: every key up to the query's position
+  int window, sinks;       // window 0: every key up to the query's position
   float scale;
   const int32_t* cu_q;
   const int32_t* cu_k;

@@ -1,10 +1,183 @@
 // Attention over packed sequences with a causal mask, a sliding window and
 // sinks: forward and backward.
+//
+// A workgroup is four waves of 32 queries (or, for dk and dv, keys), one a
+// column of the products of attn_tile.h; the rows they meet come through LDS,
+// 32 at a time, in rings of slots filled a few blocks ahead.  All three bf16
+// kernels are bound by what a wave can issue: matrix products, exponentials
+// and LDS reads together.  So they spread one block's vector work between the
+// products of other blocks, and keep their loop free of address and mask work:
+// positions are 32-bit, a head's rows are one buffer, and only blocks at the
+// edge of what is seen apply a mask.
+#include <type_traits>
+
 #include "attn_row.h"
 #include "attn_tile.h"
 
 namespace staple {
 
+constexpr int kWaves = 4;
+constexpr int kTileRows = 32 * kWaves;   // queries (keys) of a workgroup
+
+// A tile of kTileRows consecutive rows of one sequence.  Sequence b owns the
+// slots floor(cu[b] / kTileRows) + b onwards, at least as many as it has
+// tiles, so a grid of total / kTileRows + n_seqs slots holds every sequence
+// and a workgroup finds its own by a search of cu alone.
+struct TileOf {
+  int64_t seq, first;   // first: the tile's first row within the sequence; seq -1: none
+};
+__device__ __forceinline__ TileOf tile_of_slot(const int32_t* cu, int64_t n_seqs, int64_t slot) {
+  int64_t lo = 0, hi = n_seqs;   // slots of lo start at or before `slot`, those of hi after
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (cu[mid] / kTileRows + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  const int64_t tile = slot - (cu[lo] / kTileRows + lo);
+  return TileOf{tile < 0 ? -1 : lo, tile * kTileRows};
+}
+static int64_t slots(int64_t total, int64_t n_seqs) { return total / kTileRows + n_seqs; }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_id() { return uniform(threadIdx.x >> 6); }
+
+// One sequence and head, and the workgroup's tile of its queries or keys.
+struct Segment {
+  int64_t q0, k0;          // first rows
+  int nq, nk, past;        // lengths, and the position of query 0
+  int first;               // the tile's first query (key)
+  // False where the workgroup has nothing to do.
+  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int64_t slot, int* err) {
+    const TileOf tile = tile_of_slot(cu, a.n_seqs, slot);
+    if (tile.seq < 0) return false;
+    int64_t q1, k1;
+    seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
+    seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
+    if (tile.first >= (cu == a.cu_q ? q1 - q0 : k1 - k0)) return false;
+    // the same for every lane, and kept in scalar registers
+    nq = uniform(static_cast<int>(q1 - q0));
+    nk = uniform(static_cast<int>(k1 - k0));
+    past = nk - nq;
+    first = uniform(static_cast<int>(tile.first));
+    q0 = uniform(static_cast<int>(q0));
+    k0 = uniform(static_cast<int>(k0));
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------- masks
+// Applied with selects (a few integer compares an element), never by branching
+// on one element of a result.
+
+// Which keys of a block the lane's query (at position p) sees: key j = 8 (r /
+// 4) + r % 4 (+ 4 for the upper half-wave) of the block at `key` is seen when
+// j <= hi and (j >= lo or j < sink).
+struct SeenKeys {
+  int hi, lo, sink;
+  __device__ __forceinline__ SeenKeys(const AttnView& a, int p, bool in, int key) {
+    const int at = key + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+    hi = in ? p - at : -1;
+    lo = a.window > 0 ? p - a.window + 1 - at : -kMaxTokens;
+    sink = a.sinks - at;
+  }
+  __device__ __forceinline__ bool operator()(int r) const {
+    const int j = 8 * (r >> 2) + (r & 3);
+    return (j <= hi) & ((j >= lo) | (j < sink));
+  }
+};
+// Which queries of a block (the first is number i0 of the sequence) see the
+// lane's key.
+struct SeenBy {
+  int lo, hi;
+  __device__ __forceinline__ SeenBy(const AttnView& a, const Segment& s, int key, bool in, int i0) {
+    const int at = i0 + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+    lo = key - s.past - at;
+    int end = s.nq;
+    if (a.window > 0 && key >= a.sinks) end = min(end, key - s.past + a.window);
+    hi = in ? end - at : -1;
+  }
+  __device__ __forceinline__ bool operator()(int r) const {
+    const int j = 8 * (r >> 2) + (r & 3);
+    return (j >= lo) & (j < hi);
+  }
+};
+
+// True where a value is NaN or infinite.
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
+
+// The 32-key blocks that some query at a position in [p_min, p_max] sees: those
+// of the sinks, then the window's; and which of them every query of the wave's
+// range sees whole.
+struct KeyBlocks {
+  int n_sink, lo, n;
+  int nk;
+  int whole_sink, whole_lo, whole_n;
+  __device__ __forceinline__ KeyBlocks(const AttnView& a, int n_keys, int p_min, int p_max) : nk(n_keys) {
+    lo = (a.window > 0 ? max(p_min - a.window + 1, 0) : 0) / 32;
+    n_sink = p_max < 0 ? 0 : (min(a.sinks, lo * 32) + 31) / 32;
+    n = p_max < 0 ? 0 : n_sink + p_max / 32 + 1 - lo;
+    whole_sink = whole_n = 0;
+  }
+  // The wave's own queries: positions [p_min, p_max], all 32 of them there.
+  __device__ __forceinline__ void set_wave(const AttnView& a, int p_min, int p_max, bool full) {
+    const int end = full ? max(p_min + 1, 0) / 32 : 0;               // blocks that end at or before p_min
+    const int from = a.window > 0 ? (max(p_max - a.window + 1, 0) + 31) / 32 : 0;
+    // numbered as first() numbers them; the sinks' whole blocks come first
+    whole_sink = min(min(a.sinks / 32, n_sink), end);
+    whole_lo = n_sink + max(from - lo, 0);
+    whole_n = max(n_sink + end - lo - whole_lo, 0);
+  }
+  __device__ __forceinline__ bool whole(int b) const {
+    return b < whole_sink || static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
+  }
+  // First key of block b; blocks past the last lie past the keys.
+  __device__ __forceinline__ int first(int b) const { return b < n ? (b < n_sink ? b : lo + b - n_sink) * 32 : nk; }
+};
+
+// The wave's 32 queries, one a column.
+struct QueryCols : Segment {
+  int head, hk;
+  int wq, row, p;             // the wave's first query; the lane's, and its position
+  bool in;
+  __device__ __forceinline__ bool find(const AttnView& a, int64_t n_slots, int* err) {
+    const int64_t id = blockIdx.x;
+    // the last tiles of a sequence see the most keys: they start first
+    if (!Segment::find(a, a.cu_q, n_slots - 1 - id / a.n_heads, err)) return false;
+    head = static_cast<int>(id % a.n_heads);
+    hk = head / a.group;
+    wq = first + 32 * wave_id();
+    row = wq + (threadIdx.x & 31);
+    in = row < nq;
+    p = past + row;
+    return true;
+  }
+  __device__ __forceinline__ KeyBlocks blocks(const AttnView& a) const {
+    KeyBlocks b(a, nk, past + first, past + min(first + kTileRows, nq) - 1);
+    b.set_wave(a, past + wq, past + wq + 31, wq + 31 < nq);
+    return b;
+  }
+};
+
+// One side of the scores takes the scale's sign: scores in powers of two are
+// then score_factor() times the products, and as that is positive the largest
+// product has the largest score and a hidden one can be -inf before scaling.
+template <typename T>
+__device__ __forceinline__ u32x4_t signed_frag(const AttnView& a, u32x4_t v) {
+  if (a.scale < 0.0f) v = flip_sign<T>(v);
+  return a.scale == 0.0f ? u32x4_t{0, 0, 0, 0} : v;
+}
+__device__ __forceinline__ float score_factor(const AttnView& a) {
+  return a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
+}
+template <typename T, int DP>
+__device__ __forceinline__ float load_queries(const AttnView& a, const QueryCols& w, u32x4_t* qf) {
+#pragma unroll
+  for (int s = 0; s < Tile<T, DP>::kSteps; ++s)
+    qf[s] = signed_frag<T>(a, load_frag<T>(a.q, w.q0 + w.row, w.head, a.head_dim, s, w.in));
+  return score_factor(a);
+}
+
+// ------------------------------------------------------------------- forward
 // One query row, by a whole wave (row t of q, at position p of the sequence
 // whose keys start at row k0).
 template <typename T>
@@ -23,229 +196,232 @@ __device__ __forceinline__ void attn_fwd_row(const AttnView& a, int64_t t, int64
   store_row<T>(a.o, t, h, a.head_dim, sm.value());
 }
 
-// ------------------------------------------------------------------- forward
-// A tile of `rows` consecutive rows of one sequence and one head.  Sequence b
-// owns the slots floor(cu[b] / rows) + b onwards, at least as many as it has
-// tiles, so a grid of total / rows + n_seqs slots holds every sequence and a
-// workgroup finds its own by a search of cu alone.
-struct TileOf {
-  int64_t seq, first;   // first: the tile's first row within the sequence; seq -1: none
-};
-__device__ __forceinline__ TileOf tile_of_slot(const int32_t* cu, int64_t n_seqs, int rows, int64_t slot) {
-  int64_t lo = 0, hi = n_seqs;   // slots of lo start at or before `slot`, those of hi after
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (cu[mid] / rows + mid <= slot) lo = mid;
-    else hi = mid;
+// Running softmax of the lane's column: the sums stay relative to `top`, an
+// earlier maximum rounded up to an integer, until a score passes it by 8: the
+// exponentials stay below 2^9, far from fp32's range, lanes exchange maxima
+// only then, and what has been summed is scaled by a power of two, exactly.
+struct ColumnSoftmax {
+  float top = -INFINITY, sum = 0.0f;   // sum: this half-wave's keys
+  // s: the block's products, c times which are the scores.  True where `keep`
+  // has to scale the sums.
+  __device__ __forceinline__ bool raise(const f32x16_t& s, float c, float* keep) {
+    float m = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r]);
+    m *= c;
+    if (!__any((m > top + 8.0f) | ((top == -INFINITY) & (m > top)))) return false;
+    const float t = fmaxf(top, ceilf(fmaxf(m, other_half(m))));
+    *keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t);
+    top = t;
+    sum *= *keep;
+    return true;
   }
-  const int64_t tile = slot - (cu[lo] / rows + lo);
-  return TileOf{tile < 0 ? -1 : lo, tile * rows};
+  __device__ __forceinline__ float base() const { return top == -INFINITY ? 0.0f : top; }
+};
+
+// -inf for the hidden keys of the block at `key`.
+__device__ __forceinline__ void mask_keys(const AttnView& a, const QueryCols& w, int key, f32x16_t& s) {
+  const SeenKeys seen(a, w.p, w.in, key);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = seen(r) ? s[r] : -INFINITY;
 }
-static int64_t slots(int64_t total, int64_t n_seqs, int rows) { return total / rows + n_seqs; }
 
-// Workgroup id -> (slot, head).  Consecutive ids run on different XCDs, each
-// with its own L2.
-struct Work {
-  int64_t slot;
-  int head;
-};
-__device__ __forceinline__ Work work_of(int64_t n_slots, int heads) {
-  const int64_t id = blockIdx.x;
-  return Work{n_slots - 1 - id / heads, static_cast<int>(id % heads)};
-}
-
-// The key tiles of `rows` keys that some query at a position in [p_min, p_max]
-// sees: those of the sinks, then the window's.
-struct KeyTiles {
-  int64_t n_sink, lo, n;
-  int rows;
-  __device__ __forceinline__ KeyTiles(const AttnView& a, int64_t p_min, int64_t p_max, int rows_)
-      : rows(rows_) {
-    lo = (a.window > 0 && p_min >= a.window ? p_min - a.window + 1 : 0) / rows;
-    const int64_t sink_keys = a.sinks < lo * rows ? a.sinks : lo * rows;
-    n_sink = p_max < 0 ? 0 : (sink_keys + rows - 1) / rows;
-    n = p_max < 0 ? 0 : n_sink + p_max / rows + 1 - lo;
-  }
-  __device__ __forceinline__ int64_t first(int64_t it) const { return (it < n_sink ? it : lo + it - n_sink) * rows; }
-};
-// Whether no query at a position in [p_min, p_max] sees a key in [key, key +
-// n), or every one sees them all.
-__device__ __forceinline__ bool none_visible(const AttnView& a, int64_t p_min, int64_t p_max, int64_t key, int n) {
-  return key > p_max || (a.window > 0 && key + n - 1 <= p_min - a.window && key >= a.sinks);
-}
-__device__ __forceinline__ bool all_visible(const AttnView& a, int64_t p_min, int64_t p_max, int64_t key, int n) {
-  return key + n - 1 <= p_min && (a.window == 0 || key > p_max - a.window || key + n <= a.sinks);
-}
-// Masks are applied with selects (a few integer compares an element), never by
-// branching on one element of a result.
-// Which rows of a key block the lane's query (at position p) sees: row j =
-// 8 (r / 4) + r % 4 (+ 4 for the upper half-wave) of the tile that starts at
-// `key` is seen when j <= hi and (j >= lo or j < sink).
-struct SeenKeys {
-  int hi, lo, sink;
-  __device__ __forceinline__ SeenKeys(const AttnView& a, int64_t p, bool in, int64_t key) {
-    const int64_t at = key + 4 * ((threadIdx.x & 63) >> 5);
-    hi = in ? clamp_rel(p - at) : -(1 << 20);
-    lo = a.window > 0 ? clamp_rel(p - a.window + 1 - at) : -(1 << 20);
-    sink = clamp_rel(a.sinks - at);
-  }
-  __device__ __forceinline__ bool operator()(int j) const { return (j <= hi) & ((j >= lo) | (j < sink)); }
-};
-
-// Which queries of a 32-query block (the first at position p0, number i0 of
-// nq) see the lane's key: query j = 8 (r / 4) + r % 4 (+ 4 for the upper
-// half-wave) does when lo <= j < hi.
-struct SeenBy {
-  int lo, hi;
-  __device__ __forceinline__ SeenBy(const AttnView& a, int64_t key, bool in, int64_t p0, int64_t i0, int64_t nq) {
-    const int64_t up = 4 * ((threadIdx.x & 63) >> 5);
-    lo = clamp_rel(key - p0 - up);
-    int64_t end = nq - i0;
-    if (a.window > 0 && key >= a.sinks && key + a.window - p0 < end) end = key + a.window - p0;
-    hi = in ? clamp_rel(end - up) : -(1 << 20);
-  }
-  __device__ __forceinline__ bool operator()(int j) const { return (j >= lo) & (j < hi); }
-};
-
-// True where a value is NaN or infinite.
-__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
-
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void attn_fwd_kernel(AttnView a, int64_t n_slots, int* err) {
-  using TL = Tile<T, DP>;
-  constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;      // keys per tile
-  constexpr int kTile = kKeys * TL::kRow;
-  extern __shared__ __align__(1024) char smem[];
-  lds_char* const lds = (lds_char*)smem;               // [2][K, V]
-  check_offsets(a, err);
-  const Work wk = work_of(n_slots, a.n_heads);
-  const TileOf tile = tile_of_slot(a.cu_q, a.n_seqs, 32 * NW, wk.slot);
-  if (tile.seq < 0) return;
-  int64_t q0, q1, k0, k1;
-  seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
-  seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
-  const int64_t nq = q1 - q0, nk = k1 - k0, past = nk - nq;
-  if (tile.first >= nq) return;
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int head = wk.head, hk = head / a.group;
-
-  // this wave's queries, one a column
-  const int64_t wq = tile.first + 32 * (threadIdx.x >> 6);
-  const int64_t row = wq + (lane & 31);
-  const bool in = row < nq;
-  const int64_t p = past + row;
-  const int64_t p_min = past + wq, p_max = past + (wq + 31 < nq ? wq + 31 : nq - 1);
-  const bool wave_in = wq < nq && p_max >= 0;
-  u32x4_t qf[TL::kSteps];
-#pragma unroll
-  for (int s = 0; s < TL::kSteps; ++s) {
-    qf[s] = load_frag<T>(a.q, q0 + row, head, a.head_dim, s, in);
-    if (a.scale < 0.0f) qf[s] = flip_sign<T>(qf[s]);
-  }
-  const float c = fabsf(a.scale) * 1.44269504088896340736f;   // scores in powers of two
-
-  const KeyTiles keys(a, past + tile.first, past + (tile.first + 32 * NW < nq ? tile.first + 32 * NW : nq) - 1, kKeys);
-  TileLoader<T, DP, kKeys, NW> kl, vl;
-  kl.init(a.k, k0, hk, a.head_dim);
-  vl.init(a.v, k0, hk, a.head_dim);
-  f32x16_t o[TL::kDT] = {};
-  float top = -INFINITY, sum = 0.0f;   // of the lane's column; sum: this half-wave's keys
-  if (keys.n > 0) {
-    kl.load(keys.first(0), nk, lds);
-    vl.load(keys.first(0), nk, lds + kTile);
-  }
-  for (int64_t it = 0; it < keys.n; ++it) {
-    wait_vmcnt<0>();
-    lds_barrier();
-    const lds_char* kt = lds + (it & 1) * 2 * kTile;
-    const lds_char* vt = kt + kTile;
-    if (it + 1 < keys.n) {
-      lds_char* next = lds + ((it + 1) & 1) * 2 * kTile;
-      kl.load(keys.first(it + 1), nk, next);
-      vl.load(keys.first(it + 1), nk, next + kTile);
-    }
-    const int64_t key = keys.first(it);
-    if (!wave_in || none_visible(a, p_min, p_max, key, kKeys)) continue;
-    const bool all = wq + 31 < nq && all_visible(a, p_min, p_max, key, kKeys);
-    f32x16_t s[kKeys / 32];
-#pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n) {
-      s[n] = f32x16_t{};
-#pragma unroll
-      for (int st = 0; st < TL::kSteps; ++st) s[n] = mma16(TL::row_frag(kt, 32 * n, st), qf[st], s[n], T{});
-    }
-    // scaled scores, -inf where hidden
-#pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n) s[n] *= c;
-    if (!all) {
-      const SeenKeys seen(a, p, in, key);
-#pragma unroll
-      for (int n = 0; n < kKeys / 32; ++n)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[n][r] = seen(32 * n + 8 * (r >> 2) + (r & 3)) ? s[n][r] : -INFINITY;
-    }
-    float m = s[0][0];
-#pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) m = fmaxf(m, s[n][r]);
-    m = fmaxf(m, other_half(m));
-    // the sums stay relative to an earlier maximum until one grows past it by
-    // a factor of 2^8: the exponentials stay below 2^8, far from fp32's range
-    if (__any(m > top + 8.0f || (top == -INFINITY && m > top))) {
-      const float t = fmaxf(top, m);
-      const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t);
-      top = t;
-      sum *= keep;
-#pragma unroll
-      for (int d = 0; d < TL::kDT; ++d) o[d] *= keep;
-    }
-    const float base = top == -INFINITY ? 0.0f : top;
-    Column<T> pc[kKeys / 32];
-#pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[n][r] = __builtin_amdgcn_exp2f(s[n][r] - base);
-        sum += s[n][r];
-      }
-      pc[n].set(s[n]);
-    }
-#pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n)
-#pragma unroll
-      for (int d = 0; d < TL::kDT; ++d) o[d] = mma_transposed<DP>(vt, 32 * n, d, pc[n], o[d]);
-  }
-  sum += other_half(sum);
+// o / sum and lse of the wave's columns.  A NaN or an infinity may have come
+// from a value row that the query does not see (its zero weight times it):
+// such rows are done again key by key.
+template <typename T, int DP>
+__device__ __forceinline__ void finish_fwd(const AttnView& a, const QueryCols& w, const ColumnSoftmax& sm, f32x16_t* o) {
+  const int half = (threadIdx.x & 63) >> 5;
+  const float sum = sm.sum + other_half(sm.sum);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   bool bad = false;
 #pragma unroll
-  for (int d = 0; d < TL::kDT; ++d) {
+  for (int d = 0; d < Tile<T, DP>::kDT; ++d) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) bad |= not_finite(o[d][r]);
-    store_column<T>(a.o, q0 + row, head, a.head_dim, d, o[d], inv, in);
+    store_column<T>(a.o, w.q0 + w.row, w.head, a.head_dim, d, o[d], inv, w.in);
   }
-  if (in && half == 0)
-    a.lse[(q0 + row) * a.n_heads + head] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
-  // A NaN or an infinity may have come from a value row that the query does
-  // not see (its zero weight times it): such rows are done again one by one.
-  uint64_t again = __ballot(bad && in);
+  if (w.in && half == 0)
+    a.lse[(w.q0 + w.row) * a.n_heads + w.head] = (sm.top + __builtin_amdgcn_logf(sum)) * kLn2;
+  uint64_t again = __ballot(bad && w.in);
   again = (again | (again >> 32)) & 0xffffffffull;
   while (again) {
     const int i = __builtin_ctzll(again);
     again &= again - 1;
-    attn_fwd_row<T>(a, q0 + wq + i, head, past + wq + i, k0);
+    attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0);
   }
 }
 
-template <typename T, int DP>
-static hipError_t fwd_launch(const AttnView& a, hipStream_t s, int* err) {
-  constexpr int kNW = 4;
-  constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
-  constexpr size_t kLds = size_t(4) * kKeys * Tile<T, DP>::kRow;
-  const int64_t n = slots(a.total_q, a.n_seqs, 32 * kNW);
-  attn_fwd_kernel<T, DP, kNW><<<static_cast<unsigned>(n * a.n_heads), 64 * kNW, kLds, s>>>(a, n, err);
-  return hipGetLastError();
+// fp32: one block after the other.
+template <int DP, bool kWide>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, int* err) {
+  using T = float;
+  using TL = Tile<T, DP>;
+  constexpr int kBlock = 32 * TL::kRow;
+  extern __shared__ __align__(1024) char smem[];
+  lds_char* const lds = (lds_char*)smem;               // [2][K, V]
+  check_offsets(a, err);
+  QueryCols w;
+  if (!w.find(a, n_slots, err)) return;
+  const KeyBlocks keys = w.blocks(a);
+  u32x4_t qf[TL::kSteps];
+  const float c = load_queries<T, DP>(a, w, qf);
+  TileLoader<T, DP, 32, kWaves, kWide> kl, vl;
+  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
+  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+  f32x16_t o[TL::kDT] = {};
+  ColumnSoftmax sm;
+  kl.load(keys.first(0), lds);
+  vl.load(keys.first(0), lds + kBlock);
+  for (int b = 0; b < keys.n; ++b) {
+    wait_vmcnt<0>();
+    lds_barrier();
+    const lds_char* kt = lds + (b & 1) * 2 * kBlock;
+    const lds_char* vt = kt + kBlock;
+    lds_char* next = lds + ((b + 1) & 1) * 2 * kBlock;
+    kl.load(keys.first(b + 1), next);
+    vl.load(keys.first(b + 1), next + kBlock);
+    f32x16_t s = {};
+#pragma unroll
+    for (int st = 0; st < TL::kSteps; ++st) s = mma16(TL::row_frag(kt, 0, st), qf[st], s, T{});
+    if (!keys.whole(b)) mask_keys(a, w, keys.first(b), s);
+    float keep;
+    if (sm.raise(s, c, &keep)) {
+#pragma unroll
+      for (int d = 0; d < TL::kDT; ++d) o[d] *= keep;
+    }
+    const float base = sm.base();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -base));
+      sm.sum += s[r];
+    }
+    Column<T> pc;
+    pc.set(s);
+#pragma unroll
+    for (int d = 0; d < TL::kDT; ++d) o[d] = mma_transposed<DP>(vt, 0, d, pc, o[d]);
+  }
+  wait_vmcnt<0>();   // no load into LDS outlives the workgroup
+  finish_fwd<T, DP>(a, w, sm, o);
+}
+
+// bf16.  A block (32 keys x 32 queries at DP 128) is 16 MFMAs, 512 cycles, and
+// 16 exponentials a lane, nearly as many cycles of vector work.  So the wave
+// runs three blocks at a time: between the exponentials of block b stand the
+// score products of block b + 1 and the value products of block b - 1.
+template <int DP>
+struct FwdShape {
+  static constexpr int kAhead = 3, kSlots = 4;   // slots of a ring: the blocks in flight and the one at hand
+  static constexpr int kBlock = 32 * Tile<bf16_t, DP>::kRow;
+  static constexpr int kLds = 2 * kSlots * kBlock;
+};
+template <int DP, bool kWide>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, int* err) {
+  using T = bf16_t;
+  using TL = Tile<T, DP>;
+  using Shape = FwdShape<DP>;
+  constexpr int kAhead = Shape::kAhead, kMask = Shape::kSlots - 1, kBlock = Shape::kBlock;
+  extern __shared__ __align__(1024) char smem[];
+  lds_char* const kring = (lds_char*)smem;
+  lds_char* const vring = kring + Shape::kSlots * kBlock;
+  check_offsets(a, err);
+  QueryCols w;
+  if (!w.find(a, n_slots, err)) return;
+  const KeyBlocks keys = w.blocks(a);
+  f32x16_t o[TL::kDT] = {};
+  ColumnSoftmax sm;
+  if (keys.n > 0) {
+    using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
+    Loader kl, vl;
+    kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
+    vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+    constexpr int kLoads = 2 * Loader::kPer;   // instructions a wave and step
+#pragma unroll
+    for (int b = 0; b <= kAhead; ++b) kl.load(keys.first(b), kring + (b & kMask) * kBlock);
+#pragma unroll
+    for (int b = 0; b < kAhead - 1; ++b) vl.load(keys.first(b), vring + (b & kMask) * kBlock);
+    u32x4_t qf[TL::kSteps];
+    const float c = load_queries<T, DP>(a, w, qf);
+    wait_vmcnt<0>();
+    lds_barrier();
+    f32x16_t s0 = {}, s1;
+    Column<T> p0, p1;
+#pragma unroll
+    for (int st = 0; st < TL::kSteps; ++st) s0 = mma16(TL::row_frag(kring, 0, st), qf[st], s0, T{});
+
+    // Step b: exponentials of s (block b) into p, scores of block b + 1 into
+    // next, values of block b - 1 with the weights prev.
+    auto step = [&](auto is_first, int b, f32x16_t& s, f32x16_t& next, Column<T>& prev, Column<T>& p) {
+      constexpr bool kFirst = decltype(is_first)::value;
+      wait_vmcnt<(kAhead - 1) * kLoads>();   // K of block b + 1, V of block b - 1
+      lds_barrier();
+      kl.load(keys.first(b + kAhead + 1), kring + ((b + kAhead + 1) & kMask) * kBlock);
+      vl.load(keys.first(b + kAhead - 1), vring + ((b + kAhead - 1) & kMask) * kBlock);
+      const lds_char* kt = kring + ((b + 1) & kMask) * kBlock;
+      const lds_char* vt = vring + ((b - 1) & kMask) * kBlock;
+      if (!keys.whole(b)) mask_keys(a, w, keys.first(b), s);
+      float keep;
+      if (sm.raise(s, c, &keep)) {
+        if constexpr (!kFirst) {
+#pragma unroll
+          for (int d = 0; d < TL::kDT; ++d) o[d] *= keep;
+          prev.scale(keep);
+        }
+      }
+      const float base = sm.base();
+      constexpr int kPairs = TL::kSteps;   // one score MFMA and one value MFMA each
+      static_assert(kPairs == 2 * TL::kDT, "as many of either kind");
+      u32x4_t kf[2], vf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kf[i] = TL::row_frag(kt, 0, i);
+        if constexpr (!kFirst) vf[i] = column_frag<DP>(vt, 0, i & 1, i >> 1);
+      }
+      float even = 0.0f;
+      auto element = [&](int r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[r], c, -base));
+        sm.sum += e;
+        if (r & 1) {
+          uint32_t pair = pack_bf16x2(even, e);
+          pin(pair);
+          p.v[r >> 3][(r >> 1) & 3] = pair;
+        }
+        even = e;
+      };
+      constexpr int kPer = 8 / kPairs;   // elements after each MFMA
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        next = mma16(kf[i & 1], qf[i], i == 0 ? f32x16_t{} : next, T{});
+        if (i + 2 < kPairs) kf[i & 1] = TL::row_frag(kt, 0, i + 2);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) element(2 * kPer * i + e);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kFirst) {
+          o[i >> 1] = mma16(vf[i & 1], prev.v[i & 1], o[i >> 1], T{});
+          if (i + 2 < kPairs) vf[i & 1] = column_frag<DP>(vt, 0, i & 1, (i + 2) >> 1);
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) element(2 * kPer * i + kPer + e);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // an odd number of steps, the last one's keys all hidden where it is one
+    // more than there are blocks: the pair's registers change roles in place
+    const int n = keys.n | 1;
+    step(std::true_type{}, 0, s0, s1, p1, p0);
+    for (int b = 1; b < n; b += 2) {
+      step(std::false_type{}, b, s1, s0, p0, p1);
+      step(std::false_type{}, b + 1, s0, s1, p1, p0);
+    }
+    // the last block's values
+    wait_vmcnt<0>();
+    lds_barrier();
+    const lds_char* vt = vring + ((n - 1) & kMask) * kBlock;
+#pragma unroll
+    for (int d = 0; d < TL::kDT; ++d) o[d] = mma_transposed<DP>(vt, 0, d, p0, o[d]);
+  }
+  finish_fwd<T, DP>(a, w, sm, o);
 }
 
 // ------------------------------------------------------------------ backward
@@ -272,29 +448,20 @@ __device__ __forceinline__ void attn_dq_row(const AttnView& a, int64_t t, int64_
   store_row<T>(a.dq, t, h, a.head_dim, dq);
 }
 
-// The queries [begin, end) of a sequence that see key j.
-__device__ __forceinline__ void seeing_queries(const AttnView& a, int64_t j, int64_t past, int64_t nq, int64_t* begin,
-                                               int64_t* end) {
-  *begin = j > past ? j - past : 0;
-  *end = nq;
-  if (a.window > 0 && j >= a.sinks && j + a.window - past < nq) *end = j + a.window - past;
-}
-
 // One key's rows of dk and dv, by a whole wave.
 template <typename T>
-__device__ __forceinline__ void attn_dkv_row(const AttnView& a, const float* delta, int64_t j, int64_t hk, int64_t q0,
-                                             int64_t nq, int64_t k0, int64_t nk) {
-  const Row2 k = load_row<T>(a.k, k0 + j, hk, a.head_dim), v = load_row<T>(a.v, k0 + j, hk, a.head_dim);
+__device__ __forceinline__ void attn_dkv_row(const AttnView& a, const float* delta, int j, int hk, const Segment& s) {
+  const Row2 k = load_row<T>(a.k, s.k0 + j, hk, a.head_dim), v = load_row<T>(a.v, s.k0 + j, hk, a.head_dim);
   Row2 dk{{0.0f, 0.0f}}, dv{{0.0f, 0.0f}};
-  int64_t i0, i1;
-  seeing_queries(a, j, nk - nq, nq, &i0, &i1);
+  const int i0 = max(j - s.past, 0);
+  const int i1 = a.window > 0 && j >= a.sinks ? min(j - s.past + a.window, s.nq) : s.nq;
   for (int64_t g = 0; g < a.group; ++g) {
-    const int64_t h = hk * a.group + g;
+    const int64_t h = static_cast<int64_t>(hk) * a.group + g;
     for (int64_t i = i0; i < i1; ++i) {
-      const Row2 q = load_row<T>(a.q, q0 + i, h, a.head_dim);
-      const Row2 d_o = load_row<T>(a.d_o, q0 + i, h, a.head_dim);
-      const float pr = __expf(dot(q, k) * a.scale - a.lse[(q0 + i) * a.n_heads + h]);
-      const float ds = pr * (dot(d_o, v) - delta[h * a.total_q + q0 + i]);
+      const Row2 q = load_row<T>(a.q, s.q0 + i, h, a.head_dim);
+      const Row2 d_o = load_row<T>(a.d_o, s.q0 + i, h, a.head_dim);
+      const float pr = __expf(dot(q, k) * a.scale - a.lse[(s.q0 + i) * a.n_heads + h]);
+      const float ds = pr * (dot(d_o, v) - delta[h * a.total_q + s.q0 + i]);
       dk.x[0] += ds * q.x[0];
       dk.x[1] += ds * q.x[1];
       dv.x[0] += pr * d_o.x[0];
@@ -303,216 +470,405 @@ __device__ __forceinline__ void attn_dkv_row(const AttnView& a, const float* del
   }
   dk.x[0] *= a.scale;
   dk.x[1] *= a.scale;
-  store_row<T>(a.dk, k0 + j, hk, a.head_dim, dk);
-  store_row<T>(a.dv, k0 + j, hk, a.head_dim, dv);
+  store_row<T>(a.dk, s.k0 + j, hk, a.head_dim, dk);
+  store_row<T>(a.dv, s.k0 + j, hk, a.head_dim, dv);
 }
 
-// dq, and for the other kernel lse2 = lse in powers of two (0 where no key is
-// seen) and delta, both [n_heads][total_q].
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnView a, int64_t n_slots, float* lse2_out,
-                                                                                  float* delta_out, int* err) {
+// What the backward needs of the forward: lse in powers of two (0 where no key
+// is seen) and delta = sum d_o o, both [n_heads][total_q].
+struct RowStats {
+  float* lse2;
+  float* delta;
+};
+
+// dq, and the row statistics for the other kernel.  In bf16 a block is 16
+// MFMAs for the scores and their gradients, then 16 elements of vector work
+// with the 8 MFMAs of the block before in between.
+template <typename T, int DP>
+struct DqShape {
+  static constexpr int kAhead = 2;
+  static constexpr int kKSlots = kAhead + 2, kVSlots = kAhead + 1;
+  static constexpr int kBlock = 32 * Tile<T, DP>::kRow;
+  static constexpr int kLds = (kKSlots + kVSlots) * kBlock;
+};
+template <typename T, int DP, bool kWide>
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnView a, int64_t n_slots, RowStats stats,
+                                                                                      int* err) {
   using TL = Tile<T, DP>;
-  constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
-  constexpr int kTile = kKeys * TL::kRow;
+  using Shape = DqShape<T, DP>;
+  using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
+  constexpr int kAhead = Shape::kAhead, kBlock = Shape::kBlock;
   extern __shared__ __align__(1024) char smem[];
-  lds_char* const lds = (lds_char*)smem;
+  lds_char* const kring = (lds_char*)smem;
+  lds_char* const vring = kring + Shape::kKSlots * kBlock;
   check_offsets(a, err);
-  const Work wk = work_of(n_slots, a.n_heads);
-  const TileOf tile = tile_of_slot(a.cu_q, a.n_seqs, 32 * NW, wk.slot);
-  if (tile.seq < 0) return;
-  int64_t q0, q1, k0, k1;
-  seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
-  seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
-  const int64_t nq = q1 - q0, nk = k1 - k0, past = nk - nq;
-  if (tile.first >= nq) return;
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int head = wk.head, hk = head / a.group;
-  const int64_t wq = tile.first + 32 * (threadIdx.x >> 6);
-  const int64_t row = wq + (lane & 31);
-  const bool in = row < nq;
-  const int64_t p = past + row;
-  const int64_t p_min = past + wq, p_max = past + (wq + 31 < nq ? wq + 31 : nq - 1);
-  const bool wave_in = wq < nq && p_max >= 0;
-  const KeyTiles keys(a, past + tile.first, past + (tile.first + 32 * NW < nq ? tile.first + 32 * NW : nq) - 1, kKeys);
-  TileLoader<T, DP, kKeys, NW> kl, vl;
-  kl.init(a.k, k0, hk, a.head_dim);
-  vl.init(a.v, k0, hk, a.head_dim);
-  if (keys.n > 0) {
-    kl.load(keys.first(0), nk, lds);
-    vl.load(keys.first(0), nk, lds + kTile);
+  QueryCols w;
+  if (!w.find(a, n_slots, err)) return;
+  const KeyBlocks keys = w.blocks(a);
+  const int half = (threadIdx.x & 63) >> 5;
+  Loader kl, vl;
+  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
+  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+  // ring places of the blocks to read, and to load next
+  int kr = 0, vr = 0, kn = kAhead * kBlock, vn = kAhead * kBlock;
+  auto bump = [](int& at, int slots) { at = at + kBlock == slots * kBlock ? 0 : at + kBlock; };
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) {
+    kl.load(keys.first(b), kring + b * kBlock);
+    vl.load(keys.first(b), vring + b * kBlock);
   }
   u32x4_t qf[TL::kSteps], dof[TL::kSteps];
   float delta = 0.0f;
 #pragma unroll
   for (int s = 0; s < TL::kSteps; ++s) {
-    qf[s] = load_frag<T>(a.q, q0 + row, head, a.head_dim, s, in);
-    dof[s] = load_frag<T>(a.d_o, q0 + row, head, a.head_dim, s, in);
-    delta += dot_frag(dof[s], load_frag<T>(a.o, q0 + row, head, a.head_dim, s, in), T{});
+    dof[s] = load_frag<T>(a.d_o, w.q0 + w.row, w.head, a.head_dim, s, w.in);
+    delta += dot_frag(dof[s], load_frag<T>(a.o, w.q0 + w.row, w.head, a.head_dim, s, w.in), T{});
   }
   delta += other_half(delta);
-  const float lse = in ? a.lse[(q0 + row) * a.n_heads + head] : 0.0f;
-  const float lse2 = lse == -INFINITY ? 0.0f : lse * 1.44269504088896340736f;
-  if (in && half == 0) {
-    lse2_out[head * a.total_q + q0 + row] = lse2;
-    delta_out[head * a.total_q + q0 + row] = delta;
+  const float lse = w.in ? a.lse[(w.q0 + w.row) * a.n_heads + w.head] : 0.0f;
+  const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+  if (w.in && half == 0) {
+    stats.lse2[w.head * a.total_q + w.q0 + w.row] = lse2;
+    stats.delta[w.head * a.total_q + w.q0 + w.row] = delta;
   }
-  const float c = a.scale * 1.44269504088896340736f;
+  const float c = load_queries<T, DP>(a, w, qf);
   f32x16_t dq[TL::kDT] = {};
-  for (int64_t it = 0; it < keys.n; ++it) {
-    wait_vmcnt<0>();
+  Column<T> prev;
+  const lds_char* kprev = kring;
+  auto step = [&](auto is_first, int b) {
+    constexpr bool kFirst = decltype(is_first)::value;
+    // the loads of one step may be under way; the first step also waits for
+    // the columns' own
+    wait_vmcnt<kFirst ? 0 : (kAhead - 1) * 2 * Loader::kPer>();
     lds_barrier();
-    const lds_char* kt = lds + (it & 1) * 2 * kTile;
-    const lds_char* vt = kt + kTile;
-    if (it + 1 < keys.n) {
-      lds_char* next = lds + ((it + 1) & 1) * 2 * kTile;
-      kl.load(keys.first(it + 1), nk, next);
-      vl.load(keys.first(it + 1), nk, next + kTile);
+    kl.load(keys.first(b + kAhead), kring + kn);
+    vl.load(keys.first(b + kAhead), vring + vn);
+    bump(kn, Shape::kKSlots);
+    bump(vn, Shape::kVSlots);
+    const lds_char* kt = kring + kr;
+    const lds_char* vt = vring + vr;
+    bump(kr, Shape::kKSlots);
+    bump(vr, Shape::kVSlots);
+    f32x16_t s = {}, dp = {};
+#pragma unroll
+    for (int st = 0; st < TL::kSteps; ++st) {
+      s = mma16(TL::row_frag(kt, 0, st), qf[st], s, T{});
+      dp = mma16(TL::row_frag(vt, 0, st), dof[st], dp, T{});
     }
-    const int64_t key = keys.first(it);
-    if (!wave_in || none_visible(a, p_min, p_max, key, kKeys)) continue;
-    const bool all = wq + 31 < nq && all_visible(a, p_min, p_max, key, kKeys);
+    const bool whole = keys.whole(b);
+    const SeenKeys seen(a, w.p, w.in, keys.first(b));
+    if constexpr (sizeof(T) == 2) {
+      if (!whole) {
+        // hidden pairs: probability and gradient zero, whatever the products are
 #pragma unroll
-    for (int n = 0; n < kKeys / 32; ++n) {
-      f32x16_t s = {}, dp = {};
-#pragma unroll
-      for (int st = 0; st < TL::kSteps; ++st) {
-        s = mma16(TL::row_frag(kt, 32 * n, st), qf[st], s, T{});
-        dp = mma16(TL::row_frag(vt, 32 * n, st), dof[st], dp, T{});
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
-      if (!all) {
-        const SeenKeys seen(a, p, in, key);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = seen(32 * n + 8 * (r >> 2) + (r & 3)) ? s[r] : 0.0f;
+        for (int r = 0; r < 16; ++r) {
+          s[r] = seen(r) ? s[r] : -INFINITY;
+          dp[r] = seen(r) ? dp[r] : delta;
+        }
       }
       Column<T> ds;
-      ds.set(s);
+      float even = 0.0f;
+      constexpr int kMfma = 2 * TL::kDT;   // of the block before
+      u32x4_t kf[2];
+      if constexpr (!kFirst) {
 #pragma unroll
-      for (int d = 0; d < TL::kDT; ++d) dq[d] = mma_transposed<DP>(kt, 32 * n, d, ds, dq[d]);
+        for (int i = 0; i < 2; ++i) kf[i] = column_frag<DP>(kprev, 0, i & 1, i >> 1);
+      }
+#pragma unroll
+      for (int i = 0; i < kMfma; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kFirst) {
+          dq[i >> 1] = mma16(kf[i & 1], prev.v[i & 1], dq[i >> 1], T{});
+          if (i + 2 < kMfma) kf[i & 1] = column_frag<DP>(kprev, 0, i & 1, (i + 2) >> 1);
+        }
+#pragma unroll
+        for (int e = 0; e < 16 / kMfma; ++e) {
+          const int r = i * (16 / kMfma) + e;
+          const float g = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+          if (r & 1) {
+            uint32_t pair = pack_bf16x2(even, g);
+            pin(pair);
+            ds.v[r >> 3][(r >> 1) & 3] = pair;
+          }
+          even = g;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      prev = ds;
+      kprev = kt;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float g = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+        s[r] = (whole | seen(r)) ? g : 0.0f;
+      }
+      prev.set(s);
+#pragma unroll
+      for (int d = 0; d < TL::kDT; ++d) dq[d] = mma_transposed<DP>(kt, 0, d, prev, dq[d]);
+    }
+  };
+  if (keys.n > 0) {
+    step(std::true_type{}, 0);
+    for (int b = 1; b < keys.n; ++b) step(std::false_type{}, b);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int d = 0; d < TL::kDT; ++d) dq[d] = mma_transposed<DP>(kprev, 0, d, prev, dq[d]);
     }
   }
+  wait_vmcnt<0>();   // no load into LDS outlives the workgroup
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < TL::kDT; ++d) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) bad |= not_finite(dq[d][r]);
-    store_column<T>(a.dq, q0 + row, head, a.head_dim, d, dq[d], a.scale, in);
+    store_column<T>(a.dq, w.q0 + w.row, w.head, a.head_dim, d, dq[d], a.scale, w.in);
   }
   // a hidden key's rows may have brought it (zero times them): see the forward
-  uint64_t again = __ballot(bad && in);
+  uint64_t again = __ballot(bad && w.in);
   again = (again | (again >> 32)) & 0xffffffffull;
   while (again) {
     const int i = __builtin_ctzll(again);
     again &= again - 1;
-    attn_dq_row<T>(a, q0 + wq + i, head, past + wq + i, k0);
+    attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0);
   }
 }
 
-// dk and dv: one key a column, 32 a wave; the queries that see them (of every
-// head of the group) go through LDS.
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(AttnView a, int64_t n_slots, const float* lse2_in,
-                                                              const float* delta_in, int* err) {
+// dk and dv: one key a column; the queries that see them (of every head of the
+// group) go through LDS.  The two results take 2 DP registers a lane, so one
+// workgroup has a CU to itself and in bf16 the wave runs three blocks at a
+// time by itself, as in the forward: between the elements of block b stand the
+// score products of block b + 1 and the gradient products of block b - 1.
+template <typename T, int DP>
+struct DkvShape {
+  static constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kSlots = sizeof(T) == 2 ? kAhead + 3 : 2;
+  static constexpr int kBlock = 32 * Tile<T, DP>::kRow;
+  static constexpr int kStage = 2 * kBlock + 512;   // Q, dO, lse2, delta (256 bytes each, half of it used)
+  static constexpr int kLds = kSlots * kStage;
+};
+template <typename T, int DP, bool kWide>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, int64_t n_slots, RowStats stats, int* err) {
   using TL = Tile<T, DP>;
-  constexpr int kRows = sizeof(T) == 2 ? 64 : 32;      // queries per tile
-  constexpr int kTile = kRows * TL::kRow;
-  constexpr int kStage = 2 * kTile + 512;              // Q, dO, lse2 [64], delta [64]
+  using Shape = DkvShape<T, DP>;
+  using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
+  constexpr int kAhead = Shape::kAhead, kBlock = Shape::kBlock, kStage = Shape::kStage;
   extern __shared__ __align__(1024) char smem[];
-  lds_char* const lds = (lds_char*)smem;
-  const Work wk = work_of(n_slots, a.n_kv_heads);
-  const TileOf tile = tile_of_slot(a.cu_k, a.n_seqs, 32 * NW, n_slots - 1 - wk.slot);
-  if (tile.seq < 0) return;
-  int64_t q0, q1, k0, k1;
-  seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
-  seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
-  const int64_t nq = q1 - q0, nk = k1 - k0, past = nk - nq;
-  if (tile.first >= nk) return;
+  lds_char* const ring = (lds_char*)smem;
+  const int64_t id = blockIdx.x;
+  Segment w;
+  if (!w.find(a, a.cu_k, id / a.n_kv_heads, err)) return;   // the first keys are seen most: they start first
   const int lane = threadIdx.x & 63;
-  const int hk = wk.head;
-  const int64_t wkey = tile.first + 32 * (threadIdx.x >> 6);   // the wave's first key
-  const int64_t key = wkey + (lane & 31);
-  const bool in = key < nk;
-  u32x4_t kf[TL::kSteps], vf[TL::kSteps];
-#pragma unroll
-  for (int s = 0; s < TL::kSteps; ++s) {
-    kf[s] = load_frag<T>(a.k, k0 + key, hk, a.head_dim, s, in);
-    vf[s] = load_frag<T>(a.v, k0 + key, hk, a.head_dim, s, in);
-  }
-  const float c = a.scale * 1.44269504088896340736f;
+  const int hk = static_cast<int>(id % a.n_kv_heads);
+  const int wkey = w.first + 32 * wave_id();   // the wave's first key
+  const int key = wkey + (lane & 31);
+  const bool in = key < w.nk;
 
-  // query tiles that see some key of the workgroup
-  const int64_t last_key = (tile.first + 32 * NW < nk ? tile.first + 32 * NW : nk) - 1;
-  const int64_t i_lo = tile.first > past ? tile.first - past : 0;
-  int64_t i_hi = nq;
-  if (a.window > 0 && tile.first >= a.sinks && last_key + a.window - past < nq) i_hi = last_key + a.window - past;
-  const int64_t t_lo = i_lo / kRows, per_head = i_hi > i_lo ? (i_hi + kRows - 1) / kRows - t_lo : 0;
-  const int64_t n_it = per_head * a.group;
+  // 32-query blocks that see some key of the workgroup, for each head of the group
+  const int last_key = min(w.first + kTileRows, w.nk) - 1;
+  const int i_lo = max(w.first - w.past, 0);
+  const int i_hi = a.window > 0 && w.first >= a.sinks ? min(last_key - w.past + a.window, w.nq) : w.nq;
+  const int b_lo = i_lo / 32, per_head = i_hi > i_lo ? (i_hi + 31) / 32 - b_lo : 0;
+  const int n = per_head * a.group;
+  // of these, the blocks whose every query sees all of the wave's keys
+  const bool keys_in = wkey + 31 < w.nk;
+  const int from = (max(wkey + 31 - w.past, 0) + 31) / 32;
+  const int to = (a.window > 0 && wkey + 31 >= a.sinks ? min(max(wkey - w.past + a.window, 0), w.nq) : w.nq) / 32;
+  const int whole_lo = from - b_lo, whole_n = keys_in ? max(to - from, 0) : 0;
 
-  TileLoader<T, DP, kRows, NW> ql, dl;
-  auto load = [&](int64_t it, lds_char* to) {
-    const int64_t h = static_cast<int64_t>(hk) * a.group + it / per_head, first = (t_lo + it % per_head) * kRows;
-    ql.init(a.q, q0, h, a.head_dim);
-    dl.init(a.d_o, q0, h, a.head_dim);
-    ql.load(first, nq, to);
-    dl.load(first, nq, to + kTile);
-    const int w = threadIdx.x >> 6;
-    if (w < 2) {
-      const int64_t i = first + lane < nq ? first + lane : nq - 1;
-      dma4((w ? delta_in : lse2_in) + h * a.total_q + q0 + i, static_cast<lds_void*>(to + 2 * kTile + 256 * w));
+  Loader ql, dl;
+  const int64_t h0 = static_cast<int64_t>(hk) * a.group;
+  ql.init(a.q, w.q0, w.nq, h0, a.head_dim);
+  dl.init(a.d_o, w.q0, w.nq, h0, a.head_dim);
+  const int sw = wave_id();
+  const float* stat = (sw & 1 ? stats.delta : stats.lse2) + h0 * a.total_q + w.q0;
+  // the next block to load: number ln (of per_head) of its head, into place lp
+  int ln = 0, lp = 0, left = n;
+  auto load = [&]() {
+    // past the last block: nothing, but it counts
+    const int i0 = left > 0 ? (b_lo + ln) * 32 : w.nq;
+    lds_char* const at = ring + lp;
+    ql.load(i0, at);
+    dl.load(i0, at + kBlock);
+    // every wave loads one statistic (two of them the same): the counts agree
+    dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(at + 2 * kBlock + 256 * (sw & 1)));
+    lp = lp + kStage == Shape::kLds ? 0 : lp + kStage;
+    --left;
+    if (++ln == per_head) {
+      ln = 0;
+      ql.next_head(a.q);
+      dl.next_head(a.d_o);
+      if (left > 0) stat += a.total_q;
     }
   };
+  constexpr int kLoads = 2 * Loader::kPer + 1;
   f32x16_t dk[TL::kDT] = {}, dv[TL::kDT] = {};
-  if (n_it > 0) load(0, lds);
-  for (int64_t it = 0; it < n_it; ++it) {
-    wait_vmcnt<0>();
-    lds_barrier();
-    const lds_char* qt = lds + (it & 1) * kStage;
-    const lds_char* dot = qt + kTile;
-    if (it + 1 < n_it) load(it + 1, lds + ((it + 1) & 1) * kStage);
-    const int64_t first = (t_lo + it % per_head) * kRows;
+  const float c = score_factor(a);
+  if (n > 0) {
+    u32x4_t kf[TL::kSteps], vf[TL::kSteps];
 #pragma unroll
-    for (int n = 0; n < kRows / 32; ++n) {
-      const int64_t i0 = first + 32 * n;                       // queries i0 .. i0 + 31, at these positions
-      const int64_t p_min = past + i0, p_max = past + (i0 + 31 < nq ? i0 + 31 : nq - 1);
-      if (wkey >= nk || i0 >= nq || none_visible(a, p_min, p_max, wkey, 32)) continue;
-      const bool all = i0 + 31 < nq && wkey + 31 < nk && all_visible(a, p_min, p_max, wkey, 32);
-      f32x16_t s = {}, dp = {};
+    for (int s = 0; s < TL::kSteps; ++s) {
+      kf[s] = signed_frag<T>(a, load_frag<T>(a.k, w.k0 + key, hk, a.head_dim, s, in));
+      vf[s] = load_frag<T>(a.v, w.k0 + key, hk, a.head_dim, s, in);
+    }
+    int bn = 0;   // the block at hand, within its head
+    auto next_slot = [](int at) { return at + kStage == Shape::kLds ? 0 : at + kStage; };
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int b = 0; b <= kAhead; ++b) load();
+      wait_vmcnt<0>();
+      lds_barrier();
+      f32x16_t s0 = {}, s1, g0 = {}, g1;
+      Column<T> p0, p1, e0, e1;   // probabilities and score gradients
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
-        s = mma16(TL::row_frag(qt, 32 * n, st), kf[st], s, T{});
-        dp = mma16(TL::row_frag(dot, 32 * n, st), vf[st], dp, T{});
+        s0 = mma16(TL::row_frag(ring, 0, st), kf[st], s0, T{});
+        g0 = mma16(TL::row_frag(ring + kBlock, 0, st), vf[st], g0, T{});
       }
-      const lds_char* stat = qt + 2 * kTile + (32 * n + 4 * (lane >> 5)) * 4;
+      int at_prev = 0, at = 0;
+      auto step = [&](auto is_first, f32x16_t& s, f32x16_t& g, f32x16_t& sn, f32x16_t& gn, Column<T>& pp, Column<T>& ep,
+                      Column<T>& p, Column<T>& e) {
+        constexpr bool kFirst = decltype(is_first)::value;
+        wait_vmcnt<(kAhead - 1) * kLoads>();   // block b + 1
+        lds_barrier();
+        load();
+        const int at_next = next_slot(at);
+        const lds_char* qn = ring + at_next;
+        const lds_char* dn = qn + kBlock;
+        const lds_char* qp = ring + at_prev;
+        const lds_char* dp = qp + kBlock;
+        const lds_char* st = ring + at + 2 * kBlock + 16 * (lane >> 5);
+        const bool whole = static_cast<unsigned>(bn - whole_lo) < static_cast<unsigned>(whole_n);
+        const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
+        f32x4_t l4[4], d4[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t l4 = *reinterpret_cast<const lds_f32x4*>(stat + 32 * g);
-        const f32x4_t d4 = *reinterpret_cast<const lds_f32x4*>(stat + 256 + 32 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * g + e;
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[e]));
-          dp[r] = s[r] * (dp[r] - d4[e]);
+        for (int q = 0; q < 4; ++q) {
+          l4[q] = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
+          d4[q] = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
         }
-      }
-      if (!all) {
-        const SeenBy seen(a, key, in, past + i0, i0, nq);
+        if (!whole) {
+          // hidden pairs: probability and gradient zero, whatever the products
+          // and the query's statistics are
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool yes = seen(8 * (r >> 2) + (r & 3));
-          s[r] = yes ? s[r] : 0.0f;
-          dp[r] = yes ? dp[r] : 0.0f;
+          for (int r = 0; r < 16; ++r) {
+            const bool yes = seen(r);
+            s[r] = yes ? s[r] : -INFINITY;
+            l4[r >> 2][r & 3] = yes ? l4[r >> 2][r & 3] : 0.0f;
+            g[r] = yes ? g[r] : 0.0f;
+            d4[r >> 2][r & 3] = yes ? d4[r >> 2][r & 3] : 0.0f;
+          }
         }
+        float pe = 0.0f, ee = 0.0f;
+        auto element = [&](int r) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[r >> 2][r & 3]));
+          const float y = x * (g[r] - d4[r >> 2][r & 3]);
+          if (r & 1) {
+            uint32_t px = pack_bf16x2(pe, x), py = pack_bf16x2(ee, y);
+            pin(px);
+            pin(py);
+            p.v[r >> 3][(r >> 1) & 3] = px;
+            e.v[r >> 3][(r >> 1) & 3] = py;
+          }
+          pe = x;
+          ee = y;
+        };
+        constexpr int kQuads = TL::kSteps;   // one MFMA of each of the four products
+        static_assert(kQuads == 2 * TL::kDT, "as many of either kind");
+        u32x4_t qa[2], da[2], qt[2], dt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qa[i] = TL::row_frag(qn, 0, i);
+          da[i] = TL::row_frag(dn, 0, i);
+          if constexpr (!kFirst) {
+            dt[i] = column_frag<DP>(dp, 0, i & 1, i >> 1);
+            qt[i] = column_frag<DP>(qp, 0, i & 1, i >> 1);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const int x = i & 1;
+          __builtin_amdgcn_sched_barrier(0);
+          sn = mma16(qa[x], kf[i], i == 0 ? f32x16_t{} : sn, T{});
+          if (i + 2 < kQuads) qa[x] = TL::row_frag(qn, 0, i + 2);
+#pragma unroll
+          for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + r);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (!kFirst) {
+            dv[i >> 1] = mma16(dt[x], pp.v[x], dv[i >> 1], T{});
+            if (i + 2 < kQuads) dt[x] = column_frag<DP>(dp, 0, x, (i + 2) >> 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          gn = mma16(da[x], vf[i], i == 0 ? f32x16_t{} : gn, T{});
+          if (i + 2 < kQuads) da[x] = TL::row_frag(dn, 0, i + 2);
+#pragma unroll
+          for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + 8 / kQuads + r);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (!kFirst) {
+            dk[i >> 1] = mma16(qt[x], ep.v[x], dk[i >> 1], T{});
+            if (i + 2 < kQuads) qt[x] = column_frag<DP>(qp, 0, x, (i + 2) >> 1);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        at_prev = at;
+        at = at_next;
+        if (++bn == per_head) bn = 0;
+      };
+      // as in the forward: an odd number of steps, one of them over zeros
+      step(std::true_type{}, s0, g0, s1, g1, p1, e1, p0, e0);
+      for (int b = 1; b < (n | 1); b += 2) {
+        step(std::false_type{}, s1, g1, s0, g0, p0, e0, p1, e1);
+        step(std::false_type{}, s0, g0, s1, g1, p1, e1, p0, e0);
       }
-      Column<T> pc, ds;
-      pc.set(s);
-      ds.set(dp);
+      if ((n & 1) == 0) p0.v[0] = p0.v[1] = e0.v[0] = e0.v[1] = u32x4_t{0, 0, 0, 0};
+      wait_vmcnt<0>();
+      const lds_char* qp = ring + at_prev;
 #pragma unroll
       for (int d = 0; d < TL::kDT; ++d) {
-        dv[d] = mma_transposed<DP>(dot, 32 * n, d, pc, dv[d]);
-        dk[d] = mma_transposed<DP>(qt, 32 * n, d, ds, dk[d]);
+        dv[d] = mma_transposed<DP>(qp + kBlock, 0, d, p0, dv[d]);
+        dk[d] = mma_transposed<DP>(qp, 0, d, e0, dk[d]);
       }
+    } else {
+      load();
+      int at = 0;
+      for (int b = 0; b < n; ++b) {
+        wait_vmcnt<0>();
+        lds_barrier();
+        const lds_char* qt = ring + at;
+        const lds_char* dt = qt + kBlock;
+        load();
+        f32x16_t s = {}, g = {};
+#pragma unroll
+        for (int st = 0; st < TL::kSteps; ++st) {
+          s = mma16(TL::row_frag(qt, 0, st), kf[st], s, T{});
+          g = mma16(TL::row_frag(dt, 0, st), vf[st], g, T{});
+        }
+        const lds_char* st = qt + 2 * kBlock + 16 * (lane >> 5);
+        const bool whole = static_cast<unsigned>(bn - whole_lo) < static_cast<unsigned>(whole_n);
+        const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t l4 = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
+          const f32x4_t d4 = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 4 * q + x;
+            const bool yes = whole | seen(r);
+            const float pr = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[x]));
+            g[r] = yes ? pr * (g[r] - d4[x]) : 0.0f;
+            s[r] = yes ? pr : 0.0f;
+          }
+        }
+        Column<T> pc, ds;
+        pc.set(s);
+        ds.set(g);
+#pragma unroll
+        for (int d = 0; d < TL::kDT; ++d) {
+          dv[d] = mma_transposed<DP>(dt, 0, d, pc, dv[d]);
+          dk[d] = mma_transposed<DP>(qt, 0, d, ds, dk[d]);
+        }
+        at = next_slot(at);
+        if (++bn == per_head) bn = 0;
+      }
+      wait_vmcnt<0>();
     }
   }
   bool bad = false;
@@ -520,8 +876,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(AttnView a, int64_
   for (int d = 0; d < TL::kDT; ++d) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) bad |= not_finite(dk[d][r]) || not_finite(dv[d][r]);
-    store_column<T>(a.dk, k0 + key, hk, a.head_dim, d, dk[d], a.scale, in);
-    store_column<T>(a.dv, k0 + key, hk, a.head_dim, d, dv[d], 1.0f, in);
+    store_column<T>(a.dk, w.k0 + key, hk, a.head_dim, d, dk[d], a.scale, in);
+    store_column<T>(a.dv, w.k0 + key, hk, a.head_dim, d, dv[d], 1.0f, in);
   }
   // a query that does not see the key may have brought it: see the forward
   uint64_t again = __ballot(bad && in);
@@ -529,46 +885,73 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_dkv_kernel(AttnView a, int64_
   while (again) {
     const int i = __builtin_ctzll(again);
     again &= again - 1;
-    attn_dkv_row<T>(a, delta_in, wkey + i, hk, q0, nq, k0, nk);
+    attn_dkv_row<T>(a, stats.delta, wkey + i, hk, w);
   }
 }
 
+// ------------------------------------------------------------------- launches
+// Raises a kernel's limit of dynamic LDS past the 64 KB that a launch gets
+// unasked (once a kernel), then launches it.
+template <auto kKernel, int kLds, typename... Args>
+static hipError_t launch_lds(int64_t wgs, hipStream_t s, Args... args) {
+  if (wgs == 0) return hipSuccess;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (attr != hipSuccess) return attr;
+  kKernel<<<static_cast<unsigned>(wgs), 64 * kWaves, kLds, s>>>(args...);
+  return hipGetLastError();
+}
+
+// Whether a head's rows may span 2^31 bytes.
+static bool wide(const HeadsView& t, int64_t rows, int elem_bytes) {
+  return t.row_stride >= (int64_t(1) << 31) / elem_bytes / (rows + 2 * kTileRows);
+}
+
+template <bool kWide>
+static hipError_t fwd_launch(const AttnView& a, int dtype, hipStream_t s, int* err) {
+  const int64_t n = slots(a.total_q, a.n_seqs), wgs = n * a.n_heads;
+  if (dtype == STAPLE_BF16) {
+    if (a.head_dim <= 64) return launch_lds<attn_fwd_bf16_kernel<64, kWide>, FwdShape<64>::kLds>(wgs, s, a, n, err);
+    return launch_lds<attn_fwd_bf16_kernel<128, kWide>, FwdShape<128>::kLds>(wgs, s, a, n, err);
+  }
+  if (a.head_dim <= 64) return launch_lds<attn_fwd_f32_kernel<64, kWide>, 4 * 32 * 256>(wgs, s, a, n, err);
+  return launch_lds<attn_fwd_f32_kernel<128, kWide>, 4 * 32 * 512>(wgs, s, a, n, err);
+}
+
 hipError_t launch_attn_fwd(const AttnView& a, int dtype, hipStream_t s, int* err) {
-  if (dtype == STAPLE_BF16)
-    return a.head_dim <= 64 ? fwd_launch<bf16_t, 64>(a, s, err) : fwd_launch<bf16_t, 128>(a, s, err);
-  return a.head_dim <= 64 ? fwd_launch<float, 64>(a, s, err) : fwd_launch<float, 128>(a, s, err);
+  const int es = dtype == STAPLE_BF16 ? 2 : 4;
+  return wide(a.k, a.total_k, es) || wide(a.v, a.total_k, es) ? fwd_launch<true>(a, dtype, s, err)
+                                                              : fwd_launch<false>(a, dtype, s, err);
 }
 
 size_t attn_bwd_workspace_bytes(const AttnView& a, int) {
   return 2 * align_up(static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float), 256);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kWide>
 static hipError_t bwd_launch(const AttnView& a, void* ws, hipStream_t s, int* err) {
-  constexpr int kNW = 4;
-  constexpr int kRows = sizeof(T) == 2 ? 64 : 32;
-  constexpr size_t kLds = size_t(4) * kRows * Tile<T, DP>::kRow;
   Workspace w(ws, attn_bwd_workspace_bytes(a, 0));
   const size_t bytes = static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float);
-  float* lse2 = w.take<float>(bytes);
-  float* delta = w.take<float>(bytes);
-  const int64_t nq = slots(a.total_q, a.n_seqs, 32 * kNW), nk = slots(a.total_k, a.n_seqs, 32 * kNW);
-  attn_dq_kernel<T, DP, kNW><<<static_cast<unsigned>(nq * a.n_heads), 64 * kNW, kLds, s>>>(a, nq, lse2, delta, err);
-  hipError_t e = hipGetLastError();
+  RowStats stats;
+  stats.lse2 = w.take<float>(bytes);
+  stats.delta = w.take<float>(bytes);
+  const int64_t nq = slots(a.total_q, a.n_seqs), nk = slots(a.total_k, a.n_seqs);
+  hipError_t e = launch_lds<attn_dq_kernel<T, DP, kWide>, DqShape<T, DP>::kLds>(nq * a.n_heads, s, a, nq, stats, err);
   if (e != hipSuccess) return e;
-  // more than the 64 KB of LDS that a launch gets unasked
-  const auto dkv = attn_dkv_kernel<T, DP, kNW>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(dkv),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds + 1024);
-  if (attr != hipSuccess) return attr;
-  dkv<<<static_cast<unsigned>(nk * a.n_kv_heads), 64 * kNW, kLds + 1024, s>>>(a, nk, lse2, delta, err);
-  return hipGetLastError();
+  return launch_lds<attn_dkv_kernel<T, DP, kWide>, DkvShape<T, DP>::kLds>(nk * a.n_kv_heads, s, a, nk, stats, err);
+}
+
+template <bool kWide>
+static hipError_t bwd_launch(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
+  if (dtype == STAPLE_BF16)
+    return a.head_dim <= 64 ? bwd_launch<bf16_t, 64, kWide>(a, ws, s, err) : bwd_launch<bf16_t, 128, kWide>(a, ws, s, err);
+  return a.head_dim <= 64 ? bwd_launch<float, 64, kWide>(a, ws, s, err) : bwd_launch<float, 128, kWide>(a, ws, s, err);
 }
 
 hipError_t launch_attn_bwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
-  if (dtype == STAPLE_BF16)
-    return a.head_dim <= 64 ? bwd_launch<bf16_t, 64>(a, ws, s, err) : bwd_launch<bf16_t, 128>(a, ws, s, err);
-  return a.head_dim <= 64 ? bwd_launch<float, 64>(a, ws, s, err) : bwd_launch<float, 128>(a, ws, s, err);
+  const int es = dtype == STAPLE_BF16 ? 2 : 4;
+  const bool far = wide(a.q, a.total_q, es) || wide(a.d_o, a.total_q, es) || wide(a.k, a.total_k, es) || wide(a.v, a.total_k, es);
+  return far ? bwd_launch<true>(a, dtype, ws, s, err) : bwd_launch<false>(a, dtype, ws, s, err);
 }
 
 }  // namespace staple

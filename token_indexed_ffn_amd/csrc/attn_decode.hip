@@ -28,8 +28,6 @@
 namespace staple {
 
 constexpr int kDecWaves = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 template <typename T, int DP>
 struct DecBlock {

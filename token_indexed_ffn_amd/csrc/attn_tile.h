@@ -69,32 +69,44 @@ template <> struct Column<bf16_t> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[t][i] = pack_bf16x2(x[8 * t + 2 * i], x[8 * t + 2 * i + 1]);
   }
+  // times a power of two
+  __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[t][i] = pack_bf16x2(__uint_as_float(v[t][i] << 16) * f, __uint_as_float(v[t][i] & 0xffff0000u) * f);
+  }
 };
 template <> struct Column<float> {
   f32x16_t v;
   __device__ __forceinline__ void set(const f32x16_t& x) { v = x; }
 };
 
-// acc += (rows [row0, row0 + 32) of the tile, elements [32 dt, 32 dt + 32))^T x column.
+// Transposed: the A operand of rows [row0 + 16 t, row0 + 16 t + 16) and head
+// elements [32 dt, 32 dt + 32), the rows in the order of a Column.
 template <int DP>
-__device__ __forceinline__ f32x16_t mma_transposed(const lds_char* tile, int row0, int dt,
-                                                   const Column<bf16_t>& col, f32x16_t acc) {
+__device__ __forceinline__ u32x4_t column_frag(const lds_char* tile, int row0, int t, int dt) {
   using TL = Tile<bf16_t, DP>;
   const int lane = threadIdx.x & 63, i16 = lane & 15;
   // 16 lanes read 4 rows x 16 elements and get 4 rows of one element each
   const int c = dt * 32 + (lane & 16) + 4 * (i16 & 3);
+  v4s_t part[2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    v4s_t part[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = row0 + 16 * t + 8 * e + 4 * (lane >> 5) + (i16 >> 2);
-      const lds_char* p = tile + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
-      part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p);
-    }
-    const v8s_t a = {part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2], part[1][3]};
-    acc = mma16(__builtin_bit_cast(u32x4_t, a), col.v[t], acc, bf16_t{});
+  for (int e = 0; e < 2; ++e) {
+    const int row = row0 + 16 * t + 8 * e + 4 * (lane >> 5) + (i16 >> 2);
+    const lds_char* p = tile + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
+    part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p);
   }
+  const v8s_t a = {part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2], part[1][3]};
+  return __builtin_bit_cast(u32x4_t, a);
+}
+// acc += (rows [row0, row0 + 32) of the tile, elements [32 dt, 32 dt + 32))^T x column.
+template <int DP>
+__device__ __forceinline__ f32x16_t mma_transposed(const lds_char* tile, int row0, int dt,
+                                                   const Column<bf16_t>& col, f32x16_t acc) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) acc = mma16(column_frag<DP>(tile, row0, t, dt), col.v[t], acc, bf16_t{});
   return acc;
 }
 template <int DP>
@@ -117,35 +129,67 @@ __device__ const uint4 g_attn_zeros[1] = {};
 
 // Copies R-row tiles of one head from global memory straight into LDS, 16
 // bytes a lane.  Instruction i of wave w fills 1 KB of the tile; the lane's
-// source is the chunk that its LDS place holds.
-template <typename T, int DP, int R, int NW>
+// source is the chunk that its LDS place holds.  Rows past the sequence and
+// elements past head_dim come as zeros: they lie past the end of the head's
+// buffer, which is laid over the rows that exist.  kWide: row strides so large
+// that a buffer could span 2^31 bytes; 64-bit addresses then take its place.
+template <typename T, int DP, int R, int NW, bool kWide>
 struct TileLoader {
   using TL = Tile<T, DP>;
-  static constexpr int kPer = R * TL::kRow / (1024 * NW);
-  static_assert(kPer * 1024 * NW == R * TL::kRow, "tile shape");
+  static constexpr int kPer = R * TL::kRow / (1024 * NW);   // instructions per wave
+  static constexpr int kRowStep = 1024 * NW / TL::kRow;     // rows between them
+  // the spread repeats every 16 rows; 8 rows on, its lowest bit is the other one
+  static constexpr bool kFlip = kRowStep % 16 != 0;
+  static_assert(kPer * 1024 * NW == R * TL::kRow && (kRowStep % 16 == 0 || (kRowStep == 8 && TL::kChunks >= 16)), "tile shape");
   const char* base;        // row 0 of the sequence, this head
   int64_t row_bytes;
-  int dim_bytes;
+  int n, dim_bytes;
+  int row, byte;           // the lane's row and byte of it in instruction 0
+  uint32_t offset[kPer];
+  u32x4_t buffer;
+  uint32_t lds0;           // this wave's first byte of a tile
 
-  __device__ __forceinline__ void init(const HeadsView& t, int64_t row, int64_t head, int dim) {
+  __device__ __forceinline__ void init(const HeadsView& t, int64_t row0, int rows, int64_t head, int dim) {
     row_bytes = t.row_stride * static_cast<int64_t>(sizeof(T));
-    base = t.data + row * row_bytes + head * t.head_stride * static_cast<int64_t>(sizeof(T));
+    n = rows;
     dim_bytes = dim * static_cast<int>(sizeof(T));
-  }
-  // Rows [row0, row0 + R) of the sequence's n.
-  __device__ __forceinline__ void load(int64_t row0, int64_t n, lds_char* lds) const {
-    const int w = threadIdx.x >> 6;
-    const int left = static_cast<int>(n - row0 < R ? n - row0 : R);
-    const char* tile = base + row0 * row_bytes;
+    const int at = (threadIdx.x >> 6) * 1024 + (threadIdx.x & 63) * 16;
+    lds0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    row = at / TL::kRow;
+    byte = ((at % TL::kRow / 16) ^ TL::spread(row)) * 16;
+    if constexpr (!kWide) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int byte = (i * NW + w) * 1024 + (threadIdx.x & 63) * 16;
-      const int row = byte / TL::kRow;
-      const int chunk = (byte % TL::kRow / 16) ^ TL::spread(row);
-      const char* src = tile + row * row_bytes + chunk * 16;
-      const bool in = row < left && chunk * 16 < dim_bytes;
-      dma16(in ? static_cast<const void*>(src) : static_cast<const void*>(g_attn_zeros),
-            static_cast<lds_void*>(lds + (i * NW + w) * 1024));
+      for (int i = 0; i < kPer; ++i) {
+        const int x = kFlip && (i & 1) ? byte ^ 16 : byte;
+        offset[i] = x < dim_bytes ? static_cast<uint32_t>(row + i * kRowStep) * static_cast<uint32_t>(row_bytes) + x : 0x80000000u;
+      }
+    }
+    set_base(t.data + row0 * row_bytes + head * t.head_stride * static_cast<int64_t>(sizeof(T)));
+  }
+  __device__ __forceinline__ void set_base(const char* b) {
+    base = b;
+    if constexpr (!kWide)
+      buffer = make_buffer(base, n > 0 ? static_cast<uint32_t>((n - 1) * row_bytes) + dim_bytes : 0u);
+  }
+  __device__ __forceinline__ void next_head(const HeadsView& t) {
+    set_base(base + t.head_stride * static_cast<int64_t>(sizeof(T)));
+  }
+  // Rows [row0, row0 + R) of the sequence; row0 at most R past its end.
+  __device__ __forceinline__ void load(int row0, lds_char* lds) const {
+    lds_char* const to = lds + lds0;
+    if constexpr (!kWide) {
+      const uint32_t first = static_cast<uint32_t>(row0) * static_cast<uint32_t>(row_bytes);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) dma16(buffer, offset[i] + first, static_cast<lds_void*>(to + i * NW * 1024));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = row0 + row + i * kRowStep;
+        const int x = kFlip && (i & 1) ? byte ^ 16 : byte;
+        dma16(r < n && x < dim_bytes ? static_cast<const void*>(base + r * row_bytes + x)
+                                     : static_cast<const void*>(g_attn_zeros),
+              static_cast<lds_void*>(to + i * NW * 1024));
+      }
     }
   }
 };
@@ -180,6 +224,10 @@ __device__ __forceinline__ u32x4_t flip_sign(u32x4_t v) {
   const uint32_t m = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
   return v ^ u32x4_t{m, m, m, m};
 }
+
+// Keeps a value's computation where it stands in the program, between the
+// products around it, instead of where it is used.
+__device__ __forceinline__ void pin(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // The other half-wave's value of the same column.
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
@@ -222,11 +270,6 @@ __device__ __forceinline__ void store_column<float>(const HeadsView& t, int64_t 
     if (in && e < dim)
       *reinterpret_cast<f32x4_t*>(p + e * 4) = f32x4_t{x[4 * g] * mul, x[4 * g + 1] * mul, x[4 * g + 2] * mul, x[4 * g + 3] * mul};
   }
-}
-
-// Relative positions as small integers (a tile is far narrower than the clamp).
-__device__ __forceinline__ int clamp_rel(int64_t v) {
-  return static_cast<int>(v < -(1 << 20) ? -(1 << 20) : v > (1 << 20) ? (1 << 20) : v);
 }
 
 }  // namespace staple
