@@ -46,19 +46,27 @@ struct Segment {
   int64_t q0, k0;          // first rows
   int nq, nk, past;        // lengths, and the position of query 0
   int first;               // the tile's first query (key)
-  // False where the workgroup has nothing to do.
-  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int64_t slot, int* err) {
+  // False where there is no such tile.  find_lane: any slot a lane; find: one
+  // slot for the whole workgroup, kept in scalar registers.
+  __device__ __forceinline__ bool find_lane(const AttnView& a, const int32_t* cu, int64_t slot, int* err) {
     const TileOf tile = tile_of_slot(cu, a.n_seqs, slot);
     if (tile.seq < 0) return false;
     int64_t q1, k1;
     seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
     seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
     if (tile.first >= (cu == a.cu_q ? q1 - q0 : k1 - k0)) return false;
-    // the same for every lane, and kept in scalar registers
-    nq = uniform(static_cast<int>(q1 - q0));
-    nk = uniform(static_cast<int>(k1 - k0));
+    nq = static_cast<int>(q1 - q0);
+    nk = static_cast<int>(k1 - k0);
     past = nk - nq;
-    first = uniform(static_cast<int>(tile.first));
+    first = static_cast<int>(tile.first);
+    return true;
+  }
+  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int64_t slot, int* err) {
+    if (!find_lane(a, cu, slot, err)) return false;
+    nq = uniform(nq);
+    nk = uniform(nk);
+    past = nk - nq;
+    first = uniform(first);
     q0 = uniform(static_cast<int>(q0));
     k0 = uniform(static_cast<int>(k0));
     return true;
@@ -139,12 +147,11 @@ struct QueryCols : Segment {
   int head, hk;
   int wq, row, p;             // the wave's first query; the lane's, and its position
   bool in;
-  __device__ __forceinline__ bool find(const AttnView& a, int64_t n_slots, int* err) {
-    const int64_t id = blockIdx.x;
+  __device__ __forceinline__ bool find(const AttnView& a, int64_t n_slots, int64_t id, int* err) {
     // the last tiles of a sequence see the most keys: they start first
     if (!Segment::find(a, a.cu_q, n_slots - 1 - id / a.n_heads, err)) return false;
-    head = static_cast<int>(id % a.n_heads);
-    hk = head / a.group;
+    head = uniform(static_cast<int>(id % a.n_heads));
+    hk = uniform(head / a.group);
     wq = first + 32 * wave_id();
     row = wq + (threadIdx.x & 31);
     in = row < nq;
@@ -262,7 +269,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   lds_char* const lds = (lds_char*)smem;               // [2][K, V]
   check_offsets(a, err);
   QueryCols w;
-  if (!w.find(a, n_slots, err)) return;
+  if (!w.find(a, n_slots, blockIdx.x, err)) return;
   const KeyBlocks keys = w.blocks(a);
   u32x4_t qf[TL::kSteps];
   const float c = load_queries<T, DP>(a, w, qf);
@@ -308,57 +315,53 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
 // bf16.  A block (32 keys x 32 queries at DP 128) is 16 MFMAs, 512 cycles, and
 // 16 exponentials a lane, nearly as many cycles of vector work.  So the wave
 // runs three blocks at a time: between the exponentials of block b stand the
-// score products of block b + 1 and the value products of block b - 1.
+// score products of block b + 1 and the value products of block b - 1.  The
+// workgroup meets every second block: a stage loads two blocks of K and of V
+// while the two before are worked on.
 template <int DP>
 struct FwdShape {
-  static constexpr int kAhead = 3, kSlots = 4;   // slots of a ring: the blocks in flight and the one at hand
   static constexpr int kBlock = 32 * Tile<bf16_t, DP>::kRow;
-  static constexpr int kLds = 2 * kSlots * kBlock;
+  static constexpr int kLds = 8 * kBlock;   // rings of four K blocks and four V blocks
 };
 template <int DP, bool kWide>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, int* err) {
   using T = bf16_t;
   using TL = Tile<T, DP>;
-  using Shape = FwdShape<DP>;
-  constexpr int kAhead = Shape::kAhead, kMask = Shape::kSlots - 1, kBlock = Shape::kBlock;
+  constexpr int kBlock = FwdShape<DP>::kBlock;
   extern __shared__ __align__(1024) char smem[];
   lds_char* const kring = (lds_char*)smem;
-  lds_char* const vring = kring + Shape::kSlots * kBlock;
+  lds_char* const vring = kring + 4 * kBlock;
   check_offsets(a, err);
   QueryCols w;
-  if (!w.find(a, n_slots, err)) return;
+  if (!w.find(a, n_slots, blockIdx.x, err)) return;
   const KeyBlocks keys = w.blocks(a);
   f32x16_t o[TL::kDT] = {};
   ColumnSoftmax sm;
   if (keys.n > 0) {
-    using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
-    Loader kl, vl;
+    TileLoader<T, DP, 32, kWaves, kWide> kl, vl;
     kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
     vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
-    constexpr int kLoads = 2 * Loader::kPer;   // instructions a wave and step
 #pragma unroll
-    for (int b = 0; b <= kAhead; ++b) kl.load(keys.first(b), kring + (b & kMask) * kBlock);
+    for (int b = 0; b < 4; ++b) kl.load(keys.first(b), kring + b * kBlock);
 #pragma unroll
-    for (int b = 0; b < kAhead - 1; ++b) vl.load(keys.first(b), vring + (b & kMask) * kBlock);
+    for (int b = 0; b < 2; ++b) vl.load(keys.first(b), vring + b * kBlock);
     u32x4_t qf[TL::kSteps];
     const float c = load_queries<T, DP>(a, w, qf);
     wait_vmcnt<0>();
     lds_barrier();
     f32x16_t s0 = {}, s1;
     Column<T> p0, p1;
+    RowReader<T, DP> rows(kring);
+    ColumnReader<DP> cols(vring);
 #pragma unroll
-    for (int st = 0; st < TL::kSteps; ++st) s0 = mma16(TL::row_frag(kring, 0, st), qf[st], s0, T{});
+    for (int st = 0; st < TL::kSteps; ++st) s0 = mma16(rows.read(st, 0), qf[st], s0, T{});
 
     // Step b: exponentials of s (block b) into p, scores of block b + 1 into
-    // next, values of block b - 1 with the weights prev.
-    auto step = [&](auto is_first, int b, f32x16_t& s, f32x16_t& next, Column<T>& prev, Column<T>& p) {
+    // next, values of block b - 1 with the weights prev; `at` bytes past the
+    // readers' places.
+    auto step = [&](auto is_first, auto place, int b, f32x16_t& s, f32x16_t& next, Column<T>& prev, Column<T>& p) {
       constexpr bool kFirst = decltype(is_first)::value;
-      wait_vmcnt<(kAhead - 1) * kLoads>();   // K of block b + 1, V of block b - 1
-      lds_barrier();
-      kl.load(keys.first(b + kAhead + 1), kring + ((b + kAhead + 1) & kMask) * kBlock);
-      vl.load(keys.first(b + kAhead - 1), vring + ((b + kAhead - 1) & kMask) * kBlock);
-      const lds_char* kt = kring + ((b + 1) & kMask) * kBlock;
-      const lds_char* vt = vring + ((b - 1) & kMask) * kBlock;
+      constexpr int at = decltype(place)::value;
       if (!keys.whole(b)) mask_keys(a, w, keys.first(b), s);
       float keep;
       if (sm.raise(s, c, &keep)) {
@@ -374,8 +377,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
       u32x4_t kf[2], vf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        kf[i] = TL::row_frag(kt, 0, i);
-        if constexpr (!kFirst) vf[i] = column_frag<DP>(vt, 0, i & 1, i >> 1);
+        kf[i] = rows.read(i, at);
+        if constexpr (!kFirst) vf[i] = cols.read(i & 1, i >> 1, at);
       }
       float even = 0.0f;
       auto element = [&](int r) {
@@ -393,13 +396,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
       for (int i = 0; i < kPairs; ++i) {
         __builtin_amdgcn_sched_barrier(0);
         next = mma16(kf[i & 1], qf[i], i == 0 ? f32x16_t{} : next, T{});
-        if (i + 2 < kPairs) kf[i & 1] = TL::row_frag(kt, 0, i + 2);
+        if (i + 2 < kPairs) kf[i & 1] = rows.read(i + 2, at);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) element(2 * kPer * i + e);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (!kFirst) {
           o[i >> 1] = mma16(vf[i & 1], prev.v[i & 1], o[i >> 1], T{});
-          if (i + 2 < kPairs) vf[i & 1] = column_frag<DP>(vt, 0, i & 1, (i + 2) >> 1);
+          if (i + 2 < kPairs) vf[i & 1] = cols.read(i & 1, (i + 2) >> 1, at);
         }
 #pragma unroll
         for (int e = 0; e < kPer; ++e) element(2 * kPer * i + kPer + e);
@@ -409,17 +412,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
     // an odd number of steps, the last one's keys all hidden where it is one
     // more than there are blocks: the pair's registers change roles in place
     const int n = keys.n | 1;
-    step(std::true_type{}, 0, s0, s1, p1, p0);
+    using Low = std::integral_constant<int, 0>;
+    using High = std::integral_constant<int, kBlock>;
+    step(std::true_type{}, High{}, 0, s0, s1, p1, p0);
+    // a stage's blocks b - 1 and b lie in one half of the V ring, b + 1 and b +
+    // 2 in the other half of K's
+    int half = 0;
+    rows.move(2 * kBlock);
     for (int b = 1; b < n; b += 2) {
-      step(std::false_type{}, b, s1, s0, p0, p1);
-      step(std::false_type{}, b + 1, s0, s1, p1, p0);
+      const int other = 2 * kBlock - half;
+      wait_vmcnt<0>();   // the last stage's loads
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kl.load(keys.first(b + 3 + i), kring + half + i * kBlock);
+        vl.load(keys.first(b + 1 + i), vring + other + i * kBlock);
+      }
+      step(std::false_type{}, Low{}, b, s1, s0, p0, p1);
+      step(std::false_type{}, High{}, b + 1, s0, s1, p1, p0);
+      rows.move(half - other);
+      cols.move(other - half);
+      half = other;
     }
     // the last block's values
     wait_vmcnt<0>();
     lds_barrier();
-    const lds_char* vt = vring + ((n - 1) & kMask) * kBlock;
 #pragma unroll
-    for (int d = 0; d < TL::kDT; ++d) o[d] = mma_transposed<DP>(vt, 0, d, p0, o[d]);
+    for (int d = 0; d < TL::kDT; ++d)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) o[d] = mma16(cols.read(x, d, 0), p0.v[x], o[d], T{});
   }
   finish_fwd<T, DP>(a, w, sm, o);
 }
@@ -481,6 +502,109 @@ struct RowStats {
   float* delta;
 };
 
+// The 32-query blocks that see some key of a workgroup's tile: `per_head` of
+// them, from block b_lo, for each head of the group.
+struct QueryBlocks {
+  int b_lo, per_head;
+  __device__ __forceinline__ QueryBlocks(const AttnView& a, const Segment& w) {
+    const int last_key = min(w.first + kTileRows, w.nk) - 1;
+    const int lo = max(w.first - w.past, 0);
+    const int hi = a.window > 0 && w.first >= a.sinks ? min(last_key - w.past + a.window, w.nq) : w.nq;
+    b_lo = lo / 32;
+    per_head = hi > lo ? (hi + 31) / 32 - b_lo : 0;
+  }
+};
+
+// How dk and dv are worked off.  Key tiles see very different numbers of
+// queries (the first of a causal sequence all of them, a window's only its
+// own, the sinks' all again), and a shared key-value head those of every head
+// of its group.  A tile with more blocks than `chunk` is split into parts of
+// equal size, whose fp32 sums go to the workspace and are added in part order
+// by the last of them to finish; and the items (tiles and parts) start in the
+// order of their size, the largest first.  Written by one workgroup of the dq
+// kernel, which runs before.
+struct DkvPlan {
+  int32_t* head;      // [0] items
+  int32_t* blocks;    // [slots] blocks of the slot's tile
+  int32_t* parts;     // [slots] its parts
+  int32_t* first;     // [slots] its first partial result, where there are several parts
+  int32_t* split;     // [slots] its number among the split tiles
+  int32_t* items;     // [slots + max_parts][2] slot, part
+  int32_t* done;      // [max_parts][n_kv_heads] parts of a split tile that have finished
+  float* sums;        // [max_parts][n_kv_heads] dk and dv sums of a part
+  int64_t n_slots;
+  int target;         // parts per head to aim for
+};
+constexpr int kMinChunk = 16;   // blocks: a part's sums cost about as much traffic as two blocks
+constexpr int kBuckets = 64;
+
+__device__ __forceinline__ int64_t group_sum(int64_t v, int64_t* lds) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) all += lds[i];
+  return all;
+}
+
+__device__ void plan_dkv(const AttnView& a, const DkvPlan& plan, int* err) {
+  __shared__ int64_t sums[kWaves];
+  __shared__ int count[kBuckets], start[kBuckets], n_parts, n_split;
+  constexpr int kThreads = 64 * kWaves;
+  const int n_slots = static_cast<int>(plan.n_slots);
+  int64_t mine = 0;
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    Segment w;
+    int n = -1;   // no tile
+    if (w.find_lane(a, a.cu_k, s, err)) n = QueryBlocks(a, w).per_head * a.group;
+    plan.blocks[s] = n;
+    mine += max(n, 0);
+  }
+  const int64_t total = group_sum(mine, sums);
+  const int64_t share = (total + plan.target - 1) / plan.target;
+  const int chunk = static_cast<int>(share < kMinChunk ? kMinChunk : share);
+  if (threadIdx.x < kBuckets) count[threadIdx.x] = 0;
+  if (threadIdx.x == 0) n_parts = n_split = 0;
+  __syncthreads();
+  // an item has at most `chunk` blocks; bucket 0 holds the largest
+  auto bucket = [&](int size) { return kBuckets - 1 - static_cast<int>(static_cast<int64_t>(size) * (kBuckets - 1) / chunk); };
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    const int n = plan.blocks[s];
+    if (n < 0) continue;
+    const int parts = max((n + chunk - 1) / chunk, 1);
+    plan.parts[s] = parts;
+    if (parts > 1) {
+      plan.first[s] = atomicAdd(&n_parts, parts);
+      plan.split[s] = atomicAdd(&n_split, 1);
+    }
+    atomicAdd(&count[bucket((n + parts - 1) / parts)], parts);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int at = 0;
+    for (int b = 0; b < kBuckets; ++b) {
+      start[b] = at;
+      at += count[b];
+    }
+    plan.head[0] = at;
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    const int n = plan.blocks[s];
+    if (n < 0) continue;
+    const int parts = plan.parts[s];
+    int at = atomicAdd(&start[bucket((n + parts - 1) / parts)], parts);
+    for (int p = 0; p < parts; ++p, ++at) {
+      plan.items[2 * at] = s;
+      plan.items[2 * at + 1] = p;
+    }
+  }
+  for (int i = threadIdx.x; i < n_split * a.n_kv_heads; i += kThreads) plan.done[i] = 0;
+}
+
 // dq, and the row statistics for the other kernel.  In bf16 a block is 16
 // MFMAs for the scores and their gradients, then 16 elements of vector work
 // with the 8 MFMAs of the block before in between.
@@ -493,7 +617,7 @@ struct DqShape {
 };
 template <typename T, int DP, bool kWide>
 __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnView a, int64_t n_slots, RowStats stats,
-                                                                                      int* err) {
+                                                                                      DkvPlan plan, int* err) {
   using TL = Tile<T, DP>;
   using Shape = DqShape<T, DP>;
   using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
@@ -503,7 +627,11 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
   lds_char* const vring = kring + Shape::kKSlots * kBlock;
   check_offsets(a, err);
   QueryCols w;
-  if (!w.find(a, n_slots, err)) return;
+  if (blockIdx.x == 0) {
+    plan_dkv(a, plan, err);
+    return;
+  }
+  if (!w.find(a, n_slots, static_cast<int64_t>(blockIdx.x) - 1, err)) return;
   const KeyBlocks keys = w.blocks(a);
   const int half = (threadIdx.x & 63) >> 5;
   Loader kl, vl;
@@ -637,61 +765,68 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
 // group) go through LDS.  The two results take 2 DP registers a lane, so one
 // workgroup has a CU to itself and in bf16 the wave runs three blocks at a
 // time by itself, as in the forward: between the elements of block b stand the
-// score products of block b + 1 and the gradient products of block b - 1.
+// score products of block b + 1 and the gradient products of block b - 1, and
+// the workgroup meets every second block.
 template <typename T, int DP>
 struct DkvShape {
-  static constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
-  static constexpr int kSlots = sizeof(T) == 2 ? kAhead + 3 : 2;
   static constexpr int kBlock = 32 * Tile<T, DP>::kRow;
   static constexpr int kStage = 2 * kBlock + 512;   // Q, dO, lse2, delta (256 bytes each, half of it used)
+  static constexpr int kSlots = sizeof(T) == 2 ? 6 : 2;
   static constexpr int kLds = kSlots * kStage;
+  // fp32 sums of one part: per wave dk and dv, as they lie in registers
+  static constexpr int kSums = kWaves * 2 * 64 * 16 * Tile<T, DP>::kDT;
 };
+// Keeps an operand of the products in the accumulation registers, so that the
+// vector registers hold what vector instructions work on.
+__device__ __forceinline__ void park(u32x4_t& v) { asm volatile("" : "+a"(v)); }
+
 template <typename T, int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, int64_t n_slots, RowStats stats, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
   using TL = Tile<T, DP>;
   using Shape = DkvShape<T, DP>;
   using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
-  constexpr int kAhead = Shape::kAhead, kBlock = Shape::kBlock, kStage = Shape::kStage;
+  constexpr int kBlock = Shape::kBlock, kStage = Shape::kStage;
   extern __shared__ __align__(1024) char smem[];
   lds_char* const ring = (lds_char*)smem;
-  const int64_t id = blockIdx.x;
+  const int item = uniform(static_cast<int>(blockIdx.x) / a.n_kv_heads);
+  const int hk = static_cast<int>(blockIdx.x) - item * a.n_kv_heads;
+  if (item >= plan.head[0]) return;
+  const int slot = uniform(plan.items[2 * item]), part = uniform(plan.items[2 * item + 1]);
+  const int parts = uniform(plan.parts[slot]);
   Segment w;
-  if (!w.find(a, a.cu_k, id / a.n_kv_heads, err)) return;   // the first keys are seen most: they start first
+  if (!w.find(a, a.cu_k, slot, err)) return;
   const int lane = threadIdx.x & 63;
-  const int hk = static_cast<int>(id % a.n_kv_heads);
   const int wkey = w.first + 32 * wave_id();   // the wave's first key
   const int key = wkey + (lane & 31);
   const bool in = key < w.nk;
 
-  // 32-query blocks that see some key of the workgroup, for each head of the group
-  const int last_key = min(w.first + kTileRows, w.nk) - 1;
-  const int i_lo = max(w.first - w.past, 0);
-  const int i_hi = a.window > 0 && w.first >= a.sinks ? min(last_key - w.past + a.window, w.nq) : w.nq;
-  const int b_lo = i_lo / 32, per_head = i_hi > i_lo ? (i_hi + 31) / 32 - b_lo : 0;
-  const int n = per_head * a.group;
-  // of these, the blocks whose every query sees all of the wave's keys
-  const bool keys_in = wkey + 31 < w.nk;
+  const QueryBlocks blocks(a, w);
+  const int b_lo = blocks.b_lo, per_head = blocks.per_head;
+  // this part's blocks: n of them, from block ln of head h0
+  const int all = per_head * a.group, chunk = uniform((all + parts - 1) / parts);
+  const int from_block = min(part * chunk, all), n = min(chunk, all - from_block);
+  const int skip = uniform(per_head > 0 ? from_block / per_head : 0);
+  const int64_t h0 = static_cast<int64_t>(hk) * a.group + skip;
+  int ln = from_block - skip * per_head, bn = ln;   // to load next; at hand
+  // of a head's blocks, those whose every query sees all of the wave's keys
   const int from = (max(wkey + 31 - w.past, 0) + 31) / 32;
   const int to = (a.window > 0 && wkey + 31 >= a.sinks ? min(max(wkey - w.past + a.window, 0), w.nq) : w.nq) / 32;
-  const int whole_lo = from - b_lo, whole_n = keys_in ? max(to - from, 0) : 0;
+  const int whole_lo = from - b_lo, whole_n = wkey + 31 < w.nk ? max(to - from, 0) : 0;
+  auto whole = [&](int b) { return static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n); };
 
   Loader ql, dl;
-  const int64_t h0 = static_cast<int64_t>(hk) * a.group;
   ql.init(a.q, w.q0, w.nq, h0, a.head_dim);
   dl.init(a.d_o, w.q0, w.nq, h0, a.head_dim);
   const int sw = wave_id();
   const float* stat = (sw & 1 ? stats.delta : stats.lse2) + h0 * a.total_q + w.q0;
-  // the next block to load: number ln (of per_head) of its head, into place lp
-  int ln = 0, lp = 0, left = n;
-  auto load = [&]() {
-    // past the last block: nothing, but it counts
+  int left = n;
+  auto load = [&](lds_char* to_slot) {
+    // past the last block: zeros
     const int i0 = left > 0 ? (b_lo + ln) * 32 : w.nq;
-    lds_char* const at = ring + lp;
-    ql.load(i0, at);
-    dl.load(i0, at + kBlock);
-    // every wave loads one statistic (two of them the same): the counts agree
-    dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(at + 2 * kBlock + 256 * (sw & 1)));
-    lp = lp + kStage == Shape::kLds ? 0 : lp + kStage;
+    ql.load(i0, to_slot);
+    dl.load(i0, to_slot + kBlock);
+    // two waves load either statistic, the same values to the same place
+    dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(to_slot + 2 * kBlock + 256 * (sw & 1)));
     --left;
     if (++ln == per_head) {
       ln = 0;
@@ -700,7 +835,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
       if (left > 0) stat += a.total_q;
     }
   };
-  constexpr int kLoads = 2 * Loader::kPer + 1;
   f32x16_t dk[TL::kDT] = {}, dv[TL::kDT] = {};
   const float c = score_factor(a);
   if (n > 0) {
@@ -709,45 +843,43 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
     for (int s = 0; s < TL::kSteps; ++s) {
       kf[s] = signed_frag<T>(a, load_frag<T>(a.k, w.k0 + key, hk, a.head_dim, s, in));
       vf[s] = load_frag<T>(a.v, w.k0 + key, hk, a.head_dim, s, in);
+      if constexpr (sizeof(T) == 2 && DP == 128) {
+        park(kf[s]);
+        park(vf[s]);
+      }
     }
-    int bn = 0;   // the block at hand, within its head
-    auto next_slot = [](int at) { return at + kStage == Shape::kLds ? 0 : at + kStage; };
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int b = 0; b <= kAhead; ++b) load();
+      for (int b = 0; b < 4; ++b) load(ring + b * kStage);
       wait_vmcnt<0>();
       lds_barrier();
       f32x16_t s0 = {}, s1, g0 = {}, g1;
       Column<T> p0, p1, e0, e1;   // probabilities and score gradients
+      RowReader<T, DP> rows(ring);
+      ColumnReader<DP> cols(ring);
+      const lds_char* const stat0 = ring + 2 * kBlock + 16 * (lane >> 5);
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
-        s0 = mma16(TL::row_frag(ring, 0, st), kf[st], s0, T{});
-        g0 = mma16(TL::row_frag(ring + kBlock, 0, st), vf[st], g0, T{});
+        s0 = mma16(rows.read(st, 0), kf[st], s0, T{});
+        g0 = mma16(rows.read(st, kBlock), vf[st], g0, T{});
       }
-      int at_prev = 0, at = 0;
-      auto step = [&](auto is_first, f32x16_t& s, f32x16_t& g, f32x16_t& sn, f32x16_t& gn, Column<T>& pp, Column<T>& ep,
-                      Column<T>& p, Column<T>& e) {
+      // Step b: elements of block b (products s and g, statistics at st) into
+      // p and e, score products of block b + 1 into sn and gn, gradients of
+      // block b - 1 from pp and ep; `place` bytes past the readers' places.
+      auto step = [&](auto is_first, auto place, const lds_char* st, f32x16_t& s, f32x16_t& g, f32x16_t& sn, f32x16_t& gn,
+                      Column<T>& pp, Column<T>& ep, Column<T>& p, Column<T>& e) {
         constexpr bool kFirst = decltype(is_first)::value;
-        wait_vmcnt<(kAhead - 1) * kLoads>();   // block b + 1
-        lds_barrier();
-        load();
-        const int at_next = next_slot(at);
-        const lds_char* qn = ring + at_next;
-        const lds_char* dn = qn + kBlock;
-        const lds_char* qp = ring + at_prev;
-        const lds_char* dp = qp + kBlock;
-        const lds_char* st = ring + at + 2 * kBlock + 16 * (lane >> 5);
-        const bool whole = static_cast<unsigned>(bn - whole_lo) < static_cast<unsigned>(whole_n);
-        const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
+        constexpr int kAt = decltype(place)::value;
         f32x4_t l4[4], d4[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           l4[q] = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
           d4[q] = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
         }
-        if (!whole) {
+        if (!whole(bn)) {
           // hidden pairs: probability and gradient zero, whatever the products
           // and the query's statistics are
+          const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const bool yes = seen(r);
@@ -776,11 +908,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
         u32x4_t qa[2], da[2], qt[2], dt[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          qa[i] = TL::row_frag(qn, 0, i);
-          da[i] = TL::row_frag(dn, 0, i);
+          qa[i] = rows.read(i, kAt);
+          da[i] = rows.read(i, kAt + kBlock);
           if constexpr (!kFirst) {
-            dt[i] = column_frag<DP>(dp, 0, i & 1, i >> 1);
-            qt[i] = column_frag<DP>(qp, 0, i & 1, i >> 1);
+            dt[i] = cols.read(i & 1, i >> 1, kAt + kBlock);
+            qt[i] = cols.read(i & 1, i >> 1, kAt);
           }
         }
 #pragma unroll
@@ -788,53 +920,66 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
           const int x = i & 1;
           __builtin_amdgcn_sched_barrier(0);
           sn = mma16(qa[x], kf[i], i == 0 ? f32x16_t{} : sn, T{});
-          if (i + 2 < kQuads) qa[x] = TL::row_frag(qn, 0, i + 2);
+          if (i + 2 < kQuads) qa[x] = rows.read(i + 2, kAt);
 #pragma unroll
           for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + r);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (!kFirst) {
             dv[i >> 1] = mma16(dt[x], pp.v[x], dv[i >> 1], T{});
-            if (i + 2 < kQuads) dt[x] = column_frag<DP>(dp, 0, x, (i + 2) >> 1);
+            if (i + 2 < kQuads) dt[x] = cols.read(x, (i + 2) >> 1, kAt + kBlock);
           }
           __builtin_amdgcn_sched_barrier(0);
           gn = mma16(da[x], vf[i], i == 0 ? f32x16_t{} : gn, T{});
-          if (i + 2 < kQuads) da[x] = TL::row_frag(dn, 0, i + 2);
+          if (i + 2 < kQuads) da[x] = rows.read(i + 2, kAt + kBlock);
 #pragma unroll
           for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + 8 / kQuads + r);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (!kFirst) {
             dk[i >> 1] = mma16(qt[x], ep.v[x], dk[i >> 1], T{});
-            if (i + 2 < kQuads) qt[x] = column_frag<DP>(qp, 0, x, (i + 2) >> 1);
+            if (i + 2 < kQuads) qt[x] = cols.read(x, (i + 2) >> 1, kAt);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
-        at_prev = at;
-        at = at_next;
         if (++bn == per_head) bn = 0;
       };
-      // as in the forward: an odd number of steps, one of them over zeros
-      step(std::true_type{}, s0, g0, s1, g1, p1, e1, p0, e0);
+      using Low = std::integral_constant<int, 0>;
+      using High = std::integral_constant<int, kStage>;
+      // as in the forward, an odd number of steps, one of them over zeros; a
+      // stage's blocks b - 1 and b lie in one pair of slots, b + 1 and b + 2 in
+      // the next, and the pair after that is loaded
+      step(std::true_type{}, High{}, stat0, s0, g0, s1, g1, p1, e1, p0, e0);
+      auto next_pair = [](int at) { return at + 2 * kStage == Shape::kLds ? 0 : at + 2 * kStage; };
+      int here = 0;
+      rows.move(2 * kStage);
       for (int b = 1; b < (n | 1); b += 2) {
-        step(std::false_type{}, s1, g1, s0, g0, p0, e0, p1, e1);
-        step(std::false_type{}, s0, g0, s1, g1, p1, e1, p0, e0);
+        const int ahead = next_pair(here), after = next_pair(ahead);
+        wait_vmcnt<0>();   // the last stage's loads
+        lds_barrier();
+        load(ring + after);
+        load(ring + after + kStage);
+        step(std::false_type{}, Low{}, stat0 + here + kStage, s1, g1, s0, g0, p0, e0, p1, e1);
+        step(std::false_type{}, High{}, stat0 + ahead, s0, g0, s1, g1, p1, e1, p0, e0);
+        rows.move(after - ahead);
+        cols.move(ahead - here);
+        here = ahead;
       }
-      if ((n & 1) == 0) p0.v[0] = p0.v[1] = e0.v[0] = e0.v[1] = u32x4_t{0, 0, 0, 0};
-      wait_vmcnt<0>();
-      const lds_char* qp = ring + at_prev;
+      if ((n & 1) == 0) p0.v[0] = p0.v[1] = e0.v[0] = e0.v[1] = u32x4_t{0, 0, 0, 0};   // the step over zeros
 #pragma unroll
-      for (int d = 0; d < TL::kDT; ++d) {
-        dv[d] = mma_transposed<DP>(qp + kBlock, 0, d, p0, dv[d]);
-        dk[d] = mma_transposed<DP>(qp, 0, d, e0, dk[d]);
-      }
+      for (int d = 0; d < TL::kDT; ++d)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          dv[d] = mma16(cols.read(x, d, kBlock), p0.v[x], dv[d], T{});
+          dk[d] = mma16(cols.read(x, d, 0), e0.v[x], dk[d], T{});
+        }
+      wait_vmcnt<0>();   // no load into LDS outlives the workgroup
     } else {
-      load();
-      int at = 0;
+      load(ring);
       for (int b = 0; b < n; ++b) {
         wait_vmcnt<0>();
         lds_barrier();
-        const lds_char* qt = ring + at;
+        const lds_char* qt = ring + (b & 1) * kStage;
         const lds_char* dt = qt + kBlock;
-        load();
+        load(ring + ((b + 1) & 1) * kStage);
         f32x16_t s = {}, g = {};
 #pragma unroll
         for (int st = 0; st < TL::kSteps; ++st) {
@@ -842,7 +987,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
           g = mma16(TL::row_frag(dt, 0, st), vf[st], g, T{});
         }
         const lds_char* st = qt + 2 * kBlock + 16 * (lane >> 5);
-        const bool whole = static_cast<unsigned>(bn - whole_lo) < static_cast<unsigned>(whole_n);
+        const bool every = whole(bn);
         const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -851,7 +996,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = 4 * q + x;
-            const bool yes = whole | seen(r);
+            const bool yes = every | seen(r);
             const float pr = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[x]));
             g[r] = yes ? pr * (g[r] - d4[x]) : 0.0f;
             s[r] = yes ? pr : 0.0f;
@@ -865,10 +1010,50 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, in
           dv[d] = mma_transposed<DP>(dt, 0, d, pc, dv[d]);
           dk[d] = mma_transposed<DP>(qt, 0, d, ds, dk[d]);
         }
-        at = next_slot(at);
         if (++bn == per_head) bn = 0;
       }
       wait_vmcnt<0>();
+    }
+  }
+  if (parts > 1) {
+    // this part's sums to the workspace; the last part to arrive adds them all
+    constexpr int kPieces = 2 * TL::kDT * 4;   // 16-byte pieces a lane
+    auto sums_of = [&](int p) {
+      return reinterpret_cast<f32x4_t*>(plan.sums + (static_cast<int64_t>(plan.first[slot] + p) * a.n_kv_heads + hk) * Shape::kSums) +
+             sw * kPieces * 64 + lane;
+    };
+    f32x4_t* mine = sums_of(part);
+#pragma unroll
+    for (int d = 0; d < TL::kDT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        mine[(d * 8 + g) * 64] = f32x4_t{dk[d][4 * g], dk[d][4 * g + 1], dk[d][4 * g + 2], dk[d][4 * g + 3]};
+        mine[(d * 8 + 4 + g) * 64] = f32x4_t{dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
+      }
+    __shared__ int arrived;
+    __threadfence();   // the sums are visible to the device before the count
+    __syncthreads();
+    if (threadIdx.x == 0)
+      arrived = __hip_atomic_fetch_add(&plan.done[plan.split[slot] * a.n_kv_heads + hk], 1, __ATOMIC_ACQ_REL,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != parts - 1) return;
+    __threadfence();
+#pragma unroll
+    for (int d = 0; d < TL::kDT; ++d) dk[d] = dv[d] = f32x16_t{};
+    for (int p = 0; p < parts; ++p) {
+      const f32x4_t* from_part = sums_of(p);
+#pragma unroll
+      for (int d = 0; d < TL::kDT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t x = from_part[(d * 8 + g) * 64], y = from_part[(d * 8 + 4 + g) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dk[d][4 * g + e] += x[e];
+            dv[d][4 * g + e] += y[e];
+          }
+        }
     }
   }
   bool bad = false;
@@ -924,28 +1109,60 @@ hipError_t launch_attn_fwd(const AttnView& a, int dtype, hipStream_t s, int* err
                                                               : fwd_launch<false>(a, dtype, s, err);
 }
 
-size_t attn_bwd_workspace_bytes(const AttnView& a, int) {
-  return 2 * align_up(static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float), 256);
+// The backward's workspace: the row statistics, the plan, and the sums of
+// split tiles.  A split tile has more than `chunk` blocks, so that all of them
+// together have at most 2 total / chunk <= 2 target parts, and no more than
+// two for every kMinChunk blocks.
+struct BwdSpace {
+  RowStats stats;
+  DkvPlan plan;
+  int max_parts;
+  size_t bytes;
+};
+static BwdSpace bwd_space(const AttnView& a, int dtype, void* ws) {
+  BwdSpace b{};
+  const int dp = a.head_dim <= 64 ? 64 : 128;
+  const int64_t n = slots(a.total_k, a.n_seqs);
+  b.plan.n_slots = n;
+  b.plan.target = (2 * device_cus() + a.n_kv_heads - 1) / a.n_kv_heads;   // two parts a CU
+  const int64_t blocks = (a.total_q / 32 + a.n_seqs) * a.group * n;       // more than there are
+  const int64_t most = 2 * (blocks / kMinChunk) + 2;
+  b.max_parts = static_cast<int>(most < 2 * b.plan.target ? most : 2 * b.plan.target);
+  Workspace w(ws, ~size_t(0));
+  const size_t rows = static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float);
+  const size_t ints = static_cast<size_t>(n) * sizeof(int32_t);
+  b.stats.lse2 = w.take<float>(rows);
+  b.stats.delta = w.take<float>(rows);
+  b.plan.head = w.take<int32_t>(sizeof(int32_t));
+  b.plan.blocks = w.take<int32_t>(ints);
+  b.plan.parts = w.take<int32_t>(ints);
+  b.plan.first = w.take<int32_t>(ints);
+  b.plan.split = w.take<int32_t>(ints);
+  b.plan.items = w.take<int32_t>(2 * (ints + b.max_parts * sizeof(int32_t)));
+  b.plan.done = w.take<int32_t>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sizeof(int32_t));
+  const size_t sums = static_cast<size_t>(kWaves) * 2 * 64 * 16 * (dp / 32) * sizeof(float);
+  b.plan.sums = w.take<float>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sums);
+  b.bytes = w.used;
+  return b;
 }
+size_t attn_bwd_workspace_bytes(const AttnView& a, int dtype) { return bwd_space(a, dtype, nullptr).bytes; }
 
 template <typename T, int DP, bool kWide>
-static hipError_t bwd_launch(const AttnView& a, void* ws, hipStream_t s, int* err) {
-  Workspace w(ws, attn_bwd_workspace_bytes(a, 0));
-  const size_t bytes = static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float);
-  RowStats stats;
-  stats.lse2 = w.take<float>(bytes);
-  stats.delta = w.take<float>(bytes);
-  const int64_t nq = slots(a.total_q, a.n_seqs), nk = slots(a.total_k, a.n_seqs);
-  hipError_t e = launch_lds<attn_dq_kernel<T, DP, kWide>, DqShape<T, DP>::kLds>(nq * a.n_heads, s, a, nq, stats, err);
+static hipError_t bwd_launch(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
+  const BwdSpace b = bwd_space(a, dtype, ws);
+  const int64_t nq = slots(a.total_q, a.n_seqs);
+  // one workgroup more than there are query tiles: it makes the plan
+  hipError_t e = launch_lds<attn_dq_kernel<T, DP, kWide>, DqShape<T, DP>::kLds>(nq * a.n_heads + 1, s, a, nq, b.stats, b.plan, err);
   if (e != hipSuccess) return e;
-  return launch_lds<attn_dkv_kernel<T, DP, kWide>, DkvShape<T, DP>::kLds>(nk * a.n_kv_heads, s, a, nk, stats, err);
+  return launch_lds<attn_dkv_kernel<T, DP, kWide>, DkvShape<T, DP>::kLds>((b.plan.n_slots + b.max_parts) * a.n_kv_heads, s, a,
+                                                                          b.stats, b.plan, err);
 }
 
 template <bool kWide>
 static hipError_t bwd_launch(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
   if (dtype == STAPLE_BF16)
-    return a.head_dim <= 64 ? bwd_launch<bf16_t, 64, kWide>(a, ws, s, err) : bwd_launch<bf16_t, 128, kWide>(a, ws, s, err);
-  return a.head_dim <= 64 ? bwd_launch<float, 64, kWide>(a, ws, s, err) : bwd_launch<float, 128, kWide>(a, ws, s, err);
+    return a.head_dim <= 64 ? bwd_launch<bf16_t, 64, kWide>(a, dtype, ws, s, err) : bwd_launch<bf16_t, 128, kWide>(a, dtype, ws, s, err);
+  return a.head_dim <= 64 ? bwd_launch<float, 64, kWide>(a, dtype, ws, s, err) : bwd_launch<float, 128, kWide>(a, dtype, ws, s, err);
 }
 
 hipError_t launch_attn_bwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {

@@ -83,23 +83,61 @@ template <> struct Column<float> {
   __device__ __forceinline__ void set(const f32x16_t& x) { v = x; }
 };
 
-// Transposed: the A operand of rows [row0 + 16 t, row0 + 16 t + 16) and head
-// elements [32 dt, 32 dt + 32), the rows in the order of a Column.
+// The lane's LDS addresses of a 32-row block's A operands by rows, one a step;
+// move() takes them to another place of the ring, `block` is a constant offset.
+template <typename T, int DP>
+struct RowReader {
+  using TL = Tile<T, DP>;
+  const lds_char* at[TL::kSteps];
+  __device__ __forceinline__ explicit RowReader(const lds_char* ring) {
+    const int lane = threadIdx.x & 63, row = lane & 31;
+#pragma unroll
+    for (int s = 0; s < TL::kSteps; ++s) at[s] = ring + row * TL::kRow + (((2 * s + (lane >> 5)) ^ TL::spread(row)) << 4);
+  }
+  __device__ __forceinline__ void move(int bytes) {
+#pragma unroll
+    for (int s = 0; s < TL::kSteps; ++s) at[s] += bytes;
+  }
+  __device__ __forceinline__ u32x4_t read(int s, int block) const {
+    return *reinterpret_cast<const lds_u32x4*>(at[s] + block);
+  }
+};
+// The same transposed: rows [16 t, 16 t + 16) and head elements [32 dt, 32 dt +
+// 32) of the block, the rows in the order of a Column.  16 lanes read 4 rows x
+// 16 elements and get 4 rows of one element each; 8 rows on, the spread
+// differs, 16 rows on it does not.
+template <int DP>
+struct ColumnReader {
+  using TL = Tile<bf16_t, DP>;
+  const lds_char* at[TL::kDT][2];
+  __device__ __forceinline__ explicit ColumnReader(const lds_char* ring) {
+    const int lane = threadIdx.x & 63, i16 = lane & 15;
+#pragma unroll
+    for (int dt = 0; dt < TL::kDT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = dt * 32 + (lane & 16) + 4 * (i16 & 3), row = 8 * e + 4 * (lane >> 5) + (i16 >> 2);
+        at[dt][e] = ring + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
+      }
+  }
+  __device__ __forceinline__ void move(int bytes) {
+#pragma unroll
+    for (int dt = 0; dt < TL::kDT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) at[dt][e] += bytes;
+  }
+  __device__ __forceinline__ u32x4_t read(int t, int dt, int block) const {
+    v4s_t part[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(at[dt][e] + block + 16 * t * TL::kRow));
+    const v8s_t a = {part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2], part[1][3]};
+    return __builtin_bit_cast(u32x4_t, a);
+  }
+};
 template <int DP>
 __device__ __forceinline__ u32x4_t column_frag(const lds_char* tile, int row0, int t, int dt) {
-  using TL = Tile<bf16_t, DP>;
-  const int lane = threadIdx.x & 63, i16 = lane & 15;
-  // 16 lanes read 4 rows x 16 elements and get 4 rows of one element each
-  const int c = dt * 32 + (lane & 16) + 4 * (i16 & 3);
-  v4s_t part[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int row = row0 + 16 * t + 8 * e + 4 * (lane >> 5) + (i16 >> 2);
-    const lds_char* p = tile + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
-    part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p);
-  }
-  const v8s_t a = {part[0][0], part[0][1], part[0][2], part[0][3], part[1][0], part[1][1], part[1][2], part[1][3]};
-  return __builtin_bit_cast(u32x4_t, a);
+  return ColumnReader<DP>(tile + row0 * Tile<bf16_t, DP>::kRow).read(t, dt, 0);
 }
 // acc += (rows [row0, row0 + 32) of the tile, elements [32 dt, 32 dt + 32))^T x column.
 template <int DP>
@@ -179,8 +217,11 @@ struct TileLoader {
     lds_char* const to = lds + lds0;
     if constexpr (!kWide) {
       const uint32_t first = static_cast<uint32_t>(row0) * static_cast<uint32_t>(row_bytes);
+      u32x4_t scalar;   // wherever the compiler keeps it, the load takes it from scalar registers
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) dma16(buffer, offset[i] + first, static_cast<lds_void*>(to + i * NW * 1024));
+      for (int i = 0; i < 4; ++i) scalar[i] = __builtin_amdgcn_readfirstlane(buffer[i]);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) dma16(scalar, offset[i] + first, static_cast<lds_void*>(to + i * NW * 1024));
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
