@@ -376,22 +376,38 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(KvView kv, 
   }
 }
 
-// One wave a (sequence, head): the splits' partial results in split order.
+// One workgroup a (sequence, head): every wave joins the splits w, w + 4, ...
+// in that order, and then the waves' sums are added in wave order.
 template <typename T, int DP>
 __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_join_kernel(DecodeView a, int splits, DecPartials part) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kDecWaves + (threadIdx.x >> 6);
-  if (at >= a.n_seqs * a.n_heads) return;
-  const int lane = threadIdx.x & 63;
-  const float* stat = part.stat + at * splits * 2;
-  float t = -INFINITY;
-  for (int s = 0; s < splits; ++s) t = fmaxf(t, stat[2 * s]);
   constexpr int kPer = DP / 64;
+  __shared__ float joined[kDecWaves][DP], totals[kDecWaves];
+  const int64_t at = blockIdx.x;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const float* stat = part.stat + at * splits * 2;
+  // at most 128 splits: two a lane
+  float t = fmaxf(lane < splits ? stat[2 * lane] : -INFINITY, lane + 64 < splits ? stat[2 * (lane + 64)] : -INFINITY);
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) t = fmaxf(t, __shfl_xor(t, d));
   float v[kPer] = {}, total = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    const float keep = stat[2 * s] == -INFINITY && stat[2 * s + 1] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(stat[2 * s] - t);
-    total += stat[2 * s + 1] * keep;
+#pragma unroll 4
+  for (int s = w; s < splits; s += kDecWaves) {
+    const float top = stat[2 * s], sum = stat[2 * s + 1];
+    const float keep = top == -INFINITY && sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(top - t);
+    total += sum * keep;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) v[e] += part.o[(at * splits + s) * DP + kPer * lane + e] * keep;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) joined[w][kPer * lane + e] = v[e];
+  if (lane == 0) totals[w] = total;
+  __syncthreads();
+  if (w != 0) return;
+#pragma unroll
+  for (int u = 1; u < kDecWaves; ++u) {
+    total += totals[u];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) v[e] += joined[u][kPer * lane + e];
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t i = at / a.n_heads, h = at % a.n_heads;
@@ -401,6 +417,8 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_join_kernel(Decode
     if (kPer * lane + e < a.head_dim) Elem<T>::store(p, kPer * lane + e, v[e] * inv);
   if (a.lse && lane == 0) a.lse[at] = (t + __builtin_amdgcn_logf(total)) * kLn2;
 }
+
+constexpr int kDecMaxSplits = 128;   // what a wave's lanes hold two each of
 
 // How the cache is split: `chunk` blocks a workgroup, `splits` of them at most.
 struct DecPlan {
@@ -419,7 +437,7 @@ static DecPlan plan(const KvView& kv, const DecodeView& a, int dtype) {
   // at least two blocks a wave in a split
   int64_t splits = blocks / (2 * kDecWaves);
   if (splits > want) splits = want;
-  if (splits > 128) splits = 128;
+  if (splits > kDecMaxSplits) splits = kDecMaxSplits;
   if (splits < 1) splits = 1;
   const int64_t chunk = (blocks + splits - 1) / splits;
   p.chunk = static_cast<int>((chunk + kDecWaves - 1) / kDecWaves * kDecWaves);
@@ -450,8 +468,7 @@ static hipError_t decode_launch(const KvView& kv, const DecodeView& a, int dtype
   attn_decode_kernel<T, DP><<<static_cast<unsigned>(wgs), 64 * kDecWaves, 0, s>>>(kv, a, p.chunk, p.splits, p.head_tiles, part, err);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits <= 1) return e;
-  const int64_t rows = a.n_seqs * a.n_heads;
-  attn_decode_join_kernel<T, DP><<<static_cast<unsigned>((rows + kDecWaves - 1) / kDecWaves), 64 * kDecWaves, 0, s>>>(a, p.splits, part);
+  attn_decode_join_kernel<T, DP><<<static_cast<unsigned>(a.n_seqs * a.n_heads), 64 * kDecWaves, 0, s>>>(a, p.splits, part);
   return hipGetLastError();
 }
 

@@ -249,10 +249,11 @@ __device__ __forceinline__ void copy_page(const KvView& kv, int64_t layer, int s
   }
 }
 
+// blockIdx.z: part of a page, so that a few small copies still fill the GPU.
 __global__ __launch_bounds__(256) void kv_copy_list_kernel(KvView kv, const KvCopy* copies) {
   const KvCopy c = copies[blockIdx.x];
   if (c.src < 0) return;
-  copy_page(kv, blockIdx.y >> 1, blockIdx.y & 1, c.src, c.dst, c.slots, 0, 1);
+  copy_page(kv, blockIdx.y >> 1, blockIdx.y & 1, c.src, c.dst, c.slots, blockIdx.z, gridDim.z);
 }
 
 __global__ __launch_bounds__(256) void kv_copy_pages_kernel(KvView kv, const int32_t* src,
@@ -433,8 +434,11 @@ hipError_t launch_kv_extend(const KvView& kv, const int32_t* seqs, const int32_t
                                               copies, err);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  kv_copy_list_kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>(2 * kv.n_layers)), 256,
-                        0, s>>>(kv, copies);
+  // a part has at most one round of loads: 4 x 256 x 16 bytes
+  const int64_t page_bytes = static_cast<int64_t>(kv.kv_heads) * kv.page * kv.row_bytes;
+  const int64_t parts = (page_bytes + 16383) / 16384;
+  kv_copy_list_kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>(2 * kv.n_layers),
+                             static_cast<unsigned>(parts < 64 ? parts : 64)), 256, 0, s>>>(kv, copies);
   return hipGetLastError();
 }
 
