@@ -274,8 +274,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   u32x4_t qf[TL::kSteps];
   const float c = load_queries<T, DP>(a, w, qf);
   TileLoader<T, DP, 32, kWaves, kWide> kl, vl;
-  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
-  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim, wave_id());
+  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim, wave_id());
   f32x16_t o[TL::kDT] = {};
   ColumnSoftmax sm;
   kl.load(keys.first(0), lds);
@@ -339,8 +339,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
   ColumnSoftmax sm;
   if (keys.n > 0) {
     TileLoader<T, DP, 32, kWaves, kWide> kl, vl;
-    kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
-    vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+    kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim, wave_id());
+    vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim, wave_id());
 #pragma unroll
     for (int b = 0; b < 4; ++b) kl.load(keys.first(b), kring + b * kBlock);
 #pragma unroll
@@ -635,8 +635,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
   const KeyBlocks keys = w.blocks(a);
   const int half = (threadIdx.x & 63) >> 5;
   Loader kl, vl;
-  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim);
-  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim);
+  kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim, wave_id());
+  vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim, wave_id());
   // ring places of the blocks to read, and to load next
   int kr = 0, vr = 0, kn = kAhead * kBlock, vn = kAhead * kBlock;
   auto bump = [](int& at, int slots) { at = at + kBlock == slots * kBlock ? 0 : at + kBlock; };
@@ -762,124 +762,311 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
 }
 
 // dk and dv: one key a column; the queries that see them (of every head of the
-// group) go through LDS.  The two results take 2 DP registers a lane, so one
-// workgroup has a CU to itself and in bf16 the wave runs three blocks at a
-// time by itself, as in the forward: between the elements of block b stand the
-// score products of block b + 1 and the gradient products of block b - 1, and
-// the workgroup meets every second block.
+// group) go through LDS.  An item is a key tile or a part of one.
+struct DkvItem : Segment {
+  int slot, part, parts, hk;
+  int64_t h0;              // the head of the item's first block
+  int n, ln;               // its blocks, and the first one's number within its head
+  int b_lo, per_head;      // see QueryBlocks
+  int wkey, key;           // the wave's first key; the lane's
+  bool in;
+  int whole_lo, whole_n;   // of a head's blocks, those whose every query sees all of the wave's keys
+  int seen_lo, seen_hi;    // and those of which some query sees some of them: [seen_lo, seen_hi)
+  // False where there is no such item; `group`: which 32 keys of the tile the wave has.
+  __device__ __forceinline__ bool find(const AttnView& a, const DkvPlan& plan, int group_of_wave, int* err) {
+    const int item = uniform(static_cast<int>(blockIdx.x) / a.n_kv_heads);
+    if (item >= plan.head[0]) return false;
+    hk = static_cast<int>(blockIdx.x) - item * a.n_kv_heads;
+    slot = uniform(plan.items[2 * item]);
+    part = uniform(plan.items[2 * item + 1]);
+    parts = uniform(plan.parts[slot]);
+    if (!Segment::find(a, a.cu_k, slot, err)) return false;
+    wkey = first + 32 * group_of_wave;
+    key = wkey + (threadIdx.x & 31);
+    in = key < nk;
+    const QueryBlocks blocks(a, *this);
+    b_lo = blocks.b_lo;
+    per_head = blocks.per_head;
+    const int all = per_head * a.group, chunk = uniform((all + parts - 1) / parts);
+    const int from_block = min(part * chunk, all);
+    n = min(chunk, all - from_block);
+    const int skip = uniform(per_head > 0 ? from_block / per_head : 0);
+    h0 = static_cast<int64_t>(hk) * a.group + skip;
+    ln = from_block - skip * per_head;
+    const bool sink = wkey < a.sinks, all_sinks = wkey + 31 < a.sinks;
+    const int from = (max(wkey + 31 - past, 0) + 31) / 32;
+    const int to = (a.window > 0 && !all_sinks ? min(max(wkey - past + a.window, 0), nq) : nq) / 32;
+    whole_lo = from - b_lo;
+    whole_n = wkey + 31 < nk ? max(to - from, 0) : 0;
+    const int end = a.window > 0 && !sink ? min(max(wkey + 31 - past + a.window, 0), nq) : nq;
+    seen_lo = max(wkey - past, 0) / 32 - b_lo;
+    seen_hi = wkey < nk ? (end + 31) / 32 - b_lo : 0;
+    return true;
+  }
+  __device__ __forceinline__ bool whole(int b) const {
+    return static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
+  }
+};
+
+// A split tile's part: its fp32 sums to the workspace, as they lie in the
+// registers of the workgroup's kThreads threads (x: kX results a thread); true
+// in the part that arrives last, with all parts' sums added in part order.
+template <int kThreads, int kX>
+__device__ __forceinline__ bool join_parts(const DkvPlan& plan, const DkvItem& w, int n_kv_heads, f32x16_t* x) {
+  constexpr int kFloats = kThreads * 16 * kX;
+  auto sums_of = [&](int p) {
+    return reinterpret_cast<f32x4_t*>(plan.sums + (static_cast<int64_t>(plan.first[w.slot] + p) * n_kv_heads + w.hk) * kFloats) +
+           threadIdx.x;
+  };
+  f32x4_t* mine = sums_of(w.part);
+#pragma unroll
+  for (int d = 0; d < kX; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      mine[(d * 4 + g) * kThreads] = f32x4_t{x[d][4 * g], x[d][4 * g + 1], x[d][4 * g + 2], x[d][4 * g + 3]};
+  __shared__ int arrived;
+  __threadfence();   // the sums are visible to the device before the count
+  __syncthreads();
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(&plan.done[plan.split[w.slot] * n_kv_heads + w.hk], 1, __ATOMIC_ACQ_REL,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != w.parts - 1) return false;
+  __threadfence();
+#pragma unroll
+  for (int d = 0; d < kX; ++d) x[d] = f32x16_t{};
+  for (int p = 0; p < w.parts; ++p) {
+    const f32x4_t* from = sums_of(p);
+#pragma unroll
+    for (int d = 0; d < kX; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t v = from[(d * 4 + g) * kThreads];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[d][4 * g + e] += v[e];
+      }
+  }
+  return true;
+}
+
+// Keys whose gradients came out not finite: a query that does not see the key
+// may have brought it (zero times its rows), so they are done again query by
+// query; see the forward.
+template <typename T>
+__device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& stats, const DkvItem& w, bool bad) {
+  uint64_t again = __ballot(bad && w.in);
+  again = (again | (again >> 32)) & 0xffffffffull;
+  while (again) {
+    const int i = __builtin_ctzll(again);
+    again &= again - 1;
+    attn_dkv_row<T>(a, stats.delta, w.wkey + i, w.hk, w);
+  }
+}
+
+// A ring slot holds a block's Q and dO, then lse2 and delta (256 bytes each,
+// half of it used).
 template <typename T, int DP>
 struct DkvShape {
   static constexpr int kBlock = 32 * Tile<T, DP>::kRow;
-  static constexpr int kStage = 2 * kBlock + 512;   // Q, dO, lse2, delta (256 bytes each, half of it used)
-  static constexpr int kSlots = sizeof(T) == 2 ? 6 : 2;
-  static constexpr int kLds = kSlots * kStage;
-  // fp32 sums of one part: per wave dk and dv, as they lie in registers
-  static constexpr int kSums = kWaves * 2 * 64 * 16 * Tile<T, DP>::kDT;
+  static constexpr int kStage = 2 * kBlock + 512;
 };
-// Keeps an operand of the products in the accumulation registers, so that the
-// vector registers hold what vector instructions work on.
-__device__ __forceinline__ void park(u32x4_t& v) { asm volatile("" : "+a"(v)); }
 
-template <typename T, int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+// fp32: one block after the other.
+template <int DP, bool kWide>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+  using T = float;
   using TL = Tile<T, DP>;
-  using Shape = DkvShape<T, DP>;
-  using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
-  constexpr int kBlock = Shape::kBlock, kStage = Shape::kStage;
+  constexpr int kBlock = DkvShape<T, DP>::kBlock, kStage = DkvShape<T, DP>::kStage;
   extern __shared__ __align__(1024) char smem[];
   lds_char* const ring = (lds_char*)smem;
-  const int item = uniform(static_cast<int>(blockIdx.x) / a.n_kv_heads);
-  const int hk = static_cast<int>(blockIdx.x) - item * a.n_kv_heads;
-  if (item >= plan.head[0]) return;
-  const int slot = uniform(plan.items[2 * item]), part = uniform(plan.items[2 * item + 1]);
-  const int parts = uniform(plan.parts[slot]);
-  Segment w;
-  if (!w.find(a, a.cu_k, slot, err)) return;
+  DkvItem w;
+  if (!w.find(a, plan, wave_id(), err)) return;
   const int lane = threadIdx.x & 63;
-  const int wkey = w.first + 32 * wave_id();   // the wave's first key
-  const int key = wkey + (lane & 31);
-  const bool in = key < w.nk;
-
-  const QueryBlocks blocks(a, w);
-  const int b_lo = blocks.b_lo, per_head = blocks.per_head;
-  // this part's blocks: n of them, from block ln of head h0
-  const int all = per_head * a.group, chunk = uniform((all + parts - 1) / parts);
-  const int from_block = min(part * chunk, all), n = min(chunk, all - from_block);
-  const int skip = uniform(per_head > 0 ? from_block / per_head : 0);
-  const int64_t h0 = static_cast<int64_t>(hk) * a.group + skip;
-  int ln = from_block - skip * per_head, bn = ln;   // to load next; at hand
-  // of a head's blocks, those whose every query sees all of the wave's keys
-  const int from = (max(wkey + 31 - w.past, 0) + 31) / 32;
-  const int to = (a.window > 0 && wkey + 31 >= a.sinks ? min(max(wkey - w.past + a.window, 0), w.nq) : w.nq) / 32;
-  const int whole_lo = from - b_lo, whole_n = wkey + 31 < w.nk ? max(to - from, 0) : 0;
-  auto whole = [&](int b) { return static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n); };
-
-  Loader ql, dl;
-  ql.init(a.q, w.q0, w.nq, h0, a.head_dim);
-  dl.init(a.d_o, w.q0, w.nq, h0, a.head_dim);
+  TileLoader<T, DP, 32, kWaves, kWide> ql, dl;
+  ql.init(a.q, w.q0, w.nq, w.h0, a.head_dim, wave_id());
+  dl.init(a.d_o, w.q0, w.nq, w.h0, a.head_dim, wave_id());
   const int sw = wave_id();
-  const float* stat = (sw & 1 ? stats.delta : stats.lse2) + h0 * a.total_q + w.q0;
-  int left = n;
-  auto load = [&](lds_char* to_slot) {
-    // past the last block: zeros
-    const int i0 = left > 0 ? (b_lo + ln) * 32 : w.nq;
-    ql.load(i0, to_slot);
-    dl.load(i0, to_slot + kBlock);
-    // two waves load either statistic, the same values to the same place
-    dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(to_slot + 2 * kBlock + 256 * (sw & 1)));
+  const float* stat = (sw & 1 ? stats.delta : stats.lse2) + w.h0 * a.total_q + w.q0;
+  int left = w.n, ln = w.ln, bn = w.ln;   // to load; at hand
+  auto load = [&](lds_char* slot) {
+    const int i0 = left > 0 ? (w.b_lo + ln) * 32 : w.nq;   // past the last block: zeros
+    ql.load(i0, slot);
+    dl.load(i0, slot + kBlock);
+    if (sw < 2) dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(slot + 2 * kBlock + 256 * sw));
     --left;
-    if (++ln == per_head) {
+    if (++ln == w.per_head) {
       ln = 0;
       ql.next_head(a.q);
       dl.next_head(a.d_o);
       if (left > 0) stat += a.total_q;
     }
   };
-  f32x16_t dk[TL::kDT] = {}, dv[TL::kDT] = {};
+  f32x16_t x[2 * TL::kDT] = {};   // dk, then dv
   const float c = score_factor(a);
-  if (n > 0) {
+  if (w.n > 0) {
     u32x4_t kf[TL::kSteps], vf[TL::kSteps];
 #pragma unroll
     for (int s = 0; s < TL::kSteps; ++s) {
-      kf[s] = signed_frag<T>(a, load_frag<T>(a.k, w.k0 + key, hk, a.head_dim, s, in));
-      vf[s] = load_frag<T>(a.v, w.k0 + key, hk, a.head_dim, s, in);
-      if constexpr (sizeof(T) == 2 && DP == 128) {
-        park(kf[s]);
-        park(vf[s]);
-      }
+      kf[s] = signed_frag<T>(a, load_frag<T>(a.k, w.k0 + w.key, w.hk, a.head_dim, s, w.in));
+      vf[s] = load_frag<T>(a.v, w.k0 + w.key, w.hk, a.head_dim, s, w.in);
     }
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) load(ring + b * kStage);
+    load(ring);
+    for (int b = 0; b < w.n; ++b) {
       wait_vmcnt<0>();
       lds_barrier();
-      f32x16_t s0 = {}, s1, g0 = {}, g1;
-      Column<T> p0, p1, e0, e1;   // probabilities and score gradients
-      RowReader<T, DP> rows(ring);
-      ColumnReader<DP> cols(ring);
-      const lds_char* const stat0 = ring + 2 * kBlock + 16 * (lane >> 5);
+      const lds_char* qt = ring + (b & 1) * kStage;
+      const lds_char* dt = qt + kBlock;
+      load(ring + ((b + 1) & 1) * kStage);
+      f32x16_t s = {}, g = {};
 #pragma unroll
       for (int st = 0; st < TL::kSteps; ++st) {
-        s0 = mma16(rows.read(st, 0), kf[st], s0, T{});
-        g0 = mma16(rows.read(st, kBlock), vf[st], g0, T{});
+        s = mma16(TL::row_frag(qt, 0, st), kf[st], s, T{});
+        g = mma16(TL::row_frag(dt, 0, st), vf[st], g, T{});
       }
-      // Step b: elements of block b (products s and g, statistics at st) into
-      // p and e, score products of block b + 1 into sn and gn, gradients of
-      // block b - 1 from pp and ep; `place` bytes past the readers' places.
-      auto step = [&](auto is_first, auto place, const lds_char* st, f32x16_t& s, f32x16_t& g, f32x16_t& sn, f32x16_t& gn,
-                      Column<T>& pp, Column<T>& ep, Column<T>& p, Column<T>& e) {
-        constexpr bool kFirst = decltype(is_first)::value;
-        constexpr int kAt = decltype(place)::value;
+      const lds_char* st = qt + 2 * kBlock + 16 * (lane >> 5);
+      const bool every = w.whole(bn);
+      const SeenBy seen(a, w, w.key, w.in, (w.b_lo + bn) * 32);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t l4 = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
+        const f32x4_t d4 = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * q + e;
+          const bool yes = every | seen(r);
+          const float pr = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[e]));
+          g[r] = yes ? pr * (g[r] - d4[e]) : 0.0f;
+          s[r] = yes ? pr : 0.0f;
+        }
+      }
+      Column<T> pc, ds;
+      pc.set(s);
+      ds.set(g);
+#pragma unroll
+      for (int d = 0; d < TL::kDT; ++d) {
+        x[d] = mma_transposed<DP>(qt, 0, d, ds, x[d]);
+        x[TL::kDT + d] = mma_transposed<DP>(dt, 0, d, pc, x[TL::kDT + d]);
+      }
+      if (++bn == w.per_head) bn = 0;
+    }
+    wait_vmcnt<0>();   // no load into LDS outlives the workgroup
+  }
+  if (w.parts > 1 && !join_parts<64 * kWaves, 2 * TL::kDT>(plan, w, a.n_kv_heads, x)) return;
+  bool bad = false;
+#pragma unroll
+  for (int d = 0; d < TL::kDT; ++d) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) bad |= not_finite(x[d][r]) || not_finite(x[TL::kDT + d][r]);
+    store_column<T>(a.dk, w.k0 + w.key, w.hk, a.head_dim, d, x[d], a.scale, w.in);
+    store_column<T>(a.dv, w.k0 + w.key, w.hk, a.head_dim, d, x[TL::kDT + d], 1.0f, w.in);
+  }
+  redo_keys<T>(a, stats, w, bad);
+}
+
+// bf16.  dk and dv of 32 keys take 2 DP registers a lane, too many beside the
+// operands for two waves a SIMD.  So two waves share 32 keys: of a stage of
+// two query blocks each forms the probabilities and score gradients of one,
+// they trade them through LDS, and each adds both to its half of head_dim.
+// Between the elements of a stage stand the gradient products of the stage
+// before.
+constexpr int kDkvWaves = 8;
+template <int DP>
+struct DkvPair {
+  static constexpr int kStage = DkvShape<bf16_t, DP>::kStage;
+  static constexpr int kTrade = 4 * 2 * 4 * 1024;              // [keys / 32][block][P, P, dS, dS][lane]
+  static constexpr int kLds = 6 * kStage + kTrade;             // three pairs of slots: before, at hand, loading
+};
+template <int DP, bool kWide>
+__global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+  using T = bf16_t;
+  using TL = Tile<T, DP>;
+  using Shape = DkvPair<DP>;
+  constexpr int kBlock = DkvShape<T, DP>::kBlock, kStage = Shape::kStage, kPair = 2 * kStage;
+  constexpr int kHalf = TL::kDT / 2;   // 32-element blocks of head_dim a wave
+  extern __shared__ __align__(1024) char smem[];
+  lds_char* const ring = (lds_char*)smem;
+  const int keys_of = wave_id() & 3, side = wave_id() >> 2;
+  DkvItem w;
+  if (!w.find(a, plan, keys_of, err)) return;
+  const int lane = threadIdx.x & 63;
+  lds_char* const trade = ring + 6 * kStage + keys_of * (2 * 4 * 1024) + lane * 16;
+
+  // waves 0-3 load Q and lse2, waves 4-7 dO and delta
+  TileLoader<T, DP, 32, 4, kWide> loader;
+  const HeadsView& source = side ? a.d_o : a.q;
+  loader.init(source, w.q0, w.nq, w.h0, a.head_dim, keys_of);
+  const float* stat = (side ? stats.delta : stats.lse2) + w.h0 * a.total_q + w.q0;
+  int left = w.n, ln = w.ln;
+  auto load = [&](lds_char* slot) {
+    const int i0 = left > 0 ? (w.b_lo + ln) * 32 : w.nq;   // past the last block: zeros
+    loader.load(i0, slot + side * kBlock);
+    if (keys_of == 0) dma4(stat + min(i0 + lane, w.nq - 1), static_cast<lds_void*>(slot + 2 * kBlock + 256 * side));
+    --left;
+    if (++ln == w.per_head) {
+      ln = 0;
+      loader.next_head(source);
+      if (left > 0) stat += a.total_q;
+    }
+  };
+  f32x16_t x[2 * kHalf] = {};   // dk, then dv
+  const float c = score_factor(a);
+  if (w.n > 0) {
+    load(ring);
+    load(ring + kStage);
+    u32x4_t kf[TL::kSteps], vf[TL::kSteps];
+#pragma unroll
+    for (int s = 0; s < TL::kSteps; ++s) {
+      kf[s] = signed_frag<T>(a, load_frag<T>(a.k, w.k0 + w.key, w.hk, a.head_dim, s, w.in));
+      vf[s] = load_frag<T>(a.v, w.k0 + w.key, w.hk, a.head_dim, s, w.in);
+    }
+    RowReader<T, DP> rows(ring + side * kStage);                   // this wave's block of the stage
+    ColumnReader<DP, kHalf> cols(ring, side * kHalf);              // its half of head_dim, of the stage before
+    const lds_char* stat_at = ring + side * kStage + 2 * kBlock + 16 * (lane >> 5);
+    int bn = w.ln + side;   // the wave's block, within its head
+    while (bn >= w.per_head) bn -= w.per_head;
+
+    // product m of the stage before: block, result, rows and elements
+    constexpr int kProducts = 2 * 2 * 2 * kHalf;   // blocks x (dk, dv) x row halves x element blocks
+    struct Product {
+      int block, which, t, d;
+    };
+    auto product = [](int m) { return Product{m / (4 * kHalf), m / (2 * kHalf) & 1, m & 1, (m >> 1) % kHalf}; };
+    auto read_a = [&](int m) {
+      const Product q = product(m);
+      return cols.read(q.t, q.d, q.block * kStage + q.which * kBlock);
+    };
+    auto read_b = [&](int m) {   // dk takes the score gradients, dv the probabilities
+      const Product q = product(m);
+      return *reinterpret_cast<const lds_u32x4*>(trade + q.block * 4096 + ((q.which ? 0 : 2) + q.t) * 1024);
+    };
+
+    // pair_seen: whether the blocks of the stage before hold anything for these keys
+    auto stage = [&](auto is_first, int j, bool pair_seen) {
+      constexpr bool kFirst = decltype(is_first)::value;
+      wait_vmcnt<0>();   // this stage's blocks
+      lds_barrier();     // and the trade of the stage before
+      lds_char* const next = ring + (j + 1) % 3 * kPair;
+      load(next);
+      load(next + kStage);
+      Column<T> p, e;
+      const bool mine = 2 * j + side < w.n && bn >= w.seen_lo && bn < w.seen_hi;
+      if (mine || pair_seen) {
+        f32x16_t s = {}, g = {};
+#pragma unroll
+        for (int st = 0; st < TL::kSteps; ++st) {
+          s = mma16(rows.read(st, 0), kf[st], s, T{});
+          g = mma16(rows.read(st, kBlock), vf[st], g, T{});
+        }
         f32x4_t l4[4], d4[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          l4[q] = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
-          d4[q] = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
+          l4[q] = *reinterpret_cast<const lds_f32x4*>(stat_at + 32 * q);
+          d4[q] = *reinterpret_cast<const lds_f32x4*>(stat_at + 256 + 32 * q);
         }
-        if (!whole(bn)) {
+        if (!(mine && w.whole(bn))) {
           // hidden pairs: probability and gradient zero, whatever the products
           // and the query's statistics are
-          const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
+          const SeenBy seen(a, w, w.key, mine && w.in, (w.b_lo + bn) * 32);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const bool yes = seen(r);
@@ -891,199 +1078,110 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnView a, Ro
         }
         float pe = 0.0f, ee = 0.0f;
         auto element = [&](int r) {
-          const float x = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[r >> 2][r & 3]));
-          const float y = x * (g[r] - d4[r >> 2][r & 3]);
+          const float pr = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[r >> 2][r & 3]));
+          const float ds = pr * (g[r] - d4[r >> 2][r & 3]);
           if (r & 1) {
-            uint32_t px = pack_bf16x2(pe, x), py = pack_bf16x2(ee, y);
+            uint32_t px = pack_bf16x2(pe, pr), ex = pack_bf16x2(ee, ds);
             pin(px);
-            pin(py);
+            pin(ex);
             p.v[r >> 3][(r >> 1) & 3] = px;
-            e.v[r >> 3][(r >> 1) & 3] = py;
+            e.v[r >> 3][(r >> 1) & 3] = ex;
           }
-          pe = x;
-          ee = y;
+          pe = pr;
+          ee = ds;
         };
-        constexpr int kQuads = TL::kSteps;   // one MFMA of each of the four products
-        static_assert(kQuads == 2 * TL::kDT, "as many of either kind");
-        u32x4_t qa[2], da[2], qt[2], dt[2];
+        constexpr int kAhead = 2;   // operands in flight
+        u32x4_t af[kAhead], bf[kAhead];
+        if constexpr (!kFirst) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          qa[i] = rows.read(i, kAt);
-          da[i] = rows.read(i, kAt + kBlock);
-          if constexpr (!kFirst) {
-            dt[i] = cols.read(i & 1, i >> 1, kAt + kBlock);
-            qt[i] = cols.read(i & 1, i >> 1, kAt);
+          for (int m = 0; m < kAhead; ++m) {
+            af[m] = read_a(m);
+            bf[m] = read_b(m);
           }
         }
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const int x = i & 1;
-          __builtin_amdgcn_sched_barrier(0);
-          sn = mma16(qa[x], kf[i], i == 0 ? f32x16_t{} : sn, T{});
-          if (i + 2 < kQuads) qa[x] = rows.read(i + 2, kAt);
-#pragma unroll
-          for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + r);
+        for (int m = 0; m < kProducts; ++m) {
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (!kFirst) {
-            dv[i >> 1] = mma16(dt[x], pp.v[x], dv[i >> 1], T{});
-            if (i + 2 < kQuads) dt[x] = cols.read(x, (i + 2) >> 1, kAt + kBlock);
+            const Product q = product(m);
+            x[q.which * kHalf + q.d] = mma16(af[m % kAhead], bf[m % kAhead], x[q.which * kHalf + q.d], T{});
+            if (m + kAhead < kProducts) {
+              af[m % kAhead] = read_a(m + kAhead);
+              bf[m % kAhead] = read_b(m + kAhead);
+            }
           }
-          __builtin_amdgcn_sched_barrier(0);
-          gn = mma16(da[x], vf[i], i == 0 ? f32x16_t{} : gn, T{});
-          if (i + 2 < kQuads) da[x] = rows.read(i + 2, kAt + kBlock);
 #pragma unroll
-          for (int r = 0; r < 8 / kQuads; ++r) element(i * (16 / kQuads) + 8 / kQuads + r);
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (!kFirst) {
-            dk[i >> 1] = mma16(qt[x], ep.v[x], dk[i >> 1], T{});
-            if (i + 2 < kQuads) qt[x] = cols.read(x, (i + 2) >> 1, kAt);
-          }
+          for (int r = 0; r < 16 / kProducts; ++r) element(m * (16 / kProducts) + r);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (++bn == per_head) bn = 0;
-      };
-      using Low = std::integral_constant<int, 0>;
-      using High = std::integral_constant<int, kStage>;
-      // as in the forward, an odd number of steps, one of them over zeros; a
-      // stage's blocks b - 1 and b lie in one pair of slots, b + 1 and b + 2 in
-      // the next, and the pair after that is loaded
-      step(std::true_type{}, High{}, stat0, s0, g0, s1, g1, p1, e1, p0, e0);
-      auto next_pair = [](int at) { return at + 2 * kStage == Shape::kLds ? 0 : at + 2 * kStage; };
-      int here = 0;
-      rows.move(2 * kStage);
-      for (int b = 1; b < (n | 1); b += 2) {
-        const int ahead = next_pair(here), after = next_pair(ahead);
-        wait_vmcnt<0>();   // the last stage's loads
-        lds_barrier();
-        load(ring + after);
-        load(ring + after + kStage);
-        step(std::false_type{}, Low{}, stat0 + here + kStage, s1, g1, s0, g0, p0, e0, p1, e1);
-        step(std::false_type{}, High{}, stat0 + ahead, s0, g0, s1, g1, p1, e1, p0, e0);
-        rows.move(after - ahead);
-        cols.move(ahead - here);
-        here = ahead;
+      } else {
+        p.v[0] = p.v[1] = e.v[0] = e.v[1] = u32x4_t{0, 0, 0, 0};
       }
-      if ((n & 1) == 0) p0.v[0] = p0.v[1] = e0.v[0] = e0.v[1] = u32x4_t{0, 0, 0, 0};   // the step over zeros
-#pragma unroll
-      for (int d = 0; d < TL::kDT; ++d)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          dv[d] = mma16(cols.read(x, d, kBlock), p0.v[x], dv[d], T{});
-          dk[d] = mma16(cols.read(x, d, 0), e0.v[x], dk[d], T{});
-        }
-      wait_vmcnt<0>();   // no load into LDS outlives the workgroup
-    } else {
-      load(ring);
-      for (int b = 0; b < n; ++b) {
-        wait_vmcnt<0>();
-        lds_barrier();
-        const lds_char* qt = ring + (b & 1) * kStage;
-        const lds_char* dt = qt + kBlock;
-        load(ring + ((b + 1) & 1) * kStage);
-        f32x16_t s = {}, g = {};
-#pragma unroll
-        for (int st = 0; st < TL::kSteps; ++st) {
-          s = mma16(TL::row_frag(qt, 0, st), kf[st], s, T{});
-          g = mma16(TL::row_frag(dt, 0, st), vf[st], g, T{});
-        }
-        const lds_char* st = qt + 2 * kBlock + 16 * (lane >> 5);
-        const bool every = whole(bn);
-        const SeenBy seen(a, w, key, in, (b_lo + bn) * 32);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4_t l4 = *reinterpret_cast<const lds_f32x4*>(st + 32 * q);
-          const f32x4_t d4 = *reinterpret_cast<const lds_f32x4*>(st + 256 + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = 4 * q + x;
-            const bool yes = every | seen(r);
-            const float pr = __builtin_amdgcn_exp2f(fmaf(s[r], c, -l4[x]));
-            g[r] = yes ? pr * (g[r] - d4[x]) : 0.0f;
-            s[r] = yes ? pr : 0.0f;
-          }
-        }
-        Column<T> pc, ds;
-        pc.set(s);
-        ds.set(g);
-#pragma unroll
-        for (int d = 0; d < TL::kDT; ++d) {
-          dv[d] = mma_transposed<DP>(dt, 0, d, pc, dv[d]);
-          dk[d] = mma_transposed<DP>(qt, 0, d, ds, dk[d]);
-        }
-        if (++bn == per_head) bn = 0;
-      }
-      wait_vmcnt<0>();
-    }
-  }
-  if (parts > 1) {
-    // this part's sums to the workspace; the last part to arrive adds them all
-    constexpr int kPieces = 2 * TL::kDT * 4;   // 16-byte pieces a lane
-    auto sums_of = [&](int p) {
-      return reinterpret_cast<f32x4_t*>(plan.sums + (static_cast<int64_t>(plan.first[slot] + p) * a.n_kv_heads + hk) * Shape::kSums) +
-             sw * kPieces * 64 + lane;
+      lds_barrier();   // both waves have read the trade of the stage before
+      lds_char* const mine_at = trade + side * 4096;
+      *reinterpret_cast<lds_u32x4*>(mine_at) = p.v[0];
+      *reinterpret_cast<lds_u32x4*>(mine_at + 1024) = p.v[1];
+      *reinterpret_cast<lds_u32x4*>(mine_at + 2048) = e.v[0];
+      *reinterpret_cast<lds_u32x4*>(mine_at + 3072) = e.v[1];
+      const int by = (j + 1) % 3 == 0 ? -2 * kPair : kPair;
+      rows.move(by);
+      stat_at += by;
+      if constexpr (!kFirst) cols.move(j % 3 == 0 ? -2 * kPair : kPair);
     };
-    f32x4_t* mine = sums_of(part);
+    // whether some query of either block of stage j sees some of the keys
+    auto seen_pair = [&](int j) {
+      int first = bn - side;
+      if (first < 0) first += w.per_head;
+      const int second = first + 1 == w.per_head ? 0 : first + 1;
+      return (first >= w.seen_lo && first < w.seen_hi) || (2 * j + 1 < w.n && second >= w.seen_lo && second < w.seen_hi);
+    };
+    auto next_blocks = [&]() {
+      bn += 2;
+      while (bn >= w.per_head) bn -= w.per_head;
+    };
+    const int n_stages = (w.n + 1) / 2;
+    bool before = seen_pair(0);
+    stage(std::true_type{}, 0, false);
+    next_blocks();
+    for (int j = 1; j < n_stages; ++j) {
+      const bool here = seen_pair(j);
+      stage(std::false_type{}, j, before);
+      before = here;
+      next_blocks();
+    }
+    wait_vmcnt<0>();   // no load into LDS outlives the workgroup
+    lds_barrier();
+    if (before) {
 #pragma unroll
-    for (int d = 0; d < TL::kDT; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        mine[(d * 8 + g) * 64] = f32x4_t{dk[d][4 * g], dk[d][4 * g + 1], dk[d][4 * g + 2], dk[d][4 * g + 3]};
-        mine[(d * 8 + 4 + g) * 64] = f32x4_t{dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
+      for (int m = 0; m < kProducts; ++m) {
+        const Product q = product(m);
+        x[q.which * kHalf + q.d] = mma16(read_a(m), read_b(m), x[q.which * kHalf + q.d], T{});
       }
-    __shared__ int arrived;
-    __threadfence();   // the sums are visible to the device before the count
-    __syncthreads();
-    if (threadIdx.x == 0)
-      arrived = __hip_atomic_fetch_add(&plan.done[plan.split[slot] * a.n_kv_heads + hk], 1, __ATOMIC_ACQ_REL,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (arrived != parts - 1) return;
-    __threadfence();
-#pragma unroll
-    for (int d = 0; d < TL::kDT; ++d) dk[d] = dv[d] = f32x16_t{};
-    for (int p = 0; p < parts; ++p) {
-      const f32x4_t* from_part = sums_of(p);
-#pragma unroll
-      for (int d = 0; d < TL::kDT; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4_t x = from_part[(d * 8 + g) * 64], y = from_part[(d * 8 + 4 + g) * 64];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dk[d][4 * g + e] += x[e];
-            dv[d][4 * g + e] += y[e];
-          }
-        }
     }
   }
+  if (w.parts > 1 && !join_parts<64 * kDkvWaves, 2 * kHalf>(plan, w, a.n_kv_heads, x)) return;
   bool bad = false;
 #pragma unroll
-  for (int d = 0; d < TL::kDT; ++d) {
+  for (int d = 0; d < kHalf; ++d) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) bad |= not_finite(dk[d][r]) || not_finite(dv[d][r]);
-    store_column<T>(a.dk, w.k0 + key, hk, a.head_dim, d, dk[d], a.scale, in);
-    store_column<T>(a.dv, w.k0 + key, hk, a.head_dim, d, dv[d], 1.0f, in);
+    for (int r = 0; r < 16; ++r) bad |= not_finite(x[d][r]) || not_finite(x[kHalf + d][r]);
+    store_column<T>(a.dk, w.k0 + w.key, w.hk, a.head_dim, side * kHalf + d, x[d], a.scale, w.in);
+    store_column<T>(a.dv, w.k0 + w.key, w.hk, a.head_dim, side * kHalf + d, x[kHalf + d], 1.0f, w.in);
   }
-  // a query that does not see the key may have brought it: see the forward
-  uint64_t again = __ballot(bad && in);
-  again = (again | (again >> 32)) & 0xffffffffull;
-  while (again) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    attn_dkv_row<T>(a, stats.delta, wkey + i, hk, w);
-  }
+  __syncthreads();   // a row done again is stored after both its halves
+  redo_keys<T>(a, stats, w, bad);
 }
 
 // ------------------------------------------------------------------- launches
 // Raises a kernel's limit of dynamic LDS past the 64 KB that a launch gets
 // unasked (once a kernel), then launches it.
-template <auto kKernel, int kLds, typename... Args>
+template <auto kKernel, int kLds, int kThreads = 64 * kWaves, typename... Args>
 static hipError_t launch_lds(int64_t wgs, hipStream_t s, Args... args) {
   if (wgs == 0) return hipSuccess;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
-  kKernel<<<static_cast<unsigned>(wgs), 64 * kWaves, kLds, s>>>(args...);
+  kKernel<<<static_cast<unsigned>(wgs), kThreads, kLds, s>>>(args...);
   return hipGetLastError();
 }
 
@@ -1154,8 +1252,11 @@ static hipError_t bwd_launch(const AttnView& a, int dtype, void* ws, hipStream_t
   // one workgroup more than there are query tiles: it makes the plan
   hipError_t e = launch_lds<attn_dq_kernel<T, DP, kWide>, DqShape<T, DP>::kLds>(nq * a.n_heads + 1, s, a, nq, b.stats, b.plan, err);
   if (e != hipSuccess) return e;
-  return launch_lds<attn_dkv_kernel<T, DP, kWide>, DkvShape<T, DP>::kLds>((b.plan.n_slots + b.max_parts) * a.n_kv_heads, s, a,
-                                                                          b.stats, b.plan, err);
+  const int64_t items = (b.plan.n_slots + b.max_parts) * a.n_kv_heads;   // at most
+  if constexpr (sizeof(T) == 2)
+    return launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan, err);
+  else
+    return launch_lds<attn_dkv_f32_kernel<DP, kWide>, 2 * DkvShape<T, DP>::kStage>(items, s, a, b.stats, b.plan, err);
 }
 
 template <bool kWide>

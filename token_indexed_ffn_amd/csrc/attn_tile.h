@@ -106,23 +106,24 @@ struct RowReader {
 // 32) of the block, the rows in the order of a Column.  16 lanes read 4 rows x
 // 16 elements and get 4 rows of one element each; 8 rows on, the spread
 // differs, 16 rows on it does not.
-template <int DP>
+// kDT: element blocks the wave reads, from block dt0 on.
+template <int DP, int kDT = DP / 32>
 struct ColumnReader {
   using TL = Tile<bf16_t, DP>;
-  const lds_char* at[TL::kDT][2];
-  __device__ __forceinline__ explicit ColumnReader(const lds_char* ring) {
+  const lds_char* at[kDT][2];
+  __device__ __forceinline__ explicit ColumnReader(const lds_char* ring, int dt0 = 0) {
     const int lane = threadIdx.x & 63, i16 = lane & 15;
 #pragma unroll
-    for (int dt = 0; dt < TL::kDT; ++dt)
+    for (int dt = 0; dt < kDT; ++dt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int c = dt * 32 + (lane & 16) + 4 * (i16 & 3), row = 8 * e + 4 * (lane >> 5) + (i16 >> 2);
+        const int c = (dt0 + dt) * 32 + (lane & 16) + 4 * (i16 & 3), row = 8 * e + 4 * (lane >> 5) + (i16 >> 2);
         at[dt][e] = ring + row * TL::kRow + (((c >> 3) ^ TL::spread(row)) << 4) + (c & 4) * 2;
       }
   }
   __device__ __forceinline__ void move(int bytes) {
 #pragma unroll
-    for (int dt = 0; dt < TL::kDT; ++dt)
+    for (int dt = 0; dt < kDT; ++dt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) at[dt][e] += bytes;
   }
@@ -187,12 +188,13 @@ struct TileLoader {
   u32x4_t buffer;
   uint32_t lds0;           // this wave's first byte of a tile
 
-  __device__ __forceinline__ void init(const HeadsView& t, int64_t row0, int rows, int64_t head, int dim) {
+  // wave: the caller's number among the NW waves that load the tile.
+  __device__ __forceinline__ void init(const HeadsView& t, int64_t row0, int rows, int64_t head, int dim, int wave) {
     row_bytes = t.row_stride * static_cast<int64_t>(sizeof(T));
     n = rows;
     dim_bytes = dim * static_cast<int>(sizeof(T));
-    const int at = (threadIdx.x >> 6) * 1024 + (threadIdx.x & 63) * 16;
-    lds0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    const int at = wave * 1024 + (threadIdx.x & 63) * 16;
+    lds0 = wave * 1024;
     row = at / TL::kRow;
     byte = ((at % TL::kRow / 16) ^ TL::spread(row)) * 16;
     if constexpr (!kWide) {
