@@ -56,9 +56,16 @@ def _dev(*ts) -> None:
             raise ValueError("expected contiguous device tensors")
 
 
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ws(nbytes: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
@@ -868,8 +875,7 @@ def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     (window == 0 or j > p - window or j < sinks); the queries are the last positions of
     their sequence.  scale: head_dim ** -0.5 when None."""
     if out is None:
-        out = {"o": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
+        out = {"o": q.new_empty(q.shape), "lse": q.new_empty(q.shape[:2], dtype=torch.float32)}
     a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"])
     _check(lib().staple_attn_fwd(ctypes.byref(a), _stream(stream)), "staple_attn_fwd")
     return out
@@ -882,9 +888,7 @@ def staple_attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
                     stream=None) -> dict:
     """Gradients dq, dk, dv of staple_attn_fwd from do, its operands and its o and lse."""
     if out is None:
-        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               "dk": torch.empty(k.shape, dtype=k.dtype, device=q.device),
-               "dv": torch.empty(v.shape, dtype=v.dtype, device=q.device)}
+        out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
     a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do, out["dq"], out["dk"], out["dv"])
     ws = _ws(lib().staple_attn_bwd_workspace_bytes(ctypes.byref(a)), workspace, q.device)
     _check(lib().staple_attn_bwd(ctypes.byref(a), _p(ws), _ws_size(ws), _stream(stream)),
@@ -1016,8 +1020,7 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     hk = k_pages.shape[-3]
     dt = k_pages.dtype
     if out is None:
-        out = {"o": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               "lse": torch.empty((n, h), dtype=torch.float32, device=q.device)}
+        out = {"o": q.new_empty(q.shape), "lse": q.new_empty((n, h), dtype=torch.float32)}
     lse = out.get("lse")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, h) or
                             not lse.is_contiguous() or not lse.is_cuda):
