@@ -44,10 +44,13 @@ __device__ __forceinline__ void dma16(const void* src, lds_void* dst) {
 }
 
 // The same load through a buffer descriptor: the lane reads 16 bytes at
-// `offset` of the buffer, zeros where that is past its end.
+// `offset` of the buffer, zeros where that is past its end.  The compiler does
+// not look into the asm, and a scalar register that a vector instruction has
+// written (a descriptor word that was spilled to a lane and read back) may be
+// read by a memory instruction only five wait states later: hence s_nop 4.
 __device__ __forceinline__ void dma16(const u32x4_t& buffer, uint32_t offset, lds_void* dst) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer), "{m0}"(m0) : "memory");
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer), "{m0}"(m0) : "memory");
 }
 // Descriptor of `bytes` bytes at `base` (both uniform over the wave): no
 // stride, no swizzle, 32-bit data format.
