@@ -622,6 +622,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
   using Shape = DqShape<T, DP>;
   using Loader = TileLoader<T, DP, 32, kWaves, kWide>;
   constexpr int kAhead = Shape::kAhead, kBlock = Shape::kBlock;
+  constexpr int kFew = 8;   // blocks: see below
   extern __shared__ __align__(1024) char smem[];
   lds_char* const kring = (lds_char*)smem;
   lds_char* const vring = kring + Shape::kKSlots * kBlock;
@@ -640,11 +641,6 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
   // ring places of the blocks to read, and to load next
   int kr = 0, vr = 0, kn = kAhead * kBlock, vn = kAhead * kBlock;
   auto bump = [](int& at, int slots) { at = at + kBlock == slots * kBlock ? 0 : at + kBlock; };
-#pragma unroll
-  for (int b = 0; b < kAhead; ++b) {
-    kl.load(keys.first(b), kring + b * kBlock);
-    vl.load(keys.first(b), vring + b * kBlock);
-  }
   u32x4_t qf[TL::kSteps], dof[TL::kSteps];
   float delta = 0.0f;
 #pragma unroll
@@ -655,11 +651,45 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void attn_dq_k
   delta += other_half(delta);
   const float lse = w.in ? a.lse[(w.q0 + w.row) * a.n_heads + w.head] : 0.0f;
   const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+  const float c = load_queries<T, DP>(a, w, qf);
+  if constexpr (sizeof(T) == 2) {
+    // delta from the rounded o is off by sum d_o (o's rounding), which counts
+    // where o is large: where few keys share a query's weight.  A workgroup of
+    // few blocks therefore meets them once before, for delta + sum P (dP -
+    // delta), exact as sum P = 1.
+    if (keys.n <= kFew) {
+      float more = 0.0f;
+      for (int b = 0; b < keys.n; ++b) {
+        kl.load(keys.first(b), kring);
+        vl.load(keys.first(b), vring);
+        wait_vmcnt<0>();
+        lds_barrier();
+        f32x16_t s = {}, dp = {};
+#pragma unroll
+        for (int st = 0; st < TL::kSteps; ++st) {
+          s = mma16(TL::row_frag(kring, 0, st), qf[st], s, T{});
+          dp = mma16(TL::row_frag(vring, 0, st), dof[st], dp, T{});
+        }
+        const SeenKeys seen(a, w.p, w.in, keys.first(b));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float g = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+          more += seen(r) ? g : 0.0f;
+        }
+        lds_barrier();   // the block has been read
+      }
+      delta += more + other_half(more);
+    }
+  }
   if (w.in && half == 0) {
     stats.lse2[w.head * a.total_q + w.q0 + w.row] = lse2;
     stats.delta[w.head * a.total_q + w.q0 + w.row] = delta;
   }
-  const float c = load_queries<T, DP>(a, w, qf);
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) {
+    kl.load(keys.first(b), kring + b * kBlock);
+    vl.load(keys.first(b), vring + b * kBlock);
+  }
   f32x16_t dq[TL::kDT] = {};
   Column<T> prev;
   const lds_char* kprev = kring;
