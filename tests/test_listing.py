@@ -47,7 +47,7 @@ def test_too_early_finds_a_load_that_is():
     assert too_early("\ts_mov_b32 m0, s3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 v[2:3], off\n") == (1, [])
 
 
-@pytest.mark.parametrize("source", ["attn.hip", "gemm.hip"])
+@pytest.mark.parametrize("source", ["attn.hip", "attn_f32.hip", "gemm.hip"])
 def test_loads_into_lds_keep_their_wait_states(source, tmp_path):
     try:
         hipcc = B.hipcc()

@@ -32,7 +32,13 @@ static staple_status_t attn_check(const staple_attn_t* a) {
   REQUIRE(a->window >= 0 && a->sinks >= 0 && std::isfinite(a->scale));
   if (a->n_seqs > kMaxTokens || a->total_q > kMaxTokens || a->total_k > kMaxTokens ||
       a->n_heads > 65535 || a->total_q * a->n_heads > kMaxLaunchRows * 64 ||
-      a->total_k * a->n_kv_heads > kMaxLaunchRows * 64 || a->n_seqs * a->n_heads > kMaxLaunchRows)
+      a->total_k * a->n_kv_heads > kMaxLaunchRows * 64)
+    return STAPLE_ERR_UNSUPPORTED;
+  // workgroups of a launch: a tile of queries (keys) and head each, and parts of
+  // split tiles; a grid has less than 2^32 threads
+  const bool f32 = a->dtype == STAPLE_F32;
+  const int64_t tokens = a->total_q > a->total_k ? a->total_q : a->total_k;
+  if ((tokens / (f32 ? 32 : 128) + a->n_seqs + 4) * a->n_heads + 4096 > kMaxLaunchRows * (f32 ? 2 : 1))
     return STAPLE_ERR_UNSUPPORTED;
   return STAPLE_OK;
 }

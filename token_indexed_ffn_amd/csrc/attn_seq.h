@@ -1,0 +1,539 @@
+// What the attention kernels share: tiles of packed sequences, masks, the rows
+// done again one by one, and the plan of the dk, dv kernels.
+#pragma once
+
+#include "attn_row.h"
+#include "attn_tile.h"
+
+namespace staple {
+
+constexpr int kWaves = 4;   // of a workgroup, unless said otherwise
+
+// A tile of 2^rows_log2 consecutive rows of one sequence.  Sequence b owns the
+// slots floor(cu[b] / rows) + b onwards, at least as many as it has tiles, so a
+// grid of total / rows + n_seqs slots holds every sequence and a workgroup
+// finds its own by a search of cu alone.
+struct TileOf {
+  int64_t seq, first;   // first: the tile's first row within the sequence; seq -1: none
+};
+__device__ __forceinline__ TileOf tile_of_slot(const int32_t* cu, int64_t n_seqs, int rows_log2, int64_t slot) {
+  int64_t lo = 0, hi = n_seqs;   // slots of lo start at or before `slot`, those of hi after
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if ((cu[mid] >> rows_log2) + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  const int64_t tile = slot - ((cu[lo] >> rows_log2) + lo);
+  return TileOf{tile < 0 ? -1 : lo, tile << rows_log2};
+}
+inline int64_t tile_slots(int64_t total, int64_t n_seqs, int rows_log2) { return (total >> rows_log2) + n_seqs; }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_id() { return uniform(threadIdx.x >> 6); }
+
+// One sequence and head, and the workgroup's tile of its queries or keys.
+struct Segment {
+  int64_t q0, k0;          // first rows
+  int nq, nk, past;        // lengths, and the position of query 0
+  int first;               // the tile's first query (key)
+  // False where there is no such tile.  find_lane: any slot a lane; find: one
+  // slot for the whole workgroup, kept in scalar registers.
+  __device__ __forceinline__ bool find_lane(const AttnView& a, const int32_t* cu, int rows_log2, int64_t slot, int* err) {
+    const TileOf tile = tile_of_slot(cu, a.n_seqs, rows_log2, slot);
+    if (tile.seq < 0) return false;
+    int64_t q1, k1;
+    seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
+    seq_rows(a.cu_k, tile.seq, a.total_k, &k0, &k1, err);
+    if (tile.first >= (cu == a.cu_q ? q1 - q0 : k1 - k0)) return false;
+    nq = static_cast<int>(q1 - q0);
+    nk = static_cast<int>(k1 - k0);
+    past = nk - nq;
+    first = static_cast<int>(tile.first);
+    return true;
+  }
+  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int rows_log2, int64_t slot, int* err) {
+    if (!find_lane(a, cu, rows_log2, slot, err)) return false;
+    nq = uniform(nq);
+    nk = uniform(nk);
+    past = nk - nq;
+    first = uniform(first);
+    q0 = uniform(static_cast<int>(q0));
+    k0 = uniform(static_cast<int>(k0));
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------- masks
+// Applied with selects (a few integer compares an element), never by branching
+// on one element of a result.
+
+// Which keys of a block the lane's query (at position p) sees: key j = 8 (r /
+// 4) + r % 4 (+ 4 for the upper half-wave) of the block at `key` is seen when
+// j <= hi and (j >= lo or j < sink).
+struct SeenKeys {
+  int hi, lo, sink;
+  __device__ __forceinline__ SeenKeys(const AttnView& a, int p, bool in, int key) {
+    const int at = key + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+    hi = in ? p - at : -1;
+    lo = a.window > 0 ? p - a.window + 1 - at : -kMaxTokens;
+    sink = a.sinks - at;
+  }
+  __device__ __forceinline__ bool operator()(int r) const {
+    const int j = 8 * (r >> 2) + (r & 3);
+    return (j <= hi) & ((j >= lo) | (j < sink));
+  }
+};
+// Which queries of a block (the first is number i0 of the sequence) see the
+// lane's key.
+struct SeenBy {
+  int lo, hi;
+  __device__ __forceinline__ SeenBy(const AttnView& a, const Segment& s, int key, bool in, int i0) {
+    const int at = i0 + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+    lo = key - s.past - at;
+    int end = s.nq;
+    if (a.window > 0 && key >= a.sinks) end = min(end, key - s.past + a.window);
+    hi = in ? end - at : -1;
+  }
+  __device__ __forceinline__ bool operator()(int r) const {
+    const int j = 8 * (r >> 2) + (r & 3);
+    return (j >= lo) & (j < hi);
+  }
+};
+
+// True where a value is NaN or infinite.
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
+
+// The 32-key blocks that some query at a position in [p_min, p_max] sees: those
+// of the sinks, then the window's; and which of them every query of the wave's
+// range sees whole.
+struct KeyBlocks {
+  int n_sink, lo, n;
+  int nk;
+  int whole_sink, whole_lo, whole_n;
+  __device__ __forceinline__ KeyBlocks(const AttnView& a, int n_keys, int p_min, int p_max) : nk(n_keys) {
+    lo = (a.window > 0 ? max(p_min - a.window + 1, 0) : 0) / 32;
+    n_sink = p_max < 0 ? 0 : (min(a.sinks, lo * 32) + 31) / 32;
+    n = p_max < 0 ? 0 : n_sink + p_max / 32 + 1 - lo;
+    whole_sink = whole_n = 0;
+  }
+  // The wave's own queries: positions [p_min, p_max], all 32 of them there.
+  __device__ __forceinline__ void set_wave(const AttnView& a, int p_min, int p_max, bool full) {
+    const int end = full ? max(p_min + 1, 0) / 32 : 0;               // blocks that end at or before p_min
+    const int from = a.window > 0 ? (max(p_max - a.window + 1, 0) + 31) / 32 : 0;
+    // numbered as first() numbers them; the sinks' whole blocks come first
+    whole_sink = min(min(a.sinks / 32, n_sink), end);
+    whole_lo = n_sink + max(from - lo, 0);
+    whole_n = max(n_sink + end - lo - whole_lo, 0);
+  }
+  __device__ __forceinline__ bool whole(int b) const {
+    return b < whole_sink || static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
+  }
+  // First key of block b; blocks past the last lie past the keys.
+  __device__ __forceinline__ int first(int b) const { return b < n ? (b < n_sink ? b : lo + b - n_sink) * 32 : nk; }
+};
+
+// The wave's 32 queries, one a column.
+struct QueryCols : Segment {
+  int head, hk;
+  int wq, row, p;             // the wave's first query; the lane's, and its position
+  bool in;
+  int tile_rows;
+  // group_of_wave: which 32 queries of the workgroup's tile the wave has.
+  __device__ __forceinline__ bool find(const AttnView& a, int rows_log2, int64_t n_slots, int64_t id, int group_of_wave, int* err) {
+    // the last tiles of a sequence see the most keys: they start first
+    if (!Segment::find(a, a.cu_q, rows_log2, n_slots - 1 - id / a.n_heads, err)) return false;
+    tile_rows = 1 << rows_log2;
+    head = uniform(static_cast<int>(id % a.n_heads));
+    hk = uniform(head / a.group);
+    wq = first + 32 * group_of_wave;
+    row = wq + (threadIdx.x & 31);
+    in = row < nq;
+    p = past + row;
+    return true;
+  }
+  __device__ __forceinline__ KeyBlocks blocks(const AttnView& a) const {
+    KeyBlocks b(a, nk, past + first, past + min(first + tile_rows, nq) - 1);
+    b.set_wave(a, past + wq, past + wq + 31, wq + 31 < nq);
+    return b;
+  }
+};
+
+// One side of the scores takes the scale's sign: scores in powers of two are
+// then score_factor() times the products, and as that is positive the largest
+// product has the largest score and a hidden one can be -inf before scaling.
+template <typename T>
+__device__ __forceinline__ u32x4_t signed_frag(const AttnView& a, u32x4_t v) {
+  if (a.scale < 0.0f) v = flip_sign<T>(v);
+  return a.scale == 0.0f ? u32x4_t{0, 0, 0, 0} : v;
+}
+__device__ __forceinline__ float score_factor(const AttnView& a) {
+  return a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
+}
+template <typename T, int DP>
+__device__ __forceinline__ float load_queries(const AttnView& a, const QueryCols& w, u32x4_t* qf) {
+#pragma unroll
+  for (int s = 0; s < Tile<T, DP>::kSteps; ++s)
+    qf[s] = signed_frag<T>(a, load_frag<T>(a.q, w.q0 + w.row, w.head, a.head_dim, s, w.in));
+  return score_factor(a);
+}
+
+// ------------------------------------------------------------------- forward
+// One query row, by a whole wave (row t of q, at position p of the sequence
+// whose keys start at row k0).
+template <typename T>
+__device__ __forceinline__ void attn_fwd_row(const AttnView& a, int64_t t, int64_t h, int64_t p, int64_t k0) {
+  const int64_t hk = h / a.group;
+  int64_t sink_end, lo;
+  visible_keys(p, a.window, a.sinks, &sink_end, &lo);
+  const Row2 q = load_row<T>(a.q, t, h, a.head_dim);
+  RowSoftmax sm;
+  for (int64_t j = 0; j <= p; ++j) {
+    if (j == sink_end) j = lo;
+    if (j > p) break;
+    const Row2 k = load_row<T>(a.k, k0 + j, hk, a.head_dim);
+    sm.add(dot(q, k) * a.scale, load_row<T>(a.v, k0 + j, hk, a.head_dim));
+  }
+  store_row<T>(a.o, t, h, a.head_dim, sm.value());
+}
+
+// Running softmax of the lane's column: the sums stay relative to `top`, an
+// earlier maximum rounded up to an integer, until a score passes it by 8: the
+// exponentials stay below 2^9, far from fp32's range, lanes exchange maxima
+// only then, and what has been summed is scaled by a power of two, exactly.
+struct ColumnSoftmax {
+  float top = -INFINITY, sum = 0.0f;   // sum: this half-wave's keys
+  // s: the block's products, c times which are the scores.  True where `keep`
+  // has to scale the sums.
+  __device__ __forceinline__ bool raise(const f32x16_t& s, float c, float* keep) {
+    float m = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r]);
+    m *= c;
+    if (!__any((m > top + 8.0f) | ((top == -INFINITY) & (m > top)))) return false;
+    const float t = fmaxf(top, ceilf(fmaxf(m, other_half(m))));
+    *keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t);
+    top = t;
+    sum *= *keep;
+    return true;
+  }
+  __device__ __forceinline__ float base() const { return top == -INFINITY ? 0.0f : top; }
+};
+
+// -inf for the hidden keys of the block at `key`.
+__device__ __forceinline__ void mask_keys(const AttnView& a, const QueryCols& w, int key, f32x16_t& s) {
+  const SeenKeys seen(a, w.p, w.in, key);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = seen(r) ? s[r] : -INFINITY;
+}
+
+// A NaN or an infinity in a result (`bad`) may have come from a row that the
+// query does not see (its zero weight times it): such queries are done again
+// key by key.
+template <typename RowFn>
+__device__ __forceinline__ void redo_queries(bool bad, RowFn row) {
+  uint64_t again = __ballot(bad);
+  again = (again | (again >> 32)) & 0xffffffffull;
+  while (again) {
+    const int i = __builtin_ctzll(again);
+    again &= again - 1;
+    row(i);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// One query's row of dq, by a whole wave.
+template <typename T>
+__device__ __forceinline__ void attn_dq_row(const AttnView& a, int64_t t, int64_t h, int64_t p, int64_t k0) {
+  const int64_t hk = h / a.group;
+  int64_t sink_end, lo;
+  visible_keys(p, a.window, a.sinks, &sink_end, &lo);
+  const Row2 q = load_row<T>(a.q, t, h, a.head_dim), d_o = load_row<T>(a.d_o, t, h, a.head_dim);
+  const float dl = dot(d_o, load_row<T>(a.o, t, h, a.head_dim)), lse = a.lse[t * a.n_heads + h];
+  Row2 dq{{0.0f, 0.0f}};
+  for (int64_t j = 0; j <= p; ++j) {
+    if (j == sink_end) j = lo;
+    if (j > p) break;
+    const Row2 k = load_row<T>(a.k, k0 + j, hk, a.head_dim);
+    const float pr = __expf(dot(q, k) * a.scale - lse);
+    const float ds = pr * (dot(d_o, load_row<T>(a.v, k0 + j, hk, a.head_dim)) - dl);
+    dq.x[0] += ds * k.x[0];
+    dq.x[1] += ds * k.x[1];
+  }
+  dq.x[0] *= a.scale;
+  dq.x[1] *= a.scale;
+  store_row<T>(a.dq, t, h, a.head_dim, dq);
+}
+
+// One key's rows of dk and dv, by a whole wave.
+template <typename T>
+__device__ __forceinline__ void attn_dkv_row(const AttnView& a, const float* delta, int j, int hk, const Segment& s) {
+  const Row2 k = load_row<T>(a.k, s.k0 + j, hk, a.head_dim), v = load_row<T>(a.v, s.k0 + j, hk, a.head_dim);
+  Row2 dk{{0.0f, 0.0f}}, dv{{0.0f, 0.0f}};
+  const int i0 = max(j - s.past, 0);
+  const int i1 = a.window > 0 && j >= a.sinks ? min(j - s.past + a.window, s.nq) : s.nq;
+  for (int64_t g = 0; g < a.group; ++g) {
+    const int64_t h = static_cast<int64_t>(hk) * a.group + g;
+    for (int64_t i = i0; i < i1; ++i) {
+      const Row2 q = load_row<T>(a.q, s.q0 + i, h, a.head_dim);
+      const Row2 d_o = load_row<T>(a.d_o, s.q0 + i, h, a.head_dim);
+      const float pr = __expf(dot(q, k) * a.scale - a.lse[(s.q0 + i) * a.n_heads + h]);
+      const float ds = pr * (dot(d_o, v) - delta[h * a.total_q + s.q0 + i]);
+      dk.x[0] += ds * q.x[0];
+      dk.x[1] += ds * q.x[1];
+      dv.x[0] += pr * d_o.x[0];
+      dv.x[1] += pr * d_o.x[1];
+    }
+  }
+  dk.x[0] *= a.scale;
+  dk.x[1] *= a.scale;
+  store_row<T>(a.dk, s.k0 + j, hk, a.head_dim, dk);
+  store_row<T>(a.dv, s.k0 + j, hk, a.head_dim, dv);
+}
+
+// What the backward needs of the forward: lse in powers of two (0 where no key
+// is seen) and delta = sum d_o o, both [n_heads][total_q].
+struct RowStats {
+  float* lse2;
+  float* delta;
+};
+
+// The 32-query blocks that see some key of a workgroup's tile: `per_head` of
+// them, from block b_lo, for each head of the group.
+struct QueryBlocks {
+  int b_lo, per_head;
+  __device__ __forceinline__ QueryBlocks(const AttnView& a, const Segment& w, int tile_rows) {
+    const int last_key = min(w.first + tile_rows, w.nk) - 1;
+    const int lo = max(w.first - w.past, 0);
+    const int hi = a.window > 0 && w.first >= a.sinks ? min(last_key - w.past + a.window, w.nq) : w.nq;
+    b_lo = lo / 32;
+    per_head = hi > lo ? (hi + 31) / 32 - b_lo : 0;
+  }
+};
+
+// How dk and dv are worked off.  Key tiles see very different numbers of
+// queries (the first of a causal sequence all of them, a window's only its
+// own, the sinks' all again), and a shared key-value head those of every head
+// of its group.  A tile with more blocks than `chunk` is split into parts of
+// equal size, whose fp32 sums go to the workspace and are added in part order
+// by the last of them to finish; and the items (tiles and parts) start in the
+// order of their size, the largest first.  Written by one workgroup of the dq
+// kernel, which runs before.
+struct DkvPlan {
+  int32_t* head;      // [0] items
+  int32_t* blocks;    // [slots] blocks of the slot's tile
+  int32_t* parts;     // [slots] its parts
+  int32_t* first;     // [slots] its first partial result, where there are several parts
+  int32_t* split;     // [slots] its number among the split tiles
+  int32_t* items;     // [slots + max_parts][2] slot, part
+  int32_t* done;      // [max_parts][n_kv_heads] parts of a split tile that have finished
+  float* sums;        // [max_parts][n_kv_heads] dk and dv sums of a part
+  int64_t n_slots;
+  int target;         // parts per head to aim for
+  int rows_log2;      // keys of a tile
+};
+constexpr int kMinChunk = 16;   // blocks: a part's sums cost about as much traffic as two blocks
+constexpr int kBuckets = 64;
+
+__device__ __forceinline__ int64_t group_sum(int64_t v, int64_t* lds) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) all += lds[i];
+  return all;
+}
+
+__device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan, int* err) {
+  __shared__ int64_t sums[kWaves];
+  __shared__ int count[kBuckets], start[kBuckets], n_parts, n_split;
+  constexpr int kThreads = 64 * kWaves;
+  const int n_slots = static_cast<int>(plan.n_slots);
+  int64_t mine = 0;
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    Segment w;
+    int n = -1;   // no tile
+    if (w.find_lane(a, a.cu_k, plan.rows_log2, s, err)) n = QueryBlocks(a, w, 1 << plan.rows_log2).per_head * a.group;
+    plan.blocks[s] = n;
+    mine += max(n, 0);
+  }
+  const int64_t total = group_sum(mine, sums);
+  const int64_t share = (total + plan.target - 1) / plan.target;
+  const int chunk = static_cast<int>(share < kMinChunk ? kMinChunk : share);
+  if (threadIdx.x < kBuckets) count[threadIdx.x] = 0;
+  if (threadIdx.x == 0) n_parts = n_split = 0;
+  __syncthreads();
+  // an item has at most `chunk` blocks; bucket 0 holds the largest
+  auto bucket = [&](int size) { return kBuckets - 1 - static_cast<int>(static_cast<int64_t>(size) * (kBuckets - 1) / chunk); };
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    const int n = plan.blocks[s];
+    if (n < 0) continue;
+    const int parts = max((n + chunk - 1) / chunk, 1);
+    plan.parts[s] = parts;
+    if (parts > 1) {
+      plan.first[s] = atomicAdd(&n_parts, parts);
+      plan.split[s] = atomicAdd(&n_split, 1);
+    }
+    atomicAdd(&count[bucket((n + parts - 1) / parts)], parts);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int at = 0;
+    for (int b = 0; b < kBuckets; ++b) {
+      start[b] = at;
+      at += count[b];
+    }
+    plan.head[0] = at;
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < n_slots; s += kThreads) {
+    const int n = plan.blocks[s];
+    if (n < 0) continue;
+    const int parts = plan.parts[s];
+    int at = atomicAdd(&start[bucket((n + parts - 1) / parts)], parts);
+    for (int p = 0; p < parts; ++p, ++at) {
+      plan.items[2 * at] = s;
+      plan.items[2 * at + 1] = p;
+    }
+  }
+  for (int i = threadIdx.x; i < n_split * a.n_kv_heads; i += kThreads) plan.done[i] = 0;
+}
+
+// dk and dv: one key a column; the queries that see them (of every head of the
+// group) go through LDS.  An item is a key tile or a part of one.
+struct DkvItem : Segment {
+  int slot, part, parts, hk;
+  int64_t h0;              // the head of the item's first block
+  int n, ln;               // its blocks, and the first one's number within its head
+  int b_lo, per_head;      // see QueryBlocks
+  int wkey, key;           // the wave's first key; the lane's
+  bool in;
+  int whole_lo, whole_n;   // of a head's blocks, those whose every query sees all of the wave's keys
+  int seen_lo, seen_hi;    // and those of which some query sees some of them: [seen_lo, seen_hi)
+  // False where there is no such item; `group`: which 32 keys of the tile the wave has.
+  __device__ __forceinline__ bool find(const AttnView& a, const DkvPlan& plan, int group_of_wave, int* err) {
+    const int item = uniform(static_cast<int>(blockIdx.x) / a.n_kv_heads);
+    if (item >= plan.head[0]) return false;
+    hk = static_cast<int>(blockIdx.x) - item * a.n_kv_heads;
+    slot = uniform(plan.items[2 * item]);
+    part = uniform(plan.items[2 * item + 1]);
+    parts = uniform(plan.parts[slot]);
+    if (!Segment::find(a, a.cu_k, plan.rows_log2, slot, err)) return false;
+    wkey = first + 32 * group_of_wave;
+    key = wkey + (threadIdx.x & 31);
+    in = key < nk;
+    const QueryBlocks blocks(a, *this, 1 << plan.rows_log2);
+    b_lo = blocks.b_lo;
+    per_head = blocks.per_head;
+    const int all = per_head * a.group, chunk = uniform((all + parts - 1) / parts);
+    const int from_block = min(part * chunk, all);
+    n = min(chunk, all - from_block);
+    const int skip = uniform(per_head > 0 ? from_block / per_head : 0);
+    h0 = static_cast<int64_t>(hk) * a.group + skip;
+    ln = from_block - skip * per_head;
+    const bool sink = wkey < a.sinks, all_sinks = wkey + 31 < a.sinks;
+    const int from = (max(wkey + 31 - past, 0) + 31) / 32;
+    const int to = (a.window > 0 && !all_sinks ? min(max(wkey - past + a.window, 0), nq) : nq) / 32;
+    whole_lo = from - b_lo;
+    whole_n = wkey + 31 < nk ? max(to - from, 0) : 0;
+    const int end = a.window > 0 && !sink ? min(max(wkey + 31 - past + a.window, 0), nq) : nq;
+    seen_lo = max(wkey - past, 0) / 32 - b_lo;
+    seen_hi = wkey < nk ? (end + 31) / 32 - b_lo : 0;
+    return true;
+  }
+  __device__ __forceinline__ bool whole(int b) const {
+    return static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
+  }
+};
+
+// A split tile's part: its fp32 sums to the workspace, as they lie in the
+// registers of the workgroup's kThreads threads (x: kX results a thread); true
+// in the part that arrives last, with all parts' sums added in part order.
+template <int kThreads, int kX>
+__device__ __forceinline__ bool join_parts(const DkvPlan& plan, const DkvItem& w, int n_kv_heads, f32x16_t* x) {
+  constexpr int kFloats = kThreads * 16 * kX;
+  auto sums_of = [&](int p) {
+    return reinterpret_cast<f32x4_t*>(plan.sums + (static_cast<int64_t>(plan.first[w.slot] + p) * n_kv_heads + w.hk) * kFloats) +
+           threadIdx.x;
+  };
+  f32x4_t* mine = sums_of(w.part);
+#pragma unroll
+  for (int d = 0; d < kX; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      mine[(d * 4 + g) * kThreads] = f32x4_t{x[d][4 * g], x[d][4 * g + 1], x[d][4 * g + 2], x[d][4 * g + 3]};
+  __shared__ int arrived;
+  __threadfence();   // the sums are visible to the device before the count
+  __syncthreads();
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(&plan.done[plan.split[w.slot] * n_kv_heads + w.hk], 1, __ATOMIC_ACQ_REL,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != w.parts - 1) return false;
+  __threadfence();
+#pragma unroll
+  for (int d = 0; d < kX; ++d) x[d] = f32x16_t{};
+  for (int p = 0; p < w.parts; ++p) {
+    const f32x4_t* from = sums_of(p);
+#pragma unroll
+    for (int d = 0; d < kX; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t v = from[(d * 4 + g) * kThreads];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[d][4 * g + e] += v[e];
+      }
+  }
+  return true;
+}
+
+// Keys whose gradients came out not finite: a query that does not see the key
+// may have brought it (zero times its rows), so they are done again query by
+// query; see the forward.
+template <typename T>
+__device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& stats, const DkvItem& w, bool bad) {
+  uint64_t again = __ballot(bad && w.in);
+  again = (again | (again >> 32)) & 0xffffffffull;
+  while (again) {
+    const int i = __builtin_ctzll(again);
+    again &= again - 1;
+    attn_dkv_row<T>(a, stats.delta, w.wkey + i, w.hk, w);
+  }
+}
+
+// ------------------------------------------------------------------- launches
+// Raises a kernel's limit of dynamic LDS past the 64 KB that a launch gets
+// unasked (once a kernel), then launches it.
+template <auto kKernel, int kLds, int kThreads = 64 * kWaves, typename... Args>
+inline hipError_t launch_lds(int64_t wgs, hipStream_t s, Args... args) {
+  if (wgs == 0) return hipSuccess;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (attr != hipSuccess) return attr;
+  kKernel<<<static_cast<unsigned>(wgs), kThreads, kLds, s>>>(args...);
+  return hipGetLastError();
+}
+
+// Whether a head's rows may span 2^31 bytes.
+inline bool spans_buffer(const HeadsView& t, int64_t rows, int elem_bytes) {
+  return t.row_stride >= (int64_t(1) << 31) / elem_bytes / (rows + 256);
+}
+
+// The backward's workspace: the row statistics, the plan, and the sums of split
+// tiles.
+struct BwdSpace {
+  RowStats stats;
+  DkvPlan plan;
+  int max_parts;
+  size_t bytes;
+};
+
+// kernels of fp32 (attn_f32.hip)
+hipError_t launch_attn_fwd_f32(const AttnView& a, hipStream_t s, int* err);
+hipError_t launch_attn_bwd_f32(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err);
+constexpr int kF32RowsLog2 = 5;    // queries (keys) of a workgroup's tile: 32 in fp32,
+constexpr int kBf16RowsLog2 = 7;   // 128 in bf16
+
+}  // namespace staple

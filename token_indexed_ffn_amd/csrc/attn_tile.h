@@ -177,13 +177,11 @@ struct TileLoader {
   using TL = Tile<T, DP>;
   static constexpr int kPer = R * TL::kRow / (1024 * NW);   // instructions per wave
   static constexpr int kRowStep = 1024 * NW / TL::kRow;     // rows between them
-  // the spread repeats every 16 rows; 8 rows on, its lowest bit is the other one
-  static constexpr bool kFlip = kRowStep % 16 != 0;
-  static_assert(kPer * 1024 * NW == R * TL::kRow && (kRowStep % 16 == 0 || (kRowStep == 8 && TL::kChunks >= 16)), "tile shape");
+  static_assert(kPer * 1024 * NW == R * TL::kRow, "tile shape");
   const char* base;        // row 0 of the sequence, this head
   int64_t row_bytes;
   int n, dim_bytes;
-  int row, byte;           // the lane's row and byte of it in instruction 0
+  int row, place;          // the lane's row in instruction 0, and its 16-byte place in every row
   uint32_t offset[kPer];
   u32x4_t buffer;
   uint32_t lds0;           // this wave's first byte of a tile
@@ -196,16 +194,17 @@ struct TileLoader {
     const int at = wave * 1024 + (threadIdx.x & 63) * 16;
     lds0 = wave * 1024;
     row = at / TL::kRow;
-    byte = ((at % TL::kRow / 16) ^ TL::spread(row)) * 16;
+    place = at % TL::kRow / 16;
     if constexpr (!kWide) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = kFlip && (i & 1) ? byte ^ 16 : byte;
+        const int x = byte_of(i);
         offset[i] = x < dim_bytes ? static_cast<uint32_t>(row + i * kRowStep) * static_cast<uint32_t>(row_bytes) + x : 0x80000000u;
       }
     }
     set_base(t.data + row0 * row_bytes + head * t.head_stride * static_cast<int64_t>(sizeof(T)));
   }
+  __device__ __forceinline__ int byte_of(int i) const { return (place ^ TL::spread(row + i * kRowStep)) * 16; }
   __device__ __forceinline__ void set_base(const char* b) {
     base = b;
     if constexpr (!kWide)
@@ -228,7 +227,7 @@ struct TileLoader {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int r = row0 + row + i * kRowStep;
-        const int x = kFlip && (i & 1) ? byte ^ 16 : byte;
+        const int x = byte_of(i);
         dma16(r < n && x < dim_bytes ? static_cast<const void*>(base + r * row_bytes + x)
                                      : static_cast<const void*>(g_attn_zeros),
               static_cast<lds_void*>(to + i * NW * 1024));
