@@ -797,13 +797,17 @@ typedef struct staple_attn_t {
 /* Forward: writes o and lse from q, k, v.  `a` is read during the call only.
  * A pair of cu_q or cu_k entries that is out of order or past the totals sets
  * the device error word, and that sequence counts as empty.  Rows in no
- * sequence are not written. */
-staple_status_t staple_attn_fwd(const staple_attn_t* a, void* stream);
+ * sequence are not written.  Workspace: where there are too few queries to
+ * occupy the GPU, long rows' keys are split and the parts' sums joined (else 0
+ * bytes). */
+size_t staple_attn_fwd_workspace_bytes(const staple_attn_t* a);
+staple_status_t staple_attn_fwd(const staple_attn_t* a, void* ws, size_t ws_bytes, void* stream);
 
 /* Backward: writes dq, dk, dv from d_o, the forward's operands and its o and
  * lse (gradients of shared key-value heads are summed over their query
- * heads).  Overwritten, not accumulated.  Workspace: delta = sum_d d_o o
- * (fp32, total_q x n_heads) and the partial dk, dv of the sinks' keys. */
+ * heads).  Overwritten, not accumulated.  Workspace: lse and delta = sum_d d_o
+ * o of every row (fp32), the order in which key tiles are worked off, and the
+ * partial dk, dv of those that many queries see. */
 size_t staple_attn_bwd_workspace_bytes(const staple_attn_t* a);
 staple_status_t staple_attn_bwd(const staple_attn_t* a, void* ws, size_t ws_bytes, void* stream);
 

@@ -36,7 +36,7 @@ BAD_ATTN = [
 def test_attention_refuses(L, change, status):
     a = attn(L, **change)
     lib = L.load()
-    assert lib.staple_attn_fwd(ctypes.byref(a), None) == status
+    assert lib.staple_attn_fwd(ctypes.byref(a), P, 1 << 40, None) == status
     assert lib.staple_attn_bwd(ctypes.byref(a), P, 1 << 40, None) == status
 
 
@@ -46,7 +46,7 @@ def test_attention_refuses_operands(L, which, bad):
     a = attn(L, **{which: L.Heads(*bad)})
     lib = L.load()
     if which in ("q", "k", "v", "o"):
-        assert lib.staple_attn_fwd(ctypes.byref(a), None) == -1
+        assert lib.staple_attn_fwd(ctypes.byref(a), P, 1 << 40, None) == -1
     assert lib.staple_attn_bwd(ctypes.byref(a), P, 1 << 40, None) == -1
 
 
@@ -57,10 +57,16 @@ def test_attention_workspace_and_empty_calls(L):
     assert need >= 4 * 4 * 4
     assert lib.staple_attn_bwd(ctypes.byref(a), P, need - 1, None) == -3
     assert lib.staple_attn_bwd(ctypes.byref(a), None, need, None) == -1
-    assert lib.staple_attn_fwd(None, None) == -1
+    long = attn(L, n_seqs=1, total_q=4, total_k=4096)
+    need = lib.staple_attn_fwd_workspace_bytes(ctypes.byref(long))
+    assert need > 0 and lib.staple_attn_fwd_workspace_bytes(None) == 0
+    assert lib.staple_attn_fwd_workspace_bytes(ctypes.byref(attn(L, n_seqs=1, total_q=4, total_k=64))) == 0
+    assert lib.staple_attn_fwd(ctypes.byref(long), P, need - 1, None) == -3
+    assert lib.staple_attn_fwd(ctypes.byref(long), None, need, None) == -1
+    assert lib.staple_attn_fwd(None, P, 1 << 40, None) == -1
     assert lib.staple_attn_bwd_workspace_bytes(None) == 0
-    assert lib.staple_attn_fwd(ctypes.byref(attn(L, n_seqs=0)), None) == 0
-    assert lib.staple_attn_fwd(ctypes.byref(attn(L, total_q=0)), None) == 0
+    assert lib.staple_attn_fwd(ctypes.byref(attn(L, n_seqs=0)), None, 0, None) == 0
+    assert lib.staple_attn_fwd(ctypes.byref(attn(L, total_q=0)), None, 0, None) == 0
     assert lib.staple_attn_bwd(ctypes.byref(attn(L, total_q=0, total_k=0)), None, 0, None) == 0
 
 

@@ -107,6 +107,49 @@ def test_window_attention_and_its_gradients(st, dtype, case):
         check(got[n], ref[n], bound[n], n)
 
 
+# few queries of many keys: the keys in parts
+LONG_CASES = [
+    ([1], [599], 1, 1, 64, 0, 0),
+    ([7], [2993], 2, 1, 128, 0, 0),
+    ([33, 1, 0, 2], [1500, 40, 300, 2100], 4, 2, 72, 0, 0),
+    ([20], [2500], 2, 2, 128, 1000, 300),
+    ([150], [1200], 1, 1, 128, 700, 64),
+    ([130, 40], [-100, 1800], 2, 1, 40, 0, 0),
+    ([1100], [0], 1, 1, 64, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", LONG_CASES, ids=lambda c: f"q{sum(c[0])}x{len(c[0])}-p{max(c[1])}-h{c[2]}_{c[3]}-d{c[4]}-w{c[5]}-s{c[6]}")
+def test_window_attention_few_queries_of_many_keys(st, dtype, case):
+    lq, past, h, hk, d, window, sinks = case
+    print(case, dtype, flush=True)
+    ops, lk, got = run_window(st, dtype, lq, past, h, hk, d, window, sinks, seed=20)
+    ref, bound = oracle_window(dtype, ops, lq, lk, h, hk, window, sinks, d ** -0.5)
+    for n in ref:
+        check(got[n], ref[n], bound[n], n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_attention_few_queries_never_read_a_hidden_key(st, dtype):
+    """Keys before the window and after the query hold NaN and infinities in parts of their own
+    and at the edges of others."""
+    import torch
+    lk, lq, h, d, window, sinks = 2600, 5, 2, 64, 900, 40
+    q, k, v = rand((lq, h, d), dtype, 60), rand((lk, 1, d), dtype, 61), rand((lk, 1, d), dtype, 62)
+    cq, ck = cu([lq]), cu([lk])
+    ref, bound = oracle_window(dtype, (q, k, v, torch.zeros_like(q)), [lq], [lk], h, 1, window, sinks, d ** -0.5)
+    want = st.staple_attn_fwd(q, k, v, cq, ck, window=window, sinks=sinks)
+    k[sinks:lk - lq + 1 - window], v[sinks:lk - lq + 1 - window] = float("nan"), float("inf")
+    got = st.staple_attn_fwd(q, k, v, cq, ck, window=window, sinks=sinks)
+    assert torch.equal(got["lse"], want["lse"])
+    for n in ("o", "lse"):
+        check(to_np(got[n]), ref[n], bound[n], n)
+    k[lk - 2], v[lk - 2] = float("nan"), float("nan")   # the last two queries see it, the others don't
+    got = st.staple_attn_fwd(q, k, v, cq, ck, window=window, sinks=sinks)
+    assert torch.isfinite(got["o"][:3]).all() and torch.isnan(got["o"][3:]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_window_attention_peaked_scores(st, dtype):
     """Scores of a few hundred: softmax rows that one key takes whole."""

@@ -867,7 +867,7 @@ def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, dq=None, d
 def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                     cu_k: torch.Tensor, *, window: int = 0, sinks: int = 0,
                     scale: Optional[float] = None, out: Optional[dict] = None,
-                    stream=None) -> dict:
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Causal attention of packed sequences: o [tokens, heads, head_dim] and lse
     [tokens, heads].  q [tokens, heads, head_dim]; k, v [key tokens, kv heads, head_dim]
     (strided views, such as slices of one fused projection, are read in place); cu_q, cu_k
@@ -877,7 +877,9 @@ def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     if out is None:
         out = {"o": q.new_empty(q.shape), "lse": q.new_empty(q.shape[:2], dtype=torch.float32)}
     a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"])
-    _check(lib().staple_attn_fwd(ctypes.byref(a), _stream(stream)), "staple_attn_fwd")
+    ws = _ws(lib().staple_attn_fwd_workspace_bytes(ctypes.byref(a)), workspace, q.device)
+    _check(lib().staple_attn_fwd(ctypes.byref(a), _p(ws), _ws_size(ws), _stream(stream)),
+           "staple_attn_fwd")
     return out
 
 

@@ -91,7 +91,8 @@ _SIGS = {
                                         c_vp, c_i64, c_vp]),
     "staple_host_adamw_finish": (c_i32, [c_vp, c_vp]),
     "staple_host_adamw_destroy": (None, [c_vp]),
-    "staple_attn_fwd": (c_i32, [c_vp, c_vp]),
+    "staple_attn_fwd_workspace_bytes": (c_sz, [c_vp]),
+    "staple_attn_fwd": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "staple_attn_bwd_workspace_bytes": (c_sz, [c_vp]),
     "staple_attn_bwd": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "staple_kv_append": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),

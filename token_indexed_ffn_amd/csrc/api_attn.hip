@@ -148,14 +148,21 @@ using namespace staple;
 extern "C" {
 
 // ------------------------------------------------------------------ attention
-staple_status_t staple_attn_fwd(const staple_attn_t* a, void* stream) {
+size_t staple_attn_fwd_workspace_bytes(const staple_attn_t* a) {
+  return attn_check(a) == STAPLE_OK ? attn_fwd_workspace_bytes(view(a), a->dtype) : 0;
+}
+staple_status_t staple_attn_fwd(const staple_attn_t* a, void* ws, size_t ws_bytes, void* stream) {
   CHECKED(attn_check(a));
   if (a->n_seqs == 0 || a->total_q == 0) return STAPLE_OK;
   REQUIRE(a->cu_q && a->cu_k && a->lse);
   REQUIRE(heads_ok(a->q, a->dtype) && heads_ok(a->o, a->dtype));
   REQUIRE(a->total_k == 0 || (heads_ok(a->k, a->dtype) && heads_ok(a->v, a->dtype)));
+  const AttnView v = view(a);
+  const size_t need = attn_fwd_workspace_bytes(v, a->dtype);
+  if (ws_bytes < need) return STAPLE_ERR_WORKSPACE;
+  REQUIRE(need == 0 || (ws && aligned16(ws)));
   GET_ERR(err);
-  HIPCALL(launch_attn_fwd(view(a), a->dtype, S(stream), err));
+  HIPCALL(launch_attn_fwd(v, a->dtype, ws, S(stream), err));
   return STAPLE_OK;
 }
 

@@ -25,7 +25,8 @@ struct AttnView {
 };
 
 size_t attn_bwd_workspace_bytes(const AttnView& a, int dtype);
-hipError_t launch_attn_fwd(const AttnView& a, int dtype, hipStream_t s, int* err);
+size_t attn_fwd_workspace_bytes(const AttnView& a, int dtype);
+hipError_t launch_attn_fwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err);
 hipError_t launch_attn_bwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err);
 
 struct DecodeView {

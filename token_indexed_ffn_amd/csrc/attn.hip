@@ -46,7 +46,7 @@ struct FwdShape {
   static constexpr int kLds = 8 * kBlock;   // rings of four K blocks and four V blocks
 };
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, FwdParts parts, int* err) {
   using T = bf16_t;
   using TL = Tile<T, DP>;
   constexpr int kBlock = FwdShape<DP>::kBlock;
@@ -55,8 +55,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
   lds_char* const vring = kring + 4 * kBlock;
   check_offsets(a, err);
   QueryCols w;
-  if (!w.find(a, kBf16RowsLog2, n_slots, blockIdx.x, wave_id(), err)) return;
-  const KeyBlocks keys = w.blocks(a);
+  const int tile = static_cast<int>(blockIdx.x) / parts.n, part = static_cast<int>(blockIdx.x) - tile * parts.n;
+  if (!w.find(a, kBf16RowsLog2, n_slots, tile, wave_id(), err)) return;
+  KeyBlocks keys = w.blocks(a);
+  int shares = 1;
+  if (parts.n > 1) {
+    shares = keys.share(parts.n, part);
+    if (part >= shares) return;
+  }
   f32x16_t o[TL::kDT] = {};
   ColumnSoftmax sm;
   if (keys.n > 0) {
@@ -164,7 +170,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
 #pragma unroll
       for (int x = 0; x < 2; ++x) o[d] = mma16(cols.read(x, d, 0), p0.v[x], o[d], T{});
   }
-  finish_fwd<T, DP>(a, w, sm, o);
+  if (shares == 1) return finish_fwd<T, DP>(a, w, sm, o);
+  if (w.wq >= w.nq) return;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + wave_id();
+  parts.put_rows(unit, sm.top, sm.sum + other_half(sm.sum));
+#pragma unroll
+  for (int d = 0; d < TL::kDT; ++d) parts.put<TL::kDT>(unit, d, o[d]);
 }
 
 // ------------------------------------------------------------------ backward
@@ -546,17 +557,25 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
 }
 
 // ------------------------------------------------------------------- launches
-template <bool kWide>
-static hipError_t fwd_launch(const AttnView& a, hipStream_t s, int* err) {
-  const int64_t n = tile_slots(a.total_q, a.n_seqs, kBf16RowsLog2), wgs = n * a.n_heads;
-  if (a.head_dim <= 64) return launch_lds<attn_fwd_bf16_kernel<64, kWide>, FwdShape<64>::kLds>(wgs, s, a, n, err);
-  return launch_lds<attn_fwd_bf16_kernel<128, kWide>, FwdShape<128>::kLds>(wgs, s, a, n, err);
+size_t attn_fwd_workspace_bytes(const AttnView& a, int dtype) {
+  return fwd_space(a, dtype == STAPLE_F32 ? kF32RowsLog2 : kBf16RowsLog2, nullptr).bytes;
 }
 
-hipError_t launch_attn_fwd(const AttnView& a, int dtype, hipStream_t s, int* err) {
-  if (dtype == STAPLE_F32) return launch_attn_fwd_f32(a, s, err);
-  return spans_buffer(a.k, a.total_k, 2) || spans_buffer(a.v, a.total_k, 2) ? fwd_launch<true>(a, s, err)
-                                                                            : fwd_launch<false>(a, s, err);
+template <int DP, bool kWide>
+static hipError_t fwd_launch(const AttnView& a, const FwdParts& parts, hipStream_t s, int* err) {
+  const int64_t n = tile_slots(a.total_q, a.n_seqs, kBf16RowsLog2);
+  const hipError_t e =
+      launch_lds<attn_fwd_bf16_kernel<DP, kWide>, FwdShape<DP>::kLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
+  if (e != hipSuccess || parts.n == 1) return e;
+  return launch_join<bf16_t, DP>(a, kBf16RowsLog2, n, parts, s, err);
+}
+
+hipError_t launch_attn_fwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
+  if (dtype == STAPLE_F32) return launch_attn_fwd_f32(a, ws, s, err);
+  const FwdParts parts = fwd_space(a, kBf16RowsLog2, ws).parts;
+  const bool far = spans_buffer(a.k, a.total_k, 2) || spans_buffer(a.v, a.total_k, 2);
+  if (a.head_dim <= 64) return far ? fwd_launch<64, true>(a, parts, s, err) : fwd_launch<64, false>(a, parts, s, err);
+  return far ? fwd_launch<128, true>(a, parts, s, err) : fwd_launch<128, false>(a, parts, s, err);
 }
 
 // A split tile has more than `chunk` blocks, so that all of them together have

@@ -75,7 +75,7 @@ __device__ __forceinline__ void join_waves(char* smem, const f32x16_t (&x)[N], f
 
 // ------------------------------------------------------------------- forward
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, FwdParts parts, int* err) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
   constexpr int kBlock = F32Shape<DP>::kBlock;
@@ -83,8 +83,14 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   __shared__ float tops[kWaves][32], sums[kWaves][32];
   check_offsets(a, err);
   QueryCols w;
-  if (!w.find(a, kF32RowsLog2, n_slots, blockIdx.x, 0, err)) return;
-  const KeyBlocks keys = w.blocks(a);
+  const int tile = static_cast<int>(blockIdx.x) / parts.n, part = static_cast<int>(blockIdx.x) - tile * parts.n;
+  if (!w.find(a, kF32RowsLog2, n_slots, tile, 0, err)) return;
+  KeyBlocks keys = w.blocks(a);
+  int shares = 1;
+  if (parts.n > 1) {
+    shares = keys.share(parts.n, part);
+    if (part >= shares) return;
+  }
   const int lane = threadIdx.x & 63, wave = wave_id();
   lds_char* const kt = (lds_char*)smem + wave * F32Shape<DP>::kPerWave;
   lds_char* const vt = kt + kBlock;
@@ -135,25 +141,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   float top = -INFINITY, total = 0.0f;
 #pragma unroll
   for (int u = 0; u < kWaves; ++u) top = fmaxf(top, tops[u][lane & 31]);
-  auto factor = [&](float t, float x) { return t == -INFINITY && x == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(t - top); };
 #pragma unroll
-  for (int u = 0; u < kWaves; ++u) total += sums[u][lane & 31] * factor(tops[u][lane & 31], sums[u][lane & 31]);
+  for (int u = 0; u < kWaves; ++u) total += sums[u][lane & 31] * rebase(tops[u][lane & 31], sums[u][lane & 31], top);
   constexpr int kOut = (TL::kDT + kWaves - 1) / kWaves;
   f32x16_t out[kOut];
-  join_waves<DP>(smem, o, factor(sm.top, sum), out);
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  bool bad = false;
+  join_waves<DP>(smem, o, rebase(sm.top, sum, top), out);
+  if (shares == 1) return finish_dims<F32, DP>(a, w, kWaves, top, total, out);
+  if (wave == 0) parts.put_rows(blockIdx.x, top, total);
 #pragma unroll
-  for (int i = 0; i < kOut; ++i) {
-    const int d = i * kWaves + wave;
-    if (d >= TL::kDT) continue;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
-    store_column<F32>(a.o, w.q0 + w.row, w.head, a.head_dim, d, out[i], inv, w.in);
-  }
-  if (wave == 0 && w.in && lane < 32) a.lse[(w.q0 + w.row) * a.n_heads + w.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
-  __syncthreads();   // a row done again is stored after all its parts
-  redo_queries(bad && w.in, [&](int i) { attn_fwd_row<F32>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  for (int i = 0; i < kOut; ++i)
+    if (i * kWaves + wave < TL::kDT) parts.put<TL::kDT>(blockIdx.x, i * kWaves + wave, out[i]);
 }
 
 // ------------------------------------------------------------------ backward
@@ -343,15 +340,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
 
 // ------------------------------------------------------------------- launches
 template <int DP, bool kWide>
-static hipError_t fwd_launch(const AttnView& a, hipStream_t s, int* err) {
+static hipError_t fwd_launch(const AttnView& a, const FwdParts& parts, hipStream_t s, int* err) {
   const int64_t n = tile_slots(a.total_q, a.n_seqs, kF32RowsLog2);
-  return launch_lds<attn_fwd_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads, s, a, n, err);
+  const hipError_t e =
+      launch_lds<attn_fwd_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
+  if (e != hipSuccess || parts.n == 1) return e;
+  return launch_join<F32, DP>(a, kF32RowsLog2, n, parts, s, err);
 }
 
-hipError_t launch_attn_fwd_f32(const AttnView& a, hipStream_t s, int* err) {
+hipError_t launch_attn_fwd_f32(const AttnView& a, void* ws, hipStream_t s, int* err) {
+  const FwdParts parts = fwd_space(a, kF32RowsLog2, ws).parts;
   const bool far = spans_buffer(a.k, a.total_k, 4) || spans_buffer(a.v, a.total_k, 4);
-  if (a.head_dim <= 64) return far ? fwd_launch<64, true>(a, s, err) : fwd_launch<64, false>(a, s, err);
-  return far ? fwd_launch<128, true>(a, s, err) : fwd_launch<128, false>(a, s, err);
+  if (a.head_dim <= 64) return far ? fwd_launch<64, true>(a, parts, s, err) : fwd_launch<64, false>(a, parts, s, err);
+  return far ? fwd_launch<128, true>(a, parts, s, err) : fwd_launch<128, false>(a, parts, s, err);
 }
 
 template <int DP, bool kWide>

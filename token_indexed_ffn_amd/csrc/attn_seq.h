@@ -8,6 +8,7 @@
 namespace staple {
 
 constexpr int kWaves = 4;   // of a workgroup, unless said otherwise
+constexpr int kF32RowsLog2 = 5, kBf16RowsLog2 = 7;   // queries (keys) of a workgroup's tile: 32 in fp32, 128 in bf16
 
 // A tile of 2^rows_log2 consecutive rows of one sequence.  Sequence b owns the
 // slots floor(cu[b] / rows) + b onwards, at least as many as it has tiles, so a
@@ -103,12 +104,17 @@ struct SeenBy {
 // True where a value is NaN or infinite.
 __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
 
+// Blocks of a part of a tile's keys, at least.  256 queries after 2000 keys, 8
+// heads of 64, take 31 us in parts of 8; 37 of 4, 33 of 16; 8 x 16 queries
+// after 600 keys 33; 33, 40.
+constexpr int kMinShare = 8;
+
 // The 32-key blocks that some query at a position in [p_min, p_max] sees: those
 // of the sinks, then the window's; and which of them every query of the wave's
 // range sees whole.
 struct KeyBlocks {
   int n_sink, lo, n;
-  int nk;
+  int nk, skip = 0;
   int whole_sink, whole_lo, whole_n;
   __device__ __forceinline__ KeyBlocks(const AttnView& a, int n_keys, int p_min, int p_max) : nk(n_keys) {
     lo = (a.window > 0 ? max(p_min - a.window + 1, 0) : 0) / 32;
@@ -128,8 +134,21 @@ struct KeyBlocks {
   __device__ __forceinline__ bool whole(int b) const {
     return b < whole_sink || static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
   }
+  // Keeps share `part` of at most `parts`, of kMinShare blocks at least; returns
+  // how many there are.
+  __device__ __forceinline__ int share(int parts, int part) {
+    const int chunk = max((n + parts - 1) / parts, kMinShare);
+    const int shares = max((n + chunk - 1) / chunk, 1);
+    skip = min(part * chunk, n);
+    n = min(chunk, n - skip);
+    n_sink -= skip;
+    whole_sink = min(whole_sink - skip, n);
+    whole_lo -= skip;
+    whole_n = max(min(whole_n, n - whole_lo), 0);
+    return shares;
+  }
   // First key of block b; blocks past the last lie past the keys.
-  __device__ __forceinline__ int first(int b) const { return b < n ? (b < n_sink ? b : lo + b - n_sink) * 32 : nk; }
+  __device__ __forceinline__ int first(int b) const { return b < n ? (b < n_sink ? b + skip : lo + b - n_sink) * 32 : nk; }
 };
 
 // The wave's 32 queries, one a column.
@@ -238,6 +257,110 @@ __device__ __forceinline__ void redo_queries(bool bad, RowFn row) {
     again &= again - 1;
     row(i);
   }
+}
+
+// A tile's keys in parts, where there are too few tiles to occupy the GPU: each
+// part is a workgroup and leaves its sums, relative to its own reference, and
+// attn_join_kernel adds them in part order.  Calls of bf16 and dim 128 measured
+// in parts, and with a workgroup a tile:
+//   16 queries after 14000 keys, 16 heads on 4: 57 us; 388 us
+//   512 queries after 8000 keys, 16 heads on 4: 74 us; 178 us
+//   2048 queries, 4 heads: 41 us; 56 us
+//   8 sequences of 16 queries after 600 keys, 4 heads: 33 us; 36 us
+struct FwdParts {
+  int n;         // at most so many of a tile
+  f32x4_t* o;    // [tiles][heads][parts][32s of queries][32s of dims][4][64]: sums as they lie in a wave
+  float* rows;   // [tiles][heads][parts][32s of queries][2][32]: reference and sum
+  // unit: a part's number times the tile's 32s of queries, plus one of these
+  __device__ __forceinline__ void put_rows(int64_t unit, float top, float sum) const {
+    const int lane = threadIdx.x & 63;
+    if (lane < 32) {
+      rows[unit * 64 + lane] = top;
+      rows[unit * 64 + 32 + lane] = sum;
+    }
+  }
+  template <int kDT>
+  __device__ __forceinline__ void put(int64_t unit, int d, const f32x16_t& x) const {
+    f32x4_t* to = o + (unit * kDT + d) * 256 + (threadIdx.x & 63);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) to[g * 64] = f32x4_t{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+  }
+};
+
+// What a sum relative to `top` is worth relative to `all`, the largest.
+__device__ __forceinline__ float rebase(float top, float sum, float all) {
+  return top == -INFINITY && sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(top - all);
+}
+
+// The end of 32 queries' forward, by the waves that have some of their dims
+// each (every kWaves-th 32, kOut at most); `total`: the sum of the weights.
+template <typename T, int DP, int kOut>
+__device__ __forceinline__ void finish_dims(const AttnView& a, const QueryCols& w, int n_waves, float top, float total,
+                                            const f32x16_t (&out)[kOut]) {
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) {
+    const int d = i * n_waves + wave_id();
+    if (d >= Tile<T, DP>::kDT) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
+    store_column<T>(a.o, w.q0 + w.row, w.head, a.head_dim, d, out[i], inv, w.in);
+  }
+  if (wave_id() == 0 && w.in && (threadIdx.x & 63) < 32)
+    a.lse[(w.q0 + w.row) * a.n_heads + w.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
+  __syncthreads();   // a row done again is stored after all its parts
+  redo_queries(bad && w.in, [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+}
+
+// 32 queries of a tile in parts a workgroup, 32 dims a wave.
+template <typename T, int DP>
+__global__ __launch_bounds__(2 * DP) void attn_join_kernel(AttnView a, int rows_log2, int64_t n_slots, FwdParts parts, int* err) {
+  constexpr int kDT = Tile<T, DP>::kDT;
+  const int groups = 1 << (rows_log2 - 5), lane = threadIdx.x & 63;
+  const int64_t tile = blockIdx.x / groups;
+  const int group = static_cast<int>(blockIdx.x - tile * groups);
+  QueryCols w;
+  if (!w.find(a, rows_log2, n_slots, tile, group, err) || w.wq >= w.nq) return;
+  const int n = w.blocks(a).share(parts.n, 0);
+  if (n == 1) return;   // stored already
+  const int64_t unit = tile * parts.n * groups + group;
+  const float* const tops = parts.rows + unit * 64 + (lane & 31);
+  const f32x4_t* const from = parts.o + (unit * kDT + wave_id()) * 256 + lane;
+  // a batch of parts at a time: what it costs is waiting for their loads
+  constexpr int kBatch = 8;
+  float top = -INFINITY, total = 0.0f;
+  f32x16_t out[1] = {};
+  for (int u0 = 0; u0 < n; u0 += kBatch) {
+    float t[kBatch], sum[kBatch];
+    f32x4_t v[kBatch][4];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t u = static_cast<int64_t>(min(u0 + i, n - 1)) * groups;
+      t[i] = tops[u * 64];
+      sum[i] = tops[u * 64 + 32];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) v[i][g] = from[u * kDT * 256 + g * 64];
+    }
+    float all = top;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) all = fmaxf(all, t[i]);
+    const float keep = rebase(top, total, all);
+    top = all;
+    total *= keep;
+    out[0] *= keep;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (u0 + i >= n) break;
+      const float f = rebase(t[i], sum[i], top);
+      total += sum[i] * f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[0][4 * g + e] += v[i][g][e] * f;
+    }
+  }
+  finish_dims<T, DP, 1>(a, w, kDT, top, total, out);
 }
 
 // ------------------------------------------------------------------ backward
@@ -516,6 +639,41 @@ inline hipError_t launch_lds(int64_t wgs, hipStream_t s, Args... args) {
   return hipGetLastError();
 }
 
+// How many parts a tile's keys are split into: as many as make two workgroups a
+// CU, if there are keys for them.  The lengths are on the device; the longest
+// sequence is taken to have up to four times the mean.
+inline int fwd_parts(const AttnView& a, int rows_log2) {
+  const int64_t wgs = tile_slots(a.total_q, a.n_seqs, rows_log2) * a.n_heads;
+  if (wgs == 0) return 1;
+  int64_t keys = a.n_seqs > 4 ? 4 * (a.total_k / a.n_seqs) : a.total_k;
+  const int64_t window = a.window + (int64_t(1) << rows_log2) + a.sinks;
+  if (a.window > 0 && window < keys) keys = window;
+  int64_t parts = 2 * device_cus() / wgs;
+  if (parts > keys / (32 * kMinShare)) parts = keys / (32 * kMinShare);
+  return parts < 2 ? 1 : static_cast<int>(parts);
+}
+struct FwdSpace {
+  FwdParts parts;
+  size_t bytes;
+};
+inline FwdSpace fwd_space(const AttnView& a, int rows_log2, void* ws) {
+  FwdSpace f{};
+  f.parts.n = fwd_parts(a, rows_log2);
+  if (f.parts.n == 1) return f;
+  const size_t units = static_cast<size_t>(tile_slots(a.total_q, a.n_seqs, rows_log2) * a.n_heads * f.parts.n) << (rows_log2 - 5);
+  Workspace w(ws, ~size_t(0));
+  f.parts.o = w.take<f32x4_t>(units * (a.head_dim <= 64 ? 64 : 128) * 32 * sizeof(float));
+  f.parts.rows = w.take<float>(units * 64 * sizeof(float));
+  f.bytes = w.used;
+  return f;
+}
+template <typename T, int DP>
+inline hipError_t launch_join(const AttnView& a, int rows_log2, int64_t n_slots, const FwdParts& parts, hipStream_t s, int* err) {
+  attn_join_kernel<T, DP><<<static_cast<unsigned>((n_slots * a.n_heads) << (rows_log2 - 5)), 2 * DP, 0, s>>>(a, rows_log2, n_slots,
+                                                                                                            parts, err);
+  return hipGetLastError();
+}
+
 // Whether a head's rows may span 2^31 bytes.
 inline bool spans_buffer(const HeadsView& t, int64_t rows, int elem_bytes) {
   return t.row_stride >= (int64_t(1) << 31) / elem_bytes / (rows + 256);
@@ -531,9 +689,7 @@ struct BwdSpace {
 };
 
 // kernels of fp32 (attn_f32.hip)
-hipError_t launch_attn_fwd_f32(const AttnView& a, hipStream_t s, int* err);
+hipError_t launch_attn_fwd_f32(const AttnView& a, void* ws, hipStream_t s, int* err);
 hipError_t launch_attn_bwd_f32(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err);
-constexpr int kF32RowsLog2 = 5;    // queries (keys) of a workgroup's tile: 32 in fp32,
-constexpr int kBf16RowsLog2 = 7;   // 128 in bf16
 
 }  // namespace staple
