@@ -46,7 +46,7 @@ struct FwdShape {
   static constexpr int kLds = 8 * kBlock;   // rings of four K blocks and four V blocks
 };
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, FwdParts parts, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
   using T = bf16_t;
   using TL = Tile<T, DP>;
   constexpr int kBlock = FwdShape<DP>::kBlock;
@@ -190,8 +190,8 @@ struct DqShape {
   static constexpr int kLds = (kKSlots + kVSlots) * kBlock;
 };
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a, int64_t n_slots, RowStats stats, DkvPlan plan,
-                                                                      int* err) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a, int64_t n_slots, KeyParts parts, RowStats stats,
+                                                                      DkvPlan plan, int* err) {
   using T = bf16_t;
   using TL = Tile<T, DP>;
   using Shape = DqShape<DP>;
@@ -207,8 +207,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
     plan_dkv(a, plan, err);
     return;
   }
-  if (!w.find(a, kBf16RowsLog2, n_slots, static_cast<int64_t>(blockIdx.x) - 1, wave_id(), err)) return;
-  const KeyBlocks keys = w.blocks(a);
+  const int id = static_cast<int>(blockIdx.x) - 1, tile = id / parts.n, part = id - tile * parts.n;
+  if (!w.find(a, kBf16RowsLog2, n_slots, tile, wave_id(), err)) return;
+  KeyBlocks keys = w.blocks(a);
+  const bool few = keys.n <= kFew;
+  int shares = 1;
+  if (parts.n > 1) {
+    shares = keys.share(parts.n, part);
+    if (part >= shares) return;
+  }
   const int half = (threadIdx.x & 63) >> 5;
   Loader kl, vl;
   kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim, wave_id());
@@ -231,7 +238,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
   // where o is large: where few keys share a query's weight.  A workgroup of
   // few blocks therefore meets them once before, for delta + sum P (dP -
   // delta), exact as sum P = 1.
-  if (keys.n <= kFew) {
+  static_assert(kFew <= kMinShare, "all of the tile's blocks are here");
+  if (few) {
     float more = 0.0f;
     for (int b = 0; b < keys.n; ++b) {
       kl.load(keys.first(b), kring);
@@ -254,7 +262,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
     }
     delta += more + other_half(more);
   }
-  if (w.in && half == 0) {
+  if (part == 0 && w.in && half == 0) {
     stats.lse2[w.head * a.total_q + w.q0 + w.row] = lse2;
     stats.delta[w.head * a.total_q + w.q0 + w.row] = delta;
   }
@@ -334,6 +342,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
     for (int d = 0; d < TL::kDT; ++d) dq[d] = mma_transposed<DP>(kprev, 0, d, prev, dq[d]);
   }
   wait_vmcnt<0>();   // no load into LDS outlives the workgroup
+  if (shares > 1) {
+    if (w.wq >= w.nq) return;
+#pragma unroll
+    for (int d = 0; d < TL::kDT; ++d) parts.put<TL::kDT>(static_cast<int64_t>(id) * kWaves + wave_id(), d, dq[d]);
+    return;
+  }
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < TL::kDT; ++d) {
@@ -558,21 +572,23 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
 
 // ------------------------------------------------------------------- launches
 size_t attn_fwd_workspace_bytes(const AttnView& a, int dtype) {
-  return fwd_space(a, dtype == STAPLE_F32 ? kF32RowsLog2 : kBf16RowsLog2, nullptr).bytes;
+  Workspace w(nullptr, ~size_t(0));
+  take_parts(a, dtype == STAPLE_F32 ? kF32RowsLog2 : kBf16RowsLog2, w);
+  return w.used;
 }
 
 template <int DP, bool kWide>
-static hipError_t fwd_launch(const AttnView& a, const FwdParts& parts, hipStream_t s, int* err) {
+static hipError_t fwd_launch(const AttnView& a, const KeyParts& parts, hipStream_t s, int* err) {
   const int64_t n = tile_slots(a.total_q, a.n_seqs, kBf16RowsLog2);
   const hipError_t e =
       launch_lds<attn_fwd_bf16_kernel<DP, kWide>, FwdShape<DP>::kLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
-  if (e != hipSuccess || parts.n == 1) return e;
-  return launch_join<bf16_t, DP>(a, kBf16RowsLog2, n, parts, s, err);
+  return e != hipSuccess ? e : launch_join<bf16_t, DP, false>(a, kBf16RowsLog2, n, parts, s, err);
 }
 
 hipError_t launch_attn_fwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {
   if (dtype == STAPLE_F32) return launch_attn_fwd_f32(a, ws, s, err);
-  const FwdParts parts = fwd_space(a, kBf16RowsLog2, ws).parts;
+  Workspace w(ws, ~size_t(0));
+  const KeyParts parts = take_parts(a, kBf16RowsLog2, w);
   const bool far = spans_buffer(a.k, a.total_k, 2) || spans_buffer(a.v, a.total_k, 2);
   if (a.head_dim <= 64) return far ? fwd_launch<64, true>(a, parts, s, err) : fwd_launch<64, false>(a, parts, s, err);
   return far ? fwd_launch<128, true>(a, parts, s, err) : fwd_launch<128, false>(a, parts, s, err);
@@ -605,6 +621,7 @@ static BwdSpace bwd_space(const AttnView& a, int dtype, void* ws) {
   b.plan.done = w.take<int32_t>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sizeof(int32_t));
   const size_t sums = (size_t(2) << b.plan.rows_log2) * dp * sizeof(float);   // dk and dv of a tile
   b.plan.sums = w.take<float>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sums);
+  b.parts = take_parts(a, b.plan.rows_log2, w);
   b.bytes = w.used;
   return b;
 }
@@ -614,7 +631,10 @@ template <int DP, bool kWide>
 static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {
   const int64_t nq = tile_slots(a.total_q, a.n_seqs, kBf16RowsLog2);
   // one workgroup more than there are query tiles: it makes the plan
-  hipError_t e = launch_lds<attn_dq_bf16_kernel<DP, kWide>, DqShape<DP>::kLds>(nq * a.n_heads + 1, s, a, nq, b.stats, b.plan, err);
+  hipError_t e = launch_lds<attn_dq_bf16_kernel<DP, kWide>, DqShape<DP>::kLds>(nq * a.n_heads * b.parts.n + 1, s, a, nq, b.parts,
+                                                                                 b.stats, b.plan, err);
+  if (e != hipSuccess) return e;
+  e = launch_join<bf16_t, DP, true>(a, kBf16RowsLog2, nq, b.parts, s, err);
   if (e != hipSuccess) return e;
   const int64_t items = (b.plan.n_slots + b.max_parts) * a.n_kv_heads;   // at most
   return launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan, err);

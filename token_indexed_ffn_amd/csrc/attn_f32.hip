@@ -75,7 +75,7 @@ __device__ __forceinline__ void join_waves(char* smem, const f32x16_t (&x)[N], f
 
 // ------------------------------------------------------------------- forward
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, FwdParts parts, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
   constexpr int kBlock = F32Shape<DP>::kBlock;
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
 
 // ------------------------------------------------------------------ backward
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a, int64_t n_slots, RowStats stats, DkvPlan plan,
-                                                                     int* err) {
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, RowStats stats,
+                                                                     DkvPlan plan, int* err) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
   constexpr int kBlock = F32Shape<DP>::kBlock;
@@ -167,8 +167,14 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a,
     return;
   }
   QueryCols w;
-  if (!w.find(a, kF32RowsLog2, n_slots, static_cast<int64_t>(blockIdx.x) - 1, 0, err)) return;
-  const KeyBlocks keys = w.blocks(a);
+  const int id = static_cast<int>(blockIdx.x) - 1, tile = id / parts.n, part = id - tile * parts.n;
+  if (!w.find(a, kF32RowsLog2, n_slots, tile, 0, err)) return;
+  KeyBlocks keys = w.blocks(a);
+  int shares = 1;
+  if (parts.n > 1) {
+    shares = keys.share(parts.n, part);
+    if (part >= shares) return;
+  }
   const int lane = threadIdx.x & 63, wave = wave_id();
   lds_char* const kt = (lds_char*)smem + wave * F32Shape<DP>::kPerWave;
   lds_char* const vt = kt + kBlock;
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a,
   delta += other_half(delta);
   const float lse = w.in ? a.lse[(w.q0 + w.row) * a.n_heads + w.head] : 0.0f;
   const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
-  if (wave == 0 && w.in && lane < 32) {
+  if (wave == 0 && part == 0 && w.in && lane < 32) {
     stats.lse2[w.head * a.total_q + w.q0 + w.row] = lse2;
     stats.delta[w.head * a.total_q + w.q0 + w.row] = delta;
   }
@@ -220,17 +226,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a,
   constexpr int kOut = (TL::kDT + kWaves - 1) / kWaves;
   f32x16_t out[kOut];
   join_waves<DP>(smem, dq, 1.0f, out);
-  bool bad = false;
+  if (shares == 1) return finish_dq_dims<F32, DP>(a, w, kWaves, out);
 #pragma unroll
-  for (int i = 0; i < kOut; ++i) {
-    const int d = i * kWaves + wave;
-    if (d >= TL::kDT) continue;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
-    store_column<F32>(a.dq, w.q0 + w.row, w.head, a.head_dim, d, out[i], a.scale, w.in);
-  }
-  __syncthreads();
-  redo_queries(bad && w.in, [&](int i) { attn_dq_row<F32>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  for (int i = 0; i < kOut; ++i)
+    if (i * kWaves + wave < TL::kDT) parts.put<TL::kDT>(id, i * kWaves + wave, out[i]);
 }
 
 template <int DP, bool kWide>
@@ -340,16 +339,16 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
 
 // ------------------------------------------------------------------- launches
 template <int DP, bool kWide>
-static hipError_t fwd_launch(const AttnView& a, const FwdParts& parts, hipStream_t s, int* err) {
+static hipError_t fwd_launch(const AttnView& a, const KeyParts& parts, hipStream_t s, int* err) {
   const int64_t n = tile_slots(a.total_q, a.n_seqs, kF32RowsLog2);
   const hipError_t e =
       launch_lds<attn_fwd_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
-  if (e != hipSuccess || parts.n == 1) return e;
-  return launch_join<F32, DP>(a, kF32RowsLog2, n, parts, s, err);
+  return e != hipSuccess ? e : launch_join<F32, DP, false>(a, kF32RowsLog2, n, parts, s, err);
 }
 
 hipError_t launch_attn_fwd_f32(const AttnView& a, void* ws, hipStream_t s, int* err) {
-  const FwdParts parts = fwd_space(a, kF32RowsLog2, ws).parts;
+  Workspace w(ws, ~size_t(0));
+  const KeyParts parts = take_parts(a, kF32RowsLog2, w);
   const bool far = spans_buffer(a.k, a.total_k, 4) || spans_buffer(a.v, a.total_k, 4);
   if (a.head_dim <= 64) return far ? fwd_launch<64, true>(a, parts, s, err) : fwd_launch<64, false>(a, parts, s, err);
   return far ? fwd_launch<128, true>(a, parts, s, err) : fwd_launch<128, false>(a, parts, s, err);
@@ -359,7 +358,10 @@ template <int DP, bool kWide>
 static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {
   const int64_t n = tile_slots(a.total_q, a.n_seqs, kF32RowsLog2);
   // one workgroup more than there are query tiles: it makes the plan
-  hipError_t e = launch_lds<attn_dq_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads + 1, s, a, n, b.stats, b.plan, err);
+  hipError_t e = launch_lds<attn_dq_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads * b.parts.n + 1, s, a, n, b.parts,
+                                                                               b.stats, b.plan, err);
+  if (e != hipSuccess) return e;
+  e = launch_join<F32, DP, true>(a, kF32RowsLog2, n, b.parts, s, err);
   if (e != hipSuccess) return e;
   const int64_t items = (b.plan.n_slots + b.max_parts) * a.n_kv_heads;   // at most
   return launch_lds<attn_dkv_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(items, s, a, b.stats, b.plan, err);

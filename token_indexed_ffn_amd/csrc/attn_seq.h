@@ -260,14 +260,16 @@ __device__ __forceinline__ void redo_queries(bool bad, RowFn row) {
 }
 
 // A tile's keys in parts, where there are too few tiles to occupy the GPU: each
-// part is a workgroup and leaves its sums, relative to its own reference, and
-// attn_join_kernel adds them in part order.  Calls of bf16 and dim 128 measured
-// in parts, and with a workgroup a tile:
+// part is a workgroup of the forward (dq) and leaves its sums, the forward's
+// relative to its own reference, and attn_join_kernel adds them in part order.
+// Calls of bf16 and dim 128 measured in parts, and with a workgroup a tile:
 //   16 queries after 14000 keys, 16 heads on 4: 57 us; 388 us
 //   512 queries after 8000 keys, 16 heads on 4: 74 us; 178 us
 //   2048 queries, 4 heads: 41 us; 56 us
 //   8 sequences of 16 queries after 600 keys, 4 heads: 33 us; 36 us
-struct FwdParts {
+//   backward of 4096 queries, 1 head: 143 us; 245 us
+//   backward of 2048 queries, 4 heads: 153 us; 196 us
+struct KeyParts {
   int n;         // at most so many of a tile
   f32x4_t* o;    // [tiles][heads][parts][32s of queries][32s of dims][4][64]: sums as they lie in a wave
   float* rows;   // [tiles][heads][parts][32s of queries][2][32]: reference and sum
@@ -313,56 +315,6 @@ __device__ __forceinline__ void finish_dims(const AttnView& a, const QueryCols& 
   redo_queries(bad && w.in, [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
 }
 
-// 32 queries of a tile in parts a workgroup, 32 dims a wave.
-template <typename T, int DP>
-__global__ __launch_bounds__(2 * DP) void attn_join_kernel(AttnView a, int rows_log2, int64_t n_slots, FwdParts parts, int* err) {
-  constexpr int kDT = Tile<T, DP>::kDT;
-  const int groups = 1 << (rows_log2 - 5), lane = threadIdx.x & 63;
-  const int64_t tile = blockIdx.x / groups;
-  const int group = static_cast<int>(blockIdx.x - tile * groups);
-  QueryCols w;
-  if (!w.find(a, rows_log2, n_slots, tile, group, err) || w.wq >= w.nq) return;
-  const int n = w.blocks(a).share(parts.n, 0);
-  if (n == 1) return;   // stored already
-  const int64_t unit = tile * parts.n * groups + group;
-  const float* const tops = parts.rows + unit * 64 + (lane & 31);
-  const f32x4_t* const from = parts.o + (unit * kDT + wave_id()) * 256 + lane;
-  // a batch of parts at a time: what it costs is waiting for their loads
-  constexpr int kBatch = 8;
-  float top = -INFINITY, total = 0.0f;
-  f32x16_t out[1] = {};
-  for (int u0 = 0; u0 < n; u0 += kBatch) {
-    float t[kBatch], sum[kBatch];
-    f32x4_t v[kBatch][4];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int64_t u = static_cast<int64_t>(min(u0 + i, n - 1)) * groups;
-      t[i] = tops[u * 64];
-      sum[i] = tops[u * 64 + 32];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) v[i][g] = from[u * kDT * 256 + g * 64];
-    }
-    float all = top;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) all = fmaxf(all, t[i]);
-    const float keep = rebase(top, total, all);
-    top = all;
-    total *= keep;
-    out[0] *= keep;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (u0 + i >= n) break;
-      const float f = rebase(t[i], sum[i], top);
-      total += sum[i] * f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[0][4 * g + e] += v[i][g][e] * f;
-    }
-  }
-  finish_dims<T, DP, 1>(a, w, kDT, top, total, out);
-}
-
 // ------------------------------------------------------------------ backward
 // One query's row of dq, by a whole wave.
 template <typename T>
@@ -385,6 +337,81 @@ __device__ __forceinline__ void attn_dq_row(const AttnView& a, int64_t t, int64_
   dq.x[0] *= a.scale;
   dq.x[1] *= a.scale;
   store_row<T>(a.dq, t, h, a.head_dim, dq);
+}
+
+// The end of 32 queries' dq; see finish_dims.
+template <typename T, int DP, int kOut>
+__device__ __forceinline__ void finish_dq_dims(const AttnView& a, const QueryCols& w, int n_waves, const f32x16_t (&out)[kOut]) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) {
+    const int d = i * n_waves + wave_id();
+    if (d >= Tile<T, DP>::kDT) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
+    store_column<T>(a.dq, w.q0 + w.row, w.head, a.head_dim, d, out[i], a.scale, w.in);
+  }
+  __syncthreads();
+  redo_queries(bad && w.in, [&](int i) { attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+}
+
+// 32 queries of a tile in parts a workgroup, 32 dims a wave.  kGrad: dq, whose
+// parts need no weights.
+template <typename T, int DP, bool kGrad>
+__global__ __launch_bounds__(2 * DP) void attn_join_kernel(AttnView a, int rows_log2, int64_t n_slots, KeyParts parts, int* err) {
+  constexpr int kDT = Tile<T, DP>::kDT;
+  const int groups = 1 << (rows_log2 - 5), lane = threadIdx.x & 63;
+  const int64_t tile = blockIdx.x / groups;
+  const int group = static_cast<int>(blockIdx.x - tile * groups);
+  QueryCols w;
+  if (!w.find(a, rows_log2, n_slots, tile, group, err) || w.wq >= w.nq) return;
+  const int n = w.blocks(a).share(parts.n, 0);
+  if (n == 1) return;   // stored already
+  const int64_t unit = tile * parts.n * groups + group;
+  const float* const tops = parts.rows + unit * 64 + (lane & 31);
+  const f32x4_t* const from = parts.o + (unit * kDT + wave_id()) * 256 + lane;
+  // a batch of parts at a time: what it costs is waiting for their loads
+  constexpr int kBatch = 8;
+  float top = -INFINITY, total = 0.0f;
+  f32x16_t out[1] = {};
+  for (int u0 = 0; u0 < n; u0 += kBatch) {
+    float t[kBatch], sum[kBatch];
+    f32x4_t v[kBatch][4];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t u = static_cast<int64_t>(min(u0 + i, n - 1)) * groups;
+      if constexpr (!kGrad) {
+        t[i] = tops[u * 64];
+        sum[i] = tops[u * 64 + 32];
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) v[i][g] = from[u * kDT * 256 + g * 64];
+    }
+    if constexpr (!kGrad) {
+      float all = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) all = fmaxf(all, t[i]);
+      const float keep = rebase(top, total, all);
+      top = all;
+      total *= keep;
+      out[0] *= keep;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // past the last part: that one again, times zero
+      float f = u0 + i < n ? 1.0f : 0.0f;
+      if constexpr (!kGrad) {
+        f *= rebase(t[i], sum[i], top);
+        total += sum[i] * f;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[0][4 * g + e] += v[i][g][e] * f;
+    }
+  }
+  if constexpr (kGrad) finish_dq_dims<T, DP, 1>(a, w, kDT, out);
+  else finish_dims<T, DP, 1>(a, w, kDT, top, total, out);
 }
 
 // One key's rows of dk and dv, by a whole wave.
@@ -642,7 +669,7 @@ inline hipError_t launch_lds(int64_t wgs, hipStream_t s, Args... args) {
 // How many parts a tile's keys are split into: as many as make two workgroups a
 // CU, if there are keys for them.  The lengths are on the device; the longest
 // sequence is taken to have up to four times the mean.
-inline int fwd_parts(const AttnView& a, int rows_log2) {
+inline int key_parts(const AttnView& a, int rows_log2) {
   const int64_t wgs = tile_slots(a.total_q, a.n_seqs, rows_log2) * a.n_heads;
   if (wgs == 0) return 1;
   int64_t keys = a.n_seqs > 4 ? 4 * (a.total_k / a.n_seqs) : a.total_k;
@@ -652,25 +679,19 @@ inline int fwd_parts(const AttnView& a, int rows_log2) {
   if (parts > keys / (32 * kMinShare)) parts = keys / (32 * kMinShare);
   return parts < 2 ? 1 : static_cast<int>(parts);
 }
-struct FwdSpace {
-  FwdParts parts;
-  size_t bytes;
-};
-inline FwdSpace fwd_space(const AttnView& a, int rows_log2, void* ws) {
-  FwdSpace f{};
-  f.parts.n = fwd_parts(a, rows_log2);
-  if (f.parts.n == 1) return f;
-  const size_t units = static_cast<size_t>(tile_slots(a.total_q, a.n_seqs, rows_log2) * a.n_heads * f.parts.n) << (rows_log2 - 5);
-  Workspace w(ws, ~size_t(0));
-  f.parts.o = w.take<f32x4_t>(units * (a.head_dim <= 64 ? 64 : 128) * 32 * sizeof(float));
-  f.parts.rows = w.take<float>(units * 64 * sizeof(float));
-  f.bytes = w.used;
-  return f;
+inline KeyParts take_parts(const AttnView& a, int rows_log2, Workspace& w) {
+  KeyParts p{key_parts(a, rows_log2), nullptr, nullptr};
+  if (p.n == 1) return p;
+  const size_t units = static_cast<size_t>(tile_slots(a.total_q, a.n_seqs, rows_log2) * a.n_heads * p.n) << (rows_log2 - 5);
+  p.o = w.take<f32x4_t>(units * (a.head_dim <= 64 ? 64 : 128) * 32 * sizeof(float));
+  p.rows = w.take<float>(units * 64 * sizeof(float));
+  return p;
 }
-template <typename T, int DP>
-inline hipError_t launch_join(const AttnView& a, int rows_log2, int64_t n_slots, const FwdParts& parts, hipStream_t s, int* err) {
-  attn_join_kernel<T, DP><<<static_cast<unsigned>((n_slots * a.n_heads) << (rows_log2 - 5)), 2 * DP, 0, s>>>(a, rows_log2, n_slots,
-                                                                                                            parts, err);
+template <typename T, int DP, bool kGrad>
+inline hipError_t launch_join(const AttnView& a, int rows_log2, int64_t n_slots, const KeyParts& parts, hipStream_t s, int* err) {
+  if (parts.n == 1) return hipSuccess;
+  attn_join_kernel<T, DP, kGrad>
+      <<<static_cast<unsigned>((n_slots * a.n_heads) << (rows_log2 - 5)), 2 * DP, 0, s>>>(a, rows_log2, n_slots, parts, err);
   return hipGetLastError();
 }
 
@@ -680,10 +701,11 @@ inline bool spans_buffer(const HeadsView& t, int64_t rows, int elem_bytes) {
 }
 
 // The backward's workspace: the row statistics, the plan, and the sums of split
-// tiles.
+// tiles of queries and keys.
 struct BwdSpace {
   RowStats stats;
   DkvPlan plan;
+  KeyParts parts;   // of dq
   int max_parts;
   size_t bytes;
 };
