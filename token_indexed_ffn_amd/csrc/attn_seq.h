@@ -27,6 +27,25 @@ __device__ __forceinline__ TileOf tile_of_slot(const int32_t* cu, int64_t n_seqs
   const int64_t tile = slot - ((cu[lo] >> rows_log2) + lo);
   return TileOf{tile < 0 ? -1 : lo, tile << rows_log2};
 }
+// The same of one slot by a whole wave, which looks at 64 sequences at once.
+__device__ __forceinline__ TileOf tile_of_slot_wave(const int32_t* cu, int n_seqs, int rows_log2, int slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = n_seqs, start;   // the last of [lo, lo + n) that starts at or before `slot`
+  do {
+    const int stride = (n + 63) >> 6;
+    const int at = lane * stride, mid = lo + min(at, n - 1);
+    start = (cu[mid] >> rows_log2) + mid;
+    // lane 0's counts as before
+    const uint64_t before = __ballot(at < n && start <= slot) | 1;
+    const int last = 63 - __builtin_clzll(before);
+    start = __shfl(start, last);
+    lo += last * stride;
+    n = min(stride, n - last * stride);
+  } while (n > 1);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int tile = slot - __builtin_amdgcn_readfirstlane(start);
+  return TileOf{tile < 0 ? -1 : lo, static_cast<int64_t>(tile) << rows_log2};
+}
 inline int64_t tile_slots(int64_t total, int64_t n_seqs, int rows_log2) { return (total >> rows_log2) + n_seqs; }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -40,7 +59,9 @@ struct Segment {
   // False where there is no such tile.  find_lane: any slot a lane; find: one
   // slot for the whole workgroup, kept in scalar registers.
   __device__ __forceinline__ bool find_lane(const AttnView& a, const int32_t* cu, int rows_log2, int64_t slot, int* err) {
-    const TileOf tile = tile_of_slot(cu, a.n_seqs, rows_log2, slot);
+    return take(a, cu, tile_of_slot(cu, a.n_seqs, rows_log2, slot), err);
+  }
+  __device__ __forceinline__ bool take(const AttnView& a, const int32_t* cu, TileOf tile, int* err) {
     if (tile.seq < 0) return false;
     int64_t q1, k1;
     seq_rows(a.cu_q, tile.seq, a.total_q, &q0, &q1, err);
@@ -52,8 +73,8 @@ struct Segment {
     first = static_cast<int>(tile.first);
     return true;
   }
-  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int rows_log2, int64_t slot, int* err) {
-    if (!find_lane(a, cu, rows_log2, slot, err)) return false;
+  __device__ __forceinline__ bool find(const AttnView& a, const int32_t* cu, int rows_log2, int slot, int* err) {
+    if (!take(a, cu, tile_of_slot_wave(cu, static_cast<int>(a.n_seqs), rows_log2, slot), err)) return false;
     nq = uniform(nq);
     nk = uniform(nk);
     past = nk - nq;
@@ -158,12 +179,13 @@ struct QueryCols : Segment {
   bool in;
   int tile_rows;
   // group_of_wave: which 32 queries of the workgroup's tile the wave has.
-  __device__ __forceinline__ bool find(const AttnView& a, int rows_log2, int64_t n_slots, int64_t id, int group_of_wave, int* err) {
+  __device__ __forceinline__ bool find(const AttnView& a, int rows_log2, int64_t n_slots, int id, int group_of_wave, int* err) {
     // the last tiles of a sequence see the most keys: they start first
-    if (!Segment::find(a, a.cu_q, rows_log2, n_slots - 1 - id / a.n_heads, err)) return false;
+    const int back = id / static_cast<int>(a.n_heads);
+    if (!Segment::find(a, a.cu_q, rows_log2, static_cast<int>(n_slots) - 1 - back, err)) return false;
     tile_rows = 1 << rows_log2;
-    head = uniform(static_cast<int>(id % a.n_heads));
-    hk = uniform(head / a.group);
+    head = uniform(id - back * static_cast<int>(a.n_heads));
+    hk = uniform(head / static_cast<int>(a.group));
     wq = first + 32 * group_of_wave;
     row = wq + (threadIdx.x & 31);
     in = row < nq;
@@ -361,13 +383,12 @@ template <typename T, int DP, bool kGrad>
 __global__ __launch_bounds__(2 * DP) void attn_join_kernel(AttnView a, int rows_log2, int64_t n_slots, KeyParts parts, int* err) {
   constexpr int kDT = Tile<T, DP>::kDT;
   const int groups = 1 << (rows_log2 - 5), lane = threadIdx.x & 63;
-  const int64_t tile = blockIdx.x / groups;
-  const int group = static_cast<int>(blockIdx.x - tile * groups);
+  const int tile = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - tile * groups;
   QueryCols w;
   if (!w.find(a, rows_log2, n_slots, tile, group, err) || w.wq >= w.nq) return;
   const int n = w.blocks(a).share(parts.n, 0);
   if (n == 1) return;   // stored already
-  const int64_t unit = tile * parts.n * groups + group;
+  const int64_t unit = static_cast<int64_t>(tile) * parts.n * groups + group;
   const float* const tops = parts.rows + unit * 64 + (lane & 31);
   const f32x4_t* const from = parts.o + (unit * kDT + wave_id()) * 256 + lane;
   // a batch of parts at a time: what it costs is waiting for their loads
