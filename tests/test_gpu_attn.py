@@ -161,6 +161,21 @@ def test_window_attention_peaked_scores(st, dtype):
         check(got[n], ref[n], bound[n], n)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_attention_of_one_key_is_its_value(st, dtype):
+    """A window of one key, and scores far from zero: the weight is 1 in the stored type too."""
+    import torch
+    lens, h, hk, d = [1, 70, 200], 4, 2, 72
+    q, k, v = (rand((271, n, d), dtype, 70 + i, s) for i, (n, s) in enumerate(((h, 3.0), (hk, 3.0), (hk, 1.0))))
+    c = cu(lens)
+    got = st.staple_attn_fwd(q, k, v, c, c, window=1)
+    want = v.repeat_interleave(h // hk, dim=1)
+    if dtype == "bf16":
+        assert torch.equal(got["o"], want)
+    else:   # an exponential of at most (d + 4) 2^-24 |s| from zero over a sum of itself
+        assert ((got["o"] - want).abs() <= 2.0 ** -22 * want.abs()).all()
+
+
 def test_window_attention_negative_and_zero_scale(st):
     for scale in (-0.2, 0.0):
         ops, lk, got = run_window(st, "bf16", [140], [0], 2, 1, 64, 0, 0, seed=3, scale=scale)

@@ -237,10 +237,12 @@ __device__ __forceinline__ void attn_fwd_row(const AttnView& a, int64_t t, int64
   store_row<T>(a.o, t, h, a.head_dim, sm.value());
 }
 
-// Running softmax of the lane's column: the sums stay relative to `top`, an
-// earlier maximum rounded up to an integer, until a score passes it by 8: the
-// exponentials stay below 2^9, far from fp32's range, lanes exchange maxima
-// only then, and what has been summed is scaled by a power of two, exactly.
+// Running softmax of the lane's column: the sums stay relative to `top`, the
+// largest score of the first block that held one, until a score passes it by 8.
+// Then it rises by an integer: the exponentials stay below 2^9, far from fp32's
+// range, lanes exchange maxima only then, and what has been summed is scaled by
+// a power of two, exactly.  A query that sees one key has the weight 1, which a
+// rounding to bf16 leaves as it is: its o is that key's value.
 struct ColumnSoftmax {
   float top = -INFINITY, sum = 0.0f;   // sum: this half-wave's keys
   // s: the block's products, c times which are the scores.  True where `keep`
@@ -251,9 +253,11 @@ struct ColumnSoftmax {
     for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r]);
     m *= c;
     if (!__any((m > top + 8.0f) | ((top == -INFINITY) & (m > top)))) return false;
-    const float t = fmaxf(top, ceilf(fmaxf(m, other_half(m))));
-    *keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t);
-    top = t;
+    m = fmaxf(m, other_half(m));
+    const bool first = top == -INFINITY;
+    const float up = fmaxf(ceilf(m - top), 0.0f);
+    *keep = first ? 0.0f : __builtin_amdgcn_exp2f(-up);
+    top = first ? m : top + up;
     sum *= *keep;
     return true;
   }
