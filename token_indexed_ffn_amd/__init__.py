@@ -58,13 +58,14 @@ def _dev(*ts) -> None:
 
 # the current stream's handle without a Stream object around it, where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -811,28 +812,30 @@ def staple_ffn_bwd_table_grad(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
 # ----------------------------------------------------------------------------
 # Attention and its key-value cache
 # ----------------------------------------------------------------------------
-_NO_HEADS = _lib.Heads(None, 0, 0)
+_NO_HEADS = (None, 0, 0)
+_INT32 = torch.int32
 
 
 def _heads(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, rows: int, heads: int,
-           dim: int) -> _lib.Heads:
-    """A [rows, heads, dim] device tensor, dim contiguous; rows and heads may be strided."""
+           dim: int) -> tuple:
+    """A [rows, heads, dim] device tensor, dim contiguous; rows and heads may be strided.
+    The fields of a staple_heads_t."""
     if t is None:
         return _NO_HEADS
-    if not t.is_cuda or t.dtype != dtype or t.shape != (rows, heads, dim):
+    if not t.is_cuda or t.dtype is not dtype or t.shape != (rows, heads, dim):
         raise ValueError(f"{what}: needs a device tensor [{rows}, {heads}, {dim}] of {dtype}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     sr, sh, sd = t.stride()
     if sd != 1 and dim > 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return _lib.Heads(t.data_ptr(), sr, sh)
+    return t.data_ptr(), sr, sh
 
 
 def _ints(t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[int]:
     """A contiguous int32 device tensor of n elements (None: any number)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or \
+    if not t.is_cuda or t.dtype is not _INT32 or not t.is_contiguous() or \
             (n is not None and t.numel() != n):
         raise ValueError(f"{what}: needs a contiguous int32 device tensor" +
                          ("" if n is None else f" of {n} elements"))
@@ -902,27 +905,28 @@ def _kv(refs=None, table=None, lens=None, k_pages=None, v_pages=None,
         page_size: Optional[int] = None) -> _lib.Kv:
     """staple_kv_t of a cache: pools [layers, pages, kv heads, page size, head_dim] or one
     layer's [pages, kv heads, page size, head_dim]."""
-    layers, pages, hk, size, d, dt = 1, 1, 1, page_size, 8, F32
+    layers, pages, hk, size, d, dt, kp, vp = 1, 1, 1, page_size, 8, F32, None, None
     if k_pages is not None:
         _dev(k_pages, v_pages)
-        if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() not in (4, 5):
+        shape = k_pages.shape
+        if v_pages.shape != shape or v_pages.dtype is not k_pages.dtype or len(shape) not in (4, 5):
             raise ValueError("k_pages and v_pages are pools of one shape and dtype")
-        layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-        pages, hk, size, d = k_pages.shape[-4:]
-        dt = _dt(k_pages)
+        if len(shape) == 5:
+            layers, pages, hk, size, d = shape
+        else:
+            pages, hk, size, d = shape
+        dt, kp, vp = _dt(k_pages), k_pages.data_ptr(), v_pages.data_ptr()
     if refs is not None:
         if k_pages is None:
             pages = refs.numel()
-        _ints(refs, "refs", pages)
+        refs = _ints(refs, "refs", pages)
     rows, width = 1, 1
     if table is not None:
         if table.dim() != 2:
             raise ValueError("table is [rows, max pages]")
         rows, width = table.shape
-        _ints(table, "table")
-        _ints(lens, "lens", rows)
-    return _lib.Kv(layers, pages, hk, size, d, rows, width, dt, _p(k_pages), _p(v_pages), _p(refs),
-                   _p(table), _p(lens))
+        table, lens = _ints(table, "table"), _ints(lens, "lens", rows)
+    return _lib.Kv(layers, pages, hk, size, d, rows, width, dt, kp, vp, refs, table, lens)
 
 
 def staple_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
@@ -936,8 +940,8 @@ def staple_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Te
     n = k_new.shape[0]
     hk, d = k_pages.shape[-3], k_pages.shape[-1]
     n_seqs = cu_new.numel() - 1 if cu_new is not None else n
-    kn = _heads(k_new, "k_new", k_pages.dtype, n, hk, d)
-    vn = _heads(v_new, "v_new", k_pages.dtype, n, hk, d)
+    kn = _lib.Heads(*_heads(k_new, "k_new", k_pages.dtype, n, hk, d))
+    vn = _lib.Heads(*_heads(v_new, "v_new", k_pages.dtype, n, hk, d))
     _check(lib().staple_kv_append(ctypes.byref(kv), ctypes.byref(kn), ctypes.byref(vn), n,
                                   _ints(seqs, "seqs", n_seqs), n_seqs, _ints(cu_new, "cu_new"),
                                   _stream(stream)), "staple_kv_append")
@@ -1018,27 +1022,29 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     and values, also written to the cache.  max_len: a bound of the lengths known on the
     host (None: the table's width)."""
     kv = _kv(None, table, lens, k_pages, v_pages)
-    n, h, d = q.shape
-    hk = k_pages.shape[-3]
+    n, h, d = shape = q.shape
+    hk, size, dim = k_pages.shape[-3:]
     dt = k_pages.dtype
     if out is None:
-        out = {"o": q.new_empty(q.shape), "lse": q.new_empty((n, h), dtype=torch.float32)}
-    lse = out.get("lse")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, h) or
-                            not lse.is_contiguous() or not lse.is_cuda):
-        raise ValueError(f"lse: needs a contiguous float32 device tensor [{n}, {h}]")
-    if d != k_pages.shape[-1]:
+        out = {"o": q.new_empty(shape), "lse": q.new_empty((n, h), dtype=torch.float32)}
+        lse, o = out["lse"], (out["o"].data_ptr(), h * d, d)
+    else:
+        lse, o = out.get("lse"), _heads(out["o"], "o", dt, n, h, d)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, h) or
+                                not lse.is_contiguous() or not lse.is_cuda):
+            raise ValueError(f"lse: needs a contiguous float32 device tensor [{n}, {h}]")
+    if d != dim:
         raise ValueError("q and the pages have one head_dim")
     if max_len is None:
-        max_len = table.shape[1] * k_pages.shape[-2]
+        max_len = table.shape[1] * size
     a = _lib.AttnDecode(n, h, int(max_len), int(window), int(sinks), _scale(scale, d),
                         _ints(seqs, "seqs", n), _heads(q, "q", dt, n, h, d),
                         _heads(k_new, "k_new", dt, n, hk, d), _heads(v_new, "v_new", dt, n, hk, d),
-                        _heads(out["o"], "o", dt, n, h, d), _p(lse))
-    ws = _ws(lib().staple_attn_decode_workspace_bytes(ctypes.byref(kv), ctypes.byref(a)), workspace,
-             q.device)
-    _check(lib().staple_attn_decode_paged(ctypes.byref(kv), ctypes.byref(a), _p(ws), _ws_size(ws),
-                                          _stream(stream)), "staple_attn_decode_paged")
+                        o, _p(lse))
+    kv, a, native = ctypes.byref(kv), ctypes.byref(a), lib()
+    ws = _ws(native.staple_attn_decode_workspace_bytes(kv, a), workspace, q.device)
+    _check(native.staple_attn_decode_paged(kv, a, _p(ws), _ws_size(ws), _stream(stream)),
+           "staple_attn_decode_paged")
     return out
 
 
