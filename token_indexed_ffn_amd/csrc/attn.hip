@@ -557,7 +557,16 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
       }
     }
   }
-  if (w.parts > 1 && !join_parts<64 * kDkvWaves, 2 * kHalf>(plan, w, a.n_kv_heads, x)) return;
+  if (w.parts > 1) {
+    if (w.wkey >= w.nk) return;
+    f32x4_t* to = part_sums<2 * TL::kDT>(plan, plan.first[w.slot] + w.part, w.hk, a.n_kv_heads, keys_of);
+#pragma unroll
+    for (int d = 0; d < kHalf; ++d) {
+      put_sums(to, side * kHalf + d, x[d]);
+      put_sums(to, TL::kDT + side * kHalf + d, x[kHalf + d]);
+    }
+    return;
+  }
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < kHalf; ++d) {
@@ -606,21 +615,25 @@ static BwdSpace bwd_space(const AttnView& a, int dtype, void* ws) {
   b.plan.target = (2 * device_cus() + a.n_kv_heads - 1) / a.n_kv_heads;   // two parts a CU
   const int64_t blocks = (a.total_q / 32 + a.n_seqs) * a.group * n;       // more than there are
   const int64_t most = 2 * (blocks / kMinChunk) + 2;
-  b.max_parts = static_cast<int>(most < 2 * b.plan.target ? most : 2 * b.plan.target);
+  b.plan.max_parts = static_cast<int>(most < 2 * b.plan.target ? most : 2 * b.plan.target);
+  // a tile of kMinChunk blocks or less is never split
+  int64_t per_head = (a.total_q + 31) / 32;
+  const int64_t window = (a.window + (int64_t(1) << b.plan.rows_log2) + 31) / 32 + 1;
+  if (a.window > 0 && a.sinks == 0 && window < per_head) per_head = window;
+  if (per_head * a.group <= kMinChunk) b.plan.max_parts = 0;
   Workspace w(ws, ~size_t(0));
   const size_t rows = static_cast<size_t>(a.total_q) * a.n_heads * sizeof(float);
   const size_t ints = static_cast<size_t>(n) * sizeof(int32_t);
   b.stats.lse2 = w.take<float>(rows);
   b.stats.delta = w.take<float>(rows);
-  b.plan.head = w.take<int32_t>(sizeof(int32_t));
+  b.plan.head = w.take<int32_t>(2 * sizeof(int32_t));
   b.plan.blocks = w.take<int32_t>(ints);
   b.plan.parts = w.take<int32_t>(ints);
   b.plan.first = w.take<int32_t>(ints);
-  b.plan.split = w.take<int32_t>(ints);
-  b.plan.items = w.take<int32_t>(2 * (ints + b.max_parts * sizeof(int32_t)));
-  b.plan.done = w.take<int32_t>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sizeof(int32_t));
+  b.plan.split = w.take<int32_t>(b.plan.max_parts * sizeof(int32_t));
+  b.plan.items = w.take<int32_t>(2 * (ints + b.plan.max_parts * sizeof(int32_t)));
   const size_t sums = (size_t(2) << b.plan.rows_log2) * dp * sizeof(float);   // dk and dv of a tile
-  b.plan.sums = w.take<float>(static_cast<size_t>(b.max_parts) * a.n_kv_heads * sums);
+  b.plan.sums = w.take<f32x4_t>(static_cast<size_t>(b.plan.max_parts) * a.n_kv_heads * sums);
   b.parts = take_parts(a, b.plan.rows_log2, w);
   b.bytes = w.used;
   return b;
@@ -636,8 +649,9 @@ static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s
   if (e != hipSuccess) return e;
   e = launch_join<bf16_t, DP, true>(a, kBf16RowsLog2, nq, b.parts, s, err);
   if (e != hipSuccess) return e;
-  const int64_t items = (b.plan.n_slots + b.max_parts) * a.n_kv_heads;   // at most
-  return launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan, err);
+  const int64_t items = (b.plan.n_slots + b.plan.max_parts) * a.n_kv_heads;   // at most
+  e = launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan, err);
+  return e != hipSuccess ? e : launch_dkv_join<bf16_t, DP>(a, b, s, err);
 }
 
 hipError_t launch_attn_bwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {

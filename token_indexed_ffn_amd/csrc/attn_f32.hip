@@ -322,7 +322,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
   constexpr int kOut = 2 * TL::kDT / kWaves;
   f32x16_t out[kOut];
   join_waves<DP>(smem, x, 1.0f, out);
-  if (w.parts > 1 && !join_parts<64 * kWaves, kOut>(plan, w, a.n_kv_heads, out)) return;
+  if (w.parts > 1) {
+    f32x4_t* to = part_sums<2 * TL::kDT>(plan, plan.first[w.slot] + w.part, w.hk, a.n_kv_heads, 0);
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) put_sums(to, i * kWaves + wave, out[i]);
+    return;
+  }
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kOut; ++i) {
@@ -363,8 +368,9 @@ static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s
   if (e != hipSuccess) return e;
   e = launch_join<F32, DP, true>(a, kF32RowsLog2, n, b.parts, s, err);
   if (e != hipSuccess) return e;
-  const int64_t items = (b.plan.n_slots + b.max_parts) * a.n_kv_heads;   // at most
-  return launch_lds<attn_dkv_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(items, s, a, b.stats, b.plan, err);
+  const int64_t items = (b.plan.n_slots + b.plan.max_parts) * a.n_kv_heads;   // at most
+  e = launch_lds<attn_dkv_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(items, s, a, b.stats, b.plan, err);
+  return e != hipSuccess ? e : launch_dkv_join<F32, DP>(a, b, s, err);
 }
 
 hipError_t launch_attn_bwd_f32(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {

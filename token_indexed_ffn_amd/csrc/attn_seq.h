@@ -293,8 +293,8 @@ __device__ __forceinline__ void redo_queries(bool bad, RowFn row) {
 //   512 queries after 8000 keys, 16 heads on 4: 74 us; 178 us
 //   2048 queries, 4 heads: 41 us; 56 us
 //   8 sequences of 16 queries after 600 keys, 4 heads: 33 us; 36 us
-//   backward of 4096 queries, 1 head: 143 us; 245 us
-//   backward of 2048 queries, 4 heads: 153 us; 196 us
+//   backward of 4096 queries, 1 head: 90 us; 192 us
+//   backward of 2048 queries, 4 heads: 95 us; 138 us
 struct KeyParts {
   int n;         // at most so many of a tile
   f32x4_t* o;    // [tiles][heads][parts][32s of queries][32s of dims][4][64]: sums as they lie in a wave
@@ -490,23 +490,29 @@ struct QueryBlocks {
 // own, the sinks' all again), and a shared key-value head those of every head
 // of its group.  A tile with more blocks than `chunk` is split into parts of
 // equal size, whose fp32 sums go to the workspace and are added in part order
-// by the last of them to finish; and the items (tiles and parts) start in the
-// order of their size, the largest first.  Written by one workgroup of the dq
-// kernel, which runs before.
+// by attn_dkv_join_kernel; and the items (tiles and parts) start in the order
+// of their size, the largest first.  Written by one workgroup of the dq kernel,
+// which runs before.
+//
+// Joined by the part that arrives last, every part pays a flush of its L2 to
+// the device: the backward of 2048 queries of 4 heads took 153 us so and takes
+// 95 with a kernel of its own, 4096 of one head 141 and 90.
 struct DkvPlan {
-  int32_t* head;      // [0] items
+  int32_t* head;      // [0] items, [1] split tiles
   int32_t* blocks;    // [slots] blocks of the slot's tile
   int32_t* parts;     // [slots] its parts
   int32_t* first;     // [slots] its first partial result, where there are several parts
-  int32_t* split;     // [slots] its number among the split tiles
+  int32_t* split;     // [max_parts] slots of the split tiles
   int32_t* items;     // [slots + max_parts][2] slot, part
-  int32_t* done;      // [max_parts][n_kv_heads] parts of a split tile that have finished
-  float* sums;        // [max_parts][n_kv_heads] dk and dv sums of a part
+  f32x4_t* sums;      // [max_parts][n_kv_heads][32s of keys][dk, dv, 32s of dims][4][64]: as they lie in a wave
   int64_t n_slots;
+  int max_parts;
   int target;         // parts per head to aim for
   int rows_log2;      // keys of a tile
 };
-constexpr int kMinChunk = 16;   // blocks: a part's sums cost about as much traffic as two blocks
+// Blocks of a part, at least.  The backward of 2048 queries of 4 heads takes 95
+// us; 108 with 8, 107 with 32.
+constexpr int kMinChunk = 16;
 constexpr int kBuckets = 64;
 
 __device__ __forceinline__ int64_t group_sum(int64_t v, int64_t* lds) {
@@ -549,7 +555,7 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
     plan.parts[s] = parts;
     if (parts > 1) {
       plan.first[s] = atomicAdd(&n_parts, parts);
-      plan.split[s] = atomicAdd(&n_split, 1);
+      plan.split[atomicAdd(&n_split, 1)] = s;
     }
     atomicAdd(&count[bucket((n + parts - 1) / parts)], parts);
   }
@@ -561,6 +567,7 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
       at += count[b];
     }
     plan.head[0] = at;
+    plan.head[1] = n_split;
   }
   __syncthreads();
   for (int s = threadIdx.x; s < n_slots; s += kThreads) {
@@ -573,7 +580,6 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
       plan.items[2 * at + 1] = p;
     }
   }
-  for (int i = threadIdx.x; i < n_split * a.n_kv_heads; i += kThreads) plan.done[i] = 0;
 }
 
 // dk and dv: one key a column; the queries that see them (of every head of the
@@ -623,45 +629,14 @@ struct DkvItem : Segment {
   }
 };
 
-// A split tile's part: its fp32 sums to the workspace, as they lie in the
-// registers of the workgroup's kThreads threads (x: kX results a thread); true
-// in the part that arrives last, with all parts' sums added in part order.
-template <int kThreads, int kX>
-__device__ __forceinline__ bool join_parts(const DkvPlan& plan, const DkvItem& w, int n_kv_heads, f32x16_t* x) {
-  constexpr int kFloats = kThreads * 16 * kX;
-  auto sums_of = [&](int p) {
-    return reinterpret_cast<f32x4_t*>(plan.sums + (static_cast<int64_t>(plan.first[w.slot] + p) * n_kv_heads + w.hk) * kFloats) +
-           threadIdx.x;
-  };
-  f32x4_t* mine = sums_of(w.part);
+// Where a part's sums of 32 keys lie, for the lane: kTiles results of a wave.
+template <int kTiles>
+__device__ __forceinline__ f32x4_t* part_sums(const DkvPlan& plan, int64_t part, int hk, int n_kv_heads, int group) {
+  return plan.sums + ((((part * n_kv_heads + hk) << (plan.rows_log2 - 5)) + group) * kTiles) * 256 + (threadIdx.x & 63);
+}
+__device__ __forceinline__ void put_sums(f32x4_t* to, int tile, const f32x16_t& x) {
 #pragma unroll
-  for (int d = 0; d < kX; ++d)
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      mine[(d * 4 + g) * kThreads] = f32x4_t{x[d][4 * g], x[d][4 * g + 1], x[d][4 * g + 2], x[d][4 * g + 3]};
-  __shared__ int arrived;
-  __threadfence();   // the sums are visible to the device before the count
-  __syncthreads();
-  if (threadIdx.x == 0)
-    arrived = __hip_atomic_fetch_add(&plan.done[plan.split[w.slot] * n_kv_heads + w.hk], 1, __ATOMIC_ACQ_REL,
-                                     __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (arrived != w.parts - 1) return false;
-  __threadfence();
-#pragma unroll
-  for (int d = 0; d < kX; ++d) x[d] = f32x16_t{};
-  for (int p = 0; p < w.parts; ++p) {
-    const f32x4_t* from = sums_of(p);
-#pragma unroll
-    for (int d = 0; d < kX; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t v = from[(d * 4 + g) * kThreads];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[d][4 * g + e] += v[e];
-      }
-  }
-  return true;
+  for (int g = 0; g < 4; ++g) to[(tile * 4 + g) * 64] = f32x4_t{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
 }
 
 // Keys whose gradients came out not finite: a query that does not see the key
@@ -676,6 +651,51 @@ __device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& sta
     again &= again - 1;
     attn_dkv_row<T>(a, stats.delta, w.wkey + i, w.hk, w);
   }
+}
+
+// 32 keys of a split tile a workgroup, 32 dims of dk or dv a wave.
+template <typename T, int DP>
+__global__ __launch_bounds__(4 * DP) void attn_dkv_join_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+  constexpr int kDT = Tile<T, DP>::kDT, kTiles = 2 * kDT, kBatch = 8;
+  const int groups = 1 << (plan.rows_log2 - 5);
+  const int id = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - id * groups;
+  const int split = id / a.n_kv_heads;
+  if (split >= plan.head[1]) return;
+  const int slot = uniform(plan.split[split]), parts = uniform(plan.parts[slot]);
+  DkvItem w;
+  if (!w.Segment::find(a, a.cu_k, plan.rows_log2, slot, err)) return;
+  w.hk = id - split * a.n_kv_heads;
+  w.wkey = w.first + 32 * group;
+  w.key = w.wkey + (threadIdx.x & 31);
+  w.in = w.key < w.nk;
+  if (w.wkey >= w.nk) return;
+  const int tile = wave_id();
+  const int64_t first = plan.first[slot];
+  f32x16_t x = {};
+  for (int u0 = 0; u0 < parts; u0 += kBatch) {
+    f32x4_t v[kBatch][4];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const f32x4_t* from = part_sums<kTiles>(plan, first + min(u0 + i, parts - 1), w.hk, a.n_kv_heads, group);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) v[i][g] = from[(tile * 4 + g) * 64];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float f = u0 + i < parts ? 1.0f : 0.0f;   // past the last part: that one again, times zero
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * g + e] += v[i][g][e] * f;
+    }
+  }
+  bool bad = false;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) bad |= not_finite(x[r]);
+  const bool value = tile >= kDT;
+  store_column<T>(value ? a.dv : a.dk, w.k0 + w.key, w.hk, a.head_dim, value ? tile - kDT : tile, x, value ? 1.0f : a.scale, w.in);
+  __syncthreads();   // a row done again is stored after all its parts
+  redo_keys<T>(a, stats, w, bad);
 }
 
 // ------------------------------------------------------------------- launches
@@ -731,9 +751,17 @@ struct BwdSpace {
   RowStats stats;
   DkvPlan plan;
   KeyParts parts;   // of dq
-  int max_parts;
   size_t bytes;
 };
+
+template <typename T, int DP>
+inline hipError_t launch_dkv_join(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {
+  const int64_t tiles = b.plan.max_parts / 2;   // split ones have two parts or more
+  if (tiles == 0) return hipSuccess;
+  attn_dkv_join_kernel<T, DP>
+      <<<static_cast<unsigned>((tiles * a.n_kv_heads) << (b.plan.rows_log2 - 5)), 4 * DP, 0, s>>>(a, b.stats, b.plan, err);
+  return hipGetLastError();
+}
 
 // kernels of fp32 (attn_f32.hip)
 hipError_t launch_attn_fwd_f32(const AttnView& a, void* ws, hipStream_t s, int* err);
