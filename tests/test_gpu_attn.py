@@ -151,6 +151,57 @@ def test_window_attention_few_queries_never_read_a_hidden_key(st, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_attention_gradients_in_parts_never_read_a_hidden_row(st, dtype):
+    """One head of 1100 tokens: a late key holds NaN, which no earlier query's dq may take; an
+    early query's gradient does, which no later key's dk, dv may take."""
+    n, h, d = 1100, 1, 64
+    ops, lk, _ = run_window(st, dtype, [n], [0], h, h, d, 0, 0, seed=80)
+    q, k, v, do = ops
+    ref, bound = oracle_window(dtype, ops, [n], lk, h, h, 0, 0, d ** -0.5)
+    c = cu([n])
+    fwd = st.staple_attn_fwd(q, k, v, c, c)
+    bad_k, bad_v, bad_do = k.clone(), v.clone(), do.clone()
+    bad_k[1090], bad_v[1090], bad_do[5] = float("nan"), float("inf"), float("nan")
+    late = st.staple_attn_bwd(do, q, bad_k, bad_v, fwd["o"], fwd["lse"], c, c)
+    check(to_np(late["dq"])[:1090], ref["dq"][:1090], bound["dq"][:1090], "dq")
+    early = st.staple_attn_bwd(bad_do, q, k, v, fwd["o"], fwd["lse"], c, c)
+    for name in ("dk", "dv"):
+        check(to_np(early[name])[6:], ref[name][6:], bound[name][6:], name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_attention_in_a_graph(st, dtype):
+    """Forward and backward, split and not, captured once and replayed on new inputs."""
+    import torch
+    for lens, window, sinks in (([700], 0, 0), ([40, 130], 33, 2)):
+        c, n = cu(lens), sum(lens)
+        q, k, v, do = (rand((n, 2, 64), dtype, 90 + i) for i in range(4))
+
+        def step():
+            f = st.staple_attn_fwd(q, k, v, c, c, window=window, sinks=sinks)
+            return f | st.staple_attn_bwd(do, q, k, v, f["o"], f["lse"], c, c, window=window, sinks=sinks)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = step()
+        for i in range(4):
+            for j, t in enumerate((q, k, v, do)):
+                t.copy_(rand(t.shape, dtype, 100 + 10 * i + j))
+            want = step()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for name in want:
+                assert torch.equal(held[name], want[name]), (i, name)
+        assert st.staple_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_window_attention_peaked_scores(st, dtype):
     """Scores of a few hundred: softmax rows that one key takes whole."""
     lq, h, d = [200], 2, 64

@@ -9,6 +9,12 @@
 // vector work between the products of other blocks, and keep their loop free of
 // address and mask work: positions are 32-bit, a head's rows are one buffer,
 // and only blocks at the edge of what is seen apply a mask.
+//
+// Measured on 6 causal sequences of 700 to 4096 tokens, 32 heads on 8 of 128:
+// forward 470 us (850 TFLOP/s), dq 674 us (889, its three products), dk and dv
+// 920 us (868, their four).  A large matrix product reaches 1234 with a larger
+// share of busy cycles at a lower clock: the product of the two is 0.90 to 0.94
+// GHz here and 1.05 there.
 #include <type_traits>
 
 #include "attn_seq.h"
@@ -39,7 +45,10 @@ __device__ __forceinline__ void finish_fwd(const AttnView& a, const QueryCols& w
 // runs three blocks at a time: between the exponentials of block b stand the
 // score products of block b + 1 and the value products of block b - 1.  The
 // workgroup meets every second block: a stage loads two blocks of K and of V
-// while the two before are worked on.
+// while the two before are worked on.  P is rounded to bf16 for its product: a
+// relative 2^-9 a weight, which the sum averages; the sum of the weights is of
+// the unrounded ones.  64 sequences of 256 tokens, 16 heads: 73 us, 3.7 TB/s of
+// q, k, v and o, bound by them.
 template <int DP>
 struct FwdShape {
   static constexpr int kBlock = 32 * Tile<bf16_t, DP>::kRow;
@@ -181,7 +190,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_bf16_kernel(AttnView 
 // ------------------------------------------------------------------ backward
 // dq, and the row statistics for the other kernel.  A block is 16 MFMAs for the
 // scores and their gradients, then 16 elements of vector work with the 8 MFMAs
-// of the block before in between.
+// of the block before in between.  dS is rounded to bf16 for its product, as P
+// is in the forward.  8 sequences of 4096 tokens, window 1024, 16 heads: 510 us.
 template <int DP>
 struct DqShape {
   static constexpr int kAhead = 2;
@@ -363,7 +373,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
 // two query blocks each forms the probabilities and score gradients of one,
 // they trade them through LDS, and each adds both to its half of head_dim.
 // Between the elements of a stage stand the gradient products of the stage
-// before.
+// before.  8 sequences of 4096 tokens, window 1024, 16 heads: 782 us, a
+// workgroup's 37 blocks at a time; one workgroup a CU, so that its first loads
+// and its last stores overlap nothing.
 constexpr int kDkvWaves = 8;
 template <int DP>
 struct DkvPair {

@@ -23,6 +23,10 @@
 // The cache is split along its length over workgroups where the (sequence,
 // head) pairs alone are too few; the splits' partial results are joined by a
 // second kernel in split order.
+//
+// Measured: two sequences of 100001 to 131071 keys, 32 heads on 8, 167 us (5.6
+// TB/s) and 6 in the join; 64 sequences around 256 keys, 16 heads, 32 us (4.2
+// TB/s, no join); one of 37 keys 8 us, its chain of loads: length, page, rows.
 #include "attn.h"
 
 namespace staple {
