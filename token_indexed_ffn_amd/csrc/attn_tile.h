@@ -19,6 +19,7 @@
 #pragma once
 
 #include "attn.h"
+#include "lds_load.h"
 
 namespace staple {
 

@@ -113,6 +113,19 @@ struct GemmArgs {
 constexpr int kRowBytes = 128;  // bytes of k per LDS tile row and stage
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 
+// One 16-byte-per-lane global -> LDS load (global_load_lds_dwordx4: lane l
+// writes LDS bytes [dst + 16 l, +16), dst wave-uniform, passed in M0).  It is
+// issued from inline asm so that the compiler does not count it among the
+// LDS-counter events: with such a load in flight it would otherwise wait for
+// every outstanding LDS read (lgkmcnt(0)) before each MFMA group instead of
+// only the ones the group needs.  The asm has no register outputs (the data
+// goes to LDS); its completion is waited for by hand (vmcnt) before the
+// barrier that publishes the stage, as for the builtin form.
+__device__ __forceinline__ void dma16(const void* src, lds_void* dst) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+
 // K-major LDS tile rows hold RB bytes of k: 128 (8 chunks of 16 bytes) or 64
 // (4 chunks).  The chunk index is XORed with a function of the row so that the
 // MFMA fragment reads (consecutive rows, one chunk) spread over the LDS banks:

@@ -5,6 +5,9 @@
 
 namespace staple {
 
+// Bit of the device error word (beside kErrIndexRange): out of pages.
+constexpr int kErrNoPages = 2;
+
 // A [rows][heads][head_dim] operand; strides in elements.
 struct HeadsView {
   char* data;
