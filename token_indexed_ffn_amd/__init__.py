@@ -813,7 +813,7 @@ def staple_ffn_bwd_table_grad(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
 # Attention and its key-value cache
 # ----------------------------------------------------------------------------
 _NO_HEADS = (None, 0, 0)
-_INT32 = torch.int32
+_INT32, _FLOAT32 = torch.int32, torch.float32
 
 
 def _heads(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, rows: int, heads: int,
@@ -846,8 +846,15 @@ def _scale(scale: Optional[float], dim: int) -> float:
     return dim ** -0.5 if scale is None else float(scale)
 
 
-def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, dq=None, dk=None,
-          dv=None) -> _lib.Attn:
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, grads=None,
+          own=False) -> _lib.Attn:
+    """staple_attn_t.  own: the call's outputs (o and lse, or with grads those) were made for it
+    by _like() and the like, and are not looked at again."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k are [tokens, heads, head_dim]")
     tq, h, d = q.shape
@@ -855,16 +862,28 @@ def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, dq=None, d
     n = cu_q.numel() - 1
     if n < 0:
         raise ValueError("cu_q and cu_k hold n_seqs + 1 offsets")
-    if lse.dtype != torch.float32 or lse.shape != (tq, h) or not lse.is_contiguous() or not lse.is_cuda:
+    if (do is not None or not own) and (lse.dtype is not _FLOAT32 or lse.shape != (tq, h) or
+                                        not lse.is_contiguous() or not lse.is_cuda):
         raise ValueError(f"lse: needs a contiguous float32 device tensor [{tq}, {h}]")
     dt = q.dtype
     code = _dt(q)
+    heads = (_heads(q, "q", dt, tq, h, d), _heads(k, "k", dt, tk, hk, d),
+             _heads(v, "v", dt, tk, hk, d))
+    if do is None:
+        rest = (_NO_HEADS,) * 4
+        o = (o.data_ptr(), h * d, d) if own else _heads(o, "o", dt, tq, h, d)
+    else:
+        dq, dk, dv = grads
+        o = _heads(o, "o", dt, tq, h, d)
+        if own:
+            rest = ((dq.data_ptr(), h * d, d), (dk.data_ptr(), hk * d, d), (dv.data_ptr(), hk * d, d))
+        else:
+            rest = (_heads(dq, "dq", dt, tq, h, d), _heads(dk, "dk", dt, tk, hk, d),
+                    _heads(dv, "dv", dt, tk, hk, d))
+        rest = (_heads(do, "do", dt, tq, h, d),) + rest
     return _lib.Attn(n, tq, tk, h, hk, d, int(window), int(sinks), _scale(scale, d), code,
-                     _ints(cu_q, "cu_q"), _ints(cu_k, "cu_k", n + 1),
-                     _heads(q, "q", dt, tq, h, d), _heads(k, "k", dt, tk, hk, d),
-                     _heads(v, "v", dt, tk, hk, d), _heads(o, "o", dt, tq, h, d), lse.data_ptr(),
-                     _heads(do, "do", dt, tq, h, d), _heads(dq, "dq", dt, tq, h, d),
-                     _heads(dk, "dk", dt, tk, hk, d), _heads(dv, "dv", dt, tk, hk, d))
+                     _ints(cu_q, "cu_q"), _ints(cu_k, "cu_k", n + 1), *heads, o, lse.data_ptr(),
+                     *rest)
 
 
 def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -877,12 +896,13 @@ def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     int32 offsets of the sequences.  A query at position p sees key j when j <= p and
     (window == 0 or j > p - window or j < sinks); the queries are the last positions of
     their sequence.  scale: head_dim ** -0.5 when None."""
-    if out is None:
-        out = {"o": q.new_empty(q.shape), "lse": q.new_empty(q.shape[:2], dtype=torch.float32)}
-    a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"])
-    ws = _ws(lib().staple_attn_fwd_workspace_bytes(ctypes.byref(a)), workspace, q.device)
-    _check(lib().staple_attn_fwd(ctypes.byref(a), _p(ws), _ws_size(ws), _stream(stream)),
-           "staple_attn_fwd")
+    own = out is None
+    if own:
+        out = {"o": _like(q), "lse": q.new_empty(q.shape[:2], dtype=_FLOAT32)}
+    a = ctypes.byref(_attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"], own=own))
+    native = lib()
+    ws = _ws(native.staple_attn_fwd_workspace_bytes(a), workspace, q.device)
+    _check(native.staple_attn_fwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_attn_fwd")
     return out
 
 
@@ -892,12 +912,14 @@ def staple_attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
                     out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> dict:
     """Gradients dq, dk, dv of staple_attn_fwd from do, its operands and its o and lse."""
-    if out is None:
-        out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
-    a = _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do, out["dq"], out["dk"], out["dv"])
-    ws = _ws(lib().staple_attn_bwd_workspace_bytes(ctypes.byref(a)), workspace, q.device)
-    _check(lib().staple_attn_bwd(ctypes.byref(a), _p(ws), _ws_size(ws), _stream(stream)),
-           "staple_attn_bwd")
+    own = out is None
+    if own:
+        out = {"dq": _like(q), "dk": _like(k), "dv": _like(v)}
+    a = ctypes.byref(_attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do,
+                           (out["dq"], out["dk"], out["dv"]), own))
+    native = lib()
+    ws = _ws(native.staple_attn_bwd_workspace_bytes(a), workspace, q.device)
+    _check(native.staple_attn_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_attn_bwd")
     return out
 
 
