@@ -14,7 +14,7 @@
 // Measured: 16000 new tokens of 16 heads of 128 into pages 53 us (5.0 TB/s of
 // reads and writes); half a pool of 1 GB packed 217 us (4.9 TB/s) after 8 us of
 // ranking 4096 pages; of 64 beams, ending 3 us, forking 3, growing by one token
-// 10 (four loads that depend on each other, then a scan of 2048 counts) and 18
+// 7 (four loads that depend on each other, then a scan of 2048 counts) and 18
 // for their 64 half-filled pages in 4 layers (17 MB written, scattered).
 #include "common.h"
 #include "kv.h"
@@ -24,21 +24,23 @@ namespace staple {
 constexpr int kBookThreads = 1024;
 constexpr int kBookWaves = kBookThreads / 64;
 
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v) {
+// Inclusive sum over the lanes of a wave, which V holds.
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(v, d);
+    const V o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
   return v;
 }
 
 // Exclusive sum over a workgroup of kBookThreads and the whole sum in *total.
-__device__ __forceinline__ int64_t block_scan(int v, int64_t* waves, int64_t* total) {
+template <typename V>
+__device__ __forceinline__ int64_t block_scan(V v, int64_t* waves, int64_t* total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int inc = wave_scan(v);
+  const V inc = wave_scan(v);
   __syncthreads();   // the previous use of waves[] is over
   if (lane == 63) waves[w] = inc;
   __syncthreads();
@@ -113,39 +115,30 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
                                                                  int32_t* free_list, KvCopy* copies,
                                                                  int* err) {
   constexpr int kPer = kKvMaxExtend / kBookThreads;
-  __shared__ int first[kKvMaxExtend + 1], col0[kKvMaxExtend], row[kKvMaxExtend];
+  __shared__ int first[kKvMaxExtend], col0[kKvMaxExtend], row[kKvMaxExtend];
   __shared__ int64_t waves[kBookWaves];
   __shared__ int refused;
   if (threadIdx.x == 0) refused = 0;
   __syncthreads();
   const int64_t max_len = min(kv.max_pages << kv.page_log2, static_cast<int64_t>(0x7fffffff));
   int old_len[kPer], new_len[kPer], need[kPer], cow_page[kPer];
-  int mine = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = threadIdx.x * kPer + k;
+  // sequence i, by thread i % kBookThreads: the loads of one depend on each other
+  auto look = [&](int i, int k) {
     row[i] = -1;
     need[k] = 0;
     cow_page[k] = -1;
     old_len[k] = new_len[k] = 0;
-    if (i >= n) continue;
+    if (i >= n) return;
     const int s = seqs[i];
     const int add = n_new ? n_new[i] : 1;
-    if (s < 0 || s >= kv.n_rows || add < 0) {
-      flag_index_error(err);
-      continue;
-    }
+    if (s < 0 || s >= kv.n_rows || add < 0) return flag_index_error(err);
     const int len = kv.lens[s];
     const int64_t held = pages_of_row(kv, len, err);
-    if (len < 0 || (len > 0 && held == 0)) continue;
-    if (static_cast<int64_t>(len) + add > max_len) {
-      refused = 1;
-      continue;
-    }
+    if (len < 0 || (len > 0 && held == 0)) return;
     const int64_t want = (static_cast<int64_t>(len) + add + kv.page - 1) >> kv.page_log2;
-    if (want - held > kv.n_pages) {
+    if (static_cast<int64_t>(len) + add > max_len || want - held > kv.n_pages) {
       refused = 1;
-      continue;
+      return;
     }
     row[i] = s;
     col0[i] = static_cast<int>(held);
@@ -161,17 +154,17 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
         ++need[k];
       }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) mine += min(need[k], 0x1fffffff);
-  int64_t total;
-  int64_t at = block_scan(mine, waves, &total);
+  };
+  int64_t total = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    first[threadIdx.x * kPer + k] = static_cast<int>(at);
-    at += need[k];
+    if (k * kBookThreads >= n) break;
+    const int i = k * kBookThreads + threadIdx.x;
+    look(i, k);
+    int64_t all;
+    first[i] = static_cast<int>(total + block_scan(static_cast<int64_t>(need[k]), waves, &all));
+    total += all;
   }
-  if (threadIdx.x == kBookThreads - 1) first[kKvMaxExtend] = static_cast<int>(at);
   // the lowest `total` free pages
   int64_t found = 0;
   if (total <= kv.n_pages) {
@@ -200,8 +193,8 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
   if (refuse && threadIdx.x == 0) atomicOr(err, kErrNoPages);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int i = threadIdx.x * kPer + k;
-    if (i >= n) continue;
+    const int i = k * kBookThreads + threadIdx.x;
+    if (i >= n) break;
     KvCopy c{-1, -1, 0};
     if (!refuse && row[i] >= 0) {
       if (cow_page[k] >= 0) {
@@ -214,7 +207,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
   }
   if (refuse) return;
   for (int r = threadIdx.x; r < total; r += kBookThreads) {
-    int lo = 0, hi = kKvMaxExtend;   // first[lo] <= r < first[hi]
+    int lo = 0, hi = n;   // first[lo] <= r < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (first[mid] <= r) lo = mid;
