@@ -794,7 +794,11 @@ typedef struct staple_attn_t {
   staple_heads_t d_o, dq, dk, dv;    /* backward only */
 } staple_attn_t;
 
-/* Forward: writes o and lse from q, k, v.  `a` is read during the call only.
+/* Limits (STAPLE_ERR_UNSUPPORTED past them): 2^29 query or key tokens and
+ * sequences; (tokens / 128 + n_seqs + 4) n_heads + 4096 workgroups of 2^23
+ * (fp32: tokens / 32, 2^24).
+ *
+ * Forward: writes o and lse from q, k, v.  `a` is read during the call only.
  * A pair of cu_q or cu_k entries that is out of order or past the totals sets
  * the device error word, and that sequence counts as empty.  Rows in no
  * sequence are not written.  Workspace: where there are too few queries to
