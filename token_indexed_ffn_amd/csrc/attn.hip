@@ -387,7 +387,7 @@ struct DkvPair {
   static constexpr int kLds = 6 * kStage + kTrade;             // three pairs of slots: before, at hand, loading
 };
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+__global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnView a, RowStats stats, DkvPlan plan) {
   using T = bf16_t;
   using TL = Tile<T, DP>;
   using Shape = DkvPair<DP>;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
   lds_char* const ring = (lds_char*)smem;
   const int keys_of = wave_id() & 3, side = wave_id() >> 2;
   DkvItem w;
-  if (!w.find(a, plan, keys_of, err)) return;
+  if (!w.find(a, plan, keys_of)) return;
   const int lane = threadIdx.x & 63;
   lds_char* const trade = ring + 6 * kStage + keys_of * (2 * 4 * 1024) + lane * 16;
 
@@ -571,7 +571,7 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
   }
   if (w.parts > 1) {
     if (w.wkey >= w.nk) return;
-    f32x4_t* to = part_sums<2 * TL::kDT>(plan, plan.first[w.slot] + w.part, w.hk, a.n_kv_heads, keys_of);
+    f32x4_t* to = part_sums<2 * TL::kDT>(plan, w.sums + w.part, w.hk, a.n_kv_heads, keys_of);
 #pragma unroll
     for (int d = 0; d < kHalf; ++d) {
       put_sums(to, side * kHalf + d, x[d]);
@@ -640,10 +640,9 @@ static BwdSpace bwd_space(const AttnView& a, int dtype, void* ws) {
   b.stats.delta = w.take<float>(rows);
   b.plan.head = w.take<int32_t>(2 * sizeof(int32_t));
   b.plan.blocks = w.take<int32_t>(ints);
-  b.plan.parts = w.take<int32_t>(ints);
-  b.plan.first = w.take<int32_t>(ints);
+  b.plan.tiles = w.take<DkvRecord>(static_cast<size_t>(n) * sizeof(DkvRecord));
   b.plan.split = w.take<int32_t>(b.plan.max_parts * sizeof(int32_t));
-  b.plan.items = w.take<int32_t>(2 * (ints + b.plan.max_parts * sizeof(int32_t)));
+  b.plan.items = w.take<DkvRecord>((static_cast<size_t>(n) + b.plan.max_parts) * sizeof(DkvRecord));
   const size_t sums = (size_t(2) << b.plan.rows_log2) * dp * sizeof(float);   // dk and dv of a tile
   b.plan.sums = w.take<f32x4_t>(static_cast<size_t>(b.plan.max_parts) * a.n_kv_heads * sums);
   b.parts = take_parts(a, b.plan.rows_log2, w);
@@ -662,8 +661,8 @@ static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s
   e = launch_join<bf16_t, DP, true>(a, kBf16RowsLog2, nq, b.parts, s, err);
   if (e != hipSuccess) return e;
   const int64_t items = (b.plan.n_slots + b.plan.max_parts) * a.n_kv_heads;   // at most
-  e = launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan, err);
-  return e != hipSuccess ? e : launch_dkv_join<bf16_t, DP>(a, b, s, err);
+  e = launch_lds<attn_dkv_bf16_kernel<DP, kWide>, DkvPair<DP>::kLds, 64 * kDkvWaves>(items, s, a, b.stats, b.plan);
+  return e != hipSuccess ? e : launch_dkv_join<bf16_t, DP>(a, b, s);
 }
 
 hipError_t launch_attn_bwd(const AttnView& a, int dtype, void* ws, hipStream_t s, int* err) {

@@ -233,13 +233,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a,
 }
 
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a, RowStats stats, DkvPlan plan) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
   constexpr int kBlock = F32Shape<DP>::kBlock;
   extern __shared__ __align__(1024) char smem[];
   DkvItem w;
-  if (!w.find(a, plan, 0, err)) return;
+  if (!w.find(a, plan, 0)) return;
   const int lane = threadIdx.x & 63, wave = wave_id();
   lds_char* const qt = (lds_char*)smem + wave * F32Shape<DP>::kPerWave;
   lds_char* const dt = qt + kBlock;
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
   f32x16_t out[kOut];
   join_waves<DP>(smem, x, 1.0f, out);
   if (w.parts > 1) {
-    f32x4_t* to = part_sums<2 * TL::kDT>(plan, plan.first[w.slot] + w.part, w.hk, a.n_kv_heads, 0);
+    f32x4_t* to = part_sums<2 * TL::kDT>(plan, w.sums + w.part, w.hk, a.n_kv_heads, 0);
 #pragma unroll
     for (int i = 0; i < kOut; ++i) put_sums(to, i * kWaves + wave, out[i]);
     return;
@@ -369,8 +369,8 @@ static hipError_t bwd_launch(const AttnView& a, const BwdSpace& b, hipStream_t s
   e = launch_join<F32, DP, true>(a, kF32RowsLog2, n, b.parts, s, err);
   if (e != hipSuccess) return e;
   const int64_t items = (b.plan.n_slots + b.plan.max_parts) * a.n_kv_heads;   // at most
-  e = launch_lds<attn_dkv_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(items, s, a, b.stats, b.plan, err);
-  return e != hipSuccess ? e : launch_dkv_join<F32, DP>(a, b, s, err);
+  e = launch_lds<attn_dkv_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(items, s, a, b.stats, b.plan);
+  return e != hipSuccess ? e : launch_dkv_join<F32, DP>(a, b, s);
 }
 
 hipError_t launch_attn_bwd_f32(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {

@@ -497,13 +497,17 @@ struct QueryBlocks {
 // Joined by the part that arrives last, every part pays a flush of its L2 to
 // the device: the backward of 2048 queries of 4 heads took 153 us so and takes
 // 95 with a kernel of its own, 4096 of one head 141 and 90.
+struct __align__(16) DkvRecord {
+  int32_t part, parts;          // of a tile's: which, and how many
+  int32_t sums;                 // the tile's first partial result, where there are several parts
+  int32_t q0, k0, nq, nk, first;   // its Segment
+};
 struct DkvPlan {
   int32_t* head;      // [0] items, [1] split tiles
   int32_t* blocks;    // [slots] blocks of the slot's tile
-  int32_t* parts;     // [slots] its parts
-  int32_t* first;     // [slots] its first partial result, where there are several parts
+  DkvRecord* tiles;   // [slots]
   int32_t* split;     // [max_parts] slots of the split tiles
-  int32_t* items;     // [slots + max_parts][2] slot, part
+  DkvRecord* items;   // [slots + max_parts], one load for a workgroup to know its work
   f32x4_t* sums;      // [max_parts][n_kv_heads][32s of keys][dk, dv, 32s of dims][4][64]: as they lie in a wave
   int64_t n_slots;
   int max_parts;
@@ -536,7 +540,10 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
   for (int s = threadIdx.x; s < n_slots; s += kThreads) {
     Segment w;
     int n = -1;   // no tile
-    if (w.find_lane(a, a.cu_k, plan.rows_log2, s, err)) n = QueryBlocks(a, w, 1 << plan.rows_log2).per_head * a.group;
+    if (w.find_lane(a, a.cu_k, plan.rows_log2, s, err)) {
+      n = QueryBlocks(a, w, 1 << plan.rows_log2).per_head * a.group;
+      plan.tiles[s] = DkvRecord{0, 1, 0, static_cast<int>(w.q0), static_cast<int>(w.k0), w.nq, w.nk, w.first};
+    }
     plan.blocks[s] = n;
     mine += max(n, 0);
   }
@@ -552,9 +559,9 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
     const int n = plan.blocks[s];
     if (n < 0) continue;
     const int parts = max((n + chunk - 1) / chunk, 1);
-    plan.parts[s] = parts;
     if (parts > 1) {
-      plan.first[s] = atomicAdd(&n_parts, parts);
+      plan.tiles[s].parts = parts;
+      plan.tiles[s].sums = atomicAdd(&n_parts, parts);
       plan.split[atomicAdd(&n_split, 1)] = s;
     }
     atomicAdd(&count[bucket((n + parts - 1) / parts)], parts);
@@ -573,19 +580,16 @@ __device__ __forceinline__ void plan_dkv(const AttnView& a, const DkvPlan& plan,
   for (int s = threadIdx.x; s < n_slots; s += kThreads) {
     const int n = plan.blocks[s];
     if (n < 0) continue;
-    const int parts = plan.parts[s];
-    int at = atomicAdd(&start[bucket((n + parts - 1) / parts)], parts);
-    for (int p = 0; p < parts; ++p, ++at) {
-      plan.items[2 * at] = s;
-      plan.items[2 * at + 1] = p;
-    }
+    DkvRecord r = plan.tiles[s];   // this thread wrote it
+    int at = atomicAdd(&start[bucket((n + r.parts - 1) / r.parts)], r.parts);
+    for (; r.part < r.parts; ++r.part, ++at) plan.items[at] = r;
   }
 }
 
 // dk and dv: one key a column; the queries that see them (of every head of the
 // group) go through LDS.  An item is a key tile or a part of one.
 struct DkvItem : Segment {
-  int slot, part, parts, hk;
+  int part, parts, sums, hk;
   int64_t h0;              // the head of the item's first block
   int n, ln;               // its blocks, and the first one's number within its head
   int b_lo, per_head;      // see QueryBlocks
@@ -594,14 +598,12 @@ struct DkvItem : Segment {
   int whole_lo, whole_n;   // of a head's blocks, those whose every query sees all of the wave's keys
   int seen_lo, seen_hi;    // and those of which some query sees some of them: [seen_lo, seen_hi)
   // False where there is no such item; `group`: which 32 keys of the tile the wave has.
-  __device__ __forceinline__ bool find(const AttnView& a, const DkvPlan& plan, int group_of_wave, int* err) {
+  __device__ __forceinline__ bool find(const AttnView& a, const DkvPlan& plan, int group_of_wave) {
     const int item = uniform(static_cast<int>(blockIdx.x) / a.n_kv_heads);
+    const DkvRecord r = plan.items[item];
     if (item >= plan.head[0]) return false;
     hk = static_cast<int>(blockIdx.x) - item * a.n_kv_heads;
-    slot = uniform(plan.items[2 * item]);
-    part = uniform(plan.items[2 * item + 1]);
-    parts = uniform(plan.parts[slot]);
-    if (!Segment::find(a, a.cu_k, plan.rows_log2, slot, err)) return false;
+    take(r);
     wkey = first + 32 * group_of_wave;
     key = wkey + (threadIdx.x & 31);
     in = key < nk;
@@ -623,6 +625,17 @@ struct DkvItem : Segment {
     seen_lo = max(wkey - past, 0) / 32 - b_lo;
     seen_hi = wkey < nk ? (end + 31) / 32 - b_lo : 0;
     return true;
+  }
+  __device__ __forceinline__ void take(const DkvRecord& r) {
+    part = uniform(r.part);
+    parts = uniform(r.parts);
+    sums = uniform(r.sums);
+    q0 = uniform(r.q0);
+    k0 = uniform(r.k0);
+    nq = uniform(r.nq);
+    nk = uniform(r.nk);
+    past = nk - nq;
+    first = uniform(r.first);
   }
   __device__ __forceinline__ bool whole(int b) const {
     return static_cast<unsigned>(b - whole_lo) < static_cast<unsigned>(whole_n);
@@ -655,34 +668,32 @@ __device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& sta
 
 // 32 keys of a split tile a workgroup, 32 dims of dk or dv a wave.
 template <typename T, int DP>
-__global__ __launch_bounds__(4 * DP) void attn_dkv_join_kernel(AttnView a, RowStats stats, DkvPlan plan, int* err) {
+__global__ __launch_bounds__(4 * DP) void attn_dkv_join_kernel(AttnView a, RowStats stats, DkvPlan plan) {
   constexpr int kDT = Tile<T, DP>::kDT, kTiles = 2 * kDT, kBatch = 8;
   const int groups = 1 << (plan.rows_log2 - 5);
   const int id = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - id * groups;
   const int split = id / a.n_kv_heads;
   if (split >= plan.head[1]) return;
-  const int slot = uniform(plan.split[split]), parts = uniform(plan.parts[slot]);
   DkvItem w;
-  if (!w.Segment::find(a, a.cu_k, plan.rows_log2, slot, err)) return;
+  w.take(plan.tiles[uniform(plan.split[split])]);
   w.hk = id - split * a.n_kv_heads;
   w.wkey = w.first + 32 * group;
   w.key = w.wkey + (threadIdx.x & 31);
   w.in = w.key < w.nk;
   if (w.wkey >= w.nk) return;
   const int tile = wave_id();
-  const int64_t first = plan.first[slot];
   f32x16_t x = {};
-  for (int u0 = 0; u0 < parts; u0 += kBatch) {
+  for (int u0 = 0; u0 < w.parts; u0 += kBatch) {
     f32x4_t v[kBatch][4];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const f32x4_t* from = part_sums<kTiles>(plan, first + min(u0 + i, parts - 1), w.hk, a.n_kv_heads, group);
+      const f32x4_t* from = part_sums<kTiles>(plan, w.sums + min(u0 + i, w.parts - 1), w.hk, a.n_kv_heads, group);
 #pragma unroll
       for (int g = 0; g < 4; ++g) v[i][g] = from[(tile * 4 + g) * 64];
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float f = u0 + i < parts ? 1.0f : 0.0f;   // past the last part: that one again, times zero
+      const float f = u0 + i < w.parts ? 1.0f : 0.0f;   // past the last part: that one again, times zero
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -755,11 +766,11 @@ struct BwdSpace {
 };
 
 template <typename T, int DP>
-inline hipError_t launch_dkv_join(const AttnView& a, const BwdSpace& b, hipStream_t s, int* err) {
+inline hipError_t launch_dkv_join(const AttnView& a, const BwdSpace& b, hipStream_t s) {
   const int64_t tiles = b.plan.max_parts / 2;   // split ones have two parts or more
   if (tiles == 0) return hipSuccess;
   attn_dkv_join_kernel<T, DP>
-      <<<static_cast<unsigned>((tiles * a.n_kv_heads) << (b.plan.rows_log2 - 5)), 4 * DP, 0, s>>>(a, b.stats, b.plan, err);
+      <<<static_cast<unsigned>((tiles * a.n_kv_heads) << (b.plan.rows_log2 - 5)), 4 * DP, 0, s>>>(a, b.stats, b.plan);
   return hipGetLastError();
 }
 
