@@ -12,11 +12,9 @@
 // product), forward and backward, beside tiles of 128 queries whose waves share
 // the blocks that a workgroup loads:
 //   512 tokens, 4 heads of 64:         12 + 33 us;     28 + 79
-//   8 x 1024 tokens, 8 heads of 64:    130 + 415 us;   141 + 492
-//   4 x 2048 tokens, 16 heads of 128:  816 + 2402 us (84, 100 TFLOP/s);
+//   8 x 1024 tokens, 8 heads of 64:    121 + 408 us;   141 + 492
+//   4 x 2048 tokens, 16 heads of 128:  750 + 2415 us (92, 100 TFLOP/s);
 //                                      749 + 2613
-// The larger tiles read keys and values a quarter as often, which only the
-// forward of long sequences of wide heads gains by, 9% of it.
 #include "attn_seq.h"
 
 namespace staple {
@@ -41,13 +39,18 @@ struct F32Shape {
   static constexpr int kBlock = 32 * Tile<F32, DP>::kRow;
   static constexpr int kPerWave = 2 * kBlock + 512;   // two blocks, two rows of statistics
   static constexpr int kLds = kWaves * kPerWave;
+  // The forward of wide heads holds one block a wave, keys and values in turn:
+  // what a wave then waits for its loads the second workgroup of the CU uses.  2
+  // x 4096 tokens, 16 heads of 128, window 1024: 592 us; 777 with two blocks a
+  // wave and one workgroup.
+  static constexpr bool kTurns = DP > 64;
+  static constexpr int kFwdPerWave = kTurns ? kBlock : kPerWave, kFwdLds = kWaves * kFwdPerWave;
 };
 
 // Adds the waves' parts x[0 .. N) (each times the wave's own factor `mine`): a
 // wave gets results wave_id(), wave_id() + 4, ... in out[].
-template <int DP, int N>
+template <int DP, int kPerWave, int N>
 __device__ __forceinline__ void join_waves(char* smem, const f32x16_t (&x)[N], float mine, f32x16_t (&out)[(N + kWaves - 1) / kWaves]) {
-  constexpr int kPerWave = F32Shape<DP>::kPerWave;
   static_assert(N * 64 * 64 <= kPerWave, "the parts lie where the blocks were");
   const int lane = threadIdx.x & 63, w = wave_id();
   __syncthreads();
@@ -75,10 +78,12 @@ __device__ __forceinline__ void join_waves(char* smem, const f32x16_t (&x)[N], f
 
 // ------------------------------------------------------------------- forward
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
-  constexpr int kBlock = F32Shape<DP>::kBlock;
+  using Shape = F32Shape<DP>;
+  constexpr bool kTurns = Shape::kTurns;
+  constexpr int kUnder = kTurns ? 0 : Loader::kPer;   // loads that may be under way when a block is read
   extern __shared__ __align__(1024) char smem[];
   __shared__ float tops[kWaves][32], sums[kWaves][32];
   check_offsets(a, err);
@@ -92,8 +97,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
     if (part >= shares) return;
   }
   const int lane = threadIdx.x & 63, wave = wave_id();
-  lds_char* const kt = (lds_char*)smem + wave * F32Shape<DP>::kPerWave;
-  lds_char* const vt = kt + kBlock;
+  lds_char* const kt = (lds_char*)smem + wave * Shape::kFwdPerWave;
+  lds_char* const vt = kTurns ? kt : kt + Shape::kBlock;
   Loader kl, vl;
   kl.init(a.k, w.k0, w.nk, w.hk, a.head_dim, 0);
   vl.init(a.v, w.k0, w.nk, w.hk, a.head_dim, 0);
@@ -102,14 +107,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   const float c = load_queries<F32, DP>(a, w, qf);
   f32x16_t o[TL::kDT] = {};
   ColumnSoftmax sm;
-  vl.load(keys.first(wave), vt);
+  if constexpr (!kTurns) vl.load(keys.first(wave), vt);
   for (int b = wave; b < keys.n; b += kWaves) {
-    loads_done<Loader::kPer>();   // K; V may be under way
+    loads_done<kUnder>();   // K
     f32x16_t s = {};
 #pragma unroll
     for (int st = 0; st < TL::kSteps; ++st) s = mma16(TL::row_frag(kt, 0, st), qf[st], s, F32{});
     lds_reads_done();
-    kl.load(keys.first(b + kWaves), kt);
+    if constexpr (kTurns) vl.load(keys.first(b), vt);
+    else kl.load(keys.first(b + kWaves), kt);
     if (!keys.whole(b)) mask_keys(a, w, keys.first(b), s);
     float keep;
     if (sm.raise(s, c, &keep)) {
@@ -124,11 +130,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
     }
     Column<F32> p;
     p.set(s);
-    loads_done<Loader::kPer>();   // V; the next K may be under way
+    loads_done<kUnder>();   // V
 #pragma unroll
     for (int d = 0; d < TL::kDT; ++d) o[d] = mma_transposed<DP>(vt, 0, d, p, o[d]);
     lds_reads_done();
-    vl.load(keys.first(b + kWaves), vt);
+    if constexpr (kTurns) kl.load(keys.first(b + kWaves), kt);
+    else vl.load(keys.first(b + kWaves), vt);
   }
   loads_done<0>();   // none outlives the workgroup
   // the waves' references and sums, then their values relative to the largest
@@ -145,7 +152,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_f32_kernel(AttnView a
   for (int u = 0; u < kWaves; ++u) total += sums[u][lane & 31] * rebase(tops[u][lane & 31], sums[u][lane & 31], top);
   constexpr int kOut = (TL::kDT + kWaves - 1) / kWaves;
   f32x16_t out[kOut];
-  join_waves<DP>(smem, o, rebase(sm.top, sum, top), out);
+  join_waves<DP, Shape::kFwdPerWave>(smem, o, rebase(sm.top, sum, top), out);
   if (shares == 1) return finish_dims<F32, DP>(a, w, kWaves, top, total, out);
   if (wave == 0) parts.put_rows(blockIdx.x, top, total);
 #pragma unroll
@@ -225,7 +232,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dq_f32_kernel(AttnView a,
   loads_done<0>();
   constexpr int kOut = (TL::kDT + kWaves - 1) / kWaves;
   f32x16_t out[kOut];
-  join_waves<DP>(smem, dq, 1.0f, out);
+  join_waves<DP, F32Shape<DP>::kPerWave>(smem, dq, 1.0f, out);
   if (shares == 1) return finish_dq_dims<F32, DP>(a, w, kWaves, out);
 #pragma unroll
   for (int i = 0; i < kOut; ++i)
@@ -321,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
   }
   constexpr int kOut = 2 * TL::kDT / kWaves;
   f32x16_t out[kOut];
-  join_waves<DP>(smem, x, 1.0f, out);
+  join_waves<DP, F32Shape<DP>::kPerWave>(smem, x, 1.0f, out);
   if (w.parts > 1) {
     f32x4_t* to = part_sums<2 * TL::kDT>(plan, w.sums + w.part, w.hk, a.n_kv_heads, 0);
 #pragma unroll
@@ -347,7 +354,7 @@ template <int DP, bool kWide>
 static hipError_t fwd_launch(const AttnView& a, const KeyParts& parts, hipStream_t s, int* err) {
   const int64_t n = tile_slots(a.total_q, a.n_seqs, kF32RowsLog2);
   const hipError_t e =
-      launch_lds<attn_fwd_f32_kernel<DP, kWide>, F32Shape<DP>::kLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
+      launch_lds<attn_fwd_f32_kernel<DP, kWide>, F32Shape<DP>::kFwdLds>(n * a.n_heads * parts.n, s, a, n, parts, err);
   return e != hipSuccess ? e : launch_join<F32, DP, false>(a, kF32RowsLog2, n, parts, s, err);
 }
 
