@@ -1,0 +1,48 @@
+"""Host-side arithmetic of the attention and cache entry points at the ends of
+their arguments' ranges: nothing is enqueued."""
+import ctypes
+import os
+
+import pytest
+
+P = 256   # an aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    from token_indexed_ffn_amd import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libstaple.so is not built (run `python -m token_indexed_ffn_amd.build`)")
+    _lib.load()
+    return _lib
+
+
+def cache(L, **change):
+    f = dict(n_layers=1, n_pages=8, n_kv_heads=16, page_size=16, head_dim=128, n_rows=64, max_pages=4096, dtype=1,
+             k_pages=P, v_pages=P, refs=P, table=P, lens=P)
+    f.update(change)
+    return L.Kv(**f)
+
+
+def decode(L, **change):
+    f = dict(n_seqs=2, n_heads=16, max_len=65536, window=0, sinks=0, scale=0.1, seqs=None, q=L.Heads(P, 2048, 128),
+             k_new=L.Heads(None, 0, 0), v_new=L.Heads(None, 0, 0), o=L.Heads(P, 2048, 128), lse=None)
+    f.update(change)
+    return L.AttnDecode(**f)
+
+
+def decode_bytes(L, **change):
+    return L.load().staple_attn_decode_workspace_bytes(ctypes.byref(cache(L)), ctypes.byref(decode(L, **change)))
+
+
+FAR = 2 ** 63 - 1
+
+
+@pytest.mark.parametrize("n_seqs", [1, 2, 64])
+@pytest.mark.parametrize("max_len", [1, 64, 1000, 65536])
+def test_a_window_that_hides_nothing_splits_like_none(L, n_seqs, max_len):
+    """The workspace tells how the cache is split: a window of max_len keys or more, and as many
+    sinks, leave every key visible."""
+    want = decode_bytes(L, n_seqs=n_seqs, max_len=max_len)
+    for window, sinks in ((max_len, 0), (max_len, 1), (FAR, 0), (FAR, 1), (FAR, FAR), (1, FAR), (2 ** 62, 2 ** 62)):
+        assert decode_bytes(L, n_seqs=n_seqs, max_len=max_len, window=window, sinks=sinks) == want, (window, sinks)

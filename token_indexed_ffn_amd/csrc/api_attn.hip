@@ -120,8 +120,10 @@ static DecodeView view(const staple_kv_t* kv, const staple_attn_decode_t* a) {
   DecodeView v{};
   v.n_seqs = a->n_seqs;
   v.max_len = a->max_len;
-  v.window = a->window;
-  v.sinks = a->sinks;
+  // a window past every position hides nothing; more sinks than positions are all
+  // of them: sums of the two stay far from 64 bits
+  v.window = a->window >= a->max_len ? 0 : a->window;
+  v.sinks = a->sinks < a->max_len ? a->sinks : a->max_len;
   v.n_heads = static_cast<int>(a->n_heads);
   v.group = static_cast<int>(a->n_heads / kv->n_kv_heads);
   v.head_dim = static_cast<int>(kv->head_dim);
