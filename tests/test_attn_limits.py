@@ -46,3 +46,11 @@ def test_a_window_that_hides_nothing_splits_like_none(L, n_seqs, max_len):
     want = decode_bytes(L, n_seqs=n_seqs, max_len=max_len)
     for window, sinks in ((max_len, 0), (max_len, 1), (FAR, 0), (FAR, 1), (FAR, FAR), (1, FAR), (2 ** 62, 2 ** 62)):
         assert decode_bytes(L, n_seqs=n_seqs, max_len=max_len, window=window, sinks=sinks) == want, (window, sinks)
+
+
+@pytest.mark.parametrize("n_seqs", [(1 << 19) + 1, 1 << 60, 1 << 62, FAR])
+def test_decode_refuses_more_rows_than_a_launch_has(L, n_seqs):
+    """Sequences times heads: past 2^23, and past 64 bits in the last three."""
+    lib, c, a = L.load(), ctypes.byref(cache(L)), ctypes.byref(decode(L, n_seqs=n_seqs, seqs=P))
+    assert lib.staple_attn_decode_workspace_bytes(c, a) == 0
+    assert lib.staple_attn_decode_paged(c, a, P, 1 << 40, None) == -2

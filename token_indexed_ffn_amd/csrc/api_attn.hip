@@ -112,7 +112,8 @@ static staple_status_t decode_check(const staple_kv_t* kv, const staple_attn_dec
   REQUIRE(a->window >= 0 && a->sinks >= 0 && std::isfinite(a->scale));
   REQUIRE(a->max_len >= 0 && a->max_len <= kv->max_pages * kv->page_size && a->max_len <= kMaxCount);
   REQUIRE(a->seqs || a->n_seqs <= kv->n_rows);
-  if (a->n_heads > 65535 || a->n_seqs * a->n_heads > kMaxLaunchRows) return STAPLE_ERR_UNSUPPORTED;
+  if (a->n_heads > 65535 || a->n_seqs > kMaxLaunchRows || a->n_seqs * a->n_heads > kMaxLaunchRows)
+    return STAPLE_ERR_UNSUPPORTED;
   return STAPLE_OK;
 }
 
