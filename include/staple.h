@@ -831,7 +831,8 @@ staple_status_t staple_attn_bwd(const staple_attn_t* a, void* ws, size_t ws_byte
  *     entries of row s are its pages;
  *   lens  int32[n_rows]: the tokens of each row's sequence, 0: empty.
  *
- * page_size is a power of two in [16, 1024]; head_dim as in staple_attn_t.
+ * page_size is a power of two in [16, 1024]; head_dim as in staple_attn_t; a
+ * layer's keys of one page take at most 2^31 bytes.
  * Row numbers, pages and lengths out of range set the device error word and
  * are skipped.  Lists of rows (`seqs`, `children`) name each row once.
  * ------------------------------------------------------------------------ */

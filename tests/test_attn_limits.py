@@ -54,3 +54,19 @@ def test_decode_refuses_more_rows_than_a_launch_has(L, n_seqs):
     lib, c, a = L.load(), ctypes.byref(cache(L)), ctypes.byref(decode(L, n_seqs=n_seqs, seqs=P))
     assert lib.staple_attn_decode_workspace_bytes(c, a) == 0
     assert lib.staple_attn_decode_paged(c, a, P, 1 << 40, None) == -2
+
+
+def test_pages_of_more_bytes_than_32_bits_count_are_refused(L):
+    """A page's pieces of 16 bytes are numbered in 32 bits, and so is what lies a stride past the last."""
+    lib, h = L.load(), ctypes.byref(L.Heads(P, 1 << 20, 128))
+    fine = dict(n_kv_heads=8192, page_size=1024, head_dim=128)   # 2^31 bytes in bf16
+    for change in (dict(fine, n_kv_heads=8193), dict(fine, dtype=0), dict(fine, n_kv_heads=65535, dtype=0)):
+        c = ctypes.byref(cache(L, **change))
+        d = ctypes.byref(decode(L, n_heads=change["n_kv_heads"], n_seqs=1))
+        assert lib.staple_kv_append(c, h, h, 1, None, 1, None, None) == -2
+        assert lib.staple_kv_extend(c, P, None, 1, P, 1 << 30, None) == -2
+        assert lib.staple_kv_compact(c, P, P, P, P, 1 << 30, None) == -2
+        assert lib.staple_kv_copy_pages(c, P, P, 1, None) == -2
+        assert lib.staple_attn_decode_paged(c, d, P, 1 << 40, None) == -2
+    c = ctypes.byref(cache(L, **fine))
+    assert lib.staple_kv_copy_pages(c, P, P, 0, None) == 0 and lib.staple_kv_extend(c, P, None, 0, P, 0, None) == 0

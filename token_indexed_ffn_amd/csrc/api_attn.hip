@@ -11,6 +11,7 @@ namespace staple {
 constexpr int64_t kMaxCount = 0x7fffffffll;
 // Rows of one launch: workgroups times threads stay below 2^32.
 constexpr int64_t kMaxLaunchRows = int64_t(1) << 23;
+constexpr int64_t kMaxPageBytes = int64_t(1) << 31;
 
 static bool dims_ok(int64_t head_dim) { return head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0; }
 
@@ -79,6 +80,9 @@ static staple_status_t kv_check(const staple_kv_t* kv, bool pools, bool refs, bo
     return STAPLE_ERR_UNSUPPORTED;
   if (kv->n_layers > 16383 || kv->n_pages > kMaxCount || kv->n_kv_heads > 65535 ||
       kv->n_rows > kMaxCount || kv->max_pages > kMaxCount)
+    return STAPLE_ERR_UNSUPPORTED;
+  // a page's 16-byte pieces are numbered in 32 bits, with room for a stride of them
+  if (kv->n_kv_heads * kv->page_size * kv->head_dim * elem_bytes(kv->dtype) > kMaxPageBytes)
     return STAPLE_ERR_UNSUPPORTED;
   if (pools) REQUIRE(kv->k_pages && kv->v_pages && aligned16(kv->k_pages) && aligned16(kv->v_pages));
   if (refs) REQUIRE(kv->refs);
