@@ -900,7 +900,9 @@ staple_status_t staple_kv_copy_pages(const staple_kv_t* kv, const int32_t* src, 
  *     key and value, which the call also writes to position lens - 1 of the
  *     cache (as staple_kv_append would);
  *   max_len: a bound of the lengths, known on the host (<= max_pages
- *     page_size); a longer sequence sets the device error word and is cut.
+ *     page_size); a longer sequence sets the device error word and is cut: its
+ *     query stands at position max_len - 1 of what the cache holds, and its new
+ *     token is neither read nor written.
  * The cache is split along its length over several workgroups where the
  * batch alone does not fill the GPU; their partial results (workspace) are
  * joined in a fixed order.  Uses kv's k_pages, v_pages, table, lens. */

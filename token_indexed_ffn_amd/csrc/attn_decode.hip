@@ -225,7 +225,8 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(KvView kv, 
   const int64_t row = a.seqs ? a.seqs[i] : i;
   const bool row_in = row >= 0 && row < kv.n_rows;
   int64_t len = row_in ? kv.lens[row] : 0;
-  if (!row_in || len < 0 || len > a.max_len) {
+  const bool fits = row_in && len >= 0 && len <= a.max_len;
+  if (!fits) {
     flag_index_error(err);
     len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
   }
@@ -242,8 +243,10 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(KvView kv, 
   src.pages = kv.table + (row_in ? row : 0) * kv.max_pages;
   src.last = len - 1;
   visible_keys(src.last, a.window, a.sinks, &src.sink, &src.lo);
-  src.k_new = a.k_new.data ? a.k_new.data + (i * a.k_new.row_stride + hk * a.k_new.head_stride) * es : nullptr;
-  src.v_new = a.v_new.data ? a.v_new.data + (i * a.v_new.row_stride + hk * a.v_new.head_stride) * es : nullptr;
+  // a sequence that is cut ends in an older token, which keeps its rows
+  const bool has_new = fits && a.k_new.data;
+  src.k_new = has_new ? a.k_new.data + (i * a.k_new.row_stride + hk * a.k_new.head_stride) * es : nullptr;
+  src.v_new = has_new ? a.v_new.data + (i * a.v_new.row_stride + hk * a.v_new.head_stride) * es : nullptr;
   src.write_new = src.k_new != nullptr && ht == 0;
   const DecBlocks blocks(src, B::kKeys);
 
