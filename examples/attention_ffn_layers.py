@@ -140,6 +140,8 @@ class Server:
         self.table = torch.full((rows, max_pages), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
         self.book = (self.refs, self.table, self.lens)
+        # rows that the last growth left as they are: no new token of theirs is written
+        self.refused = torch.zeros(rows, dtype=torch.int32, device="cuda")
         self.layers = []
         for layer in model.layers:
             w = {n: x.detach().to(t).contiguous() for n, x in layer.items()}
@@ -165,10 +167,10 @@ class Server:
         lens = [len(p) for p in prompts]
         cu, rows = offsets(lens), torch.tensor(seqs, dtype=torch.int32, device="cuda")
         st.staple_kv_extend(*self.book, rows, torch.tensor(lens, dtype=torch.int32, device="cuda"), k_pages=self.k,
-                            v_pages=self.v)
+                            v_pages=self.v, refused=self.refused)
 
         def attend(i, q, k, v):
-            st.staple_kv_append(k, v, self.k[i], self.v[i], self.table, self.lens, rows, cu)
+            st.staple_kv_append(k, v, self.k[i], self.v[i], self.table, self.lens, rows, cu, refused=self.refused)
             return st.staple_attn_fwd(q, k, v, cu, cu, **MASK)["o"]
 
         return self.run(torch.cat(prompts), attend)[cu[1:].long() - 1]
@@ -176,20 +178,21 @@ class Server:
     def decode(self, seqs, ids):
         """One more token for each sequence."""
         rows = torch.tensor(seqs, dtype=torch.int32, device="cuda")
-        st.staple_kv_extend(*self.book, rows, k_pages=self.k, v_pages=self.v)
+        st.staple_kv_extend(*self.book, rows, k_pages=self.k, v_pages=self.v, refused=self.refused)
 
         def attend(i, q, k, v):
             return st.staple_attn_decode_paged(q, self.k[i], self.v[i], self.table, self.lens, seqs=rows, k_new=k, v_new=v,
-                                               **MASK)["o"]
+                                               refused=self.refused, **MASK)["o"]
 
         return self.run(ids, attend)
 
     def fork(self, parents, children):
         st.staple_kv_fork(*self.book, torch.tensor(parents, dtype=torch.int32, device="cuda"),
-                          torch.tensor(children, dtype=torch.int32, device="cuda"), page_size=PAGE)
+                          torch.tensor(children, dtype=torch.int32, device="cuda"), page_size=PAGE, refused=self.refused)
 
     def free(self, seqs):
-        st.staple_kv_free(*self.book, torch.tensor(seqs, dtype=torch.int32, device="cuda"), page_size=PAGE)
+        st.staple_kv_free(*self.book, torch.tensor(seqs, dtype=torch.int32, device="cuda"), page_size=PAGE,
+                          refused=self.refused)
 
     def compact(self):
         return int(st.staple_kv_compact(*self.book, self.k, self.v)["n_live"])

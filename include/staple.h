@@ -829,7 +829,14 @@ staple_status_t staple_attn_bwd(const staple_attn_t* a, void* ws, size_t ws_byte
  *   refs  int32[n_pages];
  *   table int32[n_rows][max_pages]: the first ceil(lens[s] / page_size)
  *     entries of row s are its pages;
- *   lens  int32[n_rows]: the tokens of each row's sequence, 0: empty.
+ *   lens  int32[n_rows]: the tokens of each row's sequence, 0: empty;
+ *   refused int32[n_rows], or NULL: 1 where the last staple_kv_extend that named
+ *     the row did not grow it as asked, else 0 (0 too after the row was forked
+ *     into or freed).  New tokens of a row with 1 are written nowhere, so that a
+ *     step whose growth was refused leaves the cache as it was and can be done
+ *     again once there are pages.  With NULL nothing tells the calls that write
+ *     new tokens of a refusal, and they write over the row's last ones: read the
+ *     error word between staple_kv_extend and those calls.
  *
  * page_size is a power of two in [16, 1024]; head_dim as in staple_attn_t; a
  * layer's keys of one page take at most 2^31 bytes.
@@ -842,13 +849,14 @@ typedef struct staple_kv_t {
   int32_t dtype;
   void *k_pages, *v_pages;
   int32_t *refs, *table, *lens;
+  int32_t* refused;
 } staple_kv_t;
 
 /* Writes new tokens' keys and values into one layer's pages (n_layers 1): the
  * rows [cu_new[i], cu_new[i + 1]) of k_new, v_new ([n_new rows] of n_kv_heads)
  * are the last tokens of sequence seqs[i], whose lens already counts them.
  * cu_new NULL: one row each, row i for seqs[i].  seqs NULL: row i of the table.
- * Uses k_pages, v_pages, table, lens. */
+ * Uses k_pages, v_pages, table, lens, refused. */
 staple_status_t staple_kv_append(const staple_kv_t* kv, const staple_heads_t* k_new,
                                  const staple_heads_t* v_new, int64_t n_new, const int32_t* seqs,
                                  int64_t n_seqs, const int32_t* cu_new, void* stream);
@@ -859,20 +867,21 @@ staple_status_t staple_kv_append(const staple_kv_t* kv, const staple_heads_t* k_
  * in its place, with the slots in use copied in every layer (copy on write);
  * then one page for every further page_size tokens.  Free pages go out lowest
  * index first, to seqs[0] first.  Needs every page at once: where too few are
- * free, or a row would pass max_pages, nothing changes and the device error
- * word reports STAPLE_ERR_NO_PAGES.  n_seqs <= 4096. */
+ * free, or a row would pass max_pages, nothing but `refused` changes and the
+ * device error word reports STAPLE_ERR_NO_PAGES.  n_seqs <= 4096. */
 size_t staple_kv_extend_workspace_bytes(const staple_kv_t* kv, int64_t n_seqs);
 staple_status_t staple_kv_extend(const staple_kv_t* kv, const int32_t* seqs, const int32_t* n_new,
                                  int64_t n_seqs, void* ws, size_t ws_bytes, void* stream);
 
 /* Makes the empty row children[i] share parents[i]'s pages (a parent may be
  * named more than once, but not among the children).  A child that is not
- * empty sets the device error word and is skipped.  Uses refs, table, lens. */
+ * empty sets the device error word and is skipped.  Uses refs, table, lens,
+ * refused. */
 staple_status_t staple_kv_fork(const staple_kv_t* kv, const int32_t* parents,
                                const int32_t* children, int64_t n, void* stream);
 
 /* Ends sequences: each page of row seqs[i] loses a reference, the row's
- * entries become -1 and its length 0.  Uses refs, table, lens. */
+ * entries become -1 and its length 0.  Uses refs, table, lens, refused. */
 staple_status_t staple_kv_free(const staple_kv_t* kv, const int32_t* seqs, int64_t n, void* stream);
 
 /* Packs the live pages into the pool's low end: with n_live pages live, the
@@ -898,14 +907,15 @@ staple_status_t staple_kv_copy_pages(const staple_kv_t* kv, const int32_t* src, 
  *     (seqs NULL: row i); lse float[n_seqs x n_heads] or NULL;
  *   k_new, v_new: NULL data, or n_seqs rows of n_kv_heads: the new token's
  *     key and value, which the call also writes to position lens - 1 of the
- *     cache (as staple_kv_append would);
+ *     cache (as staple_kv_append would).  The new token of a row whose growth
+ *     was refused is neither read nor written;
  *   max_len: a bound of the lengths, known on the host (<= max_pages
  *     page_size); a longer sequence sets the device error word and is cut: its
  *     query stands at position max_len - 1 of what the cache holds, and its new
  *     token is neither read nor written.
  * The cache is split along its length over several workgroups where the
  * batch alone does not fill the GPU; their partial results (workspace) are
- * joined in a fixed order.  Uses kv's k_pages, v_pages, table, lens. */
+ * joined in a fixed order.  Uses kv's k_pages, v_pages, table, lens, refused. */
 typedef struct staple_attn_decode_t {
   int64_t n_seqs, n_heads, max_len, window, sinks;
   float scale;

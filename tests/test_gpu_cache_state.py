@@ -45,3 +45,77 @@ def test_decode_of_a_sequence_past_the_bound_leaves_the_cache(st, dtype, max_len
     (o, lse), (bo, bl) = decode_ref(dtype, q, want_k, want_v, table, ints([max_len, max_len]), 0, 0, d ** -0.5)
     check(to_np(got["o"]), o, bo, "o")
     check(to_np(got["lse"]), lse, bl, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_refused_step_leaves_the_cache_and_can_be_done_again(st, dtype):
+    """Beams of one parent, with a shared, partly filled last page, and a row that fills its page
+    run out of pages: neither an append nor an attention call of the same step writes anything.
+    With pages freed, the same step gives what it gives in a pool that was large enough."""
+    import torch
+    h, hk, d, page, layers = 4, 2, 64, 16, 2
+    lens = [21, 16, 30, 0, 0]
+    kids = ints([3, 4])
+
+    def cache(more):
+        k, v, table, ln, refs = make_cache(dtype, lens, hk, d, page, 220, width=3, spare=2, layers=layers)
+        k, v = (torch.cat([t, torch.full_like(t[:, :more], float("nan"))], dim=1) for t in (k, v))
+        refs = torch.cat([refs, torch.zeros_like(refs[:more])])
+        refused = torch.full((5,), 7, dtype=torch.int32, device="cuda")
+        st.staple_kv_fork(refs, table, ln, ints([0, 0]), kids, page_size=page, refused=refused)
+        assert refused.tolist() == [7, 7, 7, 0, 0]
+        refused[:] = 0
+        return k, v, table, ln, refs, refused
+
+    rows = ints([0, 3, 4, 1])
+    q, kn, vn = (rand((layers, 4, n, d), dtype, 221 + i) for i, n in enumerate((h, hk, hk)))
+
+    def step(c, how):
+        k, v, table, ln, refs, refused = c
+        st.staple_kv_extend(refs, table, ln, rows, k_pages=k, v_pages=v, refused=refused)
+        for i in range(layers):
+            if how == "append":
+                st.staple_kv_append(kn[i], vn[i], k[i], v[i], table, ln, rows, refused=refused)
+                got = st.staple_attn_decode_paged(q[i], k[i], v[i], table, ln, seqs=rows, refused=refused)
+            else:
+                got = st.staple_attn_decode_paged(q[i], k[i], v[i], table, ln, seqs=rows, k_new=kn[i], v_new=vn[i],
+                                                  refused=refused)
+        return got
+
+    for how in ("append", "attend"):
+        print(dtype, how, flush=True)
+        c = cache(0)   # two pages are free and the step needs four: three copies on write, and one page more
+        before = [t.clone() for t in c]
+        step(c, how)
+        assert st.staple_get_device_error() == -8
+        assert c[5].tolist() == [1, 1, 0, 1, 1]
+        for name, a, b in zip(("k", "v", "table", "lens", "refs"), c, before):
+            assert torch.equal(a.float().nan_to_num(7), b.float().nan_to_num(7)), name
+        st.staple_kv_free(c[4], c[2], c[3], ints([2]), page_size=page, refused=c[5])
+        got = step(c, how)
+        assert st.staple_get_device_error() == 0 and c[5].tolist() == [0] * 5
+        large = cache(6)
+        want = step(large, how)
+        assert torch.equal(got["o"], want["o"]) and torch.equal(got["lse"], want["lse"])
+        for s in (0, 1, 3, 4):
+            n = int(c[3][s])
+            assert n == int(large[3][s])
+            for a, b in ((c[0], large[0]), (c[1], large[1])):
+                one, two = (t[:, tab[s].long()[:2]].transpose(2, 3).flatten(1, 2)[:, :n]
+                            for t, tab in ((a, c[2]), (b, large[2])))
+                assert torch.equal(one, two), (how, s)
+
+
+def test_growth_marks_the_rows_that_it_leaves(st):
+    """Rows that ask for nothing are never marked; bad counts and lengths are, the others grow."""
+    import torch
+    k, v, table, ln, refs = make_cache("bf16", [16, 5, 30, 9], 1, 8, 16, 230, width=3, spare=3, layers=1)
+    ln[3] = -2
+    refused = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    st.staple_kv_extend(refs, table, ln, ints([0, 1, 2, 3, 9]), ints([0, -1, 1, 1, 1]), k_pages=k, v_pages=v, refused=refused)
+    assert st.staple_get_device_error() == -5
+    assert refused.tolist() == [0, 1, 0, 1] and ln.tolist() == [16, 5, 31, -2]
+    st.staple_kv_extend(refs, table, ln, ints([0, 1]), ints([33, 0]), k_pages=k, v_pages=v, refused=refused)   # past its width
+    assert st.staple_get_device_error() == -8 and refused.tolist() == [1, 0, 0, 1] and ln.tolist() == [16, 5, 31, -2]
+    with pytest.raises(ValueError):
+        st.staple_kv_extend(refs, table, ln, ints([0]), k_pages=k, v_pages=v, refused=refused[:3])

@@ -924,7 +924,7 @@ def staple_attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
 
 
 def _kv(refs=None, table=None, lens=None, k_pages=None, v_pages=None,
-        page_size: Optional[int] = None) -> _lib.Kv:
+        page_size: Optional[int] = None, refused=None) -> _lib.Kv:
     """staple_kv_t of a cache: pools [layers, pages, kv heads, page size, head_dim] or one
     layer's [pages, kv heads, page size, head_dim]."""
     layers, pages, hk, size, d, dt, kp, vp = 1, 1, 1, page_size, 8, F32, None, None
@@ -948,17 +948,19 @@ def _kv(refs=None, table=None, lens=None, k_pages=None, v_pages=None,
             raise ValueError("table is [rows, max pages]")
         rows, width = table.shape
         table, lens = _ints(table, "table"), _ints(lens, "lens", rows)
-    return _lib.Kv(layers, pages, hk, size, d, rows, width, dt, kp, vp, refs, table, lens)
+    return _lib.Kv(layers, pages, hk, size, d, rows, width, dt, kp, vp, refs, table, lens,
+                   None if refused is None else _ints(refused, "refused", rows))
 
 
 def staple_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
                      v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                      seqs: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None, *,
-                     stream=None) -> None:
+                     refused: Optional[torch.Tensor] = None, stream=None) -> None:
     """Writes the last tokens of sequences (table rows) `seqs` into one layer's pages: rows
     [cu_new[i], cu_new[i + 1]) of k_new, v_new are sequence seqs[i]'s (cu_new None: one row
-    each; seqs None: row i).  lens already counts them."""
-    kv = _kv(None, table, lens, k_pages, v_pages)
+    each; seqs None: row i).  lens already counts them.  refused: see staple_kv_extend; its
+    rows' tokens are not written."""
+    kv = _kv(None, table, lens, k_pages, v_pages, refused=refused)
     n = k_new.shape[0]
     hk, d = k_pages.shape[-3], k_pages.shape[-1]
     n_seqs = cu_new.numel() - 1 if cu_new is not None else n
@@ -972,12 +974,17 @@ def staple_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Te
 def staple_kv_extend(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                      seqs: torch.Tensor, n_new: Optional[torch.Tensor] = None, *,
                      k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     refused: Optional[torch.Tensor] = None,
                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Grows each sequence seqs[i] by n_new[i] tokens (None: one), with pages of its own for
     them: a shared, partly filled last page is copied in every layer, further pages come
     from the free ones, lowest index first.  Too few pages: nothing changes, and
-    staple_get_device_error reports it."""
-    kv = _kv(refs, table, lens, k_pages, v_pages)
+    staple_get_device_error reports it.
+
+    refused: int32 [rows], becomes 1 for each row that was not grown as asked and 0 for the
+    other rows of seqs.  Given to the calls that write new tokens, it keeps them from writing
+    a refused row's over its last ones; without it, read the error first."""
+    kv = _kv(refs, table, lens, k_pages, v_pages, refused=refused)
     n = seqs.numel()
     ws = _ws(lib().staple_kv_extend_workspace_bytes(ctypes.byref(kv), n), workspace, refs.device)
     _check(lib().staple_kv_extend(ctypes.byref(kv), _ints(seqs, "seqs"), _ints(n_new, "n_new", n), n,
@@ -986,18 +993,18 @@ def staple_kv_extend(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor
 
 def staple_kv_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                    parents: torch.Tensor, children: torch.Tensor, *, page_size: int,
-                   stream=None) -> None:
+                   refused: Optional[torch.Tensor] = None, stream=None) -> None:
     """The empty rows children[i] come to share the pages of rows parents[i]."""
-    kv = _kv(refs, table, lens, page_size=page_size)
+    kv = _kv(refs, table, lens, page_size=page_size, refused=refused)
     n = children.numel()
     _check(lib().staple_kv_fork(ctypes.byref(kv), _ints(parents, "parents", n),
                                 _ints(children, "children"), n, _stream(stream)), "staple_kv_fork")
 
 
 def staple_kv_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, seqs: torch.Tensor,
-                   *, page_size: int, stream=None) -> None:
+                   *, page_size: int, refused: Optional[torch.Tensor] = None, stream=None) -> None:
     """Ends sequences: their pages lose a reference, their rows become empty."""
-    kv = _kv(refs, table, lens, page_size=page_size)
+    kv = _kv(refs, table, lens, page_size=page_size, refused=refused)
     _check(lib().staple_kv_free(ctypes.byref(kv), _ints(seqs, "seqs"), seqs.numel(),
                                 _stream(stream)), "staple_kv_free")
 
@@ -1036,14 +1043,15 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
                              k_new: Optional[torch.Tensor] = None,
                              v_new: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
                              window: int = 0, sinks: int = 0, scale: Optional[float] = None,
-                             out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
-                             stream=None) -> dict:
+                             refused: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Attention of one new token per sequence over one layer's pages: o [n, heads,
     head_dim] and lse [n, heads].  Query i belongs to table row seqs[i] (None: row i) and
     stands at position lens - 1.  k_new, v_new [n, kv heads, head_dim]: the new tokens' keys
     and values, also written to the cache.  max_len: a bound of the lengths known on the
-    host (None: the table's width)."""
-    kv = _kv(None, table, lens, k_pages, v_pages)
+    host (None: the table's width).  refused: see staple_kv_extend; its rows' new tokens are
+    neither read nor written."""
+    kv = _kv(None, table, lens, k_pages, v_pages, refused=refused)
     n, h, d = shape = q.shape
     hk, size, dim = k_pages.shape[-3:]
     dt = k_pages.dtype

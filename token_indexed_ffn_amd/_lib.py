@@ -127,7 +127,7 @@ class Kv(ctypes.Structure):
     _fields_ = ([(n, c_i64) for n in ("n_layers", "n_pages", "n_kv_heads", "page_size", "head_dim",
                                       "n_rows", "max_pages")] +
                 [("dtype", c_i32)] +
-                [(n, c_vp) for n in ("k_pages", "v_pages", "refs", "table", "lens")])
+                [(n, c_vp) for n in ("k_pages", "v_pages", "refs", "table", "lens", "refused")])
 
 
 class AttnDecode(ctypes.Structure):

@@ -97,6 +97,7 @@ static KvView view(const staple_kv_t* kv) {
   v.refs = kv->refs;
   v.table = kv->table;
   v.lens = kv->lens;
+  v.refused = kv->refused;
   v.n_layers = kv->n_layers;
   v.n_pages = kv->n_pages;
   v.n_rows = kv->n_rows;

@@ -243,8 +243,9 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(KvView kv, 
   src.pages = kv.table + (row_in ? row : 0) * kv.max_pages;
   src.last = len - 1;
   visible_keys(src.last, a.window, a.sinks, &src.sink, &src.lo);
-  // a sequence that is cut ends in an older token, which keeps its rows
-  const bool has_new = fits && a.k_new.data;
+  // a sequence that is cut, or was not grown, ends in an older token, which
+  // keeps its rows
+  const bool has_new = a.k_new.data && fits && !was_refused(kv, row);
   src.k_new = has_new ? a.k_new.data + (i * a.k_new.row_stride + hk * a.k_new.head_stride) * es : nullptr;
   src.v_new = has_new ? a.v_new.data + (i * a.v_new.row_stride + hk * a.v_new.head_stride) * es : nullptr;
   src.write_new = src.k_new != nullptr && ht == 0;

@@ -20,9 +20,13 @@ struct KvView {
   int32_t* refs;
   int32_t* table;
   int32_t* lens;
+  int32_t* refused;        // or null
   int64_t n_layers, n_pages, n_rows, max_pages;
   int kv_heads, page, page_log2, row_bytes;   // row_bytes: one slot of one head
 };
+
+// Whether row s (in range) was refused its last growth: its new tokens have no place.
+__device__ __forceinline__ bool was_refused(const KvView& kv, int64_t s) { return kv.refused && kv.refused[s] != 0; }
 
 // One page copy: the first `slots` slots of every head; src -1: nothing.
 struct KvCopy {

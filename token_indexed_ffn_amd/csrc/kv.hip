@@ -81,7 +81,10 @@ __global__ __launch_bounds__(256) void kv_free_kernel(KvView kv, const int32_t* 
     row[j] = -1;
   }
   __syncthreads();   // every thread has read the length
-  if (threadIdx.x == 0) kv.lens[s] = 0;
+  if (threadIdx.x == 0) {
+    kv.lens[s] = 0;
+    if (kv.refused) kv.refused[s] = 0;
+  }
 }
 
 __global__ __launch_bounds__(256) void kv_fork_kernel(KvView kv, const int32_t* parents,
@@ -102,7 +105,10 @@ __global__ __launch_bounds__(256) void kv_fork_kernel(KvView kv, const int32_t* 
     to[j] = p;
   }
   __syncthreads();   // every thread has read the child's length
-  if (threadIdx.x == 0 && n > 0) kv.lens[c] = len;
+  if (threadIdx.x == 0) {
+    if (n > 0) kv.lens[c] = len;
+    if (kv.refused) kv.refused[c] = 0;
+  }
 }
 
 // -------------------------------------------------------------------- extend
@@ -122,16 +128,21 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
   __syncthreads();
   const int64_t max_len = min(kv.max_pages << kv.page_log2, static_cast<int64_t>(0x7fffffff));
   int old_len[kPer], new_len[kPer], need[kPer], cow_page[kPer];
+  int asked[kPer];   // the row that is to grow, -1: none
   // sequence i, by thread i % kBookThreads: the loads of one depend on each other
   auto look = [&](int i, int k) {
     row[i] = -1;
     need[k] = 0;
     cow_page[k] = -1;
     old_len[k] = new_len[k] = 0;
+    asked[k] = -1;
     if (i >= n) return;
     const int s = seqs[i];
     const int add = n_new ? n_new[i] : 1;
-    if (s < 0 || s >= kv.n_rows || add < 0) return flag_index_error(err);
+    if (s < 0 || s >= kv.n_rows) return flag_index_error(err);
+    if (add != 0) asked[k] = s;
+    else if (kv.refused) kv.refused[s] = 0;
+    if (add < 0) return flag_index_error(err);
     const int len = kv.lens[s];
     const int64_t held = pages_of_row(kv, len, err);
     if (len < 0 || (len > 0 && held == 0)) return;
@@ -196,7 +207,9 @@ __global__ __launch_bounds__(kBookThreads) void kv_extend_kernel(KvView kv, cons
     const int i = k * kBookThreads + threadIdx.x;
     if (i >= n) break;
     KvCopy c{-1, -1, 0};
-    if (!refuse && row[i] >= 0) {
+    const bool grown = !refuse && row[i] >= 0;
+    if (kv.refused && asked[k] >= 0) kv.refused[asked[k]] = grown ? 0 : 1;
+    if (grown) {
       if (cow_page[k] >= 0) {
         c = KvCopy{cow_page[k], free_list[first[i]], old_len[k] & (kv.page - 1)};
         atomicSub(&kv.refs[cow_page[k]], 1);
@@ -384,7 +397,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvView kv, HeadsView kn,
         fine = fine && pos >= 0 && (pos >> kv.page_log2) < kv.max_pages;
         const int64_t p = fine ? kv.table[s * kv.max_pages + (pos >> kv.page_log2)] : -1;
         if (p < 0 || p >= kv.n_pages) flag_index_error(err);
-        else at = (p * kv.kv_heads * kv.page + (pos & (kv.page - 1))) * kv.row_bytes;
+        else if (!was_refused(kv, s)) at = (p * kv.kv_heads * kv.page + (pos & (kv.page - 1))) * kv.row_bytes;
       }
     }
     dst[threadIdx.x] = at;
