@@ -4,8 +4,11 @@ embedding-augmented gated FFN.
 Each function here has the name of the C entry point it calls and does
 argument marshalling only: it checks tensor placement, allocates outputs with
 torch when the caller passes none, and forwards raw device pointers and the
-current HIP stream to the library.  Every step of the computation runs in the
-library's kernels; there is no Python or CPU fallback.
+current HIP stream, or the one given as `stream`, to the library.  Every step of
+the computation runs in the library's kernels; there is no Python or CPU
+fallback.  What a call allocates (outputs, workspace) belongs to the stream that
+it runs on; tensors that a caller passes are the caller's to keep until that
+stream has used them.
 """
 from __future__ import annotations
 
@@ -69,14 +72,32 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _ws(nbytes: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
+def _own(stream, make, *args):
+    """Tensors that a call returns: make(*args), a tensor or a dict or tuple of them.  Their memory belongs to the stream that the call's kernels run on, so that it is handed
+    out again after those kernels; the current stream, where a caller may read them, is recorded
+    too."""
+    if stream is None:
+        return make(*args)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        made = make(*args)
+    for t in made.values() if isinstance(made, dict) else made if isinstance(made, tuple) else (made,):
+        if t is not None:
+            t.record_stream(here)
+    return made
+
+
+def _ws(nbytes: int, workspace: Optional[torch.Tensor], device, stream) -> Optional[torch.Tensor]:
     if nbytes == 0:
         return workspace
     if workspace is not None:
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"workspace of {nbytes} bytes required")
         return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):   # dropped when the call returns: kernels of this stream alone use it
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _ws_size(w: Optional[torch.Tensor]) -> int:
@@ -114,14 +135,14 @@ def staple_dedup(ids: torch.Tensor, vocab: int, *, out: Optional[dict] = None,
     n = ids.numel()
     dev = ids.device
     if out is None:
-        out = {
+        out = _own(stream, lambda: {
             "uniq": torch.empty(max(n, 1), dtype=torch.int32, device=dev),
             "inv": torch.empty(max(n, 1), dtype=torch.int32, device=dev),
             "sorted_pos": torch.empty(max(n, 1), dtype=torch.int32, device=dev),
             "seg_start": torch.empty(n + 1, dtype=torch.int32, device=dev),
             "n_unique": torch.empty(1, dtype=torch.int32, device=dev),
-        }
-    ws = _ws(lib().staple_dedup_workspace_bytes(n), workspace, dev)
+        })
+    ws = _ws(lib().staple_dedup_workspace_bytes(n), workspace, dev, stream)
     _check(lib().staple_dedup(_p(ids), n, int(vocab), _p(out["uniq"]), _p(out["inv"]),
                               _p(out["sorted_pos"]), _p(out["seg_start"]), _p(out["n_unique"]),
                               _p(ws), _ws_size(ws), _stream(stream)), "staple_dedup")
@@ -132,7 +153,7 @@ def staple_cache_count(ids: torch.Tensor, vocab: int, counts: Optional[torch.Ten
                        stream=None) -> torch.Tensor:
     _dev(ids, counts)
     if counts is None:
-        counts = torch.zeros(vocab, dtype=torch.int64, device=ids.device)
+        counts = _own(stream, lambda: torch.zeros(vocab, dtype=torch.int64, device=ids.device))
     _check(lib().staple_cache_count(_p(ids), ids.numel(), int(vocab), _p(counts), _stream(stream)),
            "staple_cache_count")
     return counts
@@ -145,9 +166,10 @@ def staple_cache_build(counts: torch.Tensor, capacity: int, *, out: Optional[tup
     assert counts.dtype == torch.int64
     vocab = counts.numel()
     if out is None:
-        out = (torch.empty(vocab, dtype=torch.int32, device=counts.device),
-               torch.empty(max(capacity, 1), dtype=torch.int32, device=counts.device))
-    ws = _ws(lib().staple_cache_build_workspace_bytes(vocab), workspace, counts.device)
+        out = _own(stream, lambda: (
+            torch.empty(vocab, dtype=torch.int32, device=counts.device),
+            torch.empty(max(capacity, 1), dtype=torch.int32, device=counts.device)))
+    ws = _ws(lib().staple_cache_build_workspace_bytes(vocab), workspace, counts.device, stream)
     _check(lib().staple_cache_build(_p(counts), vocab, int(capacity), _p(out[0]), _p(out[1]),
                                     _p(ws), _ws_size(ws), _stream(stream)), "staple_cache_build")
     return out
@@ -159,7 +181,8 @@ def staple_cache_fill(table: torch.Tensor, slot_to_id: torch.Tensor, capacity: i
     _dev(slot_to_id, out)
     vocab, d_ff = table.shape
     if out is None:
-        out = torch.empty(max(capacity, 1), d_ff, dtype=table.dtype, device=slot_to_id.device)
+        out = _own(stream, lambda: torch.empty(max(capacity, 1), d_ff, dtype=table.dtype,
+                                               device=slot_to_id.device))
     _check(lib().staple_cache_fill(_p(table), vocab, d_ff, _dt(table), _p(slot_to_id), int(capacity),
                                    _p(out), _stream(stream)), "staple_cache_fill")
     return out
@@ -171,9 +194,9 @@ def staple_cache_lookup(uniq: torch.Tensor, n_unique: torch.Tensor, id_to_slot: 
     _dev(uniq, n_unique, id_to_slot)
     mu = uniq.numel()
     if out is None:
-        out = {k: torch.empty(max(mu, 1), dtype=torch.int32, device=uniq.device)
-               for k in ("code", "miss_uidx", "miss_ids")}
-        out["n_miss"] = torch.empty(1, dtype=torch.int32, device=uniq.device)
+        out = _own(stream, lambda: {k: torch.empty(m, dtype=torch.int32, device=uniq.device) for k, m in
+                                    (("code", max(mu, 1)), ("miss_uidx", max(mu, 1)),
+                                     ("miss_ids", max(mu, 1)), ("n_miss", 1))})
     _check(lib().staple_cache_lookup(_p(uniq), _p(n_unique), mu, _p(id_to_slot), id_to_slot.numel(),
                                      _p(out["code"]), _p(out["miss_uidx"]), _p(out.get("miss_ids")),
                                      _p(out["n_miss"]), _stream(stream)), "staple_cache_lookup")
@@ -187,9 +210,9 @@ def staple_split_tokens(inv: torch.Tensor, code: torch.Tensor, n_unique: torch.T
     n = inv.numel()
     max_unique = min(code.numel(), n)
     if out is None:
-        out = {k: torch.empty(max(n, 1), dtype=torch.int32, device=inv.device)
-               for k in ("hit_pos", "miss_pos", "tok_row")}
-        out["counts"] = torch.empty(2, dtype=torch.int32, device=inv.device)
+        out = _own(stream, lambda: {k: torch.empty(m, dtype=torch.int32, device=inv.device) for k, m in
+                                    (("hit_pos", max(n, 1)), ("miss_pos", max(n, 1)),
+                                     ("tok_row", max(n, 1)), ("counts", 2))})
     _check(lib().staple_split_tokens(_p(inv), n, _p(code), _p(n_unique), max_unique,
                                      _p(out["hit_pos"]), _p(out["miss_pos"]), _p(out["tok_row"]),
                                      _p(out["counts"]), _stream(stream)), "staple_split_tokens")
@@ -256,7 +279,7 @@ def staple_assemble_rows(cache_rows: torch.Tensor, miss_rows: torch.Tensor, code
     d_ff = cache_rows.shape[1]
     mu = code.numel()
     if out is None:
-        out = torch.empty(mu, d_ff, dtype=cache_rows.dtype, device=code.device)
+        out = _own(stream, lambda: torch.empty(mu, d_ff, dtype=cache_rows.dtype, device=code.device))
     _check(lib().staple_assemble_rows(_p(cache_rows), cache_rows.shape[0], _p(miss_rows),
                                       miss_rows.shape[0], _p(code), _p(n_unique), mu, d_ff,
                                       _dt(cache_rows), _p(out), _stream(stream)),
@@ -277,7 +300,7 @@ def staple_assemble_rows_from_table(cache_rows: torch.Tensor, table: torch.Tenso
     mu = uniq.numel()
     cap = cache_rows.shape[0] if capacity is None else capacity
     if out is None:
-        out = torch.empty(max(mu, 1), d_ff, dtype=table.dtype, device=uniq.device)
+        out = _own(stream, lambda: torch.empty(max(mu, 1), d_ff, dtype=table.dtype, device=uniq.device))
     _check(lib().staple_assemble_rows_from_table(_p(cache_rows), cap, _p(table), vocab, _p(uniq),
                                                  _p(code), _p(n_unique), mu, d_ff, _dt(table),
                                                  _p(out), _stream(stream)),
@@ -294,7 +317,7 @@ def staple_gather_rows(src: torch.Tensor, index: torch.Tensor, n_rows: Optional[
     d_ff = src.shape[1]
     mr = index.numel()
     if out is None:
-        out = torch.empty(mr, d_ff, dtype=src.dtype, device=index.device)
+        out = _own(stream, lambda: torch.empty(mr, d_ff, dtype=src.dtype, device=index.device))
     _check(lib().staple_gather_rows(_p(src), src.shape[0], _p(index), _p(n_rows), mr, d_ff,
                                     _dt(src), _p(out), _stream(stream)), "staple_gather_rows")
     return out
@@ -313,11 +336,10 @@ def staple_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: Optional[torch.T
     dt = _dt(x)
     out_dtype = out_dtype or x.dtype
     if out is None:
-        out = {"y": torch.empty(n, d, dtype=out_dtype, device=x.device)}
-        if save:
-            for k in ("g", "u", "h"):
-                out[k] = torch.empty(n, f, dtype=x.dtype, device=x.device)
-    ws = _ws(lib().staple_ffn_fwd_workspace_bytes(n, d, f, dt), workspace, x.device)
+        out = _own(stream, lambda: {"y": torch.empty(n, d, dtype=out_dtype, device=x.device)} |
+                   {k: torch.empty(n, f, dtype=x.dtype, device=x.device)
+                    for k in (("g", "u", "h") if save else ())})
+    ws = _ws(lib().staple_ffn_fwd_workspace_bytes(n, d, f, dt), workspace, x.device, stream)
     _check(lib().staple_ffn_fwd(n, d, f, dt, _DT[out["y"].dtype], _p(x), _p(w_gate), _p(w_up),
                                 _p(w_down), _p(rows), rows.shape[0], _p(row_index), _p(out["y"]),
                                 _p(out.get("g")), _p(out.get("u")), _p(out.get("h")), _p(ws),
@@ -336,10 +358,10 @@ def staple_decode_pack_weights(w_gate: Optional[torch.Tensor], w_up: Optional[to
     ref = next(t for t in (w_gate, w_up, w_down) if t is not None)
     pgu = pd = None
     if w_gate is not None:
-        pgu = torch.empty((1 if w_up is None else 2) * d_ff * d_model, dtype=ref.dtype,
-                          device=ref.device)
+        pgu = _own(stream, lambda: torch.empty((1 if w_up is None else 2) * d_ff * d_model,
+                                               dtype=ref.dtype, device=ref.device))
     if w_down is not None:
-        pd = torch.empty(d_model * d_ff, dtype=ref.dtype, device=ref.device)
+        pd = _own(stream, lambda: torch.empty(d_model * d_ff, dtype=ref.dtype, device=ref.device))
     _check(lib().staple_decode_pack_weights(d_model, d_ff, _dt(ref), _p(w_gate), _p(w_up),
                                             _p(w_down), _p(pgu), _p(pd), _stream(stream)),
            "staple_decode_pack_weights")
@@ -369,11 +391,10 @@ def staple_ffn_fwd_packed(x: torch.Tensor, packed_gate_up: torch.Tensor,
     dt = _dt(x)
     out_dtype = out_dtype or x.dtype
     if out is None:
-        out = {"y": torch.empty(n, d, dtype=out_dtype, device=x.device)}
-        if save:
-            for k in ("g", "u", "h"):
-                out[k] = torch.empty(n, f, dtype=x.dtype, device=x.device)
-    ws = _ws(lib().staple_ffn_fwd_workspace_bytes(n, d, f, dt), workspace, x.device)
+        out = _own(stream, lambda: {"y": torch.empty(n, d, dtype=out_dtype, device=x.device)} |
+                   {k: torch.empty(n, f, dtype=x.dtype, device=x.device)
+                    for k in (("g", "u", "h") if save else ())})
+    ws = _ws(lib().staple_ffn_fwd_workspace_bytes(n, d, f, dt), workspace, x.device, stream)
     _check(lib().staple_ffn_fwd_packed(n, d, f, dt, _DT[out["y"].dtype], _p(x), _p(packed_gate_up),
                                        up, _p(packed_down), _p(rows), rows.shape[0], _p(row_index),
                                        _p(out["y"]), _p(out.get("g")), _p(out.get("u")),
@@ -422,7 +443,7 @@ def staple_ffn_down_packed(h: torch.Tensor, packed_down: torch.Tensor, y: torch.
     _dev(h, packed_down, y)
     n, f = h.shape
     d = y.shape[1]
-    ws = _ws(lib().staple_ffn_down_workspace_bytes(n, d, f, _dt(h)), workspace, h.device)
+    ws = _ws(lib().staple_ffn_down_workspace_bytes(n, d, f, _dt(h)), workspace, h.device, stream)
     _check(lib().staple_ffn_down_packed(n, d, f, _dt(h), _DT[y.dtype], _p(h), _p(packed_down),
                                         _p(y), _p(ws), _ws_size(ws), _stream(stream)),
            "staple_ffn_down_packed")
@@ -466,7 +487,7 @@ def staple_ffn_down(h: torch.Tensor, w_down: torch.Tensor, y: torch.Tensor,
     _dev(h, w_down, y)
     n, f = h.shape
     d = w_down.shape[0]
-    ws = _ws(lib().staple_ffn_down_workspace_bytes(n, d, f, _dt(h)), workspace, h.device)
+    ws = _ws(lib().staple_ffn_down_workspace_bytes(n, d, f, _dt(h)), workspace, h.device, stream)
     _check(lib().staple_ffn_down(n, d, f, _dt(h), _DT[y.dtype], _p(h), _p(w_down), _p(y), _p(ws),
                                  _ws_size(ws), _stream(stream)), "staple_ffn_down")
     return y
@@ -642,7 +663,8 @@ def staple_lowrank_expand(rows_r: torch.Tensor, n_rows: torch.Tensor, proj: torc
     max_rows, r = rows_r.shape
     f = proj.shape[0]
     if out is None:
-        out = torch.empty(max(max_rows, 1), f, dtype=rows_r.dtype, device=rows_r.device)
+        out = _own(stream, lambda: torch.empty(max(max_rows, 1), f, dtype=rows_r.dtype,
+                                               device=rows_r.device))
     _check(lib().staple_lowrank_expand(_p(rows_r), _p(n_rows), max_rows, r, f, _dt(rows_r),
                                        _p(proj), _p(out), _stream(stream)), "staple_lowrank_expand")
     return out
@@ -658,9 +680,10 @@ def staple_lowrank_bwd(d_rows: torch.Tensor, rows_r: torch.Tensor, n_rows: torch
     f = proj.shape[0]
     dev = rows_r.device
     if out is None:
-        out = {"d_rows_r": torch.empty(max(max_rows, 1), r, dtype=torch.float32, device=dev),
-               "d_proj": torch.empty(f, r, dtype=torch.float32, device=dev)}
-    ws = _ws(lib().staple_lowrank_bwd_workspace_bytes(max_rows, f, _dt(rows_r)), workspace, dev)
+        out = _own(stream, lambda: {
+            "d_rows_r": torch.empty(max(max_rows, 1), r, dtype=torch.float32, device=dev),
+            "d_proj": torch.empty(f, r, dtype=torch.float32, device=dev)})
+    ws = _ws(lib().staple_lowrank_bwd_workspace_bytes(max_rows, f, _dt(rows_r)), workspace, dev, stream)
     _check(lib().staple_lowrank_bwd(_p(d_rows), _p(rows_r), _p(n_rows), max_rows, r, f, _dt(rows_r),
                                     _p(proj), _p(out["d_rows_r"]), _p(out["d_proj"]), _p(ws),
                                     _ws_size(ws), _stream(stream)), "staple_lowrank_bwd")
@@ -790,15 +813,15 @@ def staple_ffn_bwd_table_grad(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
     mu = n if max_unique is None else int(max_unique)
     dev = x.device
     if out is None:
-        out = {
+        out = _own(stream, lambda: {
             "d_rows": torch.empty(max(mu, 1), f, dtype=torch.float32, device=dev),
             "dx": torch.empty(n, d, dtype=out_dtype or x.dtype, device=dev),
             "dw_gate": torch.empty(f, d, dtype=torch.float32, device=dev),
             "dw_up": None if freeze_up or w_up is None
             else torch.empty(f, d, dtype=torch.float32, device=dev),
             "dw_down": torch.empty(d, f, dtype=torch.float32, device=dev),
-        }
-    ws = _ws(lib().staple_ffn_bwd_workspace_bytes(n, d, f, dt), workspace, dev)
+        })
+    ws = _ws(lib().staple_ffn_bwd_workspace_bytes(n, d, f, dt), workspace, dev, stream)
     _check(lib().staple_ffn_bwd_table_grad(
         n, d, f, dt, _DT[out["dx"].dtype], _p(dy), _p(x), _p(w_gate), _p(w_up), _p(w_down),
         _p(saved_g), _p(saved_u), _p(saved_h), _p(sorted_pos), _p(inv), _p(seg_start),
@@ -851,6 +874,14 @@ def _like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
+def _rows_out(q: torch.Tensor) -> dict:
+    return {"o": _like(q), "lse": q.new_empty(q.shape[:2], dtype=_FLOAT32)}
+
+
+def _grads_out(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> dict:
+    return {"dq": _like(q), "dk": _like(k), "dv": _like(v)}
+
+
 def _attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do=None, grads=None,
           own=False) -> _lib.Attn:
     """staple_attn_t.  own: the call's outputs (o and lse, or with grads those) were made for it
@@ -898,10 +929,10 @@ def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     their sequence.  scale: head_dim ** -0.5 when None."""
     own = out is None
     if own:
-        out = {"o": _like(q), "lse": q.new_empty(q.shape[:2], dtype=_FLOAT32)}
+        out = _own(stream, _rows_out, q)
     a = ctypes.byref(_attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"], own=own))
     native = lib()
-    ws = _ws(native.staple_attn_fwd_workspace_bytes(a), workspace, q.device)
+    ws = _ws(native.staple_attn_fwd_workspace_bytes(a), workspace, q.device, stream)
     _check(native.staple_attn_fwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_attn_fwd")
     return out
 
@@ -914,11 +945,11 @@ def staple_attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     """Gradients dq, dk, dv of staple_attn_fwd from do, its operands and its o and lse."""
     own = out is None
     if own:
-        out = {"dq": _like(q), "dk": _like(k), "dv": _like(v)}
+        out = _own(stream, _grads_out, q, k, v)
     a = ctypes.byref(_attn(q, k, v, cu_q, cu_k, window, sinks, scale, o, lse, do,
                            (out["dq"], out["dk"], out["dv"]), own))
     native = lib()
-    ws = _ws(native.staple_attn_bwd_workspace_bytes(a), workspace, q.device)
+    ws = _ws(native.staple_attn_bwd_workspace_bytes(a), workspace, q.device, stream)
     _check(native.staple_attn_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_attn_bwd")
     return out
 
@@ -986,7 +1017,7 @@ def staple_kv_extend(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor
     a refused row's over its last ones; without it, read the error first."""
     kv = _kv(refs, table, lens, k_pages, v_pages, refused=refused)
     n = seqs.numel()
-    ws = _ws(lib().staple_kv_extend_workspace_bytes(ctypes.byref(kv), n), workspace, refs.device)
+    ws = _ws(lib().staple_kv_extend_workspace_bytes(ctypes.byref(kv), n), workspace, refs.device, stream)
     _check(lib().staple_kv_extend(ctypes.byref(kv), _ints(seqs, "seqs"), _ints(n_new, "n_new", n), n,
                                   _p(ws), _ws_size(ws), _stream(stream)), "staple_kv_extend")
 
@@ -1020,8 +1051,8 @@ def staple_kv_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tenso
         out.setdefault(name, own)
         _ints(out[name], name, own.numel())
     if "n_live" not in out:
-        out["n_live"] = torch.empty(1, dtype=torch.int32, device=refs.device)
-    ws = _ws(lib().staple_kv_compact_workspace_bytes(ctypes.byref(kv)), workspace, refs.device)
+        out["n_live"] = _own(stream, lambda: torch.empty(1, dtype=torch.int32, device=refs.device))
+    ws = _ws(lib().staple_kv_compact_workspace_bytes(ctypes.byref(kv)), workspace, refs.device, stream)
     _check(lib().staple_kv_compact(ctypes.byref(kv), _p(out["table"]), _p(out["refs"]),
                                    _ints(out["n_live"], "n_live", 1), _p(ws), _ws_size(ws),
                                    _stream(stream)), "staple_kv_compact")
@@ -1052,11 +1083,11 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     host (None: the table's width).  refused: see staple_kv_extend; its rows' new tokens are
     neither read nor written."""
     kv = _kv(None, table, lens, k_pages, v_pages, refused=refused)
-    n, h, d = shape = q.shape
+    n, h, d = q.shape
     hk, size, dim = k_pages.shape[-3:]
     dt = k_pages.dtype
     if out is None:
-        out = {"o": q.new_empty(shape), "lse": q.new_empty((n, h), dtype=torch.float32)}
+        out = _own(stream, _rows_out, q)
         lse, o = out["lse"], (out["o"].data_ptr(), h * d, d)
     else:
         lse, o = out.get("lse"), _heads(out["o"], "o", dt, n, h, d)
@@ -1072,7 +1103,7 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
                         _heads(k_new, "k_new", dt, n, hk, d), _heads(v_new, "v_new", dt, n, hk, d),
                         o, _p(lse))
     kv, a, native = ctypes.byref(kv), ctypes.byref(a), lib()
-    ws = _ws(native.staple_attn_decode_workspace_bytes(kv, a), workspace, q.device)
+    ws = _ws(native.staple_attn_decode_workspace_bytes(kv, a), workspace, q.device, stream)
     _check(native.staple_attn_decode_paged(kv, a, _p(ws), _ws_size(ws), _stream(stream)),
            "staple_attn_decode_paged")
     return out
