@@ -74,3 +74,15 @@ def test_workspaces_come_from_the_stream(pools):
     assert st._ws(100, None, "cuda", "side").pool == "side"
     assert st._ws(100, None, "cuda", None).pool == "current"
     assert st._ws(0, None, "cuda", "side") is None and pools == ["current"]
+
+
+def test_the_current_stream_where_torch_offers_no_raw_handle(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(st.torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(st, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(st, "_current_device", lambda: 3)
+    assert st._stream(None) == 1003 and st._stream(Stream) == 77
+    monkeypatch.setattr(st, "_raw_stream", None)
+    assert st._stream(None) == 77

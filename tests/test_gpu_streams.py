@@ -52,3 +52,16 @@ def test_memory_of_a_call_on_another_stream_is_not_handed_out(st, dtype):
             assert torch.equal(x, y)
         assert all(bool((x == 5).all()) for x in blocks)
     assert st.staple_get_device_error() == 0
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_calls_go_to_the_current_stream(st, raw, monkeypatch):
+    """With and without torch's raw handle of the current stream."""
+    import torch
+    if not raw:
+        monkeypatch.setattr(st, "_raw_stream", None)
+    assert st._stream(None) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert st._stream(None) == side.cuda_stream != torch.cuda.default_stream().cuda_stream
+    assert st._stream(None) == torch.cuda.current_stream().cuda_stream
