@@ -768,6 +768,12 @@ staple_status_t staple_ffn_bwd_table_grad(int64_t n_tokens, int64_t d_model, int
  * Products and sums are fp32 (bf16: from bf16 operands).  bf16 rounds P
  * (and, in the backward, dS) to bf16 as the operand of the next product and
  * o, dq, dk, dv once where they are stored.  The results are deterministic.
+ *
+ * A result that comes out NaN or infinite, without a NaN at its own position
+ * that explains it (a query's statistics, the value or output gradient that it
+ * always meets), is done again over the pairs that are seen, one by one: a row
+ * then takes one or two microseconds a pair.  Infinities in every row, or a chunk's
+ * NaN in keys before its queries, cost that in every row.
  * ------------------------------------------------------------------------ */
 
 /* A [rows][heads][head_dim] operand: row t, head h at data + t row_stride +

@@ -37,7 +37,13 @@ __device__ __forceinline__ void finish_fwd(const AttnView& a, const QueryCols& w
   }
   if (w.in && half == 0)
     a.lse[(w.q0 + w.row) * a.n_heads + w.head] = (sm.top + __builtin_amdgcn_logf(sum)) * kLn2;
-  redo_queries(bad && w.in, [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  bad = bad && w.in && !is_nan(sum);   // a NaN among the weights makes the row NaN
+  if (bad && w.p >= 0) {
+    bad = false;
+#pragma unroll
+    for (int d = 0; d < Tile<T, DP>::kDT; ++d) bad |= !own_value_explains<T>(a, w, d, o[d]);
+  }
+  redo(columns(bad), 0, 1, [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
 }
 
 // bf16.  A block (32 keys x 32 queries at DP 128) is 16 MFMAs, 512 cycles, and
@@ -365,7 +371,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
     for (int r = 0; r < 16; ++r) bad |= not_finite(dq[d][r]);
     store_column<T>(a.dq, w.q0 + w.row, w.head, a.head_dim, d, dq[d], a.scale, w.in);
   }
-  redo_queries(bad && w.in, [&](int i) { attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  // a NaN in the query's statistics makes the row NaN
+  bad = bad && w.in && !(w.p >= 0 && (is_nan(delta) || is_nan(lse2)));
+  redo(columns(bad), 0, 1, [&](int i) { attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
 }
 
 // dk and dv of 32 keys take 2 DP registers a lane, too many beside the
@@ -582,13 +590,12 @@ __global__ __launch_bounds__(64 * kDkvWaves, 2) void attn_dkv_bf16_kernel(AttnVi
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < kHalf; ++d) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) bad |= not_finite(x[d][r]) || not_finite(x[kHalf + d][r]);
+    bad |= has_unexplained<T>(a, stats, w, false, side * kHalf + d, x[d]);
+    bad |= has_unexplained<T>(a, stats, w, true, side * kHalf + d, x[kHalf + d]);
     store_column<T>(a.dk, w.k0 + w.key, w.hk, a.head_dim, side * kHalf + d, x[d], a.scale, w.in);
     store_column<T>(a.dv, w.k0 + w.key, w.hk, a.head_dim, side * kHalf + d, x[kHalf + d], 1.0f, w.in);
   }
-  __syncthreads();   // a row done again is stored after both its halves
-  redo_keys<T>(a, stats, w, bad);
+  redo_keys<T>(a, stats, w, bad, keys_of, 4, 2, side);
 }
 
 // ------------------------------------------------------------------- launches

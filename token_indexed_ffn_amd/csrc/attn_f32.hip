@@ -339,14 +339,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_f32_kernel(AttnView a
 #pragma unroll
   for (int i = 0; i < kOut; ++i) {
     const int d = i * kWaves + wave;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
     const bool value = d >= TL::kDT;
+    bad |= has_unexplained<F32>(a, stats, w, value, value ? d - TL::kDT : d, out[i]);
     store_column<F32>(value ? a.dv : a.dk, w.k0 + w.key, w.hk, a.head_dim, value ? d - TL::kDT : d, out[i], value ? 1.0f : a.scale,
                       w.in);
   }
-  __syncthreads();
-  redo_keys<F32>(a, stats, w, bad);
+  redo_keys<F32>(a, stats, w, bad, 0, 1, kWaves, wave);
 }
 
 // ------------------------------------------------------------------- launches

@@ -271,18 +271,60 @@ __device__ __forceinline__ void mask_keys(const AttnView& a, const QueryCols& w,
   for (int r = 0; r < 16; ++r) s[r] = seen(r) ? s[r] : -INFINITY;
 }
 
-// A NaN or an infinity in a result (`bad`) may have come from a row that the
-// query does not see (its zero weight times it): such queries are done again
-// key by key.
+// A NaN or an infinity in a result may have come from a row that the query does
+// not see (its zero weight times it): such queries are done again key by key,
+// a thousand times slower than the products.  A training step that has gone to
+// NaN must not pay that in every row, so a NaN that the query's own row explains
+// (its statistics, or the value at its own position, which it always sees) is
+// left as it is.  4 x 1024 tokens, 8 heads on 2 of 128, with NaN in one element
+// of every row of q, k, v or d_o take 44 + 123 us, as without; 21 + 156 ms with
+// every such row done again.
+
+// The columns that some lane marks, one a bit.
+__device__ __forceinline__ uint32_t columns(bool bad) {
+  const uint64_t b = __ballot(bad);
+  return static_cast<uint32_t>(b) | static_cast<uint32_t>(b >> 32);
+}
+// What the n waves first, first + step, ... have marked; their results are
+// stored by then.
+__device__ __forceinline__ uint32_t join_marks(uint32_t mine, int first, int step, int n) {
+  __shared__ uint32_t marks[8];
+  if ((threadIdx.x & 63) == 0) marks[wave_id()] = mine;
+  __syncthreads();
+  uint32_t all = 0;
+  for (int u = 0; u < n; ++u) all |= marks[first + u * step];
+  return uniform(all);
+}
+// Does every n-th marked column again, from the turn-th on.
 template <typename RowFn>
-__device__ __forceinline__ void redo_queries(bool bad, RowFn row) {
-  uint64_t again = __ballot(bad);
-  again = (again | (again >> 32)) & 0xffffffffull;
-  while (again) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    row(i);
+__device__ __forceinline__ void redo(uint32_t marked, int turn, int n, RowFn row) {
+  for (int i = 0; marked; ++i, marked &= marked - 1)
+    if (i % n == turn) row(__builtin_ctz(marked));
+}
+
+// Elements e .. e + 3 of a head's row.
+template <typename T>
+__device__ __forceinline__ f32x4_t load4(const HeadsView& t, int64_t row, int64_t head, int e) {
+  const T* p = reinterpret_cast<const T*>(t.data) + row * t.row_stride + head * t.head_stride;
+  return f32x4_t{Elem<T>::load(p, e), Elem<T>::load(p, e + 1), Elem<T>::load(p, e + 2), Elem<T>::load(p, e + 3)};
+}
+__device__ __forceinline__ bool is_nan(float x) { return x != x; }
+
+// Whether every element of x (32 dims of the lane's query, as store_column has
+// them) that is not finite is a NaN where the value at the query's own position
+// is one.
+template <typename T>
+__device__ __forceinline__ bool own_value_explains(const AttnView& a, const QueryCols& w, int d, const f32x16_t& x) {
+  bool fine = true;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int e = d * 32 + 8 * g + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+    if (e >= a.head_dim) continue;
+    const f32x4_t v = load4<T>(a.v, w.k0 + w.p, w.hk, e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fine &= !not_finite(x[4 * g + i]) | (is_nan(x[4 * g + i]) & is_nan(v[i]));
   }
+  return fine;
 }
 
 // A tile's keys in parts, where there are too few tiles to occupy the GPU: each
@@ -335,14 +377,24 @@ __device__ __forceinline__ void finish_dims(const AttnView& a, const QueryCols& 
     for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
     store_column<T>(a.o, w.q0 + w.row, w.head, a.head_dim, d, out[i], inv, w.in);
   }
+  bad = bad && w.in && !is_nan(total);   // a NaN among the weights makes the row NaN
+  if (bad && w.p >= 0) {
+    bad = false;
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+      const int d = i * n_waves + wave_id();
+      if (d < Tile<T, DP>::kDT) bad |= !own_value_explains<T>(a, w, d, out[i]);
+    }
+  }
   if (wave_id() == 0 && w.in && (threadIdx.x & 63) < 32)
     a.lse[(w.q0 + w.row) * a.n_heads + w.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
-  __syncthreads();   // a row done again is stored after all its parts
-  redo_queries(bad && w.in, [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  redo(join_marks(columns(bad), 0, 1, n_waves), wave_id(), n_waves,
+       [&](int i) { attn_fwd_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
 }
 
 // ------------------------------------------------------------------ backward
-// One query's row of dq, by a whole wave.
+// One query's row of dq, by a whole wave.  A NaN in its statistics makes the
+// whole row NaN, if the query sees a key.
 template <typename T>
 __device__ __forceinline__ void attn_dq_row(const AttnView& a, int64_t t, int64_t h, int64_t p, int64_t k0) {
   const int64_t hk = h / a.group;
@@ -350,6 +402,7 @@ __device__ __forceinline__ void attn_dq_row(const AttnView& a, int64_t t, int64_
   visible_keys(p, a.window, a.sinks, &sink_end, &lo);
   const Row2 q = load_row<T>(a.q, t, h, a.head_dim), d_o = load_row<T>(a.d_o, t, h, a.head_dim);
   const float dl = dot(d_o, load_row<T>(a.o, t, h, a.head_dim)), lse = a.lse[t * a.n_heads + h];
+  if (p >= 0 && (is_nan(dl) || is_nan(lse))) return store_row<T>(a.dq, t, h, a.head_dim, Row2{{NAN, NAN}});
   Row2 dq{{0.0f, 0.0f}};
   for (int64_t j = 0; j <= p; ++j) {
     if (j == sink_end) j = lo;
@@ -377,8 +430,8 @@ __device__ __forceinline__ void finish_dq_dims(const AttnView& a, const QueryCol
     for (int r = 0; r < 16; ++r) bad |= not_finite(out[i][r]);
     store_column<T>(a.dq, w.q0 + w.row, w.head, a.head_dim, d, out[i], a.scale, w.in);
   }
-  __syncthreads();
-  redo_queries(bad && w.in, [&](int i) { attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
+  redo(join_marks(columns(bad && w.in), 0, 1, n_waves), wave_id(), n_waves,
+       [&](int i) { attn_dq_row<T>(a, w.q0 + w.wq + i, w.head, w.past + w.wq + i, w.k0); });
 }
 
 // 32 queries of a tile in parts a workgroup, 32 dims a wave.  kGrad: dq, whose
@@ -654,16 +707,51 @@ __device__ __forceinline__ void put_sums(f32x4_t* to, int tile, const f32x16_t& 
 
 // Keys whose gradients came out not finite: a query that does not see the key
 // may have brought it (zero times its rows), so they are done again query by
-// query; see the forward.
+// query, unless the query at the key's own position explains it; see the
+// forward.  first, step, n: the waves that have these 32 keys; turn: which of
+// them this one is.
 template <typename T>
-__device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& stats, const DkvItem& w, bool bad) {
-  uint64_t again = __ballot(bad && w.in);
-  again = (again | (again >> 32)) & 0xffffffffull;
-  while (again) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    attn_dkv_row<T>(a, stats.delta, w.wkey + i, w.hk, w);
+__device__ __forceinline__ void redo_keys(const AttnView& a, const RowStats& stats, const DkvItem& w, bool bad, int first, int step,
+                                          int n, int turn) {
+  redo(join_marks(columns(bad && w.in), first, step, n), turn, n,
+       [&](int i) { attn_dkv_row<T>(a, stats.delta, w.wkey + i, w.hk, w); });
+}
+// Whether every element of x (32 dims of the lane's key's dk, or its dv) that is
+// not finite is a NaN that the query at the key's position brings: a NaN in its
+// statistics makes the whole row NaN (delta: of dk alone), one in its d_o that
+// element of dv.
+template <typename T>
+__device__ __forceinline__ bool own_query_explains(const AttnView& a, const RowStats& stats, const DkvItem& w, bool value, int d,
+                                                   const f32x16_t& x) {
+  const int i = w.key - w.past;
+  if (!w.in || i < 0) return false;
+  uint32_t nan = 0;   // a bit an element
+  for (int g = 0; g < a.group; ++g) {
+    const int64_t h = static_cast<int64_t>(w.hk) * a.group + g, at = h * a.total_q + w.q0 + i;
+    if (is_nan(stats.lse2[at]) || (!value && is_nan(stats.delta[at]))) nan = 0xffff;
+    if (!value || nan == 0xffff) continue;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int e = d * 32 + 8 * y + 4 * static_cast<int>((threadIdx.x & 63) >> 5);
+      if (e >= a.head_dim) continue;
+      const f32x4_t v = load4<T>(a.d_o, w.q0 + i, h, e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) nan |= is_nan(v[j]) ? 1u << (4 * y + j) : 0u;
+    }
   }
+  bool fine = true;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) fine &= !not_finite(x[r]) | (is_nan(x[r]) & ((nan >> r & 1) != 0));
+  return fine;
+}
+// Whether x holds something not finite that a key's row has to be done again for.
+template <typename T>
+__device__ __forceinline__ bool has_unexplained(const AttnView& a, const RowStats& stats, const DkvItem& w, bool value, int d,
+                                                const f32x16_t& x) {
+  bool bad = false;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) bad |= not_finite(x[r]);
+  return bad && !own_query_explains<T>(a, stats, w, value, d, x);
 }
 
 // 32 keys of a split tile a workgroup, 32 dims of dk or dv a wave.
@@ -700,13 +788,10 @@ __global__ __launch_bounds__(4 * DP) void attn_dkv_join_kernel(AttnView a, RowSt
         for (int e = 0; e < 4; ++e) x[4 * g + e] += v[i][g][e] * f;
     }
   }
-  bool bad = false;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) bad |= not_finite(x[r]);
   const bool value = tile >= kDT;
-  store_column<T>(value ? a.dv : a.dk, w.k0 + w.key, w.hk, a.head_dim, value ? tile - kDT : tile, x, value ? 1.0f : a.scale, w.in);
-  __syncthreads();   // a row done again is stored after all its parts
-  redo_keys<T>(a, stats, w, bad);
+  const int d = value ? tile - kDT : tile;
+  store_column<T>(value ? a.dv : a.dk, w.k0 + w.key, w.hk, a.head_dim, d, x, value ? 1.0f : a.scale, w.in);
+  redo_keys<T>(a, stats, w, has_unexplained<T>(a, stats, w, value, d, x), 0, 1, kTiles, tile);
 }
 
 // ------------------------------------------------------------------- launches
