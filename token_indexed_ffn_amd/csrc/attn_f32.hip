@@ -44,6 +44,10 @@ struct F32Shape {
   // x 4096 tokens, 16 heads of 128, window 1024: 592 us; 777 with two blocks a
   // wave and one workgroup.
   static constexpr bool kTurns = DP > 64;
+  // With 64-bit addresses (kWide) two would spill 39 registers a lane: 512 tokens
+  // of the same heads on 4 take 45 us with one workgroup and 54 with two, 2 x
+  // 4096 with the window 891 and 914, 4 x 2048 without 977 and 963.
+  static constexpr int fwd_workgroups(bool wide) { return wide && kTurns ? 1 : 2; }
   static constexpr int kFwdPerWave = kTurns ? kBlock : kPerWave, kFwdLds = kWaves * kFwdPerWave;
 };
 
@@ -78,7 +82,7 @@ __device__ __forceinline__ void join_waves(char* smem, const f32x16_t (&x)[N], f
 
 // ------------------------------------------------------------------- forward
 template <int DP, bool kWide>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
+__global__ __launch_bounds__(64 * kWaves, F32Shape<DP>::fwd_workgroups(kWide)) void attn_fwd_f32_kernel(AttnView a, int64_t n_slots, KeyParts parts, int* err) {
   using TL = Tile<F32, DP>;
   using Loader = TileLoader<F32, DP, 32, 1, kWide>;
   using Shape = F32Shape<DP>;
