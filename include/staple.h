@@ -921,7 +921,8 @@ staple_status_t staple_kv_copy_pages(const staple_kv_t* kv, const int32_t* src, 
  *     token is neither read nor written.
  * The cache is split along its length over several workgroups where the
  * batch alone does not fill the GPU; their partial results (workspace) are
- * joined in a fixed order.  Uses kv's k_pages, v_pages, table, lens, refused. */
+ * joined in a fixed order.  bf16: P keeps 16 bits or more, unlike staple_attn_fwd's.
+ * Uses kv's k_pages, v_pages, table, lens, refused. */
 typedef struct staple_attn_decode_t {
   int64_t n_seqs, n_heads, max_len, window, sinks;
   float scale;

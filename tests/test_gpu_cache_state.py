@@ -119,3 +119,32 @@ def test_growth_marks_the_rows_that_it_leaves(st):
     assert st.staple_get_device_error() == -8 and refused.tolist() == [1, 0, 0, 1] and ln.tolist() == [16, 5, 31, -2]
     with pytest.raises(ValueError):
         st.staple_kv_extend(refs, table, ln, ints([0]), k_pages=k, v_pages=v, refused=refused[:3])
+
+
+@pytest.mark.parametrize("lens,h,hk,d,page,window,sinks", [
+    ([37], 16, 16, 128, 16, 0, 0), ([300, 2, 90], 8, 2, 64, 32, 50, 4), ([5000, 17], 8, 2, 128, 64, 0, 0),
+    ([700], 40, 1, 96, 16, 0, 0)])
+def test_decode_weights_are_not_rounded_to_bf16(st, lens, h, hk, d, page, window, sinks):
+    """Between the bf16 operands and the bf16 result a weight is off by 2^-17 of it (what two bf16
+    numbers leave of it) and the bounds of fp32 arithmetic."""
+    import numpy as np
+
+    from attn_bounds import bounds
+    from oracle import attn_oracle as A
+    print(lens, h, hk, d, flush=True)
+    k, v, table, ln, _ = make_cache("bf16", lens, hk, d, page, 240)
+    q = rand((len(lens), h, d), "bf16", 241)
+    got = st.staple_attn_decode_paged(q, k, v, table, ln, window=window, sinks=sinks)
+    (o, _), _ = decode_ref("bf16", q, k, v, table, ln, window, sinks, d ** -0.5)
+    nq, nk, nv, nt = (to_np(t) for t in (q, k, v, table))
+    bound = np.zeros(o.shape)
+    for i, n in enumerate(lens):
+        j = np.arange(n)
+        ks, vs = nk[nt[i, j // page], :, j % page], nv[nt[i, j // page], :, j % page]
+        see = A.visible(1, n, window, sinks)
+        for x in range(h):
+            ops = nq[i:i + 1, x], ks[:, x // (h // hk)], vs[:, x // (h // hk)]
+            out = A.attend(*ops, see, d ** -0.5)
+            weights = (out["p"] @ np.abs(ops[2]))[0]
+            bound[i, x] = bounds("f32", *ops, out, see, d ** -0.5)["o"][0] + 2.0 ** -17 * weights + 2.0 ** -8 * np.abs(out["o"][0])
+    check(to_np(got["o"]), o, bound, "o")
