@@ -766,8 +766,8 @@ staple_status_t staple_ffn_bwd_table_grad(int64_t n_tokens, int64_t d_model, int
  * its result, whatever the key's and its value's row hold (NaN, infinities).
  *
  * Products and sums are fp32 (bf16: from bf16 operands).  bf16 rounds P
- * (and, in the backward, dS) to bf16 as the operand of the next product and
- * o, dq, dk, dv once where they are stored.  The results are deterministic.
+ * (and, in the backward, dS) to bf16 as the operand of the next product, by 2^-8
+ * of itself at most, and o, dq, dk, dv once where they are stored.  The results are deterministic.
  *
  * A result that comes out NaN or infinite, without a NaN at its own position
  * that explains it (a query's statistics, the value or output gradient that it
