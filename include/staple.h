@@ -800,16 +800,17 @@ typedef struct staple_attn_t {
   staple_heads_t d_o, dq, dk, dv;    /* backward only */
 } staple_attn_t;
 
-/* Limits (STAPLE_ERR_UNSUPPORTED past them): 2^29 query or key tokens and
- * sequences; (tokens / 128 + n_seqs + 4) n_heads + 4096 workgroups of 2^23
- * (fp32: tokens / 32, 2^24).
+/* Limits (STAPLE_ERR_UNSUPPORTED past them): 2^29 rows of query heads (total_q
+ * n_heads) and of key-value heads (total_k n_kv_heads), 2^29 sequences, 65535
+ * heads; and (tokens / 128 + n_seqs + 4) n_heads + 4096 workgroups of 2^23 (fp32:
+ * tokens / 32, 2^24), where tokens is the larger of total_q and total_k.
  *
  * Forward: writes o and lse from q, k, v.  `a` is read during the call only.
  * A pair of cu_q or cu_k entries that is out of order or past the totals sets
- * the device error word, and that sequence counts as empty.  Rows in no
- * sequence are not written.  Workspace: where there are too few queries to
- * occupy the GPU, long rows' keys are split and the parts' sums joined (else 0
- * bytes). */
+ * the device error word; that sequence counts as empty, and rows of the other
+ * sequences may be left unwritten too.  Rows in no sequence are not written.
+ * Workspace: where there are too few queries to occupy the GPU, long rows' keys
+ * are split and the parts' sums joined (else 0 bytes). */
 size_t staple_attn_fwd_workspace_bytes(const staple_attn_t* a);
 staple_status_t staple_attn_fwd(const staple_attn_t* a, void* ws, size_t ws_bytes, void* stream);
 
@@ -847,7 +848,10 @@ staple_status_t staple_attn_bwd(const staple_attn_t* a, void* ws, size_t ws_byte
  * page_size is a power of two in [16, 1024]; head_dim as in staple_attn_t; a
  * layer's keys of one page take at most 2^31 bytes.
  * Row numbers, pages and lengths out of range set the device error word and
- * are skipped.  Lists of rows (`seqs`, `children`) name each row once.
+ * are skipped.  Lists of rows (`seqs`, `children`) name each row once.  Limits
+ * (STAPLE_ERR_UNSUPPORTED past them): 2^31 - 1 pages, rows and pages of a row,
+ * 16383 layers, 65535 heads; 2^23 entries of the lists below, unless said
+ * otherwise.
  * ------------------------------------------------------------------------ */
 typedef struct staple_kv_t {
   int64_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
@@ -862,7 +866,7 @@ typedef struct staple_kv_t {
  * rows [cu_new[i], cu_new[i + 1]) of k_new, v_new ([n_new rows] of n_kv_heads)
  * are the last tokens of sequence seqs[i], whose lens already counts them.
  * cu_new NULL: one row each, row i for seqs[i].  seqs NULL: row i of the table.
- * Uses k_pages, v_pages, table, lens, refused. */
+ * n_new <= 2^23.  Uses k_pages, v_pages, table, lens, refused. */
 staple_status_t staple_kv_append(const staple_kv_t* kv, const staple_heads_t* k_new,
                                  const staple_heads_t* v_new, int64_t n_new, const int32_t* seqs,
                                  int64_t n_seqs, const int32_t* cu_new, void* stream);
@@ -915,6 +919,7 @@ staple_status_t staple_kv_copy_pages(const staple_kv_t* kv, const int32_t* src, 
  *     key and value, which the call also writes to position lens - 1 of the
  *     cache (as staple_kv_append would).  The new token of a row whose growth
  *     was refused is neither read nor written;
+ *   n_seqs n_heads <= 2^23;
  *   max_len: a bound of the lengths, known on the host (<= max_pages
  *     page_size); a longer sequence sets the device error word and is cut: its
  *     query stands at position max_len - 1 of what the cache holds, and its new

@@ -70,3 +70,50 @@ def test_pages_of_more_bytes_than_32_bits_count_are_refused(L):
         assert lib.staple_attn_decode_paged(c, d, P, 1 << 40, None) == -2
     c = ctypes.byref(cache(L, **fine))
     assert lib.staple_kv_copy_pages(c, P, P, 0, None) == 0 and lib.staple_kv_extend(c, P, None, 0, P, 0, None) == 0
+
+
+def attn(L, **change):
+    f = dict(n_seqs=1, total_q=64, total_k=64, n_heads=1, n_kv_heads=1, head_dim=64, window=0, sinks=0, scale=0.125,
+             dtype=1, cu_q=P, cu_k=P, lse=P, **{n: L.Heads(P, 256, 64) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")})
+    f.update(change)
+    return L.Attn(**f)
+
+
+ROWS = 1 << 29
+BF16_TILES = (1 << 23) - 4096 - 4        # workgroups of one head that are left for tokens and sequences
+
+
+@pytest.mark.parametrize("within,past", [
+    (dict(total_q=ROWS), dict(total_q=ROWS + 1)),
+    (dict(total_k=ROWS), dict(total_k=ROWS + 1)),
+    (dict(total_q=ROWS // 4, n_heads=4), dict(total_q=ROWS // 4 + 1, n_heads=4)),
+    (dict(total_k=ROWS // 4, n_heads=4, n_kv_heads=4), dict(total_k=ROWS // 4 + 1, n_heads=4, n_kv_heads=4)),
+    (dict(n_seqs=BF16_TILES), dict(n_seqs=BF16_TILES + 1)),
+    (dict(n_seqs=BF16_TILES - 8, total_q=8 * 128), dict(n_seqs=BF16_TILES - 7, total_q=8 * 128)),
+    (dict(dtype=0, n_seqs=(1 << 24) - 4102), dict(dtype=0, n_seqs=(1 << 24) - 4101)),   # 64 tokens are two tiles
+    (dict(n_heads=100), dict(n_heads=65536)),
+])
+def test_packed_attention_limits_are_the_headers(L, within, past):
+    """A workspace is asked for up to the limit; past it the call is refused."""
+    lib = L.load()
+    assert lib.staple_attn_bwd_workspace_bytes(ctypes.byref(attn(L, **within))) > 0
+    a = ctypes.byref(attn(L, **past))
+    assert lib.staple_attn_bwd_workspace_bytes(a) == 0
+    assert lib.staple_attn_fwd(a, P, 1 << 60, None) == -2 and lib.staple_attn_bwd(a, P, 1 << 60, None) == -2
+
+
+def test_cache_list_limits_are_the_headers(L):
+    """Past the limit: unsupported.  At it the next check speaks, a missing operand."""
+    lib, c, n = L.load(), ctypes.byref(cache(L)), 1 << 23
+    for call in (lambda n: lib.staple_kv_append(c, None, None, n, P, n, None, None),
+                 lambda n: lib.staple_kv_fork(c, None, None, n, None), lambda n: lib.staple_kv_free(c, None, n, None),
+                 lambda n: lib.staple_kv_copy_pages(c, None, None, n, None)):
+        assert call(n) == -1 and call(n + 1) == -2
+    for change in (dict(n_layers=16384), dict(n_pages=1 << 31), dict(n_rows=1 << 31), dict(max_pages=1 << 31), dict(n_kv_heads=65536)):
+        assert lib.staple_kv_copy_pages(ctypes.byref(cache(L, **change)), P, P, 0, None) == -2, change
+    seqs = 1 << 19   # of 16 heads
+    d = decode(L, n_seqs=seqs, seqs=P, max_len=4096)
+    d.q.data = None
+    assert lib.staple_attn_decode_paged(c, ctypes.byref(d), P, 1 << 60, None) == -1
+    d.n_seqs = seqs + 1
+    assert lib.staple_attn_decode_paged(c, ctypes.byref(d), P, 1 << 60, None) == -2
