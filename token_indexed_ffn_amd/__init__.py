@@ -874,8 +874,8 @@ def _like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
-def _rows_out(q: torch.Tensor) -> dict:
-    return {"o": _like(q), "lse": q.new_empty(q.shape[:2], dtype=_FLOAT32)}
+def _rows_out(q: torch.Tensor, rows: int, heads: int) -> dict:
+    return {"o": _like(q), "lse": q.new_empty((rows, heads), dtype=_FLOAT32)}
 
 
 def _grads_out(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> dict:
@@ -929,7 +929,7 @@ def staple_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     their sequence.  scale: head_dim ** -0.5 when None."""
     own = out is None
     if own:
-        out = _own(stream, _rows_out, q)
+        out = _own(stream, _rows_out, q, *q.shape[:2])
     a = ctypes.byref(_attn(q, k, v, cu_q, cu_k, window, sinks, scale, out["o"], out["lse"], own=own))
     native = lib()
     ws = _ws(native.staple_attn_fwd_workspace_bytes(a), workspace, q.device, stream)
@@ -1087,7 +1087,7 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     hk, size, dim = k_pages.shape[-3:]
     dt = k_pages.dtype
     if out is None:
-        out = _own(stream, _rows_out, q)
+        out = _own(stream, _rows_out, q, n, h)
         lse, o = out["lse"], (out["o"].data_ptr(), h * d, d)
     else:
         lse, o = out.get("lse"), _heads(out["o"], "o", dt, n, h, d)
