@@ -11,9 +11,9 @@
 // and only blocks at the edge of what is seen apply a mask.
 //
 // Measured on 6 causal sequences of 700 to 4096 tokens, 32 heads on 8 of 128:
-// forward 470 us (850 TFLOP/s), dq 674 us (889, its three products), dk and dv
-// 920 us (868, their four).  A large matrix product reaches 1234 with a larger
-// share of busy cycles at a lower clock: the product of the two is 0.90 to 0.94
+// forward 487 us (820 TFLOP/s), dq 684 us (876, its three products), dk and dv
+// 943 us (847, their four).  A large matrix product reaches 1234 with a larger
+// share of busy cycles at a lower clock: the product of the two is 0.84 to 0.92
 // GHz here and 1.05 there.
 #include <type_traits>
 
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_bf16_kernel(AttnView a
 // before.  P and dS are rounded to bf16 (dk and dv are off by 2.3e-3 of their
 // norms, of which their own rounding is 1.7e-3): of two numbers each, the trade
 // would not fit beside the ring.  8 sequences of 4096 tokens, window 1024, 16
-// heads: 782 us, a workgroup's 37 blocks at a time; one workgroup a CU, so that
+// heads: 807 us, a workgroup's 37 blocks at a time; one workgroup a CU, so that
 // its first loads and its last stores overlap nothing.
 constexpr int kDkvWaves = 8;
 template <int DP>

@@ -14,7 +14,7 @@
 //           (c = lane % 16, E = head_dim / 16); one byte permute a dword gathers
 //           the 8 keys of one element: the A operand, rows in the order E c + t.
 // The 16 columns are mostly idle for a small group, but the matrix cores are
-// far from busy: a block is 16 KB of cache and 16 MFMAs.  Bound by HBM: the
+// far from busy: a block is 16 KB of cache and 24 MFMAs.  Bound by HBM: the
 // cache is read once, and the waves of a CU keep over 100 KB in flight.
 //
 // A key that is not seen (past the length, outside the window and the sinks)
@@ -24,7 +24,7 @@
 // head) pairs alone are too few; the splits' partial results are joined by a
 // second kernel in split order.
 //
-// Measured: two sequences of 100001 to 131071 keys, 32 heads on 8, 167 us (5.6
+// Measured: two sequences of 100001 to 131071 keys, 32 heads on 8, 168 us (5.5
 // TB/s) and 6 in the join; 64 sequences around 256 keys, 16 heads, 32 us (4.2
 // TB/s, no join); one of 37 keys 8 us, its chain of loads: length, page, rows.
 #include "attn.h"

@@ -12,8 +12,8 @@
 // product), forward and backward, beside tiles of 128 queries whose waves share
 // the blocks that a workgroup loads:
 //   512 tokens, 4 heads of 64:         12 + 33 us;     28 + 79
-//   8 x 1024 tokens, 8 heads of 64:    121 + 408 us;   141 + 492
-//   4 x 2048 tokens, 16 heads of 128:  750 + 2415 us (92, 100 TFLOP/s);
+//   8 x 1024 tokens, 8 heads of 64:    122 + 411 us;   141 + 492
+//   4 x 2048 tokens, 16 heads of 128:  748 + 2421 us (92, 99 TFLOP/s);
 //                                      749 + 2613
 #include "attn_seq.h"
 
