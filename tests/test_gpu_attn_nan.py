@@ -122,3 +122,24 @@ def test_a_diverged_step_takes_no_longer(st, dtype, which):
     sound, diverged = fastest(ops), fastest(bad)
     print(f"  {dtype} {which}: {1e3 * sound:.0f} us sound, {1e3 * diverged:.0f} diverged", flush=True)
     assert diverged <= 4 * sound
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,hk,d", [(4, 2, 72), (1, 1, 128), (2, 2, 64)])
+def test_no_keys_and_no_queries_at_all(st, dtype, h, hk, d):
+    """Sequences without a single key (o = 0, lse = -inf, dq = 0), and without a single query (dk =
+    dv = 0), whatever the other side holds."""
+    import torch
+    n, mask = 150, dict(window=20, sinks=3)
+    c, none = cu([100, 0, 50]), cu([0, 0, 0])
+    rows, keys = torch.full_like(rand((n, h, d), dtype, 430), NAN), torch.full_like(rand((n, hk, d), dtype, 431), NAN)
+    print(dtype, h, hk, d, "no keys", flush=True)
+    f = st.staple_attn_fwd(rows, keys[:0], keys[:0], c, none, **mask)
+    b = st.staple_attn_bwd(rows, rows, keys[:0], keys[:0], f["o"], f["lse"], c, none, **mask)
+    assert (f["o"] == 0).all() and (f["lse"] == -float("inf")).all() and (b["dq"] == 0).all() and b["dk"].numel() == 0
+    print(dtype, h, hk, d, "no queries", flush=True)
+    f = st.staple_attn_fwd(rows[:0], keys, keys, none, c, **mask)
+    assert f["o"].numel() == 0 and f["lse"].numel() == 0
+    b = st.staple_attn_bwd(rows[:0], rows[:0], keys, keys, f["o"], f["lse"], none, c, **mask)
+    assert (b["dk"] == 0).all() and (b["dv"] == 0).all() and b["dq"].numel() == 0
+    assert st.staple_get_device_error() == 0

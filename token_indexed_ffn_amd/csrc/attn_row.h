@@ -57,7 +57,6 @@ struct RowSoftmax {
     const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
     return Row2{{acc.x[0] * r, acc.x[1] * r}};
   }
-  __device__ __forceinline__ float lse() const { return top + __logf(sum); }
 };
 
 }  // namespace staple

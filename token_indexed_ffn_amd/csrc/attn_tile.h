@@ -64,12 +64,6 @@ __device__ __forceinline__ f32x16_t mma16(const u32x4_t& a, const u32x4_t& b, f3
 template <typename T> struct Column;
 template <> struct Column<bf16_t> {
   u32x4_t v[2];   // rows 0-15, rows 16-31 of the block, rounded to bf16
-  __device__ __forceinline__ void set(const f32x16_t& x) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[t][i] = pack_bf16x2(x[8 * t + 2 * i], x[8 * t + 2 * i + 1]);
-  }
   // times a power of two
   __device__ __forceinline__ void scale(float f) {
 #pragma unroll
