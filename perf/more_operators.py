@@ -309,14 +309,14 @@ def run(state):
     if c["op"] == "norm":
         how = dict(w_pre=s["w_pre"], w_post=s["w_post"], gate=s["gate"], pre=c["pre"], post=c["post"], scale=c["scale"],
                    eps=EPS)
-        f = st.staple_norm_fwd(s["x"], s["z"], **how)
+        f = st.staple_norm_fwd(s["x"], s["z"], save=c["train"], **how)
         out = {n: f[n] for n in ("r", "h") if f[n] is not None}
         if c["train"]:
             b = st.staple_norm_bwd(s["dr"], s["dh"], f["r"], s["z"], f["rstd_r"], f["rstd_z"], **how)
             out.update({n: t for n, t in b.items() if t is not None})
         return out
     if c["op"] == "xent":
-        return st.staple_xent_fwd(s["logits"], s["targets"], s["g"] if c["train"] else None)
+        return st.staple_xent_fwd(s["logits"], s["targets"], g=s["g"] if c["train"] else None)
     return st.staple_sample(s["logits"], s["u"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"],
                             min_p=s["min_p"])
 
