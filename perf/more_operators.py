@@ -312,7 +312,9 @@ def run(state):
         f = st.staple_norm_fwd(s["x"], s["z"], save=c["train"], **how)
         out = {n: f[n] for n in ("r", "h") if f[n] is not None}
         if c["train"]:
-            b = st.staple_norm_bwd(s["dr"], s["dh"], f["r"], s["z"], f["rstd_r"], f["rstd_z"], **how)
+            # a sum stored in bf16 is formed again from what it is made of, one in fp32 is read
+            b = st.staple_norm_bwd(s["dr"], s["dh"], s["x"], s["z"], f["rstd_r"], f["rstd_z"],
+                                   r=f["r"] if c["residual"] == "f32" else None, **how)
             out.update({n: t for n, t in b.items() if t is not None})
         return out
     if c["op"] == "xent":
