@@ -939,6 +939,133 @@ size_t staple_attn_decode_workspace_bytes(const staple_kv_t* kv, const staple_at
 staple_status_t staple_attn_decode_paged(const staple_kv_t* kv, const staple_attn_decode_t* a,
                                          void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators at a model's two ends and around its blocks: embedding lookup
+ * and its gradient, norms with a block's gate and residual sum, the loss of a
+ * vocabulary's logits, sampling of the next token.
+ *
+ * Rows are contiguous and a stride apart (in elements); rows that are read may
+ * have any stride from 0, rows that are written one of at least their width.
+ * Every element type's natural alignment is enough; where all operands and
+ * strides are multiples of 16 bytes (and the width of 8 elements) a lane reads
+ * 16 bytes at once.  Sums and statistics are fp32 or wider, outputs are rounded once.  Results
+ * do not change from run to run.
+ * ------------------------------------------------------------------------ */
+
+/* Embedding: y[i] = scale table[ids[i]] (the product in fp32), y of out_dtype with y_stride
+ * elements from row to row.  An ID outside [0, vocab) sets the device error word;
+ * its row of y is zero.  d <= 2^20, n_tokens <= 2^29. */
+staple_status_t staple_embed_fwd(const void* table, int64_t vocab, int64_t d, int32_t dtype,
+                                 const int32_t* ids, int64_t n_tokens, float scale, void* y,
+                                 int64_t y_stride, int32_t out_dtype, void* stream);
+
+/* Its gradient from staple_dedup's outputs for the batch: the sum, over the positions i of
+ * unique token u, of dy[i], times scale, in fp32.
+ *   uniq NULL: into row u of grad (compact rows, as d_rows of
+ *     staple_ffn_bwd_table_grad and the gradient that staple_adamw_rows takes);
+ *   uniq given: into row uniq[u] of grad (a whole table's gradient; rows of
+ *     other tokens are left as they are).
+ * accumulate: 0 overwrites these rows, otherwise the sums are added to them.
+ * grad [grad_rows x d] fp32.  *n_unique > max_unique, and entries of the maps out of range, set
+ * the device error word; the former writes nothing.  Workspace: sums of tokens whose
+ * positions are spread over several workgroups. */
+size_t staple_embed_bwd_workspace_bytes(int64_t n_tokens, int64_t d);
+staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtype, int64_t n_tokens,
+                                 int64_t d, float scale, const int32_t* sorted_pos,
+                                 const int32_t* inv, const int32_t* seg_start,
+                                 const int32_t* n_unique, int64_t max_unique, const int32_t* uniq,
+                                 float* grad, int64_t grad_rows, int32_t accumulate, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* Norms before and after a block, with the block's gate and residual sum: with x the residual
+ * stream and z the block's output, for every row
+ *
+ *     b = post ? z / rms(z) * w_post : z,     rms(v) = sqrt(mean(v^2) + eps),
+ *     r = x + scale * gate * b,
+ *     h = r / rms(r) * w_pre                  (if pre)
+ *
+ * h from the sum r before its rounding to r_dtype.  The forward reads x, z and writes r, h:
+ *   z NULL: r = x, which is not written (r NULL; no post, no gate): a norm alone;
+ *   x NULL: r = scale * gate * b: a norm after a block without a residual sum.
+ * The types are bf16 or fp32 all through, or r_dtype fp32 beside dtype bf16 (a residual
+ * stream in fp32).
+ *
+ * The backward takes the forward's x and z, rstd_r and rstd_z (as it wrote them), dr and dh
+ * (the gradients of r and h; dr NULL: zero), and writes those of dx, dz, dgate, dw_pre,
+ * dw_post that are not NULL.  With `pre` it reads the stored r where r is given (x where z
+ * was NULL), and otherwise forms r again from x and z, as the forward had it before
+ * rounding; a bf16 r is off by its rounding, which shows in dw_pre as some 2^-9 of it.
+ *     g = dr + (t - hat(r) mean(t hat(r))) / rms(r),  t = dh w_pre,  hat(v) = v / rms(v)
+ *     dx = g,   dw_pre = sum of dh hat(r),   dgate = scale g b,   q = scale gate g,
+ *     dz = q, or (q w_post - hat(z) mean(q w_post hat(z))) / rms(z),   dw_post = sum of q hat(z)
+ * with the sums over the rows in fp32.  A gate shared by the rows has the gradient float[d],
+ * summed over the rows; a gate a row the gradient rows dgate, of dtype.
+ * An output may take the place of an input of the same type and stride.
+ * d <= 16384, n_rows <= 2^23; squares of a row's values have to stay finite in fp32. */
+typedef struct staple_rows_t {
+  void* data;
+  int64_t stride;
+} staple_rows_t;
+
+typedef struct staple_norm_t {
+  int64_t n_rows, d;
+  int32_t dtype;               /* of z, h, dz, dh, and a gate's rows with their gradient */
+  int32_t r_dtype;             /* of x, r, dx, dr */
+  int32_t w_dtype;             /* of w_pre, w_post and a gate shared by the rows */
+  int32_t pre, post;
+  float scale, eps;            /* eps > 0 */
+  staple_rows_t x, z, r, h;
+  staple_rows_t gate;          /* data NULL: none; stride 0: one row, shared by all */
+  const void *w_pre, *w_post;  /* [d], NULL: ones */
+  float *rstd_r, *rstd_z;      /* [n_rows]: 1 / rms, written by the forward where not NULL */
+  staple_rows_t dr, dh;        /* backward only, as all below */
+  staple_rows_t dx, dz, dgate; /* dgate of a shared gate: float[d] */
+  float *dw_pre, *dw_post;     /* [d] */
+} staple_norm_t;
+staple_status_t staple_norm_fwd(const staple_norm_t* a, void* stream);
+size_t staple_norm_bwd_workspace_bytes(const staple_norm_t* a);
+staple_status_t staple_norm_bwd(const staple_norm_t* a, void* ws, size_t ws_bytes, void* stream);
+
+/* Cross entropy of logits [n_rows x vocab] against targets:
+ *     lse = log sum_j exp l_j,   loss = lse - l_t,   d_logits_j = g (exp(l_j - lse) - [j = t]).
+ * A row with a negative target does not count: its loss and gradient are zero.  A target of vocab or
+ * more sets the device error word and does not count.  Classes may have -inf; a target that
+ * has it has the loss +inf, and a row that has nothing else has the gradient zero.
+ * The forward writes loss and lse float[n_rows] and, with g float[n_rows] (the gradient of each
+ * row's loss) and d_logits (of dtype, may be the logits themselves), the gradient in the same
+ * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows <= 2^23.
+ * Workspace: parts of rows where there are too few to occupy the GPU. */
+size_t staple_xent_workspace_bytes(int64_t n_rows, int64_t vocab);
+staple_status_t staple_xent_fwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
+                                int32_t dtype, const int32_t* targets, float* loss, float* lse,
+                                const float* g, void* d_logits, int64_t d_stride, void* ws,
+                                size_t ws_bytes, void* stream);
+staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
+                                int32_t dtype, const int32_t* targets, const float* lse,
+                                const float* g, void* d_logits, int64_t d_stride, void* stream);
+
+/* Sampling of one token a row from given random numbers.  With w_j = exp((l_j - max l) / T), and
+ * the tokens in the order of falling l_j (ties: rising j), a token is kept while
+ *     it is among the first k                                (0 < k < vocab),
+ *     the kept ones before it have a sum less than p times that of the first k   (p < 1),
+ *     w_j >= min_p                                           (min_p > 0),
+ * the first one always; token = the first j, in the order of j, at which the sum of the kept w
+ * passes u times their whole sum.  T that is not above 0: the first of the largest logits.
+ * NaN counts as -inf, and a token with -inf is never drawn; a row with nothing else has
+ * token -1.  logprob (NULL: not wanted): the log of the token's share of the kept sum, 0 where
+ * T is not above 0, -inf for token -1.
+ *   u float[n_rows] in [0, 1); temperature, top_p, min_p float[n_rows], top_k
+ *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.
+ * The weights are rounded to multiples of 2^-62 by vocab (2^-50 at least) and summed exactly: the
+ * same token on every run, and one that differs from the definition only where
+ * u or p lies within that rounding of a border. */
+size_t staple_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
+staple_status_t staple_sample(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
+                              int32_t dtype, const float* u, const float* temperature,
+                              const int32_t* top_k, const float* top_p, const float* min_p,
+                              int32_t* token, float* logprob, void* ws, size_t ws_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

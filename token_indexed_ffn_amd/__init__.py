@@ -1109,6 +1109,258 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     return out
 
 
+# ----------------------------------------------------------------------------
+# A model's two ends and the norms around its blocks
+# ----------------------------------------------------------------------------
+_NO_ROWS = (None, 0)
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    return not t.is_cuda or t.get_device() != _current_device()
+
+
+def _rows(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, n: int, d: int,
+          written: bool = False) -> tuple:
+    """A [n, d] tensor of the current device, d contiguous; rows may be strided (those that are
+    written: apart from each other).  The fields of a staple_rows_t."""
+    if t is None:
+        return _NO_ROWS
+    if t.dtype is not dtype or t.shape != (n, d) or _elsewhere(t):
+        raise ValueError(f"{what}: needs a [{n}, {d}] tensor of {dtype} on the current device, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    stride, one = t.stride()
+    if (one != 1 and d > 1 or written and n > 1 and stride < d) and t.numel():
+        raise ValueError(f"{what}: rows must be contiguous" + (" and apart from each other" if written else ""))
+    return t.data_ptr(), stride
+
+
+def _flat(t: Optional[torch.Tensor], what: str, n: Optional[int], dtype: torch.dtype = torch.int32) -> Optional[int]:
+    """A contiguous tensor of n elements (None: any number) on the current device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or _elsewhere(t) or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: needs a contiguous {dtype} tensor on the current device" +
+                         ("" if n is None else f" of {n} elements"))
+    return t.data_ptr()
+
+
+def staple_embed_fwd(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
+                     out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Rows scale * table[ids] [tokens, d] of out_dtype (None: the table's)."""
+    vocab, d = table.shape
+    n = ids.numel()
+    if out is None:
+        out = _own(stream, lambda: table.new_empty((n, d), dtype=out_dtype or table.dtype))
+    dt = table.dtype
+    y, stride = _rows(out, "out", out.dtype, n, d, True)
+    _check(lib().staple_embed_fwd(_flat(table, "table", None, dt), vocab, d, _dt(table), _flat(ids, "ids", n), n,
+                                  float(scale), y, stride, _dt(out), _stream(stream)), "staple_embed_fwd")
+    return out
+
+
+def staple_embed_bwd(dy: torch.Tensor, sorted_pos: torch.Tensor, seg_start: torch.Tensor,
+                     n_unique: torch.Tensor, *, inv: torch.Tensor,
+                     uniq: Optional[torch.Tensor] = None, scale: float = 1.0,
+                     max_unique: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                     accumulate: bool = False, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of staple_embed_fwd, fp32: row u is the sum of dy over the positions of unique
+    token u, times scale (sorted_pos, seg_start, n_unique, inv: staple_dedup's outputs for the
+    batch).  uniq given: row uniq[u] of `out`, the whole table's gradient [vocab, d], whose other
+    rows are left as they are.  accumulate: added to these rows of `out`.  max_unique: the most
+    unique tokens that there can be (None: as many as tokens, or rows of `out`)."""
+    n, d = dy.shape
+    if out is None:
+        if uniq is not None or accumulate:
+            raise ValueError("a table's gradient, and one that is added to, is given as out")
+        rows = n if max_unique is None else int(max_unique)
+        out = _own(stream, lambda: dy.new_empty((rows, d), dtype=torch.float32))
+    if out.dim() != 2 or out.shape[1] != d:
+        raise ValueError(f"out: needs rows of {d}")
+    rows = len(out)
+    most = rows if uniq is None else uniq.numel()
+    mu = min(n, most) if max_unique is None else int(max_unique)
+    if mu > most:
+        raise ValueError(f"{mu} unique tokens need as many rows of out, or entries of uniq, not {most}")
+    for t, least, what in ((sorted_pos, n, "sorted_pos"), (inv, n, "inv"), (seg_start, min(n, mu) + 1, "seg_start"),
+                           (n_unique, 1, "n_unique")):
+        _need(t, least, what)
+    at, stride = _rows(dy, "dy", dy.dtype, n, d)
+    native = lib()
+    ws = _ws(native.staple_embed_bwd_workspace_bytes(n, d), workspace, dy.device, stream)
+    _check(native.staple_embed_bwd(at, stride, _dt(dy), n, d, float(scale), _flat(sorted_pos, "sorted_pos", None),
+                                   _flat(inv, "inv", None), _flat(seg_start, "seg_start", None),
+                                   _flat(n_unique, "n_unique", None), mu, _flat(uniq, "uniq", None),
+                                   _flat(out, "out", None, _FLOAT32), rows, int(bool(accumulate)), _p(ws),
+                                   _ws_size(ws), _stream(stream)), "staple_embed_bwd")
+    return out
+
+
+def _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps):
+    """The fields of a staple_norm_t up to eps, and the gate's and the weights'."""
+    wt = None
+    shared = gate is not None and gate.dim() == 1
+    for w in (w_pre, w_post, gate if shared else None):
+        if w is not None:
+            if wt is not None and w.dtype is not wt:
+                raise ValueError("the weights and a shared gate have one dtype")
+            wt = w.dtype
+    if (w_pre is not None and not pre) or (w_post is not None and not post):
+        raise ValueError("weights of a norm that is not done")
+    if gate is None:
+        gate = _NO_ROWS
+    elif shared:
+        gate = (_flat(gate, "gate", d, wt), 0)
+    else:
+        gate = _rows(gate, "gate", zt, n, d)
+        if gate[1] == 0 and n > 1:
+            raise ValueError("gate: a shared one is given as [d]")
+        gate = (gate[0], gate[1] or d)
+    try:
+        codes = _DT[zt], _DT[xt], F32 if wt is None else _DT[wt]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]}; use bfloat16 or float32") from None
+    return (n, d, *codes, int(pre), int(post), float(scale), float(eps)), gate, \
+        (_flat(w_pre, "w_pre", d, wt), _flat(w_post, "w_post", d, wt)), shared
+
+
+def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None, *,
+                    w_pre: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                    gate: Optional[torch.Tensor] = None, pre: bool = True, post: bool = False,
+                    scale: float = 1.0, eps: float = 1e-6, dtype: Optional[torch.dtype] = None,
+                    save: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """Norms around a block.  x [rows, d]: the residual stream (None: no residual sum); z
+    [rows, d]: the block's output (None: a norm of x alone).  r = x + scale * gate * b with b = z,
+    or with `post` z / rms(z) * w_post; with `pre` h = r / rms(r) * w_pre.  Weights [d], None: ones.
+    gate: [d], one for all rows, or [rows, d].  h has z's dtype (z None: `dtype`, or x's), r has x's (x
+    None: z's).  Returns r (None without z), h (None without `pre`), and with `save` 1 / rms of
+    both, rstd_r and rstd_z, for staple_norm_bwd."""
+    one = z if x is None else x
+    n, d = one.shape
+    xt = one.dtype
+    zt = z.dtype if z is not None else dtype or xt
+    head, gate, weights, _ = _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps)
+    if out is None:
+        out = _own(stream, lambda: {
+            "r": None if z is None else one.new_empty((n, d)),
+            "h": one.new_empty((n, d), dtype=zt) if pre else None,
+            "rstd_r": one.new_empty(n, dtype=_FLOAT32) if pre and save else None,
+            "rstd_z": one.new_empty(n, dtype=_FLOAT32) if post and save else None})
+    a = _lib.Norm(*head, _rows(x, "x", xt, n, d), _rows(z, "z", zt, n, d),
+                  _rows(out.get("r"), "r", xt, n, d, True) if z is not None else _NO_ROWS,
+                  _rows(out["h"], "h", zt, n, d, True) if pre else _NO_ROWS, gate, *weights,
+                  _flat(out.get("rstd_r"), "rstd_r", n, _FLOAT32), _flat(out.get("rstd_z"), "rstd_z", n, _FLOAT32))
+    _check(lib().staple_norm_fwd(ctypes.byref(a), _stream(stream)), "staple_norm_fwd")
+    return out
+
+
+def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: Optional[torch.Tensor],
+                    z: Optional[torch.Tensor] = None, rstd_r: Optional[torch.Tensor] = None,
+                    rstd_z: Optional[torch.Tensor] = None, *, r: Optional[torch.Tensor] = None,
+                    w_pre: Optional[torch.Tensor] = None,
+                    w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                    pre: bool = True, post: bool = False, scale: float = 1.0, eps: float = 1e-6,
+                    out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> dict:
+    """Gradients of staple_norm_fwd from those of r (None: zero) and h: dx, dz, dgate, dw_pre,
+    dw_post (None where there is no such operand; `out`: where to, and only those that it names).
+    x and z: the forward's; rstd_r, rstd_z: what it saved.  r: its stored r, read in place of forming
+    it again (which reads x and z); in bf16 its rounding then shows in dw_pre, in fp32 it is as good and saves z
+    where nothing else needs it.  dw_pre, dw_post and the gradient of a shared gate are fp32."""
+    one = z if x is None else x
+    n, d = one.shape
+    xt = one.dtype
+    zt = z.dtype if z is not None else dh.dtype if dh is not None else xt
+    if z is None:
+        r, x = x, None
+    head, gate_at, weights, shared = _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps)
+    if out is None:
+        out = _own(stream, lambda: {
+            "dx": None if x is None and z is not None else one.new_empty((n, d)),
+            "dz": None if z is None else one.new_empty((n, d), dtype=zt),
+            "dgate": None if gate is None else one.new_empty(d, dtype=_FLOAT32) if shared
+            else one.new_empty((n, d), dtype=zt),
+            "dw_pre": None if w_pre is None else one.new_empty(d, dtype=_FLOAT32),
+            "dw_post": None if w_post is None else one.new_empty(d, dtype=_FLOAT32)})
+    dgate = out.get("dgate")
+    a = _lib.Norm(*head, _rows(x, "x", xt, n, d), _rows(z, "z", zt, n, d), _rows(r, "r", xt, n, d), _NO_ROWS, gate_at,
+                  *weights,
+                  _flat(rstd_r, "rstd_r", n, _FLOAT32), _flat(rstd_z, "rstd_z", n, _FLOAT32),
+                  _rows(dr, "dr", xt, n, d), _rows(dh, "dh", zt, n, d) if pre else _NO_ROWS,
+                  _rows(out.get("dx"), "dx", xt, n, d, True), _rows(out.get("dz"), "dz", zt, n, d, True),
+                  (_flat(dgate, "dgate", d, _FLOAT32), 0) if shared else _rows(dgate, "dgate", zt, n, d, True),
+                  _flat(out.get("dw_pre"), "dw_pre", d, _FLOAT32), _flat(out.get("dw_post"), "dw_post", d, _FLOAT32))
+    a, native = ctypes.byref(a), lib()
+    ws = _ws(native.staple_norm_bwd_workspace_bytes(a), workspace, one.device, stream)
+    _check(native.staple_norm_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_norm_bwd")
+    return out
+
+
+def staple_xent_fwd(logits: torch.Tensor, targets: torch.Tensor, *, g: Optional[torch.Tensor] = None,
+                    out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> dict:
+    """Cross entropy of logits [rows, vocab]: loss and lse [rows], fp32.  targets int32 [rows]; a
+    negative one leaves its row out.  g [rows] fp32, the gradient of each row's loss: the gradient
+    of the logits comes with them as d_logits (out["d_logits"] may be the logits)."""
+    n, vocab = logits.shape
+    if out is None:
+        out = _own(stream, lambda: {
+            "loss": logits.new_empty(n, dtype=_FLOAT32), "lse": logits.new_empty(n, dtype=_FLOAT32),
+            **({} if g is None else {"d_logits": logits.new_empty((n, vocab))})})
+    dt = logits.dtype
+    at, stride = _rows(logits, "logits", dt, n, vocab)
+    d, d_stride = _NO_ROWS if g is None else _rows(out["d_logits"], "d_logits", dt, n, vocab, True)
+    native = lib()
+    ws = _ws(native.staple_xent_workspace_bytes(n, vocab), workspace, logits.device, stream)
+    _check(native.staple_xent_fwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
+                                  _flat(out["loss"], "loss", n, _FLOAT32), _flat(out["lse"], "lse", n, _FLOAT32),
+                                  _flat(g, "g", n, _FLOAT32), d, d_stride, _p(ws), _ws_size(ws), _stream(stream)),
+           "staple_xent_fwd")
+    return out
+
+
+def staple_xent_bwd(g: torch.Tensor, logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, *,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits from that of each row's loss, g [rows] fp32, and the forward's lse;
+    `out` may be the logits."""
+    n, vocab = logits.shape
+    if out is None:
+        out = _own(stream, lambda: logits.new_empty((n, vocab)))
+    dt = logits.dtype
+    at, stride = _rows(logits, "logits", dt, n, vocab)
+    d, d_stride = _rows(out, "out", dt, n, vocab, True)
+    _check(lib().staple_xent_bwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
+                                 _flat(lse, "lse", n, _FLOAT32), _flat(g, "g", n, _FLOAT32), d, d_stride,
+                                 _stream(stream)), "staple_xent_bwd")
+    return out
+
+
+def staple_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch.Tensor] = None,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """One token for each row of logits [rows, vocab], drawn with the random numbers u [rows] fp32
+    in [0, 1): "token" int32 and "logprob" fp32, the log of its probability among the kept
+    tokens.  temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, each None or one a row:
+    a temperature that is not above 0 takes the first of the largest logits; top_k 0, top_p 1 and min_p 0
+    limit nothing."""
+    n, vocab = logits.shape
+    if out is None:
+        out = _own(stream, lambda: {"token": logits.new_empty(n, dtype=_INT32),
+                                    "logprob": logits.new_empty(n, dtype=_FLOAT32)})
+    at, stride = _rows(logits, "logits", logits.dtype, n, vocab)
+    native = lib()
+    ws = _ws(native.staple_sample_workspace_bytes(n, vocab), workspace, logits.device, stream)
+    _check(native.staple_sample(at, stride, n, vocab, _dt(logits), _flat(u, "u", n, _FLOAT32),
+                                _flat(temperature, "temperature", n, _FLOAT32), _flat(top_k, "top_k", n),
+                                _flat(top_p, "top_p", n, _FLOAT32), _flat(min_p, "min_p", n, _FLOAT32),
+                                _flat(out["token"], "token", n), _flat(out.get("logprob"), "logprob", n, _FLOAT32),
+                                _p(ws), _ws_size(ws), _stream(stream)), "staple_sample")
+    return out
+
+
 def ffn_workspace_bytes(n: int, d: int, f: int, dtype: torch.dtype) -> dict:
     return {"fwd": lib().staple_ffn_fwd_workspace_bytes(n, d, f, _DT[dtype]),
             "bwd": lib().staple_ffn_bwd_workspace_bytes(n, d, f, _DT[dtype]),

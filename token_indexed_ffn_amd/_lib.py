@@ -105,6 +105,22 @@ _SIGS = {
     "staple_kv_copy_pages": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp]),
     "staple_attn_decode_workspace_bytes": (c_sz, [c_vp, c_vp]),
     "staple_attn_decode_paged": (c_i32, [c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "staple_embed_fwd": (c_i32, [c_vp, c_i64, c_i64, c_i32, c_vp, c_i64, c_f32, c_vp, c_i64, c_i32,
+                                 c_vp]),
+    "staple_embed_bwd_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "staple_embed_bwd": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_f32, c_vp, c_vp, c_vp, c_vp,
+                                 c_i64, c_vp, c_vp, c_i64, c_i32, c_vp, c_sz, c_vp]),
+    "staple_norm_fwd": (c_i32, [c_vp, c_vp]),
+    "staple_norm_bwd_workspace_bytes": (c_sz, [c_vp]),
+    "staple_norm_bwd": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "staple_xent_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "staple_xent_fwd": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                c_i64, c_vp, c_sz, c_vp]),
+    "staple_xent_bwd": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i64,
+                                c_vp]),
+    "staple_sample_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "staple_sample": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                              c_vp, c_vp, c_sz, c_vp]),
 }
 
 
@@ -135,6 +151,22 @@ class AttnDecode(ctypes.Structure):
     _fields_ = ([(n, c_i64) for n in ("n_seqs", "n_heads", "max_len", "window", "sinks")] +
                 [("scale", c_f32), ("seqs", c_vp), ("q", Heads), ("k_new", Heads),
                  ("v_new", Heads), ("o", Heads), ("lse", c_vp)])
+
+
+class Rows(ctypes.Structure):
+    """staple_rows_t"""
+    _fields_ = [("data", c_vp), ("stride", c_i64)]
+
+
+class Norm(ctypes.Structure):
+    """staple_norm_t"""
+    _fields_ = ([("n_rows", c_i64), ("d", c_i64)] +
+                [(n, c_i32) for n in ("dtype", "r_dtype", "w_dtype", "pre", "post")] +
+                [("scale", c_f32), ("eps", c_f32)] +
+                [(n, Rows) for n in ("x", "z", "r", "h", "gate")] +
+                [(n, c_vp) for n in ("w_pre", "w_post", "rstd_r", "rstd_z")] +
+                [(n, Rows) for n in ("dr", "dh", "dx", "dz", "dgate")] +
+                [(n, c_vp) for n in ("dw_pre", "dw_post")])
 
 
 EXPORTED = tuple(_SIGS)

@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libstaple.so")
 SOURCES = ["api.hip", "sort.hip", "rows.hip", "gemm.hip", "decode.hip", "optim.hip",
-           "kv.hip", "attn.hip", "attn_f32.hip", "attn_decode.hip", "api_attn.hip", "host_pool.cpp"]
+           "kv.hip", "attn.hip", "attn_f32.hip", "attn_decode.hip", "api_attn.hip", "embed.hip", "norm.hip",
+           "xent.hip", "sample.hip", "api_model.hip", "host_pool.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,267 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   y_i = scale E[t_i],    dE_t = scale sum over the positions i with t_i = t of dy_i.
+#include "model_ops.h"
+#include "row_io.h"
+
+namespace staple {
+
+constexpr int kEmbedCols = 512;     // 64 lanes x 8 columns
+constexpr int kEmbedChunk = 32;     // sorted positions of one wave
+constexpr int kEmbedAhead = 8;      // rows in flight a lane
+
+// One wave writes U blocks of 512 columns of one token's row.
+template <typename E, typename O, bool VEC, int U>
+__global__ __launch_bounds__(256) void embed_fwd_kernel(const E* __restrict__ table, int64_t vocab, int d,
+                                                        const int32_t* __restrict__ ids, int64_t n,
+                                                        float scale, O* __restrict__ y, int64_t y_stride,
+                                                        int blocks, int* err) {
+  using R = RowGroup<64, VEC>;
+  const int lane = threadIdx.x & 63;
+  const int64_t items = n * blocks;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); w < items;
+       w += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t i = w / blocks;
+    const int g0 = static_cast<int>(w - i * blocks) * U;
+    const int32_t t = ids[i];
+    const bool fine = t >= 0 && t < vocab;
+    if (!fine && lane == 0 && g0 == 0) flag_index_error(err);
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (fine) {
+        R::load(table + static_cast<int64_t>(t) * d, g0 + u, lane, d, v[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] *= scale;
+      R::store(y + i * y_stride, g0 + u, lane, d, v[u]);
+    }
+  }
+}
+
+static bool vec_rows(const void* p, int64_t stride, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * bytes % 16 == 0;
+}
+
+template <typename E, typename O>
+static void embed_fwd(const void* table, int64_t vocab, int d, const int32_t* ids, int64_t n, float scale,
+                      RowsView y, hipStream_t s, int* err) {
+  const bool vec = d % 8 == 0 && vec_rows(table, d, sizeof(E)) && vec_rows(y.data, y.stride, sizeof(O));
+  const int groups = (d + kEmbedCols - 1) / kEmbedCols;
+  const E* tab = static_cast<const E*>(table);
+  O* out = reinterpret_cast<O*>(y.data);
+  const bool wide = groups >= 4 && n * groups > 16384;
+  const int blocks = wide ? (groups + 3) / 4 : groups;
+  const int64_t wgs = (n * blocks + 3) / 4;
+  const dim3 grid(static_cast<unsigned>(wgs < (1 << 20) ? wgs : (1 << 20)));
+#define GO(V, U) embed_fwd_kernel<E, O, V, U><<<grid, dim3(256), 0, s>>>(tab, vocab, d, ids, n, scale, out, y.stride, blocks, err)
+  if (vec) {
+    if (wide) GO(true, 4); else GO(true, 1);
+  } else {
+    if (wide) GO(false, 4); else GO(false, 1);
+  }
+#undef GO
+}
+
+hipError_t launch_embed_fwd(const void* table, int64_t vocab, int64_t d, int32_t dtype, const int32_t* ids,
+                            int64_t n, float scale, RowsView y, int32_t out_dtype, hipStream_t s, int* err) {
+  const int dim = static_cast<int>(d);
+  if (dtype == STAPLE_BF16) {
+    if (out_dtype == STAPLE_BF16) embed_fwd<bf16_t, bf16_t>(table, vocab, dim, ids, n, scale, y, s, err);
+    else embed_fwd<bf16_t, float>(table, vocab, dim, ids, n, scale, y, s, err);
+  } else {
+    if (out_dtype == STAPLE_BF16) embed_fwd<float, bf16_t>(table, vocab, dim, ids, n, scale, y, s, err);
+    else embed_fwd<float, float>(table, vocab, dim, ids, n, scale, y, s, err);
+  }
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------- gradient
+// One token can hold a tenth of a batch, so the sorted positions, not the tokens, are dealt
+// out: a wave sums the runs of equal tokens within kEmbedChunk positions, for 512 columns.
+// A run that is a whole token's goes to its row.  One that a chunk's border cuts goes to
+// first[chunk] (begun in an earlier chunk) or last[chunk] (goes on in the next), and the
+// second kernel adds last[c0], first[c0 + 1], ..., first[c1] in that order: the result does
+// not change from run to run.
+
+// Unique index of sorted position p, -1 where the maps are out of range.
+__device__ __forceinline__ int32_t unique_of(int64_t p, int64_t n, int64_t nu, const int32_t* sorted_pos,
+                                             const int32_t* inv, int32_t& row) {
+  row = sorted_pos[p];
+  if (row < 0 || row >= n) return row = -1;
+  const int32_t u = inv[row];
+  return u >= 0 && u < nu ? u : -1;
+}
+
+// Row of grad of unique token u, NULL (and the error word) where it is out of range.
+__device__ __forceinline__ float* grad_row(const EmbedGrad& a, int32_t u, int lane, int* err) {
+  int64_t r = -1;
+  if (u >= 0) r = a.uniq ? a.uniq[u] : u;
+  if (r < 0 || r >= a.grad_rows) {
+    if (lane == 0) flag_index_error(err);
+    return nullptr;
+  }
+  return a.grad + r * a.d;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, int lane, float (&acc)[8]) {
+  using R = RowGroup<64, VEC>;
+  const int d = static_cast<int>(a.d);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] *= a.scale;
+  if (a.accumulate) {
+    float old[8];
+    R::load(row, g, lane, d, old);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += old[i];
+  }
+  R::store(row, g, lane, d, acc);
+}
+
+template <typename E, bool VEC>
+__global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups, float* __restrict__ first,
+                                                        float* __restrict__ last, int64_t ld, int* err) {
+  using R = RowGroup<64, VEC>;
+  const int lane = threadIdx.x & 63;
+  const int64_t n = a.n_tokens;
+  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (w >= chunks * groups) return;
+  const int64_t nu = *a.n_unique;
+  if (nu < 0 || nu > a.max_unique) {
+    if (lane == 0) flag_index_error(err);
+    return;
+  }
+  const int64_t c = w / groups;
+  const int g = static_cast<int>(w - c * groups);
+  const int d = static_cast<int>(a.d);
+  const int64_t p0 = c * kEmbedChunk;
+  const int len = static_cast<int>(n - p0 < kEmbedChunk ? n - p0 : kEmbedChunk);
+  // lane i: position p0 + i; the lane after the last one and lane 63: the neighbours outside
+  int32_t row = -1, u = -2;
+  const int64_t p = lane == 63 ? p0 - 1 : p0 + lane;
+  if ((lane <= len || lane == 63) && p >= 0 && p < n) {
+    u = unique_of(p, n, nu, a.sorted_pos, a.inv, row);
+    if (u < 0 && lane < len) flag_index_error(err);
+  }
+  const int32_t next = __shfl(u, lane < 62 ? lane + 1 : 62, 64);
+  const uint64_t ends = __ballot(lane < len && u != next);   // a run's last position
+  const bool begun = __shfl(u, 63, 64) == __shfl(u, 0, 64);
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  bool first_run = true;
+  for (int b = 0; b < len; b += kEmbedAhead) {
+    float v[kEmbedAhead][8];
+#pragma unroll
+    for (int j = 0; j < kEmbedAhead; ++j) {
+      const int32_t r = __shfl(row, b + j < len ? b + j : len - 1, 64);
+      if (r >= 0) {
+        R::load(reinterpret_cast<const E*>(a.dy.data) + r * a.dy.stride, g, lane, d, v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kEmbedAhead; ++j) {
+      const int k = b + j;
+      if (k >= len) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
+      const bool end = (ends >> k) & 1;
+      if (!end && k + 1 < len) continue;
+      if (first_run && begun) {
+        R::store(first + c * ld, g, lane, d, acc);
+      } else if (!end) {
+        R::store(last + c * ld, g, lane, d, acc);
+      } else {
+        float* to = grad_row(a, __shfl(u, k, 64), lane, err);
+        if (to) finish<VEC>(a, to, g, lane, acc);
+      }
+      first_run = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    }
+  }
+}
+
+// The chunk in which a cut run begins adds its parts.
+template <bool VEC>
+__global__ __launch_bounds__(256) void embed_bwd_join_kernel(EmbedGrad a, int groups,
+                                                             const float* __restrict__ first,
+                                                             const float* __restrict__ last, int64_t ld,
+                                                             int* err) {
+  using R = RowGroup<64, VEC>;
+  const int lane = threadIdx.x & 63;
+  const int64_t n = a.n_tokens;
+  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t nu = *a.n_unique;
+  if (w >= chunks * groups || nu < 0 || nu > a.max_unique) return;
+  const int64_t c = w / groups;
+  const int g = static_cast<int>(w - c * groups);
+  const int d = static_cast<int>(a.d);
+  const int64_t p0 = c * kEmbedChunk, p1 = p0 + kEmbedChunk;
+  if (p1 >= n) return;
+  int32_t row;
+  const int32_t u = unique_of(p1 - 1, n, nu, a.sorted_pos, a.inv, row);
+  if (u < 0 || unique_of(p1, n, nu, a.sorted_pos, a.inv, row) != u) return;
+  const int64_t begin = a.seg_start[u], end = a.seg_start[u + 1];
+  if (begin < p0) return;
+  if (begin >= p1 || end <= p1 || end > n) {
+    if (lane == 0) flag_index_error(err);
+    return;
+  }
+  const int64_t c1 = (end - 1) / kEmbedChunk;
+  float acc[8];
+  R::load(last + c * ld, g, lane, d, acc);
+  for (int64_t b = c + 1; b <= c1; b += kEmbedAhead) {
+    float v[kEmbedAhead][8];
+#pragma unroll
+    for (int j = 0; j < kEmbedAhead; ++j) R::load(first + (b + j <= c1 ? b + j : c1) * ld, g, lane, d, v[j]);
+#pragma unroll
+    for (int j = 0; j < kEmbedAhead; ++j)
+      if (b + j <= c1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
+      }
+  }
+  float* to = grad_row(a, u, lane, err);
+  if (to) finish<VEC>(a, to, g, lane, acc);
+}
+
+static int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
+
+size_t embed_bwd_workspace_bytes(int64_t n, int64_t d) {
+  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+  return chunks > 1 ? static_cast<size_t>(2 * chunks * part_stride(d)) * sizeof(float) : 0;
+}
+
+template <typename E>
+static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
+  const int64_t chunks = (a.n_tokens + kEmbedChunk - 1) / kEmbedChunk, ld = part_stride(a.d);
+  float* first = static_cast<float*>(ws);
+  float* last = first + chunks * ld;
+  const int groups = static_cast<int>((a.d + kEmbedCols - 1) / kEmbedCols);
+  const bool vec = a.d % 8 == 0 && vec_rows(a.dy.data, a.dy.stride, sizeof(E)) && vec_rows(a.grad, a.d, 4);
+  const dim3 grid(static_cast<unsigned>((chunks * groups + 3) / 4));
+  if (vec) embed_bwd_kernel<E, true><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
+  else embed_bwd_kernel<E, false><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
+  if (chunks == 1) return;
+  if (vec) embed_bwd_join_kernel<true><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
+  else embed_bwd_join_kernel<false><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
+}
+
+hipError_t launch_embed_bwd(const EmbedGrad& a, int32_t dtype, void* ws, hipStream_t s, int* err) {
+  if (dtype == STAPLE_BF16) embed_bwd<bf16_t>(a, ws, s, err);
+  else embed_bwd<float>(a, ws, s, err);
+  return hipGetLastError();
+}
+
+}  // namespace staple

@@ -1,0 +1,347 @@
+// Norms before and after a block, with the block's gate and residual sum.
+//
+//   b = z / rms(z) w_post  (or z),   r = x + s gate b,   h = r / rms(r) w_pre,
+//   rms(v) = sqrt(mean(v^2) + eps)
+//
+// backward, with t = dh w_pre and hat(v) = v / rms(v):
+//   dx = g = dr + (t - hat(r) mean(t hat(r))) / rms(r),       dw_pre = sum over rows of dh hat(r)
+//   dgate = s g b,   q = s gate g,
+//   dz = q, or (q w_post - hat(z) mean(q w_post hat(z))) / rms(z),   dw_post = sum of q hat(z)
+#include "model_ops.h"
+#include "row_io.h"
+
+namespace staple {
+
+// Eight elements of a vector shared by the rows (ones when NULL).
+template <int T, bool VEC>
+__device__ __forceinline__ void load_shared(const void* p, bool bf16, int g, int t, int d, float (&v)[8]) {
+  using R = RowGroup<T, VEC>;
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+  } else if (bf16) {
+    R::load(static_cast<const bf16_t*>(p), g, t, d, v);
+  } else {
+    R::load(static_cast<const float*>(p), g, t, d, v);
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ E* row_of(const RowsView& v, int64_t i) {
+  return reinterpret_cast<E*>(v.data) + i * v.stride;
+}
+
+// T lanes a row, G groups of eight elements a lane; rows of one wave share a workgroup.
+template <typename X, typename Z, int T, int G, bool VEC>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a) {
+  using R = RowGroup<T, VEC>;
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  __shared__ float tmp[2][kRows][T / 64];
+  const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  if (i >= a.n_rows) return;   // T >= 256: the whole workgroup; T = 64: a wave, which meets no barrier
+  const float inv_d = 1.0f / static_cast<float>(d);
+  float r[G][8], b[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (a.x.data) R::load(row_of<const X>(a.x, i), g, t, d, r[g]);
+    if (a.z.data) R::load(row_of<const Z>(a.z, i), g, t, d, b[g]);
+  }
+  if (a.z.data) {
+    float rstd = a.scale;
+    if (a.post) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss += b[g][k] * b[g][k];
+      const float inv = rsqrtf(row_sum<T>(ss, tmp[0][slot], t) * inv_d + a.eps);
+      if (a.rstd_z && t == 0) a.rstd_z[i] = inv;
+      rstd *= inv;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[g][k] *= rstd;
+      if (a.post && a.w_post) {
+        load_shared<T, VEC>(a.w_post, a.w_bf16, g, t, d, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[g][k] *= w[k];
+      }
+      if (a.gate_kind != Gate::kNone) {
+        if (a.gate_kind == Gate::kVector) load_shared<T, VEC>(a.gate.data, a.w_bf16, g, t, d, w);
+        else R::load(row_of<const Z>(a.gate, i), g, t, d, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[g][k] *= w[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[g][k] = a.x.data ? r[g][k] + b[g][k] : b[g][k];
+      R::store(row_of<X>(a.r, i), g, t, d, r[g]);
+    }
+  }
+  if (!a.pre) return;
+  float ss = 0.0f;
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss += r[g][k] * r[g][k];
+  const float inv = rsqrtf(row_sum<T>(ss, tmp[1][slot], t) * inv_d + a.eps);
+  if (a.rstd_r && t == 0) a.rstd_r[i] = inv;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float w[8];
+    load_shared<T, VEC>(a.w_pre, a.w_bf16, g, t, d, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[g][k] *= inv * w[k];
+    R::store(row_of<Z>(a.h, i), g, t, d, r[g]);
+  }
+}
+
+// Workgroups work off rows in turn and keep the sums over their rows in registers; parts:
+// [vectors][slots of all workgroups][d], added up by norm_columns_kernel in slot order.
+template <typename X, typename Z, int T, int G, bool VEC>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a, float* parts) {
+  using R = RowGroup<T, VEC>;
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  // two sums a row, in buffers of their own for rows in turn: between a sum's reads and the
+  // next writes to its buffer stands the barrier of the row between
+  __shared__ float tmp[2][2][kRows][T / 64];
+  const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  float sum_pre[G][8], sum_post[G][8], sum_gate[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum_pre[g][k] = sum_post[g][k] = sum_gate[g][k] = 0.0f;
+  const bool branch = norm_bwd_branch(a);
+  const bool need_z = norm_bwd_reads_z(a);
+  int odd = 0;
+  for (int64_t i = me; i < a.n_rows; i += slots, odd ^= 1) {
+    float q[G][8], hat_z[G][8], gate[G][8], w[8];
+    const float inv_z = a.post ? a.rstd_z[i] : 1.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (a.dr.data) {
+        R::load(row_of<const X>(a.dr, i), g, t, d, q[g]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[g][k] = 0.0f;
+      }
+      if (need_z) {
+        R::load(row_of<const Z>(a.z, i), g, t, d, hat_z[g]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) hat_z[g][k] *= inv_z;
+      }
+      if (a.gate_kind == Gate::kRows) R::load(row_of<const Z>(a.gate, i), g, t, d, gate[g]);
+      else load_shared<T, VEC>(a.gate.data, a.w_bf16, g, t, d, gate[g]);
+    }
+    if (a.pre) {
+      const float inv = a.rstd_r[i];
+      float hat[G][8], dt[G][8], dot = 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (a.r.data) {
+          R::load(row_of<const X>(a.r, i), g, t, d, hat[g]);
+        } else {   // as the forward had it before r was rounded
+          load_shared<T, VEC>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) hat[g][k] = a.scale * gate[g][k] * w[k] * hat_z[g][k];
+          if (a.x.data) {
+            R::load(row_of<const X>(a.x, i), g, t, d, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) hat[g][k] += w[k];
+          }
+        }
+        R::load(row_of<const Z>(a.dh, i), g, t, d, dt[g]);
+        load_shared<T, VEC>(a.w_pre, a.w_bf16, g, t, d, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          hat[g][k] *= inv;
+          sum_pre[g][k] += dt[g][k] * hat[g][k];
+          dt[g][k] *= w[k];
+          dot += dt[g][k] * hat[g][k];
+        }
+      }
+      const float mean = row_sum<T>(dot, tmp[odd][0][slot], t) * inv_d;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[g][k] += inv * (dt[g][k] - hat[g][k] * mean);
+    }
+    if (a.dx.data) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) R::store(row_of<X>(a.dx, i), g, t, d, q[g]);
+    }
+    if (!branch) continue;
+    float dot = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      load_shared<T, VEC>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[g][k] *= a.scale;
+      if (a.gate_kind != Gate::kNone) {
+        if (a.dgate.data || a.dgate_sum) {
+          float dg[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            dg[k] = q[g][k] * hat_z[g][k] * w[k];
+            sum_gate[g][k] += dg[k];
+          }
+          if (a.dgate.data) R::store(row_of<Z>(a.dgate, i), g, t, d, dg);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[g][k] *= gate[g][k];
+      }
+      if (a.post) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sum_post[g][k] += q[g][k] * hat_z[g][k];
+          q[g][k] *= w[k];
+          dot += q[g][k] * hat_z[g][k];
+        }
+      }
+    }
+    if (a.post) {
+      const float mean = row_sum<T>(dot, tmp[odd][1][slot], t) * inv_d;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[g][k] = inv_z * (q[g][k] - hat_z[g][k] * mean);
+    }
+    if (a.dz.data) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) R::store(row_of<Z>(a.dz, i), g, t, d, q[g]);
+    }
+  }
+  float* part = parts + me * d;
+  const int64_t one = slots * d;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float* p = part;
+    if (a.dw_pre) {
+      R::store(p, g, t, d, sum_pre[g]);
+      p += one;
+    }
+    if (a.dw_post) {
+      R::store(p, g, t, d, sum_post[g]);
+      p += one;
+    }
+    if (a.dgate_sum) R::store(p, g, t, d, sum_gate[g]);
+  }
+}
+
+// Sums of the parts, 64 columns a workgroup: wave k adds slots k, k + 16, ..., then the waves' sums.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ parts, int slots, int d,
+                                                            float* o0, float* o1, float* o2) {
+  __shared__ float tmp[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  const float* p = parts + static_cast<int64_t>(blockIdx.y) * slots * d;
+  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+  float s = 0.0f;
+  if (col < d)
+    for (int i = wave; i < slots; i += 16) s += p[static_cast<int64_t>(i) * d + col];
+  tmp[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || col >= d) return;
+  for (int k = 1; k < 16; ++k) s += tmp[k][lane];
+  out[col] = s;
+}
+
+static bool vec_view(const RowsView& v, int bytes) {
+  return v.data == nullptr || ((reinterpret_cast<uintptr_t>(v.data) & 15) == 0 && v.stride * bytes % 16 == 0);
+}
+static bool vec_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+static bool norm_vec(const NormView& v, int32_t r_dtype, int32_t dtype) {
+  const int xb = r_dtype == STAPLE_BF16 ? 2 : 4, zb = dtype == STAPLE_BF16 ? 2 : 4;
+  const bool gate = v.gate_kind == Gate::kRows ? vec_view(v.gate, zb) : vec_ptr(v.gate.data);
+  return v.d % 8 == 0 && vec_view(v.x, xb) && vec_view(v.r, xb) && vec_view(v.dr, xb) && vec_view(v.dx, xb) &&
+         vec_view(v.z, zb) && vec_view(v.h, zb) && vec_view(v.dh, zb) && vec_view(v.dz, zb) &&
+         vec_view(v.dgate, zb) && gate && vec_ptr(v.w_pre) && vec_ptr(v.w_post);
+}
+
+// Lanes a row and groups of eight elements a lane.
+#define NORM_SHAPES(GO)                          \
+  do {                                           \
+    if (v.d <= 512) GO(64, 1);                   \
+    else if (v.d <= 1024) GO(64, 2);             \
+    else if (v.d <= 2048) GO(256, 1);            \
+    else if (v.d <= 4096) GO(256, 2);            \
+    else if (v.d <= 8192) GO(512, 2);            \
+    else GO(1024, 2);                            \
+  } while (0)
+
+static int norm_rows_a_workgroup(int d) { return d <= 1024 ? 4 : 1; }
+
+template <typename X, typename Z, bool VEC>
+static void norm_fwd(const NormView& v, hipStream_t s) {
+  const int rows = norm_rows_a_workgroup(v.d);
+  const dim3 grid(static_cast<unsigned>((v.n_rows + rows - 1) / rows));
+#define GO(T, G) norm_fwd_kernel<X, Z, T, G, VEC><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v)
+  NORM_SHAPES(GO);
+#undef GO
+}
+
+static int norm_vectors(const NormView& v) {
+  return (v.dw_pre != nullptr) + (v.dw_post != nullptr) + (v.dgate_sum != nullptr);
+}
+
+static int64_t norm_bwd_grid(const NormView& v) {
+  const int rows = norm_rows_a_workgroup(v.d);
+  const int64_t all = (v.n_rows + rows - 1) / rows;
+  const int64_t most = static_cast<int64_t>(device_cus()) * (v.d <= 4096 ? 4 : v.d <= 8192 ? 2 : 1);
+  return all < most ? all : most;
+}
+
+size_t norm_bwd_workspace_bytes(const NormView& v) {
+  return static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * norm_rows_a_workgroup(v.d) * v.d * sizeof(float);
+}
+
+template <typename X, typename Z, bool VEC>
+static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(norm_bwd_grid(v)));
+  if (v.n_rows > 0) {
+#define GO(T, G) norm_bwd_kernel<X, Z, T, G, VEC><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v, parts)
+    NORM_SHAPES(GO);
+#undef GO
+  }
+  const int n = norm_vectors(v);
+  if (n == 0) return;
+  float* out[3] = {};
+  int k = 0;
+  for (float* p : {v.dw_pre, v.dw_post, v.dgate_sum})
+    if (p) out[k++] = p;
+  norm_columns_kernel<<<dim3((v.d + 63) / 64, n), dim3(1024), 0, s>>>(
+      parts, static_cast<int>(grid.x) * norm_rows_a_workgroup(v.d), v.d, out[0], out[1], out[2]);
+}
+
+#define NORM_TYPES(CALL)                                                         \
+  const bool vec = norm_vec(v, r_dtype, dtype);                                  \
+  if (r_dtype == STAPLE_BF16) {                                                  \
+    if (vec) CALL(bf16_t, bf16_t, true); else CALL(bf16_t, bf16_t, false);       \
+  } else if (dtype == STAPLE_BF16) {                                             \
+    if (vec) CALL(float, bf16_t, true); else CALL(float, bf16_t, false);         \
+  } else {                                                                       \
+    if (vec) CALL(float, float, true); else CALL(float, float, false);           \
+  }
+
+hipError_t launch_norm_fwd(const NormView& v, int32_t r_dtype, int32_t dtype, hipStream_t s) {
+#define CALL(X, Z, V) norm_fwd<X, Z, V>(v, s)
+  NORM_TYPES(CALL)
+#undef CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormView& v, int32_t r_dtype, int32_t dtype, void* ws, hipStream_t s) {
+  float* parts = static_cast<float*>(ws);
+#define CALL(X, Z, V) norm_bwd<X, Z, V>(v, parts, s)
+  NORM_TYPES(CALL)
+#undef CALL
+  return hipGetLastError();
+}
+
+}  // namespace staple

@@ -1,0 +1,102 @@
+// Rows of bf16 or fp32 elements read and written eight elements a lane, and sums over a
+// workgroup's waves in a fixed order.
+#pragma once
+
+#include "common.h"
+
+namespace staple {
+
+// Eight consecutive elements, 16-byte aligned.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p);
+  const f32x4_t b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[i + 4] = b[i];
+  }
+}
+__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
+  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<u32x4_t*>(p) = w;
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(p->bits); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(bf16_t* p, float v) { p->bits = f32_to_bf16(v); }
+
+// The eight elements that lane t of T holds of group g of a row: with VEC, elements
+// (g T + t) 8 .. + 7, 16 bytes (two times 16 in fp32) a load; without, for rows that are
+// not 16-byte aligned or end inside eight elements, elements (8 g + i) T + t, so that
+// neighbouring lanes read neighbouring elements.
+template <int T, bool VEC>
+struct RowGroup {
+  __device__ __forceinline__ static int column(int g, int t, int i) {
+    return VEC ? (g * T + t) * 8 + i : (8 * g + i) * T + t;
+  }
+  template <typename E>
+  __device__ __forceinline__ static void load(const E* row, int g, int t, int d, float (&v)[8]) {
+    if (VEC) {
+      if (column(g, t, 0) < d) {
+        load8(row + column(g, t, 0), v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = column(g, t, i) < d ? load1(row + column(g, t, i)) : 0.0f;
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ static void store(E* row, int g, int t, int d, const float (&v)[8]) {
+    if (VEC) {
+      if (column(g, t, 0) < d) store8(row + column(g, t, 0), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (column(g, t, i) < d) store1(row + column(g, t, i), v[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// Sum over the T lanes that share a row.  tmp: T / 64 floats of LDS that no wave still
+// reads from an earlier sum (callers alternate between two).
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* tmp, int t) {
+  v = wave_sum(v);
+  if (T == 64) return v;
+  if ((t & 63) == 0) tmp[t >> 6] = v;
+  __syncthreads();
+  float s = tmp[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) s += tmp[i];
+  return s;
+}
+
+}  // namespace staple
