@@ -5,17 +5,35 @@
 // Their sums are exact in 64-bit integers, so that no order of adding, and no atomic one, changes a
 // token, and a sum is off by half a unit's inverse a logit at most, where sums in 32 bits would be
 // off by some 1e-7.
+//
+// The kept tokens are a first part of the order of falling logits (ties: rising index), so one
+// pass finds the largest logit, a second one counts and weighs the tokens in kBins intervals of
+// the logit, which tells the interval that the cut falls into, and a third one lists that
+// interval's tokens and sums the weights above it, by blocks of the row.  The list gives the
+// cut, the blocks' sums the block of the drawn token.  A row is dealt out to several workgroups
+// (as many rows as fill the GPU take one each); the last of them to arrive goes on with the row.
+// Without top-k and top-p the second pass sums the blocks and the third is not needed.
 #include "model_ops.h"
 #include "row_io.h"
 
 namespace staple {
 
-constexpr int kSampleThreads = 1024;
 typedef unsigned long long u64;
 
-// Order of the logits: larger logits have larger keys; NaN counts as -inf, -0 as 0.
+constexpr int kSampleThreads = 256;
+constexpr int kWaves = kSampleThreads / 64;
+constexpr int kBins = 512;          // two a lane of a workgroup
+constexpr int kList = 2048;         // listed tokens
+constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
+constexpr int kMostChunks = 64;     // workgroups of a row
+constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
+constexpr int kScan = (kMostBlocks + kSampleThreads - 1) / kSampleThreads;
+
+// --------------------------------------------------------------------------- logits and weights
+__device__ __forceinline__ float no_nan(float l) { return l == l ? l : -__builtin_inff(); }
+
+// Order of the logits: larger logits have larger keys, -0 that of 0.
 __device__ __forceinline__ uint32_t key_of(float l) {
-  if (!(l == l)) l = -__builtin_inff();
   const uint32_t b = __float_as_uint(l + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -23,16 +41,50 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// The weights of a row.
+// Order of a row's tokens: falling logits, ties by rising index.  No two are the same.
+constexpr int kIndexBits = 22;
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
+static_assert(kSampleMaxVocab <= int64_t(1) << kIndexBits, "an index fits");
+__device__ __forceinline__ u64 place_of(float l, int j) {
+  return static_cast<u64>(key_of(l)) << kIndexBits | (kIndexMask - static_cast<uint32_t>(j));
+}
+__device__ __forceinline__ float logit_at(u64 place) { return logit_of(static_cast<uint32_t>(place >> kIndexBits)); }
+__device__ __forceinline__ int index_at(u64 place) {
+  return static_cast<int>(kIndexMask - (static_cast<uint32_t>(place) & kIndexMask));
+}
+
+// 2^(i / 32), i < 32.
+struct Exponents {
+  double step[32];
+  __device__ __forceinline__ void fill() {
+    if (threadIdx.x < 32) step[threadIdx.x] = exp2(threadIdx.x * 0.03125);
+  }
+};
+
+// A row's weights.
 struct Weights {
-  uint32_t top;   // key of the largest logit
-  double rate;    // 1 / T
-  double unit;
-  __device__ __forceinline__ u64 operator()(uint32_t key) const {
-    if (key == top) return static_cast<u64>(unit);
-    const double l = logit_of(key), m = logit_of(top);
-    if (l == -__builtin_inf() || m == __builtin_inf()) return 0;
-    return static_cast<u64>(rint(exp((l - m) * rate) * unit));
+  float top;
+  double rate;      // log2(e) / T
+  int unit_log2;
+  const double* step;
+  __device__ __forceinline__ u64 unit() const { return u64(1) << unit_log2; }
+  // 2^y with y = n / 32 + r: the step of n's last five bits, its other bits as the exponent, and
+  // five terms of exp(r ln 2) (|r| <= 1/64: off by 2^-48)
+  __device__ __forceinline__ u64 operator()(float l) const {
+    const double far = fmax((static_cast<double>(l) - static_cast<double>(top)) * rate, -1100.0);
+    const double magic = 6755399441055744.0;   // 3 2^51: a sum with it is rounded to a whole number
+    const double big = far * 32.0 + magic;
+    const int n = static_cast<int>(__double_as_longlong(big));
+    const double r = (far - (big - magic) * 0.03125) * 0.693147180559945309417;
+    double p = 1.0 / 120.0;
+    p = p * r + 1.0 / 24.0;
+    p = p * r + 1.0 / 6.0;
+    p = p * r + 0.5;
+    p = p * r + 1.0;
+    p = p * r + 1.0;
+    const double w = ldexp(p * step[n & 31], (n >> 5) + unit_log2);
+    const u64 whole = static_cast<u64>(__double_as_longlong(w + 4503599627370496.0)) & ((u64(1) << 52) - 1);
+    return l == top ? unit() : whole;
   }
 };
 
@@ -52,27 +104,124 @@ __device__ __forceinline__ u64 part_of(float share, u64 total, bool& rest) {
   return static_cast<u64>(whole);
 }
 
-struct RowSums {
-  u64 wave[kSampleThreads / 64];
-  uint32_t key[kSampleThreads / 64];
-  u64 weights[256];
-  uint32_t counts[256];
-  u64 found[4];
+// ------------------------------------------------------------------------------- a row's layout
+// The row is cut into blocks of `size` elements that begin where its memory is 16-byte aligned
+// (`shift` elements before its first one); consecutive blocks make a workgroup's chunk.
+struct SampleGrid {
+  int chunks, blocks, blocks_a_chunk, size;
+  int64_t row_bytes;
 };
 
-__device__ __forceinline__ u64 sum_all(u64 v, RowSums& s) {
+struct RowState {
+  u64 total;             // of all weights
+  u64 weight_before;     // of the tokens above interval `lo`
+  uint32_t count_before;
+  uint32_t listed;
+  uint32_t arrived[2];
+  int lo, hi;            // intervals whose tokens are listed
+  int mode;
+};
+enum { kDone, kListed, kSearch };   // the token is known; lo and hi are listed; too many for the list
+
+struct RowSpace {
+  RowState* state;
+  u64* best;        // [chunks]: place of the largest logit
+  float* least;     // [chunks]: the smallest finite logit
+  u64* sums;        // [blocks]: kept weights, those of listed tokens aside
+  u64* list;        // [kList]: places
+  u64* weights;     // [chunks][kBins]
+  uint32_t* counts; // [chunks][kBins]
+  __host__ __device__ RowSpace(char* p, int64_t row, const SampleGrid& g) {
+    p += row * g.row_bytes;
+    state = reinterpret_cast<RowState*>(p);
+    best = reinterpret_cast<u64*>(p + 64);
+    sums = best + kMostChunks;
+    list = sums + kMostBlocks + 7;
+    weights = list + kList;
+    counts = reinterpret_cast<uint32_t*>(weights + static_cast<int64_t>(g.chunks) * kBins);
+    least = reinterpret_cast<float*>(counts + static_cast<int64_t>(g.chunks) * kBins);
+  }
+};
+static_assert(sizeof(RowState) <= 64, "before best");
+
+template <typename E>
+struct Row {
+  const E* p;
+  int n, shift;
+  __device__ __forceinline__ Row(const SampleView& a, int64_t row)
+      : p(reinterpret_cast<const E*>(a.logits) + row * a.stride), n(a.vocab),
+        shift(static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(E))) {}
+  // Index of element 0 of lane l of the it-th 512 elements of a block.
+  __device__ __forceinline__ int first(const SampleGrid& g, int block, int it, int lane) const {
+    return block * g.size + it * 512 + lane * 8 - shift;
+  }
+  // Eight elements from j; -inf for those outside the row and for NaN.
+  __device__ __forceinline__ void load(int j, float (&v)[8]) const {
+    if (j >= 0 && j + 8 <= n) {
+      load8(p + j, v);
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  u64 r = 0;
-  for (int i = 0; i < kSampleThreads / 64; ++i) r += s.wave[i];
-  return r;
+      for (int i = 0; i < 8; ++i) v[i] = no_nan(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = j + i >= 0 && j + i < n ? no_nan(load1(p + j + i)) : -__builtin_inff();
+    }
+  }
+};
+
+// A row's limits and weights, from its largest logit.
+struct Limits {
+  float top, temperature;
+  int first;             // of the largest logits
+  Weights weight;
+  u64 least_weight;      // of min-p
+  int k;                 // 0: no limit
+  float p;               // 1: no limit
+  float bin_rate;
+  bool greedy, empty;
+  // Interval of a logit, rising as it falls.
+  __device__ __forceinline__ int bin(float l) const {
+    return l == top ? 0 : static_cast<int>(fminf((top - l) * bin_rate, kBins - 1));
+  }
+};
+
+__device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& g, const RowSpace& s,
+                            const double* step) {
+  u64 best = 0;
+  float least = __builtin_inff();
+  const int lane = threadIdx.x & 63;
+  if (lane < g.chunks) {
+    best = s.best[lane];
+    least = s.least[lane];
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const u64 x = __shfl_xor(best, o, 64);
+    best = x > best ? x : best;
+    least = fminf(least, __shfl_xor(least, o, 64));
+  }
+  Limits m;
+  m.top = logit_at(best);
+  m.first = index_at(best);
+  m.empty = m.top == -__builtin_inff();
+  m.temperature = a.temperature ? a.temperature[row] : 1.0f;
+  m.greedy = !(m.temperature > 0.0f);
+  const int bits = 62 - (32 - __clz(a.vocab));
+  m.weight = Weights{m.top, 1.44269504088896340736 / static_cast<double>(m.temperature), bits < 50 ? bits : 50, step};
+  const int k = a.top_k ? a.top_k[row] : 0;
+  m.k = k > 0 && k < a.vocab ? k : 0;
+  const float p = a.top_p ? a.top_p[row] : 1.0f;
+  m.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
+  const float low = a.min_p ? a.min_p[row] : 0.0f;
+  m.least_weight = low > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(low, 1.0f)) * m.weight.unit())) : 0;
+  // weights past this distance are rounded to zero
+  const float reach = fminf(m.temperature * (0.6932f * (m.weight.unit_log2 + 2)), m.top - least);
+  m.bin_rate = reach > 0.0f ? kBins / reach : 0.0f;
+  return m;
 }
 
-// Sum over the lanes before this one, and over all.
-__device__ __forceinline__ u64 sum_before(u64 v, RowSums& s, u64& total) {
+// ------------------------------------------------------------------------------ workgroup sums
+// Sum over the lanes before this one; total over all.
+__device__ __forceinline__ u64 sum_before(u64 v, u64* wave_sums, u64& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   u64 x = v;
 #pragma unroll
@@ -81,179 +230,528 @@ __device__ __forceinline__ u64 sum_before(u64 v, RowSums& s, u64& total) {
     if (lane >= o) x += y;
   }
   __syncthreads();
-  if (lane == 63) s.wave[wave] = x;
+  if (lane == 63) wave_sums[wave] = x;
   __syncthreads();
   u64 before = 0;
   total = 0;
-  for (int i = 0; i < kSampleThreads / 64; ++i) {
-    if (i < wave) before += s.wave[i];
-    total += s.wave[i];
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < wave) before += wave_sums[i];
+    total += wave_sums[i];
   }
   return before + x - v;
 }
 
-// The kept tokens: keys above `key`, and of those equal to it the first `ties` in the row.
-struct Cut {
-  uint32_t key;
-  uint32_t ties;
+__device__ __forceinline__ u64 wave_sum(u64 v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Whether this workgroup is the last of its row's to get here; what the others wrote is then seen.
+__device__ __forceinline__ bool last_of_row(uint32_t* arrived, int chunks, uint32_t* shared) {
+  if (chunks == 1) {
+    __syncthreads();
+    return true;
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *shared = atomicAdd(arrived, 1u);
+  __syncthreads();
+  const bool last = *shared == static_cast<uint32_t>(chunks - 1);
+  if (last) __threadfence();
+  return last;
+}
+
+struct Shared {
+  Exponents exps;
+  u64 wave[kWaves];
+  u64 found[4];
+  uint32_t arrived;
 };
 
-// In the order of falling keys, ties by rising index, the shortest run of tokens whose counts
-// (BY_COUNT) or weights reach `want` (at least 1), found digit by digit of the key.
-template <typename E, bool BY_COUNT>
-__device__ Cut find_cut(const E* l, int n, const Weights& weight, u64 want, RowSums& s) {
-  uint32_t prefix = 0;
-  uint32_t ties = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    for (int b = threadIdx.x; b < 256; b += kSampleThreads) {
-      s.counts[b] = 0;
-      s.weights[b] = 0;
-    }
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSampleThreads) {
-      const uint32_t key = key_of(load1(l + j));
-      if (shift < 24 && (key >> (shift + 8)) != (prefix >> (shift + 8))) continue;
-      const int b = (key >> shift) & 255;
-      atomicAdd(&s.counts[b], 1u);
-      if (!BY_COUNT) atomicAdd(&s.weights[b], weight(key));
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 left = want;
-      int b = 255, last = 255;
-      for (; b >= 0; --b) {
-        if (s.counts[b] == 0) continue;
-        last = b;
-        const u64 here = BY_COUNT ? s.counts[b] : s.weights[b];
-        if (here >= left) break;
-        left -= here;
-      }
-      if (b < 0) {   // all of them: the last one is reached
-        b = last;
-        left += BY_COUNT ? s.counts[b] : s.weights[b];
-      }
-      s.found[0] = b;
-      s.found[1] = left;
-      s.found[2] = s.counts[b];
-    }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(s.found[0]) << shift;
-    want = s.found[1];
-    ties = static_cast<uint32_t>(s.found[2]);
+// ------------------------------------------------------------------------------------- the draw
+// The token at which the sum of the kept weights passes u times their total.  sums: of the
+// blocks; kept(l, j): whether token j, with its weight not below min-p, is kept.
+template <typename E, typename Kept>
+__device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, const u64* sums,
+                     Shared& s, Kept kept) {
+  const Row<E> r(a, row);
+  u64 mine[kScan], all = 0;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) {
+    const int b = threadIdx.x * kScan + i;
+    mine[i] = b < g.blocks ? sums[b] : 0;
+    all += mine[i];
   }
-  // `want` is left to the tokens with this key
-  if (BY_COUNT) return Cut{prefix, static_cast<uint32_t>(want < ties ? want : ties)};
-  const u64 w = weight(prefix);
-  const u64 need = w == 0 ? 1 : (want + w - 1) / w;
-  return Cut{prefix, static_cast<uint32_t>(need < ties ? (need > 0 ? need : 1) : ties)};
+  u64 total;
+  u64 before = sum_before(all, s.wave, total);
+  const float u = a.u[row];
+  bool rest;
+  const u64 target = !(u > 0.0f) ? 0 : u < 1.0f ? part_of(u, total, rest) : total - 1;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) {
+    if (before <= target && target < before + mine[i]) {
+      s.found[0] = threadIdx.x * kScan + i;
+      s.found[1] = before;
+    }
+    before += mine[i];
+  }
+  __syncthreads();
+  const int block = static_cast<int>(s.found[0]);
+  before = s.found[1];
+  const int each = g.size / kSampleThreads;   // 2, 4 or 8 elements a lane
+  const int j0 = block * g.size - r.shift + threadIdx.x * each;
+  u64 w[8];
+  float l[8];
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 0;
+    const int j = j0 + i;
+    if (i < each && j >= 0 && j < r.n) {
+      l[i] = no_nan(load1(r.p + j));
+      const u64 x = m.weight(l[i]);
+      if (x >= m.least_weight && kept(l[i], j)) w[i] = x;
+    }
+    all += w[i];
+  }
+  u64 of_block;
+  before += sum_before(all, s.wave, of_block);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (w[i] > 0 && before <= target && target < before + w[i]) {
+      a.token[row] = j0 + i;
+      if (a.logprob) {
+        const double d = l[i] == m.top ? 0.0 : (static_cast<double>(l[i]) - m.top) / static_cast<double>(m.temperature);
+        a.logprob[row] = static_cast<float>(d - log(static_cast<double>(total) / static_cast<double>(m.weight.unit())));
+      }
+    }
+    before += w[i];
+  }
 }
 
-// Sum of the kept weights.
+// -------------------------------------------------------------------------------------- pass one
 template <typename E>
-__device__ u64 kept_sum(const E* l, int n, const Weights& weight, Cut cut, RowSums& s) {
-  u64 w = 0;
-  for (int j = threadIdx.x; j < n; j += kSampleThreads) {
-    const uint32_t key = key_of(load1(l + j));
-    if (key > cut.key) w += weight(key);
-  }
-  return sum_all(w, s) + cut.ties * weight(cut.key);
-}
-
-template <typename E>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleView a) {
-  __shared__ RowSums s;
-  const int64_t row = blockIdx.x;
-  const E* l = reinterpret_cast<const E*>(a.logits) + row * a.stride;
-  const int n = a.vocab;
-  // the largest logit, and the first place of it
+__global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ u64 best_of[kWaves];
+  __shared__ float least_of[kWaves];
+  const int64_t row = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
+  const Row<E> r(a, row);
+  const RowSpace s(ws, row, g);
+  if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = s.state->listed = 0;
   u64 best = 0;
-  for (int j = threadIdx.x; j < n; j += kSampleThreads) {
-    const u64 x = static_cast<u64>(key_of(load1(l + j))) << 32 | (0xffffffffu - static_cast<uint32_t>(j));
-    best = x > best ? x : best;
-  }
+  float least = __builtin_inff();
+  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
+  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves)
+    for (int it = 0; it < g.size / 512; ++it) {
+      const int j = r.first(g, b, it, lane);
+      float v[8];
+      r.load(j, v);
+      float top = v[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (v[i] != -__builtin_inff()) least = fminf(least, v[i]);
+        const u64 x = place_of(v[i], j + i);
+        if (v[i] == top && j + i >= 0 && j + i < r.n && x > best) best = x;
+      }
+    }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
     const u64 x = __shfl_xor(best, o, 64);
     best = x > best ? x : best;
+    least = fminf(least, __shfl_xor(least, o, 64));
   }
-  if ((threadIdx.x & 63) == 0) s.wave[threadIdx.x >> 6] = best;
+  if (lane == 0) {
+    best_of[wave] = best;
+    least_of[wave] = least;
+  }
   __syncthreads();
-  for (int i = 0; i < kSampleThreads / 64; ++i) best = s.wave[i] > best ? s.wave[i] : best;
-  const uint32_t top = static_cast<uint32_t>(best >> 32);
-  const float t = a.temperature ? a.temperature[row] : 1.0f;
-  const bool empty = logit_of(top) == -__builtin_inff();
-  if (empty || !(t > 0.0f)) {
-    if (threadIdx.x == 0) {
-      a.token[row] = empty ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
-      if (a.logprob) a.logprob[row] = empty ? -__builtin_inff() : 0.0f;
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kWaves; ++i) {
+      best = best_of[i] > best ? best_of[i] : best;
+      least = fminf(least, least_of[i]);
     }
-    return;
-  }
-  const int bits = 62 - (32 - __clz(n));
-  const Weights weight{top, 1.0 / static_cast<double>(t), static_cast<double>(u64(1) << (bits < 50 ? bits : 50))};
-  Cut cut{0u, 0u};   // nothing has the key 0: all are kept
-  const int k = a.top_k ? a.top_k[row] : 0;
-  if (k > 0 && k < n) cut = find_cut<E, true>(l, n, weight, k, s);
-  u64 total = kept_sum(l, n, weight, cut, s);
-  const float p = a.top_p ? a.top_p[row] : 1.0f;
-  if (p < 1.0f) {
-    bool rest = false;
-    u64 want = p > 0.0f ? part_of(p, total, rest) : 0;
-    want += rest || want == 0;
-    const Cut by_p = find_cut<E, false>(l, n, weight, want, s);
-    if (by_p.key > cut.key || (by_p.key == cut.key && by_p.ties < cut.ties)) cut = by_p;
-    total = kept_sum(l, n, weight, cut, s);
-  }
-  double least = a.min_p && a.min_p[row] > 0.0f ? static_cast<double>(a.min_p[row]) : 0.0;
-  if (least > 1.0) least = 1.0;
-  const u64 floor_w = static_cast<u64>(ceil(least * weight.unit));
-  if (floor_w > 0) {
-    u64 w = 0;
-    for (int j = threadIdx.x; j < n; j += kSampleThreads) {
-      const uint32_t key = key_of(load1(l + j));
-      const u64 x = key > cut.key ? weight(key) : 0;
-      if (x >= floor_w) w += x;
-    }
-    const u64 tie = weight(cut.key);
-    total = sum_all(w, s) + (cut.ties > 0 && tie >= floor_w ? cut.ties * tie : 0);
-  }
-  // the first token at which the sum passes u total
-  const float u = a.u[row];
-  bool rest;
-  const u64 target = !(u > 0.0f) ? 0 : u < 1.0f ? part_of(u, total, rest) : total - 1;
-  u64 before = 0;
-  uint32_t ties = 0;
-  for (int j0 = 0; j0 < n; j0 += kSampleThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint32_t key = j < n ? key_of(load1(l + j)) : 0u;
-    u64 tied_here;
-    const bool tied = j < n && key == cut.key;
-    const uint32_t rank = ties + static_cast<uint32_t>(sum_before(tied, s, tied_here));
-    ties += static_cast<uint32_t>(tied_here);
-    u64 w = 0;
-    if (j < n && (key > cut.key || (tied && rank < cut.ties))) w = weight(key);
-    if (w < floor_w) w = 0;
-    u64 here;
-    const u64 mine = before + sum_before(w, s, here);
-    if (w > 0 && mine <= target && target < mine + w) {
-      a.token[row] = j;
-      if (a.logprob) {
-        const double d = key == top ? 0.0 : (static_cast<double>(logit_of(key)) - logit_of(top)) * weight.rate;
-        a.logprob[row] = static_cast<float>(d - log(static_cast<double>(total) / weight.unit));
-      }
-    }
-    before += here;
-    if (before > target) break;
+    s.best[c] = best;
+    s.least[c] = least;
   }
 }
 
-size_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
+// -------------------------------------------------------------------------------------- pass two
+// The token of a row that needs no sums.
+__device__ __forceinline__ bool plain_row(const SampleView& a, int64_t row, const Limits& m, int c, RowState* state) {
+  if (!m.empty && !m.greedy) return false;
+  if (c == 0 && threadIdx.x == 0) {
+    a.token[row] = m.empty ? -1 : m.first;
+    if (a.logprob) a.logprob[row] = m.empty ? -__builtin_inff() : 0.0f;
+    state->mode = kDone;
+  }
+  return true;
+}
 
-hipError_t launch_sample(const SampleView& v, int32_t dtype, void*, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(v.n_rows)), threads(kSampleThreads);
-  if (dtype == STAPLE_BF16) sample_kernel<bf16_t><<<grid, threads, 0, s>>>(v);
-  else sample_kernel<float><<<grid, threads, 0, s>>>(v);
+struct KeepAll {
+  __device__ __forceinline__ bool operator()(float, int) const { return true; }
+};
+
+// A row without top-k and top-p: the blocks' sums, and the draw.
+template <typename E>
+__device__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, const RowSpace& s,
+                         Shared& sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
+  const Row<E> r(a, row);
+  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
+  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves) {
+    u64 sum = 0;
+    for (int it = 0; it < g.size / 512; ++it) {
+      float v[8];
+      r.load(r.first(g, b, it, lane), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const u64 w = m.weight(v[i]);
+        sum += w >= m.least_weight ? w : 0;
+      }
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) s.sums[b] = sum;
+  }
+  if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
+  if (threadIdx.x == 0) s.state->mode = kDone;
+  draw<E>(a, row, g, m, s.sums, sh, KeepAll());
+}
+
+template <typename E>
+__global__ __launch_bounds__(kSampleThreads) void sample_free_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ Shared sh;
+  const int64_t row = blockIdx.y;
+  const RowSpace s(ws, row, g);
+  sh.exps.fill();
+  __syncthreads();
+  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  if (plain_row(a, row, m, blockIdx.x, s.state)) return;
+  free_row<E>(a, row, g, m, s, sh);
+}
+
+// Counts and weights of the intervals, and from all chunks' the interval of the cut.
+template <typename E>
+__global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ Shared sh;
+  __shared__ u64 weights[kBins];
+  __shared__ uint32_t counts[kBins];
+  const int64_t row = blockIdx.y;
+  const RowSpace s(ws, row, g);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  sh.exps.fill();
+  for (int i = t; i < kBins; i += kSampleThreads) {
+    weights[i] = 0;
+    counts[i] = 0;
+  }
+  __syncthreads();
+  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  if (plain_row(a, row, m, c, s.state)) return;
+  if (m.k == 0 && m.p == 1.0f) {
+    free_row<E>(a, row, g, m, s, sh);
+    return;
+  }
+  const Row<E> r(a, row);
+  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
+  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves)
+    for (int it = 0; it < g.size / 512; ++it) {
+      float v[8];
+      r.load(r.first(g, b, it, lane), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const u64 w = m.weight(v[i]);
+        if (w == 0) continue;   // never drawn, and nothing in any sum
+        const int bin = m.bin(v[i]);
+        atomicAdd(&counts[bin], 1u);
+        atomicAdd(&weights[bin], w);
+      }
+    }
+  __syncthreads();
+  if (g.chunks > 1) {
+    for (int i = t; i < kBins; i += kSampleThreads) {
+      s.weights[c * kBins + i] = weights[i];
+      s.counts[c * kBins + i] = counts[i];
+    }
+  }
+  if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
+  constexpr int kEach = kBins / kSampleThreads;
+  u64 w[kEach];
+  uint32_t n[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int bin = t * kEach + i;
+    w[i] = weights[bin];
+    n[i] = counts[bin];
+  }
+  if (g.chunks > 1) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      w[i] = 0;
+      n[i] = 0;
+    }
+#pragma unroll 8
+    for (int k = 0; k < g.chunks; ++k)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        w[i] += s.weights[k * kBins + t * kEach + i];
+        n[i] += s.counts[k * kBins + t * kEach + i];
+      }
+  }
+  u64 all_w = 0, all_n = 0, total, count;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    all_w += w[i];
+    all_n += n[i];
+  }
+  const u64 w0 = sum_before(all_w, sh.wave, total), n0 = sum_before(all_n, sh.wave, count);
+  // top-k alone, or with top-p: the interval of the k-th token, and all before it where the list
+  // holds them; top-p alone: the interval in which the sum reaches p
+  const bool by_k = m.k > 0 && static_cast<u64>(m.k) < count;
+  if (!by_k && m.p == 1.0f) {   // fewer than k have a weight: all of them are kept
+    if (t == 0) {
+      s.state->lo = s.state->hi = kBins;
+      s.state->mode = kListed;
+    }
+    return;
+  }
+  bool rest = false;
+  u64 want = 0;
+  if (!by_k) {
+    want = m.p < 1.0f ? part_of(m.p, total, rest) : total;
+    want += rest || want == 0;
+  }
+  u64 before_w = w0, before_n = n0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool here = by_k ? before_n < static_cast<u64>(m.k) && static_cast<u64>(m.k) <= before_n + n[i]
+                           : before_w < want && want <= before_w + w[i];
+    if (here) {
+      RowState x = *s.state;
+      x.total = total;
+      x.hi = t * kEach + i;
+      const bool all = by_k && before_n + n[i] <= kList;
+      x.lo = all ? 0 : x.hi;
+      x.weight_before = all ? 0 : before_w;
+      x.count_before = all ? 0 : static_cast<uint32_t>(before_n);
+      // top-p may cut anywhere above the k-th token
+      x.mode = all || (n[i] <= kList && !(by_k && m.p < 1.0f)) ? kListed : kSearch;
+      *s.state = x;
+    }
+    before_w += w[i];
+    before_n += n[i];
+  }
+}
+
+// ------------------------------------------------------------------------------------ pass three
+struct ListSpace {
+  u64 place[kList], weight[kList];
+  u64 bin_weights[256];
+  uint32_t bin_counts[256];
+};
+
+// The last kept place: in falling order, the first one at which the count (BY_COUNT) or the sum of
+// the weights reaches want >= 1; 0, before which all places lie, where it is not reached.  Digit by digit, of
+// what `each` calls its argument with: (place, weight) of every token.
+template <bool BY_COUNT, typename Each>
+__device__ u64 find_cut(u64 want, Shared& s, ListSpace& list, Each each) {
+  const int t = threadIdx.x;
+  u64 prefix = 0;
+  for (int shift = 48; shift >= 0; shift -= 8) {
+    static_assert(32 + kIndexBits <= 56, "seven digits");
+    __syncthreads();
+    list.bin_weights[t] = 0;
+    list.bin_counts[t] = 0;
+    if (t == 0) s.found[2] = 0;
+    __syncthreads();
+    each([&](u64 place, u64 w) {
+      if (w == 0 || (shift < 48 && (place >> (shift + 8)) != (prefix >> (shift + 8)))) return;
+      const int b = 255 - static_cast<int>(place >> shift & 255);
+      atomicAdd(&list.bin_counts[b], 1u);
+      if (!BY_COUNT) atomicAdd(&list.bin_weights[b], w);
+    });
+    __syncthreads();
+    const u64 here = BY_COUNT ? list.bin_counts[t] : list.bin_weights[t];
+    u64 total;
+    const u64 before = sum_before(here, s.wave, total);
+    if (before < want && want <= before + here) {
+      s.found[0] = 255 - t;
+      s.found[1] = want - before;
+      s.found[2] = list.bin_counts[t];
+    }
+    __syncthreads();
+    if (s.found[2] == 0) return 0;
+    prefix |= s.found[0] << shift;
+    want = s.found[1];
+    if (s.found[2] == 1) {   // one token: it is the one
+      const u64 above = prefix >> shift;
+      __syncthreads();
+      each([&](u64 place, u64 w) {
+        if (w > 0 && place >> shift == above) s.found[0] = place;
+      });
+      __syncthreads();
+      return s.found[0];
+    }
+  }
+  return prefix;
+}
+
+// The cut of a row's top-k and top-p, from the tokens that `each` goes through; what lies before
+// them counts and weighs as given.
+template <typename Each>
+__device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, Shared& s, ListSpace& list,
+                      Each each) {
+  u64 cut = 0;
+  if (m.k > 0) {
+    cut = find_cut<true>(m.k - count_before, s, list, each);
+    if (cut != 0 && m.p < 1.0f) {   // p of the first k
+      u64 sum = 0;
+      each([&](u64 place, u64 w) { sum += place >= cut ? w : 0; });
+      sum_before(sum, s.wave, total);
+      total += weight_before;
+    }
+  }
+  if (m.p < 1.0f) {
+    bool rest;
+    u64 want = part_of(m.p, total, rest);
+    want += rest || want == 0;
+    const u64 by_p = find_cut<false>(want - weight_before, s, list, each);
+    cut = by_p > cut ? by_p : cut;
+  }
+  return cut;
+}
+
+template <typename E>
+__global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ Shared sh;
+  __shared__ ListSpace list;
+  __shared__ u64 sums[kMostBlocks];
+  const int64_t row = blockIdx.y;
+  const RowSpace s(ws, row, g);
+  const RowState x = *s.state;
+  if (x.mode == kDone) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  sh.exps.fill();
+  __syncthreads();
+  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  const Row<E> r(a, row);
+  if (x.mode == kListed) {
+    const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
+    for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves) {
+      u64 sum = 0;
+      for (int it = 0; it < g.size / 512; ++it) {
+        const int j = r.first(g, b, it, lane);
+        float v[8];
+        r.load(j, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
+          if (bin < x.lo) {
+            const u64 w = m.weight(v[i]);
+            sum += w >= m.least_weight ? w : 0;
+          } else if (bin <= x.hi && m.weight(v[i]) > 0) {
+            const uint32_t at = atomicAdd(&s.state->listed, 1u);
+            if (at < kList) s.list[at] = place_of(v[i], j + i);
+          }
+        }
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) s.sums[b] = sum;
+    }
+  }
+  if (!last_of_row(&s.state->arrived[1], g.chunks, &sh.arrived)) return;
+  u64 cut;
+  if (x.mode == kListed) {
+    const int n = min(static_cast<int>(s.state->listed), kList);
+    for (int i = t; i < n; i += kSampleThreads) {
+      list.place[i] = s.list[i];
+      list.weight[i] = m.weight(logit_at(list.place[i]));
+    }
+    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = s.sums[b];
+    __syncthreads();
+    cut = x.lo == kBins ? 0 : cut_of(m, x.total, x.weight_before, x.count_before, sh, list, [&](auto f) {
+      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], list.weight[i]);
+    });
+    for (int i = t; i < n; i += kSampleThreads)
+      if (list.place[i] >= cut && list.weight[i] >= m.least_weight)
+        atomicAdd(&sums[(index_at(list.place[i]) + r.shift) / g.size], list.weight[i]);
+  } else {
+    // more tokens in the cut's interval than the list holds: over the whole row, one workgroup
+    const auto each = [&](auto f) {
+      for (int b = wave; b < g.blocks; b += kWaves)
+        for (int it = 0; it < g.size / 512; ++it) {
+          const int j = r.first(g, b, it, lane);
+          float v[8];
+          r.load(j, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f(place_of(v[i], j + i), m.weight(v[i]));
+        }
+    };
+    cut = cut_of(m, x.total, 0, 0, sh, list, each);
+    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = 0;
+    __syncthreads();
+    each([&](u64 place, u64 w) {
+      if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
+    });
+  }
+  __syncthreads();
+  draw<E>(a, row, g, m, sums, sh, [&](float l, int j) { return place_of(l, j) >= cut; });
+}
+
+// ------------------------------------------------------------------------------------------ host
+static SampleGrid sample_grid(int64_t n_rows, int64_t vocab) {
+  SampleGrid g;
+  g.size = vocab <= (1 << 20) ? 512 : vocab <= (1 << 21) ? 1024 : 2048;
+  g.blocks = static_cast<int>((vocab + 7 + g.size - 1) / g.size);   // wherever the row begins
+  // about four workgroups a CU, and a block at least for each of their waves
+  int64_t chunks = 4 * device_cus() / n_rows;
+  if (chunks > (g.blocks + kWaves - 1) / kWaves) chunks = (g.blocks + kWaves - 1) / kWaves;
+  if (chunks > kMostChunks) chunks = kMostChunks;
+  if (chunks < 1) chunks = 1;
+  g.blocks_a_chunk = static_cast<int>((g.blocks + chunks - 1) / chunks);
+  g.chunks = (g.blocks + g.blocks_a_chunk - 1) / g.blocks_a_chunk;
+  g.row_bytes = static_cast<int64_t>(align_up(
+      64 + 8 * (kMostChunks + kMostBlocks + 7 + kList) + 12 * static_cast<size_t>(g.chunks) * kBins + 4 * kMostChunks, 256));
+  return g;
+}
+
+size_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
+  const int64_t rows = n_rows < kRowsAtOnce ? n_rows : kRowsAtOnce;
+  return static_cast<size_t>(rows) * sample_grid(rows, vocab).row_bytes;
+}
+
+template <typename E>
+static void sample(const SampleView& v, char* ws, hipStream_t s) {
+  for (int64_t at = 0; at < v.n_rows; at += kRowsAtOnce) {
+    SampleView a = v;
+    a.n_rows = v.n_rows - at < kRowsAtOnce ? v.n_rows - at : kRowsAtOnce;
+    a.logits += at * a.stride * static_cast<int64_t>(sizeof(E));
+    a.u += at;
+    if (a.temperature) a.temperature += at;
+    if (a.top_k) a.top_k += at;
+    if (a.top_p) a.top_p += at;
+    if (a.min_p) a.min_p += at;
+    a.token += at;
+    if (a.logprob) a.logprob += at;
+    // the last rows keep the first ones' layout, which the workspace has been made for
+    const SampleGrid g = sample_grid(v.n_rows < kRowsAtOnce ? v.n_rows : kRowsAtOnce, v.vocab);
+    const dim3 grid(g.chunks, static_cast<unsigned>(a.n_rows)), threads(kSampleThreads);
+    sample_top_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+    if (!a.top_k && !a.top_p) {
+      sample_free_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+    } else {
+      sample_bins_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+      sample_cut_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+    }
+  }
+}
+
+hipError_t launch_sample(const SampleView& v, int32_t dtype, void* ws, hipStream_t s) {
+  if (dtype == STAPLE_BF16) sample<bf16_t>(v, static_cast<char*>(ws), s);
+  else sample<float>(v, static_cast<char*>(ws), s);
   return hipGetLastError();
 }
 
