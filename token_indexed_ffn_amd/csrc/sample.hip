@@ -25,7 +25,7 @@ constexpr int kWaves = kSampleThreads / 64;
 constexpr int kBins = 512;          // two a lane of a workgroup
 constexpr int kList = 2048;         // listed tokens
 constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
-constexpr int kMostChunks = 64;     // workgroups of a row
+constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all intervals' loads in flight at once
 constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
 constexpr int kScan = (kMostBlocks + kSampleThreads - 1) / kSampleThreads;
 
@@ -63,28 +63,28 @@ struct Exponents {
 
 // A row's weights.
 struct Weights {
-  float top;
-  double rate;      // log2(e) / T
+  double top;       // the largest logit, 1e300 for +inf
+  double rate;      // 32 log2(e) / T
   int unit_log2;
   const double* step;
   __device__ __forceinline__ u64 unit() const { return u64(1) << unit_log2; }
-  // 2^y with y = n / 32 + r: the step of n's last five bits, its other bits as the exponent, and
-  // five terms of exp(r ln 2) (|r| <= 1/64: off by 2^-48)
+  // 2^(y / 32) with y = n + r: the step of n's last five bits, its other bits as the exponent, and
+  // five terms of exp(r ln 2 / 32) (|r| <= 1/2: off by 2^-48)
   __device__ __forceinline__ u64 operator()(float l) const {
-    const double far = fmax((static_cast<double>(l) - static_cast<double>(top)) * rate, -1100.0);
+    const double far = fmax((fmin(static_cast<double>(l), 1e300) - top) * rate, -35200.0);
     const double magic = 6755399441055744.0;   // 3 2^51: a sum with it is rounded to a whole number
-    const double big = far * 32.0 + magic;
+    const double big = far + magic;
     const int n = static_cast<int>(__double_as_longlong(big));
-    const double r = (far - (big - magic) * 0.03125) * 0.693147180559945309417;
-    double p = 1.0 / 120.0;
-    p = p * r + 1.0 / 24.0;
-    p = p * r + 1.0 / 6.0;
-    p = p * r + 0.5;
-    p = p * r + 1.0;
-    p = p * r + 1.0;
+    const double r = far - (big - magic);
+    constexpr double c = 0.693147180559945309417 / 32;
+    double p = c * c * c * c * c / 120;
+    p = fma(p, r, c * c * c * c / 24);
+    p = fma(p, r, c * c * c / 6);
+    p = fma(p, r, c * c / 2);
+    p = fma(p, r, c);
+    p = fma(p, r, 1.0);
     const double w = ldexp(p * step[n & 31], (n >> 5) + unit_log2);
-    const u64 whole = static_cast<u64>(__double_as_longlong(w + 4503599627370496.0)) & ((u64(1) << 52) - 1);
-    return l == top ? unit() : whole;
+    return static_cast<u64>(__double_as_longlong(w + 4503599627370496.0)) & ((u64(1) << 52) - 1);
   }
 };
 
@@ -126,7 +126,7 @@ enum { kDone, kListed, kSearch };   // the token is known; lo and hi are listed;
 struct RowSpace {
   RowState* state;
   u64* best;        // [chunks]: place of the largest logit
-  float* least;     // [chunks]: the smallest finite logit
+  float* least;     // [chunks]: the smallest logit
   u64* sums;        // [blocks]: kept weights, those of listed tokens aside
   u64* list;        // [kList]: places
   u64* weights;     // [chunks][kBins]
@@ -168,6 +168,30 @@ struct Row {
   }
 };
 
+// A wave's part of chunk c, eight elements a lane at a time and U of these loads in flight: f(block, j, v),
+// and done(block) after a block's last one.
+template <int U, typename E, typename F, typename Done>
+__device__ __forceinline__ void walk(const Row<E>& r, const SampleGrid& g, int c, F f, Done done) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int begin = c * g.blocks_a_chunk + wave, end = min((c + 1) * g.blocks_a_chunk, g.blocks);
+  const int log_its = 31 - __clz(g.size >> 9);
+  const int its = 1 << log_its;
+  const int steps = begin < end ? (end - begin + kWaves - 1) / kWaves * its : 0;
+  for (int s = 0; s < steps; s += U) {
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < steps) r.load(r.first(g, begin + ((s + u) >> log_its) * kWaves, (s + u) & (its - 1), lane), v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < steps) {
+        const int block = begin + ((s + u) >> log_its) * kWaves, it = (s + u) & (its - 1);
+        f(r.first(g, block, it, lane), v[u]);
+        if (it == its - 1) done(block);
+      }
+  }
+}
+
 // A row's limits and weights, from its largest logit.
 struct Limits {
   float top, temperature;
@@ -206,15 +230,19 @@ __device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& 
   m.temperature = a.temperature ? a.temperature[row] : 1.0f;
   m.greedy = !(m.temperature > 0.0f);
   const int bits = 62 - (32 - __clz(a.vocab));
-  m.weight = Weights{m.top, 1.44269504088896340736 / static_cast<double>(m.temperature), bits < 50 ? bits : 50, step};
+  m.weight = Weights{fmin(static_cast<double>(m.top), 1e300), 46.1662413084468290355 / static_cast<double>(m.temperature),
+                     bits < 50 ? bits : 50, step};
   const int k = a.top_k ? a.top_k[row] : 0;
   m.k = k > 0 && k < a.vocab ? k : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f;
   m.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
   const float low = a.min_p ? a.min_p[row] : 0.0f;
   m.least_weight = low > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(low, 1.0f)) * m.weight.unit())) : 0;
-  // weights past this distance are rounded to zero
-  const float reach = fminf(m.temperature * (0.6932f * (m.weight.unit_log2 + 2)), m.top - least);
+  // Weights past this distance are rounded to zero.  With top-p alone also: all weights below
+  // (1 - p) / vocab, of the largest one, make less than 1 - p of the whole, so that the cut lies above them.
+  float reach = 0.6932f * (m.weight.unit_log2 + 2);
+  if (m.k == 0 && m.p < 1.0f) reach = fminf(reach, logf(static_cast<float>(a.vocab) / (1.0f - m.p)) + 0.01f);
+  reach = fminf(m.temperature * reach, m.top - least);
   m.bin_rate = reach > 0.0f ? kBins / reach : 0.0f;
   return m;
 }
@@ -248,19 +276,28 @@ __device__ __forceinline__ u64 wave_sum(u64 v) {
   return v;
 }
 
-// Whether this workgroup is the last of its row's to get here; what the others wrote is then seen.
+// What workgroups of a row tell each other in one launch goes past the caches of an XCD: written and
+// read with relaxed atomic accesses of the device's scope.  (Fences of that scope write back and drop a
+// whole L2: with one a workgroup, 64 rows took 113 us in place of XX.)
+template <typename T>
+__device__ __forceinline__ void tell(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T told(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Whether this workgroup is the last of its row's to get here: what the others told is there then.
 __device__ __forceinline__ bool last_of_row(uint32_t* arrived, int chunks, uint32_t* shared) {
-  if (chunks == 1) {
-    __syncthreads();
-    return true;
-  }
-  __threadfence();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  wait_vmcnt<0>();   // this wave's stores have reached the device's memory
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __syncthreads();
-  if (threadIdx.x == 0) *shared = atomicAdd(arrived, 1u);
+  if (chunks == 1) return true;
+  if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  const bool last = *shared == static_cast<uint32_t>(chunks - 1);
-  if (last) __threadfence();
-  return last;
+  return *shared == static_cast<uint32_t>(chunks - 1);
 }
 
 struct Shared {
@@ -271,17 +308,16 @@ struct Shared {
 };
 
 // ------------------------------------------------------------------------------------- the draw
-// The token at which the sum of the kept weights passes u times their total.  sums: of the
-// blocks; kept(l, j): whether token j, with its weight not below min-p, is kept.
-template <typename E, typename Kept>
-__device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, const u64* sums,
-                     Shared& s, Kept kept) {
+// The token at which the sum of the kept weights passes u times their total.  sum(b): of block
+// b; kept(l, j): whether token j, with its weight not below min-p, is kept.
+template <typename E, typename Sum, typename Kept>
+__device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, Shared& s, Sum sum, Kept kept) {
   const Row<E> r(a, row);
   u64 mine[kScan], all = 0;
 #pragma unroll
   for (int i = 0; i < kScan; ++i) {
     const int b = threadIdx.x * kScan + i;
-    mine[i] = b < g.blocks ? sums[b] : 0;
+    mine[i] = b < g.blocks ? sum(b) : 0;
     all += mine[i];
   }
   u64 total;
@@ -341,41 +377,44 @@ __global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a
   const Row<E> r(a, row);
   const RowSpace s(ws, row, g);
   if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = s.state->listed = 0;
-  u64 best = 0;
-  float least = __builtin_inff();
-  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
-  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves)
-    for (int it = 0; it < g.size / 512; ++it) {
-      const int j = r.first(g, b, it, lane);
-      float v[8];
-      r.load(j, v);
-      float top = v[0];
+  // a lane's largest logit and its group of eight, later the group's first element that has it
+  float best = -__builtin_inff(), least = __builtin_inff();
+  int at = 0;
+  walk<4>(r, g, c, [&](int j, const float (&v)[8]) {
+    float top = v[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, v[i]);
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, v[i]);
+    if (j >= 0 && j + 8 <= r.n) {   // not of a group that the row's ends fill up
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (v[i] != -__builtin_inff()) least = fminf(least, v[i]);
-        const u64 x = place_of(v[i], j + i);
-        if (v[i] == top && j + i >= 0 && j + i < r.n && x > best) best = x;
-      }
+      for (int i = 0; i < 8; ++i) least = fminf(least, v[i]);
     }
+    if (top > best) {
+      best = top;
+      at = j;
+    }
+  }, [](int) {});
+  int first = 0;   // a row of -inf has no token: any will do
+  if (best != -__builtin_inff())
+    for (int i = 7; i >= 0; --i)
+      if (at + i >= 0 && at + i < r.n && load1(r.p + at + i) == best) first = at + i;
+  u64 place = place_of(best, first);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
-    const u64 x = __shfl_xor(best, o, 64);
-    best = x > best ? x : best;
+    const u64 x = __shfl_xor(place, o, 64);
+    place = x > place ? x : place;
     least = fminf(least, __shfl_xor(least, o, 64));
   }
   if (lane == 0) {
-    best_of[wave] = best;
+    best_of[wave] = place;
     least_of[wave] = least;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < kWaves; ++i) {
-      best = best_of[i] > best ? best_of[i] : best;
+      place = best_of[i] > place ? best_of[i] : place;
       least = fminf(least, least_of[i]);
     }
-    s.best[c] = best;
+    s.best[c] = place;
     s.least[c] = least;
   }
 }
@@ -392,34 +431,26 @@ __device__ __forceinline__ bool plain_row(const SampleView& a, int64_t row, cons
   return true;
 }
 
-struct KeepAll {
-  __device__ __forceinline__ bool operator()(float, int) const { return true; }
-};
-
 // A row without top-k and top-p: the blocks' sums, and the draw.
 template <typename E>
 __device__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, const RowSpace& s,
                          Shared& sh) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
   const Row<E> r(a, row);
-  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
-  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves) {
-    u64 sum = 0;
-    for (int it = 0; it < g.size / 512; ++it) {
-      float v[8];
-      r.load(r.first(g, b, it, lane), v);
+  u64 sum = 0;
+  walk<2>(r, g, blockIdx.x, [&](int, const float (&v)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const u64 w = m.weight(v[i]);
-        sum += w >= m.least_weight ? w : 0;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const u64 w = m.weight(v[i]);
+      sum += w >= m.least_weight ? w : 0;
     }
+  }, [&](int block) {
     sum = wave_sum(sum);
-    if (lane == 0) s.sums[b] = sum;
-  }
+    if ((threadIdx.x & 63) == 0) tell(&s.sums[block], sum);
+    sum = 0;
+  });
   if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
   if (threadIdx.x == 0) s.state->mode = kDone;
-  draw<E>(a, row, g, m, s.sums, sh, KeepAll());
+  draw<E>(a, row, g, m, sh, [&](int b) { return told(&s.sums[b]); }, [](float, int) { return true; });
 }
 
 template <typename E>
@@ -442,7 +473,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
   __shared__ uint32_t counts[kBins];
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  const int c = blockIdx.x, t = threadIdx.x;
   sh.exps.fill();
   for (int i = t; i < kBins; i += kSampleThreads) {
     weights[i] = 0;
@@ -456,25 +487,31 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
     return;
   }
   const Row<E> r(a, row);
-  const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
-  for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves)
-    for (int it = 0; it < g.size / 512; ++it) {
-      float v[8];
-      r.load(r.first(g, b, it, lane), v);
+  if (m.k > 0) {
+    walk<2>(r, g, c, [&](int, const float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (v[i] != -__builtin_inff()) atomicAdd(&counts[m.bin(v[i])], 1u);
+    }, [](int) {});
+  } else {
+    u64 rest = 0;   // of the last interval, which half of the tokens fall into and more
+    walk<2>(r, g, c, [&](int, const float (&v)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const u64 w = m.weight(v[i]);
-        if (w == 0) continue;   // never drawn, and nothing in any sum
-        const int bin = m.bin(v[i]);
-        atomicAdd(&counts[bin], 1u);
-        atomicAdd(&weights[bin], w);
+        const int bin = v[i] == -__builtin_inff() ? kBins - 1 : m.bin(v[i]);
+        if (bin < kBins - 1) atomicAdd(&weights[bin], w);
+        else rest += w;
       }
-    }
+    }, [](int) {});
+    rest = wave_sum(rest);
+    if ((t & 63) == 0) atomicAdd(&weights[kBins - 1], rest);
+  }
   __syncthreads();
   if (g.chunks > 1) {
     for (int i = t; i < kBins; i += kSampleThreads) {
-      s.weights[c * kBins + i] = weights[i];
-      s.counts[c * kBins + i] = counts[i];
+      if (m.k == 0) tell(&s.weights[c * kBins + i], weights[i]);
+      else tell(&s.counts[c * kBins + i], counts[i]);
     }
   }
   if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
@@ -493,13 +530,14 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
       w[i] = 0;
       n[i] = 0;
     }
-#pragma unroll 8
-    for (int k = 0; k < g.chunks; ++k)
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        w[i] += s.weights[k * kBins + t * kEach + i];
-        n[i] += s.counts[k * kBins + t * kEach + i];
-      }
+    for (int k = 0; k < kMostChunks; ++k)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (k < g.chunks) {
+          if (m.k == 0) w[i] += told(&s.weights[k * kBins + t * kEach + i]);
+          else n[i] += told(&s.counts[k * kBins + t * kEach + i]);
+        }
   }
   u64 all_w = 0, all_n = 0, total, count;
 #pragma unroll
@@ -508,22 +546,19 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
     all_n += n[i];
   }
   const u64 w0 = sum_before(all_w, sh.wave, total), n0 = sum_before(all_n, sh.wave, count);
-  // top-k alone, or with top-p: the interval of the k-th token, and all before it where the list
-  // holds them; top-p alone: the interval in which the sum reaches p
-  const bool by_k = m.k > 0 && static_cast<u64>(m.k) < count;
-  if (!by_k && m.p == 1.0f) {   // fewer than k have a weight: all of them are kept
+  // with top-k the interval of the k-th token, and all before it where the list holds them; top-p
+  // alone: the interval in which the sum reaches p
+  const bool by_k = m.k > 0;
+  if (by_k && static_cast<u64>(m.k) >= count) {   // no more than k tokens: top-k limits nothing
     if (t == 0) {
       s.state->lo = s.state->hi = kBins;
-      s.state->mode = kListed;
+      s.state->mode = m.p < 1.0f ? kSearch : kListed;
     }
     return;
   }
   bool rest = false;
-  u64 want = 0;
-  if (!by_k) {
-    want = m.p < 1.0f ? part_of(m.p, total, rest) : total;
-    want += rest || want == 0;
-  }
+  u64 want = by_k ? 0 : part_of(m.p, total, rest);
+  want += rest || want == 0;
   u64 before_w = w0, before_n = n0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -537,7 +572,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
       x.lo = all ? 0 : x.hi;
       x.weight_before = all ? 0 : before_w;
       x.count_before = all ? 0 : static_cast<uint32_t>(before_n);
-      // top-p may cut anywhere above the k-th token
+      // top-p may cut anywhere above the k-th token; how many tokens a weight's interval holds is
+      // seen when they are listed
       x.mode = all || (n[i] <= kList && !(by_k && m.p < 1.0f)) ? kListed : kSearch;
       *s.state = x;
     }
@@ -548,53 +584,55 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
 
 // ------------------------------------------------------------------------------------ pass three
 struct ListSpace {
-  u64 place[kList], weight[kList];
+  u64 place[kList];
   u64 bin_weights[256];
   uint32_t bin_counts[256];
 };
 
-// The last kept place: in falling order, the first one at which the count (BY_COUNT) or the sum of
-// the weights reaches want >= 1; 0, before which all places lie, where it is not reached.  Digit by digit, of
-// what `each` calls its argument with: (place, weight) of every token.
+// The lowest place that is kept: in falling order, the first one at which the count (BY_COUNT) or
+// the sum of the weights reaches want >= 1, and 0 where none does.  Digit by digit, of what `each` calls its argument with: (place, weight) of every
+// token.  The places have the bits of `base` but for the last `bits`.
 template <bool BY_COUNT, typename Each>
-__device__ u64 find_cut(u64 want, Shared& s, ListSpace& list, Each each) {
+__device__ u64 find_cut(u64 want, u64 base, int bits, Shared& s, ListSpace& list, Each each) {
   const int t = threadIdx.x;
-  u64 prefix = 0;
-  for (int shift = 48; shift >= 0; shift -= 8) {
-    static_assert(32 + kIndexBits <= 56, "seven digits");
-    __syncthreads();
-    list.bin_weights[t] = 0;
-    list.bin_counts[t] = 0;
-    if (t == 0) s.found[2] = 0;
-    __syncthreads();
+  u64 prefix = base >> bits << bits;
+  __syncthreads();
+  list.bin_weights[t] = 0;
+  list.bin_counts[t] = 0;
+  if (t == 0) s.found[2] = 0;
+  __syncthreads();
+  for (int known = bits; known > 0;) {
+    const int shift = known > 8 ? known - 8 : 0;
     each([&](u64 place, u64 w) {
-      if (w == 0 || (shift < 48 && (place >> (shift + 8)) != (prefix >> (shift + 8)))) return;
+      if (w == 0 || place >> known != prefix >> known) return;
       const int b = 255 - static_cast<int>(place >> shift & 255);
       atomicAdd(&list.bin_counts[b], 1u);
       if (!BY_COUNT) atomicAdd(&list.bin_weights[b], w);
     });
     __syncthreads();
-    const u64 here = BY_COUNT ? list.bin_counts[t] : list.bin_weights[t];
+    const uint32_t count = list.bin_counts[t];
+    const u64 here = BY_COUNT ? count : list.bin_weights[t];
+    list.bin_counts[t] = 0;
+    list.bin_weights[t] = 0;
     u64 total;
     const u64 before = sum_before(here, s.wave, total);
     if (before < want && want <= before + here) {
       s.found[0] = 255 - t;
       s.found[1] = want - before;
-      s.found[2] = list.bin_counts[t];
+      s.found[2] = count;
     }
     __syncthreads();
     if (s.found[2] == 0) return 0;
     prefix |= s.found[0] << shift;
     want = s.found[1];
-    if (s.found[2] == 1) {   // one token: it is the one
-      const u64 above = prefix >> shift;
-      __syncthreads();
-      each([&](u64 place, u64 w) {
-        if (w > 0 && place >> shift == above) s.found[0] = place;
-      });
-      __syncthreads();
-      return s.found[0];
-    }
+    known = shift;
+    if (s.found[2] > 1) continue;
+    // one token is left.  Its own place is told from those that `each` does not go through
+    each([&](u64 place, u64 w) {
+      if (w > 0 && place >> known == prefix >> known) s.found[3] = place;
+    });
+    __syncthreads();
+    return s.found[3];
   }
   return prefix;
 }
@@ -602,12 +640,12 @@ __device__ u64 find_cut(u64 want, Shared& s, ListSpace& list, Each each) {
 // The cut of a row's top-k and top-p, from the tokens that `each` goes through; what lies before
 // them counts and weighs as given.
 template <typename Each>
-__device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, Shared& s, ListSpace& list,
-                      Each each) {
+__device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, u64 base, int bits, Shared& s,
+                      ListSpace& list, Each each) {
   u64 cut = 0;
   if (m.k > 0) {
-    cut = find_cut<true>(m.k - count_before, s, list, each);
-    if (cut != 0 && m.p < 1.0f) {   // p of the first k
+    cut = find_cut<true>(m.k - count_before, base, bits, s, list, each);
+    if (m.p < 1.0f) {   // p of the first k
       u64 sum = 0;
       each([&](u64 place, u64 w) { sum += place >= cut ? w : 0; });
       sum_before(sum, s.wave, total);
@@ -618,7 +656,7 @@ __device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_b
     bool rest;
     u64 want = part_of(m.p, total, rest);
     want += rest || want == 0;
-    const u64 by_p = find_cut<false>(want - weight_before, s, list, each);
+    const u64 by_p = find_cut<false>(want - weight_before, base, bits, s, list, each);
     cut = by_p > cut ? by_p : cut;
   }
   return cut;
@@ -639,45 +677,70 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
   const Limits m = limits_of(a, row, g, s, sh.exps.step);
   const Row<E> r(a, row);
   if (x.mode == kListed) {
-    const int end = min((c + 1) * g.blocks_a_chunk, g.blocks);
-    for (int b = c * g.blocks_a_chunk + wave; b < end; b += kWaves) {
-      u64 sum = 0;
-      for (int it = 0; it < g.size / 512; ++it) {
-        const int j = r.first(g, b, it, lane);
-        float v[8];
-        r.load(j, v);
+    u64 sum = 0;
+    walk<2>(r, g, c, [&](int j, const float (&v)[8]) {
+      unsigned listed = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
-          if (bin < x.lo) {
-            const u64 w = m.weight(v[i]);
-            sum += w >= m.least_weight ? w : 0;
-          } else if (bin <= x.hi && m.weight(v[i]) > 0) {
-            const uint32_t at = atomicAdd(&s.state->listed, 1u);
-            if (at < kList) s.list[at] = place_of(v[i], j + i);
-          }
+      for (int i = 0; i < 8; ++i) {
+        const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
+        if (bin < x.lo) {
+          const u64 w = m.weight(v[i]);
+          sum += w >= m.least_weight ? w : 0;
+        } else if (bin <= x.hi && bin < kBins) {
+          listed |= 1u << i;
         }
       }
+      if (__ballot(listed != 0) == 0) return;
+      const int mine = __popc(listed);
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(before, o, 64);
+        if (lane >= o) before += y;
+      }
+      uint32_t at = 0;
+      if (lane == 63) at = __hip_atomic_fetch_add(&s.state->listed, static_cast<uint32_t>(before), __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT);
+      at = __shfl(at, 63, 64) + before - mine;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (listed >> i & 1) {
+          if (at < kList) tell(&s.list[at], place_of(v[i], j + i));
+          ++at;
+        }
+    }, [&](int block) {
       sum = wave_sum(sum);
-      if (lane == 0) s.sums[b] = sum;
-    }
+      if (lane == 0) tell(&s.sums[block], sum);
+      sum = 0;
+    });
   }
   if (!last_of_row(&s.state->arrived[1], g.chunks, &sh.arrived)) return;
-  u64 cut;
-  if (x.mode == kListed) {
-    const int n = min(static_cast<int>(s.state->listed), kList);
+  const uint32_t listed = told(&s.state->listed);
+  u64 cut = 0;
+  if (x.mode == kListed && listed <= kList) {
+    const int n = static_cast<int>(listed);
+    u64 base = 0, other = 0;
+    if (n > 0) base = told(&s.list[0]);
     for (int i = t; i < n; i += kSampleThreads) {
-      list.place[i] = s.list[i];
-      list.weight[i] = m.weight(logit_at(list.place[i]));
+      const u64 place = told(&s.list[i]);
+      list.place[i] = place;
+      other |= place ^ base;
     }
-    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = s.sums[b];
+    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = told(&s.sums[b]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
+    if (lane == 0) sh.found[wave] = other;
     __syncthreads();
-    cut = x.lo == kBins ? 0 : cut_of(m, x.total, x.weight_before, x.count_before, sh, list, [&](auto f) {
-      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], list.weight[i]);
+    other = sh.found[0] | sh.found[1] | sh.found[2] | sh.found[3];
+    const auto each = [&](auto f) {
+      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], m.weight(logit_at(list.place[i])));
+    };
+    if (x.lo < kBins)
+      cut = cut_of(m, x.total, x.weight_before, x.count_before, base, 64 - __clzll(other), sh, list, each);
+    __syncthreads();
+    each([&](u64 place, u64 w) {
+      if (place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
     });
-    for (int i = t; i < n; i += kSampleThreads)
-      if (list.place[i] >= cut && list.weight[i] >= m.least_weight)
-        atomicAdd(&sums[(index_at(list.place[i]) + r.shift) / g.size], list.weight[i]);
   } else {
     // more tokens in the cut's interval than the list holds: over the whole row, one workgroup
     const auto each = [&](auto f) {
@@ -690,7 +753,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
           for (int i = 0; i < 8; ++i) f(place_of(v[i], j + i), m.weight(v[i]));
         }
     };
-    cut = cut_of(m, x.total, 0, 0, sh, list, each);
+    cut = cut_of(m, x.total, 0, 0, 0, 32 + kIndexBits, sh, list, each);
     for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = 0;
     __syncthreads();
     each([&](u64 place, u64 w) {
@@ -698,7 +761,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
     });
   }
   __syncthreads();
-  draw<E>(a, row, g, m, sums, sh, [&](float l, int j) { return place_of(l, j) >= cut; });
+  draw<E>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [&](float l, int j) { return place_of(l, j) >= cut; });
 }
 
 // ------------------------------------------------------------------------------------------ host
