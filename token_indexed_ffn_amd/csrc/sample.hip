@@ -27,7 +27,6 @@ constexpr int kList = 2048;         // listed tokens
 constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
 constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all intervals' loads in flight at once
 constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
-constexpr int kScan = (kMostBlocks + kSampleThreads - 1) / kSampleThreads;
 
 // --------------------------------------------------------------------------- logits and weights
 __device__ __forceinline__ float no_nan(float l) { return l == l ? l : -__builtin_inff(); }
@@ -54,10 +53,20 @@ __device__ __forceinline__ int index_at(u64 place) {
 }
 
 // 2^(i / 32), i < 32.
+__device__ const double kSteps[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002,
+};
 struct Exponents {
   double step[32];
   __device__ __forceinline__ void fill() {
-    if (threadIdx.x < 32) step[threadIdx.x] = exp2(threadIdx.x * 0.03125);
+    if (threadIdx.x < 32) step[threadIdx.x] = kSteps[threadIdx.x];
   }
 };
 
@@ -151,45 +160,116 @@ struct Row {
   __device__ __forceinline__ Row(const SampleView& a, int64_t row)
       : p(reinterpret_cast<const E*>(a.logits) + row * a.stride), n(a.vocab),
         shift(static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(E))) {}
-  // Index of element 0 of lane l of the it-th 512 elements of a block.
-  __device__ __forceinline__ int first(const SampleGrid& g, int block, int it, int lane) const {
-    return block * g.size + it * 512 + lane * 8 - shift;
+  __device__ __forceinline__ float at(int j) const { return no_nan(load1(p + j)); }
+  // The elements outside full groups of eight are held one a lane (lanes 0 to 7 the row's first
+  // ones, 32 to 39 its last ones), in the blocks that they belong to; -1: none.
+  __device__ __forceinline__ bool has_edge(const SampleGrid& g, int block) const {
+    return (block == 0 && shift > 0) || (block == (n - 1 + shift) / g.size && (n + shift & 7) != 0);
   }
-  // Eight elements from j; -inf for those outside the row and for NaN.
-  __device__ __forceinline__ void load(int j, float (&v)[8]) const {
-    if (j >= 0 && j + 8 <= n) {
-      load8(p + j, v);
+  __device__ __forceinline__ int edge(const SampleGrid& g, int block, int lane) const {
+    const int head = shift > 0 ? min(n, 8 - shift) : 0, tail = n > head ? n + shift & 7 : 0;
+    if (block == 0 && lane < head) return lane;
+    if (block == (n - 1 + shift) / g.size && lane >= 32 && lane - 32 < tail) return n - tail + lane - 32;
+    return -1;
+  }
+};
+
+// Eight elements as they lie in memory.
+template <typename E> struct Raw;
+template <> struct Raw<bf16_t> {
+  u32x4_t a;
+  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = no_nan(v[i]);
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = no_nan(__uint_as_float(a[i] << 16));
+      v[2 * i + 1] = no_nan(__uint_as_float(a[i] & 0xffff0000u));
+    }
+  }
+};
+template <> struct Raw<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4_t*>(p);
+    b = *reinterpret_cast<const f32x4_t*>(p + 4);
+  }
+  __device__ __forceinline__ void clear() {
+    const float x = -__builtin_inff();
+    a = b = f32x4_t{x, x, x, x};
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = j + i >= 0 && j + i < n ? no_nan(load1(p + j + i)) : -__builtin_inff();
+    for (int i = 0; i < 4; ++i) {
+      v[i] = no_nan(a[i]);
+      v[i + 4] = no_nan(b[i]);
     }
   }
 };
 
-// A wave's part of chunk c, eight elements a lane at a time and U of these loads in flight: f(block, j, v),
-// and done(block) after a block's last one.
-template <int U, typename E, typename F, typename Done>
-__device__ __forceinline__ void walk(const Row<E>& r, const SampleGrid& g, int c, F f, Done done) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int begin = c * g.blocks_a_chunk + wave, end = min((c + 1) * g.blocks_a_chunk, g.blocks);
-  const int log_its = 31 - __clz(g.size >> 9);
-  const int its = 1 << log_its;
-  const int steps = begin < end ? (end - begin + kWaves - 1) / kWaves * its : 0;
-  for (int s = 0; s < steps; s += U) {
-    float v[U][8];
+// Blocks begin, begin + stride, ... of a row before `end`, eight elements a lane at a time, with the
+// next kAhead loads in flight, from the walk's making on.  One copy of the body, and loops that are not
+// unrolled, here and below: these kernels run for a few microseconds, and 60 KB of code took longer to
+// fetch than to run.
+constexpr int kAhead = 3;
+template <typename E>
+struct Walk {
+  const Row<E>& r;
+  const SampleGrid& g;
+  int lane, begin, stride, steps, log_its;
+  Raw<E> raw[kAhead];
+  __device__ __forceinline__ Walk(const Row<E>& row, const SampleGrid& grid, int first_block, int end, int each)
+      : r(row), g(grid), lane(threadIdx.x & 63), begin(first_block), stride(each) {
+    log_its = 31 - __clz(g.size >> 9);
+    steps = begin < end ? (end - begin + stride - 1) / stride << log_its : 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < steps) r.load(r.first(g, begin + ((s + u) >> log_its) * kWaves, (s + u) & (its - 1), lane), v[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < steps) {
-        const int block = begin + ((s + u) >> log_its) * kWaves, it = (s + u) & (its - 1);
-        f(r.first(g, block, it, lane), v[u]);
-        if (it == its - 1) done(block);
-      }
+    for (int i = 0; i < kAhead; ++i) load(i, raw[i]);
   }
+  __device__ __forceinline__ int block(int s) const { return begin + (s >> log_its) * stride; }
+  __device__ __forceinline__ int first(int s) const {
+    return block(s) * g.size + (s & ((1 << log_its) - 1)) * 512 + lane * 8 - r.shift;
+  }
+  __device__ __forceinline__ void load(int s, Raw<E>& to) const {
+    const int j = first(s);
+    if (s < steps && j >= 0 && j + 8 <= r.n) to.load(r.p + j);
+    else to.clear();
+  }
+  // f(j, v, full): elements from j on, -inf for those that there are not; full: there are all eight.
+  // done(block): after a block's last ones.
+  template <typename F, typename Done>
+  __device__ __forceinline__ void run(F f, Done done) {
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+      float v[8];
+      raw[0].get(v);
+      int j = first(s);
+      bool full = j >= 0 && j + 8 <= r.n;
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) raw[i] = raw[i + 1];
+      load(s + kAhead, raw[kAhead - 1]);
+      const bool last = (s + 1 & ((1 << log_its) - 1)) == 0;
+      bool edge = last && r.has_edge(g, block(s));
+#pragma unroll 1
+      for (;;) {
+        f(j, v, full);
+        if (!edge) break;
+        edge = false;
+        full = false;
+        j = r.edge(g, block(s), lane);
+        v[0] = j >= 0 ? r.at(j) : -__builtin_inff();
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v[i] = -__builtin_inff();
+      }
+      if (last) done(block(s));
+    }
+  }
+};
+
+// A wave's part of its workgroup's chunk.
+template <typename E>
+__device__ __forceinline__ Walk<E> walk_of(const Row<E>& r, const SampleGrid& g) {
+  const int c = blockIdx.x;
+  return Walk<E>(r, g, c * g.blocks_a_chunk + (threadIdx.x >> 6), min((c + 1) * g.blocks_a_chunk, g.blocks), kWaves);
 }
 
 // A row's limits and weights, from its largest logit.
@@ -278,7 +358,8 @@ __device__ __forceinline__ u64 wave_sum(u64 v) {
 
 // What workgroups of a row tell each other in one launch goes past the caches of an XCD: written and
 // read with relaxed atomic accesses of the device's scope.  (Fences of that scope write back and drop a
-// whole L2: with one a workgroup, 64 rows took 113 us in place of XX.)
+// whole L2: a fence in every workgroup made each of the two passes over 64 rows take
+// 110 us in place of 25.)
 template <typename T>
 __device__ __forceinline__ void tell(T* p, T v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -304,7 +385,7 @@ struct Shared {
   Exponents exps;
   u64 wave[kWaves];
   u64 found[4];
-  uint32_t arrived;
+  uint32_t arrived, listed, place_at;
 };
 
 // ------------------------------------------------------------------------------------- the draw
@@ -313,57 +394,49 @@ struct Shared {
 template <typename E, typename Sum, typename Kept>
 __device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, Shared& s, Sum sum, Kept kept) {
   const Row<E> r(a, row);
-  u64 mine[kScan], all = 0;
-#pragma unroll
-  for (int i = 0; i < kScan; ++i) {
-    const int b = threadIdx.x * kScan + i;
-    mine[i] = b < g.blocks ? sum(b) : 0;
-    all += mine[i];
-  }
+  const int each = (g.blocks + kSampleThreads - 1) / kSampleThreads;   // consecutive blocks a lane
+  const int b0 = threadIdx.x * each, b1 = min(b0 + each, g.blocks);
+  u64 all = 0;
+  for (int b = b0; b < b1; ++b) all += sum(b);
   u64 total;
   u64 before = sum_before(all, s.wave, total);
   const float u = a.u[row];
   bool rest;
   const u64 target = !(u > 0.0f) ? 0 : u < 1.0f ? part_of(u, total, rest) : total - 1;
-#pragma unroll
-  for (int i = 0; i < kScan; ++i) {
-    if (before <= target && target < before + mine[i]) {
-      s.found[0] = threadIdx.x * kScan + i;
-      s.found[1] = before;
+  if (before <= target && target < before + all)
+    for (int b = b0; b < b1; ++b) {
+      const u64 here = sum(b);
+      if (target < before + here) {
+        s.found[0] = b;
+        s.found[1] = before;
+        break;
+      }
+      before += here;
     }
-    before += mine[i];
-  }
   __syncthreads();
   const int block = static_cast<int>(s.found[0]);
   before = s.found[1];
-  const int each = g.size / kSampleThreads;   // 2, 4 or 8 elements a lane
-  const int j0 = block * g.size - r.shift + threadIdx.x * each;
-  u64 w[8];
-  float l[8];
-  all = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 0;
-    const int j = j0 + i;
-    if (i < each && j >= 0 && j < r.n) {
-      l[i] = no_nan(load1(r.p + j));
-      const u64 x = m.weight(l[i]);
-      if (x >= m.least_weight && kept(l[i], j)) w[i] = x;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < g.size; i += kSampleThreads) {
+    const int j = block * g.size - r.shift + i;
+    u64 w = 0;
+    float l = 0.0f;
+    if (j >= 0 && j < r.n) {
+      l = r.at(j);
+      w = m.weight(l);
+      if (w < m.least_weight || !kept(l, j)) w = 0;
     }
-    all += w[i];
-  }
-  u64 of_block;
-  before += sum_before(all, s.wave, of_block);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (w[i] > 0 && before <= target && target < before + w[i]) {
-      a.token[row] = j0 + i;
+    u64 here;
+    const u64 mine_before = before + sum_before(w, s.wave, here);
+    if (w > 0 && mine_before <= target && target < mine_before + w) {
+      a.token[row] = j;
       if (a.logprob) {
-        const double d = l[i] == m.top ? 0.0 : (static_cast<double>(l[i]) - m.top) / static_cast<double>(m.temperature);
+        const double d = l == m.top ? 0.0 : (static_cast<double>(l) - m.top) / static_cast<double>(m.temperature);
         a.logprob[row] = static_cast<float>(d - log(static_cast<double>(total) / static_cast<double>(m.weight.unit())));
       }
     }
-    before += w[i];
+    before += here;
+    if (before > target) break;
   }
 }
 
@@ -377,18 +450,20 @@ __global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a
   const Row<E> r(a, row);
   const RowSpace s(ws, row, g);
   if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = s.state->listed = 0;
-  // a lane's largest logit and its group of eight, later the group's first element that has it
+  // a lane's largest logit and its group, later the group's first element that has it
   float best = -__builtin_inff(), least = __builtin_inff();
   int at = 0;
-  walk<4>(r, g, c, [&](int j, const float (&v)[8]) {
-    float top = v[0];
+  auto walk = walk_of(r, g);
+  walk.run([&](int j, const float (&v)[8], bool full) {
+    float top = v[0], low = v[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, v[i]);
-    if (j >= 0 && j + 8 <= r.n) {   // not of a group that the row's ends fill up
-#pragma unroll
-      for (int i = 0; i < 8; ++i) least = fminf(least, v[i]);
+    for (int i = 1; i < 8; ++i) {
+      top = fmaxf(top, v[i]);
+      low = fminf(low, v[i]);
     }
-    if (top > best) {
+    if (full) least = fminf(least, low);
+    // a row's first elements come after the rest of its first block
+    if (top > best || (top == best && j < at)) {
       best = top;
       at = j;
     }
@@ -433,11 +508,10 @@ __device__ __forceinline__ bool plain_row(const SampleView& a, int64_t row, cons
 
 // A row without top-k and top-p: the blocks' sums, and the draw.
 template <typename E>
-__device__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, const RowSpace& s,
-                         Shared& sh) {
-  const Row<E> r(a, row);
+__device__ __forceinline__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m,
+                                         const RowSpace& s, Shared& sh, Walk<E>& walk) {
   u64 sum = 0;
-  walk<2>(r, g, blockIdx.x, [&](int, const float (&v)[8]) {
+  walk.run([&](int, const float (&v)[8], bool) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const u64 w = m.weight(v[i]);
@@ -458,11 +532,13 @@ __global__ __launch_bounds__(kSampleThreads) void sample_free_kernel(SampleView 
   __shared__ Shared sh;
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
+  const Row<E> r(a, row);
+  auto walk = walk_of(r, g);
   sh.exps.fill();
   __syncthreads();
   const Limits m = limits_of(a, row, g, s, sh.exps.step);
   if (plain_row(a, row, m, blockIdx.x, s.state)) return;
-  free_row<E>(a, row, g, m, s, sh);
+  free_row(a, row, g, m, s, sh, walk);
 }
 
 // Counts and weights of the intervals, and from all chunks' the interval of the cut.
@@ -474,6 +550,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
   const int c = blockIdx.x, t = threadIdx.x;
+  const Row<E> r(a, row);
+  auto walk = walk_of(r, g);
   sh.exps.fill();
   for (int i = t; i < kBins; i += kSampleThreads) {
     weights[i] = 0;
@@ -483,19 +561,18 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
   const Limits m = limits_of(a, row, g, s, sh.exps.step);
   if (plain_row(a, row, m, c, s.state)) return;
   if (m.k == 0 && m.p == 1.0f) {
-    free_row<E>(a, row, g, m, s, sh);
+    free_row(a, row, g, m, s, sh, walk);
     return;
   }
-  const Row<E> r(a, row);
   if (m.k > 0) {
-    walk<2>(r, g, c, [&](int, const float (&v)[8]) {
+    walk.run([&](int, const float (&v)[8], bool) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (v[i] != -__builtin_inff()) atomicAdd(&counts[m.bin(v[i])], 1u);
     }, [](int) {});
   } else {
     u64 rest = 0;   // of the last interval, which half of the tokens fall into and more
-    walk<2>(r, g, c, [&](int, const float (&v)[8]) {
+    walk.run([&](int, const float (&v)[8], bool) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const u64 w = m.weight(v[i]);
@@ -530,14 +607,28 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
       w[i] = 0;
       n[i] = 0;
     }
+    // all chunks' loads before the first sum
+    static_assert(kEach == 2, "a lane's two counts are read as one word");
+    u64 part[kMostChunks][kEach];
+    if (m.k == 0) {
 #pragma unroll
-    for (int k = 0; k < kMostChunks; ++k)
+      for (int k = 0; k < kMostChunks; ++k)
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (k < g.chunks) {
-          if (m.k == 0) w[i] += told(&s.weights[k * kBins + t * kEach + i]);
-          else n[i] += told(&s.counts[k * kBins + t * kEach + i]);
-        }
+        for (int i = 0; i < kEach; ++i) part[k][i] = told(&s.weights[min(k, g.chunks - 1) * kBins + t * kEach + i]);
+#pragma unroll
+      for (int k = 0; k < kMostChunks; ++k)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) w[i] += k < g.chunks ? part[k][i] : 0;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kMostChunks; ++k)
+        part[k][0] = told(reinterpret_cast<const u64*>(s.counts) + (min(k, g.chunks - 1) * kBins / 2 + t));
+#pragma unroll
+      for (int k = 0; k < kMostChunks; ++k) {
+        n[0] += k < g.chunks ? static_cast<uint32_t>(part[k][0]) : 0;
+        n[1] += k < g.chunks ? static_cast<uint32_t>(part[k][0] >> 32) : 0;
+      }
+    }
   }
   u64 all_w = 0, all_n = 0, total, count;
 #pragma unroll
@@ -589,11 +680,11 @@ struct ListSpace {
   uint32_t bin_counts[256];
 };
 
-// The lowest place that is kept: in falling order, the first one at which the count (BY_COUNT) or
+// The lowest place that is kept: in falling order, the first one at which the count (by_count) or
 // the sum of the weights reaches want >= 1, and 0 where none does.  Digit by digit, of what `each` calls its argument with: (place, weight) of every
 // token.  The places have the bits of `base` but for the last `bits`.
-template <bool BY_COUNT, typename Each>
-__device__ u64 find_cut(u64 want, u64 base, int bits, Shared& s, ListSpace& list, Each each) {
+template <typename Each>
+__device__ __forceinline__ u64 find_cut(bool by_count, u64 want, u64 base, int bits, Shared& s, ListSpace& list, Each each) {
   const int t = threadIdx.x;
   u64 prefix = base >> bits << bits;
   __syncthreads();
@@ -607,11 +698,11 @@ __device__ u64 find_cut(u64 want, u64 base, int bits, Shared& s, ListSpace& list
       if (w == 0 || place >> known != prefix >> known) return;
       const int b = 255 - static_cast<int>(place >> shift & 255);
       atomicAdd(&list.bin_counts[b], 1u);
-      if (!BY_COUNT) atomicAdd(&list.bin_weights[b], w);
+      if (!by_count) atomicAdd(&list.bin_weights[b], w);
     });
     __syncthreads();
     const uint32_t count = list.bin_counts[t];
-    const u64 here = BY_COUNT ? count : list.bin_weights[t];
+    const u64 here = by_count ? count : list.bin_weights[t];
     list.bin_counts[t] = 0;
     list.bin_weights[t] = 0;
     u64 total;
@@ -640,15 +731,60 @@ __device__ u64 find_cut(u64 want, u64 base, int bits, Shared& s, ListSpace& list
 // The cut of a row's top-k and top-p, from the tokens that `each` goes through; what lies before
 // them counts and weighs as given.
 template <typename Each>
-__device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, u64 base, int bits, Shared& s,
-                      ListSpace& list, Each each) {
+__device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, u64 base, int bits,
+                                      Shared& s, ListSpace& list, Each each) {
   u64 cut = 0;
+#pragma unroll 1
+  for (int by_k = m.k > 0; by_k >= (m.p < 1.0f ? 0 : 1); --by_k) {
+    u64 want = m.k - count_before;
+    if (!by_k) {
+      if (m.k > 0) {   // p of the first k
+        u64 sum = 0;
+        each([&](u64 place, u64 w) { sum += place >= cut ? w : 0; });
+        sum_before(sum, s.wave, total);
+        total += weight_before;
+      }
+      bool rest;
+      want = part_of(m.p, total, rest);
+      want += rest || want == 0;
+      want -= weight_before;
+    }
+    const u64 found = find_cut(by_k != 0, want, base, bits, s, list, each);
+    cut = found > cut ? found : cut;
+  }
+  return cut;
+}
+
+// The same for n <= kSampleThreads listed tokens, one a lane, which are sorted: 36 exchanges, of which three go
+// through LDS, where the digits have some ten barriers each.
+__device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight_before, u64 count_before, int n, Shared& s,
+                                          ListSpace& list) {
+  const int t = threadIdx.x;
+  u64 place = t < n ? list.place[t] : 0;
+#pragma unroll 1
+  for (int size = 2; size <= kSampleThreads; size <<= 1)
+#pragma unroll 1
+    for (int o = size >> 1; o >= 1; o >>= 1) {
+      u64 x;
+      if (o >= 64) {
+        __syncthreads();
+        list.place[t] = place;
+        __syncthreads();
+        x = list.place[t ^ o];
+      } else {
+        x = __shfl_xor(place, o, 64);
+      }
+      // falling order: the lower lane of a pair keeps the larger one, the other way round in every
+      // second run
+      const bool larger = ((t & o) == 0) == ((t & size) == 0);
+      if ((x > place) == larger) place = x;
+    }
+  const u64 w = t < n ? m.weight(logit_at(place)) : 0;
+  bool keep = t < n;
   if (m.k > 0) {
-    cut = find_cut<true>(m.k - count_before, base, bits, s, list, each);
-    if (m.p < 1.0f) {   // p of the first k
-      u64 sum = 0;
-      each([&](u64 place, u64 w) { sum += place >= cut ? w : 0; });
-      sum_before(sum, s.wave, total);
+    keep = keep && t + count_before < static_cast<u64>(m.k);
+    if (m.p < 1.0f) {
+      sum_before(keep ? w : 0, s.wave, total);
       total += weight_before;
     }
   }
@@ -656,10 +792,20 @@ __device__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_b
     bool rest;
     u64 want = part_of(m.p, total, rest);
     want += rest || want == 0;
-    const u64 by_p = find_cut<false>(want - weight_before, base, bits, s, list, each);
-    cut = by_p > cut ? by_p : cut;
+    u64 all;
+    const u64 before = sum_before(w, s.wave, all);   // by every lane: it has barriers
+    keep = keep && before + weight_before < want;
   }
-  return cut;
+  // the kept ones are the first ones: the last of them is the cut
+  const u64 kept = __ballot(keep);
+  __syncthreads();
+  list.place[t] = place;
+  if ((t & 63) == 0) s.wave[t >> 6] = __popcll(kept);
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) count += static_cast<int>(s.wave[i]);
+  return count > 0 ? list.place[count - 1] : ~u64(0);
 }
 
 template <typename E>
@@ -669,16 +815,18 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
   __shared__ u64 sums[kMostBlocks];
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  const Row<E> r(a, row);
+  auto walk = walk_of(r, g);
   const RowState x = *s.state;
   if (x.mode == kDone) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  if (t == 0) sh.listed = 0;
   sh.exps.fill();
   __syncthreads();
   const Limits m = limits_of(a, row, g, s, sh.exps.step);
-  const Row<E> r(a, row);
   if (x.mode == kListed) {
     u64 sum = 0;
-    walk<2>(r, g, c, [&](int j, const float (&v)[8]) {
+    walk.run([&](int j, const float (&v)[8], bool) {
       unsigned listed = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -690,76 +838,71 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
           listed |= 1u << i;
         }
       }
-      if (__ballot(listed != 0) == 0) return;
-      const int mine = __popc(listed);
-      int before = mine;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(before, o, 64);
-        if (lane >= o) before += y;
-      }
-      uint32_t at = 0;
-      if (lane == 63) at = __hip_atomic_fetch_add(&s.state->listed, static_cast<uint32_t>(before), __ATOMIC_RELAXED,
-                                                  __HIP_MEMORY_SCOPE_AGENT);
-      at = __shfl(at, 63, 64) + before - mine;
+      if (listed == 0) return;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (listed >> i & 1) {
-          if (at < kList) tell(&s.list[at], place_of(v[i], j + i));
-          ++at;
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < kList) list.place[at] = place_of(v[i], j + i);
         }
     }, [&](int block) {
       sum = wave_sum(sum);
       if (lane == 0) tell(&s.sums[block], sum);
       sum = 0;
     });
+    // this workgroup's tokens into the row's list, as far as it goes
+    __syncthreads();
+    const uint32_t mine = sh.listed;
+    if (mine > 0 && g.chunks > 1) {
+      if (t == 0)
+        sh.place_at = __hip_atomic_fetch_add(&s.state->listed, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      const uint32_t at = sh.place_at;
+      for (uint32_t i = t; i < min(mine, static_cast<uint32_t>(kList)); i += kSampleThreads)
+        if (at + i < kList) tell(&s.list[at + i], list.place[i]);
+    }
   }
   if (!last_of_row(&s.state->arrived[1], g.chunks, &sh.arrived)) return;
-  const uint32_t listed = told(&s.state->listed);
-  u64 cut = 0;
-  if (x.mode == kListed && listed <= kList) {
-    const int n = static_cast<int>(listed);
-    u64 base = 0, other = 0;
-    if (n > 0) base = told(&s.list[0]);
+  // the listed tokens, or where they are more than the list holds the whole row, by this workgroup
+  const int n = static_cast<int>(g.chunks > 1 ? told(&s.state->listed) : sh.listed);
+  const bool in_list = x.mode == kListed && n <= kList;
+  u64 cut = 0, base = 0, other = 0;
+  if (in_list && n > 0) {
+    base = g.chunks > 1 ? told(&s.list[0]) : list.place[0];
+    __syncthreads();
     for (int i = t; i < n; i += kSampleThreads) {
-      const u64 place = told(&s.list[i]);
+      const u64 place = g.chunks > 1 ? told(&s.list[i]) : list.place[i];
       list.place[i] = place;
       other |= place ^ base;
     }
-    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = told(&s.sums[b]);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
-    if (lane == 0) sh.found[wave] = other;
-    __syncthreads();
-    other = sh.found[0] | sh.found[1] | sh.found[2] | sh.found[3];
-    const auto each = [&](auto f) {
-      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], m.weight(logit_at(list.place[i])));
-    };
-    if (x.lo < kBins)
-      cut = cut_of(m, x.total, x.weight_before, x.count_before, base, 64 - __clzll(other), sh, list, each);
-    __syncthreads();
-    each([&](u64 place, u64 w) {
-      if (place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
-    });
-  } else {
-    // more tokens in the cut's interval than the list holds: over the whole row, one workgroup
-    const auto each = [&](auto f) {
-      for (int b = wave; b < g.blocks; b += kWaves)
-        for (int it = 0; it < g.size / 512; ++it) {
-          const int j = r.first(g, b, it, lane);
-          float v[8];
-          r.load(j, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f(place_of(v[i], j + i), m.weight(v[i]));
-        }
-    };
-    cut = cut_of(m, x.total, 0, 0, 0, 32 + kIndexBits, sh, list, each);
-    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = 0;
-    __syncthreads();
-    each([&](u64 place, u64 w) {
-      if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
-    });
   }
+  if (lane == 0) sh.found[wave] = other;
+  for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = in_list ? told(&s.sums[b]) : 0;
+  __syncthreads();
+  other = sh.found[0] | sh.found[1] | sh.found[2] | sh.found[3];
+  const auto each = [&](auto f) {
+    if (in_list) {
+#pragma unroll 1
+      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], m.weight(logit_at(list.place[i])));
+    } else {
+#pragma unroll 1
+      for (int j = t; j < r.n; j += kSampleThreads) {
+        const float l = r.at(j);
+        f(place_of(l, j), m.weight(l));
+      }
+    }
+  };
+  if (in_list && x.lo < kBins && n <= kSampleThreads)
+    cut = cut_of_few(m, x.total, x.weight_before, x.count_before, n, sh, list);
+  else if (!in_list || x.lo < kBins)
+    cut = cut_of(m, x.total, in_list ? x.weight_before : 0, in_list ? x.count_before : 0, base,
+                 in_list ? 64 - __clzll(other) : 32 + kIndexBits, sh, list, each);
+  __syncthreads();
+  each([&](u64 place, u64 w) {
+    if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
+  });
   __syncthreads();
   draw<E>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [&](float l, int j) { return place_of(l, j) >= cut; });
 }
