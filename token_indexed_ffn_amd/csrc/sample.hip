@@ -290,6 +290,10 @@ struct Limits {
 
 __device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& g, const RowSpace& s,
                             const double* step) {
+  // every load before the first use, none behind a branch: u stands in for what is not given
+  const float temperature = (a.temperature ? a.temperature : a.u)[row], given_p = (a.top_p ? a.top_p : a.u)[row];
+  const float given_low = (a.min_p ? a.min_p : a.u)[row];
+  const int given_k = (a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[row];
   u64 best = 0;
   float least = __builtin_inff();
   const int lane = threadIdx.x & 63;
@@ -297,26 +301,29 @@ __device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& 
     best = s.best[lane];
     least = s.least[lane];
   }
+  static_assert(kMostChunks <= 16, "one row of lanes");
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
+  for (int o = 8; o >= 1; o >>= 1) {
     const u64 x = __shfl_xor(best, o, 64);
     best = x > best ? x : best;
     least = fminf(least, __shfl_xor(least, o, 64));
   }
+  best = __shfl(best, 0, 64);
+  least = __shfl(least, 0, 64);
   Limits m;
   m.top = logit_at(best);
   m.first = index_at(best);
   m.empty = m.top == -__builtin_inff();
-  m.temperature = a.temperature ? a.temperature[row] : 1.0f;
+  m.temperature = a.temperature ? temperature : 1.0f;
   m.greedy = !(m.temperature > 0.0f);
   const int bits = 62 - (32 - __clz(a.vocab));
   m.weight = Weights{fmin(static_cast<double>(m.top), 1e300), 46.1662413084468290355 / static_cast<double>(m.temperature),
                      bits < 50 ? bits : 50, step};
-  const int k = a.top_k ? a.top_k[row] : 0;
+  const int k = a.top_k ? given_k : 0;
   m.k = k > 0 && k < a.vocab ? k : 0;
-  const float p = a.top_p ? a.top_p[row] : 1.0f;
+  const float p = a.top_p ? given_p : 1.0f;
   m.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
-  const float low = a.min_p ? a.min_p[row] : 0.0f;
+  const float low = a.min_p ? given_low : 0.0f;
   m.least_weight = low > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(low, 1.0f)) * m.weight.unit())) : 0;
   // Weights past this distance are rounded to zero.  With top-p alone also: all weights below
   // (1 - p) / vocab, of the largest one, make less than 1 - p of the whole, so that the cut lies above them.
@@ -328,15 +335,32 @@ __device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& 
 }
 
 // ------------------------------------------------------------------------------ workgroup sums
+// v of the lane that a DPP control names, 0 where there is none or the row is masked out.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ u64 from_lane(u64 v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CONTROL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CONTROL, ROWS, 0xf, false);
+  return static_cast<u64>(hi) << 32 | lo;
+}
+
+// Sum over a wave's lanes up to this one: shifts by 1, 2, 4, 8 within rows of 16 lanes, then a row's
+// last lane to the next row, and lane 31 to the upper half.  (In registers: a shuffle through LDS takes some
+// hundred cycles a step.)
+__device__ __forceinline__ u64 sum_up_to(u64 v) {
+  v += from_lane<0x111, 0xf>(v);
+  v += from_lane<0x112, 0xf>(v);
+  v += from_lane<0x114, 0xf>(v);
+  v += from_lane<0x118, 0xf>(v);
+  v += from_lane<0x142, 0xa>(v);
+  v += from_lane<0x143, 0xc>(v);
+  return v;
+}
+// Lane 63 has the wave's sum.
+
 // Sum over the lanes before this one; total over all.
 __device__ __forceinline__ u64 sum_before(u64 v, u64* wave_sums, u64& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  u64 x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const u64 y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
+  const u64 x = sum_up_to(v);
   __syncthreads();
   if (lane == 63) wave_sums[wave] = x;
   __syncthreads();
@@ -348,12 +372,6 @@ __device__ __forceinline__ u64 sum_before(u64 v, u64* wave_sums, u64& total) {
     total += wave_sums[i];
   }
   return before + x - v;
-}
-
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
 }
 
 // What workgroups of a row tell each other in one launch goes past the caches of an XCD: written and
@@ -518,8 +536,8 @@ __device__ __forceinline__ void free_row(const SampleView& a, int64_t row, const
       sum += w >= m.least_weight ? w : 0;
     }
   }, [&](int block) {
-    sum = wave_sum(sum);
-    if ((threadIdx.x & 63) == 0) tell(&s.sums[block], sum);
+    sum = sum_up_to(sum);
+    if ((threadIdx.x & 63) == 63) tell(&s.sums[block], sum);
     sum = 0;
   });
   if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
@@ -581,8 +599,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
         else rest += w;
       }
     }, [](int) {});
-    rest = wave_sum(rest);
-    if ((t & 63) == 0) atomicAdd(&weights[kBins - 1], rest);
+    rest = sum_up_to(rest);
+    if ((t & 63) == 63) atomicAdd(&weights[kBins - 1], rest);
   }
   __syncthreads();
   if (g.chunks > 1) {
@@ -755,14 +773,14 @@ __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_bef
   return cut;
 }
 
-// The same for n <= kSampleThreads listed tokens, one a lane, which are sorted: 36 exchanges, of which three go
+// The same for n <= kSampleThreads listed tokens, one a lane, which are sorted: up to 36 exchanges, of which three go
 // through LDS, where the digits have some ten barriers each.
 __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight_before, u64 count_before, int n, Shared& s,
                                           ListSpace& list) {
   const int t = threadIdx.x;
   u64 place = t < n ? list.place[t] : 0;
 #pragma unroll 1
-  for (int size = 2; size <= kSampleThreads; size <<= 1)
+  for (int size = 2; size < 2 * n; size <<= 1)
 #pragma unroll 1
     for (int o = size >> 1; o >= 1; o >>= 1) {
       u64 x;
@@ -846,8 +864,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
           if (at < kList) list.place[at] = place_of(v[i], j + i);
         }
     }, [&](int block) {
-      sum = wave_sum(sum);
-      if (lane == 0) tell(&s.sums[block], sum);
+      if (x.lo > 0) sum = sum_up_to(sum);
+      if (lane == 63) tell(&s.sums[block], sum);
       sum = 0;
     });
     // this workgroup's tokens into the row's list, as far as it goes
