@@ -63,12 +63,6 @@ __device__ const double kSteps[32] = {
     1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
     1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002,
 };
-struct Exponents {
-  double step[32];
-  __device__ __forceinline__ void fill() {
-    if (threadIdx.x < 32) step[threadIdx.x] = kSteps[threadIdx.x];
-  }
-};
 
 // A row's weights.
 struct Weights {
@@ -125,7 +119,6 @@ struct RowState {
   u64 total;             // of all weights
   u64 weight_before;     // of the tokens above interval `lo`
   uint32_t count_before;
-  uint32_t listed;
   uint32_t arrived[2];
   int lo, hi;            // intervals whose tokens are listed
   int mode;
@@ -137,7 +130,8 @@ struct RowSpace {
   u64* best;        // [chunks]: place of the largest logit
   float* least;     // [chunks]: the smallest logit
   u64* sums;        // [blocks]: kept weights, those of listed tokens aside
-  u64* list;        // [kList]: places
+  u64* list;        // [chunks][kList]: places
+  uint32_t* listed; // [chunks]
   u64* weights;     // [chunks][kBins]
   uint32_t* counts; // [chunks][kBins]
   __host__ __device__ RowSpace(char* p, int64_t row, const SampleGrid& g) {
@@ -146,9 +140,10 @@ struct RowSpace {
     best = reinterpret_cast<u64*>(p + 64);
     sums = best + kMostChunks;
     list = sums + kMostBlocks + 7;
-    weights = list + kList;
+    weights = list + static_cast<int64_t>(g.chunks) * kList;
     counts = reinterpret_cast<uint32_t*>(weights + static_cast<int64_t>(g.chunks) * kBins);
     least = reinterpret_cast<float*>(counts + static_cast<int64_t>(g.chunks) * kBins);
+    listed = reinterpret_cast<uint32_t*>(least + kMostChunks);
   }
 };
 static_assert(sizeof(RowState) <= 64, "before best");
@@ -288,9 +283,10 @@ struct Limits {
   }
 };
 
-__device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& g, const RowSpace& s,
-                            const double* step) {
+__device__ __forceinline__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& g, const RowSpace& s,
+                                            double* step) {
   // every load before the first use, none behind a branch: u stands in for what is not given
+  const double one_step = kSteps[threadIdx.x & 31];
   const float temperature = (a.temperature ? a.temperature : a.u)[row], given_p = (a.top_p ? a.top_p : a.u)[row];
   const float given_low = (a.min_p ? a.min_p : a.u)[row];
   const int given_k = (a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[row];
@@ -331,6 +327,8 @@ __device__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& 
   if (m.k == 0 && m.p < 1.0f) reach = fminf(reach, logf(static_cast<float>(a.vocab) / (1.0f - m.p)) + 0.01f);
   reach = fminf(m.temperature * reach, m.top - least);
   m.bin_rate = reach > 0.0f ? kBins / reach : 0.0f;
+  if (threadIdx.x < 32) step[threadIdx.x] = one_step;
+  __syncthreads();
   return m;
 }
 
@@ -400,10 +398,10 @@ __device__ __forceinline__ bool last_of_row(uint32_t* arrived, int chunks, uint3
 }
 
 struct Shared {
-  Exponents exps;
+  double step[32];
   u64 wave[kWaves];
   u64 found[4];
-  uint32_t arrived, listed, place_at;
+  uint32_t arrived, listed;
 };
 
 // ------------------------------------------------------------------------------------- the draw
@@ -467,7 +465,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
   const Row<E> r(a, row);
   const RowSpace s(ws, row, g);
-  if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = s.state->listed = 0;
+  if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = 0;
   // a lane's largest logit and its group, later the group's first element that has it
   float best = -__builtin_inff(), least = __builtin_inff();
   int at = 0;
@@ -552,9 +550,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_free_kernel(SampleView 
   const RowSpace s(ws, row, g);
   const Row<E> r(a, row);
   auto walk = walk_of(r, g);
-  sh.exps.fill();
-  __syncthreads();
-  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  const Limits m = limits_of(a, row, g, s, sh.step);
   if (plain_row(a, row, m, blockIdx.x, s.state)) return;
   free_row(a, row, g, m, s, sh, walk);
 }
@@ -570,13 +566,11 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
   const int c = blockIdx.x, t = threadIdx.x;
   const Row<E> r(a, row);
   auto walk = walk_of(r, g);
-  sh.exps.fill();
   for (int i = t; i < kBins; i += kSampleThreads) {
     weights[i] = 0;
     counts[i] = 0;
   }
-  __syncthreads();
-  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  const Limits m = limits_of(a, row, g, s, sh.step);
   if (plain_row(a, row, m, c, s.state)) return;
   if (m.k == 0 && m.p == 1.0f) {
     free_row(a, row, g, m, s, sh, walk);
@@ -837,11 +831,9 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
   const Row<E> r(a, row);
   auto walk = walk_of(r, g);
   const RowState x = *s.state;
-  if (x.mode == kDone) return;
   if (t == 0) sh.listed = 0;
-  sh.exps.fill();
-  __syncthreads();
-  const Limits m = limits_of(a, row, g, s, sh.exps.step);
+  const Limits m = limits_of(a, row, g, s, sh.step);
+  if (x.mode == kDone) return;
   if (x.mode == kListed) {
     u64 sum = 0;
     walk.run([&](int j, const float (&v)[8], bool) {
@@ -868,31 +860,40 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
       if (lane == 63) tell(&s.sums[block], sum);
       sum = 0;
     });
-    // this workgroup's tokens into the row's list, as far as it goes
-    __syncthreads();
-    const uint32_t mine = sh.listed;
-    if (mine > 0 && g.chunks > 1) {
-      if (t == 0)
-        sh.place_at = __hip_atomic_fetch_add(&s.state->listed, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (g.chunks > 1) {
       __syncthreads();
-      const uint32_t at = sh.place_at;
+      const uint32_t mine = sh.listed;
       for (uint32_t i = t; i < min(mine, static_cast<uint32_t>(kList)); i += kSampleThreads)
-        if (at + i < kList) tell(&s.list[at + i], list.place[i]);
+        tell(&s.list[c * kList + i], list.place[i]);
+      if (t == 0) tell(&s.listed[c], mine);
     }
   }
   if (!last_of_row(&s.state->arrived[1], g.chunks, &sh.arrived)) return;
   // the listed tokens, or where they are more than the list holds the whole row, by this workgroup
-  const int n = static_cast<int>(g.chunks > 1 ? told(&s.state->listed) : sh.listed);
+  int n = 0, before = 0;
+  const int part = t / 16;   // sixteen lanes for a chunk's list
+  static_assert(kMostChunks * 16 <= kSampleThreads, "a row of lanes a chunk");
+  uint32_t count = 0;
+  if (x.mode == kListed) {
+    count = g.chunks > 1 ? (lane < g.chunks ? told(&s.listed[lane]) : 0) : (lane == 0 ? sh.listed : 0);
+#pragma unroll
+    for (int i = 0; i < kMostChunks; ++i) {
+      const int here = min(__shfl(static_cast<int>(count), i, 64), kList + 1);
+      if (i < part) before += here;
+      n += here;
+    }
+    count = __shfl(count, part, 64);
+  }
   const bool in_list = x.mode == kListed && n <= kList;
   u64 cut = 0, base = 0, other = 0;
   if (in_list && n > 0) {
-    base = g.chunks > 1 ? told(&s.list[0]) : list.place[0];
-    __syncthreads();
-    for (int i = t; i < n; i += kSampleThreads) {
-      const u64 place = g.chunks > 1 ? told(&s.list[i]) : list.place[i];
-      list.place[i] = place;
-      other |= place ^ base;
+    if (g.chunks > 1) {
+      if (part < g.chunks)
+        for (uint32_t i = t % 16; i < count; i += 16) list.place[before + i] = told(&s.list[part * kList + i]);
+      __syncthreads();
     }
+    base = list.place[0];
+    for (int i = t; i < n; i += kSampleThreads) other |= list.place[i] ^ base;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
   }
@@ -938,7 +939,7 @@ static SampleGrid sample_grid(int64_t n_rows, int64_t vocab) {
   g.blocks_a_chunk = static_cast<int>((g.blocks + chunks - 1) / chunks);
   g.chunks = (g.blocks + g.blocks_a_chunk - 1) / g.blocks_a_chunk;
   g.row_bytes = static_cast<int64_t>(align_up(
-      64 + 8 * (kMostChunks + kMostBlocks + 7 + kList) + 12 * static_cast<size_t>(g.chunks) * kBins + 4 * kMostChunks, 256));
+      64 + 8 * (kMostChunks + kMostBlocks + 7) + static_cast<size_t>(g.chunks) * (8 * kList + 12 * kBins) + 8 * kMostChunks, 256));
   return g;
 }
 
