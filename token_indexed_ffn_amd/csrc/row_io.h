@@ -39,6 +39,62 @@ __device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(p->
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16_t* p, float v) { p->bits = f32_to_bf16(v); }
 
+// Eight elements as they lie in memory, 16-byte aligned.
+template <typename E> struct Raw;
+template <> struct Raw<bf16_t> {
+  u32x4_t a;
+  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
+  // What was made of these elements is made again after this, rather than kept in registers.
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Raw<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4_t*>(p);
+    b = *reinterpret_cast<const f32x4_t*>(p + 4);
+  }
+  __device__ __forceinline__ void clear() {
+    const float x = -__builtin_inff();
+    a = b = f32x4_t{x, x, x, x};
+  }
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a), "+v"(b)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[i + 4] = b[i];
+    }
+  }
+};
+
+// A row's elements in groups of eight that begin where its memory is 16-byte aligned: `shift`
+// elements before the row.  The elements outside full groups are the first `head` (fewer than
+// eight) and the last `tail`.
+struct RowGroups {
+  int n, shift, head, tail;
+  template <typename E>
+  __device__ __forceinline__ RowGroups(const E* p, int width)
+      : n(width), shift(static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(E))) {
+    head = shift > 0 ? min(n, 8 - shift) : 0;
+    tail = n > head ? n + shift & 7 : 0;
+  }
+  __device__ __forceinline__ bool full(int j) const { return j >= 0 && j + 8 <= n; }
+  // The element outside full groups that a lane takes (lanes 0 to 7 the first ones, 32 to 39 the last ones),
+  // or -1.
+  __device__ __forceinline__ int edge(int lane) const {
+    if (lane < head) return lane;
+    return lane >= 32 && lane - 32 < tail ? n - tail + lane - 32 : -1;
+  }
+};
+
 // The eight elements that lane t of T holds of group g of a row: with VEC, elements
 // (g T + t) 8 .. + 7, 16 bytes (two times 16 in fp32) a load; without, for rows that are
 // not 16-byte aligned or end inside eight elements, elements (8 g + i) T + t, so that

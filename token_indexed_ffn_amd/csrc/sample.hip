@@ -169,39 +169,6 @@ struct Row {
   }
 };
 
-// Eight elements as they lie in memory.
-template <typename E> struct Raw;
-template <> struct Raw<bf16_t> {
-  u32x4_t a;
-  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
-  __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = no_nan(__uint_as_float(a[i] << 16));
-      v[2 * i + 1] = no_nan(__uint_as_float(a[i] & 0xffff0000u));
-    }
-  }
-};
-template <> struct Raw<float> {
-  f32x4_t a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const f32x4_t*>(p);
-    b = *reinterpret_cast<const f32x4_t*>(p + 4);
-  }
-  __device__ __forceinline__ void clear() {
-    const float x = -__builtin_inff();
-    a = b = f32x4_t{x, x, x, x};
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = no_nan(a[i]);
-      v[i + 4] = no_nan(b[i]);
-    }
-  }
-};
-
 // Blocks begin, begin + stride, ... of a row before `end`, eight elements a lane at a time, with the
 // next kAhead loads in flight, from the walk's making on.  One copy of the body, and loops that are not
 // unrolled, here and below: these kernels run for a few microseconds, and 60 KB of code took longer to
@@ -237,6 +204,8 @@ struct Walk {
     for (int s = 0; s < steps; ++s) {
       float v[8];
       raw[0].get(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = no_nan(v[i]);
       int j = first(s);
       bool full = j >= 0 && j + 8 <= r.n;
 #pragma unroll

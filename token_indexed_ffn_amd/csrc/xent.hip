@@ -2,7 +2,9 @@
 //
 //   lse = log sum_j exp l_j,   loss = lse - l_t,   dl_j = g (exp(l_j - lse) - [j = t])
 //
-// A row's sum runs with its maximum: (m, s) stands for s exp m, and two such pairs join into one.
+// A workgroup holds its row in registers, as it lies in memory: one read, the maximum, the sum, and
+// with the gradient one write.  Rows past what the registers hold are read once more for the gradient, their
+// sum running with its maximum: (m, s) stands for s exp m, and two such pairs join into one.
 #include "model_ops.h"
 #include "row_io.h"
 
@@ -11,6 +13,20 @@ namespace staple {
 // What exponents are taken relative to: the maximum, or 0 where it is infinite (a row of
 // -inf has the sum 0, one with +inf the sum +inf).
 __device__ __forceinline__ float reference(float m) { return __builtin_isinf(m) ? 0.0f : m; }
+
+// Sums and maxima over the T lanes of a row, in a fixed order; every lane gets them.  tmp: T / 64
+// floats that no wave still reads.
+template <int T>
+__device__ __forceinline__ float row_max(float v, float* tmp, int t) {
+  v = wave_max(v);
+  if (T == 64) return v;
+  if ((t & 63) == 0) tmp[t >> 6] = v;
+  __syncthreads();
+  v = tmp[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) v = fmaxf(v, tmp[i]);
+  return v;
+}
 
 struct MaxSum {
   float m = -__builtin_inff(), s = 0.0f;
@@ -21,103 +37,285 @@ struct MaxSum {
     m = top;
     s = a + b;
   }
-  template <int N>
-  __device__ __forceinline__ void add(const float (&v)[N]) {
+  __device__ __forceinline__ void add(const float (&v)[8]) {
     float top = m;
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i]);
     const float ref = reference(top);
     if (top != m) {
       if (s != 0.0f) s *= __expf(reference(m) - ref);
       m = top;
     }
+    float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s += __expf(v[i] - ref);
+    for (int i = 0; i < 8; i += 2) {
+      a += __expf(v[i] - ref);
+      b += __expf(v[i + 1] - ref);
+    }
+    s += a + b;
   }
 };
 
-// Joined over a workgroup of T lanes, in a fixed order; every lane gets the result.
-template <int T>
-__device__ __forceinline__ void join_all(MaxSum& x, float2* tmp) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x.join(__shfl_xor(x.m, o, 64), __shfl_xor(x.s, o, 64));
-  if (T == 64) return;
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = make_float2(x.m, x.s);
-  __syncthreads();
-  x = MaxSum{tmp[0].x, tmp[0].y};
-#pragma unroll
-  for (int i = 1; i < T / 64; ++i) x.join(tmp[i].x, tmp[i].y);
-}
-
-__device__ __forceinline__ float log_sum(const MaxSum& x) { return logf(x.s) + reference(x.m); }
-
 // The target of a row: -1 where the row does not count.
-__device__ __forceinline__ int target_of(const XentView& a, int64_t i, int* err) {
-  const int t = a.targets[i];
-  if (t < 0) return -1;
-  if (t < a.vocab) return t;
-  if (threadIdx.x == 0) flag_index_error(err);
+__device__ __forceinline__ int target_of(const XentView& a, int64_t i, int t, int* err) {
+  const int target = a.targets[i];
+  if (target < 0) return -1;
+  if (target < a.vocab) return target;
+  if (t == 0) flag_index_error(err);
   return -1;
 }
 
-// g (exp(l - ref) f - [j = t]) for one row; f = 0 where no class is possible.
+__device__ __forceinline__ void store_loss(const XentView& a, int64_t i, int target, float at, float m, float s) {
+  const float lse = logf(s) + reference(m);
+  a.lse[i] = lse;
+  a.loss[i] = target < 0 ? 0.0f : at == -__builtin_inff() && lse == lse ? __builtin_inff() : lse - at;
+}
+
+// A row's gradient: p = exp(l - ref) f, without the target's 1.
+struct Gradient {
+  float ref, f, g;
+  int target;   // -1: all zero
+  // f: 1 / s, with the reference of the sum; for a sum of +inf p is exp(l - inf)
+  __device__ __forceinline__ Gradient(const XentView& a, int64_t i, int t, float m, float s) {
+    g = a.g[i];
+    const bool top = m == __builtin_inff();
+    ref = top ? m : reference(m);
+    f = top ? 1.0f : 1.0f / s;
+    target = s == 0.0f ? -1 : t;
+  }
+  __device__ __forceinline__ Gradient(float lse, float gi, int t) : ref(lse), f(1.0f), g(gi) {
+    target = lse == -__builtin_inff() ? -1 : t;
+  }
+  __device__ __forceinline__ float one(float l, int j) const {
+    if (target < 0) return 0.0f;
+    return g * (__expf(l - ref) * f - (j == target ? 1.0f : 0.0f));
+  }
+  // Eight from element j on, in place.
+  __device__ __forceinline__ void eight(float (&v)[8], int j) const {
+    if (target < 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+      return;
+    }
+    const float gf = g * f;
+    const unsigned at = static_cast<unsigned>(target - j);
+    if (at < 8u) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = g * (__expf(v[k] - ref) * f - (k == static_cast<int>(at) ? 1.0f : 0.0f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __expf(v[k] - ref) * gf;
+    }
+  }
+};
+
+// Eight gradients from element j on: at once where the output is aligned as the logits are.
+template <typename E>
+__device__ __forceinline__ void store_eight(E* out, int j, bool aligned, const float (&v)[8]) {
+  if (aligned) {
+    store8(out + j, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store1(out + j + k, v[k]);
+  }
+}
+
+template <typename E, int T, int G>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void xent_fwd_kernel(XentView a, int* err) {
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  __shared__ float tmp[2][kRows][T / 64];
+  const int t = threadIdx.x % T, slot = threadIdx.x / T;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  if (i >= a.n_rows) return;   // T >= 256: the whole workgroup; T = 64: a wave, which meets no barrier
+  const E* l = reinterpret_cast<const E*>(a.logits) + i * a.stride;
+  const RowGroups r(l, a.vocab);
+  Raw<E> raw[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int j = (q * T + t) * 8 - r.shift;
+    if (r.full(j)) raw[q].load(l + j);
+    else raw[q].clear();
+  }
+  const int edge = t < 64 ? r.edge(t) : -1;
+  const float at_edge = edge >= 0 ? load1(l + edge) : -__builtin_inff();
+  const int target = target_of(a, i, t, err);
+  const float at = target >= 0 ? load1(l + target) : 0.0f;   // before the gradient, which may be in place
+  float m = at_edge;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    float v[8];
+    raw[q].get(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k]);
+  }
+  m = row_max<T>(m, tmp[0][slot], t);
+  const float ref = reference(m);
+  float s[4] = {__expf(at_edge - ref), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    float v[8];
+    raw[q].forget();
+    raw[q].get(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k & 3] += __expf(v[k] - ref);
+  }
+  const float sum = row_sum<T>((s[0] + s[1]) + (s[2] + s[3]), tmp[1][slot], t);
+  if (t == 0) store_loss(a, i, target, at, m, sum);
+  if (!a.d_logits) return;
+  E* out = reinterpret_cast<E*>(a.d_logits) + i * a.d_stride;
+  const bool aligned = RowGroups(out, a.vocab).shift == r.shift;
+  const Gradient grad(a, i, target, m, sum);
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int j = (q * T + t) * 8 - r.shift;
+    float v[8];
+    raw[q].forget();
+    raw[q].get(v);
+    grad.eight(v, j);
+    if (r.full(j)) store_eight(out, j, aligned, v);
+  }
+  if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
+}
+
+// Rows of any width.
 template <typename E, int T>
-__device__ __forceinline__ void gradient_row(const XentView& a, int64_t i, int target, float ref, float f) {
+__global__ __launch_bounds__(T) void xent_fwd_long_kernel(XentView a, int* err) {
+  __shared__ float2 tmp[T / 64];
+  constexpr int kAhead = 4;
+  const int t = threadIdx.x;
+  const int64_t i = blockIdx.x;
+  const E* l = reinterpret_cast<const E*>(a.logits) + i * a.stride;
+  const RowGroups r(l, a.vocab);
+  const int edge = t < 64 ? r.edge(t) : -1;
+  const float at_edge = edge >= 0 ? load1(l + edge) : -__builtin_inff();
+  const int target = target_of(a, i, t, err);
+  const float at = target >= 0 ? load1(l + target) : 0.0f;
+  MaxSum x{at_edge, at_edge == -__builtin_inff() ? 0.0f : __expf(at_edge - reference(at_edge))};
+  for (int q = 0; q * T * 8 < a.vocab + 8; q += kAhead) {
+    Raw<E> raw[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = ((q + u) * T + t) * 8 - r.shift;
+      if (r.full(j)) raw[u].load(l + j);
+      else raw[u].clear();
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float v[8];
+      raw[u].get(v);
+      x.add(v);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) x.join(__shfl_xor(x.m, o, 64), __shfl_xor(x.s, o, 64));
+  if ((t & 63) == 0) tmp[t >> 6] = make_float2(x.m, x.s);
+  __syncthreads();
+  x = MaxSum{tmp[0].x, tmp[0].y};
+#pragma unroll
+  for (int k = 1; k < T / 64; ++k) x.join(tmp[k].x, tmp[k].y);
+  if (t == 0) store_loss(a, i, target, at, x.m, x.s);
+  if (!a.d_logits) return;
+  E* out = reinterpret_cast<E*>(a.d_logits) + i * a.d_stride;
+  const bool aligned = RowGroups(out, a.vocab).shift == r.shift;
+  const Gradient grad(a, i, target, x.m, x.s);
+  for (int q = 0; q * T * 8 < a.vocab + 8; q += kAhead) {
+    Raw<E> raw[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = ((q + u) * T + t) * 8 - r.shift;
+      if (r.full(j)) raw[u].load(l + j);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = ((q + u) * T + t) * 8 - r.shift;
+      if (!r.full(j)) continue;
+      float v[8];
+      raw[u].get(v);
+      grad.eight(v, j);
+      store_eight(out, j, aligned, v);
+    }
+  }
+  if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
+}
+
+// The gradient alone: a workgroup takes kBwdGroups times 2048 elements of a row.
+constexpr int kBwdGroups = 4;
+template <typename E>
+__global__ __launch_bounds__(256) void xent_bwd_kernel(XentView a, int pieces, int* err) {
+  const int64_t i = blockIdx.x / pieces;
+  const int piece = static_cast<int>(blockIdx.x - i * pieces), t = threadIdx.x;
   const E* l = reinterpret_cast<const E*>(a.logits) + i * a.stride;
   E* out = reinterpret_cast<E*>(a.d_logits) + i * a.d_stride;
-  const float g = a.g[i];
-  if (target < 0 || f == 0.0f) {
-    for (int j = threadIdx.x; j < a.vocab; j += T) store1(out + j, 0.0f);
-    return;
+  const RowGroups r(l, a.vocab);
+  const bool aligned = RowGroups(out, a.vocab).shift == r.shift;
+  Raw<E> raw[kBwdGroups];
+  const int j0 = (piece * kBwdGroups * 256 + t) * 8 - r.shift;
+#pragma unroll
+  for (int q = 0; q < kBwdGroups; ++q)
+    if (r.full(j0 + q * 2048)) raw[q].load(l + j0 + q * 2048);
+  const int edge = piece == 0 && t < 64 ? r.edge(t) : -1;
+  const float at_edge = edge >= 0 ? load1(l + edge) : 0.0f;
+  const Gradient grad(a.lse[i], a.g[i], target_of(a, i, piece == 0 ? t : 1, err));
+#pragma unroll
+  for (int q = 0; q < kBwdGroups; ++q) {
+    const int j = j0 + q * 2048;
+    if (!r.full(j)) continue;
+    float v[8];
+    raw[q].get(v);
+    grad.eight(v, j);
+    store_eight(out, j, aligned, v);
   }
-  for (int j = threadIdx.x; j < a.vocab; j += T)
-    store1(out + j, g * (__expf(load1(l + j) - ref) * f - (j == target ? 1.0f : 0.0f)));
-}
-
-template <typename E, int T>
-__global__ __launch_bounds__(T) void xent_fwd_kernel(XentView a, int* err) {
-  __shared__ float2 tmp[T / 64];
-  const int64_t i = blockIdx.x;
-  const E* l = reinterpret_cast<const E*>(a.logits) + i * a.stride;
-  const int target = target_of(a, i, err);
-  MaxSum x;
-  for (int j = threadIdx.x; j < a.vocab; j += T) {
-    const float v[1] = {load1(l + j)};
-    x.add(v);
-  }
-  const float at = target >= 0 ? load1(l + target) : 0.0f;   // before the gradient, which may be in place
-  join_all<T>(x, tmp);
-  if (threadIdx.x == 0) {
-    const float lse = log_sum(x);
-    a.lse[i] = lse;
-    a.loss[i] = target < 0 ? 0.0f : at == -__builtin_inff() && lse == lse ? __builtin_inff() : lse - at;
-  }
-  if (a.d_logits) {
-    __syncthreads();   // every lane has read the target's logit
-    gradient_row<E, T>(a, i, target, reference(x.m), x.s == 0.0f ? 0.0f : 1.0f / x.s);
-  }
-}
-
-template <typename E, int T>
-__global__ __launch_bounds__(T) void xent_bwd_kernel(XentView a, int* err) {
-  const int64_t i = blockIdx.x;
-  const float lse = a.lse[i];
-  gradient_row<E, T>(a, i, target_of(a, i, err), lse, lse == -__builtin_inff() ? 0.0f : 1.0f);
+  if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
 }
 
 size_t xent_workspace_bytes(int64_t, int64_t) { return 0; }
 
+// The narrowest shape that holds a row: lanes and groups of eight a lane, wherever the row begins.
+template <typename E>
+static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
+  const int64_t w = v.vocab + 7;
+#define GO(T, G)                                                                                       \
+  if (w <= int64_t(T) * 8 * G) {                                                                       \
+    constexpr int kRows = T < 256 ? 256 / T : 1;                                                       \
+    xent_fwd_kernel<E, T, G><<<dim3(static_cast<unsigned>((v.n_rows + kRows - 1) / kRows)),            \
+                               dim3(T < 256 ? 256 : T), 0, s>>>(v, err);                               \
+    return;                                                                                            \
+  }
+  GO(64, 1)
+  GO(64, 2)
+  GO(256, 1)
+  GO(256, 2)
+  GO(256, 4)
+  GO(256, 8)
+  GO(512, 8)
+  GO(512, 16)
+  GO(512, 25)
+#undef GO
+  xent_fwd_long_kernel<E, 1024><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(1024), 0, s>>>(v, err);
+}
+
 hipError_t launch_xent_fwd(const XentView& v, int32_t dtype, void*, hipStream_t s, int* err) {
-  const dim3 grid(static_cast<unsigned>(v.n_rows));
-  if (dtype == STAPLE_BF16) xent_fwd_kernel<bf16_t, 512><<<grid, dim3(512), 0, s>>>(v, err);
-  else xent_fwd_kernel<float, 512><<<grid, dim3(512), 0, s>>>(v, err);
+  if (dtype == STAPLE_BF16) xent_fwd<bf16_t>(v, s, err);
+  else xent_fwd<float>(v, s, err);
   return hipGetLastError();
 }
 
 hipError_t launch_xent_bwd(const XentView& v, int32_t dtype, hipStream_t s, int* err) {
-  const dim3 grid(static_cast<unsigned>(v.n_rows));
-  if (dtype == STAPLE_BF16) xent_bwd_kernel<bf16_t, 512><<<grid, dim3(512), 0, s>>>(v, err);
-  else xent_bwd_kernel<float, 512><<<grid, dim3(512), 0, s>>>(v, err);
+  const int pieces = (v.vocab + 7 + kBwdGroups * 2048 - 1) / (kBwdGroups * 2048);
+  const int64_t at_once = (int64_t(1) << 23) / pieces;   // workgroups of a launch
+  for (int64_t i = 0; i < v.n_rows; i += at_once) {
+    XentView a = v;
+    a.n_rows = v.n_rows - i < at_once ? v.n_rows - i : at_once;
+    const int64_t size = dtype == STAPLE_BF16 ? 2 : 4;
+    a.logits += i * a.stride * size;
+    a.d_logits += i * a.d_stride * size;
+    a.targets += i;
+    a.lse += i;
+    a.g += i;
+    const dim3 grid(static_cast<unsigned>(a.n_rows * pieces));
+    if (dtype == STAPLE_BF16) xent_bwd_kernel<bf16_t><<<grid, dim3(256), 0, s>>>(a, pieces, err);
+    else xent_bwd_kernel<float><<<grid, dim3(256), 0, s>>>(a, pieces, err);
+  }
   return hipGetLastError();
 }
 
