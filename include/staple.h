@@ -1033,13 +1033,10 @@ staple_status_t staple_norm_bwd(const staple_norm_t* a, void* ws, size_t ws_byte
  * has it has the loss +inf, and a row that has nothing else has the gradient zero.
  * The forward writes loss and lse float[n_rows] and, with g float[n_rows] (the gradient of each
  * row's loss) and d_logits (of dtype, may be the logits themselves), the gradient in the same
- * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows <= 2^23.
- * Workspace: parts of rows where there are too few to occupy the GPU. */
-size_t staple_xent_workspace_bytes(int64_t n_rows, int64_t vocab);
+ * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows <= 2^23. */
 staple_status_t staple_xent_fwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                                 int32_t dtype, const int32_t* targets, float* loss, float* lse,
-                                const float* g, void* d_logits, int64_t d_stride, void* ws,
-                                size_t ws_bytes, void* stream);
+                                const float* g, void* d_logits, int64_t d_stride, void* stream);
 staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                                 int32_t dtype, const int32_t* targets, const float* lse,
                                 const float* g, void* d_logits, int64_t d_stride, void* stream);

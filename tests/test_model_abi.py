@@ -137,12 +137,10 @@ def test_norm_backward_refuses_combinations(L):
 
 
 def xent(L, **change):
-    f = dict(logits=P, stride=100, n=4, vocab=100, dtype=1, targets=P, loss=P, lse=P, g=P, d_logits=P, d_stride=100,
-             ws=P, ws_bytes=1 << 40)
+    f = dict(logits=P, stride=100, n=4, vocab=100, dtype=1, targets=P, loss=P, lse=P, g=P, d_logits=P, d_stride=100)
     f.update(change)
     fwd = L.load().staple_xent_fwd(*f.values(), None)
-    for n in ("loss", "ws", "ws_bytes"):
-        f.pop(n)
+    f.pop("loss")
     return fwd, L.load().staple_xent_bwd(*f.values(), None)
 
 
@@ -155,14 +153,12 @@ def test_loss_refuses(L, change, status):
     assert xent(L, **change) == (status, status)
 
 
-def test_loss_workspace(L):
-    lib = L.load()
-    assert lib.staple_xent_workspace_bytes(0, 100) == 0 and lib.staple_xent_workspace_bytes(4, 1 << 23) == 0
+def test_loss_refuses_without_its_outputs(L):
     assert xent(L, loss=None)[0] == -1
-    need = lib.staple_xent_workspace_bytes(1, 1 << 22)
-    if need:
-        assert xent(L, n=1, vocab=1 << 22, stride=1 << 22, d_stride=1 << 22, ws_bytes=need - 1)[0] == -3
-        assert xent(L, n=1, vocab=1 << 22, stride=1 << 22, d_stride=1 << 22, ws=None)[0] == -1
+    # the gradient and what it starts from come together
+    lib = L.load()
+    assert lib.staple_xent_fwd(P, 100, 4, 100, 1, P, P, P, None, P, 100, None) == -1
+    assert lib.staple_xent_fwd(P, 100, 4, 100, 1, P, P, P, P, None, 100, None) == -1
 
 
 def sample(L, **change):

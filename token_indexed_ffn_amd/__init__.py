@@ -1299,8 +1299,7 @@ def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: O
 
 
 def staple_xent_fwd(logits: torch.Tensor, targets: torch.Tensor, *, g: Optional[torch.Tensor] = None,
-                    out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
-                    stream=None) -> dict:
+                    out: Optional[dict] = None, stream=None) -> dict:
     """Cross entropy of logits [rows, vocab]: loss and lse [rows], fp32.  targets int32 [rows]; a
     negative one leaves its row out.  g [rows] fp32, the gradient of each row's loss: the gradient
     of the logits comes with them as d_logits (out["d_logits"] may be the logits)."""
@@ -1312,12 +1311,9 @@ def staple_xent_fwd(logits: torch.Tensor, targets: torch.Tensor, *, g: Optional[
     dt = logits.dtype
     at, stride = _rows(logits, "logits", dt, n, vocab)
     d, d_stride = _NO_ROWS if g is None else _rows(out["d_logits"], "d_logits", dt, n, vocab, True)
-    native = lib()
-    ws = _ws(native.staple_xent_workspace_bytes(n, vocab), workspace, logits.device, stream)
-    _check(native.staple_xent_fwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
-                                  _flat(out["loss"], "loss", n, _FLOAT32), _flat(out["lse"], "lse", n, _FLOAT32),
-                                  _flat(g, "g", n, _FLOAT32), d, d_stride, _p(ws), _ws_size(ws), _stream(stream)),
-           "staple_xent_fwd")
+    _check(lib().staple_xent_fwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
+                                 _flat(out["loss"], "loss", n, _FLOAT32), _flat(out["lse"], "lse", n, _FLOAT32),
+                                 _flat(g, "g", n, _FLOAT32), d, d_stride, _stream(stream)), "staple_xent_fwd")
     return out
 
 

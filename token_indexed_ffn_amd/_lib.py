@@ -113,9 +113,8 @@ _SIGS = {
     "staple_norm_fwd": (c_i32, [c_vp, c_vp]),
     "staple_norm_bwd_workspace_bytes": (c_sz, [c_vp]),
     "staple_norm_bwd": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
-    "staple_xent_workspace_bytes": (c_sz, [c_i64, c_i64]),
     "staple_xent_fwd": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
-                                c_i64, c_vp, c_sz, c_vp]),
+                                c_i64, c_vp]),
     "staple_xent_bwd": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i64,
                                 c_vp]),
     "staple_sample_workspace_bytes": (c_sz, [c_i64, c_i64]),

@@ -128,9 +128,8 @@ staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtyp
   if (!valid_dtype(dtype)) return STAPLE_ERR_UNSUPPORTED;
   REQUIRE(n_tokens >= 0 && d >= 1 && std::isfinite(scale) && max_unique >= 0 && grad_rows >= 0);
   REQUIRE(uniq || max_unique <= grad_rows);
-  // workgroups of a launch: one for four pieces of 512 columns of 32 positions
-  if (n_tokens > kMaxTokens29 || d > kMaxWidth ||
-      (n_tokens / 32 + 1) * (d / 512 + 1) > (int64_t(1) << 26) - 4)
+  // workgroups of 512 lanes of a launch: one for 512 columns of 32 positions
+  if (n_tokens > kMaxTokens29 || d > kMaxWidth || (n_tokens / 32 + 1) * (d / 512 + 1) >= int64_t(1) << 23)
     return STAPLE_ERR_UNSUPPORTED;
   if (n_tokens == 0) return STAPLE_OK;
   REQUIRE(in_ok(dy, dy_stride, dtype) && sorted_pos && inv && seg_start && n_unique);
@@ -191,27 +190,18 @@ staple_status_t staple_norm_bwd(const staple_norm_t* a, void* ws, size_t ws_byte
 }
 
 // ----------------------------------------------------------------------- loss
-size_t staple_xent_workspace_bytes(int64_t n_rows, int64_t vocab) {
-  return n_rows >= 1 && n_rows <= kMaxRows && vocab >= 1 && vocab <= kSampleMaxVocab
-             ? xent_workspace_bytes(n_rows, vocab) : 0;
-}
-
 staple_status_t staple_xent_fwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                                 int32_t dtype, const int32_t* targets, float* loss, float* lse,
-                                const float* g, void* d_logits, int64_t d_stride, void* ws,
-                                size_t ws_bytes, void* stream) {
+                                const float* g, void* d_logits, int64_t d_stride, void* stream) {
   CHECKED(logits_check(n_rows, vocab, dtype, stride));
   REQUIRE((g == nullptr) == (d_logits == nullptr));
   if (n_rows == 0) return STAPLE_OK;
   REQUIRE(in_ok(logits, stride, dtype) && targets && loss && lse);
   REQUIRE(!d_logits || out_ok(d_logits, d_stride, n_rows, vocab, dtype));
-  const size_t need = xent_workspace_bytes(n_rows, vocab);
-  if (ws_bytes < need) return STAPLE_ERR_WORKSPACE;
-  REQUIRE(need == 0 || (ws && aligned16(ws)));
   GET_ERR(err);
   const XentView v{static_cast<const char*>(logits), stride, n_rows, static_cast<int>(vocab), targets,
                    loss, lse, g, static_cast<char*>(d_logits), d_stride};
-  HIPCALL(launch_xent_fwd(v, dtype, ws, S(stream), err));
+  HIPCALL(launch_xent_fwd(v, dtype, S(stream), err));
   return STAPLE_OK;
 }
 

@@ -7,7 +7,6 @@
 namespace staple {
 
 constexpr int kEmbedCols = 512;     // 64 lanes x 8 columns
-constexpr int kEmbedChunk = 32;     // sorted positions of one wave
 constexpr int kEmbedAhead = 8;      // rows in flight a lane
 
 // One wave writes U blocks of 512 columns of one token's row.
@@ -84,11 +83,25 @@ hipError_t launch_embed_fwd(const void* table, int64_t vocab, int64_t d, int32_t
 
 // ------------------------------------------------------------------------------- gradient
 // One token can hold a tenth of a batch, so the sorted positions, not the tokens, are dealt
-// out: a wave sums the runs of equal tokens within kEmbedChunk positions, for 512 columns.
+// out: a wave sums the runs of equal tokens within a chunk of positions, for 512 columns.
 // A run that is a whole token's goes to its row.  One that a chunk's border cuts goes to
 // first[chunk] (begun in an earlier chunk) or last[chunk] (goes on in the next), and the
-// second kernel adds last[c0], first[c0 + 1], ..., first[c1] in that order: the result does
-// not change from run to run.
+// second kernel adds last[c0], first[c0 + 1], ..., first[c1], eight waves an eighth of them each and
+// the eighths in turn: the order is fixed, and the result does not change from run to run.
+constexpr int kJoinWaves = 8;
+
+// Eight elements of a row whose columns past d repeat the last one: no branch around any load (the sums
+// of such columns are stored nowhere).
+template <bool VEC, typename E>
+__device__ __forceinline__ void load_row(const E* row, int g, int lane, int d, float (&v)[8]) {
+  using R = RowGroup<64, VEC>;
+  if (VEC) {
+    load8(row + min(R::column(g, lane, 0), d - 8), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = load1(row + min(R::column(g, lane, i), d - 1));
+  }
+}
 
 // Unique index of sorted position p, -1 where the maps are out of range.
 __device__ __forceinline__ int32_t unique_of(int64_t p, int64_t n, int64_t nu, const int32_t* sorted_pos,
@@ -125,25 +138,26 @@ __device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, in
   R::store(row, g, lane, d, acc);
 }
 
-template <typename E, bool VEC>
+template <typename E, bool VEC, int CHUNK>
 __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups, float* __restrict__ first,
                                                         float* __restrict__ last, int64_t ld, int* err) {
   using R = RowGroup<64, VEC>;
   const int lane = threadIdx.x & 63;
   const int64_t n = a.n_tokens;
-  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+  const int64_t chunks = (n + CHUNK - 1) / CHUNK;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (w >= chunks * groups) return;
-  const int64_t nu = *a.n_unique;
+  int64_t nu = *a.n_unique;
   if (nu < 0 || nu > a.max_unique) {
     if (lane == 0) flag_index_error(err);
     return;
   }
+  nu = nu < n ? nu : n;
   const int64_t c = w / groups;
   const int g = static_cast<int>(w - c * groups);
   const int d = static_cast<int>(a.d);
-  const int64_t p0 = c * kEmbedChunk;
-  const int len = static_cast<int>(n - p0 < kEmbedChunk ? n - p0 : kEmbedChunk);
+  const int64_t p0 = c * CHUNK;
+  const int len = static_cast<int>(n - p0 < CHUNK ? n - p0 : CHUNK);
   // lane i: position p0 + i; the lane after the last one and lane 63: the neighbours outside
   int32_t row = -1, u = -2;
   const int64_t p = lane == 63 ? p0 - 1 : p0 + lane;
@@ -160,13 +174,9 @@ __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups,
     float v[kEmbedAhead][8];
 #pragma unroll
     for (int j = 0; j < kEmbedAhead; ++j) {
-      const int32_t r = __shfl(row, b + j < len ? b + j : len - 1, 64);
-      if (r >= 0) {
-        R::load(reinterpret_cast<const E*>(a.dy.data) + r * a.dy.stride, g, lane, d, v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      }
+      const int32_t r = __builtin_amdgcn_readlane(row, b + j < len ? b + j : len - 1);
+      // a position out of range: row 0, in a run whose sum is stored nowhere
+      load_row<VEC>(reinterpret_cast<const E*>(a.dy.data) + (r >= 0 ? r : 0) * a.dy.stride, g, lane, d, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < kEmbedAhead; ++j) {
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups,
       } else if (!end) {
         R::store(last + c * ld, g, lane, d, acc);
       } else {
-        float* to = grad_row(a, __shfl(u, k, 64), lane, err);
+        float* to = grad_row(a, __builtin_amdgcn_readlane(u, k), lane, err);
         if (to) finish<VEC>(a, to, g, lane, acc);
       }
       first_run = false;
@@ -191,23 +201,23 @@ __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups,
   }
 }
 
-// The chunk in which a cut run begins adds its parts.
-template <bool VEC>
-__global__ __launch_bounds__(256) void embed_bwd_join_kernel(EmbedGrad a, int groups,
-                                                             const float* __restrict__ first,
-                                                             const float* __restrict__ last, int64_t ld,
-                                                             int* err) {
+// The chunk in which a cut run begins adds its parts: a workgroup a chunk and 512 columns.
+template <bool VEC, int CHUNK>
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGrad a, int groups,
+                                                                         const float* __restrict__ first,
+                                                                         const float* __restrict__ last, int64_t ld,
+                                                                         int* err) {
   using R = RowGroup<64, VEC>;
-  const int lane = threadIdx.x & 63;
+  __shared__ float part[kJoinWaves][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n = a.n_tokens;
-  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t nu = *a.n_unique;
-  if (w >= chunks * groups || nu < 0 || nu > a.max_unique) return;
-  const int64_t c = w / groups;
-  const int g = static_cast<int>(w - c * groups);
+  int64_t nu = *a.n_unique;
+  if (nu < 0 || nu > a.max_unique) return;   // flagged by the first kernel
+  nu = nu < n ? nu : n;
+  const int64_t c = blockIdx.x / groups;
+  const int g = static_cast<int>(blockIdx.x - c * groups);
   const int d = static_cast<int>(a.d);
-  const int64_t p0 = c * kEmbedChunk, p1 = p0 + kEmbedChunk;
+  const int64_t p0 = c * CHUNK, p1 = p0 + CHUNK;
   if (p1 >= n) return;
   int32_t row;
   const int32_t u = unique_of(p1 - 1, n, nu, a.sorted_pos, a.inv, row);
@@ -215,47 +225,73 @@ __global__ __launch_bounds__(256) void embed_bwd_join_kernel(EmbedGrad a, int gr
   const int64_t begin = a.seg_start[u], end = a.seg_start[u + 1];
   if (begin < p0) return;
   if (begin >= p1 || end <= p1 || end > n) {
-    if (lane == 0) flag_index_error(err);
+    if (threadIdx.x == 0) flag_index_error(err);
     return;
   }
-  const int64_t c1 = (end - 1) / kEmbedChunk;
-  float acc[8];
-  R::load(last + c * ld, g, lane, d, acc);
-  for (int64_t b = c + 1; b <= c1; b += kEmbedAhead) {
+  // part 0 is last[c], part k first[c + k]
+  const int64_t parts = (end - 1) / CHUNK - c + 1, each = (parts + kJoinWaves - 1) / kJoinWaves;
+  const int64_t k0 = wave * each, k1 = k0 + each < parts ? k0 + each : parts;
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t b = k0; b < k1; b += kEmbedAhead) {
     float v[kEmbedAhead][8];
 #pragma unroll
-    for (int j = 0; j < kEmbedAhead; ++j) R::load(first + (b + j <= c1 ? b + j : c1) * ld, g, lane, d, v[j]);
+    for (int j = 0; j < kEmbedAhead; ++j) {
+      const int64_t k = b + j < k1 ? b + j : k1 - 1;
+      load_row<VEC>(k == 0 ? last + c * ld : first + (c + k) * ld, g, lane, d, v[j]);
+    }
 #pragma unroll
     for (int j = 0; j < kEmbedAhead; ++j)
-      if (b + j <= c1) {
+      if (b + j < k1) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
       }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[wave][i * 64 + lane] = acc[i];
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += part[k][i * 64 + lane];
   float* to = grad_row(a, u, lane, err);
   if (to) finish<VEC>(a, to, g, lane, acc);
 }
 
 static int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
 
+// Positions of a chunk: 32, or 8 where those make too few waves to hide their loads behind.
+static int chunk_of(int64_t n, int64_t d) {
+  const int64_t groups = (d + kEmbedCols - 1) / kEmbedCols;
+  return n / 32 * groups >= 16 * 256 ? 32 : 8;
+}
+
 size_t embed_bwd_workspace_bytes(int64_t n, int64_t d) {
-  const int64_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+  const int64_t chunk = chunk_of(n, d), chunks = (n + chunk - 1) / chunk;
   return chunks > 1 ? static_cast<size_t>(2 * chunks * part_stride(d)) * sizeof(float) : 0;
+}
+
+template <typename E, bool VEC, int CHUNK>
+static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
+  const int64_t chunks = (a.n_tokens + CHUNK - 1) / CHUNK, ld = part_stride(a.d);
+  float* first = static_cast<float*>(ws);
+  float* last = first + chunks * ld;
+  const int groups = static_cast<int>((a.d + kEmbedCols - 1) / kEmbedCols);
+  embed_bwd_kernel<E, VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks * groups + 3) / 4)), dim3(256), 0, s>>>(
+      a, groups, first, last, ld, err);
+  if (chunks > 1)
+    embed_bwd_join_kernel<VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks - 1) * groups)), dim3(64 * kJoinWaves), 0, s>>>(
+        a, groups, first, last, ld, err);
 }
 
 template <typename E>
 static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
-  const int64_t chunks = (a.n_tokens + kEmbedChunk - 1) / kEmbedChunk, ld = part_stride(a.d);
-  float* first = static_cast<float*>(ws);
-  float* last = first + chunks * ld;
-  const int groups = static_cast<int>((a.d + kEmbedCols - 1) / kEmbedCols);
   const bool vec = a.d % 8 == 0 && vec_rows(a.dy.data, a.dy.stride, sizeof(E)) && vec_rows(a.grad, a.d, 4);
-  const dim3 grid(static_cast<unsigned>((chunks * groups + 3) / 4));
-  if (vec) embed_bwd_kernel<E, true><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
-  else embed_bwd_kernel<E, false><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
-  if (chunks == 1) return;
-  if (vec) embed_bwd_join_kernel<true><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
-  else embed_bwd_join_kernel<false><<<grid, dim3(256), 0, s>>>(a, groups, first, last, ld, err);
+  if (chunk_of(a.n_tokens, a.d) == 32) {
+    if (vec) embed_bwd<E, true, 32>(a, ws, s, err); else embed_bwd<E, false, 32>(a, ws, s, err);
+  } else {
+    if (vec) embed_bwd<E, true, 8>(a, ws, s, err); else embed_bwd<E, false, 8>(a, ws, s, err);
+  }
 }
 
 hipError_t launch_embed_bwd(const EmbedGrad& a, int32_t dtype, void* ws, hipStream_t s, int* err) {

@@ -65,8 +65,7 @@ struct XentView {
   char* d_logits;
   int64_t d_stride;
 };
-size_t xent_workspace_bytes(int64_t n_rows, int64_t vocab);
-hipError_t launch_xent_fwd(const XentView& v, int32_t dtype, void* ws, hipStream_t s, int* err);
+hipError_t launch_xent_fwd(const XentView& v, int32_t dtype, hipStream_t s, int* err);
 hipError_t launch_xent_bwd(const XentView& v, int32_t dtype, hipStream_t s, int* err);
 
 struct SampleView {

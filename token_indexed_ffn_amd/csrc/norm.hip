@@ -98,8 +98,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a)
   }
 }
 
-// Workgroups work off rows in turn and keep the sums over their rows in registers; parts:
-// [vectors][slots of all workgroups][d], added up by norm_columns_kernel in slot order.
+// What the backward reads of a row.
+template <typename X, typename Z, int T, int G, bool VEC>
+struct NormRow {
+  Ahead<X, T, VEC> dr[G], r[G];   // r: the stored sum, or x
+  Ahead<Z, T, VEC> dh[G], z[G], gate[G];
+  float rstd_r, rstd_z;
+  __device__ __forceinline__ void load(const NormView& a, int64_t i, int t, bool need_z) {
+    const RowsView& sum = a.r.data ? a.r : a.x;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (a.dr.data) dr[g].load(row_of<const X>(a.dr, i), g, t, a.d);
+      if (a.pre) {
+        if (sum.data) r[g].load(row_of<const X>(sum, i), g, t, a.d);
+        dh[g].load(row_of<const Z>(a.dh, i), g, t, a.d);
+      }
+      if (need_z) z[g].load(row_of<const Z>(a.z, i), g, t, a.d);
+      if (a.gate_kind == Gate::kRows) gate[g].load(row_of<const Z>(a.gate, i), g, t, a.d);
+    }
+    rstd_r = a.pre ? a.rstd_r[i] : 0.0f;
+    rstd_z = a.post ? a.rstd_z[i] : 1.0f;
+  }
+};
+
+// Workgroups work off rows in turn, the next row's loads in flight, and keep the sums over their rows in
+// registers; parts: [vectors][slots of all workgroups][d], added up by norm_columns_kernel in slot order.
 template <typename X, typename Z, int T, int G, bool VEC>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a, float* parts) {
   using R = RowGroup<T, VEC>;
@@ -111,51 +134,54 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
   const float inv_d = 1.0f / static_cast<float>(d);
   const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  const bool branch = norm_bwd_branch(a), need_z = norm_bwd_reads_z(a);
   float sum_pre[G][8], sum_post[G][8], sum_gate[G][8];
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum_pre[g][k] = sum_post[g][k] = sum_gate[g][k] = 0.0f;
-  const bool branch = norm_bwd_branch(a);
-  const bool need_z = norm_bwd_reads_z(a);
+  NormRow<X, Z, T, G, VEC> next;
+  if (me < a.n_rows) next.load(a, me, t, need_z);
   int odd = 0;
   for (int64_t i = me; i < a.n_rows; i += slots, odd ^= 1) {
+    const NormRow<X, Z, T, G, VEC> row = next;
+    if (i + slots < a.n_rows) next.load(a, i + slots, t, need_z);
     float q[G][8], hat_z[G][8], gate[G][8], w[8];
-    const float inv_z = a.post ? a.rstd_z[i] : 1.0f;
+    const float inv_z = row.rstd_z;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       if (a.dr.data) {
-        R::load(row_of<const X>(a.dr, i), g, t, d, q[g]);
+        row.dr[g].get(q[g]);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[g][k] = 0.0f;
       }
       if (need_z) {
-        R::load(row_of<const Z>(a.z, i), g, t, d, hat_z[g]);
+        row.z[g].get(hat_z[g]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) hat_z[g][k] *= inv_z;
       }
-      if (a.gate_kind == Gate::kRows) R::load(row_of<const Z>(a.gate, i), g, t, d, gate[g]);
+      if (a.gate_kind == Gate::kRows) row.gate[g].get(gate[g]);
       else load_shared<T, VEC>(a.gate.data, a.w_bf16, g, t, d, gate[g]);
     }
     if (a.pre) {
-      const float inv = a.rstd_r[i];
+      const float inv = row.rstd_r;
       float hat[G][8], dt[G][8], dot = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         if (a.r.data) {
-          R::load(row_of<const X>(a.r, i), g, t, d, hat[g]);
+          row.r[g].get(hat[g]);
         } else {   // as the forward had it before r was rounded
           load_shared<T, VEC>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w);
 #pragma unroll
           for (int k = 0; k < 8; ++k) hat[g][k] = a.scale * gate[g][k] * w[k] * hat_z[g][k];
           if (a.x.data) {
-            R::load(row_of<const X>(a.x, i), g, t, d, w);
+            row.r[g].get(w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) hat[g][k] += w[k];
           }
         }
-        R::load(row_of<const Z>(a.dh, i), g, t, d, dt[g]);
+        row.dh[g].get(dt[g]);
         load_shared<T, VEC>(a.w_pre, a.w_bf16, g, t, d, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -233,21 +259,30 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
   }
 }
 
-// Sums of the parts, 64 columns a workgroup: wave k adds slots k, k + 16, ..., then the waves' sums.
+// Sums of the parts, 16 columns a workgroup: 64 of its lanes a column, which add slots k, k + 64, ... and
+// are then added up in turn.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ parts, int slots, int d,
                                                             float* o0, float* o1, float* o2) {
-  __shared__ float tmp[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
-  const float* p = parts + static_cast<int64_t>(blockIdx.y) * slots * d;
+  constexpr int kAhead = 8;
+  __shared__ float tmp[64][16];
+  const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
+  const int col = min(static_cast<int>(blockIdx.x) * 16 + c, d - 1);
+  const float* p = parts + static_cast<int64_t>(blockIdx.y) * slots * d + col;
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   float s = 0.0f;
-  if (col < d)
-    for (int i = wave; i < slots; i += 16) s += p[static_cast<int64_t>(i) * d + col];
-  tmp[wave][lane] = s;
+  for (int i = k0; i < slots; i += 64 * kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = i + 64 * u < slots ? p[static_cast<int64_t>(i + 64 * u) * d] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) s += v[u];
+  }
+  tmp[k0][c] = s;
   __syncthreads();
-  if (wave != 0 || col >= d) return;
-  for (int k = 1; k < 16; ++k) s += tmp[k][lane];
+  if (threadIdx.x >= 16 || static_cast<int>(blockIdx.x) * 16 + c >= d) return;
+  s = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < 64; ++k) s += tmp[k][c];
   out[col] = s;
 }
 
@@ -315,7 +350,7 @@ static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
   int k = 0;
   for (float* p : {v.dw_pre, v.dw_post, v.dgate_sum})
     if (p) out[k++] = p;
-  norm_columns_kernel<<<dim3((v.d + 63) / 64, n), dim3(1024), 0, s>>>(
+  norm_columns_kernel<<<dim3((v.d + 15) / 16, n), dim3(1024), 0, s>>>(
       parts, static_cast<int>(grid.x) * norm_rows_a_workgroup(v.d), v.d, out[0], out[1], out[2]);
 }
 

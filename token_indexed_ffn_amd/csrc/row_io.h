@@ -45,6 +45,7 @@ template <> struct Raw<bf16_t> {
   u32x4_t a;
   __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
   __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
+  __device__ __forceinline__ void zero() { a = u32x4_t{0, 0, 0, 0}; }
   // What was made of these elements is made again after this, rather than kept in registers.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -65,6 +66,7 @@ template <> struct Raw<float> {
     const float x = -__builtin_inff();
     a = b = f32x4_t{x, x, x, x};
   }
+  __device__ __forceinline__ void zero() { a = b = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a), "+v"(b)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -130,15 +132,57 @@ struct RowGroup {
   }
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
+// A lane's eight elements of a row, loaded ahead of their use: as they lie in memory where they are aligned.
+template <typename E, int T, bool VEC>
+struct Ahead {
+  Raw<E> raw;
+  __device__ __forceinline__ void load(const E* row, int g, int t, int d) {
+    const int j = RowGroup<T, true>::column(g, t, 0);
+    if (j < d) raw.load(row + j);
+    else raw.zero();
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { raw.get(v); }
+};
+template <typename E, int T>
+struct Ahead<E, T, false> {
+  float v8[8];
+  __device__ __forceinline__ void load(const E* row, int g, int t, int d) { RowGroup<T, false>::load(row, g, t, d, v8); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+    for (int i = 0; i < 8; ++i) v[i] = v8[i];
+  }
+};
+
+// v of the lane that a DPP control names; `none` where there is none or the row is masked out.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ float from_lane(float v, float none) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(none), __float_as_uint(v), CONTROL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+
+// Over a wave's lanes, in a fixed order: shifts by 1, 2, 4, 8 within rows of 16 lanes, a row's last lane
+// to the next row, lane 31 to the upper half, and lane 63, which then has all, to every lane.  (In registers:
+// a shuffle through LDS takes some hundred cycles a step.)
+__device__ __forceinline__ float wave_sum(float v) {
+  v += from_lane<0x111, 0xf>(v, 0.0f);
+  v += from_lane<0x112, 0xf>(v, 0.0f);
+  v += from_lane<0x114, 0xf>(v, 0.0f);
+  v += from_lane<0x118, 0xf>(v, 0.0f);
+  v += from_lane<0x142, 0xa>(v, 0.0f);
+  v += from_lane<0x143, 0xc>(v, 0.0f);
+  return last_lane(v);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  const float none = -__builtin_inff();
+  v = fmaxf(v, from_lane<0x111, 0xf>(v, none));
+  v = fmaxf(v, from_lane<0x112, 0xf>(v, none));
+  v = fmaxf(v, from_lane<0x114, 0xf>(v, none));
+  v = fmaxf(v, from_lane<0x118, 0xf>(v, none));
+  v = fmaxf(v, from_lane<0x142, 0xa>(v, none));
+  v = fmaxf(v, from_lane<0x143, 0xc>(v, none));
+  return last_lane(v);
 }
 
 // Sum over the T lanes that share a row.  tmp: T / 64 floats of LDS that no wave still
