@@ -86,8 +86,8 @@ hipError_t launch_embed_fwd(const void* table, int64_t vocab, int64_t d, int32_t
 // out: a wave sums the runs of equal tokens within a chunk of positions, for 512 columns.
 // A run that is a whole token's goes to its row.  One that a chunk's border cuts goes to
 // first[chunk] (begun in an earlier chunk) or last[chunk] (goes on in the next), and the
-// second kernel adds last[c0], first[c0 + 1], ..., first[c1], eight waves an eighth of them each and
-// the eighths in turn: the order is fixed, and the result does not change from run to run.
+// second kernel adds last[c0], first[c0 + 1], ..., first[c1], where they are many eight waves an eighth of
+// them each and the eighths in turn: the order is fixed, and the result does not change from run to run.
 constexpr int kJoinWaves = 8;
 
 // Eight elements of a row whose columns past d repeat the last one: no branch around any load (the sums
@@ -201,37 +201,10 @@ __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups,
   }
 }
 
-// The chunk in which a cut run begins adds its parts: a workgroup a chunk and 512 columns.
-template <bool VEC, int CHUNK>
-__global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGrad a, int groups,
-                                                                         const float* __restrict__ first,
-                                                                         const float* __restrict__ last, int64_t ld,
-                                                                         int* err) {
-  using R = RowGroup<64, VEC>;
-  __shared__ float part[kJoinWaves][512];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = a.n_tokens;
-  int64_t nu = *a.n_unique;
-  if (nu < 0 || nu > a.max_unique) return;   // flagged by the first kernel
-  nu = nu < n ? nu : n;
-  const int64_t c = blockIdx.x / groups;
-  const int g = static_cast<int>(blockIdx.x - c * groups);
-  const int d = static_cast<int>(a.d);
-  const int64_t p0 = c * CHUNK, p1 = p0 + CHUNK;
-  if (p1 >= n) return;
-  int32_t row;
-  const int32_t u = unique_of(p1 - 1, n, nu, a.sorted_pos, a.inv, row);
-  if (u < 0 || unique_of(p1, n, nu, a.sorted_pos, a.inv, row) != u) return;
-  const int64_t begin = a.seg_start[u], end = a.seg_start[u + 1];
-  if (begin < p0) return;
-  if (begin >= p1 || end <= p1 || end > n) {
-    if (threadIdx.x == 0) flag_index_error(err);
-    return;
-  }
-  // part 0 is last[c], part k first[c + k]
-  const int64_t parts = (end - 1) / CHUNK - c + 1, each = (parts + kJoinWaves - 1) / kJoinWaves;
-  const int64_t k0 = wave * each, k1 = k0 + each < parts ? k0 + each : parts;
-  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+// The chunk in which a cut run begins adds its parts: part 0 is last[c], part k first[c + k].
+template <bool VEC>
+__device__ __forceinline__ void add_parts(const float* first, const float* last, int64_t ld, int64_t c, int64_t k0,
+                                          int64_t k1, int g, int lane, int d, float (&acc)[8]) {
   for (int64_t b = k0; b < k1; b += kEmbedAhead) {
     float v[kEmbedAhead][8];
 #pragma unroll
@@ -246,16 +219,73 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
         for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
       }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[wave][i * 64 + lane] = acc[i];
+}
+
+// A wave looks at one chunk (for 512 columns) and adds up to kEmbedAhead parts itself; runs of more are
+// added by the whole workgroup.
+template <bool VEC, int CHUNK>
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGrad a, int groups,
+                                                                         const float* __restrict__ first,
+                                                                         const float* __restrict__ last, int64_t ld,
+                                                                         int* err) {
+  __shared__ float part[kJoinWaves][512];
+  __shared__ int64_t long_parts[kJoinWaves];
+  __shared__ int32_t long_token[kJoinWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = a.n_tokens;
+  int64_t nu = *a.n_unique;
+  if (nu < 0 || nu > a.max_unique) return;   // flagged by the first kernel
+  nu = nu < n ? nu : n;
+  const int64_t c0 = blockIdx.x / groups * kJoinWaves, c = c0 + wave;
+  const int g = static_cast<int>(blockIdx.x % groups);
+  const int d = static_cast<int>(a.d);
+  const int64_t p0 = c * CHUNK, p1 = p0 + CHUNK;
+  int64_t parts = 0;
+  int32_t u = -1;
+  if (p1 < n) {
+    int32_t row;
+    u = unique_of(p1 - 1, n, nu, a.sorted_pos, a.inv, row);
+    const int32_t after = unique_of(p1, n, nu, a.sorted_pos, a.inv, row);
+    if (u >= 0 && after == u) {
+      const int64_t begin = a.seg_start[u], end = a.seg_start[u + 1];
+      if (begin >= p1 || end <= p1 || end > n) {
+        if (lane == 0) flag_index_error(err);
+      } else if (begin >= p0) {
+        parts = (end - 1) / CHUNK - c + 1;
+      }
+    }
+  }
+  if (lane == 0) {
+    long_parts[wave] = parts > kEmbedAhead ? parts : 0;
+    long_token[wave] = u;
+  }
+  if (parts > 0 && parts <= kEmbedAhead) {
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    add_parts<VEC>(first, last, ld, c, 0, parts, g, lane, d, acc);
+    float* to = grad_row(a, u, lane, err);
+    if (to) finish<VEC>(a, to, g, lane, acc);
+  }
   __syncthreads();
-  if (wave != 0) return;
+  for (int w = 0; w < kJoinWaves; ++w) {
+    const int64_t all = long_parts[w];
+    if (all == 0) continue;
+    const int64_t each = (all + kJoinWaves - 1) / kJoinWaves;
+    const int64_t k0 = wave * each, k1 = k0 + each < all ? k0 + each : all;
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    add_parts<VEC>(first, last, ld, c0 + w, k0, k1, g, lane, d, acc);
 #pragma unroll
-  for (int k = 1; k < kJoinWaves; ++k)
+    for (int i = 0; i < 8; ++i) part[wave][i * 64 + lane] = acc[i];
+    __syncthreads();
+    if (wave == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += part[k][i * 64 + lane];
-  float* to = grad_row(a, u, lane, err);
-  if (to) finish<VEC>(a, to, g, lane, acc);
+      for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += part[k][i * 64 + lane];
+      float* to = grad_row(a, long_token[w], lane, err);
+      if (to) finish<VEC>(a, to, g, lane, acc);
+    }
+    __syncthreads();
+  }
 }
 
 static int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
@@ -280,7 +310,7 @@ static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
   embed_bwd_kernel<E, VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks * groups + 3) / 4)), dim3(256), 0, s>>>(
       a, groups, first, last, ld, err);
   if (chunks > 1)
-    embed_bwd_join_kernel<VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks - 1) * groups)), dim3(64 * kJoinWaves), 0, s>>>(
+    embed_bwd_join_kernel<VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks + kJoinWaves - 1) / kJoinWaves * groups)), dim3(64 * kJoinWaves), 0, s>>>(
         a, groups, first, last, ld, err);
 }
 

@@ -98,11 +98,71 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a)
   }
 }
 
+// V (4 or 8) elements of a row that a lane of the backward holds of group g, as they lie in memory where
+// they are aligned (VEC): elements (g T + t) V on, otherwise (g V + i) T + t.
+template <typename E, int T, bool VEC, int V>
+struct Part {
+  static constexpr int kWords = VEC ? V * static_cast<int>(sizeof(E)) / 4 : V;
+  typedef __attribute__((ext_vector_type(kWords))) uint32_t words_t;
+  words_t w;
+  __device__ __forceinline__ static int column(int g, int t, int i) { return VEC ? (g * T + t) * V + i : (g * V + i) * T + t; }
+  __device__ __forceinline__ void load(const E* row, int g, int t, int d) {
+    if (VEC) {
+      w = *reinterpret_cast<const words_t*>(row + min(column(g, t, 0), d - V));   // lanes past the end: the last ones again
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(load1(row + min(column(g, t, i), d - 1)));
+    }
+  }
+  // 0 past the row's end.
+  __device__ __forceinline__ void get(float (&v)[V], int g, int t, int d) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (VEC && sizeof(E) == 2) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      else v[i] = __uint_as_float(w[i]);
+      if (column(g, t, i) >= d) v[i] = 0.0f;
+    }
+  }
+  __device__ __forceinline__ static void store(E* row, int g, int t, int d, const float (&v)[V]) {
+    if (VEC) {
+      if (column(g, t, 0) >= d) return;
+      words_t x;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if (sizeof(E) == 2) x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        else x[i] = __float_as_uint(v[i]);
+      }
+      *reinterpret_cast<words_t*>(row + column(g, t, 0)) = x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (column(g, t, i) < d) store1(row + column(g, t, i), v[i]);
+    }
+  }
+};
+
+// A vector shared by the rows: ones when NULL.
+template <int T, bool VEC, int V>
+__device__ __forceinline__ void load_vector(const void* p, bool bf16, int g, int t, int d, float (&v)[V]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 1.0f;
+  } else if (bf16) {
+    Part<bf16_t, T, VEC, V> x;
+    x.load(static_cast<const bf16_t*>(p), g, t, d);
+    x.get(v, g, t, d);
+  } else {
+    Part<float, T, VEC, V> x;
+    x.load(static_cast<const float*>(p), g, t, d);
+    x.get(v, g, t, d);
+  }
+}
+
 // What the backward reads of a row.
-template <typename X, typename Z, int T, int G, bool VEC>
+template <typename X, typename Z, int T, int G, bool VEC, int V>
 struct NormRow {
-  Ahead<X, T, VEC> dr[G], r[G];   // r: the stored sum, or x
-  Ahead<Z, T, VEC> dh[G], z[G], gate[G];
+  Part<X, T, VEC, V> dr[G], r[G];   // r: the stored sum, or x
+  Part<Z, T, VEC, V> dh[G], z[G], gate[G];
   float rstd_r, rstd_z;
   __device__ __forceinline__ void load(const NormView& a, int64_t i, int t, bool need_z) {
     const RowsView& sum = a.r.data ? a.r : a.x;
@@ -121,12 +181,16 @@ struct NormRow {
   }
 };
 
-// Workgroups work off rows in turn, the next row's loads in flight, and keep the sums over their rows in
-// registers; parts: [vectors][slots of all workgroups][d], added up by norm_columns_kernel in slot order.
-template <typename X, typename Z, int T, int G, bool VEC>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a, float* parts) {
-  using R = RowGroup<T, VEC>;
+// Waves a SIMD that the backward is held to the registers of; its grid fills the GPU with them once.
+constexpr int norm_bwd_waves(int lanes, int v) { return lanes >= 512 ? 4 : v == 4 ? 5 : 3; }
+
+// Workgroups work off rows in turn, the next row's loads in flight, and keep the sums over their rows, and
+// the weights, in registers; parts: [vectors][slots of all workgroups][d], added up by norm_columns_kernel in
+// slot order.
+template <typename X, typename Z, int T, int G, bool VEC, int V>
+__global__ __launch_bounds__(T < 256 ? 256 : T, norm_bwd_waves(T, V)) void norm_bwd_kernel(NormView a, float* parts) {
   constexpr int kRows = T < 256 ? 256 / T : 1;
+  constexpr bool kKept = G == 1;   // the weights
   // two sums a row, in buffers of their own for rows in turn: between a sum's reads and the
   // next writes to its buffer stands the barrier of the row between
   __shared__ float tmp[2][2][kRows][T / 64];
@@ -135,59 +199,59 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
   const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kRows + slot;
   const bool branch = norm_bwd_branch(a), need_z = norm_bwd_reads_z(a);
-  float sum_pre[G][8], sum_post[G][8], sum_gate[G][8];
+  const bool rows_gate = a.gate_kind == Gate::kRows;
+  float sum_pre[G][V], sum_post[G][V], sum_gate[G][V], w_pre[G][V], w_post[G][V], gate[G][V];
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum_pre[g][k] = sum_post[g][k] = sum_gate[g][k] = 0.0f;
-  NormRow<X, Z, T, G, VEC> next;
+    for (int k = 0; k < V; ++k) sum_pre[g][k] = sum_post[g][k] = sum_gate[g][k] = 0.0f;
+    if (kKept) {
+      load_vector<T, VEC, V>(a.w_pre, a.w_bf16, g, t, d, w_pre[g]);
+      load_vector<T, VEC, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post[g]);
+      load_vector<T, VEC, V>(rows_gate ? nullptr : a.gate.data, a.w_bf16, g, t, d, gate[g]);
+    }
+  }
+  NormRow<X, Z, T, G, VEC, V> next;
   if (me < a.n_rows) next.load(a, me, t, need_z);
   int odd = 0;
   for (int64_t i = me; i < a.n_rows; i += slots, odd ^= 1) {
-    const NormRow<X, Z, T, G, VEC> row = next;
+    const NormRow<X, Z, T, G, VEC, V> row = next;
     if (i + slots < a.n_rows) next.load(a, i + slots, t, need_z);
-    float q[G][8], hat_z[G][8], gate[G][8], w[8];
+    float q[G][V], hat_z[G][V];
     const float inv_z = row.rstd_z;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      if (a.dr.data) {
-        row.dr[g].get(q[g]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[g][k] = 0.0f;
-      }
       if (need_z) {
-        row.z[g].get(hat_z[g]);
+        row.z[g].get(hat_z[g], g, t, d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) hat_z[g][k] *= inv_z;
+        for (int k = 0; k < V; ++k) hat_z[g][k] *= inv_z;
       }
-      if (a.gate_kind == Gate::kRows) row.gate[g].get(gate[g]);
-      else load_shared<T, VEC>(a.gate.data, a.w_bf16, g, t, d, gate[g]);
+      if (rows_gate) row.gate[g].get(gate[g], g, t, d);
+      else if (!kKept) load_vector<T, VEC, V>(a.gate.data, a.w_bf16, g, t, d, gate[g]);
+      if (!kKept) load_vector<T, VEC, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post[g]);
     }
     if (a.pre) {
       const float inv = row.rstd_r;
-      float hat[G][8], dt[G][8], dot = 0.0f;
+      float hat[G][V], dt[G][V], dot = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         if (a.r.data) {
-          row.r[g].get(hat[g]);
+          row.r[g].get(hat[g], g, t, d);
         } else {   // as the forward had it before r was rounded
-          load_shared<T, VEC>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w);
+          float x[V];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) hat[g][k] = a.scale * gate[g][k] * w[k] * hat_z[g][k];
-          if (a.x.data) {
-            row.r[g].get(w);
+          for (int k = 0; k < V; ++k) x[k] = 0.0f;
+          if (a.x.data) row.r[g].get(x, g, t, d);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) hat[g][k] += w[k];
-          }
+          for (int k = 0; k < V; ++k) hat[g][k] = x[k] + a.scale * gate[g][k] * w_post[g][k] * hat_z[g][k];
         }
-        row.dh[g].get(dt[g]);
-        load_shared<T, VEC>(a.w_pre, a.w_bf16, g, t, d, w);
+        row.dh[g].get(dt[g], g, t, d);
+        if (!kKept) load_vector<T, VEC, V>(a.w_pre, a.w_bf16, g, t, d, w_pre[g]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < V; ++k) {
           hat[g][k] *= inv;
           sum_pre[g][k] += dt[g][k] * hat[g][k];
-          dt[g][k] *= w[k];
+          dt[g][k] *= w_pre[g][k];
           dot += dt[g][k] * hat[g][k];
         }
       }
@@ -195,37 +259,47 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[g][k] += inv * (dt[g][k] - hat[g][k] * mean);
-    }
-    if (a.dx.data) {
+        for (int k = 0; k < V; ++k) q[g][k] = inv * (dt[g][k] - hat[g][k] * mean);
+    } else {
 #pragma unroll
-      for (int g = 0; g < G; ++g) R::store(row_of<X>(a.dx, i), g, t, d, q[g]);
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < V; ++k) q[g][k] = 0.0f;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (a.dr.data) {
+        float v[V];
+        row.dr[g].get(v, g, t, d);
+#pragma unroll
+        for (int k = 0; k < V; ++k) q[g][k] += v[k];
+      }
+      if (a.dx.data) Part<X, T, VEC, V>::store(row_of<X>(a.dx, i), g, t, d, q[g]);
     }
     if (!branch) continue;
     float dot = 0.0f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      load_shared<T, VEC>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[g][k] *= a.scale;
+      for (int k = 0; k < V; ++k) q[g][k] *= a.scale;
       if (a.gate_kind != Gate::kNone) {
         if (a.dgate.data || a.dgate_sum) {
-          float dg[8];
+          float dg[V];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            dg[k] = q[g][k] * hat_z[g][k] * w[k];
+          for (int k = 0; k < V; ++k) {
+            dg[k] = q[g][k] * hat_z[g][k] * w_post[g][k];
             sum_gate[g][k] += dg[k];
           }
-          if (a.dgate.data) R::store(row_of<Z>(a.dgate, i), g, t, d, dg);
+          if (a.dgate.data) Part<Z, T, VEC, V>::store(row_of<Z>(a.dgate, i), g, t, d, dg);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[g][k] *= gate[g][k];
+        for (int k = 0; k < V; ++k) q[g][k] *= gate[g][k];
       }
       if (a.post) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < V; ++k) {
           sum_post[g][k] += q[g][k] * hat_z[g][k];
-          q[g][k] *= w[k];
+          q[g][k] *= w_post[g][k];
           dot += q[g][k] * hat_z[g][k];
         }
       }
@@ -235,11 +309,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[g][k] = inv_z * (q[g][k] - hat_z[g][k] * mean);
+        for (int k = 0; k < V; ++k) q[g][k] = inv_z * (q[g][k] - hat_z[g][k] * mean);
     }
     if (a.dz.data) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) R::store(row_of<Z>(a.dz, i), g, t, d, q[g]);
+      for (int g = 0; g < G; ++g) Part<Z, T, VEC, V>::store(row_of<Z>(a.dz, i), g, t, d, q[g]);
     }
   }
   float* part = parts + me * d;
@@ -248,14 +322,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormView a,
   for (int g = 0; g < G; ++g) {
     float* p = part;
     if (a.dw_pre) {
-      R::store(p, g, t, d, sum_pre[g]);
+      Part<float, T, VEC, V>::store(p, g, t, d, sum_pre[g]);
       p += one;
     }
     if (a.dw_post) {
-      R::store(p, g, t, d, sum_post[g]);
+      Part<float, T, VEC, V>::store(p, g, t, d, sum_post[g]);
       p += one;
     }
-    if (a.dgate_sum) R::store(p, g, t, d, sum_gate[g]);
+    if (a.dgate_sum) Part<float, T, VEC, V>::store(p, g, t, d, sum_gate[g]);
   }
 }
 
@@ -310,6 +384,33 @@ static bool norm_vec(const NormView& v, int32_t r_dtype, int32_t dtype) {
     else GO(1024, 2);                            \
   } while (0)
 
+// The backward's, with elements a group: its sums, weights and loads in flight are some 20 registers an
+// element.
+#define NORM_BWD_SHAPES(GO)                      \
+  do {                                           \
+    if (v.d <= 256) GO(64, 1, 4);                \
+    else if (v.d <= 512) GO(64, 1, 8);           \
+    else if (v.d <= 1024) GO(256, 1, 4);         \
+    else if (v.d <= 2048) GO(512, 1, 4);         \
+    else if (v.d <= 4096) GO(1024, 1, 4);        \
+    else if (v.d <= 8192) GO(1024, 1, 8);        \
+    else GO(1024, 2, 8);                         \
+  } while (0)
+struct NormBwdShape {
+  int lanes, groups, elements;
+  int rows() const { return lanes < 256 ? 256 / lanes : 1; }                 // of a workgroup
+  int64_t workgroups() const {                                               // that fill the GPU
+    const int waves = (lanes < 256 ? 256 : lanes) / 64;
+    const int a_cu = norm_bwd_waves(lanes, elements) * 4 / waves;
+    return static_cast<int64_t>(device_cus()) * (a_cu > 0 ? a_cu : 1);
+  }
+};
+static NormBwdShape norm_bwd_shape(const NormView& v) {
+#define GO(T, G, V) return NormBwdShape{T, G, V}
+  NORM_BWD_SHAPES(GO);
+#undef GO
+}
+
 static int norm_rows_a_workgroup(int d) { return d <= 1024 ? 4 : 1; }
 
 template <typename X, typename Z, bool VEC>
@@ -326,22 +427,21 @@ static int norm_vectors(const NormView& v) {
 }
 
 static int64_t norm_bwd_grid(const NormView& v) {
-  const int rows = norm_rows_a_workgroup(v.d);
-  const int64_t all = (v.n_rows + rows - 1) / rows;
-  const int64_t most = static_cast<int64_t>(device_cus()) * (v.d <= 4096 ? 4 : v.d <= 8192 ? 2 : 1);
+  const NormBwdShape shape = norm_bwd_shape(v);
+  const int64_t all = (v.n_rows + shape.rows() - 1) / shape.rows(), most = shape.workgroups();
   return all < most ? all : most;
 }
 
 size_t norm_bwd_workspace_bytes(const NormView& v) {
-  return static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * norm_rows_a_workgroup(v.d) * v.d * sizeof(float);
+  return static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * norm_bwd_shape(v).rows() * v.d * sizeof(float);
 }
 
 template <typename X, typename Z, bool VEC>
 static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(norm_bwd_grid(v)));
   if (v.n_rows > 0) {
-#define GO(T, G) norm_bwd_kernel<X, Z, T, G, VEC><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v, parts)
-    NORM_SHAPES(GO);
+#define GO(T, G, V) norm_bwd_kernel<X, Z, T, G, VEC, V><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v, parts)
+    NORM_BWD_SHAPES(GO);
 #undef GO
   }
   const int n = norm_vectors(v);
@@ -351,7 +451,7 @@ static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
   for (float* p : {v.dw_pre, v.dw_post, v.dgate_sum})
     if (p) out[k++] = p;
   norm_columns_kernel<<<dim3((v.d + 15) / 16, n), dim3(1024), 0, s>>>(
-      parts, static_cast<int>(grid.x) * norm_rows_a_workgroup(v.d), v.d, out[0], out[1], out[2]);
+      parts, static_cast<int>(grid.x) * norm_bwd_shape(v).rows(), v.d, out[0], out[1], out[2]);
 }
 
 #define NORM_TYPES(CALL)                                                         \

@@ -45,7 +45,6 @@ template <> struct Raw<bf16_t> {
   u32x4_t a;
   __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
   __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
-  __device__ __forceinline__ void zero() { a = u32x4_t{0, 0, 0, 0}; }
   // What was made of these elements is made again after this, rather than kept in registers.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -66,7 +65,6 @@ template <> struct Raw<float> {
     const float x = -__builtin_inff();
     a = b = f32x4_t{x, x, x, x};
   }
-  __device__ __forceinline__ void zero() { a = b = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a), "+v"(b)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -129,27 +127,6 @@ struct RowGroup {
       for (int i = 0; i < 8; ++i)
         if (column(g, t, i) < d) store1(row + column(g, t, i), v[i]);
     }
-  }
-};
-
-// A lane's eight elements of a row, loaded ahead of their use: as they lie in memory where they are aligned.
-template <typename E, int T, bool VEC>
-struct Ahead {
-  Raw<E> raw;
-  __device__ __forceinline__ void load(const E* row, int g, int t, int d) {
-    const int j = RowGroup<T, true>::column(g, t, 0);
-    if (j < d) raw.load(row + j);
-    else raw.zero();
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const { raw.get(v); }
-};
-template <typename E, int T>
-struct Ahead<E, T, false> {
-  float v8[8];
-  __device__ __forceinline__ void load(const E* row, int g, int t, int d) { RowGroup<T, false>::load(row, g, t, d, v8); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v8[i];
   }
 };
 
