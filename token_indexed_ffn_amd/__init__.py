@@ -1115,32 +1115,37 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
 _NO_ROWS = (None, 0)
 
 
-def _elsewhere(t: torch.Tensor) -> bool:
-    return not t.is_cuda or t.get_device() != _current_device()
+def _on(t: torch.Tensor, what: str) -> int:
+    """The number of the device that a call's tensors are on: the current one, whose stream it uses."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{what}: needs a tensor on the current device, got one on {t.device}")
+    return dev
 
 
-def _rows(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, n: int, d: int,
+def _rows(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, shape: tuple, dev: int,
           written: bool = False) -> tuple:
-    """A [n, d] tensor of the current device, d contiguous; rows may be strided (those that are
+    """A [n, d] tensor of device `dev`, d contiguous; rows may be strided (those that are
     written: apart from each other).  The fields of a staple_rows_t."""
     if t is None:
         return _NO_ROWS
-    if t.dtype is not dtype or t.shape != (n, d) or _elsewhere(t):
-        raise ValueError(f"{what}: needs a [{n}, {d}] tensor of {dtype} on the current device, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{what}: needs a {list(shape)} tensor of {dtype} on device {dev}, got "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
     stride, one = t.stride()
-    if (one != 1 and d > 1 or written and n > 1 and stride < d) and t.numel():
+    if (one != 1 or (written and stride < shape[1])) and t.numel() and \
+            (one != 1 and shape[1] > 1 or written and shape[0] > 1 and stride < shape[1]):
         raise ValueError(f"{what}: rows must be contiguous" + (" and apart from each other" if written else ""))
     return t.data_ptr(), stride
 
 
-def _flat(t: Optional[torch.Tensor], what: str, n: Optional[int], dtype: torch.dtype = torch.int32) -> Optional[int]:
-    """A contiguous tensor of n elements (None: any number) on the current device."""
+def _flat(t: Optional[torch.Tensor], what: str, n: Optional[int], dev: int, dtype: torch.dtype = torch.int32) -> Optional[int]:
+    """A contiguous tensor of n elements (None: any number) of device `dev`."""
     if t is None:
         return None
-    if t.dtype is not dtype or _elsewhere(t) or not t.is_contiguous() or \
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
             (n is not None and t.numel() != n):
-        raise ValueError(f"{what}: needs a contiguous {dtype} tensor on the current device" +
+        raise ValueError(f"{what}: needs a contiguous {dtype} tensor on device {dev}" +
                          ("" if n is None else f" of {n} elements"))
     return t.data_ptr()
 
@@ -1150,13 +1155,15 @@ def staple_embed_fwd(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
                      stream=None) -> torch.Tensor:
     """Rows scale * table[ids] [tokens, d] of out_dtype (None: the table's)."""
     vocab, d = table.shape
-    n = ids.numel()
+    n, dev = ids.numel(), _on(table, "table")
     if out is None:
         out = _own(stream, lambda: table.new_empty((n, d), dtype=out_dtype or table.dtype))
-    dt = table.dtype
-    y, stride = _rows(out, "out", out.dtype, n, d, True)
-    _check(lib().staple_embed_fwd(_flat(table, "table", None, dt), vocab, d, _dt(table), _flat(ids, "ids", n), n,
-                                  float(scale), y, stride, _dt(out), _stream(stream)), "staple_embed_fwd")
+        y, stride = out.data_ptr(), d
+    else:
+        y, stride = _rows(out, "out", out.dtype, (n, d), dev, True)
+    _check(lib().staple_embed_fwd(_flat(table, "table", None, dev, table.dtype), vocab, d, _dt(table),
+                                  _flat(ids, "ids", n, dev), n, float(scale), y, stride, _dt(out), _stream(stream)),
+           "staple_embed_fwd")
     return out
 
 
@@ -1187,43 +1194,44 @@ def staple_embed_bwd(dy: torch.Tensor, sorted_pos: torch.Tensor, seg_start: torc
     for t, least, what in ((sorted_pos, n, "sorted_pos"), (inv, n, "inv"), (seg_start, min(n, mu) + 1, "seg_start"),
                            (n_unique, 1, "n_unique")):
         _need(t, least, what)
-    at, stride = _rows(dy, "dy", dy.dtype, n, d)
+    dev = _on(dy, "dy")
+    at, stride = _rows(dy, "dy", dy.dtype, (n, d), dev)
     native = lib()
     ws = _ws(native.staple_embed_bwd_workspace_bytes(n, d), workspace, dy.device, stream)
-    _check(native.staple_embed_bwd(at, stride, _dt(dy), n, d, float(scale), _flat(sorted_pos, "sorted_pos", None),
-                                   _flat(inv, "inv", None), _flat(seg_start, "seg_start", None),
-                                   _flat(n_unique, "n_unique", None), mu, _flat(uniq, "uniq", None),
-                                   _flat(out, "out", None, _FLOAT32), rows, int(bool(accumulate)), _p(ws),
+    _check(native.staple_embed_bwd(at, stride, _dt(dy), n, d, float(scale), _flat(sorted_pos, "sorted_pos", None, dev),
+                                   _flat(inv, "inv", None, dev), _flat(seg_start, "seg_start", None, dev),
+                                   _flat(n_unique, "n_unique", None, dev), mu, _flat(uniq, "uniq", None, dev),
+                                   _flat(out, "out", None, dev, _FLOAT32), rows, int(bool(accumulate)), _p(ws),
                                    _ws_size(ws), _stream(stream)), "staple_embed_bwd")
     return out
 
 
-def _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps):
-    """The fields of a staple_norm_t up to eps, and the gate's and the weights'."""
-    wt = None
+def _norm(one, zt, w_pre, w_post, gate, pre, post, scale, eps):
+    """The fields of a staple_norm_t up to eps, the gate's and the weights', whether the gate is shared, and the
+    device; `one`: x, or z without it."""
+    n, d = one.shape
     shared = gate is not None and gate.dim() == 1
-    for w in (w_pre, w_post, gate if shared else None):
-        if w is not None:
-            if wt is not None and w.dtype is not wt:
-                raise ValueError("the weights and a shared gate have one dtype")
-            wt = w.dtype
+    w = w_pre if w_pre is not None else w_post if w_post is not None else gate if shared else None
+    wt = _FLOAT32 if w is None else w.dtype
+    if (w_post is not None and w_post.dtype is not wt) or (shared and gate.dtype is not wt):
+        raise ValueError("the weights and a shared gate have one dtype")
     if (w_pre is not None and not pre) or (w_post is not None and not post):
         raise ValueError("weights of a norm that is not done")
-    if gate is None:
-        gate = _NO_ROWS
-    elif shared:
-        gate = (_flat(gate, "gate", d, wt), 0)
-    else:
-        gate = _rows(gate, "gate", zt, n, d)
-        if gate[1] == 0 and n > 1:
-            raise ValueError("gate: a shared one is given as [d]")
-        gate = (gate[0], gate[1] or d)
     try:
-        codes = _DT[zt], _DT[xt], F32 if wt is None else _DT[wt]
+        head = (n, d, _DT[zt], _DT[one.dtype], _DT[wt], 1 if pre else 0, 1 if post else 0, float(scale), float(eps))
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]}; use bfloat16 or float32") from None
-    return (n, d, *codes, int(pre), int(post), float(scale), float(eps)), gate, \
-        (_flat(w_pre, "w_pre", d, wt), _flat(w_post, "w_post", d, wt)), shared
+    dev = _on(one, "the rows")
+    if gate is None:
+        at = _NO_ROWS
+    elif shared:
+        at = (_flat(gate, "gate", d, dev, wt), 0)
+    else:
+        at = _rows(gate, "gate", zt, (n, d), dev)
+        if at[1] == 0 and n > 1:
+            raise ValueError("gate: a shared one is given as [d]")
+        at = (at[0], at[1] or d)
+    return head, at, (_flat(w_pre, "w_pre", d, dev, wt), _flat(w_post, "w_post", d, dev, wt)), shared, dev
 
 
 def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None, *,
@@ -1238,20 +1246,23 @@ def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None,
     None: z's).  Returns r (None without z), h (None without `pre`), and with `save` 1 / rms of
     both, rstd_r and rstd_z, for staple_norm_bwd."""
     one = z if x is None else x
-    n, d = one.shape
+    n, d = shape = one.shape
     xt = one.dtype
     zt = z.dtype if z is not None else dtype or xt
-    head, gate, weights, _ = _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps)
+    head, gate, weights, _, dev = _norm(one, zt, w_pre, w_post, gate, pre, post, scale, eps)
     if out is None:
         out = _own(stream, lambda: {
-            "r": None if z is None else one.new_empty((n, d)),
-            "h": one.new_empty((n, d), dtype=zt) if pre else None,
+            "r": None if z is None else one.new_empty(shape),
+            "h": None if not pre else one.new_empty(shape, dtype=zt),
             "rstd_r": one.new_empty(n, dtype=_FLOAT32) if pre and save else None,
             "rstd_z": one.new_empty(n, dtype=_FLOAT32) if post and save else None})
-    a = _lib.Norm(*head, _rows(x, "x", xt, n, d), _rows(z, "z", zt, n, d),
-                  _rows(out.get("r"), "r", xt, n, d, True) if z is not None else _NO_ROWS,
-                  _rows(out["h"], "h", zt, n, d, True) if pre else _NO_ROWS, gate, *weights,
-                  _flat(out.get("rstd_r"), "rstd_r", n, _FLOAT32), _flat(out.get("rstd_z"), "rstd_z", n, _FLOAT32))
+        r, h = (_NO_ROWS if t is None else (t.data_ptr(), d) for t in (out["r"], out["h"]))
+        saved = _p(out["rstd_r"]), _p(out["rstd_z"])
+    else:
+        r = _NO_ROWS if z is None else _rows(out.get("r"), "r", xt, shape, dev, True)
+        h = _rows(out["h"], "h", zt, shape, dev, True) if pre else _NO_ROWS
+        saved = [_flat(out.get(k), k, n, dev, _FLOAT32) for k in ("rstd_r", "rstd_z")]
+    a = _lib.Norm(*head, _rows(x, "x", xt, shape, dev), _rows(z, "z", zt, shape, dev), r, h, gate, *weights, *saved)
     _check(lib().staple_norm_fwd(ctypes.byref(a), _stream(stream)), "staple_norm_fwd")
     return out
 
@@ -1270,28 +1281,29 @@ def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: O
     it again (which reads x and z); in bf16 its rounding then shows in dw_pre, in fp32 it is as good and saves z
     where nothing else needs it.  dw_pre, dw_post and the gradient of a shared gate are fp32."""
     one = z if x is None else x
-    n, d = one.shape
+    n, d = shape = one.shape
     xt = one.dtype
     zt = z.dtype if z is not None else dh.dtype if dh is not None else xt
     if z is None:
         r, x = x, None
-    head, gate_at, weights, shared = _norm(n, d, zt, xt, w_pre, w_post, gate, pre, post, scale, eps)
+    head, gate_at, weights, shared, dev = _norm(one, zt, w_pre, w_post, gate, pre, post, scale, eps)
     if out is None:
         out = _own(stream, lambda: {
-            "dx": None if x is None and z is not None else one.new_empty((n, d)),
-            "dz": None if z is None else one.new_empty((n, d), dtype=zt),
+            "dx": None if x is None and z is not None else one.new_empty(shape),
+            "dz": None if z is None else one.new_empty(shape, dtype=zt),
             "dgate": None if gate is None else one.new_empty(d, dtype=_FLOAT32) if shared
-            else one.new_empty((n, d), dtype=zt),
+            else one.new_empty(shape, dtype=zt),
             "dw_pre": None if w_pre is None else one.new_empty(d, dtype=_FLOAT32),
             "dw_post": None if w_post is None else one.new_empty(d, dtype=_FLOAT32)})
     dgate = out.get("dgate")
-    a = _lib.Norm(*head, _rows(x, "x", xt, n, d), _rows(z, "z", zt, n, d), _rows(r, "r", xt, n, d), _NO_ROWS, gate_at,
-                  *weights,
-                  _flat(rstd_r, "rstd_r", n, _FLOAT32), _flat(rstd_z, "rstd_z", n, _FLOAT32),
-                  _rows(dr, "dr", xt, n, d), _rows(dh, "dh", zt, n, d) if pre else _NO_ROWS,
-                  _rows(out.get("dx"), "dx", xt, n, d, True), _rows(out.get("dz"), "dz", zt, n, d, True),
-                  (_flat(dgate, "dgate", d, _FLOAT32), 0) if shared else _rows(dgate, "dgate", zt, n, d, True),
-                  _flat(out.get("dw_pre"), "dw_pre", d, _FLOAT32), _flat(out.get("dw_post"), "dw_post", d, _FLOAT32))
+    a = _lib.Norm(*head, _rows(x, "x", xt, shape, dev), _rows(z, "z", zt, shape, dev), _rows(r, "r", xt, shape, dev),
+                  _NO_ROWS, gate_at, *weights, _flat(rstd_r, "rstd_r", n, dev, _FLOAT32),
+                  _flat(rstd_z, "rstd_z", n, dev, _FLOAT32), _rows(dr, "dr", xt, shape, dev),
+                  _rows(dh, "dh", zt, shape, dev) if pre else _NO_ROWS, _rows(out.get("dx"), "dx", xt, shape, dev, True),
+                  _rows(out.get("dz"), "dz", zt, shape, dev, True),
+                  (_flat(dgate, "dgate", d, dev, _FLOAT32), 0) if shared else _rows(dgate, "dgate", zt, shape, dev, True),
+                  _flat(out.get("dw_pre"), "dw_pre", d, dev, _FLOAT32),
+                  _flat(out.get("dw_post"), "dw_post", d, dev, _FLOAT32))
     a, native = ctypes.byref(a), lib()
     ws = _ws(native.staple_norm_bwd_workspace_bytes(a), workspace, one.device, stream)
     _check(native.staple_norm_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_norm_bwd")
@@ -1303,17 +1315,17 @@ def staple_xent_fwd(logits: torch.Tensor, targets: torch.Tensor, *, g: Optional[
     """Cross entropy of logits [rows, vocab]: loss and lse [rows], fp32.  targets int32 [rows]; a
     negative one leaves its row out.  g [rows] fp32, the gradient of each row's loss: the gradient
     of the logits comes with them as d_logits (out["d_logits"] may be the logits)."""
-    n, vocab = logits.shape
+    n, vocab = shape = logits.shape
+    dt, dev = logits.dtype, _on(logits, "logits")
     if out is None:
         out = _own(stream, lambda: {
             "loss": logits.new_empty(n, dtype=_FLOAT32), "lse": logits.new_empty(n, dtype=_FLOAT32),
-            **({} if g is None else {"d_logits": logits.new_empty((n, vocab))})})
-    dt = logits.dtype
-    at, stride = _rows(logits, "logits", dt, n, vocab)
-    d, d_stride = _NO_ROWS if g is None else _rows(out["d_logits"], "d_logits", dt, n, vocab, True)
-    _check(lib().staple_xent_fwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
-                                 _flat(out["loss"], "loss", n, _FLOAT32), _flat(out["lse"], "lse", n, _FLOAT32),
-                                 _flat(g, "g", n, _FLOAT32), d, d_stride, _stream(stream)), "staple_xent_fwd")
+            **({} if g is None else {"d_logits": logits.new_empty(shape)})})
+    at, stride = _rows(logits, "logits", dt, shape, dev)
+    d, d_stride = _NO_ROWS if g is None else _rows(out["d_logits"], "d_logits", dt, shape, dev, True)
+    _check(lib().staple_xent_fwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n, dev),
+                                 _flat(out["loss"], "loss", n, dev, _FLOAT32), _flat(out["lse"], "lse", n, dev, _FLOAT32),
+                                 _flat(g, "g", n, dev, _FLOAT32), d, d_stride, _stream(stream)), "staple_xent_fwd")
     return out
 
 
@@ -1321,14 +1333,14 @@ def staple_xent_bwd(g: torch.Tensor, logits: torch.Tensor, targets: torch.Tensor
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits from that of each row's loss, g [rows] fp32, and the forward's lse;
     `out` may be the logits."""
-    n, vocab = logits.shape
+    n, vocab = shape = logits.shape
+    dt, dev = logits.dtype, _on(logits, "logits")
     if out is None:
-        out = _own(stream, lambda: logits.new_empty((n, vocab)))
-    dt = logits.dtype
-    at, stride = _rows(logits, "logits", dt, n, vocab)
-    d, d_stride = _rows(out, "out", dt, n, vocab, True)
-    _check(lib().staple_xent_bwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n),
-                                 _flat(lse, "lse", n, _FLOAT32), _flat(g, "g", n, _FLOAT32), d, d_stride,
+        out = _own(stream, lambda: logits.new_empty(shape))
+    at, stride = _rows(logits, "logits", dt, shape, dev)
+    d, d_stride = _rows(out, "out", dt, shape, dev, True)
+    _check(lib().staple_xent_bwd(at, stride, n, vocab, _dt(logits), _flat(targets, "targets", n, dev),
+                                 _flat(lse, "lse", n, dev, _FLOAT32), _flat(g, "g", n, dev, _FLOAT32), d, d_stride,
                                  _stream(stream)), "staple_xent_bwd")
     return out
 
@@ -1342,17 +1354,19 @@ def staple_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optiona
     tokens.  temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, each None or one a row:
     a temperature that is not above 0 takes the first of the largest logits; top_k 0, top_p 1 and min_p 0
     limit nothing."""
-    n, vocab = logits.shape
+    n, vocab = shape = logits.shape
+    dev = _on(logits, "logits")
     if out is None:
         out = _own(stream, lambda: {"token": logits.new_empty(n, dtype=_INT32),
                                     "logprob": logits.new_empty(n, dtype=_FLOAT32)})
-    at, stride = _rows(logits, "logits", logits.dtype, n, vocab)
+    at, stride = _rows(logits, "logits", logits.dtype, shape, dev)
     native = lib()
     ws = _ws(native.staple_sample_workspace_bytes(n, vocab), workspace, logits.device, stream)
-    _check(native.staple_sample(at, stride, n, vocab, _dt(logits), _flat(u, "u", n, _FLOAT32),
-                                _flat(temperature, "temperature", n, _FLOAT32), _flat(top_k, "top_k", n),
-                                _flat(top_p, "top_p", n, _FLOAT32), _flat(min_p, "min_p", n, _FLOAT32),
-                                _flat(out["token"], "token", n), _flat(out.get("logprob"), "logprob", n, _FLOAT32),
+    _check(native.staple_sample(at, stride, n, vocab, _dt(logits), _flat(u, "u", n, dev, _FLOAT32),
+                                _flat(temperature, "temperature", n, dev, _FLOAT32), _flat(top_k, "top_k", n, dev),
+                                _flat(top_p, "top_p", n, dev, _FLOAT32), _flat(min_p, "min_p", n, dev, _FLOAT32),
+                                _flat(out["token"], "token", n, dev),
+                                _flat(out.get("logprob"), "logprob", n, dev, _FLOAT32),
                                 _p(ws), _ws_size(ws), _stream(stream)), "staple_sample")
     return out
 
