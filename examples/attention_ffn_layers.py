@@ -3,12 +3,13 @@ documents, then served from a paged key-value cache.
 
     python examples/attention_ffn_layers.py [--dtype bf16|f32] [--steps 20]
 
-Training joins staple_attn_fwd and staple_attn_bwd with the FFN's calls in
-torch's autograd.  Serving prefills prompts of different lengths into pages
+Training joins staple_attn_fwd and staple_attn_bwd with the FFN's calls, the
+embedding (staple_embed_*), the norms around the blocks (staple_norm_*) and the loss
+(staple_xent_fwd) in torch's autograd.  Serving prefills prompts of different lengths into pages
 (staple_kv_extend, staple_attn_fwd, staple_kv_append), decodes token by token
 (staple_attn_decode_paged), forks a sequence into beams that share its pages
-until they write, ends sequences, packs the pool and goes on decoding.  The
-logits of every served token are checked against one pass over whole sequences.
+until they write, ends sequences, packs the pool and goes on decoding, each token
+chosen by staple_sample.  The logits of every served token are checked against one pass over whole sequences.
 """
 from __future__ import annotations
 
@@ -68,14 +69,59 @@ class TokenFFN(torch.autograd.Function):
         return d["dx"], d["dw_gate"], d["dw_up"], d["dw_down"], d["d_rows"][:ctx.n_rows], None
 
 
+class Embed(torch.autograd.Function):
+    """Rows of the fp32 table in the model's type; the gradient by the batch's unique tokens."""
+
+    @staticmethod
+    def forward(ctx, table, ids, batch, dtype):
+        ctx.shape, ctx.batch = table.shape, batch
+        return st.staple_embed_fwd(table, ids, out_dtype=dtype)
+
+    @staticmethod
+    def backward(ctx, dy):
+        b = ctx.batch
+        grad = torch.zeros(ctx.shape, device=dy.device)
+        st.staple_embed_bwd(dy.contiguous(), b["sorted_pos"], b["seg_start"], b["n_unique"], inv=b["inv"], uniq=b["uniq"],
+                            out=grad)
+        return grad, None, None, None
+
+
+class AddNorm(torch.autograd.Function):
+    """The residual sum r = x + z, and its norm; without z the norm of x."""
+
+    @staticmethod
+    def forward(ctx, x, z, weight):
+        ctx.set_materialize_grads(False)   # the last residual sum goes nowhere: its gradient is None
+        out = st.staple_norm_fwd(x, z, w_pre=weight, save=True)
+        ctx.save_for_backward(x, z, weight, out["rstd_r"])
+        return out["h"] if z is None else (out["r"], out["h"])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        x, z, weight, rstd = ctx.saved_tensors
+        dr, dh = (None, *grads) if z is None else grads
+        d = st.staple_norm_bwd(None if dr is None else dr.contiguous(), dh.contiguous(), x, z, rstd, w_pre=weight)
+        return d["dx"], d["dz"], d["dw_pre"]
+
+
+class Loss(torch.autograd.Function):
+    """The mean cross entropy over the targets that count; the logits' gradient comes with it."""
+
+    @staticmethod
+    def forward(ctx, logits, target):
+        share = 1.0 / (target >= 0).sum()
+        out = st.staple_xent_fwd(logits, target, g=share.float().expand(len(logits)).contiguous())
+        ctx.save_for_backward(out["d_logits"])
+        return out["loss"].sum() * share
+
+    @staticmethod
+    def backward(ctx, d):
+        return ctx.saved_tensors[0] * d, None
+
+
 def heads_of(qkv):
     t = qkv.view(len(qkv), HEADS + 2 * KV_HEADS, HEAD_DIM)
     return t[:, :HEADS], t[:, HEADS:HEADS + KV_HEADS], t[:, HEADS + KV_HEADS:]
-
-
-def norm(x):
-    y = x.float()
-    return (y * torch.rsqrt(y.pow(2).mean(dim=1, keepdim=True) + 1e-6)).to(x.dtype)
 
 
 def offsets(lens):
@@ -95,19 +141,24 @@ class Model:
         self.layers = [dict(qkv=weight(width, D_MODEL), o=weight(D_MODEL, HEADS * HEAD_DIM), gate=weight(D_FF, D_MODEL),
                             up=weight(D_FF, D_MODEL), down=weight(D_MODEL, D_FF), table=weight(VOCAB, D_FF))
                        for _ in range(LAYERS)]
+        # before each attention and each FFN, and before the logits
+        self.norms = [torch.ones(D_MODEL, device="cuda", requires_grad=True) for _ in range(2 * LAYERS + 1)]
 
     def parameters(self):
-        return [self.embed] + [w for layer in self.layers for w in layer.values()]
+        return [self.embed] + self.norms + [w for layer in self.layers for w in layer.values()]
 
     def forward(self, ids, cu):
         """Logits of packed sequences."""
         batch = st.staple_dedup(ids, VOCAB)
         uniq = batch["uniq"][:int(batch["n_unique"])].long()
-        x = self.embed[ids.long()].to(self.dtype)
-        for layer in self.layers:
-            x = x + Attention.apply(norm(x) @ layer["qkv"].to(x.dtype).T, cu) @ layer["o"].to(x.dtype).T
-            x = x + TokenFFN.apply(norm(x), layer["gate"], layer["up"], layer["down"], layer["table"][uniq], batch)
-        return norm(x).float() @ self.embed.T
+        x = Embed.apply(self.embed, ids, batch, self.dtype)
+        h = AddNorm.apply(x, None, self.norms[0])
+        for i, layer in enumerate(self.layers):
+            z = Attention.apply(h @ layer["qkv"].to(x.dtype).T, cu) @ layer["o"].to(x.dtype).T
+            x, h = AddNorm.apply(x, z, self.norms[2 * i + 1])
+            z = TokenFFN.apply(h, layer["gate"], layer["up"], layer["down"], layer["table"][uniq], batch)
+            x, h = AddNorm.apply(x, z, self.norms[2 * i + 2])
+        return h.float() @ self.embed.T
 
 
 def train(model, steps):
@@ -116,12 +167,12 @@ def train(model, steps):
     gen = torch.Generator().manual_seed(1)
     ids = torch.randint(VOCAB, (sum(lens),), generator=gen, dtype=torch.int32).cuda()
     cu = offsets(lens)
-    target = torch.roll(ids.long(), -1)
+    target = torch.roll(ids, -1)
     target[cu[1:].long() - 1] = -100   # a document's last token has no next one
     adam = torch.optim.AdamW(model.parameters(), lr=3e-3)
     losses = []
     for _ in range(steps):
-        loss = torch.nn.functional.cross_entropy(model.forward(ids, cu), target, ignore_index=-100)
+        loss = Loss.apply(model.forward(ids, cu), target)
         adam.zero_grad()
         loss.backward()
         adam.step()
@@ -156,12 +207,16 @@ class Server:
 
     def run(self, ids, attend):
         """Logits of new tokens; attend: (layer, q, k, v) -> o."""
-        x = self.model.embed.detach()[ids.long()].to(self.model.dtype)
+        model = self.model
+        norms = [w.detach() for w in model.norms]
+        x = st.staple_embed_fwd(model.embed.detach(), ids, out_dtype=model.dtype)
+        h = st.staple_norm_fwd(x, w_pre=norms[0])["h"]
         for i, w in enumerate(self.layers):
-            o = attend(i, *heads_of(norm(x) @ w["qkv"].T))
-            x = x + o.reshape(len(ids), -1) @ w["o"].T
-            x = x + self.ffn(w, norm(x), ids)
-        return norm(x).float() @ self.model.embed.detach().T
+            o = attend(i, *heads_of(h @ w["qkv"].T))
+            seam = st.staple_norm_fwd(x, o.reshape(len(ids), -1) @ w["o"].T, w_pre=norms[2 * i + 1])
+            seam = st.staple_norm_fwd(seam["r"], self.ffn(w, seam["h"], ids), w_pre=norms[2 * i + 2])
+            x, h = seam["r"], seam["h"]
+        return h.float() @ model.embed.detach().T
 
     def prefill(self, seqs, prompts):
         lens = [len(p) for p in prompts]
@@ -210,9 +265,14 @@ def serve(model, steps=20):
     def keep(seqs, out):
         logits.update(zip(seqs, out))
 
-    def step(seqs, rank=lambda s: 0):
-        """Each sequence goes on with its best token, or the one of that rank."""
-        ids = torch.stack([logits[s].topk(rank(s) + 1).indices[-1] for s in seqs]).int()
+    def step(seqs, rank=None):
+        """Each sequence goes on with its best token (temperature 0), or the one of that rank."""
+        rows = torch.stack([logits[s] for s in seqs])
+        if rank is None:
+            unused = torch.zeros(len(seqs), device="cuda")
+            ids = st.staple_sample(rows, unused, temperature=unused)["token"]
+        else:
+            ids = torch.stack([r.topk(rank(s) + 1).indices[-1] for s, r in zip(seqs, rows)]).int()
         for s, t in zip(seqs, ids):
             text[s] = torch.cat((text[s], t.view(1)))
         keep(seqs, server.decode(seqs, ids))

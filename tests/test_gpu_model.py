@@ -105,6 +105,29 @@ def test_embedding_gradient(st, dtype, pattern, d, pad):
     fine(st)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [2048, 2047])
+def test_embedding_gradient_of_many_tokens(st, dtype, d):
+    """A training batch: wide chunks, tokens that hold thousands of positions."""
+    import torch
+    n, vocab = 33100, 3000
+    ids = np.minimum(np.random.default_rng(12).zipf(1.2, n), vocab).astype(np.int32) - 1
+    dy = rand((n, d), dtype, 13)
+    dd = st.staple_dedup(torch.from_numpy(ids).cuda(), vocab)
+    rows = st.staple_embed_bwd(dy, dd["sorted_pos"], dd["seg_start"], dd["n_unique"], inv=dd["inv"], scale=2.0, max_unique=vocab)
+    fine(st)
+    host = to_np(dy[:, ::73])
+    ref, bound = M.embed_grad(host, ids, 2.0), B.embed_grad(host, ids, 2.0)
+    uniq = sorted(ref)
+    check(to_np(rows[:len(uniq)][:, ::73]), np.array([ref[t] for t in uniq]), np.array([bound[t] for t in uniq]), "rows")
+    # every column against a sum in another order
+    total = torch.zeros(vocab, d, dtype=torch.float64, device="cuda").index_add_(0, torch.from_numpy(ids).cuda().long(), dy.double())
+    size = torch.zeros(vocab, d, dtype=torch.float64, device="cuda").index_add_(0, torch.from_numpy(ids).cuda().long(), dy.double().abs())
+    at = torch.tensor(uniq, device="cuda")
+    most = 2 * B.E * size[at] * (34 + torch.bincount(torch.from_numpy(ids).cuda().long(), minlength=vocab)[at, None])
+    assert bool(((rows[:len(uniq)].double() - 2 * total[at]).abs() <= most).all())
+
+
 def test_embedding_gradient_of_one_row_for_all(st):
     """A gradient that is the same for all positions, given by one row."""
     import torch
@@ -157,7 +180,9 @@ def test_embedding_gradient_with_bad_maps(st):
 # ----------------------------------------------------------------------------------------- norms
 TYPES = [("bf16", "bf16", "bf16"), ("bf16", "bf16", "f32"), ("bf16", "f32", "f32"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16")]
 DIMS = [(5, 1), (3, 7), (9, 8), (4, 64), (7, 512), (6, 520), (5, 1000), (5, 1111), (4, 2048), (3, 2056), (3, 4096), (2, 5001),
-        (2, 8192), (2, 16384), (700, 264), (1, 2048), (1500, 33)]
+        (2, 8192), (2, 16384), (700, 264), (1, 2048), (1500, 33),
+        # more rows than there are places for them at once
+        (9000, 40), (4000, 300), (3000, 1000), (1500, 2048), (1300, 4096), (600, 5001), (530, 16384)]
 
 
 def run_norm(st, n, d, dtype, r_dtype, w_dtype, pre, post, gate, residual, scale, pad, seed, x=None):
@@ -335,7 +360,8 @@ XENT_CHAIN = lambda v: 3 * (v / 64 + 64)
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,v,pad", [(1, 1, 0), (3, 2, 0), (5, 7, 0), (4, 8, 8), (70, 63, 1), (9, 513, 0), (130, 1024, 0), (33, 4096, 0),
-                                     (6, 5003, 5), (2, 100352, 0), (3, 100277, 0), (1, 262147, 0), (300, 2050, 0)])
+                                     (6, 5003, 5), (2, 100352, 0), (3, 100277, 0), (1, 262147, 0), (300, 2050, 0),
+                                     (3, 9001, 0), (3, 20000, 0), (3, 60001, 1), (2, 120001, 0), (2, 131072, 0), (2, 131073, 0)])
 def test_loss_and_its_gradient(st, dtype, n, v, pad):
     print(dtype, n, v, pad, flush=True)
     rng = np.random.default_rng(v)
