@@ -1048,8 +1048,8 @@ staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_ro
  *     w_j >= min_p                                           (min_p > 0),
  * the first one always; token = the first j, in the order of j, at which the sum of the kept w
  * passes u times their whole sum.  T that is not above 0: the first of the largest logits.
- * NaN counts as -inf, and a token with -inf is never drawn; a row with nothing else has
- * token -1.  logprob (NULL: not wanted): the log of the token's share of the kept sum, 0 where
+ * NaN counts as -inf, +inf as the largest finite number; a token with -inf is never drawn, and a
+ * row with nothing else has token -1.  logprob (NULL: not wanted): the log of the token's share of the kept sum, 0 where
  * T is not above 0, -inf for token -1.
  *   u float[n_rows] in [0, 1); temperature, top_p, min_p float[n_rows], top_k
  *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.

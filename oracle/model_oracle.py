@@ -113,7 +113,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
     logits = f64(logits)
     tokens, logprobs = [], []
     for i, l in enumerate(logits):
-        l = np.where(np.isnan(l), -np.inf, l)
+        l = np.minimum(np.where(np.isnan(l), -np.inf, l), float(np.finfo(np.float32).max))
         top = l.max()
         t = 1.0 if temperature is None else float(temperature[i])
         if top == -np.inf:
@@ -124,9 +124,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
             tokens.append(int(np.argmax(l)))
             logprobs.append(0.0)
             continue
-        with np.errstate(invalid="ignore"):
-            d = np.where(l == top, 0.0, np.where((l == -np.inf) | (top == np.inf), -np.inf, l - top) / t)
-        w = np.where(l == -np.inf, 0.0, np.exp(np.where(l == -np.inf, -np.inf, d)))
+        d = np.where(l == -np.inf, 0.0, l - top) / t
+        w = np.where(l == -np.inf, 0.0, np.exp(d))
         order = sorted(range(len(l)), key=lambda j: (-l[j], j))
         kept = order
         if top_k is not None and 0 < int(top_k[i]) < len(l):

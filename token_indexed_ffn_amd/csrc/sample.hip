@@ -29,7 +29,8 @@ constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all
 constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
 
 // --------------------------------------------------------------------------- logits and weights
-__device__ __forceinline__ float no_nan(float l) { return l == l ? l : -__builtin_inff(); }
+// NaN as -inf, +inf as the largest finite number.
+__device__ __forceinline__ float plain(float l) { return fminf(fmaxf(l, -__builtin_inff()), 3.402823466e38f); }
 
 // Order of the logits: larger logits have larger keys, -0 that of 0.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -66,15 +67,16 @@ __device__ const double kSteps[32] = {
 
 // A row's weights.
 struct Weights {
-  double top;       // the largest logit, 1e300 for +inf
+  double top;       // the largest logit
   double rate;      // 32 log2(e) / T
+  double lowest;    // exponents from here on are rounded to a weight of 0
   int unit_log2;
   const double* step;
   __device__ __forceinline__ u64 unit() const { return u64(1) << unit_log2; }
-  // 2^(y / 32) with y = n + r: the step of n's last five bits, its other bits as the exponent, and
-  // five terms of exp(r ln 2 / 32) (|r| <= 1/2: off by 2^-48)
+  // 2^(y / 32) with y = n + r: the step of n's last five bits, its other bits added to the exponent, and
+  // five terms of exp(r ln 2 / 32) (|r| <= 1/2: off by 2^-48).  Some 22 instructions, 14 of them in 64 bits.
   __device__ __forceinline__ u64 operator()(float l) const {
-    const double far = fmax((fmin(static_cast<double>(l), 1e300) - top) * rate, -35200.0);
+    const double far = fmax((static_cast<double>(l) - top) * rate, lowest);
     const double magic = 6755399441055744.0;   // 3 2^51: a sum with it is rounded to a whole number
     const double big = far + magic;
     const int n = static_cast<int>(__double_as_longlong(big));
@@ -86,8 +88,8 @@ struct Weights {
     p = fma(p, r, c * c / 2);
     p = fma(p, r, c);
     p = fma(p, r, 1.0);
-    const double w = ldexp(p * step[n & 31], (n >> 5) + unit_log2);
-    return static_cast<u64>(__double_as_longlong(w + 4503599627370496.0)) & ((u64(1) << 52) - 1);
+    const u64 bits = __double_as_longlong(p * step[n & 31]) + (static_cast<u64>((n >> 5) + unit_log2) << 52);
+    return __double_as_longlong(__longlong_as_double(bits) + 4503599627370496.0) & ((u64(1) << 52) - 1);
   }
 };
 
@@ -155,7 +157,7 @@ struct Row {
   __device__ __forceinline__ Row(const SampleView& a, int64_t row)
       : p(reinterpret_cast<const E*>(a.logits) + row * a.stride), n(a.vocab),
         shift(static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(E))) {}
-  __device__ __forceinline__ float at(int j) const { return no_nan(load1(p + j)); }
+  __device__ __forceinline__ float at(int j) const { return plain(load1(p + j)); }
   // The elements outside full groups of eight are held one a lane (lanes 0 to 7 the row's first
   // ones, 32 to 39 its last ones), in the blocks that they belong to; -1: none.
   __device__ __forceinline__ bool has_edge(const SampleGrid& g, int block) const {
@@ -205,7 +207,7 @@ struct Walk {
       float v[8];
       raw[0].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = no_nan(v[i]);
+      for (int i = 0; i < 8; ++i) v[i] = plain(v[i]);
       int j = first(s);
       bool full = j >= 0 && j + 8 <= r.n;
 #pragma unroll
@@ -282,8 +284,8 @@ __device__ __forceinline__ Limits limits_of(const SampleView& a, int64_t row, co
   m.temperature = a.temperature ? temperature : 1.0f;
   m.greedy = !(m.temperature > 0.0f);
   const int bits = 62 - (32 - __clz(a.vocab));
-  m.weight = Weights{fmin(static_cast<double>(m.top), 1e300), 46.1662413084468290355 / static_cast<double>(m.temperature),
-                     bits < 50 ? bits : 50, step};
+  const int unit = bits < 50 ? bits : 50;
+  m.weight = Weights{m.top, 46.1662413084468290355 / static_cast<double>(m.temperature), -32.0 * (unit + 2), unit, step};
   const int k = a.top_k ? given_k : 0;
   m.k = k > 0 && k < a.vocab ? k : 0;
   const float p = a.top_p ? given_p : 1.0f;
@@ -456,7 +458,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a
   int first = 0;   // a row of -inf has no token: any will do
   if (best != -__builtin_inff())
     for (int i = 7; i >= 0; --i)
-      if (at + i >= 0 && at + i < r.n && load1(r.p + at + i) == best) first = at + i;
+      if (at + i >= 0 && at + i < r.n && r.at(at + i) == best) first = at + i;
   u64 place = place_of(best, first);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
