@@ -266,6 +266,27 @@ def test_many_rows_are_sampled_as_few_are(st, dtype):
     fine(st)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v", [301, 7001, 16800, 16900, 32001, 60001, 100352])
+def test_rows_are_sampled_alike_alone_and_among_many(st, dtype, v):
+    """One workgroup for a row, several, a row in registers: the same tokens to the bit, from rows that begin
+    at and between 16-byte addresses."""
+    import torch
+    n = 130
+    r = np.random.default_rng(v)
+    u, given = floats(r.random(n)), dict(temperature=floats(0.1 + 1.5 * r.random(n)), min_p=floats(0.2 * r.random(n)))
+    more = dict(top_k=ints(r.integers(0, 3000, n)), top_p=floats(0.3 + r.random(n)))
+    for pad in (0, 1):
+        logits = rand((n, v + pad), dtype, 160, 3.0)[:, pad:]
+        for limits in (given, {**given, **more}):
+            all_rows = st.staple_sample(logits, u, **limits)
+            for a, b in ((0, 1), (40, 47), (120, 130)):
+                few = st.staple_sample(logits[a:b], u[a:b], **{k: t[a:b] for k, t in limits.items()})
+                for k, t in few.items():
+                    assert torch.equal(t, all_rows[k][a:b])
+    fine(st)
+
+
 # ------------------------------------------------------------------------------------ the example
 def plain(example):
     """The example's functions in torch's own operations."""

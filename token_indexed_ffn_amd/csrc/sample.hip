@@ -27,6 +27,8 @@ constexpr int kList = 2048;         // listed tokens
 constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
 constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all intervals' loads in flight at once
 constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
+constexpr int64_t kRowsForOnePass = 128;
+constexpr int kShortBlocks = 33;    // of a row that one workgroup takes through all passes
 
 // --------------------------------------------------------------------------- logits and weights
 // NaN as -inf, +inf as the largest finite number.
@@ -117,15 +119,19 @@ struct SampleGrid {
   int64_t row_bytes;
 };
 
-struct RowState {
+enum { kDone, kListed, kSearch };   // the token is known; lo to hi are listed; too many for the list
+struct Border {
   u64 total;             // of all weights
   u64 weight_before;     // of the tokens above interval `lo`
   uint32_t count_before;
-  uint32_t arrived[2];
-  int lo, hi;            // intervals whose tokens are listed
+  int lo, hi;            // intervals whose tokens are listed: the cut is among them
   int mode;
 };
-enum { kDone, kListed, kSearch };   // the token is known; lo and hi are listed; too many for the list
+
+struct RowState {
+  Border border;
+  uint32_t arrived[2];
+};
 
 struct RowSpace {
   RowState* state;
@@ -231,11 +237,10 @@ struct Walk {
   }
 };
 
-// A wave's part of its workgroup's chunk.
-template <typename E>
-__device__ __forceinline__ Walk<E> walk_of(const Row<E>& r, const SampleGrid& g) {
-  const int c = blockIdx.x;
-  return Walk<E>(r, g, c * g.blocks_a_chunk + (threadIdx.x >> 6), min((c + 1) * g.blocks_a_chunk, g.blocks), kWaves);
+// A wave's part of chunk c, of a workgroup of T lanes.
+template <int T = kSampleThreads, typename E>
+__device__ __forceinline__ Walk<E> walk_of(const Row<E>& r, const SampleGrid& g, int c) {
+  return Walk<E>(r, g, c * g.blocks_a_chunk + (threadIdx.x >> 6), min((c + 1) * g.blocks_a_chunk, g.blocks), T / 64);
 }
 
 // A row's limits and weights, from its largest logit.
@@ -254,13 +259,51 @@ struct Limits {
   }
 };
 
+// A row's arguments.  Every load before the first use, none behind a branch: u stands in for what is not given.
+struct Arguments {
+  float temperature, p, low;
+  int k;
+  double step;
+  __device__ __forceinline__ Arguments(const SampleView& a, int64_t row) {
+    step = kSteps[threadIdx.x & 31];
+    temperature = (a.temperature ? a.temperature : a.u)[row];
+    p = (a.top_p ? a.top_p : a.u)[row];
+    low = (a.min_p ? a.min_p : a.u)[row];
+    k = (a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[row];
+  }
+};
+
+// best: the place of the largest logit; least: the smallest logit, or one that is near it.
+__device__ __forceinline__ Limits limits_of(const SampleView& a, const Arguments& given, u64 best, float least, double* step) {
+  Limits m;
+  m.top = logit_at(best);
+  m.first = index_at(best);
+  m.empty = m.top == -__builtin_inff();
+  m.temperature = a.temperature ? given.temperature : 1.0f;
+  m.greedy = !(m.temperature > 0.0f);
+  const int bits = 62 - (32 - __clz(a.vocab));
+  const int unit = bits < 50 ? bits : 50;
+  m.weight = Weights{m.top, 46.1662413084468290355 / static_cast<double>(m.temperature), -32.0 * (unit + 2), unit, step};
+  const int k = a.top_k ? given.k : 0;
+  m.k = k > 0 && k < a.vocab ? k : 0;
+  const float p = a.top_p ? given.p : 1.0f;
+  m.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
+  const float low = a.min_p ? given.low : 0.0f;
+  m.least_weight = low > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(low, 1.0f)) * m.weight.unit())) : 0;
+  // Weights past this distance are rounded to zero.  With top-p alone also: all weights below
+  // (1 - p) / vocab, of the largest one, make less than 1 - p of the whole, so that the cut lies above them.
+  float reach = 0.6932f * (m.weight.unit_log2 + 2);
+  if (m.k == 0 && m.p < 1.0f) reach = fminf(reach, logf(static_cast<float>(a.vocab) / (1.0f - m.p)) + 0.01f);
+  reach = fminf(m.temperature * reach, m.top - least);
+  m.bin_rate = reach > 0.0f ? kBins / reach : 0.0f;
+  if (threadIdx.x < 32) step[threadIdx.x] = given.step;
+  __syncthreads();
+  return m;
+}
+
 __device__ __forceinline__ Limits limits_of(const SampleView& a, int64_t row, const SampleGrid& g, const RowSpace& s,
                                             double* step) {
-  // every load before the first use, none behind a branch: u stands in for what is not given
-  const double one_step = kSteps[threadIdx.x & 31];
-  const float temperature = (a.temperature ? a.temperature : a.u)[row], given_p = (a.top_p ? a.top_p : a.u)[row];
-  const float given_low = (a.min_p ? a.min_p : a.u)[row];
-  const int given_k = (a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[row];
+  const Arguments given(a, row);
   u64 best = 0;
   float least = __builtin_inff();
   const int lane = threadIdx.x & 63;
@@ -277,30 +320,7 @@ __device__ __forceinline__ Limits limits_of(const SampleView& a, int64_t row, co
   }
   best = __shfl(best, 0, 64);
   least = __shfl(least, 0, 64);
-  Limits m;
-  m.top = logit_at(best);
-  m.first = index_at(best);
-  m.empty = m.top == -__builtin_inff();
-  m.temperature = a.temperature ? temperature : 1.0f;
-  m.greedy = !(m.temperature > 0.0f);
-  const int bits = 62 - (32 - __clz(a.vocab));
-  const int unit = bits < 50 ? bits : 50;
-  m.weight = Weights{m.top, 46.1662413084468290355 / static_cast<double>(m.temperature), -32.0 * (unit + 2), unit, step};
-  const int k = a.top_k ? given_k : 0;
-  m.k = k > 0 && k < a.vocab ? k : 0;
-  const float p = a.top_p ? given_p : 1.0f;
-  m.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
-  const float low = a.min_p ? given_low : 0.0f;
-  m.least_weight = low > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(low, 1.0f)) * m.weight.unit())) : 0;
-  // Weights past this distance are rounded to zero.  With top-p alone also: all weights below
-  // (1 - p) / vocab, of the largest one, make less than 1 - p of the whole, so that the cut lies above them.
-  float reach = 0.6932f * (m.weight.unit_log2 + 2);
-  if (m.k == 0 && m.p < 1.0f) reach = fminf(reach, logf(static_cast<float>(a.vocab) / (1.0f - m.p)) + 0.01f);
-  reach = fminf(m.temperature * reach, m.top - least);
-  m.bin_rate = reach > 0.0f ? kBins / reach : 0.0f;
-  if (threadIdx.x < 32) step[threadIdx.x] = one_step;
-  __syncthreads();
-  return m;
+  return limits_of(a, given, best, least, step);
 }
 
 // ------------------------------------------------------------------------------ workgroup sums
@@ -326,7 +346,8 @@ __device__ __forceinline__ u64 sum_up_to(u64 v) {
 }
 // Lane 63 has the wave's sum.
 
-// Sum over the lanes before this one; total over all.
+// Sum over the lanes before this one, of W waves; total over all.
+template <int W = kWaves>
 __device__ __forceinline__ u64 sum_before(u64 v, u64* wave_sums, u64& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const u64 x = sum_up_to(v);
@@ -336,7 +357,7 @@ __device__ __forceinline__ u64 sum_before(u64 v, u64* wave_sums, u64& total) {
   u64 before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
+  for (int i = 0; i < W; ++i) {
     if (i < wave) before += wave_sums[i];
     total += wave_sums[i];
   }
@@ -368,9 +389,10 @@ __device__ __forceinline__ bool last_of_row(uint32_t* arrived, int chunks, uint3
   return *shared == static_cast<uint32_t>(chunks - 1);
 }
 
+constexpr int kRowThreads = 512;   // of a workgroup that has a row to itself
 struct Shared {
   double step[32];
-  u64 wave[kWaves];
+  u64 wave[kRowThreads / 64];
   u64 found[4];
   uint32_t arrived, listed;
 };
@@ -378,15 +400,15 @@ struct Shared {
 // ------------------------------------------------------------------------------------- the draw
 // The token at which the sum of the kept weights passes u times their total.  sum(b): of block
 // b; kept(l, j): whether token j, with its weight not below min-p, is kept.
-template <typename E, typename Sum, typename Kept>
-__device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, Shared& s, Sum sum, Kept kept) {
+template <typename E, int T = kSampleThreads, typename Sum, typename Kept>
+__device__ __forceinline__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m, Shared& s, Sum sum, Kept kept) {
   const Row<E> r(a, row);
-  const int each = (g.blocks + kSampleThreads - 1) / kSampleThreads;   // consecutive blocks a lane
+  const int each = (g.blocks + T - 1) / T;   // consecutive blocks a lane
   const int b0 = threadIdx.x * each, b1 = min(b0 + each, g.blocks);
   u64 all = 0;
   for (int b = b0; b < b1; ++b) all += sum(b);
   u64 total;
-  u64 before = sum_before(all, s.wave, total);
+  u64 before = sum_before<T / 64>(all, s.wave, total);
   const float u = a.u[row];
   bool rest;
   const u64 target = !(u > 0.0f) ? 0 : u < 1.0f ? part_of(u, total, rest) : total - 1;
@@ -404,7 +426,7 @@ __device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, cons
   const int block = static_cast<int>(s.found[0]);
   before = s.found[1];
 #pragma unroll 1
-  for (int i = threadIdx.x; i < g.size; i += kSampleThreads) {
+  for (int i = threadIdx.x; i < g.size; i += T) {
     const int j = block * g.size - r.shift + i;
     u64 w = 0;
     float l = 0.0f;
@@ -414,7 +436,7 @@ __device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, cons
       if (w < m.least_weight || !kept(l, j)) w = 0;
     }
     u64 here;
-    const u64 mine_before = before + sum_before(w, s.wave, here);
+    const u64 mine_before = before + sum_before<T / 64>(w, s.wave, here);
     if (w > 0 && mine_before <= target && target < mine_before + w) {
       a.token[row] = j;
       if (a.logprob) {
@@ -428,19 +450,17 @@ __device__ void draw(const SampleView& a, int64_t row, const SampleGrid& g, cons
 }
 
 // -------------------------------------------------------------------------------------- pass one
-template <typename E>
-__global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a, SampleGrid g, char* ws) {
-  __shared__ u64 best_of[kWaves];
-  __shared__ float least_of[kWaves];
-  const int64_t row = blockIdx.y;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
-  const Row<E> r(a, row);
-  const RowSpace s(ws, row, g);
-  if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = 0;
+struct Top {
+  u64 place;     // of the largest logit
+  float least;   // the smallest logit of full groups
+};
+
+// Of a workgroup's part of a row; lane 0 of the workgroup has it, or (ALL) every lane.
+template <int T, bool ALL, typename E>
+__device__ __forceinline__ Top find_top(const Row<E>& r, Walk<E> walk, u64* place_of_wave, float* least_of_wave) {
   // a lane's largest logit and its group, later the group's first element that has it
   float best = -__builtin_inff(), least = __builtin_inff();
   int at = 0;
-  auto walk = walk_of(r, g);
   walk.run([&](int j, const float (&v)[8], bool full) {
     float top = v[0], low = v[0];
 #pragma unroll
@@ -459,44 +479,53 @@ __global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a
   if (best != -__builtin_inff())
     for (int i = 7; i >= 0; --i)
       if (at + i >= 0 && at + i < r.n && r.at(at + i) == best) first = at + i;
-  u64 place = place_of(best, first);
+  Top x{place_of(best, first), least};
+  const auto join = [&](u64 place, float low) {
+    x.place = place > x.place ? place : x.place;
+    x.least = fminf(x.least, low);
+  };
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const u64 x = __shfl_xor(place, o, 64);
-    place = x > place ? x : place;
-    least = fminf(least, __shfl_xor(least, o, 64));
-  }
-  if (lane == 0) {
-    best_of[wave] = place;
-    least_of[wave] = least;
+  for (int o = 32; o >= 1; o >>= 1) join(__shfl_xor(x.place, o, 64), __shfl_xor(x.least, o, 64));
+  if ((threadIdx.x & 63) == 0) {
+    place_of_wave[threadIdx.x >> 6] = x.place;
+    least_of_wave[threadIdx.x >> 6] = x.least;
   }
   __syncthreads();
+  if (ALL || threadIdx.x == 0)
+    for (int i = 0; i < T / 64; ++i) join(place_of_wave[i], least_of_wave[i]);
+  return x;
+}
+
+template <typename E>
+__global__ __launch_bounds__(kSampleThreads) void sample_top_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ u64 places[kWaves];
+  __shared__ float leasts[kWaves];
+  const int64_t row = blockIdx.y;
+  const int c = blockIdx.x;
+  const Row<E> r(a, row);
+  const RowSpace s(ws, row, g);
+  if (c == 0 && threadIdx.x == 0) s.state->arrived[0] = s.state->arrived[1] = 0;
+  const Top top = find_top<kSampleThreads, false>(r, walk_of(r, g, c), places, leasts);
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kWaves; ++i) {
-      place = best_of[i] > place ? best_of[i] : place;
-      least = fminf(least, least_of[i]);
-    }
-    s.best[c] = place;
-    s.least[c] = least;
+    s.best[c] = top.place;
+    s.least[c] = top.least;
   }
 }
 
 // -------------------------------------------------------------------------------------- pass two
-// The token of a row that needs no sums.
-__device__ __forceinline__ bool plain_row(const SampleView& a, int64_t row, const Limits& m, int c, RowState* state) {
+// Whether a row needs no sums; then its token is written by the workgroup that is told to.
+__device__ __forceinline__ bool plain_row(const SampleView& a, int64_t row, const Limits& m, bool write) {
   if (!m.empty && !m.greedy) return false;
-  if (c == 0 && threadIdx.x == 0) {
+  if (write && threadIdx.x == 0) {
     a.token[row] = m.empty ? -1 : m.first;
     if (a.logprob) a.logprob[row] = m.empty ? -__builtin_inff() : 0.0f;
-    state->mode = kDone;
   }
   return true;
 }
 
-// A row without top-k and top-p: the blocks' sums, and the draw.
-template <typename E>
-__device__ __forceinline__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m,
-                                         const RowSpace& s, Shared& sh, Walk<E>& walk) {
+// The blocks' sums of the weights not below min-p: put(block, sum) by lane 63.
+template <typename E, typename Put>
+__device__ __forceinline__ void sum_blocks(const Limits& m, Walk<E> walk, Put put) {
   u64 sum = 0;
   walk.run([&](int, const float (&v)[8], bool) {
 #pragma unroll
@@ -506,11 +535,18 @@ __device__ __forceinline__ void free_row(const SampleView& a, int64_t row, const
     }
   }, [&](int block) {
     sum = sum_up_to(sum);
-    if ((threadIdx.x & 63) == 63) tell(&s.sums[block], sum);
+    if ((threadIdx.x & 63) == 63) put(block, sum);
     sum = 0;
   });
+}
+
+// A row without top-k and top-p: the blocks' sums, and the draw.
+template <typename E>
+__device__ __forceinline__ void free_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m,
+                                         const RowSpace& s, Shared& sh, const Walk<E>& walk) {
+  sum_blocks(m, walk, [&](int b, u64 sum) { tell(&s.sums[b], sum); });
   if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
-  if (threadIdx.x == 0) s.state->mode = kDone;
+  if (threadIdx.x == 0) s.state->border.mode = kDone;
   draw<E>(a, row, g, m, sh, [&](int b) { return told(&s.sums[b]); }, [](float, int) { return true; });
 }
 
@@ -520,58 +556,196 @@ __global__ __launch_bounds__(kSampleThreads) void sample_free_kernel(SampleView 
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
   const Row<E> r(a, row);
-  auto walk = walk_of(r, g);
+  const auto walk = walk_of(r, g, blockIdx.x);
   const Limits m = limits_of(a, row, g, s, sh.step);
-  if (plain_row(a, row, m, blockIdx.x, s.state)) return;
+  if (plain_row(a, row, m, blockIdx.x == 0)) return;
   free_row(a, row, g, m, s, sh, walk);
 }
 
-// Counts and weights of the intervals, and from all chunks' the interval of the cut.
-template <typename E>
-__global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView a, SampleGrid g, char* ws) {
+// The same in one pass, for rows enough to give each a workgroup: the row stays in registers, as it lies in
+// memory, between its largest logit and its weights; G groups of eight elements a lane.  509 rows of
+// 50021 bf16 logits, temperature alone: XXX us, where the two passes take 51.
+template <typename E, int G>
+__global__ __launch_bounds__(kRowThreads) void sample_row_kernel(SampleView a) {
+  constexpr int T = kRowThreads, kRowWaves = T / 64;
   __shared__ Shared sh;
-  __shared__ u64 weights[kBins];
-  __shared__ uint32_t counts[kBins];
-  const int64_t row = blockIdx.y;
-  const RowSpace s(ws, row, g);
-  const int c = blockIdx.x, t = threadIdx.x;
+  __shared__ u64 sums[G * kRowWaves];   // of blocks of 512 elements
+  __shared__ u64 best_of[kRowWaves];
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const Row<E> r(a, row);
-  auto walk = walk_of(r, g);
-  for (int i = t; i < kBins; i += kSampleThreads) {
-    weights[i] = 0;
-    counts[i] = 0;
+  const E* l = r.p;
+  const RowGroups groups(l, r.n);
+  Raw<E> raw[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int j = (q * T + t) * 8 - groups.shift;
+    if (groups.full(j)) raw[q].load(l + j);
+    else raw[q].clear();
   }
-  const Limits m = limits_of(a, row, g, s, sh.step);
-  if (plain_row(a, row, m, c, s.state)) return;
-  if (m.k == 0 && m.p == 1.0f) {
-    free_row(a, row, g, m, s, sh, walk);
-    return;
+  const int edge = wave == 0 ? groups.edge(lane) : -1;
+  const float at_edge = edge >= 0 ? r.at(edge) : -__builtin_inff();
+  const Arguments given(a, row);
+  // a lane's largest logit and its group
+  float best = -__builtin_inff();
+  int at = 0;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    float v[8], top = -__builtin_inff();
+    raw[q].get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i]);   // passes over NaN
+    top = plain(top);
+    if (top > best) {
+      best = top;
+      at = (q * T + t) * 8 - groups.shift;
+    }
   }
+  int first = 0;
+  if (best != -__builtin_inff())
+    for (int i = 7; i >= 0; --i)
+      if (r.at(at + i) == best) first = at + i;
+  u64 place = place_of(best, first);
+  if (edge >= 0) {
+    const u64 x = place_of(at_edge, edge);
+    place = x > place ? x : place;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const u64 x = __shfl_xor(place, o, 64);
+    place = x > place ? x : place;
+  }
+  if (lane == 0) best_of[wave] = place;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRowWaves; ++i) place = best_of[i] > place ? best_of[i] : place;
+  const Limits m = limits_of(a, given, place, 0.0f, sh.step);
+  if (plain_row(a, row, m, true)) return;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    float v[8];
+    raw[q].forget();
+    raw[q].get(v);
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const u64 w = m.weight(plain(v[i]));
+      sum += w >= m.least_weight ? w : 0;
+    }
+    sum = sum_up_to(sum);
+    if (lane == 63) sums[q * kRowWaves + wave] = sum;
+  }
+  __syncthreads();
+  if (edge >= 0) {
+    const u64 w = m.weight(at_edge);
+    if (w >= m.least_weight) atomicAdd(&sums[(edge + groups.shift) / 512], w);
+  }
+  __syncthreads();
+  const SampleGrid g{1, G * kRowWaves, G * kRowWaves, 512, 0};
+  draw<E, T>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [](float, int) { return true; });
+}
+
+// Tokens (with top-k) or weights of the intervals.
+struct Bins {
+  u64 weights[kBins];
+  uint32_t counts[kBins];
+  __device__ __forceinline__ void clear(int threads) {
+    for (int i = threadIdx.x; i < kBins; i += threads) {
+      weights[i] = 0;
+      counts[i] = 0;
+    }
+  }
+};
+
+template <typename E>
+__device__ __forceinline__ void fill_bins(const Limits& m, Walk<E> walk, Bins& bins) {
   if (m.k > 0) {
     walk.run([&](int, const float (&v)[8], bool) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (v[i] != -__builtin_inff()) atomicAdd(&counts[m.bin(v[i])], 1u);
+        if (v[i] != -__builtin_inff()) atomicAdd(&bins.counts[m.bin(v[i])], 1u);
     }, [](int) {});
-  } else {
-    u64 rest = 0;   // of the last interval, which half of the tokens fall into and more
-    walk.run([&](int, const float (&v)[8], bool) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const u64 w = m.weight(v[i]);
-        const int bin = v[i] == -__builtin_inff() ? kBins - 1 : m.bin(v[i]);
-        if (bin < kBins - 1) atomicAdd(&weights[bin], w);
-        else rest += w;
-      }
-    }, [](int) {});
-    rest = sum_up_to(rest);
-    if ((t & 63) == 63) atomicAdd(&weights[kBins - 1], rest);
+    return;
   }
+  u64 rest = 0;   // of the last interval, which half of the tokens fall into and more
+  walk.run([&](int, const float (&v)[8], bool) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const u64 w = m.weight(v[i]);
+      const int bin = v[i] == -__builtin_inff() ? kBins - 1 : m.bin(v[i]);
+      if (bin < kBins - 1) atomicAdd(&bins.weights[bin], w);
+      else rest += w;
+    }
+  }, [](int) {});
+  rest = sum_up_to(rest);
+  if ((threadIdx.x & 63) == 63) atomicAdd(&bins.weights[kBins - 1], rest);
+}
+
+// The intervals that the cut lies in, from the consecutive ones that each of T lanes has: one lane writes them.
+template <int T>
+__device__ __forceinline__ void find_border(const Limits& m, const u64 (&w)[kBins / T], const uint32_t (&n)[kBins / T],
+                                            Shared& sh, Border* out) {
+  constexpr int kEach = kBins / T;
+  const int t = threadIdx.x;
+  u64 all_w = 0, all_n = 0, total, count;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    all_w += w[i];
+    all_n += n[i];
+  }
+  u64 before_w = sum_before<T / 64>(all_w, sh.wave, total), before_n = sum_before<T / 64>(all_n, sh.wave, count);
+  // with top-k the interval of the k-th token, and all before it where the list holds them; top-p
+  // alone: the interval in which the sum reaches p
+  const bool by_k = m.k > 0;
+  if (by_k && static_cast<u64>(m.k) >= count) {   // no more than k tokens: top-k limits nothing
+    if (t == 0) *out = Border{0, 0, 0, kBins, kBins, m.p < 1.0f ? kSearch : kListed};
+    return;
+  }
+  bool rest = false;
+  u64 want = by_k ? 0 : part_of(m.p, total, rest);
+  want += rest || want == 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool here = by_k ? before_n < static_cast<u64>(m.k) && static_cast<u64>(m.k) <= before_n + n[i]
+                           : before_w < want && want <= before_w + w[i];
+    if (here) {
+      const bool all = by_k && before_n + n[i] <= kList;
+      const int hi = t * kEach + i;
+      // top-p may cut anywhere above the k-th token; how many tokens a weight's interval holds is
+      // seen when they are listed
+      *out = Border{total, all ? 0 : before_w, all ? 0 : static_cast<uint32_t>(before_n), all ? 0 : hi, hi,
+                    all || (n[i] <= kList && !(by_k && m.p < 1.0f)) ? kListed : kSearch};
+    }
+    before_w += w[i];
+    before_n += n[i];
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView a, SampleGrid g, char* ws) {
+  __shared__ Shared sh;
+  __shared__ Bins bins;
+  const int64_t row = blockIdx.y;
+  const RowSpace s(ws, row, g);
+  const int c = blockIdx.x, t = threadIdx.x;
+  const Row<E> r(a, row);
+  const auto walk = walk_of(r, g, c);
+  bins.clear(kSampleThreads);
+  const Limits m = limits_of(a, row, g, s, sh.step);
+  if (plain_row(a, row, m, c == 0)) {
+    if (c == 0 && t == 0) s.state->border.mode = kDone;
+    return;
+  }
+  if (m.k == 0 && m.p == 1.0f) {
+    free_row(a, row, g, m, s, sh, walk);
+    return;
+  }
+  fill_bins(m, walk, bins);
   __syncthreads();
   if (g.chunks > 1) {
     for (int i = t; i < kBins; i += kSampleThreads) {
-      if (m.k == 0) tell(&s.weights[c * kBins + i], weights[i]);
-      else tell(&s.counts[c * kBins + i], counts[i]);
+      if (m.k == 0) tell(&s.weights[c * kBins + i], bins.weights[i]);
+      else tell(&s.counts[c * kBins + i], bins.counts[i]);
     }
   }
   if (!last_of_row(&s.state->arrived[0], g.chunks, &sh.arrived)) return;
@@ -580,16 +754,10 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
   uint32_t n[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int bin = t * kEach + i;
-    w[i] = weights[bin];
-    n[i] = counts[bin];
+    w[i] = g.chunks > 1 ? 0 : bins.weights[t * kEach + i];
+    n[i] = g.chunks > 1 ? 0 : bins.counts[t * kEach + i];
   }
   if (g.chunks > 1) {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      w[i] = 0;
-      n[i] = 0;
-    }
     // all chunks' loads before the first sum
     static_assert(kEach == 2, "a lane's two counts are read as one word");
     u64 part[kMostChunks][kEach];
@@ -613,47 +781,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
       }
     }
   }
-  u64 all_w = 0, all_n = 0, total, count;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    all_w += w[i];
-    all_n += n[i];
-  }
-  const u64 w0 = sum_before(all_w, sh.wave, total), n0 = sum_before(all_n, sh.wave, count);
-  // with top-k the interval of the k-th token, and all before it where the list holds them; top-p
-  // alone: the interval in which the sum reaches p
-  const bool by_k = m.k > 0;
-  if (by_k && static_cast<u64>(m.k) >= count) {   // no more than k tokens: top-k limits nothing
-    if (t == 0) {
-      s.state->lo = s.state->hi = kBins;
-      s.state->mode = m.p < 1.0f ? kSearch : kListed;
-    }
-    return;
-  }
-  bool rest = false;
-  u64 want = by_k ? 0 : part_of(m.p, total, rest);
-  want += rest || want == 0;
-  u64 before_w = w0, before_n = n0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const bool here = by_k ? before_n < static_cast<u64>(m.k) && static_cast<u64>(m.k) <= before_n + n[i]
-                           : before_w < want && want <= before_w + w[i];
-    if (here) {
-      RowState x = *s.state;
-      x.total = total;
-      x.hi = t * kEach + i;
-      const bool all = by_k && before_n + n[i] <= kList;
-      x.lo = all ? 0 : x.hi;
-      x.weight_before = all ? 0 : before_w;
-      x.count_before = all ? 0 : static_cast<uint32_t>(before_n);
-      // top-p may cut anywhere above the k-th token; how many tokens a weight's interval holds is
-      // seen when they are listed
-      x.mode = all || (n[i] <= kList && !(by_k && m.p < 1.0f)) ? kListed : kSearch;
-      *s.state = x;
-    }
-    before_w += w[i];
-    before_n += n[i];
-  }
+  find_border<kSampleThreads>(m, w, n, sh, &s.state->border);
 }
 
 // ------------------------------------------------------------------------------------ pass three
@@ -666,13 +794,15 @@ struct ListSpace {
 // The lowest place that is kept: in falling order, the first one at which the count (by_count) or
 // the sum of the weights reaches want >= 1, and 0 where none does.  Digit by digit, of what `each` calls its argument with: (place, weight) of every
 // token.  The places have the bits of `base` but for the last `bits`.
-template <typename Each>
+template <int T, typename Each>
 __device__ __forceinline__ u64 find_cut(bool by_count, u64 want, u64 base, int bits, Shared& s, ListSpace& list, Each each) {
   const int t = threadIdx.x;
   u64 prefix = base >> bits << bits;
   __syncthreads();
-  list.bin_weights[t] = 0;
-  list.bin_counts[t] = 0;
+  if (t < 256) {
+    list.bin_weights[t] = 0;
+    list.bin_counts[t] = 0;
+  }
   if (t == 0) s.found[2] = 0;
   __syncthreads();
   for (int known = bits; known > 0;) {
@@ -684,12 +814,16 @@ __device__ __forceinline__ u64 find_cut(bool by_count, u64 want, u64 base, int b
       if (!by_count) atomicAdd(&list.bin_weights[b], w);
     });
     __syncthreads();
-    const uint32_t count = list.bin_counts[t];
-    const u64 here = by_count ? count : list.bin_weights[t];
-    list.bin_counts[t] = 0;
-    list.bin_weights[t] = 0;
+    uint32_t count = 0;
+    u64 here = 0;
+    if (t < 256) {
+      count = list.bin_counts[t];
+      here = by_count ? count : list.bin_weights[t];
+      list.bin_counts[t] = 0;
+      list.bin_weights[t] = 0;
+    }
     u64 total;
-    const u64 before = sum_before(here, s.wave, total);
+    const u64 before = sum_before<T / 64>(here, s.wave, total);
     if (before < want && want <= before + here) {
       s.found[0] = 255 - t;
       s.found[1] = want - before;
@@ -713,7 +847,7 @@ __device__ __forceinline__ u64 find_cut(bool by_count, u64 want, u64 base, int b
 
 // The cut of a row's top-k and top-p, from the tokens that `each` goes through; what lies before
 // them counts and weighs as given.
-template <typename Each>
+template <int T, typename Each>
 __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_before, u64 count_before, u64 base, int bits,
                                       Shared& s, ListSpace& list, Each each) {
   u64 cut = 0;
@@ -724,7 +858,7 @@ __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_bef
       if (m.k > 0) {   // p of the first k
         u64 sum = 0;
         each([&](u64 place, u64 w) { sum += place >= cut ? w : 0; });
-        sum_before(sum, s.wave, total);
+        sum_before<T / 64>(sum, s.wave, total);
         total += weight_before;
       }
       bool rest;
@@ -732,14 +866,15 @@ __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_bef
       want += rest || want == 0;
       want -= weight_before;
     }
-    const u64 found = find_cut(by_k != 0, want, base, bits, s, list, each);
+    const u64 found = find_cut<T>(by_k != 0, want, base, bits, s, list, each);
     cut = found > cut ? found : cut;
   }
   return cut;
 }
 
-// The same for n <= kSampleThreads listed tokens, one a lane, which are sorted: up to 36 exchanges, of which three go
+// The same for n <= T listed tokens, one a lane, which are sorted: up to 45 exchanges, of which six go
 // through LDS, where the digits have some ten barriers each.
+template <int T>
 __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight_before, u64 count_before, int n, Shared& s,
                                           ListSpace& list) {
   const int t = threadIdx.x;
@@ -767,7 +902,7 @@ __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight
   if (m.k > 0) {
     keep = keep && t + count_before < static_cast<u64>(m.k);
     if (m.p < 1.0f) {
-      sum_before(keep ? w : 0, s.wave, total);
+      sum_before<T / 64>(keep ? w : 0, s.wave, total);
       total += weight_before;
     }
   }
@@ -776,7 +911,7 @@ __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight
     u64 want = part_of(m.p, total, rest);
     want += rest || want == 0;
     u64 all;
-    const u64 before = sum_before(w, s.wave, all);   // by every lane: it has barriers
+    const u64 before = sum_before<T / 64>(w, s.wave, all);   // by every lane: it has barriers
     keep = keep && before + weight_before < want;
   }
   // the kept ones are the first ones: the last of them is the cut
@@ -787,8 +922,86 @@ __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight
   __syncthreads();
   int count = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) count += static_cast<int>(s.wave[i]);
+  for (int i = 0; i < T / 64; ++i) count += static_cast<int>(s.wave[i]);
   return count > 0 ? list.place[count - 1] : ~u64(0);
+}
+
+// The tokens of the border's intervals into list.place, as far as it goes (sh.listed: their number), and the
+// sums of what lies above them: put(block, sum) by lane 63.
+template <typename E, typename Put>
+__device__ __forceinline__ void list_tokens(const Limits& m, const Border& x, Walk<E> walk, Shared& sh, ListSpace& list,
+                                            Put put) {
+  u64 sum = 0;
+  walk.run([&](int j, const float (&v)[8], bool) {
+    unsigned listed = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
+      if (bin < x.lo) {
+        const u64 w = m.weight(v[i]);
+        sum += w >= m.least_weight ? w : 0;
+      } else if (bin <= x.hi && bin < kBins) {
+        listed |= 1u << i;
+      }
+    }
+    if (listed == 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (listed >> i & 1) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kList) list.place[at] = place_of(v[i], j + i);
+      }
+  }, [&](int block) {
+    if (x.lo > 0) sum = sum_up_to(sum);
+    if ((threadIdx.x & 63) == 63) put(block, sum);
+    sum = 0;
+  });
+}
+
+// The cut and the draw, by one workgroup: from the n listed tokens, or where they are more than the list holds
+// the whole row.  sums: of the blocks, the listed tokens aside.
+template <typename E, int T>
+__device__ __forceinline__ void finish_row(const SampleView& a, int64_t row, const SampleGrid& g, const Limits& m,
+                                           const Border& x, int n, const Row<E>& r, Shared& sh, ListSpace& list, u64* sums) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
+  const bool in_list = x.mode == kListed && n <= kList;
+  u64 cut = 0, base = 0, other = 0;
+  if (in_list && n > 0) {
+    base = list.place[0];
+    for (int i = t; i < n; i += T) other |= list.place[i] ^ base;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
+  }
+  if (lane == 0) sh.wave[wave] = other;
+  if (!in_list)
+    for (int b = t; b < g.blocks; b += T) sums[b] = 0;
+  __syncthreads();
+  other = 0;
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) other |= sh.wave[i];
+  const auto each = [&](auto f) {
+    if (in_list) {
+#pragma unroll 1
+      for (int i = t; i < n; i += T) f(list.place[i], m.weight(logit_at(list.place[i])));
+    } else {
+#pragma unroll 1
+      for (int j = t; j < r.n; j += T) {
+        const float l = r.at(j);
+        f(place_of(l, j), m.weight(l));
+      }
+    }
+  };
+  if (in_list && x.lo < kBins && n <= T)
+    cut = cut_of_few<T>(m, x.total, x.weight_before, x.count_before, n, sh, list);
+  else if (!in_list || x.lo < kBins)
+    cut = cut_of<T>(m, x.total, in_list ? x.weight_before : 0, in_list ? x.count_before : 0, base,
+                    in_list ? 64 - __clzll(other) : 32 + kIndexBits, sh, list, each);
+  __syncthreads();
+  each([&](u64 place, u64 w) {
+    if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
+  });
+  __syncthreads();
+  draw<E, T>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [&](float l, int j) { return place_of(l, j) >= cut; });
 }
 
 template <typename E>
@@ -798,39 +1011,15 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
   __shared__ u64 sums[kMostBlocks];
   const int64_t row = blockIdx.y;
   const RowSpace s(ws, row, g);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x, t = threadIdx.x;
+  const int lane = threadIdx.x & 63, c = blockIdx.x, t = threadIdx.x;
   const Row<E> r(a, row);
-  auto walk = walk_of(r, g);
-  const RowState x = *s.state;
+  const auto walk = walk_of(r, g, c);
+  const Border x = s.state->border;
   if (t == 0) sh.listed = 0;
   const Limits m = limits_of(a, row, g, s, sh.step);
   if (x.mode == kDone) return;
   if (x.mode == kListed) {
-    u64 sum = 0;
-    walk.run([&](int j, const float (&v)[8], bool) {
-      unsigned listed = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
-        if (bin < x.lo) {
-          const u64 w = m.weight(v[i]);
-          sum += w >= m.least_weight ? w : 0;
-        } else if (bin <= x.hi && bin < kBins) {
-          listed |= 1u << i;
-        }
-      }
-      if (listed == 0) return;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (listed >> i & 1) {
-          const uint32_t at = atomicAdd(&sh.listed, 1u);
-          if (at < kList) list.place[at] = place_of(v[i], j + i);
-        }
-    }, [&](int block) {
-      if (x.lo > 0) sum = sum_up_to(sum);
-      if (lane == 63) tell(&s.sums[block], sum);
-      sum = 0;
-    });
+    list_tokens(m, x, walk, sh, list, [&](int b, u64 sum) { tell(&s.sums[b], sum); });
     if (g.chunks > 1) {
       __syncthreads();
       const uint32_t mine = sh.listed;
@@ -840,13 +1029,11 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
     }
   }
   if (!last_of_row(&s.state->arrived[1], g.chunks, &sh.arrived)) return;
-  // the listed tokens, or where they are more than the list holds the whole row, by this workgroup
   int n = 0, before = 0;
   const int part = t / 16;   // sixteen lanes for a chunk's list
   static_assert(kMostChunks * 16 <= kSampleThreads, "a row of lanes a chunk");
-  uint32_t count = 0;
   if (x.mode == kListed) {
-    count = g.chunks > 1 ? (lane < g.chunks ? told(&s.listed[lane]) : 0) : (lane == 0 ? sh.listed : 0);
+    uint32_t count = g.chunks > 1 ? (lane < g.chunks ? told(&s.listed[lane]) : 0) : (lane == 0 ? sh.listed : 0);
 #pragma unroll
     for (int i = 0; i < kMostChunks; ++i) {
       const int here = min(__shfl(static_cast<int>(count), i, 64), kList + 1);
@@ -854,54 +1041,74 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
       n += here;
     }
     count = __shfl(count, part, 64);
+    if (g.chunks > 1 && n <= kList && part < g.chunks)
+      for (uint32_t i = t % 16; i < count; i += 16) list.place[before + i] = told(&s.list[part * kList + i]);
+    for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = told(&s.sums[b]);
+    __syncthreads();
   }
-  const bool in_list = x.mode == kListed && n <= kList;
-  u64 cut = 0, base = 0, other = 0;
-  if (in_list && n > 0) {
-    if (g.chunks > 1) {
-      if (part < g.chunks)
-        for (uint32_t i = t % 16; i < count; i += 16) list.place[before + i] = told(&s.list[part * kList + i]);
-      __syncthreads();
-    }
-    base = list.place[0];
-    for (int i = t; i < n; i += kSampleThreads) other |= list.place[i] ^ base;
+  finish_row<E, kSampleThreads>(a, row, g, m, x, n, r, sh, list, sums);
+}
+
+// ----------------------------------------------------------------------------- a row a workgroup
+// All passes in one launch, for rows short enough that one workgroup is as fast as several with their two more
+// launches: XXX
+template <typename E>
+__global__ __launch_bounds__(kRowThreads) void sample_short_kernel(SampleView a, SampleGrid g) {
+  constexpr int T = kRowThreads;
+  __shared__ Shared sh;
+  __shared__ Bins bins;
+  __shared__ ListSpace list;
+  __shared__ u64 sums[kShortBlocks], places[T / 64];
+  __shared__ float leasts[T / 64];
+  __shared__ Border border;
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x;
+  const Row<E> r(a, row);
+  const auto walk = walk_of<T>(r, g, 0);
+  const Arguments given(a, row);
+  bins.clear(T);
+  if (t == 0) sh.listed = 0;
+  const Top top = find_top<T, true>(r, walk, places, leasts);
+  const Limits m = limits_of(a, given, top.place, top.least, sh.step);
+  if (plain_row(a, row, m, true)) return;
+  const auto put = [&](int b, u64 sum) { sums[b] = sum; };
+  if (m.k == 0 && m.p == 1.0f) {
+    sum_blocks(m, walk, put);
+    __syncthreads();
+    draw<E, T>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [](float, int) { return true; });
+    return;
+  }
+  fill_bins(m, walk, bins);
+  __syncthreads();
+  constexpr int kEach = kBins / T;
+  u64 w[kEach];
+  uint32_t n[kEach];
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
+  for (int i = 0; i < kEach; ++i) {
+    w[i] = bins.weights[t * kEach + i];
+    n[i] = bins.counts[t * kEach + i];
   }
-  if (lane == 0) sh.found[wave] = other;
-  for (int b = t; b < g.blocks; b += kSampleThreads) sums[b] = in_list ? told(&s.sums[b]) : 0;
+  find_border<T>(m, w, n, sh, &border);
   __syncthreads();
-  other = sh.found[0] | sh.found[1] | sh.found[2] | sh.found[3];
-  const auto each = [&](auto f) {
-    if (in_list) {
-#pragma unroll 1
-      for (int i = t; i < n; i += kSampleThreads) f(list.place[i], m.weight(logit_at(list.place[i])));
-    } else {
-#pragma unroll 1
-      for (int j = t; j < r.n; j += kSampleThreads) {
-        const float l = r.at(j);
-        f(place_of(l, j), m.weight(l));
-      }
-    }
-  };
-  if (in_list && x.lo < kBins && n <= kSampleThreads)
-    cut = cut_of_few(m, x.total, x.weight_before, x.count_before, n, sh, list);
-  else if (!in_list || x.lo < kBins)
-    cut = cut_of(m, x.total, in_list ? x.weight_before : 0, in_list ? x.count_before : 0, base,
-                 in_list ? 64 - __clzll(other) : 32 + kIndexBits, sh, list, each);
+  const Border x = border;
+  if (x.mode == kListed) list_tokens(m, x, walk, sh, list, put);
   __syncthreads();
-  each([&](u64 place, u64 w) {
-    if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
-  });
-  __syncthreads();
-  draw<E>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [&](float l, int j) { return place_of(l, j) >= cut; });
+  finish_row<E, T>(a, row, g, m, x, static_cast<int>(sh.listed), r, sh, list, sums);
 }
 
 // ------------------------------------------------------------------------------------------ host
-static SampleGrid sample_grid(int64_t n_rows, int64_t vocab) {
+static SampleGrid whole_row(int64_t vocab) {
   SampleGrid g;
   g.size = vocab <= (1 << 20) ? 512 : vocab <= (1 << 21) ? 1024 : 2048;
   g.blocks = static_cast<int>((vocab + 7 + g.size - 1) / g.size);   // wherever the row begins
+  g.chunks = 1;
+  g.blocks_a_chunk = g.blocks;
+  g.row_bytes = 0;
+  return g;
+}
+
+static SampleGrid sample_grid(int64_t n_rows, int64_t vocab) {
+  SampleGrid g = whole_row(vocab);
   // about four workgroups a CU, and a block at least for each of their waves
   int64_t chunks = 4 * device_cus() / n_rows;
   if (chunks > (g.blocks + kWaves - 1) / kWaves) chunks = (g.blocks + kWaves - 1) / kWaves;
@@ -919,8 +1126,39 @@ size_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
   return static_cast<size_t>(rows) * sample_grid(rows, vocab).row_bytes;
 }
 
+// Whether rows without top-k and top-p are worked off in registers: G, or 0.
+template <typename E>
+static int row_groups(const SampleView& v) {
+  const int64_t w = v.vocab + 7;
+  if (v.top_k || v.top_p || (v.n_rows < kRowsForOnePass && w > kRowThreads * 8 * 4)) return 0;
+  for (int g : {2, 4, 8, 16})
+    if (w <= int64_t(kRowThreads) * 8 * g) return g;
+  return sizeof(E) == 2 && w <= int64_t(kRowThreads) * 8 * 25 ? 25 : 0;
+}
+
+template <typename E>
+static bool sample_rows(const SampleView& v, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(v.n_rows)), threads(kRowThreads);
+  switch (row_groups<E>(v)) {
+    case 2: sample_row_kernel<E, 2><<<grid, threads, 0, s>>>(v); return true;
+    case 4: sample_row_kernel<E, 4><<<grid, threads, 0, s>>>(v); return true;
+    case 8: sample_row_kernel<E, 8><<<grid, threads, 0, s>>>(v); return true;
+    case 16: sample_row_kernel<E, 16><<<grid, threads, 0, s>>>(v); return true;
+    case 25:
+      if constexpr (sizeof(E) == 2) sample_row_kernel<E, 25><<<grid, threads, 0, s>>>(v);
+      return true;
+    default: return false;
+  }
+}
+
 template <typename E>
 static void sample(const SampleView& v, char* ws, hipStream_t s) {
+  if (sample_rows<E>(v, s)) return;
+  const SampleGrid all = whole_row(v.vocab);
+  if (all.size == 512 && all.blocks <= kShortBlocks) {
+    sample_short_kernel<E><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(kRowThreads), 0, s>>>(v, all);
+    return;
+  }
   for (int64_t at = 0; at < v.n_rows; at += kRowsAtOnce) {
     SampleView a = v;
     a.n_rows = v.n_rows - at < kRowsAtOnce ? v.n_rows - at : kRowsAtOnce;
