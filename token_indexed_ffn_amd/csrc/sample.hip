@@ -10,9 +10,10 @@
 // pass finds the largest logit, a second one counts and weighs the tokens in kBins intervals of
 // the logit, which tells the interval that the cut falls into, and a third one lists that
 // interval's tokens and sums the weights above it, by blocks of the row.  The list gives the
-// cut, the blocks' sums the block of the drawn token.  A row is dealt out to several workgroups
-// (as many rows as fill the GPU take one each); the last of them to arrive goes on with the row.
-// Without top-k and top-p the second pass sums the blocks and the third is not needed.
+// cut, the blocks' sums the block of the drawn token.  Without top-k and top-p the second pass sums the
+// blocks and the third is not needed.  A long row among few is dealt out to several workgroups, a launch for each
+// pass, and the last of them to arrive goes on with the row; otherwise a workgroup takes a row through
+// all passes.
 #include "model_ops.h"
 #include "row_io.h"
 
@@ -26,9 +27,6 @@ constexpr int kBins = 512;          // two a lane of a workgroup
 constexpr int kList = 2048;         // listed tokens
 constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
 constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all intervals' loads in flight at once
-constexpr int kRowsAtOnce = 1024;   // rows that the workspace holds
-constexpr int64_t kRowsForOnePass = 128;
-constexpr int kShortBlocks = 33;    // of a row that one workgroup takes through all passes
 
 // --------------------------------------------------------------------------- logits and weights
 // NaN as -inf, +inf as the largest finite number.
@@ -562,9 +560,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_free_kernel(SampleView 
   free_row(a, row, g, m, s, sh, walk);
 }
 
-// The same in one pass, for rows enough to give each a workgroup: the row stays in registers, as it lies in
-// memory, between its largest logit and its weights; G groups of eight elements a lane.  509 rows of
-// 50021 bf16 logits, temperature alone: XXX us, where the two passes take 51.
+// The same in one pass: the row stays in registers, as it lies in memory, between its largest logit and its
+// weights; G groups of eight elements a lane.
 template <typename E, int G>
 __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(SampleView a) {
   constexpr int T = kRowThreads, kRowWaves = T / 64;
@@ -1050,15 +1047,13 @@ __global__ __launch_bounds__(kSampleThreads) void sample_cut_kernel(SampleView a
 }
 
 // ----------------------------------------------------------------------------- a row a workgroup
-// All passes in one launch, for rows short enough that one workgroup is as fast as several with their two more
-// launches: XXX
-template <typename E>
-__global__ __launch_bounds__(kRowThreads) void sample_short_kernel(SampleView a, SampleGrid g) {
-  constexpr int T = kRowThreads;
+// All passes in one launch, the later ones from the caches.
+template <typename E, int T>
+__global__ __launch_bounds__(T) void sample_whole_kernel(SampleView a, SampleGrid g) {
   __shared__ Shared sh;
   __shared__ Bins bins;
   __shared__ ListSpace list;
-  __shared__ u64 sums[kShortBlocks], places[T / 64];
+  __shared__ u64 sums[kMostBlocks], places[T / 64];
   __shared__ float leasts[T / 64];
   __shared__ Border border;
   const int64_t row = blockIdx.x;
@@ -1121,16 +1116,25 @@ static SampleGrid sample_grid(int64_t n_rows, int64_t vocab) {
   return g;
 }
 
+// A row gets one workgroup where there are rows for all CUs, or where it is short.  bf16, us with one and with
+// several workgroups a row: top-k and top-p, 64 rows of 2000: 15, 20; of 16000: 23, 25; of 32000: 32, 30; of
+// 100352: 66, 36; 256 rows of 32000: 33, 41; of 100352: 69, 71; 512 rows: 45, 57; 95, 110.
+constexpr int kShortBlocks = 33;
+static bool one_workgroup(int64_t n_rows, const SampleGrid& g) { return n_rows >= device_cus() || g.blocks <= kShortBlocks; }
+
 size_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
-  const int64_t rows = n_rows < kRowsAtOnce ? n_rows : kRowsAtOnce;
-  return static_cast<size_t>(rows) * sample_grid(rows, vocab).row_bytes;
+  const SampleGrid g = sample_grid(n_rows, vocab);
+  return one_workgroup(n_rows, g) ? 0 : static_cast<size_t>(n_rows) * g.row_bytes;
 }
 
-// Whether rows without top-k and top-p are worked off in registers: G, or 0.
+// Groups of eight elements a lane with which rows of temperature and min-p alone are worked off in registers, or
+// 0: long rows too few to occupy half of the CUs are faster in parts.  bf16, us in registers and
+// otherwise: 64 rows of 16000: 9, 12; of 50021: 20, 16; 128 rows: 21, 23; 512 rows: 41, 52; 512 rows of
+// 100352: 68, 86.
 template <typename E>
 static int row_groups(const SampleView& v) {
   const int64_t w = v.vocab + 7;
-  if (v.top_k || v.top_p || (v.n_rows < kRowsForOnePass && w > kRowThreads * 8 * 4)) return 0;
+  if (v.top_k || v.top_p || (v.n_rows < device_cus() / 2 && w > kRowThreads * 8 * 4)) return 0;
   for (int g : {2, 4, 8, 16})
     if (w <= int64_t(kRowThreads) * 8 * g) return g;
   return sizeof(E) == 2 && w <= int64_t(kRowThreads) * 8 * 25 ? 25 : 0;
@@ -1152,34 +1156,24 @@ static bool sample_rows(const SampleView& v, hipStream_t s) {
 }
 
 template <typename E>
-static void sample(const SampleView& v, char* ws, hipStream_t s) {
-  if (sample_rows<E>(v, s)) return;
-  const SampleGrid all = whole_row(v.vocab);
-  if (all.size == 512 && all.blocks <= kShortBlocks) {
-    sample_short_kernel<E><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(kRowThreads), 0, s>>>(v, all);
+static void sample(const SampleView& a, char* ws, hipStream_t s) {
+  if (sample_rows<E>(a, s)) return;
+  SampleGrid g = sample_grid(a.n_rows, a.vocab);
+  if (one_workgroup(a.n_rows, g)) {
+    g = whole_row(a.vocab);
+    const dim3 grid(static_cast<unsigned>(a.n_rows));
+    // four waves where a row has no more than two blocks for each: with eight 2048 rows of 500 take 72 us
+    if (g.blocks <= 9) sample_whole_kernel<E, 256><<<grid, dim3(256), 0, s>>>(a, g);
+    else sample_whole_kernel<E, 512><<<grid, dim3(512), 0, s>>>(a, g);
     return;
   }
-  for (int64_t at = 0; at < v.n_rows; at += kRowsAtOnce) {
-    SampleView a = v;
-    a.n_rows = v.n_rows - at < kRowsAtOnce ? v.n_rows - at : kRowsAtOnce;
-    a.logits += at * a.stride * static_cast<int64_t>(sizeof(E));
-    a.u += at;
-    if (a.temperature) a.temperature += at;
-    if (a.top_k) a.top_k += at;
-    if (a.top_p) a.top_p += at;
-    if (a.min_p) a.min_p += at;
-    a.token += at;
-    if (a.logprob) a.logprob += at;
-    // the last rows keep the first ones' layout, which the workspace has been made for
-    const SampleGrid g = sample_grid(v.n_rows < kRowsAtOnce ? v.n_rows : kRowsAtOnce, v.vocab);
-    const dim3 grid(g.chunks, static_cast<unsigned>(a.n_rows)), threads(kSampleThreads);
-    sample_top_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
-    if (!a.top_k && !a.top_p) {
-      sample_free_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
-    } else {
-      sample_bins_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
-      sample_cut_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
-    }
+  const dim3 grid(g.chunks, static_cast<unsigned>(a.n_rows)), threads(kSampleThreads);
+  sample_top_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+  if (!a.top_k && !a.top_p) {
+    sample_free_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+  } else {
+    sample_bins_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
+    sample_cut_kernel<E><<<grid, threads, 0, s>>>(a, g, ws);
   }
 }
 
