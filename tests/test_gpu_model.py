@@ -481,7 +481,7 @@ def test_sampling_of_whole_vocabularies(st, dtype, n, v):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("v", [6, 3000, 50021])
+@pytest.mark.parametrize("v", [6, 3000, 9000, 50021])
 def test_sampling_of_equal_and_ruled_out_logits(st, dtype, v):
     """Ties at every border, rows without a token, infinities and NaN, the type's lowest value."""
     import torch
@@ -507,6 +507,44 @@ def test_sampling_of_equal_and_ruled_out_logits(st, dtype, v):
         run_sample(st, logits, [r] * n, top_k=[max(1, v // 4)] * n, top_p=[0.25] * n)
         run_sample(st, logits, [r] * n, top_k=[1 + i] * n, min_p=[1.0] * n, temperature=[1e-30] * n)
         run_sample(st, logits, [r] * n, temperature=[float("inf")] * n, top_k=[3] * n)
+
+
+def by_sorting(l, u, t, k, p, low):
+    """One row's token, for rows that the oracle's loops take long for (no ties at a border)."""
+    order = np.argsort(-l, kind="stable")
+    w = np.exp((l[order] - l[order[0]]) / t)
+    count = k if 0 < k < len(l) else len(l)
+    if p < 1:
+        sums = np.cumsum(w[:count])
+        count = 1 + int(np.searchsorted(sums, p * sums[-1]))
+    at = np.sort(order[:count][w[:count] >= low])
+    sums = np.cumsum(np.exp((l[at] - l.max()) / t))
+    return int(at[np.searchsorted(sums, u * sums[-1], side="right")])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v", [(2, 1048577), (3, 2000003), (2, 1 << 22), (260, 30011)])
+def test_sampling_of_the_longest_rows(st, dtype, n, v):
+    print(dtype, n, v, flush=True)
+    logits = rand((n, v), dtype, 74, 3.0)
+    host = to_np(logits)
+    rng = np.random.default_rng(v)
+    f = lambda a: a.astype(np.float32).astype(np.float64)
+    u, t, p, low = f(rng.random(n)), f(0.5 + rng.random(n)), f(0.5 + 0.6 * rng.random(n)), f(0.01 * rng.random(n))
+    k = np.where(rng.random(n) < 0.5, 0, rng.integers(1, v, n))
+    none = np.zeros(n)
+    for kk, pp, ll in ((none, none + 1, none), (none, none + 1, low), (k, none + 1, none), (none, p, none), (k, p, low)):
+        limits = {}
+        if kk is not none:
+            limits["top_k"] = ints(kk)
+        if (pp < 1).any():
+            limits["top_p"] = floats(pp)
+        if ll is not none:
+            limits["min_p"] = floats(ll)
+        got = st.staple_sample(logits, floats(u), temperature=floats(t), **limits)["token"].cpu().numpy()
+        rows = range(n) if n < 10 else range(0, n, 37)
+        assert [int(got[i]) for i in rows] == [by_sorting(host[i], u[i], t[i], int(kk[i]), pp[i], ll[i]) for i in rows]
+    fine(st)
 
 
 def test_sampling_with_arguments_at_their_ends(st):

@@ -45,6 +45,8 @@ template <> struct Raw<bf16_t> {
   u32x4_t a;
   __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4_t*>(p); }
   __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
+  // Of data that nothing reads again soon: it is not to push other lines out of the caches.
+  __device__ __forceinline__ void load_once(const bf16_t* p) { a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p)); }
   // What was made of these elements is made again after this, rather than kept in registers.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -64,6 +66,10 @@ template <> struct Raw<float> {
   __device__ __forceinline__ void clear() {
     const float x = -__builtin_inff();
     a = b = f32x4_t{x, x, x, x};
+  }
+  __device__ __forceinline__ void load_once(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p + 4));
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a), "+v"(b)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
