@@ -1001,7 +1001,7 @@ staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtyp
  * with the sums over the rows in fp32.  A gate shared by the rows has the gradient float[d],
  * summed over the rows; a gate a row the gradient rows dgate, of dtype.
  * An output may take the place of an input of the same type and stride.
- * d <= 16384, n_rows <= 2^23; squares of a row's values have to stay finite in fp32. */
+ * d <= 16384, n_rows < 2^22; squares of a row's values have to stay finite in fp32. */
 typedef struct staple_rows_t {
   void* data;
   int64_t stride;
@@ -1033,7 +1033,7 @@ staple_status_t staple_norm_bwd(const staple_norm_t* a, void* ws, size_t ws_byte
  * has it has the loss +inf, and a row that has nothing else has the gradient zero.
  * The forward writes loss and lse float[n_rows] and, with g float[n_rows] (the gradient of each
  * row's loss) and d_logits (of dtype, may be the logits themselves), the gradient in the same
- * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows <= 2^23. */
+ * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows < 2^22. */
 staple_status_t staple_xent_fwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                                 int32_t dtype, const int32_t* targets, float* loss, float* lse,
                                 const float* g, void* d_logits, int64_t d_stride, void* stream);
@@ -1055,7 +1055,7 @@ staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_ro
  *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.
  * The weights are rounded to multiples of 2^-62 by vocab (2^-50 at least) and summed exactly: the
  * same token on every run, and one that differs from the definition only where
- * u or p lies within that rounding of a border. */
+ * u or p lies within that rounding of a border.  vocab <= 2^22, n_rows < 2^22. */
 size_t staple_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
 staple_status_t staple_sample(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                               int32_t dtype, const float* u, const float* temperature,

@@ -74,7 +74,7 @@ def norm(L, **change):
 
 BOTH = [
     (dict(dtype=2), -2), (dict(r_dtype=2), -2), (dict(w_dtype=2), -2), (dict(dtype=0, r_dtype=1), -2),
-    (dict(n_rows=-1), -1), (dict(n_rows=(1 << 23) + 1), -2), (dict(d=0), -1), (dict(d=16385), -2),
+    (dict(n_rows=-1), -1), (dict(n_rows=1 << 22), -2), (dict(d=0), -1), (dict(d=16385), -2),
     (dict(scale=NAN), -1), (dict(scale=INF), -1), (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=NAN), -1),
     (dict(eps=INF), -1), (dict(w_pre=P + 1), -1), (dict(w_post=P + 1), -1),
 ]
@@ -145,7 +145,7 @@ def xent(L, **change):
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dtype=5), -2), (dict(n=-1), -1), (dict(n=(1 << 23) + 1), -2), (dict(vocab=0), -1),
+    (dict(dtype=5), -2), (dict(n=-1), -1), (dict(n=1 << 22), -2), (dict(vocab=0), -1),
     (dict(vocab=(1 << 22) + 1), -2), (dict(stride=-1), -1), (dict(logits=None), -1), (dict(logits=P + 1), -1),
     (dict(targets=None), -1), (dict(lse=None), -1), (dict(g=None), -1), (dict(d_logits=None), -1),
     (dict(d_logits=P + 1), -1), (dict(d_stride=99), -1), (dict(n=0, logits=None, lse=None), 0)], ids=str)
@@ -169,7 +169,7 @@ def sample(L, **change):
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dtype=5), -2), (dict(n=-1), -1), (dict(n=(1 << 23) + 1), -2), (dict(vocab=0), -1),
+    (dict(dtype=5), -2), (dict(n=-1), -1), (dict(n=1 << 22), -2), (dict(vocab=0), -1),
     (dict(vocab=(1 << 22) + 1), -2), (dict(stride=-1), -1), (dict(logits=None), -1), (dict(logits=P + 1), -1),
     (dict(u=None), -1), (dict(token=None), -1), (dict(n=0, logits=None), 0)], ids=str)
 def test_sampling_refuses(L, change, status):

@@ -7,7 +7,7 @@
 
 namespace staple {
 
-constexpr int64_t kMaxRows = int64_t(1) << 23;      // rows of a launch: times 1024 lanes below 2^33
+constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;   // a launch has fewer than 2^32 lanes, and a row up to 1024
 constexpr int64_t kMaxTokens29 = int64_t(1) << 29;
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 

@@ -139,16 +139,6 @@ __device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] += old[i];
   }
-  #ifdef NTS
-  if (VEC) {
-    if (R::column(g, lane, 0) < d) {
-      float* p = row + R::column(g, lane, 0);
-      __builtin_nontemporal_store(f32x4_t{acc[0], acc[1], acc[2], acc[3]}, reinterpret_cast<f32x4_t*>(p));
-      __builtin_nontemporal_store(f32x4_t{acc[4], acc[5], acc[6], acc[7]}, reinterpret_cast<f32x4_t*>(p + 4));
-    }
-    return;
-  }
-#endif
   R::store(row, g, lane, d, acc);
 }
 

@@ -106,9 +106,12 @@ struct Part {
   typedef __attribute__((ext_vector_type(kWords))) uint32_t words_t;
   words_t w;
   __device__ __forceinline__ static int column(int g, int t, int i) { return VEC ? (g * T + t) * V + i : (g * V + i) * T + t; }
+  // ONCE: rows, which nothing reads again soon, past the caches
+  template <bool ONCE>
   __device__ __forceinline__ void load(const E* row, int g, int t, int d) {
-    if (VEC) {
-      w = *reinterpret_cast<const words_t*>(row + min(column(g, t, 0), d - V));   // lanes past the end: the last ones again
+    if (VEC) {   // lanes past the end: the last elements again
+      const words_t* p = reinterpret_cast<const words_t*>(row + min(column(g, t, 0), d - V));
+      w = ONCE ? __builtin_nontemporal_load(p) : *p;
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) w[i] = __float_as_uint(load1(row + min(column(g, t, i), d - 1)));
@@ -149,11 +152,11 @@ __device__ __forceinline__ void load_vector(const void* p, bool bf16, int g, int
     for (int i = 0; i < V; ++i) v[i] = 1.0f;
   } else if (bf16) {
     Part<bf16_t, T, VEC, V> x;
-    x.load(static_cast<const bf16_t*>(p), g, t, d);
+    x.template load<false>(static_cast<const bf16_t*>(p), g, t, d);
     x.get(v, g, t, d);
   } else {
     Part<float, T, VEC, V> x;
-    x.load(static_cast<const float*>(p), g, t, d);
+    x.template load<false>(static_cast<const float*>(p), g, t, d);
     x.get(v, g, t, d);
   }
 }
@@ -168,13 +171,13 @@ struct NormRow {
     const RowsView& sum = a.r.data ? a.r : a.x;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      if (a.dr.data) dr[g].load(row_of<const X>(a.dr, i), g, t, a.d);
+      if (a.dr.data) dr[g].template load<true>(row_of<const X>(a.dr, i), g, t, a.d);
       if (a.pre) {
-        if (sum.data) r[g].load(row_of<const X>(sum, i), g, t, a.d);
-        dh[g].load(row_of<const Z>(a.dh, i), g, t, a.d);
+        if (sum.data) r[g].template load<true>(row_of<const X>(sum, i), g, t, a.d);
+        dh[g].template load<true>(row_of<const Z>(a.dh, i), g, t, a.d);
       }
-      if (need_z) z[g].load(row_of<const Z>(a.z, i), g, t, a.d);
-      if (a.gate_kind == Gate::kRows) gate[g].load(row_of<const Z>(a.gate, i), g, t, a.d);
+      if (need_z) z[g].template load<true>(row_of<const Z>(a.z, i), g, t, a.d);
+      if (a.gate_kind == Gate::kRows) gate[g].template load<true>(row_of<const Z>(a.gate, i), g, t, a.d);
     }
     rstd_r = a.pre ? a.rstd_r[i] : 0.0f;
     rstd_z = a.post ? a.rstd_z[i] : 1.0f;
