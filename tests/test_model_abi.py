@@ -217,3 +217,14 @@ def test_the_binding_refuses_combinations():
         st.staple_norm_fwd(f, f, w_pre=v, w_post=v.bfloat16(), post=True)
     with pytest.raises(TypeError):
         st.staple_norm_fwd(f.double(), f.double())
+
+
+def test_packed_norm_arguments_are_the_structure(L):
+    head = (5, 8, 1, 0, 1, 1, 0, 0.5, 1e-6)
+    rows = [(1000 + 8 * i, 10 + i) for i in range(10)]
+    ends = [2000 + 8 * i for i in range(6)]
+    flat = [v for r in rows for v in r]
+    whole = bytes(L.Norm(*head, *rows[:5], *ends[:4], *rows[5:], *ends[4:]))
+    assert L.pack_norm_bwd(*head, *flat[:10], *ends[:4], *flat[10:], *ends[4:]) == whole
+    first = L.Norm(*head, *rows[:5], *ends[:4])
+    assert L.pack_norm_fwd(*head, *flat[:10], *ends[:4]) == bytes(first)

@@ -1112,7 +1112,7 @@ def staple_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
 # ----------------------------------------------------------------------------
 # A model's two ends and the norms around its blocks
 # ----------------------------------------------------------------------------
-_NO_ROWS = (None, 0)
+_NO_ROWS = (0, 0)
 
 
 def _on(t: torch.Tensor, what: str) -> int:
@@ -1231,7 +1231,7 @@ def _norm(one, zt, w_pre, w_post, gate, pre, post, scale, eps):
         if at[1] == 0 and n > 1:
             raise ValueError("gate: a shared one is given as [d]")
         at = (at[0], at[1] or d)
-    return head, at, (_flat(w_pre, "w_pre", d, dev, wt), _flat(w_post, "w_post", d, dev, wt)), shared, dev
+    return head, at, (_flat(w_pre, "w_pre", d, dev, wt) or 0, _flat(w_post, "w_post", d, dev, wt) or 0), shared, dev
 
 
 def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None, *,
@@ -1257,13 +1257,14 @@ def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None,
             "rstd_r": one.new_empty(n, dtype=_FLOAT32) if pre and save else None,
             "rstd_z": one.new_empty(n, dtype=_FLOAT32) if post and save else None})
         r, h = (_NO_ROWS if t is None else (t.data_ptr(), d) for t in (out["r"], out["h"]))
-        saved = _p(out["rstd_r"]), _p(out["rstd_z"])
+        saved = _p(out["rstd_r"]) or 0, _p(out["rstd_z"]) or 0
     else:
         r = _NO_ROWS if z is None else _rows(out.get("r"), "r", xt, shape, dev, True)
         h = _rows(out["h"], "h", zt, shape, dev, True) if pre else _NO_ROWS
-        saved = [_flat(out.get(k), k, n, dev, _FLOAT32) for k in ("rstd_r", "rstd_z")]
-    a = _lib.Norm(*head, _rows(x, "x", xt, shape, dev), _rows(z, "z", zt, shape, dev), r, h, gate, *weights, *saved)
-    _check(lib().staple_norm_fwd(ctypes.byref(a), _stream(stream)), "staple_norm_fwd")
+        saved = [_flat(out.get(k), k, n, dev, _FLOAT32) or 0 for k in ("rstd_r", "rstd_z")]
+    a = _lib.pack_norm_fwd(*head, *_rows(x, "x", xt, shape, dev), *_rows(z, "z", zt, shape, dev), *r, *h, *gate, *weights,
+                           *saved)
+    _check(lib().staple_norm_fwd(a, _stream(stream)), "staple_norm_fwd")
     return out
 
 
@@ -1296,15 +1297,16 @@ def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: O
             "dw_pre": None if w_pre is None else one.new_empty(d, dtype=_FLOAT32),
             "dw_post": None if w_post is None else one.new_empty(d, dtype=_FLOAT32)})
     dgate = out.get("dgate")
-    a = _lib.Norm(*head, _rows(x, "x", xt, shape, dev), _rows(z, "z", zt, shape, dev), _rows(r, "r", xt, shape, dev),
-                  _NO_ROWS, gate_at, *weights, _flat(rstd_r, "rstd_r", n, dev, _FLOAT32),
-                  _flat(rstd_z, "rstd_z", n, dev, _FLOAT32), _rows(dr, "dr", xt, shape, dev),
-                  _rows(dh, "dh", zt, shape, dev) if pre else _NO_ROWS, _rows(out.get("dx"), "dx", xt, shape, dev, True),
-                  _rows(out.get("dz"), "dz", zt, shape, dev, True),
-                  (_flat(dgate, "dgate", d, dev, _FLOAT32), 0) if shared else _rows(dgate, "dgate", zt, shape, dev, True),
-                  _flat(out.get("dw_pre"), "dw_pre", d, dev, _FLOAT32),
-                  _flat(out.get("dw_post"), "dw_post", d, dev, _FLOAT32))
-    a, native = ctypes.byref(a), lib()
+    a = _lib.pack_norm_bwd(
+        *head, *_rows(x, "x", xt, shape, dev), *_rows(z, "z", zt, shape, dev), *_rows(r, "r", xt, shape, dev),
+        *_NO_ROWS, *gate_at, *weights, _flat(rstd_r, "rstd_r", n, dev, _FLOAT32) or 0,
+        _flat(rstd_z, "rstd_z", n, dev, _FLOAT32) or 0, *_rows(dr, "dr", xt, shape, dev),
+        *(_rows(dh, "dh", zt, shape, dev) if pre else _NO_ROWS), *_rows(out.get("dx"), "dx", xt, shape, dev, True),
+        *_rows(out.get("dz"), "dz", zt, shape, dev, True),
+        *((_flat(dgate, "dgate", d, dev, _FLOAT32) or 0, 0) if shared else _rows(dgate, "dgate", zt, shape, dev, True)),
+        _flat(out.get("dw_pre"), "dw_pre", d, dev, _FLOAT32) or 0,
+        _flat(out.get("dw_post"), "dw_post", d, dev, _FLOAT32) or 0)
+    native = lib()
     ws = _ws(native.staple_norm_bwd_workspace_bytes(a), workspace, one.device, stream)
     _check(native.staple_norm_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_norm_bwd")
     return out

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch  # noqa: F401  (loads the HIP runtime the library binds to)
 
@@ -166,6 +167,12 @@ class Norm(ctypes.Structure):
                 [(n, c_vp) for n in ("w_pre", "w_post", "rstd_r", "rstd_z")] +
                 [(n, Rows) for n in ("dr", "dh", "dx", "dz", "dgate")] +
                 [(n, c_vp) for n in ("dw_pre", "dw_post")])
+
+
+# A Norm's bytes: packing them takes 0.75 us, making the structure 2.7.  The forward's ends with its outputs.
+_NORM = "@2q5i2f" + 5 * "Pq" + "4P"
+pack_norm_fwd = struct.Struct(_NORM + "96x").pack
+pack_norm_bwd = struct.Struct(_NORM + 5 * "Pq" + "2P").pack
 
 
 EXPORTED = tuple(_SIGS)
