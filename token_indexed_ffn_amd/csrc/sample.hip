@@ -23,7 +23,7 @@ typedef unsigned long long u64;
 
 constexpr int kSampleThreads = 256;
 constexpr int kWaves = kSampleThreads / 64;
-constexpr int kBins = 512;          // two a lane of a workgroup
+constexpr int kBins = 512;          // two a lane of four waves
 constexpr int kList = 2048;         // listed tokens
 constexpr int kMostBlocks = 2049;   // blocks of a row: 512 elements each, 1024 or 2048 past 2^20 logits
 constexpr int kMostChunks = 16;     // workgroups of a row: the last one has all intervals' loads in flight at once
@@ -110,11 +110,12 @@ __device__ __forceinline__ u64 part_of(float share, u64 total, bool& rest) {
 }
 
 // ------------------------------------------------------------------------------- a row's layout
-// The row is cut into blocks of `size` elements that begin where its memory is 16-byte aligned
+// The row is cut into blocks of 2^log_size elements that begin where its memory is 16-byte aligned
 // (`shift` elements before its first one); consecutive blocks make a workgroup's chunk.
 struct SampleGrid {
-  int chunks, blocks, blocks_a_chunk, size;
+  int chunks, blocks, blocks_a_chunk, log_size;
   int64_t row_bytes;
+  __host__ __device__ int size() const { return 1 << log_size; }
 };
 
 enum { kDone, kListed, kSearch };   // the token is known; lo to hi are listed; too many for the list
@@ -165,12 +166,12 @@ struct Row {
   // The elements outside full groups of eight are held one a lane (lanes 0 to 7 the row's first
   // ones, 32 to 39 its last ones), in the blocks that they belong to; -1: none.
   __device__ __forceinline__ bool has_edge(const SampleGrid& g, int block) const {
-    return (block == 0 && shift > 0) || (block == (n - 1 + shift) / g.size && (n + shift & 7) != 0);
+    return (block == 0 && shift > 0) || (block == n - 1 + shift >> g.log_size && (n + shift & 7) != 0);
   }
   __device__ __forceinline__ int edge(const SampleGrid& g, int block, int lane) const {
     const int head = shift > 0 ? min(n, 8 - shift) : 0, tail = n > head ? n + shift & 7 : 0;
     if (block == 0 && lane < head) return lane;
-    if (block == (n - 1 + shift) / g.size && lane >= 32 && lane - 32 < tail) return n - tail + lane - 32;
+    if (block == n - 1 + shift >> g.log_size && lane >= 32 && lane - 32 < tail) return n - tail + lane - 32;
     return -1;
   }
 };
@@ -188,14 +189,14 @@ struct Walk {
   Raw<E> raw[kAhead];
   __device__ __forceinline__ Walk(const Row<E>& row, const SampleGrid& grid, int first_block, int end, int each)
       : r(row), g(grid), lane(threadIdx.x & 63), begin(first_block), stride(each) {
-    log_its = 31 - __clz(g.size >> 9);
+    log_its = g.log_size - 9;
     steps = begin < end ? (end - begin + stride - 1) / stride << log_its : 0;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(i, raw[i]);
   }
   __device__ __forceinline__ int block(int s) const { return begin + (s >> log_its) * stride; }
   __device__ __forceinline__ int first(int s) const {
-    return block(s) * g.size + (s & ((1 << log_its) - 1)) * 512 + lane * 8 - r.shift;
+    return (block(s) << g.log_size) + (s & ((1 << log_its) - 1)) * 512 + lane * 8 - r.shift;
   }
   __device__ __forceinline__ void load(int s, Raw<E>& to) const {
     const int j = first(s);
@@ -424,8 +425,8 @@ __device__ __forceinline__ void draw(const SampleView& a, int64_t row, const Sam
   const int block = static_cast<int>(s.found[0]);
   before = s.found[1];
 #pragma unroll 1
-  for (int i = threadIdx.x; i < g.size; i += T) {
-    const int j = block * g.size - r.shift + i;
+  for (int i = threadIdx.x; i < g.size(); i += T) {
+    const int j = (block << g.log_size) - r.shift + i;
     u64 w = 0;
     float l = 0.0f;
     if (j >= 0 && j < r.n) {
@@ -474,9 +475,14 @@ __device__ __forceinline__ Top find_top(const Row<E>& r, Walk<E> walk, u64* plac
     }
   }, [](int) {});
   int first = 0;   // a row of -inf has no token: any will do
-  if (best != -__builtin_inff())
+  if (best != -__builtin_inff()) {
+    float v[8];   // all loads before the first comparison: none behind a branch
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r.at(min(max(at + i, 0), r.n - 1));
+#pragma unroll
     for (int i = 7; i >= 0; --i)
-      if (at + i >= 0 && at + i < r.n && r.at(at + i) == best) first = at + i;
+      if (v[i] == best) first = min(max(at + i, 0), r.n - 1);
+  }
   Top x{place_of(best, first), least};
   const auto join = [&](u64 place, float low) {
     x.place = place > x.place ? place : x.place;
@@ -638,7 +644,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(SampleView a) {
     if (w >= m.least_weight) atomicAdd(&sums[(edge + groups.shift) / 512], w);
   }
   __syncthreads();
-  const SampleGrid g{1, G * kRowWaves, G * kRowWaves, 512, 0};
+  const SampleGrid g{1, G * kRowWaves, G * kRowWaves, 9, 0};
   draw<E, T>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [](float, int) { return true; });
 }
 
@@ -869,31 +875,20 @@ __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_bef
   return cut;
 }
 
-// The same for n <= T listed tokens, one a lane, which are sorted: up to 45 exchanges, of which six go
-// through LDS, where the digits have some ten barriers each.
+// The same for n <= T listed tokens, which are sorted: a lane counts the places before its own, n reads that all
+// lanes share and that do not wait for each other, where exchanges wait for each other up to 45 times.
 template <int T>
 __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight_before, u64 count_before, int n, Shared& s,
                                           ListSpace& list) {
   const int t = threadIdx.x;
   u64 place = t < n ? list.place[t] : 0;
-#pragma unroll 1
-  for (int size = 2; size < 2 * n; size <<= 1)
-#pragma unroll 1
-    for (int o = size >> 1; o >= 1; o >>= 1) {
-      u64 x;
-      if (o >= 64) {
-        __syncthreads();
-        list.place[t] = place;
-        __syncthreads();
-        x = list.place[t ^ o];
-      } else {
-        x = __shfl_xor(place, o, 64);
-      }
-      // falling order: the lower lane of a pair keeps the larger one, the other way round in every
-      // second run
-      const bool larger = ((t & o) == 0) == ((t & size) == 0);
-      if ((x > place) == larger) place = x;
-    }
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) rank += list.place[i] > place;
+  u64* sorted = list.place + T;
+  if (t < n) sorted[rank] = place;
+  __syncthreads();
+  if (t < n) place = sorted[t];
   const u64 w = t < n ? m.weight(logit_at(place)) : 0;
   bool keep = t < n;
   if (m.k > 0) {
@@ -914,13 +909,20 @@ __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight
   // the kept ones are the first ones: the last of them is the cut
   const u64 kept = __ballot(keep);
   __syncthreads();
-  list.place[t] = place;
   if ((t & 63) == 0) s.wave[t >> 6] = __popcll(kept);
   __syncthreads();
   int count = 0;
 #pragma unroll
   for (int i = 0; i < T / 64; ++i) count += static_cast<int>(s.wave[i]);
-  return count > 0 ? list.place[count - 1] : ~u64(0);
+  return count > 0 ? sorted[count - 1] : ~u64(0);
+}
+
+// v[i], by selections: an array that is indexed by a register leaves the registers.
+__device__ __forceinline__ float pick(const float (&v)[8], int i) {
+  const bool one = i & 1, two = i & 2;
+  const float a = one ? v[1] : v[0], b = one ? v[3] : v[2], c = one ? v[5] : v[4], d = one ? v[7] : v[6];
+  const float low = two ? b : a, high = two ? d : c;
+  return i & 4 ? high : low;
 }
 
 // The tokens of the border's intervals into list.place, as far as it goes (sh.listed: their number), and the
@@ -930,24 +932,26 @@ __device__ __forceinline__ void list_tokens(const Limits& m, const Border& x, Wa
                                             Put put) {
   u64 sum = 0;
   walk.run([&](int j, const float (&v)[8], bool) {
-    unsigned listed = 0;
+    // first what each of the eight is, without a branch, then the few that count one by one
+    unsigned above = 0, listed = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int bin = v[i] == -__builtin_inff() ? kBins : m.bin(v[i]);
-      if (bin < x.lo) {
-        const u64 w = m.weight(v[i]);
-        sum += w >= m.least_weight ? w : 0;
-      } else if (bin <= x.hi && bin < kBins) {
-        listed |= 1u << i;
-      }
+      above |= static_cast<unsigned>(bin < x.lo) << i;
+      listed |= static_cast<unsigned>(bin >= x.lo && bin <= x.hi && bin < kBins) << i;
+    }
+#pragma unroll 1
+    for (; above; above &= above - 1) {
+      const u64 w = m.weight(pick(v, __ffs(above) - 1));
+      sum += w >= m.least_weight ? w : 0;
     }
     if (listed == 0) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (listed >> i & 1) {
-        const uint32_t at = atomicAdd(&sh.listed, 1u);
-        if (at < kList) list.place[at] = place_of(v[i], j + i);
-      }
+    uint32_t at = atomicAdd(&sh.listed, static_cast<uint32_t>(__popc(listed)));
+#pragma unroll 1
+    for (; listed && at < kList; listed &= listed - 1, ++at) {
+      const int i = __ffs(listed) - 1;
+      list.place[at] = place_of(pick(v, i), j + i);
+    }
   }, [&](int block) {
     if (x.lo > 0) sum = sum_up_to(sum);
     if ((threadIdx.x & 63) == 63) put(block, sum);
@@ -962,20 +966,11 @@ __device__ __forceinline__ void finish_row(const SampleView& a, int64_t row, con
                                            const Border& x, int n, const Row<E>& r, Shared& sh, ListSpace& list, u64* sums) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
   const bool in_list = x.mode == kListed && n <= kList;
-  u64 cut = 0, base = 0, other = 0;
-  if (in_list && n > 0) {
-    base = list.place[0];
-    for (int i = t; i < n; i += T) other |= list.place[i] ^ base;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
-  }
-  if (lane == 0) sh.wave[wave] = other;
-  if (!in_list)
+  u64 cut = 0;
+  if (!in_list) {
     for (int b = t; b < g.blocks; b += T) sums[b] = 0;
-  __syncthreads();
-  other = 0;
-#pragma unroll
-  for (int i = 0; i < T / 64; ++i) other |= sh.wave[i];
+    __syncthreads();
+  }
   const auto each = [&](auto f) {
     if (in_list) {
 #pragma unroll 1
@@ -988,14 +983,29 @@ __device__ __forceinline__ void finish_row(const SampleView& a, int64_t row, con
       }
     }
   };
-  if (in_list && x.lo < kBins && n <= T)
-    cut = cut_of_few<T>(m, x.total, x.weight_before, x.count_before, n, sh, list);
-  else if (!in_list || x.lo < kBins)
-    cut = cut_of<T>(m, x.total, in_list ? x.weight_before : 0, in_list ? x.count_before : 0, base,
-                    in_list ? 64 - __clzll(other) : 32 + kIndexBits, sh, list, each);
+  if (in_list && n <= T) {
+    if (x.lo < kBins) cut = cut_of_few<T>(m, x.total, x.weight_before, x.count_before, n, sh, list);
+  } else if (!in_list || x.lo < kBins) {
+    u64 base = 0;   // what the listed tokens' places have in common
+    int bits = 32 + kIndexBits;
+    if (in_list) {
+      base = list.place[0];
+      u64 other = 0;
+      for (int i = t; i < n; i += T) other |= list.place[i] ^ base;
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) other |= __shfl_xor(other, o, 64);
+      if (lane == 0) sh.wave[wave] = other;
+      __syncthreads();
+      other = 0;
+#pragma unroll
+      for (int i = 0; i < T / 64; ++i) other |= sh.wave[i];
+      bits = 64 - __clzll(other);
+    }
+    cut = cut_of<T>(m, x.total, in_list ? x.weight_before : 0, in_list ? x.count_before : 0, base, bits, sh, list, each);
+  }
   __syncthreads();
   each([&](u64 place, u64 w) {
-    if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[(index_at(place) + r.shift) / g.size], w);
+    if (w > 0 && place >= cut && w >= m.least_weight) atomicAdd(&sums[index_at(place) + r.shift >> g.log_size], w);
   });
   __syncthreads();
   draw<E, T>(a, row, g, m, sh, [&](int b) { return sums[b]; }, [&](float l, int j) { return place_of(l, j) >= cut; });
@@ -1094,8 +1104,8 @@ __global__ __launch_bounds__(T) void sample_whole_kernel(SampleView a, SampleGri
 // ------------------------------------------------------------------------------------------ host
 static SampleGrid whole_row(int64_t vocab) {
   SampleGrid g;
-  g.size = vocab <= (1 << 20) ? 512 : vocab <= (1 << 21) ? 1024 : 2048;
-  g.blocks = static_cast<int>((vocab + 7 + g.size - 1) / g.size);   // wherever the row begins
+  g.log_size = vocab <= (1 << 20) ? 9 : vocab <= (1 << 21) ? 10 : 11;
+  g.blocks = static_cast<int>((vocab + 7 + g.size() - 1) / g.size());   // wherever the row begins
   g.chunks = 1;
   g.blocks_a_chunk = g.blocks;
   g.row_bytes = 0;
