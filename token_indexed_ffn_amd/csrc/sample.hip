@@ -789,7 +789,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(SampleView 
 
 // ------------------------------------------------------------------------------------ pass three
 struct ListSpace {
-  u64 place[kList];
+  alignas(16) u64 place[kList];
   u64 bin_weights[256];
   uint32_t bin_counts[256];
 };
@@ -875,17 +875,29 @@ __device__ __forceinline__ u64 cut_of(const Limits& m, u64 total, u64 weight_bef
   return cut;
 }
 
-// The same for n <= T listed tokens, which are sorted: a lane counts the places before its own, n reads that all
-// lanes share and that do not wait for each other, where exchanges wait for each other up to 45 times.
+// The same for n <= T listed tokens, which are sorted: a lane counts the places before its own, in reads that all
+// lanes share and that do not wait for each other, where exchanges wait for each other up to 45 times.  (As
+// positive numbers in floating point, places are in the same order.)
 template <int T>
 __device__ __forceinline__ u64 cut_of_few(const Limits& m, u64 total, u64 weight_before, u64 count_before, int n, Shared& s,
                                           ListSpace& list) {
   const int t = threadIdx.x;
+  constexpr int kAtOnce = 16;
+  static_assert(2 * T + kAtOnce <= kList, "beside each other");
+  u64* sorted = list.place + T + kAtOnce;
   u64 place = t < n ? list.place[t] : 0;
+  if (t < kAtOnce) list.place[n + t] = 0;
+  __syncthreads();
   int rank = 0;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) rank += list.place[i] > place;
-  u64* sorted = list.place + T;
+#pragma unroll 1
+  for (int i = 0; i < n; i += kAtOnce) {
+    double2 x[kAtOnce / 2];
+#pragma unroll
+    for (int k = 0; k < kAtOnce / 2; ++k) x[k] = reinterpret_cast<const double2*>(list.place + i)[k];
+#pragma unroll
+    for (int k = 0; k < kAtOnce / 2; ++k)
+      rank += (x[k].x > __longlong_as_double(place)) + (x[k].y > __longlong_as_double(place));
+  }
   if (t < n) sorted[rank] = place;
   __syncthreads();
   if (t < n) place = sorted[t];
