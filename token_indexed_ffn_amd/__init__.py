@@ -1296,16 +1296,20 @@ def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: O
             else one.new_empty(shape, dtype=zt),
             "dw_pre": None if w_pre is None else one.new_empty(d, dtype=_FLOAT32),
             "dw_post": None if w_post is None else one.new_empty(d, dtype=_FLOAT32)})
-    dgate = out.get("dgate")
+        dx, dz, dgate = ((0, 0) if t is None else (t.data_ptr(), 0 if t.dim() == 1 else d)
+                         for t in (out["dx"], out["dz"], out["dgate"]))
+        sums = [0 if t is None else t.data_ptr() for t in (out["dw_pre"], out["dw_post"])]
+    else:
+        dx = _rows(out.get("dx"), "dx", xt, shape, dev, True)
+        dz = _rows(out.get("dz"), "dz", zt, shape, dev, True)
+        dgate = out.get("dgate")
+        dgate = (_flat(dgate, "dgate", d, dev, _FLOAT32) or 0, 0) if shared else _rows(dgate, "dgate", zt, shape, dev, True)
+        sums = [_flat(out.get(k), k, d, dev, _FLOAT32) or 0 for k in ("dw_pre", "dw_post")]
     a = _lib.pack_norm_bwd(
         *head, *_rows(x, "x", xt, shape, dev), *_rows(z, "z", zt, shape, dev), *_rows(r, "r", xt, shape, dev),
         *_NO_ROWS, *gate_at, *weights, _flat(rstd_r, "rstd_r", n, dev, _FLOAT32) or 0,
         _flat(rstd_z, "rstd_z", n, dev, _FLOAT32) or 0, *_rows(dr, "dr", xt, shape, dev),
-        *(_rows(dh, "dh", zt, shape, dev) if pre else _NO_ROWS), *_rows(out.get("dx"), "dx", xt, shape, dev, True),
-        *_rows(out.get("dz"), "dz", zt, shape, dev, True),
-        *((_flat(dgate, "dgate", d, dev, _FLOAT32) or 0, 0) if shared else _rows(dgate, "dgate", zt, shape, dev, True)),
-        _flat(out.get("dw_pre"), "dw_pre", d, dev, _FLOAT32) or 0,
-        _flat(out.get("dw_post"), "dw_post", d, dev, _FLOAT32) or 0)
+        *(_rows(dh, "dh", zt, shape, dev) if pre else _NO_ROWS), *dx, *dz, *dgate, *sums)
     native = lib()
     ws = _ws(native.staple_norm_bwd_workspace_bytes(a), workspace, one.device, stream)
     _check(native.staple_norm_bwd(a, _p(ws), _ws_size(ws), _stream(stream)), "staple_norm_bwd")
