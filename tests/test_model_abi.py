@@ -37,7 +37,7 @@ def test_embedding_refuses(L, change, status):
 
 
 def embed_bwd(L, **change):
-    f = dict(dy=P, dy_stride=64, dtype=1, n=40, d=64, scale=1.0, sorted_pos=P, inv=P, seg_start=P, n_unique=P,
+    f = dict(dy=P, dy_stride=64, dtype=1, n=400, d=64, scale=1.0, sorted_pos=P, inv=P, seg_start=P, n_unique=P,
              max_unique=8, uniq=None, grad=P, grad_rows=8, accumulate=0, ws=P, ws_bytes=1 << 40)
     f.update(change)
     return L.load().staple_embed_bwd(*f.values(), None)
@@ -57,8 +57,8 @@ def test_embedding_gradient_refuses(L, change, status):
 def test_embedding_gradient_workspace(L):
     size = L.load().staple_embed_bwd_workspace_bytes
     assert size(0, 64) == 0 and size(-1, 64) == 0 and size(40, 0) == 0 and size(40, 1 << 21) == 0
-    assert size(40, 64) > 0
-    assert embed_bwd(L, ws_bytes=size(40, 64) - 1) == -3
+    assert size(400, 64) > 0
+    assert embed_bwd(L, ws_bytes=size(400, 64) - 1) == -3
 
 
 def norm(L, **change):

@@ -128,8 +128,8 @@ staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtyp
   if (!valid_dtype(dtype)) return STAPLE_ERR_UNSUPPORTED;
   REQUIRE(n_tokens >= 0 && d >= 1 && std::isfinite(scale) && max_unique >= 0 && grad_rows >= 0);
   REQUIRE(uniq || max_unique <= grad_rows);
-  // workgroups of 512 lanes of a launch: one for 512 columns of 32 positions
-  if (n_tokens > kMaxTokens29 || d > kMaxWidth || (n_tokens / 32 + 1) * (d / 512 + 1) >= int64_t(1) << 23)
+  // workgroups of 512 lanes of a launch: one for 512 columns of 64 positions
+  if (n_tokens > kMaxTokens29 || d > kMaxWidth || (n_tokens / 64 + 1) * (d / 512 + 1) >= int64_t(1) << 23)
     return STAPLE_ERR_UNSUPPORTED;
   if (n_tokens == 0) return STAPLE_OK;
   REQUIRE(in_ok(dy, dy_stride, dtype) && sorted_pos && inv && seg_start && n_unique);

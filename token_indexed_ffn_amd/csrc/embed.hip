@@ -82,12 +82,16 @@ hipError_t launch_embed_fwd(const void* table, int64_t vocab, int64_t d, int32_t
 }
 
 // ------------------------------------------------------------------------------- gradient
-// One token can hold a tenth of a batch, so the sorted positions, not the tokens, are dealt
-// out: a wave sums the runs of equal tokens within a chunk of positions, for 512 columns.
-// A run that is a whole token's goes to its row.  One that a chunk's border cuts goes to
-// first[chunk] (begun in an earlier chunk) or last[chunk] (goes on in the next), and the
-// second kernel adds last[c0], first[c0 + 1], ..., first[c1], where they are many eight waves an eighth of
-// them each and the eighths in turn: the order is fixed, and the result does not change from run to run.
+// One token can hold half of a batch, so the sorted positions, not the tokens, are dealt out: a wave sums
+// the runs of equal tokens within a chunk of kChunk positions, for 512 columns.  A run that is a whole
+// token's goes to its row.  The parts of one that a chunk's border cuts meet in LDS, and where the run is
+// cut by the border of the workgroup's kSpan positions too, in first[span] (begun in an earlier span) or
+// last[span] (goes on in the next): the second kernel adds last[s0], first[s0 + 1], ..., first[s1], where
+// they are many eight waves an eighth of them each and the eighths in turn.  The order is fixed, and the
+// result does not change from run to run.
+constexpr int kChunk = 8;                    // as many rows as a lane has in flight
+constexpr int kChunks = 8;                   // of a workgroup: one a wave
+constexpr int kSpan = kChunk * kChunks;
 constexpr int kJoinWaves = 8;
 
 // Eight elements of a row whose columns past d repeat the last one: no branch around any load (the sums
@@ -142,59 +146,59 @@ __device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, in
   R::store(row, g, lane, d, acc);
 }
 
-template <typename E, bool VEC, int CHUNK>
-__global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups, float* __restrict__ first,
-                                                        float* __restrict__ last, int64_t ld, int* err) {
+template <typename E, bool VEC>
+__global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, int groups, float* __restrict__ first,
+                                                                 float* __restrict__ last, int64_t ld, int* err) {
   using R = RowGroup<64, VEC>;
-  const int lane = threadIdx.x & 63;
+  // the sums of a chunk's run that began before it, and of the one that goes on after it
+  __shared__ float begun_sum[kChunks][kEmbedCols], open_sum[kChunks][kEmbedCols];
+  __shared__ bool ended[kChunks];              // whether the former ends in the chunk
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n = a.n_tokens;
-  const int64_t chunks = (n + CHUNK - 1) / CHUNK;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (w >= chunks * groups) return;
   int64_t nu = *a.n_unique;
   if (nu < 0 || nu > a.max_unique) {
     if (lane == 0) flag_index_error(err);
     return;
   }
   nu = nu < n ? nu : n;
-  const int64_t c = w / groups;
-  const int g = static_cast<int>(w - c * groups);
+  const int64_t span = blockIdx.x / groups;
+  const int g = static_cast<int>(blockIdx.x - span * groups);
   const int d = static_cast<int>(a.d);
-  const int64_t p0 = c * CHUNK;
-  const int len = static_cast<int>(n - p0 < CHUNK ? n - p0 : CHUNK);
+  const int64_t p0 = span * kSpan + wave * kChunk;
+  const int len = static_cast<int>(max(int64_t(0), min(n - p0, int64_t(kChunk))));
   // lane i: position p0 + i; the lane after the last one and lane 63: the neighbours outside
   int32_t row = -1, u = -2;
   const int64_t p = lane == 63 ? p0 - 1 : p0 + lane;
-  if ((lane <= len || lane == 63) && p >= 0 && p < n) {
+  if (len > 0 && (lane <= len || lane == 63) && p >= 0 && p < n) {
     u = unique_of(p, n, nu, a.sorted_pos, a.inv, row);
     if (u < 0 && lane < len) flag_index_error(err);
   }
   const int32_t next = __shfl(u, lane < 62 ? lane + 1 : 62, 64);
   const uint64_t ends = __ballot(lane < len && u != next);   // a run's last position
-  const bool begun = __shfl(u, 63, 64) == __shfl(u, 0, 64);
+  const bool begun = len > 0 && __shfl(u, 63, 64) == __shfl(u, 0, 64);
+  const bool open = len > 0 && !(ends >> (len - 1) & 1) && !(begun && ends == 0);
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  bool first_run = true;
-  for (int b = 0; b < len; b += kEmbedAhead) {
-    float v[kEmbedAhead][8];
+  if (len > 0) {
+    float v[kChunk][8];
 #pragma unroll
-    for (int j = 0; j < kEmbedAhead; ++j) {
-      const int32_t r = __builtin_amdgcn_readlane(row, b + j < len ? b + j : len - 1);
+    for (int j = 0; j < kChunk; ++j) {
+      const int32_t r = __builtin_amdgcn_readlane(row, min(j, len - 1));
       // a position out of range: row 0, in a run whose sum is stored nowhere
       // (read past the caches, which takes the kernel from 63 to 50 us for 32768 rows of 2048)
       load_row<VEC, true>(reinterpret_cast<const E*>(a.dy.data) + (r >= 0 ? r : 0) * a.dy.stride, g, lane, d, v[j]);
     }
+    bool first_run = begun;
 #pragma unroll
-    for (int j = 0; j < kEmbedAhead; ++j) {
-      const int k = b + j;
+    for (int k = 0; k < kChunk; ++k) {
       if (k >= len) break;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
+      for (int i = 0; i < 8; ++i) acc[i] += v[k][i];
       const bool end = (ends >> k) & 1;
       if (!end && k + 1 < len) continue;
-      if (first_run && begun) {
-        R::store(first + c * ld, g, lane, d, acc);
-      } else if (!end) {
-        R::store(last + c * ld, g, lane, d, acc);
+      if (first_run || !end) {
+        float* to = first_run ? begun_sum[wave] : open_sum[wave];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[i * 64 + lane] = acc[i];
       } else {
         float* to = grad_row(a, __builtin_amdgcn_readlane(u, k), lane, err);
         if (to) finish<VEC>(a, to, g, lane, acc);
@@ -204,9 +208,36 @@ __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedGrad a, int groups,
       for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     }
   }
+  if (lane == 0) ended[wave] = ends != 0;
+  // the maps agree, also where no border asks for a token's first and last position
+  if (g == 0 && lane < len && u >= 0 && (a.seg_start[u] > p || a.seg_start[u + 1] <= p)) flag_index_error(err);
+  __syncthreads();
+  // a cut run's parts, from that of the chunk in which it begins, or of the span's first chunk
+#pragma unroll 1
+  for (int from_before = 0; from_before < 2; ++from_before) {
+    if (from_before ? !(wave == 0 && begun) : !open) continue;
+    const float(*parts)[kEmbedCols] = from_before ? begun_sum : open_sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = parts[wave][i * 64 + lane];
+    bool over = from_before && ended[0];
+#pragma unroll 1
+    for (int k = wave + 1; k < kChunks && !over; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += begun_sum[k][i * 64 + lane];
+      over = ended[k];
+    }
+    if (from_before) {
+      R::store(first + span * ld, g, lane, d, acc);
+    } else if (!over) {
+      R::store(last + span * ld, g, lane, d, acc);
+    } else {
+      float* to = grad_row(a, __builtin_amdgcn_readlane(u, len - 1), lane, err);
+      if (to) finish<VEC>(a, to, g, lane, acc);
+    }
+  }
 }
 
-// The chunk in which a cut run begins adds its parts: part 0 is last[c], part k first[c + k].
+// The span in which a cut run begins adds its parts: part 0 is last[c], part k first[c + k].
 template <bool VEC>
 __device__ __forceinline__ void add_parts(const float* first, const float* last, int64_t ld, int64_t c, int64_t k0,
                                           int64_t k1, int g, int lane, int d, float (&acc)[8]) {
@@ -226,9 +257,9 @@ __device__ __forceinline__ void add_parts(const float* first, const float* last,
   }
 }
 
-// A wave looks at one chunk (for 512 columns) and adds up to kEmbedAhead parts itself; runs of more are
+// A wave looks at one span (for 512 columns) and adds up to kEmbedAhead parts itself; runs of more are
 // added by the whole workgroup.
-template <bool VEC, int CHUNK>
+template <bool VEC>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGrad a, int groups,
                                                                          const float* __restrict__ first,
                                                                          const float* __restrict__ last, int64_t ld,
@@ -244,7 +275,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
   const int64_t c0 = blockIdx.x / groups * kJoinWaves, c = c0 + wave;
   const int g = static_cast<int>(blockIdx.x % groups);
   const int d = static_cast<int>(a.d);
-  const int64_t p0 = c * CHUNK, p1 = p0 + CHUNK;
+  const int64_t p0 = c * kSpan, p1 = p0 + kSpan;
   int64_t parts = 0;
   int32_t u = -1;
   if (p1 < n) {
@@ -256,7 +287,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
       if (begin >= p1 || end <= p1 || end > n) {
         if (lane == 0) flag_index_error(err);
       } else if (begin >= p0) {
-        parts = (end - 1) / CHUNK - c + 1;
+        parts = (end - 1) / kSpan - c + 1;
       }
     }
   }
@@ -295,38 +326,29 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
 
 static int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
 
-// Positions of a chunk: 32, or 8 where those make too few waves to hide their loads behind.
-static int chunk_of(int64_t n, int64_t d) {
-  const int64_t groups = (d + kEmbedCols - 1) / kEmbedCols;
-  return n / 32 * groups >= 16 * 256 ? 32 : 8;
-}
-
 size_t embed_bwd_workspace_bytes(int64_t n, int64_t d) {
-  const int64_t chunk = chunk_of(n, d), chunks = (n + chunk - 1) / chunk;
-  return chunks > 1 ? static_cast<size_t>(2 * chunks * part_stride(d)) * sizeof(float) : 0;
+  const int64_t spans = (n + kSpan - 1) / kSpan;
+  return spans > 1 ? static_cast<size_t>(2 * spans * part_stride(d)) * sizeof(float) : 0;
 }
 
-template <typename E, bool VEC, int CHUNK>
+template <typename E, bool VEC>
 static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
-  const int64_t chunks = (a.n_tokens + CHUNK - 1) / CHUNK, ld = part_stride(a.d);
+  const int64_t spans = (a.n_tokens + kSpan - 1) / kSpan, ld = part_stride(a.d);
   float* first = static_cast<float*>(ws);
-  float* last = first + chunks * ld;
+  float* last = first + spans * ld;
   const int groups = static_cast<int>((a.d + kEmbedCols - 1) / kEmbedCols);
-  embed_bwd_kernel<E, VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks * groups + 3) / 4)), dim3(256), 0, s>>>(
+  embed_bwd_kernel<E, VEC><<<dim3(static_cast<unsigned>(spans * groups)), dim3(64 * kChunks), 0, s>>>(
       a, groups, first, last, ld, err);
-  if (chunks > 1)
-    embed_bwd_join_kernel<VEC, CHUNK><<<dim3(static_cast<unsigned>((chunks + kJoinWaves - 1) / kJoinWaves * groups)), dim3(64 * kJoinWaves), 0, s>>>(
-        a, groups, first, last, ld, err);
+  if (spans > 1)
+    embed_bwd_join_kernel<VEC><<<dim3(static_cast<unsigned>((spans + kJoinWaves - 1) / kJoinWaves * groups)),
+                                 dim3(64 * kJoinWaves), 0, s>>>(a, groups, first, last, ld, err);
 }
 
 template <typename E>
 static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
   const bool vec = a.d % 8 == 0 && vec_rows(a.dy.data, a.dy.stride, sizeof(E)) && vec_rows(a.grad, a.d, 4);
-  if (chunk_of(a.n_tokens, a.d) == 32) {
-    if (vec) embed_bwd<E, true, 32>(a, ws, s, err); else embed_bwd<E, false, 32>(a, ws, s, err);
-  } else {
-    if (vec) embed_bwd<E, true, 8>(a, ws, s, err); else embed_bwd<E, false, 8>(a, ws, s, err);
-  }
+  if (vec) embed_bwd<E, true>(a, ws, s, err);
+  else embed_bwd<E, false>(a, ws, s, err);
 }
 
 hipError_t launch_embed_bwd(const EmbedGrad& a, int32_t dtype, void* ws, hipStream_t s, int* err) {
