@@ -374,7 +374,7 @@ def test_loss_and_its_gradient(st, dtype, n, v, pad):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("v", [5, 700, 5001, 100352])
+@pytest.mark.parametrize("v", [5, 700, 5001, 100352, 200003])
 def test_loss_with_ruled_out_classes(st, dtype, v):
     """-inf in some classes, in the target's, in all; large offsets; the type's lowest value."""
     import torch
@@ -414,7 +414,7 @@ def test_loss_of_nan_and_infinity_and_bad_targets(st):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n,v", [(40, 333), (5, 5001), (2, 100352), (300, 4097)])
+@pytest.mark.parametrize("n,v", [(40, 333), (5, 5001), (2, 100352), (300, 4097), (2, 151936), (3, 260001)])
 def test_loss_in_place_and_to_strided_rows(st, dtype, n, v):
     import torch
     logits, t, g = rand((n, v), dtype, 63, 3.0), ints(np.arange(n) % v), floats(np.linspace(0, 1, n))

@@ -3,8 +3,9 @@
 //   lse = log sum_j exp l_j,   loss = lse - l_t,   dl_j = g (exp(l_j - lse) - [j = t])
 //
 // A workgroup holds its row in registers, as it lies in memory: one read, the maximum, the sum, and
-// with the gradient one write.  Rows past what the registers hold are read once more for the gradient, their
-// sum running with its maximum: (m, s) stands for s exp m, and two such pairs join into one.
+// with the gradient one write.  What the registers do not hold of a row is read once more for the gradient, its
+// sum running with its maximum: (m, s) stands for s exp m, and two such pairs join into one.  Bound by
+// bytes: 8192 x 100352 in bf16 with the gradient take 675 us, 4.9 TB/s.
 #include "model_ops.h"
 #include "row_io.h"
 
@@ -177,21 +178,36 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void xent_fwd_kernel(XentView a,
   if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
 }
 
-// Rows of any width.
-template <typename E, int T>
+// Rows of any width.  G groups a lane stay in registers for the gradient; the rest of the row is read once more,
+// from its end on, where the caches still have it.
+template <typename E, int T, int G>
 __global__ __launch_bounds__(T) void xent_fwd_long_kernel(XentView a, int* err) {
   __shared__ float2 tmp[T / 64];
-  constexpr int kAhead = 4;
+  constexpr int kAhead = G > 0 ? 2 : 4;   // with more the kept groups spill
   const int t = threadIdx.x;
   const int64_t i = blockIdx.x;
   const E* l = reinterpret_cast<const E*>(a.logits) + i * a.stride;
   const RowGroups r(l, a.vocab);
+  const int steps = (a.vocab + r.shift + T * 8 - 1) / (T * 8);   // a lane's groups
+  Raw<E> kept[G > 0 ? G : 1];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int j = (q * T + t) * 8 - r.shift;
+    if (r.full(j)) kept[q].load(l + j);
+    else kept[q].clear();
+  }
   const int edge = t < 64 ? r.edge(t) : -1;
   const float at_edge = edge >= 0 ? load1(l + edge) : -__builtin_inff();
   const int target = target_of(a, i, t, err);
   const float at = target >= 0 ? load1(l + target) : 0.0f;
   MaxSum x{at_edge, at_edge == -__builtin_inff() ? 0.0f : __expf(at_edge - reference(at_edge))};
-  for (int q = 0; q * T * 8 < a.vocab + 8; q += kAhead) {
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    float v[8];
+    kept[q].get(v);
+    x.add(v);
+  }
+  for (int q = G; q < steps; q += kAhead) {
     Raw<E> raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -218,22 +234,31 @@ __global__ __launch_bounds__(T) void xent_fwd_long_kernel(XentView a, int* err) 
   E* out = reinterpret_cast<E*>(a.d_logits) + i * a.d_stride;
   const bool aligned = RowGroups(out, a.vocab).shift == r.shift;
   const Gradient grad(a, i, target, x.m, x.s);
-  for (int q = 0; q * T * 8 < a.vocab + 8; q += kAhead) {
+  for (int q = steps - 1; q >= G; q -= kAhead) {
     Raw<E> raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int j = ((q + u) * T + t) * 8 - r.shift;
-      if (r.full(j)) raw[u].load(l + j);
+      const int j = ((q - u) * T + t) * 8 - r.shift;
+      if (q - u >= G && r.full(j)) raw[u].load(l + j);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int j = ((q + u) * T + t) * 8 - r.shift;
-      if (!r.full(j)) continue;
+      const int j = ((q - u) * T + t) * 8 - r.shift;
+      if (q - u < G || !r.full(j)) continue;
       float v[8];
       raw[u].get(v);
       grad.eight(v, j);
       store_eight(out, j, aligned, v);
     }
+  }
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int j = (q * T + t) * 8 - r.shift;
+    float v[8];
+    kept[q].forget();
+    kept[q].get(v);
+    grad.eight(v, j);
+    if (r.full(j)) store_eight(out, j, aligned, v);
   }
   if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
 }
@@ -269,10 +294,13 @@ __global__ __launch_bounds__(256) void xent_bwd_kernel(XentView a, int pieces, i
 }
 
 // The narrowest shape that holds a row: lanes and groups of eight a lane (rows that begin between
-// 16-byte addresses need up to one group more).  8192 x 100352 bf16 logits with their gradient take 684 us
-// (4.8 TB/s) in 512 x 25, which keeps 170 registers a lane, and 729 us in the long kernel; held to
+// 16-byte addresses need up to one group more).  8192 x 100352 bf16 logits with their gradient take 675 us
+// in 512 x 25, which keeps 170 registers a lane, and 729 in the long kernel with nothing kept; held to
 // 128 registers, for two workgroups a CU, 512 x 25 spills and takes 869.  The loss alone, which has
 // only the read to overlap with, is faster in the long kernel's many small steps: 325 us, 376 in 512 x 25.
+// Wider rows in the long kernel, 4096 rows with nothing kept and with 64 registers of them: bf16,
+// 151936: 587, 512; 260001: 1267, 950; fp32, 128256: 973, 838; 256000: 2255, 1916.  fp32 rows of 100352 take 662 us
+// in it and 703 in 512 x 25.
 template <typename E>
 static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
   const bool aligned = reinterpret_cast<uintptr_t>(v.logits) % 16 == 0 && v.stride * sizeof(E) % 16 == 0;
@@ -293,13 +321,15 @@ static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
   GO(512, 8)
   GO(512, 16)
   if (v.d_logits) {
-    GO(512, 25)
     if constexpr (sizeof(E) == 2) {
+      GO(512, 25)
       GO(1024, 16)
     }
   }
 #undef GO
-  xent_fwd_long_kernel<E, 1024><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(1024), 0, s>>>(v, err);
+  const dim3 grid(static_cast<unsigned>(v.n_rows)), threads(1024);
+  if (v.d_logits) xent_fwd_long_kernel<E, 1024, 32 / sizeof(E)><<<grid, threads, 0, s>>>(v, err);
+  else xent_fwd_long_kernel<E, 1024, 0><<<grid, threads, 0, s>>>(v, err);
 }
 
 hipError_t launch_xent_fwd(const XentView& v, int32_t dtype, hipStream_t s, int* err) {
