@@ -14,6 +14,11 @@
 // blocks and the third is not needed.  A long row among few is dealt out to several workgroups, a launch for each
 // pass, and the last of them to arrive goes on with the row; otherwise a workgroup takes a row through
 // all passes.
+//
+// What bounds it: of one row of 100352, whose bytes are nothing, latency: three launches of 5, 8 and 15 us,
+// in which a wave has three or four steps of some 0.6 us, and the row's last workgroup sorts, sums and draws
+// alone.  64 such rows in fp32: 10 us for the read, 17 and 23 for the others (26 MB, 5 us at a copy's
+// rate).  509 rows of 50021 in bf16 with a temperature alone: 39 us, of which the 64-bit exponentials are some 15.
 #include "model_ops.h"
 #include "row_io.h"
 
@@ -795,8 +800,9 @@ struct ListSpace {
 };
 
 // The lowest place that is kept: in falling order, the first one at which the count (by_count) or
-// the sum of the weights reaches want >= 1, and 0 where none does.  Digit by digit, of what `each` calls its argument with: (place, weight) of every
-// token.  The places have the bits of `base` but for the last `bits`.
+// the sum of the weights reaches want >= 1, and 0 where none does.  Digit by digit, of what `each` calls
+// its argument with: (place, weight) of every token.  The places have the bits of `base` but for the
+// last `bits`.
 template <int T, typename Each>
 __device__ __forceinline__ u64 find_cut(bool by_count, u64 want, u64 base, int bits, Shared& s, ListSpace& list, Each each) {
   const int t = threadIdx.x;
