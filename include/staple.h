@@ -1045,14 +1045,16 @@ staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_ro
  * the tokens in the order of falling l_j (ties: rising j), a token is kept while
  *     it is among the first k                                (0 < k < vocab),
  *     the kept ones before it have a sum less than p times that of the first k   (p < 1),
- *     w_j >= min_p                                           (min_p > 0),
+ *     w_j >= min_p, or 1 where min_p is more                  (min_p > 0),
  * the first one always; token = the first j, in the order of j, at which the sum of the kept w
  * passes u times their whole sum.  T that is not above 0: the first of the largest logits.
  * NaN counts as -inf, +inf as the largest finite number; a token with -inf is never drawn, and a
  * row with nothing else has token -1.  logprob (NULL: not wanted): the log of the token's share of the kept sum, 0 where
  * T is not above 0, -inf for token -1.
  *   u float[n_rows] in [0, 1); temperature, top_p, min_p float[n_rows], top_k
- *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.
+ *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.  A p or min_p that is NaN limits nothing, one of 0
+ *   or less keeps the first token (p) or limits nothing (min_p); u outside [0, 1) or NaN counts as the
+ *   nearest, NaN as 0.
  * The weights are rounded to multiples of 2^-62 by vocab (2^-50 at least) and summed exactly: the
  * same token on every run, and one that differs from the definition only where
  * u or p lies within that rounding of a border.  vocab <= 2^22, n_rows < 2^22. */

@@ -217,6 +217,10 @@ def test_the_binding_refuses_combinations():
         st.staple_norm_fwd(f, f, w_pre=v, w_post=v.bfloat16(), post=True)
     with pytest.raises(TypeError):
         st.staple_norm_fwd(f.double(), f.double())
+    with pytest.raises(ValueError, match="x, z or both"):
+        st.staple_norm_fwd(None)
+    with pytest.raises(ValueError, match="x, z or both"):
+        st.staple_norm_bwd(f, f, None)
 
 
 def test_packed_norm_arguments_are_the_structure(L):

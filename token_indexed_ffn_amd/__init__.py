@@ -1246,6 +1246,8 @@ def staple_norm_fwd(x: Optional[torch.Tensor], z: Optional[torch.Tensor] = None,
     None: z's).  Returns r (None without z), h (None without `pre`), and with `save` 1 / rms of
     both, rstd_r and rstd_z, for staple_norm_bwd."""
     one = z if x is None else x
+    if one is None:
+        raise ValueError("needs x, z or both")
     n, d = shape = one.shape
     xt = one.dtype
     zt = z.dtype if z is not None else dtype or xt
@@ -1282,6 +1284,8 @@ def staple_norm_bwd(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: O
     it again (which reads x and z); in bf16 its rounding then shows in dw_pre, in fp32 it is as good and saves z
     where nothing else needs it.  dw_pre, dw_post and the gradient of a shared gate are fp32."""
     one = z if x is None else x
+    if one is None:
+        raise ValueError("needs x, z or both")
     n, d = shape = one.shape
     xt = one.dtype
     zt = z.dtype if z is not None else dh.dtype if dh is not None else xt
