@@ -45,6 +45,7 @@ static NormView view(const staple_norm_t* a) {
   v.pre = a->pre != 0;
   v.post = a->post != 0;
   v.w_bf16 = a->w_dtype == STAPLE_BF16;
+  v.r_bf16 = a->r_dtype == STAPLE_BF16;
   v.gate_kind = !a->gate.data ? Gate::kNone : a->gate.stride == 0 ? Gate::kVector : Gate::kRows;
   v.scale = a->scale;
   v.eps = a->eps;

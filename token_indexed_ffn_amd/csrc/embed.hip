@@ -16,12 +16,12 @@ constexpr int kEmbedAhead = 8;      // rows in flight a lane
 // One wave writes U blocks of 512 columns of one token's row: four where that leaves waves enough to fill the
 // GPU, whose loads are then in flight together (32768 x 2048: 41 us, one block a wave 46), otherwise one (64 x
 // 2048: 2.9 us, four 3.3 to 5.4).
-template <typename E, typename O, bool VEC, int U>
+template <typename E, typename O, Layout LAYOUT, int U>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(const E* __restrict__ table, int64_t vocab, int d,
                                                         const int32_t* __restrict__ ids, int64_t n,
                                                         float scale, O* __restrict__ y, int64_t y_stride,
                                                         int blocks, int* err) {
-  using R = RowGroup<64, VEC>;
+  using R = RowGroup<64, LAYOUT>;
   const int lane = threadIdx.x & 63;
   const int64_t items = n * blocks;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); w < items;
@@ -57,7 +57,7 @@ static bool vec_rows(const void* p, int64_t stride, int bytes) {
 template <typename E, typename O>
 static void embed_fwd(const void* table, int64_t vocab, int d, const int32_t* ids, int64_t n, float scale,
                       RowsView y, hipStream_t s, int* err) {
-  const bool vec = d % 8 == 0 && vec_rows(table, d, sizeof(E)) && vec_rows(y.data, y.stride, sizeof(O));
+  const bool aligned = d % 8 == 0 && vec_rows(table, d, sizeof(E)) && vec_rows(y.data, y.stride, sizeof(O));
   const int groups = (d + kEmbedCols - 1) / kEmbedCols;
   const E* tab = static_cast<const E*>(table);
   O* out = reinterpret_cast<O*>(y.data);
@@ -66,10 +66,12 @@ static void embed_fwd(const void* table, int64_t vocab, int d, const int32_t* id
   const int64_t wgs = (n * blocks + 3) / 4;
   const dim3 grid(static_cast<unsigned>(wgs < (1 << 20) ? wgs : (1 << 20)));
 #define GO(V, U) embed_fwd_kernel<E, O, V, U><<<grid, dim3(256), 0, s>>>(tab, vocab, d, ids, n, scale, out, y.stride, blocks, err)
-  if (vec) {
-    if (wide) GO(true, 4); else GO(true, 1);
+  if (aligned) {
+    if (wide) GO(kAligned, 4); else GO(kAligned, 1);
+  } else if (d >= 8) {
+    if (wide) GO(kLoose, 4); else GO(kLoose, 1);
   } else {
-    if (wide) GO(false, 4); else GO(false, 1);
+    GO(kSingle, 1);
   }
 #undef GO
 }
@@ -102,21 +104,26 @@ constexpr int kChunks = 8;                   // of a workgroup: one a wave
 constexpr int kSpan = kChunk * kChunks;
 constexpr int kJoinWaves = 8;
 
-// Eight elements of a row whose columns past d repeat the last one: no branch around any load (the sums
-// of such columns are stored nowhere).
-template <bool VEC, bool ONCE, typename E>
+// Eight elements of a row; columns past d repeat the last ones: no branch around any load (the sums of such
+// columns are stored nowhere).
+template <Layout LAYOUT, bool ONCE, typename E>
 __device__ __forceinline__ void load_row(const E* row, int g, int lane, int d, float (&v)[8]) {
-  using R = RowGroup<64, VEC>;
-  if (VEC) {
-    const E* p = row + min(R::column(g, lane, 0), d - 8);
-    Raw<E> raw;
-    if (ONCE) raw.load_once(p);
-    else raw.load(p);
-    raw.get(v);
-  } else {
+  using R = RowGroup<64, LAYOUT>;
+  if (LAYOUT == kSingle) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = load1(row + min(R::column(g, lane, i), d - 1));
+    return;
   }
+  const E* p = row + min(R::column(g, lane, 0), d - 8);
+  Raw<E> raw;
+  if (LAYOUT == kAligned) {
+    if (ONCE) raw.load_once(p);
+    else raw.load(p);
+  } else {
+    if (ONCE) raw.load_loose_once(p);
+    else raw.load_loose(p);
+  }
+  raw.get(v);
 }
 
 // Unique index of sorted position p, -1 where the maps are out of range.
@@ -139,9 +146,9 @@ __device__ __forceinline__ float* grad_row(const EmbedGrad& a, int32_t u, int la
   return a.grad + r * a.d;
 }
 
-template <bool VEC>
+template <Layout LAYOUT>
 __device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, int lane, float (&acc)[8]) {
-  using R = RowGroup<64, VEC>;
+  using R = RowGroup<64, LAYOUT>;
   const int d = static_cast<int>(a.d);
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] *= a.scale;
@@ -154,10 +161,10 @@ __device__ __forceinline__ void finish(const EmbedGrad& a, float* row, int g, in
   R::store(row, g, lane, d, acc);
 }
 
-template <typename E, bool VEC>
+template <typename E, Layout LAYOUT>
 __global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, int groups, float* __restrict__ first,
                                                                  float* __restrict__ last, int64_t ld, int* err) {
-  using R = RowGroup<64, VEC>;
+  using R = RowGroup<64, LAYOUT>;
   // the sums of a chunk's run that began before it, and of the one that goes on after it
   __shared__ float begun_sum[kChunks][kEmbedCols], open_sum[kChunks][kEmbedCols];
   __shared__ bool ended[kChunks];              // whether the former ends in the chunk
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, in
       // a position out of range: row 0, in a run whose sum is stored nowhere
       // (read past the caches: 32768 rows of 2048 that are not in them take 41 us, through them 54; ones that
       // were just written take 41 and 31)
-      load_row<VEC, true>(reinterpret_cast<const E*>(a.dy.data) + (r >= 0 ? r : 0) * a.dy.stride, g, lane, d, v[j]);
+      load_row<LAYOUT, true>(reinterpret_cast<const E*>(a.dy.data) + (r >= 0 ? r : 0) * a.dy.stride, g, lane, d, v[j]);
     }
     bool first_run = begun;
 #pragma unroll
@@ -210,7 +217,7 @@ __global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, in
         for (int i = 0; i < 8; ++i) to[i * 64 + lane] = acc[i];
       } else {
         float* to = grad_row(a, __builtin_amdgcn_readlane(u, k), lane, err);
-        if (to) finish<VEC>(a, to, g, lane, acc);
+        if (to) finish<LAYOUT>(a, to, g, lane, acc);
       }
       first_run = false;
 #pragma unroll
@@ -241,13 +248,13 @@ __global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, in
       R::store(last + span * ld, g, lane, d, acc);
     } else {
       float* to = grad_row(a, __builtin_amdgcn_readlane(u, len - 1), lane, err);
-      if (to) finish<VEC>(a, to, g, lane, acc);
+      if (to) finish<LAYOUT>(a, to, g, lane, acc);
     }
   }
 }
 
 // The span in which a cut run begins adds its parts: part 0 is last[c], part k first[c + k].
-template <bool VEC>
+template <Layout LAYOUT>
 __device__ __forceinline__ void add_parts(const float* first, const float* last, int64_t ld, int64_t c, int64_t k0,
                                           int64_t k1, int g, int lane, int d, float (&acc)[8]) {
   for (int64_t b = k0; b < k1; b += kEmbedAhead) {
@@ -255,7 +262,7 @@ __device__ __forceinline__ void add_parts(const float* first, const float* last,
 #pragma unroll
     for (int j = 0; j < kEmbedAhead; ++j) {
       const int64_t k = b + j < k1 ? b + j : k1 - 1;
-      load_row<VEC, false>(k == 0 ? last + c * ld : first + (c + k) * ld, g, lane, d, v[j]);
+      load_row<LAYOUT, false>(k == 0 ? last + c * ld : first + (c + k) * ld, g, lane, d, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < kEmbedAhead; ++j)
@@ -268,7 +275,7 @@ __device__ __forceinline__ void add_parts(const float* first, const float* last,
 
 // A wave looks at one span (for 512 columns) and adds up to kEmbedAhead parts itself; runs of more are
 // added by the whole workgroup.
-template <bool VEC>
+template <Layout LAYOUT>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGrad a, int groups,
                                                                          const float* __restrict__ first,
                                                                          const float* __restrict__ last, int64_t ld,
@@ -306,9 +313,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
   }
   if (parts > 0 && parts <= kEmbedAhead) {
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    add_parts<VEC>(first, last, ld, c, 0, parts, g, lane, d, acc);
+    add_parts<LAYOUT>(first, last, ld, c, 0, parts, g, lane, d, acc);
     float* to = grad_row(a, u, lane, err);
-    if (to) finish<VEC>(a, to, g, lane, acc);
+    if (to) finish<LAYOUT>(a, to, g, lane, acc);
   }
   __syncthreads();
   for (int w = 0; w < kJoinWaves; ++w) {
@@ -317,7 +324,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
     const int64_t each = (all + kJoinWaves - 1) / kJoinWaves;
     const int64_t k0 = wave * each, k1 = k0 + each < all ? k0 + each : all;
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    add_parts<VEC>(first, last, ld, c0 + w, k0, k1, g, lane, d, acc);
+    add_parts<LAYOUT>(first, last, ld, c0 + w, k0, k1, g, lane, d, acc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[wave][i * 64 + lane] = acc[i];
     __syncthreads();
@@ -327,7 +334,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_bwd_join_kernel(EmbedGr
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += part[k][i * 64 + lane];
       float* to = grad_row(a, long_token[w], lane, err);
-      if (to) finish<VEC>(a, to, g, lane, acc);
+      if (to) finish<LAYOUT>(a, to, g, lane, acc);
     }
     __syncthreads();
   }
@@ -340,24 +347,25 @@ size_t embed_bwd_workspace_bytes(int64_t n, int64_t d) {
   return spans > 1 ? static_cast<size_t>(2 * spans * part_stride(d)) * sizeof(float) : 0;
 }
 
-template <typename E, bool VEC>
+template <typename E, Layout LAYOUT>
 static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
   const int64_t spans = (a.n_tokens + kSpan - 1) / kSpan, ld = part_stride(a.d);
   float* first = static_cast<float*>(ws);
   float* last = first + spans * ld;
   const int groups = static_cast<int>((a.d + kEmbedCols - 1) / kEmbedCols);
-  embed_bwd_kernel<E, VEC><<<dim3(static_cast<unsigned>(spans * groups)), dim3(64 * kChunks), 0, s>>>(
+  embed_bwd_kernel<E, LAYOUT><<<dim3(static_cast<unsigned>(spans * groups)), dim3(64 * kChunks), 0, s>>>(
       a, groups, first, last, ld, err);
   if (spans > 1)
-    embed_bwd_join_kernel<VEC><<<dim3(static_cast<unsigned>((spans + kJoinWaves - 1) / kJoinWaves * groups)),
+    embed_bwd_join_kernel<LAYOUT><<<dim3(static_cast<unsigned>((spans + kJoinWaves - 1) / kJoinWaves * groups)),
                                  dim3(64 * kJoinWaves), 0, s>>>(a, groups, first, last, ld, err);
 }
 
 template <typename E>
 static void embed_bwd(const EmbedGrad& a, void* ws, hipStream_t s, int* err) {
-  const bool vec = a.d % 8 == 0 && vec_rows(a.dy.data, a.dy.stride, sizeof(E)) && vec_rows(a.grad, a.d, 4);
-  if (vec) embed_bwd<E, true>(a, ws, s, err);
-  else embed_bwd<E, false>(a, ws, s, err);
+  const bool aligned = a.d % 8 == 0 && vec_rows(a.dy.data, a.dy.stride, sizeof(E)) && vec_rows(a.grad, a.d, 4);
+  if (aligned) embed_bwd<E, kAligned>(a, ws, s, err);
+  else if (a.d >= 8) embed_bwd<E, kLoose>(a, ws, s, err);
+  else embed_bwd<E, kSingle>(a, ws, s, err);
 }
 
 hipError_t launch_embed_bwd(const EmbedGrad& a, int32_t dtype, void* ws, hipStream_t s, int* err) {

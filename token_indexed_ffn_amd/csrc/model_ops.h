@@ -34,7 +34,7 @@ enum class Gate { kNone, kVector, kRows };
 struct NormView {
   int64_t n_rows;
   int d;
-  bool pre, post, w_bf16;
+  bool pre, post, w_bf16, r_bf16;
   Gate gate_kind;
   float scale, eps;
   RowsView x, z, gate, r, h;

@@ -18,9 +18,9 @@
 namespace staple {
 
 // Eight elements of a vector shared by the rows (ones when NULL).
-template <int T, bool VEC>
+template <int T, Layout LAYOUT>
 __device__ __forceinline__ void load_shared(const void* p, bool bf16, int g, int t, int d, float (&v)[8]) {
-  using R = RowGroup<T, VEC>;
+  using R = RowGroup<T, LAYOUT>;
   if (p == nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 1.0f;
@@ -37,9 +37,9 @@ __device__ __forceinline__ E* row_of(const RowsView& v, int64_t i) {
 }
 
 // T lanes a row, G groups of eight elements a lane; rows of one wave share a workgroup.
-template <typename X, typename Z, int T, int G, bool VEC>
+template <typename X, typename Z, int T, int G, Layout LAYOUT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a) {
-  using R = RowGroup<T, VEC>;
+  using R = RowGroup<T, LAYOUT>;
   constexpr int kRows = T < 256 ? 256 / T : 1;
   __shared__ float tmp[2][kRows][T / 64];
   const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d;
@@ -70,12 +70,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a)
 #pragma unroll
       for (int k = 0; k < 8; ++k) b[g][k] *= rstd;
       if (a.post && a.w_post) {
-        load_shared<T, VEC>(a.w_post, a.w_bf16, g, t, d, w);
+        load_shared<T, LAYOUT>(a.w_post, a.w_bf16, g, t, d, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) b[g][k] *= w[k];
       }
       if (a.gate_kind != Gate::kNone) {
-        if (a.gate_kind == Gate::kVector) load_shared<T, VEC>(a.gate.data, a.w_bf16, g, t, d, w);
+        if (a.gate_kind == Gate::kVector) load_shared<T, LAYOUT>(a.gate.data, a.w_bf16, g, t, d, w);
         else R::load(row_of<const Z>(a.gate, i), g, t, d, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) b[g][k] *= w[k];
@@ -96,26 +96,33 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a)
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     float w[8];
-    load_shared<T, VEC>(a.w_pre, a.w_bf16, g, t, d, w);
+    load_shared<T, LAYOUT>(a.w_pre, a.w_bf16, g, t, d, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) r[g][k] *= inv * w[k];
     R::store(row_of<Z>(a.h, i), g, t, d, r[g]);
   }
 }
 
-// V (4 or 8) elements of a row that a lane of the backward holds of group g, as they lie in memory where
-// they are aligned (VEC): elements (g T + t) V on, otherwise (g V + i) T + t.
-template <typename E, int T, bool VEC, int V>
+// V (4 or 8) elements of a row that a lane of the backward holds of group g, as they lie in memory: as in a
+// RowGroup, with V for eight.
+template <typename E, int T, Layout LAYOUT, int V>
 struct Part {
-  static constexpr int kWords = VEC ? V * static_cast<int>(sizeof(E)) / 4 : V;
+  static constexpr int kWords = LAYOUT == kSingle ? V : V * static_cast<int>(sizeof(E)) / 4;
   typedef __attribute__((ext_vector_type(kWords))) uint32_t words_t;
+  typedef typename LooseWords<E, kWords>::type loose_t;
   words_t w;
-  __device__ __forceinline__ static int column(int g, int t, int i) { return VEC ? (g * T + t) * V + i : (g * V + i) * T + t; }
+  __device__ __forceinline__ static int column(int g, int t, int i) {
+    return LAYOUT == kSingle ? (g * V + i) * T + t : (g * T + t) * V + i;
+  }
+  __device__ __forceinline__ static int skip(int g, int t, int d) { return max(column(g, t, 0) - (d - V), 0); }
   // ONCE: rows, which nothing reads again soon, past the caches
   template <bool ONCE>
   __device__ __forceinline__ void load(const E* row, int g, int t, int d) {
-    if (VEC) {   // lanes past the end: the last elements again
+    if (LAYOUT == kAligned) {   // lanes past the end: the last elements again
       const words_t* p = reinterpret_cast<const words_t*>(row + min(column(g, t, 0), d - V));
+      w = ONCE ? __builtin_nontemporal_load(p) : *p;
+    } else if (LAYOUT == kLoose) {
+      const loose_t* p = reinterpret_cast<const loose_t*>(row + min(column(g, t, 0), d - V));
       w = ONCE ? __builtin_nontemporal_load(p) : *p;
     } else {
 #pragma unroll
@@ -124,221 +131,262 @@ struct Part {
   }
   // 0 past the row's end.
   __device__ __forceinline__ void get(float (&v)[V], int g, int t, int d) const {
+    const int none = skip(g, t, d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (VEC && sizeof(E) == 2) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      if (LAYOUT != kSingle && sizeof(E) == 2) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
       else v[i] = __uint_as_float(w[i]);
-      if (column(g, t, i) >= d) v[i] = 0.0f;
+      if (LAYOUT == kLoose ? i < none : column(g, t, i) >= d) v[i] = 0.0f;
     }
   }
   __device__ __forceinline__ static void store(E* row, int g, int t, int d, const float (&v)[V]) {
-    if (VEC) {
-      if (column(g, t, 0) >= d) return;
+    if (LAYOUT == kSingle) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (column(g, t, i) < d) store1(row + column(g, t, i), v[i]);
+      return;
+    }
+    const int none = skip(g, t, d);
+    if (none == 0) {
       words_t x;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         if (sizeof(E) == 2) x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         else x[i] = __float_as_uint(v[i]);
       }
-      *reinterpret_cast<words_t*>(row + column(g, t, 0)) = x;
-    } else {
+      E* p = row + column(g, t, 0);
+      if (LAYOUT == kAligned) *reinterpret_cast<words_t*>(p) = x;
+      else *reinterpret_cast<loose_t*>(p) = x;
+    } else if (LAYOUT == kLoose && none < V) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (column(g, t, i) < d) store1(row + column(g, t, i), v[i]);
+      for (int i = 1; i < V; ++i)
+        if (i >= none) store1(row + d - V + i, v[i]);
     }
   }
 };
 
 // A vector shared by the rows: ones when NULL.
-template <int T, bool VEC, int V>
+template <int T, Layout LAYOUT, int V>
 __device__ __forceinline__ void load_vector(const void* p, bool bf16, int g, int t, int d, float (&v)[V]) {
   if (p == nullptr) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 1.0f;
   } else if (bf16) {
-    Part<bf16_t, T, VEC, V> x;
+    Part<bf16_t, T, LAYOUT, V> x;
     x.template load<false>(static_cast<const bf16_t*>(p), g, t, d);
     x.get(v, g, t, d);
   } else {
-    Part<float, T, VEC, V> x;
+    Part<float, T, LAYOUT, V> x;
     x.template load<false>(static_cast<const float*>(p), g, t, d);
     x.get(v, g, t, d);
   }
 }
 
-// What the backward reads of a row.
-template <typename X, typename Z, int T, int G, bool VEC, int V>
+// What the backward reads of group g of a row.
+template <typename X, typename Z, int T, Layout LAYOUT, int V>
 struct NormRow {
-  Part<X, T, VEC, V> dr[G], r[G];   // r: the stored sum, or x
-  Part<Z, T, VEC, V> dh[G], z[G], gate[G];
+  Part<X, T, LAYOUT, V> dr, r;   // r: the stored sum, or x
+  Part<Z, T, LAYOUT, V> dh, z, gate;
   float rstd_r, rstd_z;
-  __device__ __forceinline__ void load(const NormView& a, int64_t i, int t, bool need_z) {
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const NormView& a, int64_t i, int g, int t, bool need_z) {
     const RowsView& sum = a.r.data ? a.r : a.x;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (a.dr.data) dr[g].template load<true>(row_of<const X>(a.dr, i), g, t, a.d);
-      if (a.pre) {
-        if (sum.data) r[g].template load<true>(row_of<const X>(sum, i), g, t, a.d);
-        dh[g].template load<true>(row_of<const Z>(a.dh, i), g, t, a.d);
-      }
-      if (need_z) z[g].template load<true>(row_of<const Z>(a.z, i), g, t, a.d);
-      if (a.gate_kind == Gate::kRows) gate[g].template load<true>(row_of<const Z>(a.gate, i), g, t, a.d);
+    if (a.dr.data) dr.template load<ONCE>(row_of<const X>(a.dr, i), g, t, a.d);
+    if (a.pre) {
+      if (sum.data) r.template load<ONCE>(row_of<const X>(sum, i), g, t, a.d);
+      dh.template load<ONCE>(row_of<const Z>(a.dh, i), g, t, a.d);
     }
+    if (need_z) z.template load<ONCE>(row_of<const Z>(a.z, i), g, t, a.d);
+    if (a.gate_kind == Gate::kRows) gate.template load<ONCE>(row_of<const Z>(a.gate, i), g, t, a.d);
     rstd_r = a.pre ? a.rstd_r[i] : 0.0f;
     rstd_z = a.post ? a.rstd_z[i] : 1.0f;
   }
 };
 
 // Waves a SIMD that the backward is held to the registers of; its grid fills the GPU with them once.
-constexpr int norm_bwd_waves(int lanes, int v) { return lanes >= 512 ? 4 : v == 4 ? 5 : 3; }
+constexpr int norm_bwd_waves(int lanes, int v) { return lanes >= 512 || v == 4 ? 4 : 3; }
 
 // Workgroups work off rows in turn, the next row's loads in flight, and keep the sums over their rows, and
 // the weights, in registers; parts: [vectors][slots of all workgroups][d], added up by norm_columns_kernel in
-// slot order.
-template <typename X, typename Z, int T, int G, bool VEC, int V>
-__global__ __launch_bounds__(T < 256 ? 256 : T, norm_bwd_waves(T, V)) void norm_bwd_kernel(NormView a, float* parts) {
+// slot order.  SLABS: a workgroup takes group blockIdx.y of its rows, T V columns, and norm_means_kernel's means,
+// two a row, from the last row on, of which the caches still have most; otherwise whole rows, whose means it
+// forms itself.
+template <typename X, typename Z, int T, Layout LAYOUT, int V, bool SLABS>
+__global__ __launch_bounds__(T < 256 ? 256 : T, norm_bwd_waves(T, V)) void norm_bwd_kernel(NormView a, const float* means,
+                                                                                         float* parts) {
   constexpr int kRows = T < 256 ? 256 / T : 1;
-  constexpr bool kKept = G == 1;   // the weights
   // two sums a row, in buffers of their own for rows in turn: between a sum's reads and the
   // next writes to its buffer stands the barrier of the row between
   __shared__ float tmp[2][2][kRows][T / 64];
-  const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d;
+  const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d, g = SLABS ? blockIdx.y : 0;
   const float inv_d = 1.0f / static_cast<float>(d);
   const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kRows + slot;
+  const auto row_at = [&](int64_t i) { return SLABS ? a.n_rows - 1 - i : i; };
   const bool branch = norm_bwd_branch(a), need_z = norm_bwd_reads_z(a);
   const bool rows_gate = a.gate_kind == Gate::kRows;
-  float sum_pre[G][V], sum_post[G][V], sum_gate[G][V], w_pre[G][V], w_post[G][V], gate[G][V];
+  float sum_pre[V], sum_post[V], sum_gate[V], w_pre[V], w_post[V], gate[V];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) sum_pre[g][k] = sum_post[g][k] = sum_gate[g][k] = 0.0f;
-    if (kKept) {
-      load_vector<T, VEC, V>(a.w_pre, a.w_bf16, g, t, d, w_pre[g]);
-      load_vector<T, VEC, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post[g]);
-      load_vector<T, VEC, V>(rows_gate ? nullptr : a.gate.data, a.w_bf16, g, t, d, gate[g]);
-    }
-  }
-  NormRow<X, Z, T, G, VEC, V> next;
-  if (me < a.n_rows) next.load(a, me, t, need_z);
+  for (int k = 0; k < V; ++k) sum_pre[k] = sum_post[k] = sum_gate[k] = 0.0f;
+  load_vector<T, LAYOUT, V>(a.w_pre, a.w_bf16, g, t, d, w_pre);
+  load_vector<T, LAYOUT, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post);
+  load_vector<T, LAYOUT, V>(rows_gate ? nullptr : a.gate.data, a.w_bf16, g, t, d, gate);
+  NormRow<X, Z, T, LAYOUT, V> next;
+  float next_mean = 0.0f, next_mean_z = 0.0f;
+  const auto read_means = [&](int64_t i) {
+    if (!SLABS) return;
+    next_mean = means[2 * i];
+    next_mean_z = means[2 * i + 1];
+  };
+  if (me < a.n_rows) read_means(row_at(me));
+  if (me < a.n_rows) next.template load<!SLABS>(a, row_at(me), g, t, need_z);
   int odd = 0;
   for (int64_t i = me; i < a.n_rows; i += slots, odd ^= 1) {
-    const NormRow<X, Z, T, G, VEC, V> row = next;
-    if (i + slots < a.n_rows) next.load(a, i + slots, t, need_z);
-    float q[G][V], hat_z[G][V];
+    const int64_t at = row_at(i);
+    const NormRow<X, Z, T, LAYOUT, V> row = next;
+    const float given_mean = next_mean, given_mean_z = next_mean_z;
+    if (i + slots < a.n_rows) read_means(row_at(i + slots));
+    if (i + slots < a.n_rows) next.template load<!SLABS>(a, row_at(i + slots), g, t, need_z);
+    float q[V], hat_z[V];
     const float inv_z = row.rstd_z;
+    if (need_z) {
+      row.z.get(hat_z, g, t, d);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (need_z) {
-        row.z[g].get(hat_z[g], g, t, d);
-#pragma unroll
-        for (int k = 0; k < V; ++k) hat_z[g][k] *= inv_z;
-      }
-      if (rows_gate) row.gate[g].get(gate[g], g, t, d);
-      else if (!kKept) load_vector<T, VEC, V>(a.gate.data, a.w_bf16, g, t, d, gate[g]);
-      if (!kKept) load_vector<T, VEC, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post[g]);
+      for (int k = 0; k < V; ++k) hat_z[k] *= inv_z;
     }
+    if (rows_gate) row.gate.get(gate, g, t, d);
     if (a.pre) {
       const float inv = row.rstd_r;
-      float hat[G][V], dt[G][V], dot = 0.0f;
+      float hat[V], dt[V], dot = 0.0f;
+      if (a.r.data) {
+        row.r.get(hat, g, t, d);
+      } else {   // as the forward had it before r was rounded
+        float x[V];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (a.r.data) {
-          row.r[g].get(hat[g], g, t, d);
-        } else {   // as the forward had it before r was rounded
-          float x[V];
+        for (int k = 0; k < V; ++k) x[k] = 0.0f;
+        if (a.x.data) row.r.get(x, g, t, d);
 #pragma unroll
-          for (int k = 0; k < V; ++k) x[k] = 0.0f;
-          if (a.x.data) row.r[g].get(x, g, t, d);
-#pragma unroll
-          for (int k = 0; k < V; ++k) hat[g][k] = x[k] + a.scale * gate[g][k] * w_post[g][k] * hat_z[g][k];
-        }
-        row.dh[g].get(dt[g], g, t, d);
-        if (!kKept) load_vector<T, VEC, V>(a.w_pre, a.w_bf16, g, t, d, w_pre[g]);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          hat[g][k] *= inv;
-          sum_pre[g][k] += dt[g][k] * hat[g][k];
-          dt[g][k] *= w_pre[g][k];
-          dot += dt[g][k] * hat[g][k];
-        }
+        for (int k = 0; k < V; ++k) hat[k] = x[k] + a.scale * gate[k] * w_post[k] * hat_z[k];
       }
-      const float mean = row_sum<T>(dot, tmp[odd][0][slot], t) * inv_d;
+      row.dh.get(dt, g, t, d);
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int k = 0; k < V; ++k) {
+        hat[k] *= inv;
+        sum_pre[k] += dt[k] * hat[k];
+        dt[k] *= w_pre[k];
+        dot += dt[k] * hat[k];
+      }
+      const float mean = SLABS ? given_mean : row_sum<T>(dot, tmp[odd][0][slot], t) * inv_d;
 #pragma unroll
-        for (int k = 0; k < V; ++k) q[g][k] = inv * (dt[g][k] - hat[g][k] * mean);
+      for (int k = 0; k < V; ++k) q[k] = inv * (dt[k] - hat[k] * mean);
     } else {
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int k = 0; k < V; ++k) q[g][k] = 0.0f;
+      for (int k = 0; k < V; ++k) q[k] = 0.0f;
     }
+    if (a.dr.data) {
+      float v[V];
+      row.dr.get(v, g, t, d);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (a.dr.data) {
-        float v[V];
-        row.dr[g].get(v, g, t, d);
-#pragma unroll
-        for (int k = 0; k < V; ++k) q[g][k] += v[k];
-      }
-      if (a.dx.data) Part<X, T, VEC, V>::store(row_of<X>(a.dx, i), g, t, d, q[g]);
+      for (int k = 0; k < V; ++k) q[k] += v[k];
     }
+    if (a.dx.data) Part<X, T, LAYOUT, V>::store(row_of<X>(a.dx, at), g, t, d, q);
     if (!branch) continue;
     float dot = 0.0f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) q[g][k] *= a.scale;
-      if (a.gate_kind != Gate::kNone) {
-        if (a.dgate.data || a.dgate_sum) {
-          float dg[V];
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            dg[k] = q[g][k] * hat_z[g][k] * w_post[g][k];
-            sum_gate[g][k] += dg[k];
-          }
-          if (a.dgate.data) Part<Z, T, VEC, V>::store(row_of<Z>(a.dgate, i), g, t, d, dg);
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) q[g][k] *= gate[g][k];
-      }
-      if (a.post) {
+    for (int k = 0; k < V; ++k) q[k] *= a.scale;
+    if (a.gate_kind != Gate::kNone) {
+      if (a.dgate.data || a.dgate_sum) {
+        float dg[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          sum_post[g][k] += q[g][k] * hat_z[g][k];
-          q[g][k] *= w_post[g][k];
-          dot += q[g][k] * hat_z[g][k];
+          dg[k] = q[k] * hat_z[k] * w_post[k];
+          sum_gate[k] += dg[k];
         }
+        if (a.dgate.data) Part<Z, T, LAYOUT, V>::store(row_of<Z>(a.dgate, at), g, t, d, dg);
       }
+#pragma unroll
+      for (int k = 0; k < V; ++k) q[k] *= gate[k];
     }
     if (a.post) {
-      const float mean = row_sum<T>(dot, tmp[odd][1][slot], t) * inv_d;
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int k = 0; k < V; ++k) {
+        sum_post[k] += q[k] * hat_z[k];
+        q[k] *= w_post[k];
+        dot += q[k] * hat_z[k];
+      }
+      const float mean = SLABS ? given_mean_z : row_sum<T>(dot, tmp[odd][1][slot], t) * inv_d;
 #pragma unroll
-        for (int k = 0; k < V; ++k) q[g][k] = inv_z * (q[g][k] - hat_z[g][k] * mean);
+      for (int k = 0; k < V; ++k) q[k] = inv_z * (q[k] - hat_z[k] * mean);
     }
-    if (a.dz.data) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) Part<Z, T, VEC, V>::store(row_of<Z>(a.dz, i), g, t, d, q[g]);
-    }
+    if (a.dz.data) Part<Z, T, LAYOUT, V>::store(row_of<Z>(a.dz, at), g, t, d, q);
   }
   float* part = parts + me * d;
   const int64_t one = slots * d;
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    float* p = part;
-    if (a.dw_pre) {
-      Part<float, T, VEC, V>::store(p, g, t, d, sum_pre[g]);
-      p += one;
-    }
-    if (a.dw_post) {
-      Part<float, T, VEC, V>::store(p, g, t, d, sum_post[g]);
-      p += one;
-    }
-    if (a.dgate_sum) Part<float, T, VEC, V>::store(p, g, t, d, sum_gate[g]);
+  if (a.dw_pre) {
+    Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_pre);
+    part += one;
   }
+  if (a.dw_post) {
+    Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_post);
+    part += one;
+  }
+  if (a.dgate_sum) Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_gate);
+}
+
+// The means of wide rows, for norm_bwd_kernel's slabs, both from sums of one pass: with c = s gate w_post hat(z),
+// a = dr + t / rms(r) and m = mean(t hat(r)),
+//   g = a - hat(r) m / rms(r),    mean(q w_post hat(z)) = mean(c g) = mean(c a) - m mean(c hat(r) / rms(r)).
+template <typename X, typename Z, Layout LAYOUT>
+__global__ __launch_bounds__(512) void norm_means_kernel(NormView a, float* means) {
+  constexpr int T = 512, V = 8;
+  __shared__ float tmp[3][T / 64];
+  const int t = threadIdx.x, d = a.d;
+  const int64_t i = blockIdx.x;
+  const bool need_z = norm_bwd_reads_z(a), rows_gate = a.gate_kind == Gate::kRows;
+  float s[3] = {0.0f, 0.0f, 0.0f};
+  for (int g = 0; g * T * V < d; ++g) {
+    NormRow<X, Z, T, LAYOUT, V> row;
+    row.template load<false>(a, i, g, t, need_z);
+    float sums[V], hat[V], dh[V], hat_z[V], w_pre[V], w_post[V], gate[V];
+    load_vector<T, LAYOUT, V>(a.pre ? a.w_pre : nullptr, a.w_bf16, g, t, d, w_pre);
+    load_vector<T, LAYOUT, V>(a.post ? a.w_post : nullptr, a.w_bf16, g, t, d, w_post);
+    if (rows_gate) row.gate.get(gate, g, t, d);
+    else load_vector<T, LAYOUT, V>(a.gate.data, a.w_bf16, g, t, d, gate);
+#pragma unroll
+    for (int k = 0; k < V; ++k) sums[k] = hat[k] = dh[k] = hat_z[k] = 0.0f;
+    if (need_z) row.z.get(hat_z, g, t, d);
+    if (a.dr.data) row.dr.get(sums, g, t, d);
+    if (a.pre) {
+      row.dh.get(dh, g, t, d);
+      if (a.r.data || a.x.data) row.r.get(hat, g, t, d);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float c = a.scale * gate[k] * w_post[k] * (hat_z[k] * row.rstd_z), tk = dh[k] * w_pre[k];
+      if (!a.r.data) hat[k] += c;   // as the forward had it
+      hat[k] *= row.rstd_r;
+      s[0] += tk * hat[k];
+      s[1] += c * (sums[k] + row.rstd_r * tk);
+      s[2] += c * (hat[k] * row.rstd_r);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    s[j] = wave_sum(s[j]);
+    if ((t & 63) == 0) tmp[j][t >> 6] = s[j];
+  }
+  __syncthreads();
+  if (t > 0) return;
+  const float inv_d = 1.0f / static_cast<float>(d);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    s[j] = tmp[j][0];
+#pragma unroll
+    for (int k = 1; k < T / 64; ++k) s[j] += tmp[j][k];
+    s[j] *= inv_d;
+  }
+  means[2 * i] = s[0];
+  means[2 * i + 1] = s[1] - s[0] * s[2];
 }
 
 // Sums of the parts, 16 columns a workgroup: 64 of its lanes a column, which add slots k, k + 64, ... and
@@ -373,12 +421,15 @@ static bool vec_view(const RowsView& v, int bytes) {
 }
 static bool vec_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-static bool norm_vec(const NormView& v, int32_t r_dtype, int32_t dtype) {
+static Layout norm_layout(const NormView& v, int32_t r_dtype, int32_t dtype) {
   const int xb = r_dtype == STAPLE_BF16 ? 2 : 4, zb = dtype == STAPLE_BF16 ? 2 : 4;
   const bool gate = v.gate_kind == Gate::kRows ? vec_view(v.gate, zb) : vec_ptr(v.gate.data);
-  return v.d % 8 == 0 && vec_view(v.x, xb) && vec_view(v.r, xb) && vec_view(v.dr, xb) && vec_view(v.dx, xb) &&
+  if (v.d < 8) return kSingle;
+  const bool aligned =
+      v.d % 8 == 0 && vec_view(v.x, xb) && vec_view(v.r, xb) && vec_view(v.dr, xb) && vec_view(v.dx, xb) &&
          vec_view(v.z, zb) && vec_view(v.h, zb) && vec_view(v.dh, zb) && vec_view(v.dz, zb) &&
          vec_view(v.dgate, zb) && gate && vec_ptr(v.w_pre) && vec_ptr(v.w_post);
+  return aligned ? kAligned : kLoose;
 }
 
 // Lanes a row and groups of eight elements a lane: rows of up to 1024 in a wave, whose sums need no LDS, wider
@@ -396,39 +447,44 @@ static bool norm_vec(const NormView& v, int32_t r_dtype, int32_t dtype) {
 // The backward's, with elements a group: its sums, weights and loads in flight are some 20 registers an
 // element, so that four elements a lane in more lanes leave more waves a SIMD: 2048 in 512 x 4 takes 153 us, in
 // 256 x 8 233; 4096 in 1024 x 4 198, in 512 x 8 230 (both before rows were read past the caches).
-#define NORM_BWD_SHAPES(GO)                      \
-  do {                                           \
-    if (v.d <= 256) GO(64, 1, 4);                \
-    else if (v.d <= 512) GO(64, 1, 8);           \
-    else if (v.d <= 1024) GO(256, 1, 4);         \
-    else if (v.d <= 2048) GO(512, 1, 4);         \
-    else if (v.d <= 4096) GO(1024, 1, 4);        \
-    else if (v.d <= 8192) GO(1024, 1, 8);        \
-    else GO(1024, 2, 8);                         \
+// Wider rows spill there (8192 with r in fp32: 252 to 350 us for 4096 rows; bf16, 16384: 493 for 2048) and are
+// read twice: means first, then slabs of 1024 columns.
+#define NORM_BWD_SHAPES(GO, SLABS)                    \
+  do {                                                \
+    if (v.d <= 256) GO(64, 4);                        \
+    else if (v.d <= 512) GO(64, 8);                   \
+    else if (v.d <= 1024) GO(256, 4);                 \
+    else if (v.d <= 2048) GO(512, 4);                 \
+    else if (v.d <= 4096) GO(1024, 4);                \
+    else if (v.d <= 8192 && v.r_bf16) GO(1024, 8);    \
+    else SLABS(256, 4);                               \
   } while (0)
 struct NormBwdShape {
-  int lanes, groups, elements;
+  int lanes, elements, slabs;
   int rows() const { return lanes < 256 ? 256 / lanes : 1; }                 // of a workgroup
   int64_t workgroups() const {                                               // that fill the GPU
     const int waves = (lanes < 256 ? 256 : lanes) / 64;
     const int a_cu = norm_bwd_waves(lanes, elements) * 4 / waves;
-    return static_cast<int64_t>(device_cus()) * (a_cu > 0 ? a_cu : 1);
+    return (static_cast<int64_t>(device_cus()) * (a_cu > 0 ? a_cu : 1) + slabs - 1) / slabs;
   }
 };
 static NormBwdShape norm_bwd_shape(const NormView& v) {
-#define GO(T, G, V) return NormBwdShape{T, G, V}
-  NORM_BWD_SHAPES(GO);
+#define GO(T, V) return NormBwdShape{T, V, 1}
+#define SLABS(T, V) return NormBwdShape{T, V, (v.d + T * V - 1) / (T * V)}
+  NORM_BWD_SHAPES(GO, SLABS);
+#undef SLABS
 #undef GO
 }
 
 static int norm_rows_a_workgroup(int d) { return d <= 1024 ? 4 : 1; }
 
-template <typename X, typename Z, bool VEC>
+template <typename X, typename Z, Layout LAYOUT>
 static void norm_fwd(const NormView& v, hipStream_t s) {
   const int rows = norm_rows_a_workgroup(v.d);
   const dim3 grid(static_cast<unsigned>((v.n_rows + rows - 1) / rows));
-#define GO(T, G) norm_fwd_kernel<X, Z, T, G, VEC><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v)
-  NORM_SHAPES(GO);
+#define GO(T, G) norm_fwd_kernel<X, Z, T, G, LAYOUT><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v)
+  if constexpr (LAYOUT == kSingle) GO(64, 1);
+  else NORM_SHAPES(GO);
 #undef GO
 }
 
@@ -443,15 +499,30 @@ static int64_t norm_bwd_grid(const NormView& v) {
 }
 
 size_t norm_bwd_workspace_bytes(const NormView& v) {
-  return static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * norm_bwd_shape(v).rows() * v.d * sizeof(float);
+  const NormBwdShape shape = norm_bwd_shape(v);
+  const size_t means = shape.slabs > 1 ? 2 * static_cast<size_t>(v.n_rows) : 0;
+  return (means + static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * shape.rows() * v.d) * sizeof(float);
 }
 
-template <typename X, typename Z, bool VEC>
-static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
+template <typename X, typename Z, Layout LAYOUT>
+static void norm_bwd(const NormView& v, float* ws, hipStream_t s) {
+  const NormBwdShape shape = norm_bwd_shape(v);
   const dim3 grid(static_cast<unsigned>(norm_bwd_grid(v)));
+  float *means = ws, *parts = shape.slabs > 1 ? ws + 2 * v.n_rows : ws;
   if (v.n_rows > 0) {
-#define GO(T, G, V) norm_bwd_kernel<X, Z, T, G, VEC, V><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v, parts)
-    NORM_BWD_SHAPES(GO);
+#define GO(T, V)                                                                                             \
+  do {                                                                                                       \
+    if constexpr (T * V <= 4096 || sizeof(X) == 2)                                                           \
+      norm_bwd_kernel<X, Z, T, LAYOUT, V, false><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v, nullptr, parts); \
+  } while (0)
+#define SLABS(T, V)                                                                                          \
+  do {                                                                                                       \
+    norm_means_kernel<X, Z, LAYOUT><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(512), 0, s>>>(v, means);   \
+    norm_bwd_kernel<X, Z, T, LAYOUT, V, true><<<dim3(grid.x, shape.slabs), dim3(T), 0, s>>>(v, means, parts); \
+  } while (0)
+    if constexpr (LAYOUT == kSingle) GO(64, 4);
+    else NORM_BWD_SHAPES(GO, SLABS);
+#undef SLABS
 #undef GO
   }
   const int n = norm_vectors(v);
@@ -461,18 +532,20 @@ static void norm_bwd(const NormView& v, float* parts, hipStream_t s) {
   for (float* p : {v.dw_pre, v.dw_post, v.dgate_sum})
     if (p) out[k++] = p;
   norm_columns_kernel<<<dim3((v.d + 15) / 16, n), dim3(1024), 0, s>>>(
-      parts, static_cast<int>(grid.x) * norm_bwd_shape(v).rows(), v.d, out[0], out[1], out[2]);
+      parts, static_cast<int>(grid.x) * shape.rows(), v.d, out[0], out[1], out[2]);
 }
 
+#define NORM_LAYOUTS(CALL, X, Z)                  \
+  do {                                            \
+    if (layout == kAligned) CALL(X, Z, kAligned); \
+    else if (layout == kLoose) CALL(X, Z, kLoose); \
+    else CALL(X, Z, kSingle);                     \
+  } while (0)
 #define NORM_TYPES(CALL)                                                         \
-  const bool vec = norm_vec(v, r_dtype, dtype);                                  \
-  if (r_dtype == STAPLE_BF16) {                                                  \
-    if (vec) CALL(bf16_t, bf16_t, true); else CALL(bf16_t, bf16_t, false);       \
-  } else if (dtype == STAPLE_BF16) {                                             \
-    if (vec) CALL(float, bf16_t, true); else CALL(float, bf16_t, false);         \
-  } else {                                                                       \
-    if (vec) CALL(float, float, true); else CALL(float, float, false);           \
-  }
+  const Layout layout = norm_layout(v, r_dtype, dtype);                          \
+  if (r_dtype == STAPLE_BF16) NORM_LAYOUTS(CALL, bf16_t, bf16_t);                \
+  else if (dtype == STAPLE_BF16) NORM_LAYOUTS(CALL, float, bf16_t);              \
+  else NORM_LAYOUTS(CALL, float, float);
 
 hipError_t launch_norm_fwd(const NormView& v, int32_t r_dtype, int32_t dtype, hipStream_t s) {
 #define CALL(X, Z, V) norm_fwd<X, Z, V>(v, s)
@@ -482,8 +555,7 @@ hipError_t launch_norm_fwd(const NormView& v, int32_t r_dtype, int32_t dtype, hi
 }
 
 hipError_t launch_norm_bwd(const NormView& v, int32_t r_dtype, int32_t dtype, void* ws, hipStream_t s) {
-  float* parts = static_cast<float*>(ws);
-#define CALL(X, Z, V) norm_bwd<X, Z, V>(v, parts, s)
+#define CALL(X, Z, V) norm_bwd<X, Z, V>(v, static_cast<float*>(ws), s)
   NORM_TYPES(CALL)
 #undef CALL
   return hipGetLastError();

@@ -39,7 +39,12 @@ __device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(p->
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16_t* p, float v) { p->bits = f32_to_bf16(v); }
 
-// Eight elements as they lie in memory, 16-byte aligned.
+// Words that begin at any element of type E: global memory takes 16 bytes at any address.
+template <typename E, int WORDS> struct LooseWords {
+  typedef __attribute__((ext_vector_type(WORDS), aligned(sizeof(E)))) uint32_t type;
+};
+
+// Eight elements as they lie in memory, 16-byte aligned (load) or not (load_loose).
 template <typename E> struct Raw;
 template <> struct Raw<bf16_t> {
   u32x4_t a;
@@ -47,6 +52,9 @@ template <> struct Raw<bf16_t> {
   __device__ __forceinline__ void clear() { a = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
   // Of data that nothing reads again soon: it is not to push other lines out of the caches.
   __device__ __forceinline__ void load_once(const bf16_t* p) { a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p)); }
+  typedef LooseWords<bf16_t, 4>::type loose_t;
+  __device__ __forceinline__ void load_loose(const bf16_t* p) { a = *reinterpret_cast<const loose_t*>(p); }
+  __device__ __forceinline__ void load_loose_once(const bf16_t* p) { a = __builtin_nontemporal_load(reinterpret_cast<const loose_t*>(p)); }
   // What was made of these elements is made again after this, rather than kept in registers.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -70,6 +78,15 @@ template <> struct Raw<float> {
   __device__ __forceinline__ void load_once(const float* p) {
     a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
     b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p + 4));
+  }
+  typedef __attribute__((ext_vector_type(4), aligned(4))) float loose_t;
+  __device__ __forceinline__ void load_loose(const float* p) {
+    a = *reinterpret_cast<const loose_t*>(p);
+    b = *reinterpret_cast<const loose_t*>(p + 4);
+  }
+  __device__ __forceinline__ void load_loose_once(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const loose_t*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const loose_t*>(p + 4));
   }
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a), "+v"(b)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -101,24 +118,48 @@ struct RowGroups {
   }
 };
 
-// The eight elements that lane t of T holds of group g of a row: with VEC, elements
-// (g T + t) 8 .. + 7, 16 bytes (two times 16 in fp32) a load; without, for rows that are
-// not 16-byte aligned or end inside eight elements, elements (8 g + i) T + t, so that
-// neighbouring lanes read neighbouring elements.
-template <int T, bool VEC>
+__device__ __forceinline__ void store8_loose(float* p, const float (&v)[8]) {
+  typedef Raw<float>::loose_t loose_t;
+  *reinterpret_cast<loose_t*>(p) = loose_t{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<loose_t*>(p + 4) = loose_t{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void store8_loose(bf16_t* p, const float (&v)[8]) {
+  Raw<bf16_t>::loose_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<Raw<bf16_t>::loose_t*>(p) = w;
+}
+
+// How rows lie: kAligned, 16-byte aligned and of whole groups of eight; kLoose, at any element and of eight
+// elements or more; kSingle, narrower.
+enum Layout { kSingle, kLoose, kAligned };
+
+// The eight elements that lane t of T holds of group g of a row: (g T + t) 8 .. + 7, 16 bytes (two times 16
+// in fp32) a load.  Where a loose row ends inside them a lane holds the row's last eight, of which those
+// that its neighbour has too (the first `skip`) count as 0 and are not stored.  kSingle: elements (8 g + i) T + t.
+// (2048 rows of 2047 in bf16 that are read and written an element at a time take twice as long.)
+template <int T, Layout LAYOUT>
 struct RowGroup {
   __device__ __forceinline__ static int column(int g, int t, int i) {
-    return VEC ? (g * T + t) * 8 + i : (8 * g + i) * T + t;
+    return LAYOUT == kSingle ? (8 * g + i) * T + t : (g * T + t) * 8 + i;
   }
+  __device__ __forceinline__ static int skip(int g, int t, int d) { return max(column(g, t, 0) - (d - 8), 0); }
   template <typename E>
   __device__ __forceinline__ static void load(const E* row, int g, int t, int d, float (&v)[8]) {
-    if (VEC) {
+    if (LAYOUT == kAligned) {
       if (column(g, t, 0) < d) {
         load8(row + column(g, t, 0), v);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.0f;
       }
+    } else if (LAYOUT == kLoose) {
+      Raw<E> raw;
+      raw.load_loose(row + min(column(g, t, 0), d - 8));
+      raw.get(v);
+      const int none = skip(g, t, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i >= none ? v[i] : 0.0f;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = column(g, t, i) < d ? load1(row + column(g, t, i)) : 0.0f;
@@ -126,8 +167,17 @@ struct RowGroup {
   }
   template <typename E>
   __device__ __forceinline__ static void store(E* row, int g, int t, int d, const float (&v)[8]) {
-    if (VEC) {
+    if (LAYOUT == kAligned) {
       if (column(g, t, 0) < d) store8(row + column(g, t, 0), v);
+    } else if (LAYOUT == kLoose) {
+      const int none = skip(g, t, d);
+      if (none == 0) {
+        store8_loose(row + column(g, t, 0), v);
+      } else if (none < 8) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+          if (i >= none) store1(row + d - 8 + i, v[i]);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
