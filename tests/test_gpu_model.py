@@ -180,9 +180,11 @@ def test_embedding_gradient_with_bad_maps(st):
 # ----------------------------------------------------------------------------------------- norms
 TYPES = [("bf16", "bf16", "bf16"), ("bf16", "bf16", "f32"), ("bf16", "f32", "f32"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16")]
 DIMS = [(5, 1), (3, 7), (9, 8), (4, 64), (7, 512), (6, 520), (5, 1000), (5, 1111), (4, 2048), (3, 2056), (3, 4096), (2, 5001),
-        (2, 8192), (2, 16384), (700, 264), (1, 2048), (1500, 33),
+        (2, 8192), (2, 16384), (700, 264), (1, 2048), (1500, 33), (37, 65), (50, 128), (21, 129), (11, 255),
+        (3, 4097), (2, 8191), (2, 8200), (2, 12291), (2, 16383),
         # more rows than there are places for them at once
-        (9000, 40), (4000, 300), (3000, 1000), (1500, 2048), (1300, 4096), (600, 5001), (530, 16384)]
+        (9000, 40), (4000, 300), (3000, 1000), (1500, 2048), (1300, 4096), (600, 5001), (530, 16384),
+        (20000, 64), (9000, 127), (1100, 2047), (300, 8193)]
 
 
 def run_norm(st, n, d, dtype, r_dtype, w_dtype, pre, post, gate, residual, scale, pad, seed, x=None):
@@ -312,10 +314,10 @@ def test_nan_and_infinity_stay_in_their_row(st):
         assert bool(torch.isnan(got[k][2]).any()) and bool(torch.isnan(got[k][4]).any())
 
 
-def test_norms_in_place(st):
+@pytest.mark.parametrize("n,d", [(70, 1024), (333, 63), (90, 1111), (600, 2047), (40, 8191), (33, 16384), (31, 16383)])
+def test_norms_in_place(st, n, d):
     """Outputs that take the place of inputs of their type."""
     import torch
-    n, d = 70, 1024
     x, z, dr, dh = (rand((n, d), "bf16", 50 + i) for i in range(4))
     w = 1 + rand((d,), "f32", 55, 0.2)
     how = dict(w_pre=w, w_post=w, post=True, scale=0.5)

@@ -41,10 +41,10 @@ template <typename X, typename Z, int T, int G, Layout LAYOUT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormView a) {
   using R = RowGroup<T, LAYOUT>;
   constexpr int kRows = T < 256 ? 256 / T : 1;
-  __shared__ float tmp[2][kRows][T / 64];
+  __shared__ float tmp[2][kRows][T < 64 ? 1 : T / 64];
   const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + slot;
-  if (i >= a.n_rows) return;   // T >= 256: the whole workgroup; T = 64: a wave, which meets no barrier
+  if (i >= a.n_rows) return;   // T >= 256: the whole workgroup; otherwise lanes that meet no barrier
   const float inv_d = 1.0f / static_cast<float>(d);
   float r[G][8], b[G][8];
 #pragma unroll
@@ -207,8 +207,8 @@ struct NormRow {
 constexpr int norm_bwd_waves(int lanes, int v) { return lanes >= 512 || v == 4 ? 4 : 3; }
 
 // Workgroups work off rows in turn, the next row's loads in flight, and keep the sums over their rows, and
-// the weights, in registers; parts: [vectors][slots of all workgroups][d], added up by norm_columns_kernel in
-// slot order.  SLABS: a workgroup takes group blockIdx.y of its rows, T V columns, and norm_means_kernel's means,
+// the weights, in registers; parts: [vectors][workgroups][d], added up by norm_columns_kernel in their
+// order.  SLABS: a workgroup takes group blockIdx.y of its rows, T V columns, and norm_means_kernel's means,
 // two a row, from the last row on, of which the caches still have most; otherwise whole rows, whose means it
 // forms itself.
 template <typename X, typename Z, int T, Layout LAYOUT, int V, bool SLABS>
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, norm_bwd_waves(T, V)) void norm_
   constexpr int kRows = T < 256 ? 256 / T : 1;
   // two sums a row, in buffers of their own for rows in turn: between a sum's reads and the
   // next writes to its buffer stands the barrier of the row between
-  __shared__ float tmp[2][2][kRows][T / 64];
+  __shared__ float tmp[2][2][kRows][T < 64 ? 1 : T / 64];
   const int t = threadIdx.x % T, slot = threadIdx.x / T, d = a.d, g = SLABS ? blockIdx.y : 0;
   const float inv_d = 1.0f / static_cast<float>(d);
   const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows;
@@ -320,17 +320,26 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, norm_bwd_waves(T, V)) void norm_
     }
     if (a.dz.data) Part<Z, T, LAYOUT, V>::store(row_of<Z>(a.dz, at), g, t, d, q);
   }
-  float* part = parts + me * d;
-  const int64_t one = slots * d;
-  if (a.dw_pre) {
-    Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_pre);
+  // the workgroup's rows in turn, then its part
+  float* part = parts + static_cast<int64_t>(blockIdx.x) * d;
+  const int64_t one = static_cast<int64_t>(gridDim.x) * d;
+  const auto put = [&](float (&v)[V]) {
+    if (kRows > 1) {
+      __shared__ float all[kRows][V][T];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < V; ++k) all[slot][k][t] = v[k];
+      __syncthreads();
+      for (int j = 1; j < kRows; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = j == 1 ? all[0][k][t] + all[1][k][t] : v[k] + all[j][k][t];
+    }
+    if (slot == 0) Part<float, T, LAYOUT, V>::store(part, g, t, d, v);
     part += one;
-  }
-  if (a.dw_post) {
-    Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_post);
-    part += one;
-  }
-  if (a.dgate_sum) Part<float, T, LAYOUT, V>::store(part, g, t, d, sum_gate);
+  };
+  if (a.dw_pre) put(sum_pre);
+  if (a.dw_post) put(sum_post);
+  if (a.dgate_sum) put(sum_gate);
 }
 
 // The means of wide rows, for norm_bwd_kernel's slabs, both from sums of one pass: with c = s gate w_post hat(z),
@@ -389,7 +398,7 @@ __global__ __launch_bounds__(512) void norm_means_kernel(NormView a, float* mean
   means[2 * i + 1] = s[1] - s[0] * s[2];
 }
 
-// Sums of the parts, 16 columns a workgroup: 64 of its lanes a column, which add slots k, k + 64, ... and
+// Sums of the parts (slots), 16 columns a workgroup: 64 of its lanes a column, which add slots k, k + 64, ... and
 // are then added up in turn.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ parts, int slots, int d,
                                                             float* o0, float* o1, float* o2) {
@@ -432,11 +441,15 @@ static Layout norm_layout(const NormView& v, int32_t r_dtype, int32_t dtype) {
   return aligned ? kAligned : kLoose;
 }
 
-// Lanes a row and groups of eight elements a lane: rows of up to 1024 in a wave, whose sums need no LDS, wider
-// ones in four and more.  2048 in 64 x 4: 122 us, in 256 x 1 112 (32768 rows of bf16).
+// Lanes a row and groups of eight elements a lane: rows of up to 1024 in a wave or less, whose sums need no LDS,
+// wider ones in four waves and more.  2048 in 64 x 4: 122 us, in 256 x 1 112 (32768 rows of bf16); 524288 rows of 64 in
+// 8 lanes: 49 us, in 64 215.
 #define NORM_SHAPES(GO)                          \
   do {                                           \
-    if (v.d <= 512) GO(64, 1);                   \
+    if (v.d <= 64) GO(8, 1);                     \
+    else if (v.d <= 128) GO(16, 1);              \
+    else if (v.d <= 256) GO(32, 1);              \
+    else if (v.d <= 512) GO(64, 1);              \
     else if (v.d <= 1024) GO(64, 2);             \
     else if (v.d <= 2048) GO(256, 1);            \
     else if (v.d <= 4096) GO(256, 2);            \
@@ -446,12 +459,15 @@ static Layout norm_layout(const NormView& v, int32_t r_dtype, int32_t dtype) {
 
 // The backward's, with elements a group: its sums, weights and loads in flight are some 20 registers an
 // element, so that four elements a lane in more lanes leave more waves a SIMD: 2048 in 512 x 4 takes 153 us, in
-// 256 x 8 233; 4096 in 1024 x 4 198, in 512 x 8 230 (both before rows were read past the caches).
+// 256 x 8 233; 4096 in 1024 x 4 198, in 512 x 8 230 (both before rows were read past the caches); 64 in
+// 16 lanes 76, in 64 176.
 // Wider rows spill there (8192 with r in fp32: 252 to 350 us for 4096 rows; bf16, 16384: 493 for 2048) and are
-// read twice: means first, then slabs of 1024 columns.
+// read twice, means first, then slabs of 1024 columns: 202 to 324, 149.  bf16 of 8192 in 1024 x 8: 92, in slabs 166.
 #define NORM_BWD_SHAPES(GO, SLABS)                    \
   do {                                                \
-    if (v.d <= 256) GO(64, 4);                        \
+    if (v.d <= 64) GO(16, 4);                         \
+    else if (v.d <= 128) GO(32, 4);                   \
+    else if (v.d <= 256) GO(64, 4);                   \
     else if (v.d <= 512) GO(64, 8);                   \
     else if (v.d <= 1024) GO(256, 4);                 \
     else if (v.d <= 2048) GO(512, 4);                 \
@@ -476,14 +492,15 @@ static NormBwdShape norm_bwd_shape(const NormView& v) {
 #undef GO
 }
 
-static int norm_rows_a_workgroup(int d) { return d <= 1024 ? 4 : 1; }
-
 template <typename X, typename Z, Layout LAYOUT>
 static void norm_fwd(const NormView& v, hipStream_t s) {
-  const int rows = norm_rows_a_workgroup(v.d);
-  const dim3 grid(static_cast<unsigned>((v.n_rows + rows - 1) / rows));
-#define GO(T, G) norm_fwd_kernel<X, Z, T, G, LAYOUT><<<grid, dim3(T < 256 ? 256 : T), 0, s>>>(v)
-  if constexpr (LAYOUT == kSingle) GO(64, 1);
+#define GO(T, G)                                                                                    \
+  do {                                                                                              \
+    constexpr int kRows = T < 256 ? 256 / T : 1;                                                    \
+    norm_fwd_kernel<X, Z, T, G, LAYOUT>                                                             \
+        <<<dim3(static_cast<unsigned>((v.n_rows + kRows - 1) / kRows)), dim3(T * kRows), 0, s>>>(v); \
+  } while (0)
+  if constexpr (LAYOUT == kSingle) GO(8, 1);
   else NORM_SHAPES(GO);
 #undef GO
 }
@@ -501,7 +518,7 @@ static int64_t norm_bwd_grid(const NormView& v) {
 size_t norm_bwd_workspace_bytes(const NormView& v) {
   const NormBwdShape shape = norm_bwd_shape(v);
   const size_t means = shape.slabs > 1 ? 2 * static_cast<size_t>(v.n_rows) : 0;
-  return (means + static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * shape.rows() * v.d) * sizeof(float);
+  return (means + static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * v.d) * sizeof(float);
 }
 
 template <typename X, typename Z, Layout LAYOUT>
@@ -520,7 +537,7 @@ static void norm_bwd(const NormView& v, float* ws, hipStream_t s) {
     norm_means_kernel<X, Z, LAYOUT><<<dim3(static_cast<unsigned>(v.n_rows)), dim3(512), 0, s>>>(v, means);   \
     norm_bwd_kernel<X, Z, T, LAYOUT, V, true><<<dim3(grid.x, shape.slabs), dim3(T), 0, s>>>(v, means, parts); \
   } while (0)
-    if constexpr (LAYOUT == kSingle) GO(64, 4);
+    if constexpr (LAYOUT == kSingle) GO(16, 4);
     else NORM_BWD_SHAPES(GO, SLABS);
 #undef SLABS
 #undef GO
@@ -532,7 +549,7 @@ static void norm_bwd(const NormView& v, float* ws, hipStream_t s) {
   for (float* p : {v.dw_pre, v.dw_post, v.dgate_sum})
     if (p) out[k++] = p;
   norm_columns_kernel<<<dim3((v.d + 15) / 16, n), dim3(1024), 0, s>>>(
-      parts, static_cast<int>(grid.x) * shape.rows(), v.d, out[0], out[1], out[2]);
+      parts, static_cast<int>(grid.x), v.d, out[0], out[1], out[2]);
 }
 
 #define NORM_LAYOUTS(CALL, X, Z)                  \

@@ -222,6 +222,14 @@ __device__ __forceinline__ float wave_max(float v) {
 // reads from an earlier sum (callers alternate between two).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* tmp, int t) {
+  if (T < 64) {   // rows of 8, 16 or 32 lanes: neighbours, pairs, and mirrors of 8 and 16, which give all lanes the same
+    v += from_lane<0xb1, 0xf>(v, 0.0f);
+    v += from_lane<0x4e, 0xf>(v, 0.0f);
+    v += from_lane<0x141, 0xf>(v, 0.0f);
+    if (T >= 16) v += from_lane<0x140, 0xf>(v, 0.0f);
+    if (T == 32) v += __shfl_xor(v, 16, 64);
+    return v;
+  }
   v = wave_sum(v);
   if (T == 64) return v;
   if ((t & 63) == 0) tmp[t >> 6] = v;
