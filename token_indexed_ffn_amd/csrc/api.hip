@@ -238,7 +238,7 @@ const char* staple_status_string(staple_status_t st) {
   }
 }
 
-const char* staple_version(void) { return "libstaple 0.2 (gfx950)"; }
+const char* staple_version(void) { return "libstaple 0.3 (gfx950)"; }
 
 staple_status_t staple_get_device_error(void* stream) {
   GET_ERR(err);

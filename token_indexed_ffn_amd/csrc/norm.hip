@@ -515,17 +515,20 @@ static int64_t norm_bwd_grid(const NormView& v) {
   return all < most ? all : most;
 }
 
+// Floats of the workspace before the parts: two means a row where there are slabs, in 16 bytes.
+static size_t norm_means(const NormView& v) {
+  return norm_bwd_shape(v).slabs > 1 ? (2 * static_cast<size_t>(v.n_rows) + 3) / 4 * 4 : 0;
+}
+
 size_t norm_bwd_workspace_bytes(const NormView& v) {
-  const NormBwdShape shape = norm_bwd_shape(v);
-  const size_t means = shape.slabs > 1 ? 2 * static_cast<size_t>(v.n_rows) : 0;
-  return (means + static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * v.d) * sizeof(float);
+  return (norm_means(v) + static_cast<size_t>(norm_vectors(v)) * norm_bwd_grid(v) * v.d) * sizeof(float);
 }
 
 template <typename X, typename Z, Layout LAYOUT>
 static void norm_bwd(const NormView& v, float* ws, hipStream_t s) {
   const NormBwdShape shape = norm_bwd_shape(v);
   const dim3 grid(static_cast<unsigned>(norm_bwd_grid(v)));
-  float *means = ws, *parts = shape.slabs > 1 ? ws + 2 * v.n_rows : ws;
+  float *means = ws, *parts = ws + norm_means(v);
   if (v.n_rows > 0) {
 #define GO(T, V)                                                                                             \
   do {                                                                                                       \
