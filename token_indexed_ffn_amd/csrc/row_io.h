@@ -137,7 +137,7 @@ enum Layout { kSingle, kLoose, kAligned };
 // The eight elements that lane t of T holds of group g of a row: (g T + t) 8 .. + 7, 16 bytes (two times 16
 // in fp32) a load.  Where a loose row ends inside them a lane holds the row's last eight, of which those
 // that its neighbour has too (the first `skip`) count as 0 and are not stored.  kSingle: elements (8 g + i) T + t.
-// (2048 rows of 2047 in bf16 that are read and written an element at a time take twice as long.)
+// (16384 rows of 2047 in bf16 through the norms, forward and backward: 154 us, an element at a time 222.)
 template <int T, Layout LAYOUT>
 struct RowGroup {
   __device__ __forceinline__ static int column(int g, int t, int i) {
