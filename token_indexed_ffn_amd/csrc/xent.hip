@@ -294,13 +294,12 @@ __global__ __launch_bounds__(256) void xent_bwd_kernel(XentView a, int pieces, i
 }
 
 // The narrowest shape that holds a row: lanes and groups of eight a lane (rows that begin between
-// 16-byte addresses need up to one group more).  8192 x 100352 bf16 logits with their gradient take 675 us
-// in 512 x 25, which keeps 170 registers a lane, and 729 in the long kernel with nothing kept; held to
-// 128 registers, for two workgroups a CU, 512 x 25 spills and takes 869.  The loss alone, which has
-// only the read to overlap with, is faster in the long kernel's many small steps: 325 us, 376 in 512 x 25.
-// Wider rows in the long kernel, 4096 rows with nothing kept and with 64 registers of them: bf16,
-// 151936: 587, 512; 260001: 1267, 950; fp32, 128256: 973, 838; 256000: 2255, 1916.  fp32 rows of 100352 take 662 us
-// in it and 703 in 512 x 25.
+// 16-byte addresses need up to one group more).  Wider rows in the long kernel, which keeps 32 registers of a bf16 row
+// and 64 of a wide one, 64 of an fp32 one: its read of the rest overlaps, where a workgroup with the whole row
+// in registers is alone on its CU and first reads, then writes.  us for 4096 bf16 rows with the gradient, nothing
+// kept, 32, 64 registers: 70000 classes: -, 286, 326 (all of it in 512 lanes); 100352: 393, 362, 363; 128256: 488, 448, 421;
+// 151936: 587, 535, 512; 260001: 1267, -, 950.  fp32, nothing and 64: 100352: 703 (all of it), 662; 128256: 973,
+// 838; 256000: 2255, 1916.  The loss alone is only read and keeps nothing.
 template <typename E>
 static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
   const bool aligned = reinterpret_cast<uintptr_t>(v.logits) % 16 == 0 && v.stride * sizeof(E) % 16 == 0;
@@ -320,16 +319,11 @@ static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
   GO(256, 8)
   GO(512, 8)
   GO(512, 16)
-  if (v.d_logits) {
-    if constexpr (sizeof(E) == 2) {
-      GO(512, 25)
-      GO(1024, 16)
-    }
-  }
 #undef GO
   const dim3 grid(static_cast<unsigned>(v.n_rows)), threads(1024);
-  if (v.d_logits) xent_fwd_long_kernel<E, 1024, 32 / sizeof(E)><<<grid, threads, 0, s>>>(v, err);
-  else xent_fwd_long_kernel<E, 1024, 0><<<grid, threads, 0, s>>>(v, err);
+  if (!v.d_logits) xent_fwd_long_kernel<E, 1024, 0><<<grid, threads, 0, s>>>(v, err);
+  else if (sizeof(E) == 4 || w <= 114688) xent_fwd_long_kernel<E, 1024, 8><<<grid, threads, 0, s>>>(v, err);
+  else if constexpr (sizeof(E) == 2) xent_fwd_long_kernel<E, 1024, 16><<<grid, threads, 0, s>>>(v, err);
 }
 
 hipError_t launch_xent_fwd(const XentView& v, int32_t dtype, hipStream_t s, int* err) {
