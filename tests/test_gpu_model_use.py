@@ -120,6 +120,40 @@ def test_two_captured_steps_share_a_workspace(st, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d,vocab", [(37, 8201, 70001), (130, 16384, 131080)])
+def test_wide_rows_captured_and_replayed(st, dtype, n, d, vocab):
+    """Norms whose backward takes two passes and a loss that reads its rows twice, in a graph, with the same calls
+    between its replays."""
+    import torch
+    x, z, dr, dh = (rand((n, d), dtype, 70 + i) for i in range(4))
+    logits, targets, g = rand((n, vocab), dtype, 74, 3.0), ints(np.arange(n) * 7 % vocab), floats(np.linspace(-1, 1, n))
+    w = 1 + rand((d,), "f32", 75, 0.1)
+    ws = workspace(st)
+
+    def run():
+        how = dict(w_pre=w, w_post=w, gate=w, post=True)
+        f = st.staple_norm_fwd(x, z, save=True, **how)
+        b = st.staple_norm_bwd(dr, dh, x, z, f["rstd_r"], f["rstd_z"], workspace=ws, **how)
+        loss = st.staple_xent_fwd(logits, targets, g=g)
+        return [f["r"], f["h"], *(t for t in b.values() if t is not None), *loss.values()]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for turn in range(4):
+        for t in (x, z, dr, dh, logits):
+            t.copy_(torch.roll(t, 1, 0))
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), turn
+    fine(st)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_memory_of_a_step_on_another_stream_is_not_handed_out(st, dtype):
     import torch
     step = Step(dtype, 3)
