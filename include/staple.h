@@ -946,9 +946,8 @@ staple_status_t staple_attn_decode_paged(const staple_kv_t* kv, const staple_att
  *
  * Rows are contiguous and a stride apart (in elements); rows that are read may
  * have any stride from 0, rows that are written one of at least their width.
- * Every element type's natural alignment is enough; where all operands and
- * strides are multiples of 16 bytes (and the width of 8 elements) a lane reads
- * 16 bytes at once.  Sums and statistics are fp32 or wider, outputs are rounded once.  Results
+ * Every element type's natural alignment is enough; rows that are 16-byte aligned and of a multiple of 8
+ * elements are read and written fastest.  Sums and statistics are fp32 or wider, outputs are rounded once.  Results
  * do not change from run to run.
  * ------------------------------------------------------------------------ */
 
