@@ -285,6 +285,30 @@ def test_a_norm_alone(st, dtype, out, n, d):
             check(to_np(b[k]), ref[k], bound[k], k)
 
 
+@pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("n,d", [(3, 7), (9, 63), (20, 264), (3, 2048), (2, 4104), (2, 8201), (2, 8208)])
+def test_gradients_that_need_nothing_of_a_block(st, dtype, r_dtype, n, d):
+    """A norm after the block whose gradients nobody asks for: z and its 1 / rms are not read, and need not be given."""
+    import torch
+    print(dtype, r_dtype, n, d, flush=True)
+    x, z = rand((n, d), r_dtype, 46, 2.0), rand((n, d), dtype, 47)
+    dr, dh = rand((n, d), r_dtype, 48), rand((n, d), dtype, 49)
+    w = 1 + rand((d,), "f32", 56, 0.2)
+    how = dict(w_pre=w, post=True, scale=0.5)
+    f = st.staple_norm_fwd(x, z, save=True, **how)
+    room = lambda: {"dx": torch.full_like(x, 7.0), "dw_pre": torch.full((d,), 7.0, device="cuda")}
+    want = st.staple_norm_bwd(dr, dh, x, z, f["rstd_r"], f["rstd_z"], r=f["r"], out=room(), **how)
+    for block in (z, None):   # without z the sum takes x's place
+        got = st.staple_norm_bwd(dr, dh, x if block is not None else f["r"], block, f["rstd_r"], r=f["r"], out=room(), **how)
+        fine(st)
+        for k, t in want.items():
+            assert torch.equal(got[k], t), k
+    # without the norm before the next block the sum's gradient is the residual stream's
+    got = st.staple_norm_bwd(dr, None, x, z, out={"dx": torch.empty_like(x)}, pre=False, post=True)
+    fine(st)
+    assert torch.equal(got["dx"], dr)
+
+
 def test_norms_without_weights_and_of_extreme_rows(st):
     import torch
     x = torch.zeros(4, 128, device="cuda")

@@ -199,7 +199,7 @@ struct NormRow {
     if (need_z) z.template load<ONCE>(row_of<const Z>(a.z, i), g, t, a.d);
     if (a.gate_kind == Gate::kRows) gate.template load<ONCE>(row_of<const Z>(a.gate, i), g, t, a.d);
     rstd_r = a.pre ? a.rstd_r[i] : 0.0f;
-    rstd_z = a.post ? a.rstd_z[i] : 1.0f;
+    rstd_z = a.post && need_z ? a.rstd_z[i] : 1.0f;   // given only where z is read
   }
 };
 
