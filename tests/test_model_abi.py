@@ -223,6 +223,16 @@ def test_the_binding_refuses_combinations():
         st.staple_norm_bwd(f, f, None)
 
 
+def test_the_binding_refuses_two_types_of_one_output():
+    f, i = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="out_dtype"):
+        st.staple_embed_fwd(f, i, out=f, out_dtype=torch.bfloat16)
+    # one of them, or both alike: refused for where the tensors are
+    for how in (dict(out=f), dict(out_dtype=torch.bfloat16), dict(out=f, out_dtype=torch.float32)):
+        with pytest.raises(ValueError, match="device"):
+            st.staple_embed_fwd(f, i, **how)
+
+
 def test_packed_norm_arguments_are_the_structure(L):
     head = (5, 8, 1, 0, 1, 1, 0, 0.5, 1e-6)
     rows = [(1000 + 8 * i, 10 + i) for i in range(10)]

@@ -1153,7 +1153,9 @@ def _flat(t: Optional[torch.Tensor], what: str, n: Optional[int], dev: int, dtyp
 def staple_embed_fwd(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
                      out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
-    """Rows scale * table[ids] [tokens, d] of out_dtype (None: the table's)."""
+    """Rows scale * table[ids] [tokens, d] of out_dtype (None: that of `out`, or the table's)."""
+    if out is not None and out_dtype is not None and out.dtype is not out_dtype:
+        raise ValueError(f"out: {out.dtype}, with out_dtype {out_dtype}")
     vocab, d = table.shape
     n, dev = ids.numel(), _on(table, "table")
     if out is None:
