@@ -1054,9 +1054,10 @@ staple_status_t staple_xent_bwd(const void* logits, int64_t stride, int64_t n_ro
  *   int32[n_rows]: each NULL for 1, 1, 0, and no limit.  A p or min_p that is NaN limits nothing, one of 0
  *   or less keeps the first token (p) or limits nothing (min_p); u outside [0, 1) or NaN counts as the
  *   nearest, NaN as 0.
- * The weights are rounded to multiples of 2^-62 by vocab (2^-50 at least) and summed exactly: the
- * same token on every run, and one that differs from the definition only where
- * u or p lies within that rounding of a border.  vocab <= 2^22, n_rows < 2^22. */
+ * The weights are held as multiples of 2^-50, or of 2^(b - 62) where that is more, with b the bits of vocab:
+ * each is the definition's to 2^-47 of itself and one multiple.  They are summed exactly: the same token on
+ * every run, and one that differs from the definition only where u, p or min_p lies within these errors, added
+ * up, of a border.  vocab <= 2^22, n_rows < 2^22. */
 size_t staple_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
 staple_status_t staple_sample(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                               int32_t dtype, const float* u, const float* temperature,

@@ -585,6 +585,46 @@ def test_sampling_with_arguments_at_their_ends(st):
     assert st.staple_sample(logits[:0], floats([]))["token"].shape == (0,)
 
 
+def next_to_a_border(kind):
+    """Rows of two logits, (-x, 0) at temperature T, and a u, p or min_p that is between 1.5 and 64 times as far from a
+    border as the weights' errors reach (the distance, formed in 64 bits, is off by less than the half).  Token 0, of
+    weight a = exp(-x / T), is drawn where u < a / (1 + a), kept where p > 1 / (1 + a), kept where min_p <= a.  A weight
+    is off by 2^-47 of itself and a unit of 2^-50, the largest one by nothing."""
+    from decimal import Decimal, localcontext
+    rng = np.random.default_rng(80)
+    f32 = lambda a: a.astype(np.float32).astype(np.float64)
+    n = 1 << 20
+    value = f32(rng.uniform(0.05, 0.45, n) if kind == "u" else rng.uniform(0.55, 0.95, n) if kind == "top_p" else rng.uniform(0.05, 0.95, n))
+    t = f32(rng.uniform(0.3, 2.0, n))
+    a = {"u": value / (1 - value), "top_p": 1 / value - 1, "min_p": value}[kind]
+    x = f32(-t * np.log(a))
+    a = np.exp(-x / t)
+    error = 2.0 ** -47 * a + 2.0 ** -50
+    far = np.abs({"u": a - value * (1 + a), "top_p": value * (1 + a) - 1, "min_p": a - value}[kind])   # a's factor here is 1 at most
+    at = np.nonzero((far > 1.5 * error) & (far < 64 * error))[0][:400]
+    first = []
+    with localcontext() as c:
+        c.prec = 40
+        for i in at:
+            w, v = (Decimal(-x[i]) / Decimal(t[i])).exp(), Decimal(value[i])
+            first.append({"u": v * (1 + w) < w, "top_p": v * (1 + w) > 1, "min_p": v <= w}[kind])
+    return x[at], t[at], value[at], np.array(first)
+
+
+@pytest.mark.parametrize("kind", ["u", "top_p", "min_p"])
+def test_sampling_next_to_a_border(st, kind):
+    """The definition's token, as near to a border as the weights' errors allow."""
+    import torch
+    x, t, value, first = next_to_a_border(kind)
+    n = len(x)
+    assert n >= 20 and 0 < first.sum() < n
+    logits = torch.stack((floats(-x), torch.zeros(n, device="cuda")), 1)
+    limit = {} if kind == "u" else {kind: floats(value)}
+    got = st.staple_sample(logits, floats(value if kind == "u" else np.zeros(n)), temperature=floats(t), **limit)["token"]
+    fine(st)
+    assert (got.cpu().numpy() == 0).tolist() == first.tolist()
+
+
 def test_sampling_shares(st):
     """Over an even grid of random numbers each token comes up as often as its share says."""
     import torch

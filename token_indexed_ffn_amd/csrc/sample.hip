@@ -3,8 +3,9 @@
 // The weights are whole numbers: w_j = round(unit exp((l_j - max l) / T)), from an exponential in
 // 64 bits, with unit a power of two: 2^62 by the number of logits, at most 2^50 (2^45 for 100352).
 // Their sums are exact in 64-bit integers, so that no order of adding, and no atomic one, changes a
-// token, and a sum is off by half a unit's inverse a logit at most, where sums in 32 bits would be
-// off by some 1e-7.
+// token.  A weight is off by half a unit's inverse from its rounding, by 2^-48 of itself from the exponential's
+// terms, and by |ln w| 2^-51 of itself from its argument, which is rounded four times: by 2^-47 of itself and one unit's
+// inverse in all, where sums in 32 bits would be off by some 1e-7.
 //
 // The kept tokens are a first part of the order of falling logits (ties: rising index), so one
 // pass finds the largest logit, a second one counts and weighs the tokens in kBins intervals of
