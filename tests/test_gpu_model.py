@@ -177,6 +177,33 @@ def test_embedding_gradient_with_bad_maps(st):
     assert call(seg_start=(2, -5))[0] in (0, -5)
 
 
+@pytest.mark.parametrize("each", [20, 90])
+def test_embedding_gradient_with_bad_segments(st, each):
+    """Every entry of seg_start that is out of range, or that its neighbours' positions contradict, sets the error
+    word; tokens within a workgroup's positions and across them."""
+    import torch
+    tokens, d = 5, 72
+    ids = torch.from_numpy(np.repeat(np.arange(tokens), each).astype(np.int32)).cuda()
+    n = len(ids)
+    dy = rand((n, d), "f32", 11)
+    dd = st.staple_dedup(ids, tokens)
+    right = each * np.arange(tokens + 1)
+
+    def call(at, value):
+        seg = dd["seg_start"].clone()
+        seg[at] = value
+        big = torch.full((tokens + 2, d), 7.0, device="cuda")
+        st.staple_embed_bwd(dy, dd["sorted_pos"], seg, dd["n_unique"], inv=dd["inv"], max_unique=tokens, out=big[1:-1])
+        assert bool((big[0] == 7).all()) and bool((big[-1] == 7).all())
+        return st.staple_get_device_error()
+
+    for at in range(tokens + 1):
+        print(each, at, flush=True)
+        assert call(at, int(right[at])) == 0
+        for bad in (-5, -1, right[at] - 1, right[at] + 1, n + 1, 2 ** 31 - 1, -2 ** 31):
+            assert call(at, int(bad)) == -5, (at, bad)
+
+
 # ----------------------------------------------------------------------------------------- norms
 TYPES = [("bf16", "bf16", "bf16"), ("bf16", "bf16", "f32"), ("bf16", "f32", "f32"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16")]
 DIMS = [(5, 1), (3, 7), (9, 8), (4, 64), (7, 512), (6, 520), (5, 1000), (5, 1111), (4, 2048), (3, 2056), (3, 4096), (2, 5001),

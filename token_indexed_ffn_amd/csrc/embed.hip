@@ -226,7 +226,10 @@ __global__ __launch_bounds__(64 * kChunks) void embed_bwd_kernel(EmbedGrad a, in
   }
   if (lane == 0) ended[wave] = ends != 0;
   // the maps agree, also where no border asks for a token's first and last position
-  if (g == 0 && lane < len && u >= 0 && (a.seg_start[u] > p || a.seg_start[u + 1] <= p)) flag_index_error(err);
+  if (g == 0 && lane < len && u >= 0) {
+    const int64_t begin = a.seg_start[u], end = a.seg_start[u + 1];
+    if (begin < 0 || begin > p || end <= p || end > n) flag_index_error(err);
+  }
   __syncthreads();
   // a cut run's parts, from that of the chunk in which it begins, or of the span's first chunk
 #pragma unroll 1
