@@ -312,6 +312,55 @@ def test_a_norm_alone(st, dtype, out, n, d):
             check(to_np(b[k]), ref[k], bound[k], k)
 
 
+@pytest.fixture
+def two_passes(monkeypatch):
+    """Chains of sums where the backward reads rows twice: a lane adds up to 32 terms (16384 columns in 512 lanes), a wave's
+    lanes join in 6 steps, 8 waves in turn, and the second mean is two sums' difference, each of whose terms has 6
+    roundings: 52 and the 6 that the bounds add to CHAIN."""
+    monkeypatch.setattr(B, "CHAIN", 52)
+
+
+@pytest.mark.parametrize("types", TYPES[1:4], ids="-".join)
+@pytest.mark.parametrize("pre", [True, False])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [None, "vector", "rows"])
+@pytest.mark.parametrize("residual", [True, False])
+def test_wide_norm_combinations(st, two_passes, types, pre, post, gate, residual):
+    """Widths whose backward takes two passes: past 4096 with r in fp32, past 8192 in bf16."""
+    dtype, r_dtype, w_dtype = types
+    if not residual:
+        types = (dtype, dtype, w_dtype)
+    for n, d, pad in ((3, 4104, 0), (2, 8201, 1), (5, 8208, 8), (2, 16384, 0)):
+        print(types, pre, post, gate, residual, n, d, pad, flush=True)
+        made = run_norm(st, n, d, *types, pre, post, gate, residual, -1.25, pad, 35)
+        check_norm(*made, dtype, types[1])
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("n,d", [(3, 4104), (2, 8201), (5, 16384)])
+def test_a_wide_norm_alone(st, two_passes, dtype, out, n, d):
+    test_a_norm_alone(st, dtype, out, n, d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d", [(300, 264), (5, 8201), (300, 8208)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_gates_gradients_in_place(st, dtype, n, d, residual):
+    """A gate a row, whose gradient takes its place, and the others' theirs."""
+    import torch
+    x, z, gate, dr, dh = (rand((n, d), dtype, 57 + i) for i in range(5))
+    x = x if residual else None
+    w = 1 + rand((d,), "f32", 62, 0.2)
+    how = dict(w_pre=w, w_post=w, post=True, scale=0.5)
+    f = st.staple_norm_fwd(x, z, gate=gate, save=True, **how)
+    want = st.staple_norm_bwd(dr, dh, x, z, f["rstd_r"], f["rstd_z"], gate=gate, **how)
+    out = {"dz": z, "dgate": gate, **({"dx": x} if residual else {})}
+    got = st.staple_norm_bwd(dr, dh, x, z, f["rstd_r"], f["rstd_z"], gate=gate, out=out, **how)
+    fine(st)
+    for k, t in got.items():
+        assert torch.equal(t, want[k]), k
+
+
 @pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("n,d", [(3, 7), (9, 63), (20, 264), (3, 2048), (2, 4104), (2, 8201), (2, 8208)])
 def test_gradients_that_need_nothing_of_a_block(st, dtype, r_dtype, n, d):
