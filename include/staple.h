@@ -967,7 +967,8 @@ staple_status_t staple_embed_fwd(const void* table, int64_t vocab, int64_t d, in
  * accumulate: 0 overwrites these rows, otherwise the sums are added to them.
  * grad [grad_rows x d] fp32.  *n_unique > max_unique, and entries of the maps out of range, set
  * the device error word; the former writes nothing.  Workspace: sums of tokens whose
- * positions are spread over several workgroups. */
+ * positions are spread over several workgroups.  d <= 2^20, n_tokens <= 2^29,
+ * (n_tokens / 64 + 1) (d / 512 + 1) < 2^23, in whole numbers. */
 size_t staple_embed_bwd_workspace_bytes(int64_t n_tokens, int64_t d);
 staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtype, int64_t n_tokens,
                                  int64_t d, float scale, const int32_t* sorted_pos,
@@ -991,9 +992,12 @@ staple_status_t staple_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtyp
  *
  * The backward takes the forward's x and z, rstd_r and rstd_z (as it wrote them), dr and dh
  * (the gradients of r and h; dr NULL: zero), and writes those of dx, dz, dgate, dw_pre,
- * dw_post that are not NULL.  With `pre` it reads the stored r where r is given (x where z
- * was NULL), and otherwise forms r again from x and z, as the forward had it before
- * rounding; a bf16 r is off by its rounding, which shows in dw_pre as some 2^-9 of it.
+ * dw_post that are not NULL; one of what is not done (dw_pre without pre, dw_post without post,
+ * dgate without a gate) is left as it is.  With `pre` it reads the stored r where r is given, which is x for
+ * a forward without z, and otherwise forms r again from x and z, as the forward had it before
+ * rounding; a bf16 r is off by its rounding, which shows in dw_pre as some 2^-9 of it.  z and rstd_z may be
+ * NULL where nothing reads them: without dgate, without `post` or without dz and dw_post, and with r given or
+ * without `pre`.
  *     g = dr + (t - hat(r) mean(t hat(r))) / rms(r),  t = dh w_pre,  hat(v) = v / rms(v)
  *     dx = g,   dw_pre = sum of dh hat(r),   dgate = scale g b,   q = scale gate g,
  *     dz = q, or (q w_post - hat(z) mean(q w_post hat(z))) / rms(z),   dw_post = sum of q hat(z)
@@ -1032,7 +1036,9 @@ staple_status_t staple_norm_bwd(const staple_norm_t* a, void* ws, size_t ws_byte
  * has it has the loss +inf, and a row that has nothing else has the gradient zero.
  * The forward writes loss and lse float[n_rows] and, with g float[n_rows] (the gradient of each
  * row's loss) and d_logits (of dtype, may be the logits themselves), the gradient in the same
- * call; staple_xent_bwd writes it from a forward's lse.  vocab <= 2^22, n_rows < 2^22. */
+ * call; staple_xent_bwd writes it from a forward's lse, whose rounding, 2^-24 of |lse|, is then one of every
+ * exponent: where all logits are far from 0 the forward's gradient is the more exact one.
+ * vocab <= 2^22, n_rows < 2^22. */
 staple_status_t staple_xent_fwd(const void* logits, int64_t stride, int64_t n_rows, int64_t vocab,
                                 int32_t dtype, const int32_t* targets, float* loss, float* lse,
                                 const float* g, void* d_logits, int64_t d_stride, void* stream);

@@ -4,7 +4,7 @@
 //
 // Both are bound by bytes: the rows of distinct tokens and the output, the gradients and a row in fp32 for each
 // distinct token.  32768 positions, 7700 distinct, of 2048 in bf16: 41 us (4.0 TB/s) and, with the join of
-// cut tokens, 49 (4.1 TB/s).
+// cut tokens, 49 (4.1 TB/s), from rows in fp32 75 (4.4 TB/s).
 #include "model_ops.h"
 #include "row_io.h"
 

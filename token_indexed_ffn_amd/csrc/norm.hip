@@ -463,6 +463,9 @@ static Layout norm_layout(const NormView& v, int32_t r_dtype, int32_t dtype) {
 // 16 lanes 76, in 64 176.
 // Wider rows spill there (8192 with r in fp32: 252 to 350 us for 4096 rows; bf16, 16384: 493 for 2048) and are
 // read twice, means first, then slabs of 1024 columns: 202 to 324, 149.  bf16 of 8192 in 1024 x 8: 92, in slabs 166.
+// Of the shapes that are taken 1024 x 8 in bf16 spills 25 registers (rows at any element: 3), and 64 x 8 in fp32, for
+// widths of 257 to 512, 5 (15): 32768 rows of 512 take 86 us, of 511 98, 60000 of 300 109, and in 256 x 4, which spills
+// none, 87, 98 and 108.
 #define NORM_BWD_SHAPES(GO, SLABS)                    \
   do {                                                \
     if (v.d <= 64) GO(16, 4);                         \

@@ -1159,7 +1159,8 @@ size_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
 // Groups of eight elements a lane with which rows of temperature and min-p alone are worked off in registers, or
 // 0: long rows too few to occupy half of the CUs are faster in parts.  bf16, us in registers and
 // otherwise: 64 rows of 16000: 9, 12; of 50021: 20, 16; 128 rows: 21, 23; 512 rows: 41, 52; 512 rows of
-// 100352: 68, 86.
+// 100352: 68, 86.  25 groups are the most: in 32 (201 registers) and otherwise 128 rows of 102400 take 38, 32, 512 rows 81,
+// 75; of 128256 128 rows take 37, 35, 256 rows 43, 57, 512 rows 85, 91.
 template <typename E>
 static int row_groups(const SampleView& v) {
   const int64_t w = v.vocab + 7;

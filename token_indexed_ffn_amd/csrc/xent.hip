@@ -263,7 +263,8 @@ __global__ __launch_bounds__(T) void xent_fwd_long_kernel(XentView a, int* err) 
   if (edge >= 0) store1(out + edge, grad.one(at_edge, edge));
 }
 
-// The gradient alone: a workgroup takes kBwdGroups times 2048 elements of a row.
+// The gradient alone: a workgroup takes kBwdGroups times 2048 elements of a row.  4096 rows of 100352: bf16 304 us
+// (5.4 TB/s), fp32 589 (5.6); of 100277: 308, 607.
 constexpr int kBwdGroups = 4;
 template <typename E>
 __global__ __launch_bounds__(256) void xent_bwd_kernel(XentView a, int pieces, int* err) {
@@ -299,7 +300,8 @@ __global__ __launch_bounds__(256) void xent_bwd_kernel(XentView a, int pieces, i
 // in registers is alone on its CU and first reads, then writes.  us for 4096 bf16 rows with the gradient, nothing
 // kept, 32, 64 registers: 70000 classes: -, 286, 326 (all of it in 512 lanes); 100352: 393, 362, 363; 128256: 488, 448, 421;
 // 151936: 587, 535, 512; 260001: 1267, -, 950.  fp32, nothing and 64: 100352: 703 (all of it), 662; 128256: 973,
-// 838; 256000: 2255, 1916.  The loss alone is only read and keeps nothing.
+// 838; 256000: 2255, 1916.  The loss alone is only read and keeps nothing: 4096 bf16 rows of 100352 take 178 to 204 us
+// (4.0 to 4.6 TB/s), fp32 271 (6.1).
 template <typename E>
 static void xent_fwd(const XentView& v, hipStream_t s, int* err) {
   const bool aligned = reinterpret_cast<uintptr_t>(v.logits) % 16 == 0 && v.stride * sizeof(E) % 16 == 0;
