@@ -712,3 +712,19 @@ def test_sampling_shares(st):
     share = torch.bincount(got, minlength=5).float() / n
     assert float((share - p).abs().max()) <= 1.0 / n
     fine(st)
+
+
+def test_workspaces_in_host_memory_are_refused(st):
+    import torch
+    room = torch.empty(1 << 22, dtype=torch.uint8)
+    x, w = rand((100, 64), "f32", 81), torch.ones(64, device="cuda")
+    f = st.staple_norm_fwd(x, w_pre=w, save=True)
+    dd = st.staple_dedup(ints(np.arange(100) % 3), 3)
+    logits = rand((2, 100352), "bf16", 82)
+    assert st.lib().staple_sample_workspace_bytes(2, 100352) > 0
+    for call in (lambda: st.staple_norm_bwd(None, x, x, None, f["rstd_r"], w_pre=w, workspace=room),
+                 lambda: st.staple_embed_bwd(x, dd["sorted_pos"], dd["seg_start"], dd["n_unique"], inv=dd["inv"], workspace=room),
+                 lambda: st.staple_sample(logits, floats([0.5, 0.5]), workspace=room)):
+        with pytest.raises(ValueError, match="workspace: needs"):
+            call()
+    fine(st)

@@ -233,6 +233,18 @@ def test_the_binding_refuses_two_types_of_one_output():
             st.staple_embed_fwd(f, i, **how)
 
 
+def test_a_workspace_elsewhere_is_refused():
+    """The kernels write there: host memory, another device's, or the gaps of a strided tensor are not handed to them."""
+    here, room = torch.device("cpu"), torch.empty(64, dtype=torch.uint8)
+    assert st._ws(64, room, here, None) is room and st._ws(0, None, here, None) is None
+    for device, workspace in ((torch.device("cuda", 0), room), (here, torch.empty(256, dtype=torch.uint8)[::2]),
+                              (here, torch.empty(64, dtype=torch.uint8, device="meta"))):
+        with pytest.raises(ValueError, match="workspace: needs"):
+            st._ws(64, workspace, device, None)
+    with pytest.raises(ValueError, match="required"):
+        st._ws(65, room, here, None)
+
+
 def test_packed_norm_arguments_are_the_structure(L):
     head = (5, 8, 1, 0, 1, 1, 0, 0.5, 1e-6)
     rows = [(1000 + 8 * i, 10 + i) for i in range(10)]

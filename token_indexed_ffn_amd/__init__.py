@@ -91,6 +91,8 @@ def _ws(nbytes: int, workspace: Optional[torch.Tensor], device, stream) -> Optio
     if nbytes == 0:
         return workspace
     if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: needs a contiguous tensor on {device}, got one on {workspace.device}")
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"workspace of {nbytes} bytes required")
         return workspace
